@@ -216,10 +216,10 @@ def _quantise(x, fmt, rounding, bits, gs):
         if rounding == "stochastic":
             up = (six * s8.float() < a) & (s8.view(torch.uint8) < 0x7E)
             s8 = (s8.view(torch.uint8) + up.to(torch.uint8)).view(torch.float8_e4m3fn)
-        d = s8.float() * gs
-        inverse = torch.where(d > 0, torch.reciprocal(d), 0.0)
+        d = (s8.float() * gs).unsqueeze(-1)
         scales = torch.where(whole, s8.view(torch.uint8), 0x7F).to(torch.uint8)
-    v = (xb * inverse.unsqueeze(-1)).abs().clamp(max=6.0)
+    v = xb * inverse.unsqueeze(-1) if fmt == "mxfp4" else torch.where(d > 0, xb / d, 0.0)
+    v = v.abs().clamp(max=6.0)
     if rounding == "nearest":
         code = ((v > 0.25).byte() + (v >= 0.75).byte() + (v > 1.25).byte() + (v >= 1.75).byte()
                 + (v > 2.5).byte() + (v >= 3.5).byte() + (v > 5.0).byte())
