@@ -306,6 +306,106 @@ int gemm_baseline(int variant, int64_t M, int64_t N, int64_t K,
                   void *C, int64_t ldc,
                   void *stream);
 
+/*
+ * Microscaled 4-bit matrices
+ * --------------------------
+ * A matrix of R rows of K values is held as codes and block scales:
+ *   codes   E2M1: sign, two exponent bits, one mantissa bit (0, 0.5, 1, 1.5, 2,
+ *           3, 4, 6), two per byte, the even element in the low nibble.  Row r
+ *           starts at byte r * pitch; pitch is a multiple of 16 and at least
+ *           16 * ceil(K / 32); the codes past K up to there are zero.
+ *   scales  one byte per block of consecutive elements of a row, in tiles of
+ *           128 rows x 4 blocks (512 bytes), ceil(blocks / 4) tiles per 128
+ *           rows: block b of row r at byte
+ *             (r / 128 * ceil(blocks / 4) + b / 4) * 512
+ *             + r % 32 * 16 + r % 128 / 32 * 4 + b % 4.
+ *           The buffer holds whole tiles.  The bytes of blocks past K must not
+ *           be NaN; those of rows past R may hold anything.
+ *   PTC_FP4_MX  blocks of 32, scale 2^(byte - 127), 0xFF: the block is NaN
+ *   PTC_FP4_NV  blocks of 16, E4M3 scale, 0x7F: the block is NaN; the whole
+ *               matrix is also scaled by a float on the device (NULL: 1),
+ *               which must lie in 2^-100 .. 2^100.
+ * Codes and scales are 16-byte aligned.  (The study has no floating-point
+ * 4-bit format; these are the ones the GB300 tensor cores multiply directly.)
+ *
+ * Random numbers: element (row, column) of a call with `seed` and `offset`
+ * (below 2^63) has 16 bits of Philox4x32-10 (Salmon et al., "Parallel random
+ * numbers: as easy as 1, 2, 3", SC 2011) with key = seed and counter (column / 8,
+ * row, offset's low word, offset's high word | purpose << 31), purpose 0 for
+ * dropout and 1 for rounding; column % 8 = j takes bits 16 (j % 2) .. of word
+ * j / 2.  They depend on nothing else: the same call gives the same bits on any
+ * device, stream and layout.
+ */
+#define PTC_FP4_MX 0
+#define PTC_FP4_NV 1
+#define PTC_ROUND_NEAREST 0
+#define PTC_ROUND_STOCHASTIC 1
+
+/*
+ * Dropout without a stored mask: y = [r < T] x * (65536 / T) (+ residual), in
+ * FP32 with one rounding per operation and one to the element type
+ * (PTC_OUT_F32, PTC_OUT_BF16, PTC_OUT_F16); r the element's 16 bits,
+ * T = floor((1 - p) * 65536 + 1/2), so that the expectation is x's exactly.  A
+ * dropped element is +0 whatever its value.  residual may be NULL.  The
+ * gradient of x is the same call on the gradient of y without a residual.
+ * x, residual, y: rows of `cols` elements, ld >= cols elements apart, aligned
+ * to the element (16-byte rows run faster); y may be x or the residual (same
+ * ld), otherwise it must not overlap them.
+ */
+int ptc_dropout(int64_t rows, int64_t cols, const void *x, int64_t ldx, const void *residual, int64_t ldr, void *y,
+                int64_t ldy, int type, double p, uint64_t seed, uint64_t offset, void *stream);
+
+/*
+ * Quantisation of x (rows x cols, ldx elements apart, type PTC_OUT_*) to a
+ * microscaled 4-bit matrix: of its rows (codes, pitch, scales: rows x cols),
+ * of its columns (codes_t, pitch_t, scales_t: cols x rows, blocks along the
+ * rows of x), or both in one pass; a NULL codes pointer leaves that one out.
+ * With p > 0 the values are those of ptc_dropout(x) in FP32.
+ *   PTC_FP4_MX  scale 2^(floor(log2 amax) - 2), amax the block's largest
+ *               magnitude; stochastic: the least power of two with
+ *               amax <= 6 * scale
+ *   PTC_FP4_NV  scale rn_e4m3(amax / (6 G)), at most 448, G the matrix scale;
+ *               stochastic: the next one up where 6 G * scale < amax
+ * and codes of x / scale (PTC_FP4_NV: x / rn(scale * G)), the quotient rounded
+ * to FP32 and at most 6 in magnitude, rounded to nearest with ties to even, or (PTC_ROUND_STOCHASTIC)
+ * up when remainder / gap >= 1 - r / 65536.  A block with an infinity or NaN
+ * becomes NaN (codes 0).  x is aligned to its element.  Outputs must not
+ * overlap each other or the inputs.
+ */
+int ptc_quantize_fp4(int64_t rows, int64_t cols, const void *x, int64_t ldx, int type, int format, int rounding,
+                     const float *matrix_scale, void *codes, int64_t pitch, void *scales, void *codes_t,
+                     int64_t pitch_t, void *scales_t, double p, uint64_t seed, uint64_t offset, void *stream);
+
+/* Values of a microscaled 4-bit matrix: y = rn(code * scale) (rn(* G)), each
+ * product in FP32, then rounded to y's type. */
+int ptc_dequantize_fp4(int64_t rows, int64_t cols, const void *codes, int64_t pitch, const void *scales, int format,
+                       const float *matrix_scale, void *y, int64_t ldy, int type, void *stream);
+
+/*
+ * C[M x N] = out( rn(GA GB) * sum_k a_ik b_jk ) of two microscaled 4-bit
+ * matrices of the same format: A of M rows of K, B of N rows of K (B's
+ * columns as rows, like gemm_s4), lda and ldb the code pitches in BYTES, SA / SB
+ * their scales, GA / GB their matrix scales (PTC_FP4_NV; NULL: 1).  Products
+ * are exact, sums are the tensor cores' FP32 sums; C is float32, bfloat16 or
+ * binary16 (PTC_OUT_*), ldc >= N elements apart, aligned to its element
+ * (16-byte rows run faster).  K == 0 writes zeros.  No workspace is used.
+ * Results are the same from call to call; the summation order depends on the
+ * sizes (and the keys fp4_tile, fp4_ksplit).
+ */
+int gemm_fp4(int64_t M, int64_t N, int64_t K, int format, const void *A, int64_t lda, const void *SA, const float *GA,
+             const void *B, int64_t ldb, const void *SB, const float *GB, void *C, int64_t ldc, int out_type,
+             void *stream);
+
+/*
+ * C[M x N] = out( GW * sum_k x_ik w_jk ): a few rows (tokens) of bfloat16 or
+ * binary16 activations X (`type`, ldx elements apart) with a microscaled 4-bit
+ * matrix W of N rows of K (ldw bytes apart); C has X's type.  Products are
+ * exact, sums FP32.  Meant for M up to 16, where W is read once; more rows are
+ * taken 16 at a time.  X and C are aligned to the element.
+ */
+int gemm_a16_fp4(int64_t M, int64_t N, int64_t K, int type, const void *X, int64_t ldx, int format, const void *W,
+                 int64_t ldw, const void *SW, const float *GW, void *C, int64_t ldc, void *stream);
+
 /* Human-readable text of a status code.  For PTC_ERR_LAUNCH the text of the
  * failing CUDA call on the calling thread is appended.  Never NULL; the
  * string stays valid until the next call on the same thread. */
@@ -508,6 +608,12 @@ int ptc_last_conversion(int *mode);
  *                  (single-wave launches with few K blocks per CTA: small
  *                  products such as N = 512); 0: never; 2: on every one-CTA
  *                  shape.  Results do not depend on the choice.
+ *   "fp4_tile"     gemm_fp4's output tiles: 0 (default) by size, 64 or 128: one
+ *                  CTA per 128 x 64 / 128 x 128 tile, 256: CTA pairs on
+ *                  256 x 256 tiles.
+ *   "fp4_ksplit"   gemm_fp4's one-CTA tiles: CTAs of a cluster that share a
+ *                  tile's K range: 0 (default) by size, 1, 2, 4 or 8.
+ *   "fp4_group_m"  gemm_fp4's tile rows per raster group, default 8.
  * No accepted value of any key changes an INT8 or INT4 result. */
 int ptc_set_tuning(const char *key, int64_t value);
 

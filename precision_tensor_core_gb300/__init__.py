@@ -10,7 +10,8 @@ library's CUDA kernels):
 * ``gemm_f16``, ``gemm_f16_f16acc``, ``gemm_s8``, ``gemm_s4``, ``gemm_s8_scaled``, ``gemm_s4_scaled``,
   ``gemm_s8_noalloc``, ``gemm_s8_b_rowmajor``, ``gemm_status_string``,
   ``gemm_poll_device_error``, ``ptc_kernel_launch_count``, ``ptc_last_launch``, ``ptc_last_conversion``, ``ptc_plan_shape``,
-  ``ptc_debug_set_wait_limit``, ``ptc_set_tuning``: the C ABI of
+  ``ptc_debug_set_wait_limit``, ``ptc_set_tuning``, ``gemm_fp4``, ``gemm_a16_fp4``, ``ptc_dropout``,
+  ``ptc_quantize_fp4``, ``ptc_dequantize_fp4``: the C ABI of
   ``include/ptc.h`` under the same names, taking integers (sizes, leading
   dimensions, device addresses, a cudaStream_t handle).  A nonzero status
   raises :class:`PtcError`.
@@ -19,6 +20,10 @@ library's CUDA kernels):
   on the current CUDA stream; host (CPU) tensors of ``matmul_f16`` /
   ``matmul_s8`` / ``matmul_s4`` go through the host-buffer entry points
   (``gemm_*_host``), which pipeline the copies inside the library.
+* ``dropout``, ``quantize_fp4``, ``dequantize_fp4``, ``matmul_fp4``, ``matmul_a16_fp4`` and
+  :class:`Fp4Matrix`: counter-based dropout and microscaled 4-bit matrices on
+  torch tensors of the device; :mod:`precision_tensor_core_gb300.fp4_linear`
+  puts them together as a linear layer's training and decoding steps.
 
 There is no CPU fallback: if ``libptc.so`` has not been built the first call
 raises, and on a machine without a compute-capability 10.3 GPU every GEMM call
@@ -55,6 +60,11 @@ PTC_OUT_F32 = 0
 PTC_OUT_BF16 = 1
 PTC_OUT_F16 = 2
 
+PTC_FP4_MX = 0
+PTC_FP4_NV = 1
+PTC_ROUND_NEAREST = 0
+PTC_ROUND_STOCHASTIC = 1
+
 _i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
 _lib = None
@@ -84,6 +94,18 @@ def lib() -> ctypes.CDLL:
             fn = getattr(L, name)
             fn.restype = ctypes.c_int
             fn.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, ctypes.c_int, _vp]
+        _int, _u64, _f64 = ctypes.c_int, ctypes.c_uint64, ctypes.c_double
+        for name, args in (
+                ("ptc_dropout", [_i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _int, _f64, _u64, _u64, _vp]),
+                ("ptc_quantize_fp4", [_i64, _i64, _vp, _i64, _int, _int, _int, _vp, _vp, _i64, _vp, _vp, _i64, _vp,
+                                      _f64, _u64, _u64, _vp]),
+                ("ptc_dequantize_fp4", [_i64, _i64, _vp, _i64, _vp, _int, _vp, _vp, _i64, _int, _vp]),
+                ("gemm_fp4", [_i64, _i64, _i64, _int, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _int,
+                              _vp]),
+                ("gemm_a16_fp4", [_i64, _i64, _i64, _int, _vp, _i64, _int, _vp, _i64, _vp, _vp, _vp, _i64, _vp])):
+            fn = getattr(L, name)
+            fn.restype = ctypes.c_int
+            fn.argtypes = args
         L.gemm_baseline.restype = ctypes.c_int
         L.gemm_baseline.argtypes = [ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp]
         L.gemm_status_string.restype = ctypes.c_char_p
@@ -182,6 +204,34 @@ def gemm_s4_host(M, N, K, A, lda, B, ldb, C, ldc, stream=0) -> int:
 def gemm_baseline(variant, M, N, K, A, lda, B, ldb, C, ldc, stream=0) -> int:
     """The paper's WMMA / mma.sync kernel families on GB300 (PTC_BASELINE_*); see include/ptc.h."""
     return _check(lib().gemm_baseline(variant, M, N, K, A, lda, B, ldb, C, ldc, stream))
+
+
+def ptc_dropout(rows, cols, x, ldx, residual, ldr, y, ldy, type, p, seed, offset, stream=0) -> int:
+    """y = dropout(x) (+ residual), mask from (seed, offset); device addresses."""
+    return _check(lib().ptc_dropout(rows, cols, x, ldx, residual, ldr, y, ldy, type, p, seed, offset, stream))
+
+
+def ptc_quantize_fp4(rows, cols, x, ldx, type, format, rounding, matrix_scale, codes, pitch, scales, codes_t, pitch_t,
+                     scales_t, p, seed, offset, stream=0) -> int:
+    """x to microscaled 4-bit rows and / or columns; see include/ptc.h."""
+    return _check(lib().ptc_quantize_fp4(rows, cols, x, ldx, type, format, rounding, matrix_scale, codes, pitch,
+                                         scales, codes_t, pitch_t, scales_t, p, seed, offset, stream))
+
+
+def ptc_dequantize_fp4(rows, cols, codes, pitch, scales, format, matrix_scale, y, ldy, type, stream=0) -> int:
+    """Values of a microscaled 4-bit matrix; device addresses."""
+    return _check(lib().ptc_dequantize_fp4(rows, cols, codes, pitch, scales, format, matrix_scale, y, ldy, type,
+                                           stream))
+
+
+def gemm_fp4(M, N, K, format, A, lda, SA, GA, B, ldb, SB, GB, C, ldc, out_type, stream=0) -> int:
+    """C[MxN] = A[MxK] . B[NxK]^T of two microscaled 4-bit matrices (code pitches in bytes)."""
+    return _check(lib().gemm_fp4(M, N, K, format, A, lda, SA, GA, B, ldb, SB, GB, C, ldc, out_type, stream))
+
+
+def gemm_a16_fp4(M, N, K, type, X, ldx, format, W, ldw, SW, GW, C, ldc, stream=0) -> int:
+    """C[MxN] = X[MxK] (bfloat16 / binary16) . W[NxK]^T, W microscaled 4-bit."""
+    return _check(lib().gemm_a16_fp4(M, N, K, type, X, ldx, format, W, ldw, SW, GW, C, ldc, stream))
 
 
 def gemm_poll_device_error() -> int:
@@ -386,3 +436,276 @@ def matmul_s4_scaled(A, Bt, K, scale_a=None, scale_b=None, out_dtype=None, out=N
 
 
 _HOST_FN.update({gemm_f16: gemm_f16_host, gemm_s8: gemm_s8_host, gemm_s4: gemm_s4_host})
+
+
+# ---------------------------------------------------------------- 4-bit operators on tensors
+_FP4 = {"mxfp4": (PTC_FP4_MX, 32), "nvfp4": (PTC_FP4_NV, 16)}
+_ROUNDING = {"nearest": PTC_ROUND_NEAREST, "stochastic": PTC_ROUND_STOCHASTIC}
+_MASK64 = (1 << 64) - 1
+_TYPES = {}
+
+
+def _type_of(dtype):
+    """PTC_OUT_* of a torch dtype."""
+    if not _TYPES:
+        import torch
+        _TYPES.update({torch.float32: PTC_OUT_F32, torch.bfloat16: PTC_OUT_BF16, torch.float16: PTC_OUT_F16})
+    code = _TYPES.get(dtype)
+    if code is None:
+        raise TypeError("tensors are float32, bfloat16 or float16")
+    return code
+
+
+def _rows_of(t, name):
+    """Row pitch in elements of a 2-D device tensor with unit column stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    rows, cols = t.shape
+    s0, s1 = t.stride()
+    if (cols > 1 and s1 != 1) or (rows > 1 and s0 < cols):
+        raise ValueError(f"{name} must be a 2-D tensor with unit column stride and rows that do not overlap")
+    return s0 if rows > 1 else cols
+
+
+def _on(stream, tensor):
+    """(stream handle, device guard) of a call on `tensor`'s device."""
+    import torch
+    index = tensor.device.index
+    if stream is None:
+        return torch.cuda.current_stream(index).cuda_stream
+    return _stream(stream)
+
+
+class _Guard:
+    """Makes a tensor's device current for a call where it is not already."""
+
+    def __init__(self, tensor):
+        import torch
+        index = tensor.device.index
+        self.guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def fp4_scale_bytes(rows: int, cols: int, fmt: str) -> int:
+    """Bytes of the tiled scales of `rows` rows of `cols` values."""
+    blocks = -(-cols // _FP4[fmt][1])
+    return -(-rows // 128) * -(-blocks // 4) * 512
+
+
+class Fp4Matrix:
+    """A microscaled 4-bit matrix of ``codes.shape[0]`` rows of ``K`` values.
+
+    codes: uint8 (rows, >= 16 * ceil(K / 32)) with unit column stride, a row pitch
+        that is a multiple of 16 bytes, and zeros past K
+    scales: contiguous uint8 of ``fp4_scale_bytes(rows, K, fmt)`` bytes in the
+        tiled layout of include/ptc.h (:meth:`tile_scales` makes it from rows)
+    fmt: "mxfp4" or "nvfp4"; tensor_scale: None, or (nvfp4) a float32 device
+        tensor of one element that scales the whole matrix.
+    """
+
+    __slots__ = ("codes", "scales", "K", "fmt", "tensor_scale")
+
+    def __init__(self, codes, scales, K, fmt="mxfp4", tensor_scale=None):
+        import torch
+        if fmt not in _FP4:
+            raise ValueError("fmt is 'mxfp4' or 'nvfp4'")
+        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+            raise TypeError("codes and scales are uint8")
+        if K < 0 or _rows_of(codes, "codes") % 16 and codes.shape[0] > 1 or codes.shape[1] < -(-K // 32) * 16:
+            raise ValueError("codes must hold 16 * ceil(K / 32) bytes per row, rows a multiple of 16 bytes apart")
+        if not scales.is_contiguous() or scales.numel() < fp4_scale_bytes(codes.shape[0], K, fmt):
+            raise ValueError("scales must be contiguous and hold whole tiles of 128 rows x 4 blocks")
+        _check_tensor_scale(tensor_scale, fmt)
+        if scales.device != codes.device or (tensor_scale is not None and tensor_scale.device != codes.device):
+            raise ValueError("codes and scales must be on one device")
+        self.codes, self.scales, self.K, self.fmt, self.tensor_scale = codes, scales, int(K), fmt, tensor_scale
+
+    @property
+    def shape(self):
+        return (self.codes.shape[0], self.K)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def record_stream(self, stream):
+        """As torch.Tensor.record_stream, for every tensor of the matrix."""
+        for t in (self.codes, self.scales, self.tensor_scale):
+            if t is not None:
+                t.record_stream(stream)
+
+    @staticmethod
+    def tile_scales(scales):
+        """Row-major scale bytes (rows, blocks) to the tiled layout (laid out once, e.g. when weights are loaded)."""
+        import torch
+        r, b = scales.shape
+        s = torch.nn.functional.pad(scales, (0, -b % 4, 0, -r % 128))
+        return s.view(s.shape[0] // 128, 4, 32, s.shape[1] // 4, 4).permute(0, 3, 2, 1, 4).reshape(-1)
+
+    def row_scales(self):
+        """Row-major scale bytes (rows, blocks)."""
+        r, b = self.codes.shape[0], -(-self.K // _FP4[self.fmt][1])
+        kt = -(-b // 4)
+        s = self.scales[:fp4_scale_bytes(r, self.K, self.fmt)].view(-1, kt, 32, 4, 4)
+        return s.permute(0, 3, 2, 1, 4).reshape(-1, kt * 4)[:r, :b]
+
+    def _pitch(self):
+        c = self.codes
+        return c.stride(0) if c.shape[0] > 1 else (c.shape[1] + 15) // 16 * 16
+
+    def _gp(self):
+        return None if self.tensor_scale is None else self.tensor_scale.data_ptr()
+
+
+def _check_tensor_scale(ts, fmt):
+    if ts is None:
+        return
+    import torch
+    if fmt != "nvfp4":
+        raise ValueError("only nvfp4 has a tensor scale")
+    if ts.dtype != torch.float32 or ts.numel() != 1 or not ts.is_cuda:
+        raise ValueError("tensor_scale is a float32 device tensor of one element")
+
+
+def dropout(x, p, seed, offset=0, residual=None, out=None, stream=None):
+    """``x`` with each element dropped with probability ``p`` (kept ones scaled so
+    that the expectation is x's), plus ``residual`` if given; float32, bfloat16
+    or float16 (rows, cols).  The mask is a function of (seed, offset, row,
+    column) and is never stored: the backward pass is the same call on the
+    gradient.  ``out`` may be ``x`` or ``residual``."""
+    import torch
+    code = _type_of(x.dtype)
+    ldx = _rows_of(x, "x")
+    ldr, rp = 0, None
+    for t, name in ((residual, "residual"), (out, "out")):
+        if t is not None and (t.dtype != x.dtype or t.shape != x.shape or t.device != x.device):
+            raise ValueError(f"{name} must have x's shape, dtype and device")
+    if residual is not None:
+        ldr, rp = _rows_of(residual, "residual"), residual.data_ptr()
+    y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    rows, cols = x.shape
+    with _Guard(x):
+        ptc_dropout(rows, cols, x.data_ptr(), ldx, rp, ldr, y.data_ptr(), _rows_of(y, "out"), code, float(p),
+                    int(seed) & _MASK64, int(offset), _on(stream, x))
+    return y
+
+
+def _new_fp4(rows, cols, fmt, device, ts):
+    """An uninitialised matrix; codes and scales share one allocation."""
+    import torch
+    width = -(-cols // 32) * 16
+    buf = torch.empty(rows * width + fp4_scale_bytes(rows, cols, fmt), dtype=torch.uint8, device=device)
+    q = Fp4Matrix.__new__(Fp4Matrix)
+    q.codes, q.scales = buf[:rows * width].view(rows, width), buf[rows * width:]
+    q.K, q.fmt, q.tensor_scale = cols, fmt, ts
+    return q
+
+
+def quantize_fp4(x, fmt="mxfp4", transposed=False, rounding="nearest", tensor_scale=None, p=0.0, seed=0, offset=0,
+                 stream=None):
+    """``x`` (rows, cols) as a microscaled 4-bit :class:`Fp4Matrix`.
+
+    transposed: False for blocks along the rows of x; True for the matrix of
+        x's columns (cols, rows), which a product that contracts over x's rows
+        takes; "both" for the pair (one pass over x).
+    rounding: "nearest" (ties to even) or "stochastic" (bits from seed, offset).
+    p: with p > 0 the values are ``dropout(x, p, seed, offset)`` in float32.
+    """
+    if fmt not in _FP4:
+        raise ValueError("fmt is 'mxfp4' or 'nvfp4'")
+    if rounding not in _ROUNDING:
+        raise ValueError("rounding is 'nearest' or 'stochastic'")
+    if transposed not in (False, True, "both"):
+        raise ValueError("transposed is False, True or 'both'")
+    code = _type_of(x.dtype)
+    ldx = _rows_of(x, "x")
+    _check_tensor_scale(tensor_scale, fmt)
+    if tensor_scale is not None and tensor_scale.device != x.device:
+        raise ValueError("tensor_scale must be on x's device")
+    rows, cols = x.shape
+    q = _new_fp4(rows, cols, fmt, x.device, tensor_scale) if transposed is not True else None
+    qt = _new_fp4(cols, rows, fmt, x.device, tensor_scale) if transposed is not False else None
+    with _Guard(x):
+        ptc_quantize_fp4(rows, cols, x.data_ptr(), ldx, code, _FP4[fmt][0], _ROUNDING[rounding],
+                         None if tensor_scale is None else tensor_scale.data_ptr(),
+                         q and q.codes.data_ptr(), q._pitch() if q else 0, q and q.scales.data_ptr(),
+                         qt and qt.codes.data_ptr(), qt._pitch() if qt else 0, qt and qt.scales.data_ptr(),
+                         float(p), int(seed) & _MASK64, int(offset), _on(stream, x))
+    return (q, qt) if transposed == "both" else (qt if transposed else q)
+
+
+def dequantize_fp4(q, dtype=None, out=None, stream=None):
+    """The values of an :class:`Fp4Matrix` as float32, bfloat16 (default) or float16."""
+    import torch
+    if out is not None:
+        if out.shape != q.shape or out.device != q.device:
+            raise ValueError("out must have the matrix's shape and device")
+        dtype = out.dtype
+    dtype = dtype or torch.bfloat16
+    code = _type_of(dtype)
+    y = out if out is not None else torch.empty(q.shape, dtype=dtype, device=q.device)
+    with _Guard(y):
+        ptc_dequantize_fp4(q.shape[0], q.K, q.codes.data_ptr(), q._pitch(), q.scales.data_ptr(), _FP4[q.fmt][0],
+                           q._gp(), y.data_ptr(), _rows_of(y, "out"), code, _on(stream, y))
+    return y
+
+
+def _result(out, shape, dtype, device):
+    import torch
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(out.shape) != shape or out.device != device:
+        raise ValueError(f"out must be a {shape} tensor on the operands' device")
+    return out
+
+
+def matmul_fp4(A, Bt, out_dtype=None, out=None, stream=None):
+    """A (M,K) @ B with B given as Bt (N,K), both :class:`Fp4Matrix` of one format
+    -> float32, bfloat16 (default) or float16 (M,N), summed in FP32 on the
+    block-scaled tensor cores."""
+    import torch
+    if A.fmt != Bt.fmt:
+        raise ValueError("both matrices must have the same format")
+    if A.K != Bt.K:
+        raise ValueError("inner dimensions differ")
+    if A.device != Bt.device:
+        raise ValueError("both matrices must be on one device")
+    dt = out.dtype if out is not None else (out_dtype or torch.bfloat16)
+    code = _type_of(dt)
+    M, N = A.codes.shape[0], Bt.codes.shape[0]
+    C = _result(out, (M, N), dt, A.device)
+    with _Guard(C):
+        gemm_fp4(M, N, A.K, _FP4[A.fmt][0], A.codes.data_ptr(), A._pitch(), A.scales.data_ptr(), A._gp(),
+                 Bt.codes.data_ptr(), Bt._pitch(), Bt.scales.data_ptr(), Bt._gp(), C.data_ptr(), _rows_of(C, "out"),
+                 code, _on(stream, C))
+    return C
+
+
+def matmul_a16_fp4(x, Wt, out=None, stream=None):
+    """x (M,K) bfloat16 or float16 @ W given as Wt (N,K) :class:`Fp4Matrix` -> x's
+    dtype (M,N), summed in FP32: the product of a decoding step, for M up to 16
+    rows (more are taken 16 at a time; quantise x and use :func:`matmul_fp4`
+    for many)."""
+    import torch
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("matmul_a16_fp4 takes bfloat16 or float16 activations")
+    ldx = _rows_of(x, "x")
+    if x.shape[1] != Wt.K:
+        raise ValueError("inner dimensions differ")
+    if x.device != Wt.device or (out is not None and out.dtype != x.dtype):
+        raise ValueError("x, the weights and out must share a device, x and out a dtype")
+    M, N = x.shape[0], Wt.codes.shape[0]
+    C = _result(out, (M, N), x.dtype, x.device)
+    with _Guard(C):
+        gemm_a16_fp4(M, N, Wt.K, _type_of(x.dtype), x.data_ptr(), ldx, _FP4[Wt.fmt][0], Wt.codes.data_ptr(),
+                     Wt._pitch(), Wt.scales.data_ptr(), Wt._gp(), C.data_ptr(), _rows_of(C, "out"), _on(stream, C))
+    return C

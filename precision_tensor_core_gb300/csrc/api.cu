@@ -440,6 +440,37 @@ int encode_tmap_2d(CUtensorMap *map, bool one_byte, const void *base, uint64_t i
     return make_tmap(map, one_byte ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                      base, inner, outer, pitch, box_inner, box_outer);
 }
+int encode_tmap_scales(CUtensorMap *map, const void *base, uint64_t ktiles, uint64_t rtiles, uint32_t box_k,
+                       uint32_t box_r) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return fail(PTC_ERR_LAUNCH, "cuTensorMapEncodeTiled unavailable");
+    cuuint64_t dims[3] = {128, ktiles, rtiles};  // 32-bit words of a tile, tiles along K, along the rows
+    cuuint64_t strides[2] = {512, ktiles * 512};
+    cuuint32_t box[3] = {128, box_k, box_r};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void *>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        std::snprintf(g_msg, sizeof(g_msg), "cuTensorMapEncodeTiled failed (CUresult %d)", int(r));
+        return PTC_ERR_LAUNCH;
+    }
+    return PTC_OK;
+}
+int fail_status(int code, const char *text) { return fail(code, text); }
+int fail_launch(cudaError_t e, const char *what) { return fail_cuda(e, what); }
+int usable_device(int *sms) {
+    int dev;
+    DevInfo *d;
+    const int rc = current_device(&dev, &d);
+    if (!rc) *sms = d->sms;
+    return rc;
+}
+bool pdl_enabled() { return g_pdl.load() != 0; }
+uint64_t wait_limit_ns() { return g_wait_ns.load(); }
+int take_stall_tile() { return int(g_stall_tile.exchange(-1)); }
+uint64_t span_of(int64_t rows, int64_t cols, int64_t ld, int esize) { return span_bytes(rows, cols, ld, esize, 1); }
+bool ranges_overlap(const void *a, uint64_t alen, const void *b, uint64_t blen) { return overlaps(a, alen, b, blen); }
 }  // namespace ptc
 
 namespace {
@@ -1059,7 +1090,10 @@ int gemm_poll_device_error(void) {
     uint32_t w = 0;
     cudaError_t e = ptc::read_and_clear_error_word(&w);
     if (e != cudaSuccess) return fail_cuda(e, "reading the device error word");
-    return w ? PTC_ERR_TIMEOUT : PTC_OK;
+    uint32_t w4 = 0;
+    e = ptc::read_and_clear_fp4_error_word(&w4);
+    if (e != cudaSuccess) return fail_cuda(e, "reading the device error word");
+    return (w | w4) ? PTC_ERR_TIMEOUT : PTC_OK;
 }
 
 uint64_t ptc_kernel_launch_count(void) { return g_launches.load(); }
@@ -1208,6 +1242,7 @@ int ptc_set_tuning(const char *key, int64_t value) {
         g_cta_pair.store(int(value));
         return PTC_OK;
     }
+    if (ptc::set_fp4_tuning(key, value)) return PTC_OK;
     return fail(PTC_ERR_INVALID, "unknown tuning key or value out of range");
 }
 

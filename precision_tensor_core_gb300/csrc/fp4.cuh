@@ -1,0 +1,242 @@
+// fp4.cuh -- device primitives of the microscaled 4-bit formats and of the
+// counter-based generator: E2M1 codes, block scales, the tiled scale layout,
+// and 16 random bits per element.
+//
+// Formats (include/ptc.h, "Microscaled 4-bit matrices"): a block of
+// consecutive elements of a row shares one scale byte,
+//   mxfp4  32 elements, scale 2^(byte - 127), 0xFF: NaN
+//   nvfp4  16 elements, E4M3 scale, 0x7F: NaN, and one FP32 scale per matrix
+// and each element is an E2M1 code (sign, 0 / 0.5 / 1 / 1.5 / 2 / 3 / 4 / 6).
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace ptc {
+
+// ------------------------------------------------------------ generator
+// Philox4x32-10 (Salmon, Moraes, Dror, Shaw: "Parallel random numbers: as easy
+// as 1, 2, 3", SC 2011): ten rounds of two 32 x 32 -> 64-bit products.  One
+// call gives the 16 bits of eight consecutive elements of a row.
+__device__ __forceinline__ uint4 philox10(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t k0,
+                                          uint32_t k1) {
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+        const uint64_t p0 = uint64_t(0xD2511F53u) * c0, p1 = uint64_t(0xCD9E8D57u) * c2;
+        c0 = uint32_t(p1 >> 32) ^ c1 ^ k0;
+        c1 = uint32_t(p1);
+        c2 = uint32_t(p0 >> 32) ^ c3 ^ k1;
+        c3 = uint32_t(p0);
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return make_uint4(c0, c1, c2, c3);
+}
+
+// What a stream of random bits is for: its own counters for each.
+constexpr uint32_t kRngDropout = 0, kRngRounding = 1;
+
+struct RngArgs {
+    uint32_t k0, k1;          // seed
+    uint32_t off_lo, off_hi;  // offset (63 bits)
+};
+
+// The 16-bit numbers of elements (row, 8 group .. 8 group + 7): element j has
+// bits 16 (j & 1) .. of word j >> 1.
+__device__ __forceinline__ uint4 random_bits8(const RngArgs &g, uint32_t purpose, uint32_t row, uint32_t group) {
+    return philox10(group, row, g.off_lo, g.off_hi | (purpose << 31), g.k0, g.k1);
+}
+
+__device__ __forceinline__ uint32_t bits16(const uint4 &w, int j) {
+    const uint32_t x = (j >> 1) == 0 ? w.x : (j >> 1) == 1 ? w.y : (j >> 1) == 2 ? w.z : w.w;
+    return (j & 1) ? x >> 16 : x & 0xFFFFu;
+}
+
+// ------------------------------------------------------------ element types
+enum class Elem : int { F32 = 0, BF16 = 1, F16 = 2 };  // the values of PTC_OUT_*
+
+template <Elem E>
+struct ElemOf;
+template <>
+struct ElemOf<Elem::F32> {
+    using type = float;
+};
+template <>
+struct ElemOf<Elem::BF16> {
+    using type = __nv_bfloat16;
+};
+template <>
+struct ElemOf<Elem::F16> {
+    using type = __half;
+};
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+
+template <typename T>
+__device__ __forceinline__ T from_float(float v);
+template <>
+__device__ __forceinline__ float from_float<float>(float v) {
+    return v;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) {
+    return __float2bfloat16_rn(v);
+}
+template <>
+__device__ __forceinline__ __half from_float<__half>(float v) {
+    return __float2half_rn(v);
+}
+
+// Eight consecutive elements as they lie in memory (16 or 32 bytes).
+template <typename T>
+struct Pack8 {
+    static constexpr int W = sizeof(T) * 8 / 16;
+    uint4 v[W];
+    __device__ __forceinline__ T get(int j) const { return reinterpret_cast<const T *>(v)[j]; }
+    __device__ __forceinline__ void set(int j, T x) { reinterpret_cast<T *>(v)[j] = x; }
+};
+
+// `n` (1 .. 8) elements at p; the others +0.  `vec`: p is 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ Pack8<T> load8(const T *p, int n, bool vec) {
+    Pack8<T> r;
+    if (vec && n >= 8) {
+#pragma unroll
+        for (int w = 0; w < Pack8<T>::W; ++w) r.v[w] = reinterpret_cast<const uint4 *>(p)[w];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r.set(j, j < n ? p[j] : from_float<T>(0.0f));
+    }
+    return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T *p, const Pack8<T> &r, int n, bool vec) {
+    if (vec && n >= 8) {
+#pragma unroll
+        for (int w = 0; w < Pack8<T>::W; ++w) reinterpret_cast<uint4 *>(p)[w] = r.v[w];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n) p[j] = r.get(j);
+    }
+}
+
+// ------------------------------------------------------------ scales
+constexpr int kScaleTile = 512;  // bytes of a tile of 128 rows x 4 blocks
+
+// Offset of row r's four scale bytes of blocks 4 kt .. 4 kt + 3.
+__host__ __device__ __forceinline__ int64_t scale_word(int64_t r, int64_t kt, int64_t ktiles) {
+    return ((r >> 7) * ktiles + kt) * kScaleTile + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+}
+
+// A scale byte as FP32.
+template <bool NV>
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+    if constexpr (NV) {
+        uint32_t h;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(byte)));
+        return __half2float(__ushort_as_half(uint16_t(h)));
+    } else {
+        return byte == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte == 0u ? 0x00400000u : byte << 23);
+    }
+}
+
+constexpr uint32_t kInfBits = 0x7F800000u;
+
+// A block's scale: the reciprocal it is applied by, and for nvfp4 the scale.
+template <bool NV>
+struct BlockScale {
+    float inverse, d;
+    // x / scale rounded to FP32.  mxfp4 scales are powers of two, so the
+    // product is exact; for nvfp4 the product with the rounded reciprocal is
+    // corrected by its remainder (Markstein, "Computation of elementary
+    // functions on the IBM RISC System/6000 processor", 1990), without which
+    // exact midpoints of the codes could fall to either side.
+    __device__ __forceinline__ float apply(float x) const {
+        const float q = __fmul_rn(x, inverse);
+        if constexpr (!NV) return q;
+        // (Far above the largest code, where the remainder could overflow, q saturates as it is.)
+        return fabsf(q) < 16.0f ? __fmaf_rn(__fmaf_rn(-q, d, x), inverse, q) : q;
+    }
+};
+
+// Scale byte and scale of a block whose largest magnitude has the
+// FP32 bits `amax` (at least kInfBits: some element is not finite).
+//   mxfp4, nearest:    2^(floor(log2 amax) - 2): elements in (6, 8) x scale
+//                      saturate, the rule of the OCP microscaling format
+//   mxfp4, stochastic: the least power of two with amax <= 6 x scale, so that
+//                      no element saturates and the rounding has no bias
+//   nvfp4:             amax / (6 G) rounded to E4M3 (stochastic: up to the next
+//                      one where amax would saturate), G the matrix scale
+template <bool NV, bool SR>
+__device__ __forceinline__ BlockScale<NV> block_scale(uint32_t amax, float g, uint32_t &byte) {
+    BlockScale<NV> s{0.0f, 0.0f};
+    const bool finite = amax < kInfBits;
+    if constexpr (!NV) {
+        int e = int(amax >> 23) - 2;
+        if constexpr (SR) e += (amax & 0x7FFFFFu) > 0x400000u ? 1 : 0;
+        e = e < 0 ? 0 : e;
+        byte = finite ? uint32_t(e) : 255u;
+        s.inverse = __uint_as_float(uint32_t(254 - (finite ? e : 0)) << 23);
+    } else {
+        const float a = __uint_as_float(amax), six = __fmul_rn(g, 6.0f);
+        uint16_t q;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(q) : "f"(0.0f), "f"(__fdiv_rn(a, six)));
+        uint32_t b = q & 0x7Fu;
+        if constexpr (SR)
+            if (__fmul_rn(six, scale_value<true>(b)) < a && b < 0x7Eu) ++b;
+        s.d = __fmul_rn(scale_value<true>(b), g);
+        byte = finite ? b : 0x7Fu;
+        s.inverse = s.d > 0.0f ? __frcp_rn(s.d) : 0.0f;
+    }
+    return s;
+}
+
+// ------------------------------------------------------------ codes
+// Eight FP32 values to eight codes, nearest with ties to even, at most 6 in
+// magnitude; value j in bits 4 j .. 4 j + 3.
+__device__ __forceinline__ uint32_t codes_nearest(const float (&v)[8]) {
+    uint32_t q;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(q)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return q;
+}
+
+// One value rounded down or up to the neighbouring codes, up when its
+// remainder (in 1/65536 of the gap) plus r reaches 65536.  The gaps are 0.5
+// below 2, 1 below 4 and 2 below 6; scaling by 1 / gap, floor and remainder
+// are exact, so the result is a function of the value and r alone.
+__device__ __forceinline__ uint32_t code_stochastic(float v, uint32_t r) {
+    const float u = fminf(fabsf(v), 6.0f);
+    const bool low2 = u < 2.0f, low4 = u < 4.0f;
+    const float t = u * (low2 ? 2.0f : low4 ? 1.0f : 0.5f);
+    const float f = floorf(t);
+    const bool up = (t - f) * 65536.0f >= float(65536u - r);
+    const uint32_t code = (low2 ? 0u : low4 ? 2u : 4u) + uint32_t(f) + (up ? 1u : 0u);
+    return code | ((__float_as_uint(v) >> 28) & 8u);
+}
+
+// Eight codes (a 32-bit word) as eight binary16 values, exactly: word i of the
+// result holds values 2 i (low half) and 2 i + 1.
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+
+}  // namespace ptc

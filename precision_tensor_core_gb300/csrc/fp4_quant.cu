@@ -1,0 +1,602 @@
+// fp4_quant.cu -- dropout, quantisation to the microscaled 4-bit formats and
+// the way back (ptc_dropout, ptc_quantize_fp4, ptc_dequantize_fp4 of
+// include/ptc.h).  All of them read and write each byte once and are bound by
+// memory traffic; the random numbers are made where they are used, so no mask
+// is ever stored.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <cstring>
+
+#include "fp4.cuh"
+#include "internal.h"
+#include "ptc.h"
+#include "ptx.cuh"
+
+namespace ptc {
+namespace {
+
+// Position of a thread in a rows x groups walk with a fixed stride: one
+// division at the start, additions after it.
+struct Walk {
+    int64_t row, drow;
+    uint32_t group, dgroup, groups;
+    __device__ __forceinline__ Walk(int64_t index, int64_t stride, uint32_t groups_) : groups(groups_) {
+        row = index / groups;
+        group = uint32_t(index - row * groups);
+        drow = stride / groups;
+        dgroup = uint32_t(stride - drow * groups);
+    }
+    __device__ __forceinline__ void next() {
+        row += drow;
+        group += dgroup;
+        if (group >= groups) {
+            group -= groups;
+            ++row;
+        }
+    }
+};
+
+struct DropArgs {
+    uint32_t kept;  // of 65536; 65536: nothing is dropped
+    float scale;    // 65536 / kept
+    RngArgs rng;
+};
+
+// ------------------------------------------------------------ dropout
+// y = [r < kept] x * (65536 / kept) (+ residual), eight elements of a row per
+// step: 2 to 3 times 16 bytes of traffic and one generator call (ten rounds,
+// about 70 integer instructions, under the ~170 that eight 16-bit elements'
+// traffic leaves time for).
+template <typename T, bool RES>
+__global__ void __launch_bounds__(256) dropout_kernel(const T *x, int64_t ldx, const T *res, int64_t ldr, T *y,
+                                                      int64_t ldy, int64_t rows, int64_t cols, DropArgs d, int vec) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const uint32_t groups = uint32_t((cols + 7) / 8);
+    Walk w(int64_t(blockIdx.x) * blockDim.x + threadIdx.x, int64_t(gridDim.x) * blockDim.x, groups);
+    for (; w.row < rows; w.next()) {
+        const int64_t c = int64_t(w.group) * 8;
+        const int n = int(min(int64_t(8), cols - c));
+        const Pack8<T> a = load8(x + w.row * ldx + c, n, vec != 0);
+        Pack8<T> r, o;
+        if constexpr (RES) r = load8(res + w.row * ldr + c, n, vec != 0);
+        const uint4 bits = random_bits8(d.rng, kRngDropout, uint32_t(w.row), w.group);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            // Selected, not multiplied by zero: a dropped infinity or NaN leaves +0.
+            float v = bits16(bits, j) < d.kept ? __fmul_rn(to_float(a.get(j)), d.scale) : 0.0f;
+            if constexpr (RES) v = __fadd_rn(v, to_float(r.get(j)));
+            o.set(j, from_float<T>(v));
+        }
+        store8(y + w.row * ldy + c, o, n, vec != 0);
+    }
+}
+
+// ------------------------------------------------------------ quantisation
+struct QuantArgs {
+    int64_t rows, cols, ldx;
+    uint8_t *codes;   // rows of the matrix: codes, pitch, tiled scales
+    int64_t pitch;
+    uint8_t *scales;
+    uint8_t *codes_t;  // its columns
+    int64_t pitch_t;
+    uint8_t *scales_t;
+    const float *g;  // matrix scale (NULL: 1)
+    DropArgs drop;
+    int vec;
+};
+
+// FP32 values of eight loaded elements after dropout.
+template <typename T, bool DROP>
+__device__ __forceinline__ void dropped8(const Pack8<T> &a, const DropArgs &d, int64_t row, uint32_t group,
+                                         float (&v)[8]) {
+    if constexpr (DROP) {
+        const uint4 bits = random_bits8(d.rng, kRngDropout, uint32_t(row), group);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = bits16(bits, j) < d.kept ? __fmul_rn(to_float(a.get(j)), d.scale) : 0.0f;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = to_float(a.get(j));
+    }
+}
+
+__device__ __forceinline__ uint32_t max_abs8(const float (&v)[8]) {
+    uint32_t m = 0;  // of the bits, so that infinities and NaN come out on top
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    return m;
+}
+
+// Eight codes of values v with the block's scale.
+template <bool NV, bool SR>
+__device__ __forceinline__ uint32_t codes8(const float (&v)[8], uint32_t amax, const BlockScale<NV> &scale,
+                                           const uint4 &bits) {
+    uint32_t q = 0;
+    if constexpr (SR) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q |= code_stochastic(scale.apply(v[j]), bits16(bits, j)) << (4 * j);
+    } else {
+        float s[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = scale.apply(v[j]);
+        q = codes_nearest(s);
+    }
+    return amax < kInfBits ? q : 0u;
+}
+
+// Rows only.  A warp takes 256 columns of a row, a lane eight of them: the
+// block's maximum by one or two shuffles, codes as 4 bytes per lane (128
+// contiguous bytes per warp), scales gathered to one 4-byte store per tile.
+// Rows past the last one to the end of the scale tile get zero scales.
+template <typename T, bool NV, bool SR, bool DROP>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const T *x, const QuantArgs a) {
+    griddep_wait();
+    griddep_launch_dependents();
+    constexpr int LPB = NV ? 2 : 4;          // lanes per block
+    constexpr int LPT = 4 * LPB;             // lanes per scale word
+    const int lane = threadIdx.x & 31;
+    const float g = (NV && a.g != nullptr) ? __ldg(a.g) : 1.0f;
+    const int64_t ktiles = (a.cols + 8 * LPT - 1) / (8 * LPT);
+    const int64_t rows_p = (a.rows + 127) / 128 * 128;
+    const int64_t cols_p = (a.cols + 31) / 32 * 32;
+    Walk w((int64_t(blockIdx.x) * blockDim.x + threadIdx.x) / 32, int64_t(gridDim.x) * blockDim.x / 32,
+           uint32_t((a.cols + 255) / 256));
+    for (; w.row < rows_p; w.next()) {
+        const int64_t c = int64_t(w.group) * 256 + lane * 8;
+        const bool real = w.row < a.rows;
+        uint32_t word = 0;
+        if (real) {  // uniform over the warp
+            const int n = int(max(int64_t(0), min(int64_t(8), a.cols - c)));
+            const Pack8<T> p = load8(x + w.row * a.ldx + (n > 0 ? c : 0), n, a.vec != 0);
+            float v[8];
+            dropped8<T, DROP>(p, a.drop, w.row, uint32_t(c / 8), v);
+            if constexpr (DROP) {
+                if (n < 8) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j >= n) v[j] = 0.0f;
+                }
+            }
+            uint32_t m = max_abs8(v);
+            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+            if constexpr (!NV) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+            uint32_t byte;
+            const BlockScale<NV> scale = block_scale<NV, SR>(m, g, byte);
+            uint4 bits = make_uint4(0, 0, 0, 0);
+            if constexpr (SR) bits = random_bits8(a.drop.rng, kRngRounding, uint32_t(w.row), uint32_t(c / 8));
+            const uint32_t q = codes8<NV, SR>(v, m, scale, bits);
+            if (c < cols_p) *reinterpret_cast<uint32_t *>(a.codes + w.row * a.pitch + c / 2) = q;
+            // Four blocks' bytes to one word (held by the first lane of the four).
+            word = byte;
+            word |= __shfl_down_sync(0xFFFFFFFFu, word, LPB) << 8;
+            word |= __shfl_down_sync(0xFFFFFFFFu, word, 2 * LPB) << 16;
+        }
+        const int64_t kt = (int64_t(w.group) * 32 + lane) / LPT;
+        if (lane % LPT == 0 && kt < ktiles)
+            *reinterpret_cast<uint32_t *>(a.scales + scale_word(w.row, kt, ktiles)) = word;
+    }
+}
+
+// Columns (and rows).  A CTA takes 128 x 128 elements: read once, dropped out,
+// kept in shared memory as they came (dropped ones +0) beside their rounding
+// bits; rows are quantised on the way in (16 lanes per row), columns from
+// shared memory, where consecutive lanes hold consecutive columns.
+constexpr int kTile = 128;
+
+template <typename T, bool SR>
+constexpr size_t tile_smem() {
+    return size_t(kTile) * kTile * (sizeof(T) + (SR ? 2 : 0));
+}
+
+template <typename T, bool NV, bool SR, bool DROP, bool ROWS>
+__global__ void __launch_bounds__(256) quantize_tile_kernel(const T *x, const QuantArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    T *xs = reinterpret_cast<T *>(smem);
+    uint16_t *rs = reinterpret_cast<uint16_t *>(smem + size_t(kTile) * kTile * sizeof(T));
+    griddep_wait();
+    griddep_launch_dependents();
+    constexpr int BPT = NV ? 8 : 4;  // blocks per 128 elements
+    constexpr int KPT = BPT / 4;     // scale words per 128 elements
+    const float g = (NV && a.g != nullptr) ? __ldg(a.g) : 1.0f;
+    const int64_t tiles_c = (a.cols + kTile - 1) / kTile, tiles_r = (a.rows + kTile - 1) / kTile;
+    const int64_t kt_rows = (a.cols + 128 / KPT - 1) / (128 / KPT), kt_cols = (a.rows + 128 / KPT - 1) / (128 / KPT);
+    for (int64_t t = blockIdx.x; t < tiles_r * tiles_c; t += gridDim.x) {
+        const int64_t r0 = t / tiles_c * kTile, c0 = (t % tiles_c) * kTile;
+        const int grp = threadIdx.x & 15;
+#pragma unroll 2
+        for (int lr = threadIdx.x / 16; lr < kTile; lr += 16) {
+            const int64_t r = r0 + lr, c = c0 + grp * 8;
+            const int n = r < a.rows ? int(max(int64_t(0), min(int64_t(8), a.cols - c))) : 0;
+            Pack8<T> p = load8(x + (n > 0 ? r * a.ldx + c : 0), n, a.vec != 0);
+            if constexpr (DROP) {
+                const uint4 bits = random_bits8(a.drop.rng, kRngDropout, uint32_t(r), uint32_t(c / 8));
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (bits16(bits, j) >= a.drop.kept) p.set(j, from_float<T>(0.0f));
+            }
+            uint4 bits = make_uint4(0, 0, 0, 0);
+            if constexpr (SR) {
+                bits = random_bits8(a.drop.rng, kRngRounding, uint32_t(r), uint32_t(c / 8));
+                *reinterpret_cast<uint4 *>(rs + lr * kTile + grp * 8) = bits;
+            }
+#pragma unroll
+            for (int i = 0; i < Pack8<T>::W; ++i)
+                reinterpret_cast<uint4 *>(xs + lr * kTile + grp * 8)[i] = p.v[i];
+            if constexpr (ROWS) {
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = DROP ? __fmul_rn(to_float(p.get(j)), a.drop.scale) : to_float(p.get(j));
+                uint32_t m = max_abs8(v);
+                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+                if constexpr (!NV) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+                uint32_t byte;
+                const BlockScale<NV> scale = block_scale<NV, SR>(m, g, byte);
+                const uint32_t q = codes8<NV, SR>(v, m, scale, bits);
+                if (r < a.rows && c < (a.cols + 31) / 32 * 32)
+                    *reinterpret_cast<uint32_t *>(a.codes + r * a.pitch + c / 2) = q;
+                constexpr int LPB = NV ? 2 : 4;
+                uint32_t word = r < a.rows ? byte : 0u;
+                word |= __shfl_down_sync(0xFFFFFFFFu, word, LPB) << 8;
+                word |= __shfl_down_sync(0xFFFFFFFFu, word, 2 * LPB) << 16;
+                const int64_t kt = c0 / (128 / KPT) + grp / (4 * LPB);
+                if (grp % (4 * LPB) == 0 && kt < kt_rows)
+                    *reinterpret_cast<uint32_t *>(a.scales + scale_word(r, kt, kt_rows)) = word;
+            }
+        }
+        __syncthreads();
+        // Column c0 + lc, rows 64 half .. + 63: two units of 32 rows.
+        const int lc = threadIdx.x & 127, half = threadIdx.x >> 7;
+        const int64_t col = c0 + lc;
+        uint32_t bytes[2 * BPT / 4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int lr = half * 64 + u * 32;
+            uint32_t q[4];
+#pragma unroll
+            for (int b = 0; b < (NV ? 2 : 1); ++b) {
+                constexpr int BS = NV ? 16 : 32;
+                float v[BS];
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 0; i < BS; ++i) {
+                    const float f = to_float(xs[(lr + b * BS + i) * kTile + lc]);
+                    v[i] = DROP ? __fmul_rn(f, a.drop.scale) : f;
+                    m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+                }
+                uint32_t byte;
+                const BlockScale<NV> scale = block_scale<NV, SR>(m, g, byte);
+                bytes[u * (BPT / 4) + b] = byte;
+#pragma unroll
+                for (int w = 0; w < BS / 8; ++w) {
+                    uint32_t code = 0;
+                    if constexpr (SR) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            code |= code_stochastic(scale.apply(v[8 * w + j]),
+                                                    rs[(lr + b * BS + 8 * w + j) * kTile + lc])
+                                    << (4 * j);
+                    } else {
+                        float s[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) s[j] = scale.apply(v[8 * w + j]);
+                        code = codes_nearest(s);
+                    }
+                    q[b * (BS / 8) + w] = m < kInfBits ? code : 0u;
+                }
+            }
+            if (col < a.cols && r0 + lr < a.rows)
+                *reinterpret_cast<uint4 *>(a.codes_t + col * a.pitch_t + (r0 + lr) / 2) =
+                    make_uint4(q[0], q[1], q[2], q[3]);
+        }
+        // This half's scale bytes: two of a word (mxfp4) or a whole word (nvfp4).
+        const bool real = col < a.cols;
+        const int64_t kt = r0 / (128 / KPT) + (NV ? half : 0);
+        if (kt < kt_cols) {
+            uint8_t *dst = a.scales_t + scale_word(col, kt, kt_cols);
+            if constexpr (NV)
+                *reinterpret_cast<uint32_t *>(dst) =
+                    real ? bytes[0] | (bytes[1] << 8) | (bytes[2] << 16) | (bytes[3] << 24) : 0u;
+            else
+                *reinterpret_cast<uint16_t *>(dst + 2 * half) = real ? uint16_t(bytes[0] | (bytes[1] << 8)) : uint16_t(0);
+        }
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------ back to values
+// value = code x scale (x matrix scale), each product in FP32, rounded once
+// more to the output type; eight elements per step.
+template <typename T, bool NV>
+__global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *codes, int64_t pitch, const uint8_t *scales,
+                                                         const float *gp, int64_t rows, int64_t cols, T *y,
+                                                         int64_t ldy, int vec) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const bool has_g = gp != nullptr;
+    const float g = has_g ? __ldg(gp) : 1.0f;
+    constexpr int GPB = NV ? 2 : 4;  // groups of eight per block
+    const int64_t blocks = (cols + 8 * GPB - 1) / (8 * GPB), ktiles = (blocks + 3) / 4;
+    Walk w(int64_t(blockIdx.x) * blockDim.x + threadIdx.x, int64_t(gridDim.x) * blockDim.x,
+           uint32_t((cols + 7) / 8));
+    for (; w.row < rows; w.next()) {
+        const int64_t c = int64_t(w.group) * 8;
+        const int n = int(min(int64_t(8), cols - c));
+        const uint32_t q = *reinterpret_cast<const uint32_t *>(codes + w.row * pitch + c / 2);
+        const uint32_t b = w.group / GPB;
+        const float s = scale_value<NV>(scales[scale_word(w.row, b >> 2, ktiles) + (b & 3)]);
+        uint32_t h[4];
+        codes_to_f16(q, h);
+        Pack8<T> o;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float f = __half2float(__ushort_as_half(uint16_t((j & 1) ? h[j >> 1] >> 16 : h[j >> 1] & 0xFFFFu)));
+            float v = __fmul_rn(f, s);
+            if (has_g) v = __fmul_rn(v, g);
+            o.set(j, from_float<T>(v));
+        }
+        store8(y + w.row * ldy + c, o, n, vec != 0);
+    }
+}
+
+// ------------------------------------------------------------ host side
+constexpr int64_t kMaxDim = int64_t(1) << 30;
+constexpr int64_t kMaxLd = int64_t(1) << 36;
+
+int elem_bytes(int type) { return type == PTC_OUT_F32 ? 4 : 2; }
+bool known_type(int type) { return type == PTC_OUT_F32 || type == PTC_OUT_BF16 || type == PTC_OUT_F16; }
+bool multiple_of(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// 16-byte accesses: base and row pitch are multiples of 16 bytes.
+bool wide_rows(const void *p, int64_t ld, int esize) { return multiple_of(p, 16) && (ld * esize) % 16 == 0; }
+
+template <typename... P, typename... A>
+cudaError_t launch(void (*fn)(P...), int64_t blocks, int threads, size_t smem, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[1];
+    std::memset(&cfg, 0, sizeof(cfg));
+    std::memset(attr, 0, sizeof(attr));
+    cfg.gridDim = dim3(unsigned(blocks), 1, 1);
+    cfg.blockDim = dim3(unsigned(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    if (pdl_enabled()) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.numAttrs = 1;
+    }
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
+    if (e == cudaSuccess) note_launches(1);
+    return e;
+}
+
+int64_t grid_for(int64_t threads, int sms) {
+    const int64_t blocks = (threads + 255) / 256, most = int64_t(sms) * 16;
+    return blocks < most ? blocks : most;
+}
+
+// Dropout probability to the kept count of 65536, the generator's key and counter.
+DropArgs drop_args(double p, uint64_t seed, uint64_t offset) {
+    DropArgs d;
+    d.kept = uint32_t((1.0 - p) * 65536.0 + 0.5);
+    d.scale = float(65536.0 / (d.kept > 0 ? d.kept : 1u));
+    d.rng = {uint32_t(seed), uint32_t(seed >> 32), uint32_t(offset), uint32_t(offset >> 32)};
+    return d;
+}
+
+int check_random(double p, uint64_t offset) {
+    if (!(p >= 0.0 && p <= 1.0)) return fail_status(PTC_ERR_INVALID, "p must be in [0, 1]");
+    if (offset >> 63) return fail_status(PTC_ERR_INVALID, "offset must be below 2^63");
+    return PTC_OK;
+}
+
+template <typename T>
+int run_dropout(int64_t rows, int64_t cols, const void *x, int64_t ldx, const void *res, int64_t ldr, void *y,
+                int64_t ldy, const DropArgs &d, int sms, cudaStream_t s) {
+    const int vec = wide_rows(x, ldx, sizeof(T)) && wide_rows(y, ldy, sizeof(T)) &&
+                    (res == nullptr || wide_rows(res, ldr, sizeof(T)));
+    const int64_t grid = grid_for(rows * ((cols + 7) / 8), sms);
+    const T *xp = static_cast<const T *>(x), *rp = static_cast<const T *>(res);
+    T *yp = static_cast<T *>(y);
+    const cudaError_t e = res ? launch(dropout_kernel<T, true>, grid, 256, 0, s, xp, ldx, rp, ldr, yp, ldy, rows, cols, d, vec)
+                              : launch(dropout_kernel<T, false>, grid, 256, 0, s, xp, ldx, rp, ldr, yp, ldy, rows, cols, d, vec);
+    return e == cudaSuccess ? PTC_OK : fail_launch(e, "dropout launch");
+}
+
+template <typename T, bool NV, bool SR, bool DROP>
+cudaError_t launch_quantize(const T *x, const QuantArgs &a, int sms, cudaStream_t s) {
+    if (a.codes_t == nullptr) {
+        const int64_t warps = (a.rows + 127) / 128 * 128 * ((a.cols + 255) / 256);
+        return launch(quantize_rows_kernel<T, NV, SR, DROP>, grid_for(warps * 32, sms), 256, 0, s, x, a);
+    }
+    const int64_t tiles = ((a.rows + kTile - 1) / kTile) * ((a.cols + kTile - 1) / kTile);
+    const int64_t grid = tiles < int64_t(1) << 30 ? tiles : int64_t(1) << 30;
+    constexpr size_t smem = tile_smem<T, SR>();
+    auto *fn = a.codes ? quantize_tile_kernel<T, NV, SR, DROP, true> : quantize_tile_kernel<T, NV, SR, DROP, false>;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        if (e != cudaSuccess) return e;
+    }
+    return launch(fn, grid, 256, smem, s, x, a);
+}
+
+template <typename T>
+cudaError_t run_quantize(const void *x, const QuantArgs &a, bool nv, bool sr, int sms, cudaStream_t s) {
+    const T *p = static_cast<const T *>(x);
+    const bool drop = a.drop.kept < 65536u;
+    auto go = [&](auto n, auto r) {
+        return drop ? launch_quantize<T, decltype(n)::value, decltype(r)::value, true>(p, a, sms, s)
+                    : launch_quantize<T, decltype(n)::value, decltype(r)::value, false>(p, a, sms, s);
+    };
+    using yes = std::integral_constant<bool, true>;
+    using no = std::integral_constant<bool, false>;
+    if (nv) return sr ? go(yes(), yes()) : go(yes(), no());
+    return sr ? go(no(), yes()) : go(no(), no());
+}
+
+}  // namespace
+
+// Bytes of a matrix's tiled scales.
+uint64_t fp4_scale_bytes(int64_t rows, int64_t cols, bool nv) {
+    const int64_t block = nv ? 16 : 32, blocks = (cols + block - 1) / block;
+    return uint64_t((rows + 127) / 128) * uint64_t((blocks + 3) / 4) * kScaleTile;
+}
+
+// Checks of a 4-bit matrix of `rows` rows of `cols` values.
+int check_fp4(const void *codes, int64_t pitch, const void *scales, const void *g, int64_t rows, int64_t cols, bool nv) {
+    if (!codes || !scales) return fail_status(PTC_ERR_INVALID, "codes or scales is NULL");
+    if (pitch < (cols + 31) / 32 * 16 || pitch > kMaxLd)
+        return fail_status(PTC_ERR_INVALID, "the code pitch must hold whole 32-element blocks (16 bytes each)");
+    if (g && !nv) return fail_status(PTC_ERR_INVALID, "mxfp4 has no matrix scale");
+    if (!multiple_of(codes, 16) || !multiple_of(scales, 16) || pitch % 16)
+        return fail_status(PTC_ERR_ALIGN, "codes, scales must be 16-byte aligned with a code pitch that is a multiple of 16");
+    if (g && !multiple_of(g, 4)) return fail_status(PTC_ERR_ALIGN, "matrix scales must be 4-byte aligned");
+    (void)rows;
+    return PTC_OK;
+}
+
+uint64_t fp4_code_span(int64_t rows, int64_t cols, int64_t pitch) {
+    return span_of(rows, (cols + 31) / 32 * 16, pitch, 1);
+}
+
+}  // namespace ptc
+
+using namespace ptc;
+
+extern "C" {
+
+int ptc_dropout(int64_t rows, int64_t cols, const void *x, int64_t ldx, const void *residual, int64_t ldr, void *y,
+                int64_t ldy, int type, double p, uint64_t seed, uint64_t offset, void *stream) {
+    set_message("");
+    if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim)
+        return fail_status(PTC_ERR_INVALID, "sizes must satisfy 0 <= rows, cols <= 2^30");
+    if (!known_type(type)) return fail_status(PTC_ERR_INVALID, "unknown element type");
+    int rc = check_random(p, offset);
+    if (rc) return rc;
+    if (rows == 0 || cols == 0) return PTC_OK;
+    if (!x || !y) return fail_status(PTC_ERR_INVALID, "x or y is NULL");
+    if (ldx < cols || ldy < cols || (residual && ldr < cols) || ldx > kMaxLd || ldy > kMaxLd || (residual && ldr > kMaxLd))
+        return fail_status(PTC_ERR_INVALID, "leading dimensions must be cols .. 2^36");
+    const int es = elem_bytes(type);
+    if (!multiple_of(x, es) || !multiple_of(y, es) || (residual && !multiple_of(residual, es)))
+        return fail_status(PTC_ERR_ALIGN, "pointers must be aligned to the element");
+    const uint64_t ybytes = span_of(rows, cols, ldy, es);
+    if ((y != x || ldy != ldx) && ranges_overlap(y, ybytes, x, span_of(rows, cols, ldx, es)))
+        return fail_status(PTC_ERR_OVERLAP, "y overlaps x without being x");
+    if (residual && (y != residual || ldy != ldr) && ranges_overlap(y, ybytes, residual, span_of(rows, cols, ldr, es)))
+        return fail_status(PTC_ERR_OVERLAP, "y overlaps the residual without being it");
+    int sms;
+    if ((rc = usable_device(&sms))) return rc;
+    const DropArgs d = drop_args(p, seed, offset);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (type == PTC_OUT_F32) return run_dropout<float>(rows, cols, x, ldx, residual, ldr, y, ldy, d, sms, s);
+    if (type == PTC_OUT_BF16) return run_dropout<__nv_bfloat16>(rows, cols, x, ldx, residual, ldr, y, ldy, d, sms, s);
+    return run_dropout<__half>(rows, cols, x, ldx, residual, ldr, y, ldy, d, sms, s);
+}
+
+int ptc_quantize_fp4(int64_t rows, int64_t cols, const void *x, int64_t ldx, int type, int format, int rounding,
+                     const float *matrix_scale, void *codes, int64_t pitch, void *scales, void *codes_t,
+                     int64_t pitch_t, void *scales_t, double p, uint64_t seed, uint64_t offset, void *stream) {
+    set_message("");
+    if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim)
+        return fail_status(PTC_ERR_INVALID, "sizes must satisfy 0 <= rows, cols <= 2^30");
+    if (!known_type(type)) return fail_status(PTC_ERR_INVALID, "unknown element type");
+    if (format != PTC_FP4_MX && format != PTC_FP4_NV) return fail_status(PTC_ERR_INVALID, "unknown 4-bit format");
+    if (rounding != PTC_ROUND_NEAREST && rounding != PTC_ROUND_STOCHASTIC)
+        return fail_status(PTC_ERR_INVALID, "unknown rounding");
+    int rc = check_random(p, offset);
+    if (rc) return rc;
+    if (rows == 0 || cols == 0) return PTC_OK;
+    if (!x) return fail_status(PTC_ERR_INVALID, "x is NULL");
+    if (!codes && !codes_t) return fail_status(PTC_ERR_INVALID, "neither rows nor columns are asked for");
+    if (ldx < cols || ldx > kMaxLd) return fail_status(PTC_ERR_INVALID, "ldx must be cols .. 2^36");
+    const bool nv = format == PTC_FP4_NV;
+    const int es = elem_bytes(type);
+    if (codes && (rc = check_fp4(codes, pitch, scales, matrix_scale, rows, cols, nv))) return rc;
+    if (codes_t && (rc = check_fp4(codes_t, pitch_t, scales_t, matrix_scale, cols, rows, nv))) return rc;
+    if (!multiple_of(x, es)) return fail_status(PTC_ERR_ALIGN, "x must be aligned to its element");
+    struct Range {
+        const void *p;
+        uint64_t n;
+        bool out;
+    };
+    const Range r[6] = {{x, span_of(rows, cols, ldx, es), false},
+                        {matrix_scale, matrix_scale ? 4u : 0u, false},
+                        {codes, codes ? fp4_code_span(rows, cols, pitch) : 0, true},
+                        {codes ? scales : nullptr, codes ? fp4_scale_bytes(rows, cols, nv) : 0, true},
+                        {codes_t, codes_t ? fp4_code_span(cols, rows, pitch_t) : 0, true},
+                        {codes_t ? scales_t : nullptr, codes_t ? fp4_scale_bytes(cols, rows, nv) : 0, true}};
+    for (int i = 0; i < 6; ++i)
+        for (int j = i + 1; j < 6; ++j)
+            if (r[i].n && r[j].n && r[j].out && ranges_overlap(r[i].p, r[i].n, r[j].p, r[j].n))
+                return fail_status(PTC_ERR_OVERLAP, "an output overlaps another argument");
+    int sms;
+    if ((rc = usable_device(&sms))) return rc;
+    QuantArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.rows = rows;
+    a.cols = cols;
+    a.ldx = ldx;
+    a.codes = static_cast<uint8_t *>(codes);
+    a.pitch = pitch;
+    a.scales = static_cast<uint8_t *>(scales);
+    a.codes_t = static_cast<uint8_t *>(codes_t);
+    a.pitch_t = pitch_t;
+    a.scales_t = static_cast<uint8_t *>(scales_t);
+    a.g = matrix_scale;
+    a.drop = drop_args(p, seed, offset);
+    a.vec = wide_rows(x, ldx, es);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool sr = rounding == PTC_ROUND_STOCHASTIC;
+    const cudaError_t e = type == PTC_OUT_F32    ? run_quantize<float>(x, a, nv, sr, sms, s)
+                          : type == PTC_OUT_BF16 ? run_quantize<__nv_bfloat16>(x, a, nv, sr, sms, s)
+                                                 : run_quantize<__half>(x, a, nv, sr, sms, s);
+    return e == cudaSuccess ? PTC_OK : fail_launch(e, "quantisation launch");
+}
+
+int ptc_dequantize_fp4(int64_t rows, int64_t cols, const void *codes, int64_t pitch, const void *scales, int format,
+                       const float *matrix_scale, void *y, int64_t ldy, int type, void *stream) {
+    set_message("");
+    if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim)
+        return fail_status(PTC_ERR_INVALID, "sizes must satisfy 0 <= rows, cols <= 2^30");
+    if (!known_type(type)) return fail_status(PTC_ERR_INVALID, "unknown element type");
+    if (format != PTC_FP4_MX && format != PTC_FP4_NV) return fail_status(PTC_ERR_INVALID, "unknown 4-bit format");
+    if (rows == 0 || cols == 0) return PTC_OK;
+    const bool nv = format == PTC_FP4_NV;
+    if (!y) return fail_status(PTC_ERR_INVALID, "y is NULL");
+    if (ldy < cols || ldy > kMaxLd) return fail_status(PTC_ERR_INVALID, "ldy must be cols .. 2^36");
+    int rc = check_fp4(codes, pitch, scales, matrix_scale, rows, cols, nv);
+    if (rc) return rc;
+    const int es = elem_bytes(type);
+    if (!multiple_of(y, es)) return fail_status(PTC_ERR_ALIGN, "y must be aligned to its element");
+    const uint64_t yb = span_of(rows, cols, ldy, es);
+    if (ranges_overlap(y, yb, codes, fp4_code_span(rows, cols, pitch)) ||
+        ranges_overlap(y, yb, scales, fp4_scale_bytes(rows, cols, nv)) ||
+        (matrix_scale && ranges_overlap(y, yb, matrix_scale, 4)))
+        return fail_status(PTC_ERR_OVERLAP, "y overlaps an input");
+    int sms;
+    if ((rc = usable_device(&sms))) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int vec = wide_rows(y, ldy, es);
+    const uint8_t *cp = static_cast<const uint8_t *>(codes), *sp = static_cast<const uint8_t *>(scales);
+    const int64_t grid = grid_for(rows * ((cols + 7) / 8), sms);
+    auto go = [&](auto fn, auto *out) {
+        return launch(fn, grid, 256, 0, s, cp, pitch, sp, matrix_scale, rows, cols, out, ldy, vec);
+    };
+    cudaError_t e;
+    if (type == PTC_OUT_F32)
+        e = nv ? go(dequantize_kernel<float, true>, static_cast<float *>(y))
+               : go(dequantize_kernel<float, false>, static_cast<float *>(y));
+    else if (type == PTC_OUT_BF16)
+        e = nv ? go(dequantize_kernel<__nv_bfloat16, true>, static_cast<__nv_bfloat16 *>(y))
+               : go(dequantize_kernel<__nv_bfloat16, false>, static_cast<__nv_bfloat16 *>(y));
+    else
+        e = nv ? go(dequantize_kernel<__half, true>, static_cast<__half *>(y))
+               : go(dequantize_kernel<__half, false>, static_cast<__half *>(y));
+    return e == cudaSuccess ? PTC_OK : fail_launch(e, "dequantisation launch");
+}
+
+}  // extern "C"
