@@ -13,7 +13,9 @@
 // to them.  The issuing thread copies a stage's scale tiles from shared memory
 // into tensor memory (tcgen05.cp, replicated to the four lane quarters) and
 // then issues the stage's four MMAs of 64 codes; copies and MMAs of one
-// thread execute in order.
+// thread execute in order.  The copies cost nothing (8192^3 in mxfp4: 169 us
+// with and without them); writing the scales by four more warps with
+// tcgen05.st took 253 us, for the barriers between them and the issuer.
 //
 // Tiles.  Large products run on CTA pairs (256 x 256 per pair, cta_group::2):
 // each CTA holds 128 rows of A, 128 rows of B and the scales of its A rows and
@@ -122,11 +124,23 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint
 #undef PTC_MMA4
 }
 
+// Shared-memory descriptors as two words: the high word is a constant, the low
+// word the address (in 16 bytes) and the leading offset, so that an operand
+// costs the issuing thread one addition.  K-major rows of 128 bytes in the
+// 128-byte swizzle (eight rows 1024 bytes apart), and unswizzled rows of 16
+// bytes (eight rows 128 bytes apart) for scale tiles.
+constexpr uint32_t kDescLow = 1u << 16;
+constexpr uint32_t kDescHighSw128 = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kDescHighRows16 = (128u >> 4) | (1u << 14);
+
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr) { return (saddr >> 4) | kDescLow; }
+__device__ __forceinline__ uint64_t desc_of(uint32_t low, uint32_t high) { return (uint64_t(high) << 32) | low; }
+
 // One scale tile (32 rows of 16 bytes in shared memory) to four tensor-memory
 // columns of every lane quarter; a pair copies in both CTAs.
 template <int CTAS>
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
-    const uint64_t d = uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(1) << 16) | (uint64_t(8) << 32) | (uint64_t(1) << 46);
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t low) {
+    const uint64_t d = desc_of(low, kDescHighRows16);
     if constexpr (CTAS == 1)
         asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
     else
@@ -148,6 +162,13 @@ __device__ __forceinline__ void load_scales(uint32_t dst, const CUtensorMap *map
             " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(kt), "r"(rt), "r"(bar)
             : "memory");
+}
+
+// One lane of the (converged) warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ void tile_of(int t, const Fp4Args &a, int &mb, int &nb) {
@@ -317,17 +338,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMA issuer
-        if (lane == 0 && rank == 0) {
+        // The whole warp walks the stages and one elected lane issues, so that
+        // addresses and descriptors stay uniform over the warp.  (Issued by
+        // lane 0 in a branch of its own, every copy and MMA took about 45
+        // clocks to issue: 8192^3 in mxfp4 took 237 us, in nvfp4 302 us.)
+        if (rank == 0) {
             int s = 0, n = 0;
             uint32_t ph = 0;
             bool ok = true;
             for (int t = cluster; t < args.num_tiles && ok; t += nclusters, ++n) {
                 int mb, nb;
                 tile_of(t, args, mb, nb);
-                if (n > 0 && !mbar_wait(&st->acc_free, uint32_t(n - 1) & 1u, &st->abort, &g_fp4_error, limit)) {
-                    ok = false;
-                    break;
-                }
+                if (n > 0)
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&st->acc_free, uint32_t(n - 1) & 1u, &st->abort, &g_fp4_error, limit));
+                if (!ok) break;
                 tc_fence_after_sync();
                 const uint32_t d = tmem + ((n & 1) ? C_::ACC1 : 0);
                 // A 64-column tile starts in the middle of a 128-row scale tile
@@ -335,53 +359,56 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t sfa = tmem + C_::SFA_COL;
                 const uint32_t sfb = tmem + C_::SFB_COL + (BN == 64 ? uint32_t(nb & 1) * 2u : 0u);
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait(&st->full[s], ph, &st->abort, &g_fp4_error, limit)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&st->full[s], ph, &st->abort, &g_fp4_error, limit));
+                    if (!ok) break;
                     tc_fence_after_sync();
-                    const uint32_t a = ring + s * C_::STAGE, b = a + C_::A_BYTES, sa = b + C_::B_BYTES;
-                    const uint32_t sb = sa + C_::SFA_BYTES;
-#pragma unroll
-                    for (int j = 0; j < C_::KAT; ++j) {
-                        copy_scales<CTAS>(tmem + C_::SFA_COL + 4 * j, sa + j * kScaleTile);
-#pragma unroll
-                        for (int q = 0; q < C_::NBLK; ++q)
-                            copy_scales<CTAS>(tmem + C_::SFB_COL + 4 * (j * C_::NBLK + q),
-                                              sb + (q * C_::KAT + j) * kScaleTile);
-                    }
+                    const uint32_t a = desc_low(ring + s * C_::STAGE), b = a + C_::A_BYTES / 16;
+                    const uint32_t sa = b + C_::B_BYTES / 16, sb = sa + C_::SFA_BYTES / 16;
                     const int steps = args.k_steps - kb * 4;  // of this stage: past K there is nothing
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (k < steps) {
-                            const int j = NV ? k : k / 2;  // scale tile of these 64 codes
-                            const uint32_t idesc = (!NV && (k & 1)) ? instr_desc_fp4(NV, 128 * CTAS, BN, 2)
-                                                                    : instr_desc_fp4(NV, 128 * CTAS, BN, 0);
-                            mma_fp4<CTAS, NV>(d, smem_desc_sw128(a + k * 32, 16, 1024), smem_desc_sw128(b + k * 32, 16, 1024),
-                                              idesc, sfa + 4 * j, sfb + 4 * (j * C_::NBLK), (kb > kb0 || k > 0) ? 1u : 0u);
+                        for (int j = 0; j < C_::KAT; ++j) {
+                            copy_scales<CTAS>(tmem + C_::SFA_COL + 4 * j, sa + j * (kScaleTile / 16));
+#pragma unroll
+                            for (int q = 0; q < C_::NBLK; ++q)
+                                copy_scales<CTAS>(tmem + C_::SFB_COL + 4 * (j * C_::NBLK + q),
+                                                  sb + (q * C_::KAT + j) * (kScaleTile / 16));
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (k < steps) {
+                                const int j = NV ? k : k / 2;  // scale tile of these 64 codes
+                                const uint32_t idesc = instr_desc_fp4(NV, 128 * CTAS, BN, (!NV && (k & 1)) ? 2 : 0);
+                                mma_fp4<CTAS, NV>(d, desc_of(a + 2 * k, kDescHighSw128), desc_of(b + 2 * k, kDescHighSw128),
+                                                  idesc, sfa + 4 * j, sfb + 4 * (j * C_::NBLK), (kb > kb0 || k > 0) ? 1u : 0u);
+                            }
+                        }
+                        if constexpr (CTAS == 1)
+                            mma_commit<1>(&st->empty[s]);
+                        else
+                            mma_commit_pair(&st->empty[s], 3);
+                        if (kb + 1 == kb1) {
+                            if constexpr (CTAS == 1)
+                                mma_commit<1>(&st->acc_full);
+                            else
+                                mma_commit_pair(&st->acc_full, 3);
                         }
                     }
-                    if constexpr (CTAS == 1)
-                        mma_commit<1>(&st->empty[s]);
-                    else
-                        mma_commit_pair(&st->empty[s], 3);
+                    __syncwarp();
                     if (++s == STAGES) {
                         s = 0;
                         ph ^= 1u;
                     }
                 }
-                if (!ok) break;
-                if constexpr (CTAS == 1)
-                    mma_commit<1>(&st->acc_full);
-                else
-                    mma_commit_pair(&st->acc_full, 3);
             }
             if (!ok) {  // abort: the MMAs issued so far end before tensor memory is freed
-                mma_commit<CTAS>(&st->drain);
-                mbar_wait(&st->drain, 0, nullptr, nullptr, limit);
+                if (elect_one()) {
+                    mma_commit<CTAS>(&st->drain);
+                    mbar_wait(&st->drain, 0, nullptr, nullptr, limit);
+                }
+                __syncwarp();
             }
         }
-        __syncwarp();
     } else {
         // ---------------------------------------------------------- epilogue
         const int ew = warp - 2, q = warp & 3, h = ew >> 2;
