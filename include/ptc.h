@@ -400,8 +400,11 @@ int gemm_fp4(int64_t M, int64_t N, int64_t K, int format, const void *A, int64_t
  * C[M x N] = out( GW * sum_k x_ik w_jk ): a few rows (tokens) of bfloat16 or
  * binary16 activations X (`type`, ldx elements apart) with a microscaled 4-bit
  * matrix W of N rows of K (ldw bytes apart); C has X's type.  Products are
- * exact, sums FP32.  Meant for M up to 16, where W is read once; more rows are
- * taken 16 at a time.  X and C are aligned to the element.
+ * exact and sums FP32; bfloat16 activations are taken as binary16 relative to a
+ * power of two per token and 32 elements, which is exact down to 2^-32 of the
+ * largest of them and off by at most 2^-40 of it below.  Meant for M up to 16,
+ * where W is read once; more rows are taken 16 at a time.  X and C are aligned to
+ * the element.
  */
 int gemm_a16_fp4(int64_t M, int64_t N, int64_t K, int type, const void *X, int64_t ldx, int format, const void *W,
                  int64_t ldw, const void *SW, const float *GW, void *C, int64_t ldc, void *stream);

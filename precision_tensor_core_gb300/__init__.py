@@ -439,17 +439,32 @@ _HOST_FN.update({gemm_f16: gemm_f16_host, gemm_s8: gemm_s8_host, gemm_s4: gemm_s
 
 
 # ---------------------------------------------------------------- 4-bit operators on tensors
+# These calls are a few microseconds on the device at decoding sizes, so the
+# marshalling below is kept to a few microseconds too: torch is looked up once,
+# the current stream and device are read through torch's raw accessors, and the
+# ctypes functions are called directly.
 _FP4 = {"mxfp4": (PTC_FP4_MX, 32), "nvfp4": (PTC_FP4_NV, 16)}
 _ROUNDING = {"nearest": PTC_ROUND_NEAREST, "stochastic": PTC_ROUND_STOCHASTIC}
 _MASK64 = (1 << 64) - 1
 _TYPES = {}
+_torch = _u8 = _current_device = _current_stream = None
+
+
+def _load_torch():
+    """torch, imported by the first call (the package itself loads without it)."""
+    global _torch, _u8, _current_device, _current_stream
+    import torch
+    _TYPES.update({torch.float32: PTC_OUT_F32, torch.bfloat16: PTC_OUT_BF16, torch.float16: PTC_OUT_F16})
+    _u8 = torch.uint8
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _current_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                       or (lambda index: torch.cuda.current_stream(index).cuda_stream))
+    _torch = torch
+    return torch
 
 
 def _type_of(dtype):
     """PTC_OUT_* of a torch dtype."""
-    if not _TYPES:
-        import torch
-        _TYPES.update({torch.float32: PTC_OUT_F32, torch.bfloat16: PTC_OUT_BF16, torch.float16: PTC_OUT_F16})
     code = _TYPES.get(dtype)
     if code is None:
         raise TypeError("tensors are float32, bfloat16 or float16")
@@ -457,42 +472,29 @@ def _type_of(dtype):
 
 
 def _rows_of(t, name):
-    """Row pitch in elements of a 2-D device tensor with unit column stride."""
+    """(rows, columns, row pitch in elements) of a 2-D device tensor with unit column stride."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     rows, cols = t.shape
     s0, s1 = t.stride()
-    if (cols > 1 and s1 != 1) or (rows > 1 and s0 < cols):
+    if rows <= 1:
+        s0 = cols
+    if (s1 != 1 and cols > 1) or s0 < cols:
         raise ValueError(f"{name} must be a 2-D tensor with unit column stride and rows that do not overlap")
-    return s0 if rows > 1 else cols
+    return rows, cols, s0
 
 
-def _on(stream, tensor):
-    """(stream handle, device guard) of a call on `tensor`'s device."""
-    import torch
-    index = tensor.device.index
-    if stream is None:
-        return torch.cuda.current_stream(index).cuda_stream
-    return _stream(stream)
-
-
-class _Guard:
-    """Makes a tensor's device current for a call where it is not already."""
-
-    def __init__(self, tensor):
-        import torch
-        index = tensor.device.index
-        self.guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(fn, index, stream, *args):
+    """fn(*args, stream) with device `index` current, on the current stream of that device by default."""
+    if index == _current_device():
+        status = fn(*args, _current_stream(index) if stream is None else _stream(stream))
+    else:
+        with _torch.cuda.device(index):
+            status = fn(*args, _current_stream(index) if stream is None else _stream(stream))
+    if status:
+        _check(status)
 
 
 def fp4_scale_bytes(rows: int, cols: int, fmt: str) -> int:
@@ -512,34 +514,46 @@ class Fp4Matrix:
         tensor of one element that scales the whole matrix.
     """
 
-    __slots__ = ("codes", "scales", "K", "fmt", "tensor_scale")
+    __slots__ = ("_codes", "_scales", "_K", "_fmt", "_ts", "_rows", "_pitch", "_code", "_index")
 
     def __init__(self, codes, scales, K, fmt="mxfp4", tensor_scale=None):
-        import torch
-        if fmt not in _FP4:
+        if _torch is None:
+            _load_torch()
+        f = _FP4.get(fmt)
+        if f is None:
             raise ValueError("fmt is 'mxfp4' or 'nvfp4'")
-        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        if codes.dtype != _u8 or scales.dtype != _u8:
             raise TypeError("codes and scales are uint8")
-        if K < 0 or _rows_of(codes, "codes") % 16 and codes.shape[0] > 1 or codes.shape[1] < -(-K // 32) * 16:
+        rows, width, pitch = _rows_of(codes, "codes")
+        K = int(K)
+        need = -(-K // 32) * 16
+        if rows <= 1:
+            pitch = max(16, -(-width // 16) * 16)
+        if K < 0 or width < need or pitch % 16:
             raise ValueError("codes must hold 16 * ceil(K / 32) bytes per row, rows a multiple of 16 bytes apart")
-        if not scales.is_contiguous() or scales.numel() < fp4_scale_bytes(codes.shape[0], K, fmt):
+        if not scales.is_contiguous() or scales.numel() < -(-rows // 128) * -(-K // (4 * f[1])) * 512:
             raise ValueError("scales must be contiguous and hold whole tiles of 128 rows x 4 blocks")
-        _check_tensor_scale(tensor_scale, fmt)
-        if scales.device != codes.device or (tensor_scale is not None and tensor_scale.device != codes.device):
+        self._set(codes, scales, K, fmt, tensor_scale, rows, pitch, f[0], codes.get_device())
+        if scales.get_device() != self._index:
             raise ValueError("codes and scales must be on one device")
-        self.codes, self.scales, self.K, self.fmt, self.tensor_scale = codes, scales, int(K), fmt, tensor_scale
+        if tensor_scale is not None:
+            _check_tensor_scale(tensor_scale, fmt, self._index)
 
-    @property
-    def shape(self):
-        return (self.codes.shape[0], self.K)
+    def _set(self, codes, scales, K, fmt, ts, rows, pitch, code, index):
+        self._codes, self._scales, self._K, self._fmt, self._ts = codes, scales, K, fmt, ts
+        self._rows, self._pitch, self._code, self._index = rows, pitch, code, index
 
-    @property
-    def device(self):
-        return self.codes.device
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
+    tensor_scale = property(lambda self: self._ts)
+    K = property(lambda self: self._K)
+    fmt = property(lambda self: self._fmt)
+    shape = property(lambda self: (self._rows, self._K))
+    device = property(lambda self: self._codes.device)
 
     def record_stream(self, stream):
         """As torch.Tensor.record_stream, for every tensor of the matrix."""
-        for t in (self.codes, self.scales, self.tensor_scale):
+        for t in (self._codes, self._scales, self._ts):
             if t is not None:
                 t.record_stream(stream)
 
@@ -553,27 +567,22 @@ class Fp4Matrix:
 
     def row_scales(self):
         """Row-major scale bytes (rows, blocks)."""
-        r, b = self.codes.shape[0], -(-self.K // _FP4[self.fmt][1])
+        r, b = self._rows, -(-self._K // _FP4[self._fmt][1])
         kt = -(-b // 4)
-        s = self.scales[:fp4_scale_bytes(r, self.K, self.fmt)].view(-1, kt, 32, 4, 4)
+        s = self._scales.view(-1)[:fp4_scale_bytes(r, self._K, self._fmt)].view(-1, kt, 32, 4, 4)
         return s.permute(0, 3, 2, 1, 4).reshape(-1, kt * 4)[:r, :b]
 
-    def _pitch(self):
-        c = self.codes
-        return c.stride(0) if c.shape[0] > 1 else (c.shape[1] + 15) // 16 * 16
-
-    def _gp(self):
-        return None if self.tensor_scale is None else self.tensor_scale.data_ptr()
+    def _args(self):
+        """(codes, pitch, scales, matrix scale) of the C calls."""
+        ts = self._ts
+        return self._codes.data_ptr(), self._pitch, self._scales.data_ptr(), None if ts is None else ts.data_ptr()
 
 
-def _check_tensor_scale(ts, fmt):
-    if ts is None:
-        return
-    import torch
+def _check_tensor_scale(ts, fmt, index):
     if fmt != "nvfp4":
         raise ValueError("only nvfp4 has a tensor scale")
-    if ts.dtype != torch.float32 or ts.numel() != 1 or not ts.is_cuda:
-        raise ValueError("tensor_scale is a float32 device tensor of one element")
+    if ts.dtype != _torch.float32 or ts.numel() != 1 or not ts.is_cuda or ts.get_device() != index:
+        raise ValueError("tensor_scale is a float32 tensor of one element on the matrix's device")
 
 
 def dropout(x, p, seed, offset=0, residual=None, out=None, stream=None):
@@ -582,31 +591,35 @@ def dropout(x, p, seed, offset=0, residual=None, out=None, stream=None):
     or float16 (rows, cols).  The mask is a function of (seed, offset, row,
     column) and is never stored: the backward pass is the same call on the
     gradient.  ``out`` may be ``x`` or ``residual``."""
-    import torch
-    code = _type_of(x.dtype)
-    ldx = _rows_of(x, "x")
+    torch = _torch or _load_torch()
+    dtype = x.dtype
+    code = _type_of(dtype)
+    rows, cols, ldx = _rows_of(x, "x")
+    index = x.get_device()
     ldr, rp = 0, None
-    for t, name in ((residual, "residual"), (out, "out")):
-        if t is not None and (t.dtype != x.dtype or t.shape != x.shape or t.device != x.device):
-            raise ValueError(f"{name} must have x's shape, dtype and device")
     if residual is not None:
-        ldr, rp = _rows_of(residual, "residual"), residual.data_ptr()
-    y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    rows, cols = x.shape
-    with _Guard(x):
-        ptc_dropout(rows, cols, x.data_ptr(), ldx, rp, ldr, y.data_ptr(), _rows_of(y, "out"), code, float(p),
-                    int(seed) & _MASK64, int(offset), _on(stream, x))
-    return y
+        if residual.dtype != dtype or residual.shape != x.shape or residual.get_device() != index:
+            raise ValueError("residual must have x's shape, dtype and device")
+        ldr, rp = _rows_of(residual, "residual")[2], residual.data_ptr()
+    if out is None:
+        out, ldy = torch.empty((rows, cols), dtype=dtype, device=x.device), cols
+    else:
+        if out.dtype != dtype or out.shape != x.shape or out.get_device() != index:
+            raise ValueError("out must have x's shape, dtype and device")
+        ldy = _rows_of(out, "out")[2]
+    _call((_lib or lib()).ptc_dropout, index, stream, rows, cols, x.data_ptr(), ldx, rp, ldr, out.data_ptr(), ldy, code,
+          p, seed & _MASK64, offset)
+    return out
 
 
-def _new_fp4(rows, cols, fmt, device, ts):
-    """An uninitialised matrix; codes and scales share one allocation."""
-    import torch
+def _new_fp4(rows, cols, fmt, f, device, index, ts):
+    """An uninitialised matrix."""
+    empty = _torch.empty
     width = -(-cols // 32) * 16
-    buf = torch.empty(rows * width + fp4_scale_bytes(rows, cols, fmt), dtype=torch.uint8, device=device)
     q = Fp4Matrix.__new__(Fp4Matrix)
-    q.codes, q.scales = buf[:rows * width].view(rows, width), buf[rows * width:]
-    q.K, q.fmt, q.tensor_scale = cols, fmt, ts
+    q._set(empty((rows, width), dtype=_u8, device=device),
+           empty(-(-rows // 128) * -(-cols // (4 * f[1])) * 512, dtype=_u8, device=device),
+           cols, fmt, ts, rows, width or 16, f[0], index)
     return q
 
 
@@ -620,73 +633,72 @@ def quantize_fp4(x, fmt="mxfp4", transposed=False, rounding="nearest", tensor_sc
     rounding: "nearest" (ties to even) or "stochastic" (bits from seed, offset).
     p: with p > 0 the values are ``dropout(x, p, seed, offset)`` in float32.
     """
-    if fmt not in _FP4:
+    if _torch is None:
+        _load_torch()
+    f = _FP4.get(fmt)
+    if f is None:
         raise ValueError("fmt is 'mxfp4' or 'nvfp4'")
-    if rounding not in _ROUNDING:
+    how = _ROUNDING.get(rounding)
+    if how is None:
         raise ValueError("rounding is 'nearest' or 'stochastic'")
     if transposed not in (False, True, "both"):
         raise ValueError("transposed is False, True or 'both'")
     code = _type_of(x.dtype)
-    ldx = _rows_of(x, "x")
-    _check_tensor_scale(tensor_scale, fmt)
-    if tensor_scale is not None and tensor_scale.device != x.device:
-        raise ValueError("tensor_scale must be on x's device")
-    rows, cols = x.shape
-    q = _new_fp4(rows, cols, fmt, x.device, tensor_scale) if transposed is not True else None
-    qt = _new_fp4(cols, rows, fmt, x.device, tensor_scale) if transposed is not False else None
-    with _Guard(x):
-        ptc_quantize_fp4(rows, cols, x.data_ptr(), ldx, code, _FP4[fmt][0], _ROUNDING[rounding],
-                         None if tensor_scale is None else tensor_scale.data_ptr(),
-                         q and q.codes.data_ptr(), q._pitch() if q else 0, q and q.scales.data_ptr(),
-                         qt and qt.codes.data_ptr(), qt._pitch() if qt else 0, qt and qt.scales.data_ptr(),
-                         float(p), int(seed) & _MASK64, int(offset), _on(stream, x))
+    rows, cols, ldx = _rows_of(x, "x")
+    index, device = x.get_device(), x.device
+    gp = None
+    if tensor_scale is not None:
+        _check_tensor_scale(tensor_scale, fmt, index)
+        gp = tensor_scale.data_ptr()
+    q = qt = None
+    a = b = (None, 0, None)
+    if transposed is not True:
+        q = _new_fp4(rows, cols, fmt, f, device, index, tensor_scale)
+        a = q._args()
+    if transposed is not False:
+        qt = _new_fp4(cols, rows, fmt, f, device, index, tensor_scale)
+        b = qt._args()
+    _call((_lib or lib()).ptc_quantize_fp4, index, stream, rows, cols, x.data_ptr(), ldx, code, f[0], how, gp, a[0],
+          a[1], a[2], b[0], b[1], b[2], p, seed & _MASK64, offset)
     return (q, qt) if transposed == "both" else (qt if transposed else q)
+
+
+def _result(out, rows, cols, dtype, index, device):
+    """(result tensor, its pitch)."""
+    if out is None:
+        return _torch.empty((rows, cols), dtype=dtype, device=device), cols
+    if out.dim() != 2 or out.shape[0] != rows or out.shape[1] != cols or out.get_device() != index:
+        raise ValueError(f"out must be a ({rows}, {cols}) tensor on the operands' device")
+    return out, _rows_of(out, "out")[2]
 
 
 def dequantize_fp4(q, dtype=None, out=None, stream=None):
     """The values of an :class:`Fp4Matrix` as float32, bfloat16 (default) or float16."""
-    import torch
-    if out is not None:
-        if out.shape != q.shape or out.device != q.device:
-            raise ValueError("out must have the matrix's shape and device")
-        dtype = out.dtype
-    dtype = dtype or torch.bfloat16
+    dtype = out.dtype if out is not None else (dtype or _torch.bfloat16)
     code = _type_of(dtype)
-    y = out if out is not None else torch.empty(q.shape, dtype=dtype, device=q.device)
-    with _Guard(y):
-        ptc_dequantize_fp4(q.shape[0], q.K, q.codes.data_ptr(), q._pitch(), q.scales.data_ptr(), _FP4[q.fmt][0],
-                           q._gp(), y.data_ptr(), _rows_of(y, "out"), code, _on(stream, y))
+    y, ldy = _result(out, q._rows, q._K, dtype, q._index, q._codes.device)
+    c, pitch, s, g = q._args()
+    _call((_lib or lib()).ptc_dequantize_fp4, q._index, stream, q._rows, q._K, c, pitch, s, q._code, g, y.data_ptr(), ldy,
+          code)
     return y
-
-
-def _result(out, shape, dtype, device):
-    import torch
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(out.shape) != shape or out.device != device:
-        raise ValueError(f"out must be a {shape} tensor on the operands' device")
-    return out
 
 
 def matmul_fp4(A, Bt, out_dtype=None, out=None, stream=None):
     """A (M,K) @ B with B given as Bt (N,K), both :class:`Fp4Matrix` of one format
     -> float32, bfloat16 (default) or float16 (M,N), summed in FP32 on the
     block-scaled tensor cores."""
-    import torch
-    if A.fmt != Bt.fmt:
+    if A._code != Bt._code:
         raise ValueError("both matrices must have the same format")
-    if A.K != Bt.K:
+    if A._K != Bt._K:
         raise ValueError("inner dimensions differ")
-    if A.device != Bt.device:
+    index = A._index
+    if index != Bt._index:
         raise ValueError("both matrices must be on one device")
-    dt = out.dtype if out is not None else (out_dtype or torch.bfloat16)
-    code = _type_of(dt)
-    M, N = A.codes.shape[0], Bt.codes.shape[0]
-    C = _result(out, (M, N), dt, A.device)
-    with _Guard(C):
-        gemm_fp4(M, N, A.K, _FP4[A.fmt][0], A.codes.data_ptr(), A._pitch(), A.scales.data_ptr(), A._gp(),
-                 Bt.codes.data_ptr(), Bt._pitch(), Bt.scales.data_ptr(), Bt._gp(), C.data_ptr(), _rows_of(C, "out"),
-                 code, _on(stream, C))
+    dtype = out.dtype if out is not None else (out_dtype or _torch.bfloat16)
+    code = _type_of(dtype)
+    C, ldc = _result(out, A._rows, Bt._rows, dtype, index, A._codes.device)
+    _call((_lib or lib()).gemm_fp4, index, stream, A._rows, Bt._rows, A._K, A._code, *A._args(), *Bt._args(),
+          C.data_ptr(), ldc, code)
     return C
 
 
@@ -695,17 +707,20 @@ def matmul_a16_fp4(x, Wt, out=None, stream=None):
     dtype (M,N), summed in FP32: the product of a decoding step, for M up to 16
     rows (more are taken 16 at a time; quantise x and use :func:`matmul_fp4`
     for many)."""
-    import torch
-    if x.dtype not in (torch.bfloat16, torch.float16):
+    if _torch is None:
+        _load_torch()
+    dtype = x.dtype
+    code = _type_of(dtype)
+    if code == PTC_OUT_F32:
         raise TypeError("matmul_a16_fp4 takes bfloat16 or float16 activations")
-    ldx = _rows_of(x, "x")
-    if x.shape[1] != Wt.K:
+    rows, cols, ldx = _rows_of(x, "x")
+    if cols != Wt._K:
         raise ValueError("inner dimensions differ")
-    if x.device != Wt.device or (out is not None and out.dtype != x.dtype):
+    index = Wt._index
+    if x.get_device() != index or (out is not None and out.dtype != dtype):
         raise ValueError("x, the weights and out must share a device, x and out a dtype")
-    M, N = x.shape[0], Wt.codes.shape[0]
-    C = _result(out, (M, N), x.dtype, x.device)
-    with _Guard(C):
-        gemm_a16_fp4(M, N, Wt.K, _type_of(x.dtype), x.data_ptr(), ldx, _FP4[Wt.fmt][0], Wt.codes.data_ptr(),
-                     Wt._pitch(), Wt.scales.data_ptr(), Wt._gp(), C.data_ptr(), _rows_of(C, "out"), _on(stream, C))
+    C, ldc = _result(out, rows, Wt._rows, dtype, index, x.device)
+    w, pitch, s, g = Wt._args()
+    _call((_lib or lib()).gemm_a16_fp4, index, stream, rows, Wt._rows, cols, code, x.data_ptr(), ldx, Wt._code, w, pitch, s, g,
+          C.data_ptr(), ldc)
     return C

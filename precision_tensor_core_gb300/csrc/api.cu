@@ -441,12 +441,12 @@ int encode_tmap_2d(CUtensorMap *map, bool one_byte, const void *base, uint64_t i
                      base, inner, outer, pitch, box_inner, box_outer);
 }
 int encode_tmap_scales(CUtensorMap *map, const void *base, uint64_t ktiles, uint64_t rtiles, uint32_t box_k,
-                       uint32_t box_r) {
+                       uint32_t box_r, uint32_t box_words) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return fail(PTC_ERR_LAUNCH, "cuTensorMapEncodeTiled unavailable");
     cuuint64_t dims[3] = {128, ktiles, rtiles};  // 32-bit words of a tile, tiles along K, along the rows
     cuuint64_t strides[2] = {512, ktiles * 512};
-    cuuint32_t box[3] = {128, box_k, box_r};
+    cuuint32_t box[3] = {box_words, box_k, box_r};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void *>(base), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1090,10 +1090,11 @@ int gemm_poll_device_error(void) {
     uint32_t w = 0;
     cudaError_t e = ptc::read_and_clear_error_word(&w);
     if (e != cudaSuccess) return fail_cuda(e, "reading the device error word");
-    uint32_t w4 = 0;
+    uint32_t w4 = 0, wt = 0;
     e = ptc::read_and_clear_fp4_error_word(&w4);
+    if (e == cudaSuccess) e = ptc::read_and_clear_tokens_error_word(&wt);
     if (e != cudaSuccess) return fail_cuda(e, "reading the device error word");
-    return (w | w4) ? PTC_ERR_TIMEOUT : PTC_OK;
+    return (w | w4 | wt) ? PTC_ERR_TIMEOUT : PTC_OK;
 }
 
 uint64_t ptc_kernel_launch_count(void) { return g_launches.load(); }

@@ -213,9 +213,10 @@ int encode_tmap_c32(CUtensorMap *map, const void *C, uint64_t n, uint64_t m, uin
 int encode_tmap_2d(CUtensorMap *map, bool one_byte, const void *base, uint64_t inner, uint64_t outer,
                    uint64_t pitch, uint32_t box_inner, uint32_t box_outer);
 // Tiled block scales (tiles of 512 bytes, ktiles per 128 rows, rtiles x 128
-// rows): boxes of box_k x box_r whole tiles, zero fill outside.
+// rows): boxes of box_k x box_r tiles, of the first dimension box_words 32-bit
+// words, zero fill outside.
 int encode_tmap_scales(CUtensorMap *map, const void *base, uint64_t ktiles, uint64_t rtiles, uint32_t box_k,
-                       uint32_t box_r);
+                       uint32_t box_r, uint32_t box_words = 128);
 
 // Host helpers of the entry points (api.cu): a status with its text, a failed
 // CUDA call, the current device's SM count (PTC_ERR_DEVICE when it is not
@@ -237,8 +238,9 @@ uint64_t fp4_scale_bytes(int64_t rows, int64_t cols, bool nv);
 uint64_t fp4_code_span(int64_t rows, int64_t cols, int64_t pitch);
 int check_fp4(const void *codes, int64_t pitch, const void *scales, const void *g, int64_t rows, int64_t cols, bool nv);
 
-// The 4-bit product's error word (fp4_gemm.cu), read and cleared.
+// The 4-bit products' error words (fp4_gemm.cu, fp4_tokens.cu), read and cleared.
 cudaError_t read_and_clear_fp4_error_word(uint32_t *out);
+cudaError_t read_and_clear_tokens_error_word(uint32_t *out);
 // The keys "fp4_tile", "fp4_ksplit" and "fp4_group_m" of ptc_set_tuning;
 // false for another key or a value out of range.
 bool set_fp4_tuning(const char *key, int64_t value);

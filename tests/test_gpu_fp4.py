@@ -397,6 +397,22 @@ def test_product_wait_limit_is_reported(tile):
         ptc.ptc_set_tuning("fp4_tile", 0)
 
 
+def test_few_tokens_wait_limit_is_reported():
+    """Weights that never arrive: as above for the product of a few tokens."""
+    W, w = matrix(300, 1024, "mxfp4", 4)
+    x = normal(5, 1024, 1, torch.bfloat16, 0.2)
+    try:
+        ptc.ptc_debug_set_wait_limit(2_000_000, 0)
+        ptc.matmul_a16_fp4(x, W)
+        torch.cuda.synchronize()
+        assert ptc.gemm_poll_device_error() == ptc.PTC_ERR_TIMEOUT
+        ptc.ptc_debug_set_wait_limit(0, -1)
+        check_product(ptc.matmul_a16_fp4(x, W), host(x), w, 1024)
+        assert ptc.gemm_poll_device_error() == ptc.PTC_OK
+    finally:
+        ptc.ptc_debug_set_wait_limit(0, -1)
+
+
 # ------------------------------------------------------------------ few tokens
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
