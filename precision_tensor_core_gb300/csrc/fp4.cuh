@@ -214,15 +214,16 @@ __device__ __forceinline__ uint32_t codes_nearest(const float (&v)[8]) {
 
 // One value rounded down or up to the neighbouring codes, up when its
 // remainder (in 1/65536 of the gap) plus r reaches 65536.  The gaps are 0.5
-// below 2, 1 below 4 and 2 below 6; scaling by 1 / gap, floor and remainder
-// are exact, so the result is a function of the value and r alone.
+// below 2, 1 below 4 and 2 below 6.  The distance to the first code of the
+// range in 1/65536 of the gap is u * 65536 / gap rounded down to a whole number
+// (an addition of 2^23 that rounds down leaves it in the low bits), and the
+// sum with r carries into bit 16 exactly where the code goes up.
 __device__ __forceinline__ uint32_t code_stochastic(float v, uint32_t r) {
     const float u = fminf(fabsf(v), 6.0f);
     const bool low2 = u < 2.0f, low4 = u < 4.0f;
-    const float t = u * (low2 ? 2.0f : low4 ? 1.0f : 0.5f);
-    const float f = floorf(t);
-    const bool up = (t - f) * 65536.0f >= float(65536u - r);
-    const uint32_t code = (low2 ? 0u : low4 ? 2u : 4u) + uint32_t(f) + (up ? 1u : 0u);
+    const float t = __fmaf_rd(u, low2 ? 131072.0f : low4 ? 65536.0f : 32768.0f, 8388608.0f);
+    const uint32_t base = (low2 ? 0u : low4 ? 2u << 16 : 4u << 16) - 0x4B000000u;  // bits of 2^23
+    const uint32_t code = (__float_as_uint(t) + base + r) >> 16;
     return code | ((__float_as_uint(v) >> 28) & 8u);
 }
 

@@ -127,11 +127,12 @@ __device__ __forceinline__ uint32_t codes8(const float (&v)[8], uint32_t amax, c
     return amax < kInfBits ? q : 0u;
 }
 
-// Rows only.  A warp takes 256 columns of a row, a lane eight of them: the
-// block's maximum by one or two shuffles, codes as 4 bytes per lane (128
-// contiguous bytes per warp), scales gathered to one 4-byte store per tile.
-// Rows past the last one to the end of the scale tile get zero scales.
-template <typename T, bool NV, bool SR, bool DROP>
+// Rows only.  A warp takes U x 256 columns of a row, a lane U times eight of
+// them, all loads before the first use: the block's maximum by one or two
+// shuffles, codes as 4 bytes per lane (128 contiguous bytes per warp), scales
+// gathered to one 4-byte store per tile.  Rows past the last one to the end of
+// the scale tile get zero scales.
+template <typename T, bool NV, bool SR, bool DROP, int U>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *x, const QuantArgs a) {
     griddep_wait();
     griddep_launch_dependents();
@@ -143,92 +144,117 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *x, const Qu
     const int64_t rows_p = (a.rows + 127) / 128 * 128;
     const int64_t cols_p = (a.cols + 31) / 32 * 32;
     Walk w((int64_t(blockIdx.x) * blockDim.x + threadIdx.x) / 32, int64_t(gridDim.x) * blockDim.x / 32,
-           uint32_t((a.cols + 255) / 256));
+           uint32_t((a.cols + 256 * U - 1) / (256 * U)));
     for (; w.row < rows_p; w.next()) {
-        const int64_t c = int64_t(w.group) * 256 + lane * 8;
-        const bool real = w.row < a.rows;
-        uint32_t word = 0;
-        if (real) {  // uniform over the warp
-            const int n = int(max(int64_t(0), min(int64_t(8), a.cols - c)));
-            const Pack8<T> p = load8(x + w.row * a.ldx + (n > 0 ? c : 0), n, a.vec != 0);
-            float v[8];
-            dropped8<T, DROP>(p, a.drop, w.row, uint32_t(c / 8), v);
-            if constexpr (DROP) {
-                if (n < 8) {
+        const int64_t c0 = int64_t(w.group) * (256 * U) + lane * 8;
+        const bool real = w.row < a.rows;  // uniform over the warp
+        Pack8<T> p[U];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j >= n) v[j] = 0.0f;
-                }
-            }
-            uint32_t m = max_abs8(v);
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-            if constexpr (!NV) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-            uint32_t byte;
-            const BlockScale<NV> scale = block_scale<NV, SR>(m, g, byte);
-            uint4 bits = make_uint4(0, 0, 0, 0);
-            if constexpr (SR) bits = random_bits8(a.drop.rng, kRngRounding, uint32_t(w.row), uint32_t(c / 8));
-            const uint32_t q = codes8<NV, SR>(v, m, scale, bits);
-            if (c < cols_p) *reinterpret_cast<uint32_t *>(a.codes + w.row * a.pitch + c / 2) = q;
-            // Four blocks' bytes to one word (held by the first lane of the four).
-            word = byte;
-            word |= __shfl_down_sync(0xFFFFFFFFu, word, LPB) << 8;
-            word |= __shfl_down_sync(0xFFFFFFFFu, word, 2 * LPB) << 16;
+        for (int u = 0; u < U; ++u) {
+            const int64_t c = c0 + 256 * u;
+            const int n = real ? int(max(int64_t(0), min(int64_t(8), a.cols - c))) : 0;
+            p[u] = load8(x + (n > 0 ? w.row * a.ldx + c : 0), n, a.vec != 0);
         }
-        const int64_t kt = (int64_t(w.group) * 32 + lane) / LPT;
-        if (lane % LPT == 0 && kt < ktiles)
-            *reinterpret_cast<uint32_t *>(a.scales + scale_word(w.row, kt, ktiles)) = word;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t c = c0 + 256 * u;
+            if (U > 1 && c - lane * 8 >= cols_p) break;  // (uniform: nothing of these 256 columns exists)
+            uint32_t word = 0;
+            if (real) {
+                float v[8];
+                dropped8<T, DROP>(p[u], a.drop, w.row, uint32_t(c / 8), v);
+                if constexpr (DROP) {
+                    if (c + 8 > a.cols) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (c + j >= a.cols) v[j] = 0.0f;
+                    }
+                }
+                uint32_t m = max_abs8(v);
+                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+                if constexpr (!NV) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+                uint32_t byte;
+                const BlockScale<NV> scale = block_scale<NV, SR>(m, g, byte);
+                uint4 bits = make_uint4(0, 0, 0, 0);
+                if constexpr (SR) bits = random_bits8(a.drop.rng, kRngRounding, uint32_t(w.row), uint32_t(c / 8));
+                const uint32_t q = codes8<NV, SR>(v, m, scale, bits);
+                if (c < cols_p) *reinterpret_cast<uint32_t *>(a.codes + w.row * a.pitch + c / 2) = q;
+                // Four blocks' bytes to one word (held by the first lane of the four).
+                word = byte;
+                word |= __shfl_down_sync(0xFFFFFFFFu, word, LPB) << 8;
+                word |= __shfl_down_sync(0xFFFFFFFFu, word, 2 * LPB) << 16;
+            }
+            const int64_t kt = c / (8 * LPT);
+            if (lane % LPT == 0 && kt < ktiles)
+                *reinterpret_cast<uint32_t *>(a.scales + scale_word(w.row, kt, ktiles)) = word;
+        }
     }
 }
 
-// Columns (and rows).  A CTA takes 128 x 128 elements: read once, dropped out,
-// kept in shared memory as they came (dropped ones +0) beside their rounding
-// bits; rows are quantised on the way in (16 lanes per row), columns from
-// shared memory, where consecutive lanes hold consecutive columns.
-constexpr int kTile = 128;
+// Columns (and rows).  A CTA takes 128 rows x 64 columns: read once (four
+// loads per thread in flight), dropped out, kept in shared memory as they came
+// (dropped ones +0) beside their rounding bits; rows are quantised on the way
+// in, eight lanes per row.  For the columns a lane takes two adjacent columns
+// and a warp 16 rows: a block of nvfp4, half of one of mxfp4, whose maximum two
+// warps share.  Codes and scale bytes go through shared memory so that a
+// column's 64 bytes are written together.
+constexpr int kTileR = 128, kTileC = 64;
+constexpr int kCodePitch = 80;  // of a column's 64 code bytes in shared memory
 
 template <typename T, bool SR>
 constexpr size_t tile_smem() {
-    return size_t(kTile) * kTile * (sizeof(T) + (SR ? 2 : 0));
+    return size_t(kTileR) * kTileC * (sizeof(T) + (SR ? 2 : 0));
 }
 
 template <typename T, bool NV, bool SR, bool DROP, bool ROWS>
 __global__ void __launch_bounds__(256) quantize_tile_kernel(const T *x, const QuantArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
     T *xs = reinterpret_cast<T *>(smem);
-    uint16_t *rs = reinterpret_cast<uint16_t *>(smem + size_t(kTile) * kTile * sizeof(T));
+    uint16_t *rs = reinterpret_cast<uint16_t *>(smem + size_t(kTileR) * kTileC * sizeof(T));
+    __shared__ __align__(16) uint8_t ct[kTileC * kCodePitch];
+    __shared__ __align__(8) uint8_t sct[kTileC * 8];
+    __shared__ uint32_t top[NV ? 1 : 8 * kTileC];
     griddep_wait();
     griddep_launch_dependents();
-    constexpr int BPT = NV ? 8 : 4;  // blocks per 128 elements
-    constexpr int KPT = BPT / 4;     // scale words per 128 elements
+    constexpr int KW = NV ? 64 : 128;  // columns (rows) per scale word
     const float g = (NV && a.g != nullptr) ? __ldg(a.g) : 1.0f;
-    const int64_t tiles_c = (a.cols + kTile - 1) / kTile, tiles_r = (a.rows + kTile - 1) / kTile;
-    const int64_t kt_rows = (a.cols + 128 / KPT - 1) / (128 / KPT), kt_cols = (a.rows + 128 / KPT - 1) / (128 / KPT);
-    for (int64_t t = blockIdx.x; t < tiles_r * tiles_c; t += gridDim.x) {
-        const int64_t r0 = t / tiles_c * kTile, c0 = (t % tiles_c) * kTile;
-        const int grp = threadIdx.x & 15;
-#pragma unroll 2
-        for (int lr = threadIdx.x / 16; lr < kTile; lr += 16) {
-            const int64_t r = r0 + lr, c = c0 + grp * 8;
+    const int64_t tiles_c = (a.cols + kTileC - 1) / kTileC;
+    const int64_t kt_rows = (a.cols + KW - 1) / KW, kt_cols = (a.rows + KW - 1) / KW;
+    const int64_t r0 = blockIdx.x / tiles_c * kTileR, c0 = (blockIdx.x % tiles_c) * kTileC;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    {
+        const int grp = threadIdx.x & 7;
+        const int64_t c = c0 + grp * 8;
+        Pack8<T> p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t r = r0 + (threadIdx.x >> 3) + 32 * i;
             const int n = r < a.rows ? int(max(int64_t(0), min(int64_t(8), a.cols - c))) : 0;
-            Pack8<T> p = load8(x + (n > 0 ? r * a.ldx + c : 0), n, a.vec != 0);
+            p[i] = load8(x + (n > 0 ? r * a.ldx + c : 0), n, a.vec != 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int lr = (threadIdx.x >> 3) + 32 * i;
+            const int64_t r = r0 + lr;
             if constexpr (DROP) {
                 const uint4 bits = random_bits8(a.drop.rng, kRngDropout, uint32_t(r), uint32_t(c / 8));
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (bits16(bits, j) >= a.drop.kept) p.set(j, from_float<T>(0.0f));
+                    if (bits16(bits, j) >= a.drop.kept) p[i].set(j, from_float<T>(0.0f));
             }
             uint4 bits = make_uint4(0, 0, 0, 0);
             if constexpr (SR) {
                 bits = random_bits8(a.drop.rng, kRngRounding, uint32_t(r), uint32_t(c / 8));
-                *reinterpret_cast<uint4 *>(rs + lr * kTile + grp * 8) = bits;
+                *reinterpret_cast<uint4 *>(rs + lr * kTileC + grp * 8) = bits;
             }
 #pragma unroll
-            for (int i = 0; i < Pack8<T>::W; ++i)
-                reinterpret_cast<uint4 *>(xs + lr * kTile + grp * 8)[i] = p.v[i];
+            for (int w = 0; w < Pack8<T>::W; ++w) reinterpret_cast<uint4 *>(xs + lr * kTileC + grp * 8)[w] = p[i].v[w];
             if constexpr (ROWS) {
                 float v[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = DROP ? __fmul_rn(to_float(p.get(j)), a.drop.scale) : to_float(p.get(j));
+                for (int j = 0; j < 8; ++j)
+                    v[j] = DROP ? __fmul_rn(to_float(p[i].get(j)), a.drop.scale) : to_float(p[i].get(j));
                 uint32_t m = max_abs8(v);
                 m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
                 if constexpr (!NV) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
@@ -237,79 +263,107 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const T *x, const Qu
                 const uint32_t q = codes8<NV, SR>(v, m, scale, bits);
                 if (r < a.rows && c < (a.cols + 31) / 32 * 32)
                     *reinterpret_cast<uint32_t *>(a.codes + r * a.pitch + c / 2) = q;
-                constexpr int LPB = NV ? 2 : 4;
+                // The row's scale bytes of these 64 columns: a word (nvfp4), or half
+                // of one; a last first half also clears the other.
                 uint32_t word = r < a.rows ? byte : 0u;
-                word |= __shfl_down_sync(0xFFFFFFFFu, word, LPB) << 8;
-                word |= __shfl_down_sync(0xFFFFFFFFu, word, 2 * LPB) << 16;
-                const int64_t kt = c0 / (128 / KPT) + grp / (4 * LPB);
-                if (grp % (4 * LPB) == 0 && kt < kt_rows)
-                    *reinterpret_cast<uint32_t *>(a.scales + scale_word(r, kt, kt_rows)) = word;
-            }
-        }
-        __syncthreads();
-        // Column c0 + lc, rows 64 half .. + 63: two units of 32 rows.
-        const int lc = threadIdx.x & 127, half = threadIdx.x >> 7;
-        const int64_t col = c0 + lc;
-        uint32_t bytes[2 * BPT / 4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int lr = half * 64 + u * 32;
-            uint32_t q[4];
-#pragma unroll
-            for (int b = 0; b < (NV ? 2 : 1); ++b) {
-                constexpr int BS = NV ? 16 : 32;
-                float v[BS];
-                uint32_t m = 0;
-#pragma unroll
-                for (int i = 0; i < BS; ++i) {
-                    const float f = to_float(xs[(lr + b * BS + i) * kTile + lc]);
-                    v[i] = DROP ? __fmul_rn(f, a.drop.scale) : f;
-                    m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-                }
-                uint32_t byte;
-                const BlockScale<NV> scale = block_scale<NV, SR>(m, g, byte);
-                bytes[u * (BPT / 4) + b] = byte;
-#pragma unroll
-                for (int w = 0; w < BS / 8; ++w) {
-                    uint32_t code = 0;
-                    if constexpr (SR) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            code |= code_stochastic(scale.apply(v[8 * w + j]),
-                                                    rs[(lr + b * BS + 8 * w + j) * kTile + lc])
-                                    << (4 * j);
-                    } else {
-                        float s[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) s[j] = scale.apply(v[8 * w + j]);
-                        code = codes_nearest(s);
+                uint8_t *dst = a.scales + scale_word(r, c0 / KW, kt_rows);
+                if constexpr (NV) {
+                    word |= __shfl_down_sync(0xFFFFFFFFu, word, 2) << 8;
+                    word |= __shfl_down_sync(0xFFFFFFFFu, word, 4) << 16;
+                    if (grp == 0) *reinterpret_cast<uint32_t *>(dst) = word;
+                } else {
+                    word |= __shfl_down_sync(0xFFFFFFFFu, word, 4) << 8;
+                    if (grp == 0) {
+                        const int half = int(c0 / kTileC) & 1;
+                        if (half == 0 && c0 + kTileC >= a.cols)
+                            *reinterpret_cast<uint32_t *>(dst) = word & 0xFFFFu;
+                        else
+                            *reinterpret_cast<uint16_t *>(dst + 2 * half) = uint16_t(word);
                     }
-                    q[b * (BS / 8) + w] = m < kInfBits ? code : 0u;
                 }
             }
-            if (col < a.cols && r0 + lr < a.rows)
-                *reinterpret_cast<uint4 *>(a.codes_t + col * a.pitch_t + (r0 + lr) / 2) =
-                    make_uint4(q[0], q[1], q[2], q[3]);
         }
-        // This half's scale bytes: two of a word (mxfp4) or a whole word (nvfp4).
-        const bool real = col < a.cols;
-        const int64_t kt = r0 / (128 / KPT) + (NV ? half : 0);
-        if (kt < kt_cols) {
-            uint8_t *dst = a.scales_t + scale_word(col, kt, kt_cols);
-            if constexpr (NV)
-                *reinterpret_cast<uint32_t *>(dst) =
-                    real ? bytes[0] | (bytes[1] << 8) | (bytes[2] << 16) | (bytes[3] << 24) : 0u;
-            else
-                *reinterpret_cast<uint16_t *>(dst + 2 * half) = real ? uint16_t(bytes[0] | (bytes[1] << 8)) : uint16_t(0);
-        }
+    }
+    __syncthreads();
+
+    float va[16], vb[16];  // columns 2 lane and 2 lane + 1, rows 16 warp ..
+    uint32_t ma = 0, mb = 0;
+    struct alignas(2 * sizeof(T)) Two {
+        T a, b;
+    };
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const Two t = *reinterpret_cast<const Two *>(xs + (16 * warp + i) * kTileC + 2 * lane);
+        va[i] = DROP ? __fmul_rn(to_float(t.a), a.drop.scale) : to_float(t.a);
+        vb[i] = DROP ? __fmul_rn(to_float(t.b), a.drop.scale) : to_float(t.b);
+        ma = max(ma, __float_as_uint(va[i]) & 0x7FFFFFFFu);
+        mb = max(mb, __float_as_uint(vb[i]) & 0x7FFFFFFFu);
+    }
+    if constexpr (!NV) {
+        top[warp * kTileC + 2 * lane] = ma;
+        top[warp * kTileC + 2 * lane + 1] = mb;
         __syncthreads();
+        ma = max(ma, top[(warp ^ 1) * kTileC + 2 * lane]);
+        mb = max(mb, top[(warp ^ 1) * kTileC + 2 * lane + 1]);
+    }
+    uint32_t ba, bb;
+    const BlockScale<NV> sa = block_scale<NV, SR>(ma, g, ba), sb = block_scale<NV, SR>(mb, g, bb);
+    uint32_t qa[2] = {0u, 0u}, qb[2] = {0u, 0u};
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        if constexpr (SR) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t r = *reinterpret_cast<const uint32_t *>(rs + (16 * warp + 8 * w + j) * kTileC + 2 * lane);
+                qa[w] |= code_stochastic(sa.apply(va[8 * w + j]), r & 0xFFFFu) << (4 * j);
+                qb[w] |= code_stochastic(sb.apply(vb[8 * w + j]), r >> 16) << (4 * j);
+            }
+        } else {
+            float s[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] = sa.apply(va[8 * w + j]);
+            qa[w] = codes_nearest(s);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] = sb.apply(vb[8 * w + j]);
+            qb[w] = codes_nearest(s);
+        }
+        qa[w] = ma < kInfBits ? qa[w] : 0u;
+        qb[w] = mb < kInfBits ? qb[w] : 0u;
+    }
+    *reinterpret_cast<uint2 *>(ct + (2 * lane) * kCodePitch + 8 * warp) = make_uint2(qa[0], qa[1]);
+    *reinterpret_cast<uint2 *>(ct + (2 * lane + 1) * kCodePitch + 8 * warp) = make_uint2(qb[0], qb[1]);
+    if (NV || (warp & 1) == 0) {
+        const int at = NV ? warp : warp >> 1;
+        sct[(2 * lane) * 8 + at] = uint8_t(ba);
+        sct[(2 * lane + 1) * 8 + at] = uint8_t(bb);
+    }
+    __syncthreads();
+    {
+        const int lc = threadIdx.x >> 2, piece = threadIdx.x & 3;
+        const int64_t col = c0 + lc;
+        if (col < a.cols && r0 + 32 * piece < a.rows)
+            *reinterpret_cast<uint4 *>(a.codes_t + col * a.pitch_t + r0 / 2 + 16 * piece) =
+                *reinterpret_cast<const uint4 *>(ct + lc * kCodePitch + 16 * piece);
+        // Scale words: one (mxfp4) or two (nvfp4) per column; columns past the last
+        // to the end of the 128-row scale tile get zeros.
+        constexpr int W = NV ? 2 : 1;
+        if (piece < W) {
+            const int64_t kt = r0 / KW + piece;
+            if (kt < kt_cols) {
+                const uint32_t word = *reinterpret_cast<const uint32_t *>(sct + lc * 8 + 4 * piece);
+                *reinterpret_cast<uint32_t *>(a.scales_t + scale_word(col, kt, kt_cols)) = col < a.cols ? word : 0u;
+                if (c0 + kTileC >= a.cols && c0 % 128 == 0)
+                    *reinterpret_cast<uint32_t *>(a.scales_t + scale_word(col + kTileC, kt, kt_cols)) = 0u;
+            }
+        }
     }
 }
 
 // ------------------------------------------------------------ back to values
 // value = code x scale (x matrix scale), each product in FP32, rounded once
-// more to the output type; eight elements per step.
-template <typename T, bool NV>
+// more to the output type.  A warp takes U x 256 columns of a row, a lane U
+// times eight of them, all loads before the first use.
+template <typename T, bool NV, int U>
 __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *codes, int64_t pitch, const uint8_t *scales,
                                                          const float *gp, int64_t rows, int64_t cols, T *y,
                                                          int64_t ldy, int vec) {
@@ -317,27 +371,42 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *codes, i
     griddep_launch_dependents();
     const bool has_g = gp != nullptr;
     const float g = has_g ? __ldg(gp) : 1.0f;
-    constexpr int GPB = NV ? 2 : 4;  // groups of eight per block
-    const int64_t blocks = (cols + 8 * GPB - 1) / (8 * GPB), ktiles = (blocks + 3) / 4;
-    Walk w(int64_t(blockIdx.x) * blockDim.x + threadIdx.x, int64_t(gridDim.x) * blockDim.x,
-           uint32_t((cols + 7) / 8));
+    constexpr int EPB = NV ? 16 : 32;
+    const int64_t ktiles = (cols + 4 * EPB - 1) / (4 * EPB);
+    const int lane = threadIdx.x & 31;
+    Walk w((int64_t(blockIdx.x) * blockDim.x + threadIdx.x) / 32, int64_t(gridDim.x) * blockDim.x / 32,
+           uint32_t((cols + 256 * U - 1) / (256 * U)));
     for (; w.row < rows; w.next()) {
-        const int64_t c = int64_t(w.group) * 8;
-        const int n = int(min(int64_t(8), cols - c));
-        const uint32_t q = *reinterpret_cast<const uint32_t *>(codes + w.row * pitch + c / 2);
-        const uint32_t b = w.group / GPB;
-        const float s = scale_value<NV>(scales[scale_word(w.row, b >> 2, ktiles) + (b & 3)]);
-        uint32_t h[4];
-        codes_to_f16(q, h);
-        Pack8<T> o;
+        const int64_t c0 = int64_t(w.group) * (256 * U) + lane * 8;
+        uint32_t q[U], b[U];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float f = __half2float(__ushort_as_half(uint16_t((j & 1) ? h[j >> 1] >> 16 : h[j >> 1] & 0xFFFFu)));
-            float v = __fmul_rn(f, s);
-            if (has_g) v = __fmul_rn(v, g);
-            o.set(j, from_float<T>(v));
+        for (int u = 0; u < U; ++u) {
+            const int64_t c = c0 + 256 * u;
+            q[u] = b[u] = 0u;
+            if (c < cols) {
+                q[u] = __ldcs(reinterpret_cast<const uint32_t *>(codes + w.row * pitch + c / 2));
+                const int64_t blk = c / EPB;
+                b[u] = scales[scale_word(w.row, blk >> 2, ktiles) + (blk & 3)];
+            }
         }
-        store8(y + w.row * ldy + c, o, n, vec != 0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t c = c0 + 256 * u;
+            if (c >= cols) break;
+            const float s = scale_value<NV>(b[u]);
+            uint32_t h[4];
+            codes_to_f16(q[u], h);
+            Pack8<T> o;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float f =
+                    __half2float(__ushort_as_half(uint16_t((j & 1) ? h[j >> 1] >> 16 : h[j >> 1] & 0xFFFFu)));
+                float v = __fmul_rn(f, s);
+                if (has_g) v = __fmul_rn(v, g);
+                o.set(j, from_float<T>(v));
+            }
+            store8(y + w.row * ldy + c, o, int(min(int64_t(8), cols - c)), vec != 0);
+        }
     }
 }
 
@@ -409,18 +478,23 @@ int run_dropout(int64_t rows, int64_t cols, const void *x, int64_t ldx, const vo
 template <typename T, bool NV, bool SR, bool DROP>
 cudaError_t launch_quantize(const T *x, const QuantArgs &a, int sms, cudaStream_t s) {
     if (a.codes_t == nullptr) {
-        const int64_t warps = (a.rows + 127) / 128 * 128 * ((a.cols + 255) / 256);
-        return launch(quantize_rows_kernel<T, NV, SR, DROP>, grid_for(warps * 32, sms), 256, 0, s, x, a);
+        // Four loads in flight per lane where rows are long enough and there is more than a wave of them.
+        const int64_t rows_p = (a.rows + 127) / 128 * 128;
+        const int64_t warps = rows_p * ((a.cols + 1023) / 1024);
+        if (a.cols > 512 && warps >= int64_t(sms) * 64)
+            return launch(quantize_rows_kernel<T, NV, SR, DROP, 4>, grid_for(warps * 32, sms), 256, 0, s, x, a);
+        return launch(quantize_rows_kernel<T, NV, SR, DROP, 1>, grid_for(rows_p * ((a.cols + 255) / 256) * 32, sms), 256, 0, s,
+                      x, a);
     }
-    const int64_t tiles = ((a.rows + kTile - 1) / kTile) * ((a.cols + kTile - 1) / kTile);
-    const int64_t grid = tiles < int64_t(1) << 30 ? tiles : int64_t(1) << 30;
+    const int64_t tiles = ((a.rows + kTileR - 1) / kTileR) * ((a.cols + kTileC - 1) / kTileC);
+    if (tiles >= int64_t(1) << 31) return cudaErrorInvalidConfiguration;  // (more elements than a GPU holds)
     constexpr size_t smem = tile_smem<T, SR>();
     auto *fn = a.codes ? quantize_tile_kernel<T, NV, SR, DROP, true> : quantize_tile_kernel<T, NV, SR, DROP, false>;
-    if (smem > 48 * 1024) {
+    if (smem + 8192 > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         if (e != cudaSuccess) return e;
     }
-    return launch(fn, grid, 256, smem, s, x, a);
+    return launch(fn, tiles, 256, smem, s, x, a);
 }
 
 template <typename T>
@@ -582,20 +656,23 @@ int ptc_dequantize_fp4(int64_t rows, int64_t cols, const void *codes, int64_t pi
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int vec = wide_rows(y, ldy, es);
     const uint8_t *cp = static_cast<const uint8_t *>(codes), *sp = static_cast<const uint8_t *>(scales);
-    const int64_t grid = grid_for(rows * ((cols + 7) / 8), sms);
-    auto go = [&](auto fn, auto *out) {
-        return launch(fn, grid, 256, 0, s, cp, pitch, sp, matrix_scale, rows, cols, out, ldy, vec);
+    const bool many = cols > 512 && rows * ((cols + 1023) / 1024) >= int64_t(sms) * 64;
+    const int64_t grid = grid_for(rows * (many ? (cols + 1023) / 1024 : (cols + 255) / 256) * 32, sms);
+    auto go = [&](auto one, auto four, auto *out) {
+        return launch(many ? four : one, grid, 256, 0, s, cp, pitch, sp, matrix_scale, rows, cols, out, ldy, vec);
     };
     cudaError_t e;
     if (type == PTC_OUT_F32)
-        e = nv ? go(dequantize_kernel<float, true>, static_cast<float *>(y))
-               : go(dequantize_kernel<float, false>, static_cast<float *>(y));
+        e = nv ? go(dequantize_kernel<float, true, 1>, dequantize_kernel<float, true, 4>, static_cast<float *>(y))
+               : go(dequantize_kernel<float, false, 1>, dequantize_kernel<float, false, 4>, static_cast<float *>(y));
     else if (type == PTC_OUT_BF16)
-        e = nv ? go(dequantize_kernel<__nv_bfloat16, true>, static_cast<__nv_bfloat16 *>(y))
-               : go(dequantize_kernel<__nv_bfloat16, false>, static_cast<__nv_bfloat16 *>(y));
+        e = nv ? go(dequantize_kernel<__nv_bfloat16, true, 1>, dequantize_kernel<__nv_bfloat16, true, 4>,
+                    static_cast<__nv_bfloat16 *>(y))
+               : go(dequantize_kernel<__nv_bfloat16, false, 1>, dequantize_kernel<__nv_bfloat16, false, 4>,
+                    static_cast<__nv_bfloat16 *>(y));
     else
-        e = nv ? go(dequantize_kernel<__half, true>, static_cast<__half *>(y))
-               : go(dequantize_kernel<__half, false>, static_cast<__half *>(y));
+        e = nv ? go(dequantize_kernel<__half, true, 1>, dequantize_kernel<__half, true, 4>, static_cast<__half *>(y))
+               : go(dequantize_kernel<__half, false, 1>, dequantize_kernel<__half, false, 4>, static_cast<__half *>(y));
     return e == cudaSuccess ? PTC_OK : fail_launch(e, "dequantisation launch");
 }
 
