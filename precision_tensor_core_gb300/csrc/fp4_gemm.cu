@@ -164,6 +164,14 @@ __device__ __forceinline__ void load_scales(uint32_t dst, const CUtensorMap *map
             : "memory");
 }
 
+// Arrives on a barrier of the cluster without ordering this thread's earlier
+// global stores before it: what it announces is that tensor-memory loads are
+// complete (their values are in registers), and a release would wait for the
+// output stores of the tile before.
+__device__ __forceinline__ void arrive_relaxed_cluster(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // One lane of the (converged) warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -435,10 +443,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) {
-                        if constexpr (CTAS == 1)
+                        if (CTAS == 1 || rank == 0)
                             mbar_arrive(&st->acc_free);
                         else
-                            mbar_arrive_cluster(mapa_shared(smem_u32(&st->acc_free), 0));
+                            arrive_relaxed_cluster(mapa_shared(smem_u32(&st->acc_free), 0));
                     }
                 }
                 const int col = nb * BN + 32 * c;
