@@ -62,6 +62,7 @@ struct Fp4Args {
     int k_steps;   // MMAs of kMmaK codes in all
     int tiles_m, tiles_n, num_tiles, group_m;
     int ks;        // CTAs per cluster sharing a tile's K range (one-CTA tiles)
+    int stages;    // stages of the ring (fewer where C is staged)
     int vec;       // C's base and pitch are multiples of: 2: 32 bytes, 1: 16 bytes, 0: neither
     const float *ga, *gb;
     int stall_tile;
@@ -86,6 +87,8 @@ struct Cfg4 {
     static constexpr int TMEM_COLS = COLS_USED <= 256 ? 256 : 512;
     static_assert(COLS_USED <= 512, "accumulators and scales fit tensor memory");
     static constexpr size_t SMEM = size_t(STAGES) * STAGE + 2048;
+    static constexpr int TURN_STAGES = (kEpiWarps * 32 * 33 * 4 + STAGE - 1) / STAGE;  // of the ring, where C is staged
+    static_assert(STAGES - TURN_STAGES >= 3, "a ring remains");
     static_assert(size_t(STAGES) * STAGE >= 128 * BN * 4 || CTAS == 2, "a K-split partial tile fits the ring");
 };
 
@@ -247,6 +250,15 @@ __device__ __forceinline__ void store_row(const Fp4Args &a, int64_t at, const fl
     }
 }
 
+__device__ __forceinline__ void store_one(const Fp4Args &a, int64_t at, float v) {
+    if (a.out_type == PTC_OUT_F32)
+        static_cast<float *>(a.C)[at] = v;
+    else if (a.out_type == PTC_OUT_BF16)
+        static_cast<__nv_bfloat16 *>(a.C)[at] = __float2bfloat16_rn(v);
+    else
+        static_cast<__half *>(a.C)[at] = __float2half_rn(v);
+}
+
 template <int CTAS, int BN, bool NV>
 __global__ void __launch_bounds__(kThreads, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -259,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
     const uint32_t ring = raw_addr + pad;  // stages: A, B, scales of A, scales of B
     Tail4<STAGES> *st = reinterpret_cast<Tail4<STAGES> *>(smem_raw + pad + STAGES * C_::STAGE);
+    const int nst = args.stages;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint64_t limit = args.wait_limit;
     const int cl = CTAS == 2 ? 2 : args.ks;  // CTAs per cluster
@@ -332,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             load_scales<2>(sa + C_::SFA_BYTES, &tmSB, bar, kb * C_::KAT, n0 / 128);
                         }
                     }
-                    if (++s == STAGES) {
+                    if (++s == nst) {
                         s = 0;
                         ph ^= 1u;
                     }
@@ -403,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     __syncwarp();
-                    if (++s == STAGES) {
+                    if (++s == nst) {
                         s = 0;
                         ph ^= 1u;
                     }
@@ -420,6 +433,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ---------------------------------------------------------- epilogue
         const int ew = warp - 2, q = warp & 3, h = ew >> 2;
+        // Rows that are not 16-byte aligned leave through the end of the ring.
+        float *turn = reinterpret_cast<float *>(smem_raw + pad + nst * C_::STAGE) + ew * (32 * 33);
         constexpr int NCH = BN / 64;  // 32-column chunks per warp
         const float alpha = __fmul_rn(args.ga ? __ldg(args.ga) : 1.0f, args.gb ? __ldg(args.gb) : 1.0f);
         int n = 0;
@@ -460,6 +475,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                             st_shared_v4(base + (uint32_t((8 * c + j) ^ (lrow & 7)) << 4), r[4 * j], r[4 * j + 1],
                                          r[4 * j + 2], r[4 * j + 3]);
                     }
+                } else if (args.vec == 0) {
+                    // A lane per row would write 32 scattered elements at a time;
+                    // turned around, the warp writes 32 columns of one row.
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) turn[lane * 33 + j] = __fmul_rn(__uint_as_float(r[j]), alpha);
+                    __syncwarp();
+                    const int first = row - lane, rows = min(32, args.M - first);
+                    if (col + lane < args.N) {
+                        int64_t at = int64_t(first) * args.ldc + col + lane;
+#pragma unroll 4
+                        for (int i2 = 0; i2 < rows; ++i2, at += args.ldc) store_one(args, at, turn[i2 * 33 + lane]);
+                    }
+                    __syncwarp();
                 } else if (row < args.M && col < args.N) {
                     float v[32];
 #pragma unroll
@@ -524,18 +552,36 @@ struct Shape4 {
     int tile, ks;  // 256: CTA pairs
 };
 
+// The shape of least estimated time, in units of 0.01 us, fitted to every shape
+// at 21 sizes (M 1 .. 2048, N 128 .. 16384, K 512 .. 8192): a call of 128 x 64
+// tiles takes 2.6 us plus 0.25 us per stage and wave, of 128 x 128 tiles 3.4 and
+// 0.27, of pairs 4.75 and 0.30; sharing K in a cluster costs 1.8 or 2.3 us and
+// is taken where it saves a tenth.
 Shape4 choose4(int64_t M, int64_t N, int num_kb, int sms) {
-    int tile = g_tile.load(), ks = g_split.load();
-    const int64_t t128 = ceil_div(M, 128) * ceil_div(N, 128), t64 = ceil_div(M, 128) * ceil_div(N, 64);
-    if (tile == 0) tile = 4 * t128 > 3 * sms ? 256 : 2 * t128 > sms ? 128 : 64;
-    if (tile == 256) return {256, 1};
-    const int64_t tiles = tile == 128 ? t128 : t64;
-    if (ks == 0) {
-        ks = 8;
-        while (ks > 1 && (tiles * ks > sms || num_kb < ks)) ks /= 2;
+    const int tile = g_tile.load(), ks = g_split.load();
+    const int64_t m128 = ceil_div(M, 128);
+    Shape4 best{256, 1};
+    int64_t best_cost = INT64_MAX;
+    if (tile == 0 || tile == 256)
+        best_cost = 475 + ceil_div(ceil_div(M, 256) * ceil_div(N, 256), sms / 2) * num_kb * 30;
+    const ClusterCaps caps = cluster_caps(sms);
+    for (int bn : {128, 64}) {
+        if (tile != 0 && tile != bn) continue;
+        const int64_t tiles = m128 * ceil_div(N, bn);
+        for (int k : {1, 2, 4, 8}) {
+            if ((ks != 0 && k != ks && k > 1) || num_kb < k) continue;
+            if (ks == 0 && k > 1 && tiles > caps.of(k)) continue;  // one wave of clusters
+            const int64_t waves = ceil_div(tiles * k, sms);
+            int64_t cost = (bn == 64 ? 260 : 340) + waves * ceil_div(num_kb, k) * (bn == 64 ? 25 : 27);
+            if (k > 1) cost = (cost + (bn == 64 ? 180 : 230)) * 11 / 10;
+            if (k > 1 && k == ks) cost = tile == 0 ? cost : -1;  // asked for
+            if (cost < best_cost) {
+                best_cost = cost;
+                best = {bn, k};
+            }
+        }
     }
-    if (num_kb < ks) ks = 1;
-    return {tile, ks};
+    return best;
 }
 
 template <int CTAS, int BN, bool NV>
@@ -581,6 +627,7 @@ cudaError_t launch4(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensor
         attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
         ++cfg.numAttrs;
     }
+    a.stages = C_::STAGES - (a.vec == 0 && a.ks == 1 ? C_::TURN_STAGES : 0);
     // K-split clusters take one tile each; the others walk the tiles.
     const int units = a.ks > 1 ? a.num_tiles : std::min(a.num_tiles, have);
     cfg.gridDim = dim3(unsigned(units * cl), 1, 1);
