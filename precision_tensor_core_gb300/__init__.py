@@ -439,62 +439,29 @@ _HOST_FN.update({gemm_f16: gemm_f16_host, gemm_s8: gemm_s8_host, gemm_s4: gemm_s
 
 
 # ---------------------------------------------------------------- 4-bit operators on tensors
-# These calls are a few microseconds on the device at decoding sizes, so the
-# marshalling below is kept to a few microseconds too: torch is looked up once,
-# the current stream and device are read through torch's raw accessors, and the
-# ctypes functions are called directly.
+# These calls are a few microseconds on the device at decoding sizes, so their
+# marshalling is native: _native.so (csrc/binding.cpp) checks the tensors,
+# allocates results and calls the C ABI.
 _FP4 = {"mxfp4": (PTC_FP4_MX, 32), "nvfp4": (PTC_FP4_NV, 16)}
 _ROUNDING = {"nearest": PTC_ROUND_NEAREST, "stochastic": PTC_ROUND_STOCHASTIC}
-_MASK64 = (1 << 64) - 1
-_TYPES = {}
-_torch = _u8 = _current_device = _current_stream = None
+_native = None
 
 
-def _load_torch():
-    """torch, imported by the first call (the package itself loads without it)."""
-    global _torch, _u8, _current_device, _current_stream
-    import torch
-    _TYPES.update({torch.float32: PTC_OUT_F32, torch.bfloat16: PTC_OUT_BF16, torch.float16: PTC_OUT_F16})
-    _u8 = torch.uint8
-    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-    _current_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
-                       or (lambda index: torch.cuda.current_stream(index).cuda_stream))
-    _torch = torch
-    return torch
-
-
-def _type_of(dtype):
-    """PTC_OUT_* of a torch dtype."""
-    code = _TYPES.get(dtype)
-    if code is None:
-        raise TypeError("tensors are float32, bfloat16 or float16")
-    return code
-
-
-def _rows_of(t, name):
-    """(rows, columns, row pitch in elements) of a 2-D device tensor with unit column stride."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D")
-    rows, cols = t.shape
-    s0, s1 = t.stride()
-    if rows <= 1:
-        s0 = cols
-    if (s1 != 1 and cols > 1) or s0 < cols:
-        raise ValueError(f"{name} must be a 2-D tensor with unit column stride and rows that do not overlap")
-    return rows, cols, s0
-
-
-def _call(fn, index, stream, *args):
-    """fn(*args, stream) with device `index` current, on the current stream of that device by default."""
-    if index == _current_device():
-        status = fn(*args, _current_stream(index) if stream is None else _stream(stream))
-    else:
-        with _torch.cuda.device(index):
-            status = fn(*args, _current_stream(index) if stream is None else _stream(stream))
-    if status:
-        _check(status)
+def _load_native():
+    """The native module, bound to libptc by the first call."""
+    global _native
+    import importlib
+    import torch  # noqa: F401  (its libraries are what the module links against)
+    path = os.path.join(_HERE, "_native.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"_native.so is not built ({path}); run __graft_entry__.build()")
+    n = importlib.import_module(__name__ + "._native")
+    L = lib()
+    n.init(*(ctypes.cast(getattr(L, f), _vp).value for f in ("ptc_dropout", "ptc_quantize_fp4", "ptc_dequantize_fp4",
+                                                             "gemm_fp4", "gemm_a16_fp4")),
+           _check, _stream, Fp4Matrix)
+    _native = n
+    return n
 
 
 def fp4_scale_bytes(rows: int, cols: int, fmt: str) -> int:
@@ -514,41 +481,18 @@ class Fp4Matrix:
         tensor of one element that scales the whole matrix.
     """
 
-    __slots__ = ("_codes", "_scales", "_K", "_fmt", "_ts", "_rows", "_pitch", "_code", "_index")
+    __slots__ = ("_codes", "_scales", "_K", "_fmt", "_ts")
 
     def __init__(self, codes, scales, K, fmt="mxfp4", tensor_scale=None):
-        if _torch is None:
-            _load_torch()
-        f = _FP4.get(fmt)
-        if f is None:
-            raise ValueError("fmt is 'mxfp4' or 'nvfp4'")
-        if codes.dtype != _u8 or scales.dtype != _u8:
-            raise TypeError("codes and scales are uint8")
-        rows, width, pitch = _rows_of(codes, "codes")
-        K = int(K)
-        need = -(-K // 32) * 16
-        if rows <= 1:
-            pitch = max(16, -(-width // 16) * 16)
-        if K < 0 or width < need or pitch % 16:
-            raise ValueError("codes must hold 16 * ceil(K / 32) bytes per row, rows a multiple of 16 bytes apart")
-        if not scales.is_contiguous() or scales.numel() < -(-rows // 128) * -(-K // (4 * f[1])) * 512:
-            raise ValueError("scales must be contiguous and hold whole tiles of 128 rows x 4 blocks")
-        self._set(codes, scales, K, fmt, tensor_scale, rows, pitch, f[0], codes.get_device())
-        if scales.get_device() != self._index:
-            raise ValueError("codes and scales must be on one device")
-        if tensor_scale is not None:
-            _check_tensor_scale(tensor_scale, fmt, self._index)
-
-    def _set(self, codes, scales, K, fmt, ts, rows, pitch, code, index):
-        self._codes, self._scales, self._K, self._fmt, self._ts = codes, scales, K, fmt, ts
-        self._rows, self._pitch, self._code, self._index = rows, pitch, code, index
+        (_native or _load_native()).check_matrix(codes, scales, K, fmt, tensor_scale)
+        self._codes, self._scales, self._K, self._fmt, self._ts = codes, scales, K, fmt, tensor_scale
 
     codes = property(lambda self: self._codes)
     scales = property(lambda self: self._scales)
     tensor_scale = property(lambda self: self._ts)
     K = property(lambda self: self._K)
     fmt = property(lambda self: self._fmt)
-    shape = property(lambda self: (self._rows, self._K))
+    shape = property(lambda self: (self._codes.shape[0], self._K))
     device = property(lambda self: self._codes.device)
 
     def record_stream(self, stream):
@@ -567,22 +511,10 @@ class Fp4Matrix:
 
     def row_scales(self):
         """Row-major scale bytes (rows, blocks)."""
-        r, b = self._rows, -(-self._K // _FP4[self._fmt][1])
+        r, b = self._codes.shape[0], -(-self._K // _FP4[self._fmt][1])
         kt = -(-b // 4)
         s = self._scales.view(-1)[:fp4_scale_bytes(r, self._K, self._fmt)].view(-1, kt, 32, 4, 4)
         return s.permute(0, 3, 2, 1, 4).reshape(-1, kt * 4)[:r, :b]
-
-    def _args(self):
-        """(codes, pitch, scales, matrix scale) of the C calls."""
-        ts = self._ts
-        return self._codes.data_ptr(), self._pitch, self._scales.data_ptr(), None if ts is None else ts.data_ptr()
-
-
-def _check_tensor_scale(ts, fmt, index):
-    if fmt != "nvfp4":
-        raise ValueError("only nvfp4 has a tensor scale")
-    if ts.dtype != _torch.float32 or ts.numel() != 1 or not ts.is_cuda or ts.get_device() != index:
-        raise ValueError("tensor_scale is a float32 tensor of one element on the matrix's device")
 
 
 def dropout(x, p, seed, offset=0, residual=None, out=None, stream=None):
@@ -591,36 +523,7 @@ def dropout(x, p, seed, offset=0, residual=None, out=None, stream=None):
     or float16 (rows, cols).  The mask is a function of (seed, offset, row,
     column) and is never stored: the backward pass is the same call on the
     gradient.  ``out`` may be ``x`` or ``residual``."""
-    torch = _torch or _load_torch()
-    dtype = x.dtype
-    code = _type_of(dtype)
-    rows, cols, ldx = _rows_of(x, "x")
-    index = x.get_device()
-    ldr, rp = 0, None
-    if residual is not None:
-        if residual.dtype != dtype or residual.shape != x.shape or residual.get_device() != index:
-            raise ValueError("residual must have x's shape, dtype and device")
-        ldr, rp = _rows_of(residual, "residual")[2], residual.data_ptr()
-    if out is None:
-        out, ldy = torch.empty((rows, cols), dtype=dtype, device=x.device), cols
-    else:
-        if out.dtype != dtype or out.shape != x.shape or out.get_device() != index:
-            raise ValueError("out must have x's shape, dtype and device")
-        ldy = _rows_of(out, "out")[2]
-    _call((_lib or lib()).ptc_dropout, index, stream, rows, cols, x.data_ptr(), ldx, rp, ldr, out.data_ptr(), ldy, code,
-          p, seed & _MASK64, offset)
-    return out
-
-
-def _new_fp4(rows, cols, fmt, f, device, index, ts):
-    """An uninitialised matrix."""
-    empty = _torch.empty
-    width = -(-cols // 32) * 16
-    q = Fp4Matrix.__new__(Fp4Matrix)
-    q._set(empty((rows, width), dtype=_u8, device=device),
-           empty(-(-rows // 128) * -(-cols // (4 * f[1])) * 512, dtype=_u8, device=device),
-           cols, fmt, ts, rows, width or 16, f[0], index)
-    return q
+    return (_native or _load_native()).dropout(x, p, seed, offset, residual, out, stream)
 
 
 def quantize_fp4(x, fmt="mxfp4", transposed=False, rounding="nearest", tensor_scale=None, p=0.0, seed=0, offset=0,
@@ -633,73 +536,25 @@ def quantize_fp4(x, fmt="mxfp4", transposed=False, rounding="nearest", tensor_sc
     rounding: "nearest" (ties to even) or "stochastic" (bits from seed, offset).
     p: with p > 0 the values are ``dropout(x, p, seed, offset)`` in float32.
     """
-    if _torch is None:
-        _load_torch()
-    f = _FP4.get(fmt)
-    if f is None:
-        raise ValueError("fmt is 'mxfp4' or 'nvfp4'")
     how = _ROUNDING.get(rounding)
     if how is None:
         raise ValueError("rounding is 'nearest' or 'stochastic'")
-    if transposed not in (False, True, "both"):
+    which = 0 if transposed is False else 1 if transposed is True else 2
+    if which == 2 and transposed != "both":
         raise ValueError("transposed is False, True or 'both'")
-    code = _type_of(x.dtype)
-    rows, cols, ldx = _rows_of(x, "x")
-    index, device = x.get_device(), x.device
-    gp = None
-    if tensor_scale is not None:
-        _check_tensor_scale(tensor_scale, fmt, index)
-        gp = tensor_scale.data_ptr()
-    q = qt = None
-    a = b = (None, 0, None)
-    if transposed is not True:
-        q = _new_fp4(rows, cols, fmt, f, device, index, tensor_scale)
-        a = q._args()
-    if transposed is not False:
-        qt = _new_fp4(cols, rows, fmt, f, device, index, tensor_scale)
-        b = qt._args()
-    _call((_lib or lib()).ptc_quantize_fp4, index, stream, rows, cols, x.data_ptr(), ldx, code, f[0], how, gp, a[0],
-          a[1], a[2], b[0], b[1], b[2], p, seed & _MASK64, offset)
-    return (q, qt) if transposed == "both" else (qt if transposed else q)
-
-
-def _result(out, rows, cols, dtype, index, device):
-    """(result tensor, its pitch)."""
-    if out is None:
-        return _torch.empty((rows, cols), dtype=dtype, device=device), cols
-    if out.dim() != 2 or out.shape[0] != rows or out.shape[1] != cols or out.get_device() != index:
-        raise ValueError(f"out must be a ({rows}, {cols}) tensor on the operands' device")
-    return out, _rows_of(out, "out")[2]
+    return (_native or _load_native()).quantize(x, fmt, which, how, tensor_scale, p, seed, offset, stream)
 
 
 def dequantize_fp4(q, dtype=None, out=None, stream=None):
     """The values of an :class:`Fp4Matrix` as float32, bfloat16 (default) or float16."""
-    dtype = out.dtype if out is not None else (dtype or _torch.bfloat16)
-    code = _type_of(dtype)
-    y, ldy = _result(out, q._rows, q._K, dtype, q._index, q._codes.device)
-    c, pitch, s, g = q._args()
-    _call((_lib or lib()).ptc_dequantize_fp4, q._index, stream, q._rows, q._K, c, pitch, s, q._code, g, y.data_ptr(), ldy,
-          code)
-    return y
+    return (_native or _load_native()).dequantize(q, dtype, out, stream)
 
 
 def matmul_fp4(A, Bt, out_dtype=None, out=None, stream=None):
     """A (M,K) @ B with B given as Bt (N,K), both :class:`Fp4Matrix` of one format
     -> float32, bfloat16 (default) or float16 (M,N), summed in FP32 on the
     block-scaled tensor cores."""
-    if A._code != Bt._code:
-        raise ValueError("both matrices must have the same format")
-    if A._K != Bt._K:
-        raise ValueError("inner dimensions differ")
-    index = A._index
-    if index != Bt._index:
-        raise ValueError("both matrices must be on one device")
-    dtype = out.dtype if out is not None else (out_dtype or _torch.bfloat16)
-    code = _type_of(dtype)
-    C, ldc = _result(out, A._rows, Bt._rows, dtype, index, A._codes.device)
-    _call((_lib or lib()).gemm_fp4, index, stream, A._rows, Bt._rows, A._K, A._code, *A._args(), *Bt._args(),
-          C.data_ptr(), ldc, code)
-    return C
+    return (_native or _load_native()).matmul(A, Bt, out_dtype, out, stream)
 
 
 def matmul_a16_fp4(x, Wt, out=None, stream=None):
@@ -707,20 +562,4 @@ def matmul_a16_fp4(x, Wt, out=None, stream=None):
     dtype (M,N), summed in FP32: the product of a decoding step, for M up to 16
     rows (more are taken 16 at a time; quantise x and use :func:`matmul_fp4`
     for many)."""
-    if _torch is None:
-        _load_torch()
-    dtype = x.dtype
-    code = _type_of(dtype)
-    if code == PTC_OUT_F32:
-        raise TypeError("matmul_a16_fp4 takes bfloat16 or float16 activations")
-    rows, cols, ldx = _rows_of(x, "x")
-    if cols != Wt._K:
-        raise ValueError("inner dimensions differ")
-    index = Wt._index
-    if x.get_device() != index or (out is not None and out.dtype != dtype):
-        raise ValueError("x, the weights and out must share a device, x and out a dtype")
-    C, ldc = _result(out, rows, Wt._rows, dtype, index, x.device)
-    w, pitch, s, g = Wt._args()
-    _call((_lib or lib()).gemm_a16_fp4, index, stream, rows, Wt._rows, cols, code, x.data_ptr(), ldx, Wt._code, w, pitch, s, g,
-          C.data_ptr(), ldc)
-    return C
+    return (_native or _load_native()).matmul_a16(x, Wt, out, stream)

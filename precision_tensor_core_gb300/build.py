@@ -5,6 +5,8 @@ one nvcc link produces ``precision_tensor_core_gb300/libptc.so`` with the CUDA
 runtime linked statically (the driver API is reached at run time through the
 runtime's entry-point query, so the library loads on machines without a GPU
 driver).  ptxas register/shared-memory reports go to ``_build/ptxas.log``.
+Beside it ``_native.so``, the CPython module of the 4-bit operators' tensor layer
+(csrc/binding.cpp), compiles with g++ against the installed torch's headers.
 """
 from __future__ import annotations
 
@@ -22,6 +24,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libptc.so")
 SOURCES = ["gemm_tc.cu", "convert.cu", "api.cu", "gemm_s8_noalloc.cu", "baseline.cu", "fp4_quant.cu",
            "fp4_gemm.cu", "fp4_tokens.cu"]
+BINDING = "binding.cpp"
+NATIVE = os.path.join(HERE, "_native.so")
 GENCODE = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -40,10 +44,31 @@ def _compile(src: str) -> tuple[str, str]:
     return obj, r.stderr
 
 
+def _compile_binding() -> None:
+    """_native.so, against the torch that `import torch` would load (not imported here)."""
+    import importlib.util
+    import sysconfig
+    spec = importlib.util.find_spec("torch")
+    if spec is None or spec.origin is None:
+        raise RuntimeError("torch is not installed; the tensor layer of the 4-bit operators needs its headers")
+    torch = os.path.dirname(spec.origin)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    tmp = NATIVE + f".tmp{os.getpid()}"
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-I", INCLUDE, "-I", os.path.join(torch, "include"),
+           "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_path("include"),
+           os.path.join(CSRC, BINDING), "-o", tmp, "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu",
+           "-ltorch", "-lc10", "-lc10_cuda", "-Wl,-rpath," + os.path.join(torch, "lib")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING}:\n{r.stderr}\n{r.stdout}")
+    os.replace(tmp, NATIVE)
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(NATIVE):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(NATIVE))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "ptc.h"), __file__]
     return any(os.path.getmtime(d) > t for d in deps)
 
@@ -52,8 +77,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(_compile, SOURCES))
+        binding.result()
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         for (obj, log), src in zip(results, SOURCES):
             f.write(f"== {src}\n{log}\n")
