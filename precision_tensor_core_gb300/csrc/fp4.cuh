@@ -18,34 +18,42 @@ namespace ptc {
 // ------------------------------------------------------------ generator
 // Philox4x32-10 (Salmon, Moraes, Dror, Shaw: "Parallel random numbers: as easy
 // as 1, 2, 3", SC 2011): ten rounds of two 32 x 32 -> 64-bit products.  One
-// call gives the 16 bits of eight consecutive elements of a row.
-__device__ __forceinline__ uint4 philox10(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t k0,
-                                          uint32_t k1) {
-#pragma unroll
-    for (int i = 0; i < 10; ++i) {
-        const uint64_t p0 = uint64_t(0xD2511F53u) * c0, p1 = uint64_t(0xCD9E8D57u) * c2;
-        c0 = uint32_t(p1 >> 32) ^ c1 ^ k0;
-        c1 = uint32_t(p1);
-        c2 = uint32_t(p0 >> 32) ^ c3 ^ k1;
-        c3 = uint32_t(p0);
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
+// call gives the 16 bits of eight consecutive elements of a row.  The ten
+// rounds' keys are made on the host, so that a round is two products and two
+// three-way exclusive ors with a kernel parameter.
+struct RngArgs {
+    uint32_t key[20];         // of round i: key[2 i], key[2 i + 1]
+    uint32_t off_lo, off_hi;  // offset (63 bits)
+};
+
+inline RngArgs make_rng(uint64_t seed, uint64_t offset) {
+    RngArgs r;
+    uint32_t k0 = uint32_t(seed), k1 = uint32_t(seed >> 32);
+    for (int i = 0; i < 10; ++i, k0 += 0x9E3779B9u, k1 += 0xBB67AE85u) {
+        r.key[2 * i] = k0;
+        r.key[2 * i + 1] = k1;
     }
-    return make_uint4(c0, c1, c2, c3);
+    r.off_lo = uint32_t(offset);
+    r.off_hi = uint32_t(offset >> 32);
+    return r;
 }
 
 // What a stream of random bits is for: its own counters for each.
 constexpr uint32_t kRngDropout = 0, kRngRounding = 1;
 
-struct RngArgs {
-    uint32_t k0, k1;          // seed
-    uint32_t off_lo, off_hi;  // offset (63 bits)
-};
-
 // The 16-bit numbers of elements (row, 8 group .. 8 group + 7): element j has
 // bits 16 (j & 1) .. of word j >> 1.
 __device__ __forceinline__ uint4 random_bits8(const RngArgs &g, uint32_t purpose, uint32_t row, uint32_t group) {
-    return philox10(group, row, g.off_lo, g.off_hi | (purpose << 31), g.k0, g.k1);
+    uint32_t c0 = group, c1 = row, c2 = g.off_lo, c3 = g.off_hi | (purpose << 31);
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+        const uint64_t p0 = uint64_t(0xD2511F53u) * c0, p1 = uint64_t(0xCD9E8D57u) * c2;
+        c0 = uint32_t(p1 >> 32) ^ c1 ^ g.key[2 * i];
+        c1 = uint32_t(p1);
+        c2 = uint32_t(p0 >> 32) ^ c3 ^ g.key[2 * i + 1];
+        c3 = uint32_t(p0);
+    }
+    return make_uint4(c0, c1, c2, c3);
 }
 
 __device__ __forceinline__ uint32_t bits16(const uint4 &w, int j) {
@@ -213,18 +221,38 @@ __device__ __forceinline__ uint32_t codes_nearest(const float (&v)[8]) {
 }
 
 // One value rounded down or up to the neighbouring codes, up when its
-// remainder (in 1/65536 of the gap) plus r reaches 65536.  The gaps are 0.5
-// below 2, 1 below 4 and 2 below 6.  The distance to the first code of the
-// range in 1/65536 of the gap is u * 65536 / gap rounded down to a whole number
-// (an addition of 2^23 that rounds down leaves it in the low bits), and the
-// sum with r carries into bit 16 exactly where the code goes up.
-__device__ __forceinline__ uint32_t code_stochastic(float v, uint32_t r) {
+// remainder (in 1/65536 of the gap) plus r reaches 65536; the code in bits 16 ..
+// 19 of the result, other bits undefined.  With e the exponent of max(u, 1),
+// u = |v| at most 6, the gap is 2^(e - 1) and the range starts at code 2 e.  The
+// distance from 0 in 1/65536 of the gap, u 2^(17 - e), is rounded down to a
+// whole number T by an addition of 2^23 that rounds down; from there code
+// 2 e is 2 e (65536) further than in a uniform grid: (T + 2 e 65536 + r) / 65536
+// rounded down is the code.  `r2` is r + 2 * 65536, which makes up for the bias
+// 127 of the exponent field (2 * 127 = -2 modulo 8); the sum's higher bits, of
+// 2^23 and of the field, stay clear of bits 16 .. 18.
+__device__ __forceinline__ uint32_t code_stochastic(float v, uint32_t r2) {
     const float u = fminf(fabsf(v), 6.0f);
-    const bool low2 = u < 2.0f, low4 = u < 4.0f;
-    const float t = __fmaf_rd(u, low2 ? 131072.0f : low4 ? 65536.0f : 32768.0f, 8388608.0f);
-    const uint32_t base = (low2 ? 0u : low4 ? 2u << 16 : 4u << 16) - 0x4B000000u;  // bits of 2^23
-    const uint32_t code = (__float_as_uint(t) + base + r) >> 16;
-    return code | ((__float_as_uint(v) >> 28) & 8u);
+    const uint32_t m = max(__float_as_uint(u), 0x3F800000u) & 0x7F800000u;  // e + 127 in the exponent field
+    const float t = __fmaf_rd(u, __uint_as_float(0x87800000u - m), 8388608.0f);
+    const uint32_t code = __float_as_uint(t) + (m >> 6) + r2;
+    return (code & 0x70000u) | ((__float_as_uint(v) >> 12) & 0x80000u);
+}
+
+// Eight codes of code_stochastic, value j in bits 4 j .. 4 j + 3 of the result.
+__device__ __forceinline__ uint32_t pack_stochastic(const uint32_t (&c)[8]) {
+    uint32_t p[4];  // two codes in bits 16 .. 23
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = c[2 * i] + 16u * c[2 * i + 1];
+    return __byte_perm(__byte_perm(p[0], p[1], 0x0062), __byte_perm(p[2], p[3], 0x0062), 0x5410);
+}
+
+// r + 2 * 65536 of element j of eight (bits as random_bits8 gives them), and of
+// the low and high half of a word.
+__device__ __forceinline__ uint32_t low_r2(uint32_t w) { return __byte_perm(w, 2u, 0x5410); }
+__device__ __forceinline__ uint32_t high_r2(uint32_t w) { return __byte_perm(w, 2u, 0x5432); }
+__device__ __forceinline__ uint32_t bits_r2(const uint4 &w, int j) {
+    const uint32_t x = (j >> 1) == 0 ? w.x : (j >> 1) == 1 ? w.y : (j >> 1) == 2 ? w.z : w.w;
+    return (j & 1) ? high_r2(x) : low_r2(x);
 }
 
 // Eight codes (a 32-bit word) as eight binary16 values, exactly: word i of the

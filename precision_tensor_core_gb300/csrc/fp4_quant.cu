@@ -8,6 +8,7 @@
 
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "fp4.cuh"
 #include "internal.h"
@@ -103,6 +104,24 @@ __device__ __forceinline__ void dropped8(const Pack8<T> &a, const DropArgs &d, i
     }
 }
 
+// The FP32 bits of the largest magnitude of eight elements as they came; of
+// 16-bit elements in pairs (their bits order like the magnitudes).
+template <typename T>
+__device__ __forceinline__ uint32_t max_abs8(const Pack8<T> &p) {
+    if constexpr (sizeof(T) == 4) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(to_float(p.get(j))) & 0x7FFFFFFFu);
+        return m;
+    } else {
+        const uint4 &w = p.v[0];
+        constexpr uint32_t K = 0x7FFF7FFFu;
+        const uint32_t m = __vmaxu2(__vmaxu2(w.x & K, w.y & K), __vmaxu2(w.z & K, w.w & K));
+        const uint16_t top = uint16_t(max(m & 0xFFFFu, m >> 16));
+        return __float_as_uint(to_float(reinterpret_cast<const T &>(top)));
+    }
+}
+
 __device__ __forceinline__ uint32_t max_abs8(const float (&v)[8]) {
     uint32_t m = 0;  // of the bits, so that infinities and NaN come out on top
 #pragma unroll
@@ -116,8 +135,10 @@ __device__ __forceinline__ uint32_t codes8(const float (&v)[8], uint32_t amax, c
                                            const uint4 &bits) {
     uint32_t q = 0;
     if constexpr (SR) {
+        uint32_t c[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q |= code_stochastic(scale.apply(v[j]), bits16(bits, j)) << (4 * j);
+        for (int j = 0; j < 8; ++j) c[j] = code_stochastic(scale.apply(v[j]), bits_r2(bits, j));
+        q = pack_stochastic(c);
     } else {
         float s[8];
 #pragma unroll
@@ -142,35 +163,50 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *x, const Qu
     const float g = (NV && a.g != nullptr) ? __ldg(a.g) : 1.0f;
     const int64_t ktiles = (a.cols + 8 * LPT - 1) / (8 * LPT);
     const int64_t rows_p = (a.rows + 127) / 128 * 128;
-    const int64_t cols_p = (a.cols + 31) / 32 * 32;
+    const int cols = int(a.cols);
     Walk w((int64_t(blockIdx.x) * blockDim.x + threadIdx.x) / 32, int64_t(gridDim.x) * blockDim.x / 32,
-           uint32_t((a.cols + 256 * U - 1) / (256 * U)));
+           uint32_t((cols + 256 * U - 1) / (256 * U)));
     for (; w.row < rows_p; w.next()) {
-        const int64_t c0 = int64_t(w.group) * (256 * U) + lane * 8;
-        const bool real = w.row < a.rows;  // uniform over the warp
-        Pack8<T> p[U];
+        const int c0 = int(w.group) * (256 * U);
+        uint8_t *const scale_row = a.scales + scale_word(w.row, 0, ktiles);
+        if (w.row >= a.rows) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t c = c0 + 256 * u;
-            const int n = real ? int(max(int64_t(0), min(int64_t(8), a.cols - c))) : 0;
-            p[u] = load8(x + (n > 0 ? w.row * a.ldx + c : 0), n, a.vec != 0);
+            for (int u = 0; u < U; ++u) {
+                const int64_t kt = (c0 + 256 * u + lane * 8) / (8 * LPT);
+                if (lane % LPT == 0 && kt < ktiles) *reinterpret_cast<uint32_t *>(scale_row + kt * kScaleTile) = 0u;
+            }
+            continue;
         }
+        const T *const row = x + w.row * a.ldx;
+        uint8_t *const code_row = a.codes + w.row * a.pitch;
+        // Whole: 256 U aligned columns that all exist.
+        auto chunk = [&](auto whole) {
+            constexpr bool WHOLE = decltype(whole)::value;
+            Pack8<T> p[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t c = c0 + 256 * u;
-            if (U > 1 && c - lane * 8 >= cols_p) break;  // (uniform: nothing of these 256 columns exists)
-            uint32_t word = 0;
-            if (real) {
+            for (int u = 0; u < U; ++u) {
+                const int c = c0 + 256 * u + lane * 8;
+                const int n = WHOLE ? 8 : max(0, min(8, cols - c));
+                p[u] = load8(row + (n > 0 ? c : 0), n, WHOLE || a.vec != 0);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = c0 + 256 * u + lane * 8;
+                if (!WHOLE && c0 + 256 * u >= cols) break;  // (uniform)
                 float v[8];
-                dropped8<T, DROP>(p[u], a.drop, w.row, uint32_t(c / 8), v);
+                uint32_t m;
                 if constexpr (DROP) {
-                    if (c + 8 > a.cols) {
+                    dropped8<T, DROP>(p[u], a.drop, w.row, uint32_t(c / 8), v);
+                    if (!WHOLE && c + 8 > cols) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            if (c + j >= a.cols) v[j] = 0.0f;
+                            if (c + j >= cols) v[j] = 0.0f;
                     }
+                    m = max_abs8(v);
+                } else {
+                    dropped8<T, DROP>(p[u], a.drop, w.row, uint32_t(c / 8), v);
+                    m = max_abs8(p[u]);
                 }
-                uint32_t m = max_abs8(v);
                 m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
                 if constexpr (!NV) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
                 uint32_t byte;
@@ -178,16 +214,20 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *x, const Qu
                 uint4 bits = make_uint4(0, 0, 0, 0);
                 if constexpr (SR) bits = random_bits8(a.drop.rng, kRngRounding, uint32_t(w.row), uint32_t(c / 8));
                 const uint32_t q = codes8<NV, SR>(v, m, scale, bits);
-                if (c < cols_p) *reinterpret_cast<uint32_t *>(a.codes + w.row * a.pitch + c / 2) = q;
+                if (WHOLE || c < (cols + 31) / 32 * 32) *reinterpret_cast<uint32_t *>(code_row + c / 2) = q;
                 // Four blocks' bytes to one word (held by the first lane of the four).
-                word = byte;
+                uint32_t word = byte;
                 word |= __shfl_down_sync(0xFFFFFFFFu, word, LPB) << 8;
                 word |= __shfl_down_sync(0xFFFFFFFFu, word, 2 * LPB) << 16;
+                const int64_t kt = c / (8 * LPT);
+                if (lane % LPT == 0 && (WHOLE || kt < ktiles))
+                    *reinterpret_cast<uint32_t *>(scale_row + kt * kScaleTile) = word;
             }
-            const int64_t kt = c / (8 * LPT);
-            if (lane % LPT == 0 && kt < ktiles)
-                *reinterpret_cast<uint32_t *>(a.scales + scale_word(w.row, kt, ktiles)) = word;
-        }
+        };
+        if (a.vec != 0 && c0 + 256 * U <= cols)
+            chunk(std::integral_constant<bool, true>());
+        else
+            chunk(std::integral_constant<bool, false>());
     }
 }
 
@@ -312,12 +352,15 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const T *x, const Qu
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
         if constexpr (SR) {
+            uint32_t ca[8], cb[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint32_t r = *reinterpret_cast<const uint32_t *>(rs + (16 * warp + 8 * w + j) * kTileC + 2 * lane);
-                qa[w] |= code_stochastic(sa.apply(va[8 * w + j]), r & 0xFFFFu) << (4 * j);
-                qb[w] |= code_stochastic(sb.apply(vb[8 * w + j]), r >> 16) << (4 * j);
+                ca[j] = code_stochastic(sa.apply(va[8 * w + j]), low_r2(r));
+                cb[j] = code_stochastic(sb.apply(vb[8 * w + j]), high_r2(r));
             }
+            qa[w] = pack_stochastic(ca);
+            qb[w] = pack_stochastic(cb);
         } else {
             float s[8];
 #pragma unroll
@@ -376,6 +419,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *codes, i
     const int lane = threadIdx.x & 31;
     Walk w((int64_t(blockIdx.x) * blockDim.x + threadIdx.x) / 32, int64_t(gridDim.x) * blockDim.x / 32,
            uint32_t((cols + 256 * U - 1) / (256 * U)));
+    __shared__ __align__(16) T turn[8][256];  // a warp's 256 values where rows are not aligned
     for (; w.row < rows; w.next()) {
         const int64_t c0 = int64_t(w.group) * (256 * U) + lane * 8;
         uint32_t q[U], b[U];
@@ -392,7 +436,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *codes, i
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t c = c0 + 256 * u;
-            if (c >= cols) break;
+            if (c - lane * 8 >= cols) break;  // (uniform)
             const float s = scale_value<NV>(b[u]);
             uint32_t h[4];
             codes_to_f16(q[u], h);
@@ -405,7 +449,21 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *codes, i
                 if (has_g) v = __fmul_rn(v, g);
                 o.set(j, from_float<T>(v));
             }
-            store8(y + w.row * ldy + c, o, int(min(int64_t(8), cols - c)), vec != 0);
+            if (vec != 0) {
+                if (c < cols) store8(y + w.row * ldy + c, o, int(min(int64_t(8), cols - c)), true);
+            } else {
+                // Turned around, so that a store writes 32 consecutive elements.
+                T *t = turn[threadIdx.x >> 5];
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < Pack8<T>::W; ++i) reinterpret_cast<uint4 *>(t + lane * 8)[i] = o.v[i];
+                __syncwarp();
+                T *dst = y + w.row * ldy + (c - lane * 8);
+                const int n = int(min(int64_t(256), cols - (c - lane * 8)));
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (32 * i + lane < n) dst[32 * i + lane] = t[32 * i + lane];
+            }
         }
     }
 }
@@ -452,7 +510,7 @@ DropArgs drop_args(double p, uint64_t seed, uint64_t offset) {
     DropArgs d;
     d.kept = uint32_t((1.0 - p) * 65536.0 + 0.5);
     d.scale = float(65536.0 / (d.kept > 0 ? d.kept : 1u));
-    d.rng = {uint32_t(seed), uint32_t(seed >> 32), uint32_t(offset), uint32_t(offset >> 32)};
+    d.rng = make_rng(seed, offset);
     return d;
 }
 
