@@ -129,6 +129,12 @@ __device__ __forceinline__ uint32_t max_abs8(const float (&v)[8]) {
     return m;
 }
 
+// The bits of a magnitude after dropout's scaling (monotonic, so the largest
+// stays the largest; a NaN stays one, whatever its sign).
+__device__ __forceinline__ uint32_t scaled_bits(uint32_t m, float scale) {
+    return __float_as_uint(__fmul_rn(__uint_as_float(m), scale)) & 0x7FFFFFFFu;
+}
+
 // Eight codes of values v with the block's scale.
 template <bool NV, bool SR>
 __device__ __forceinline__ uint32_t codes8(const float (&v)[8], uint32_t amax, const BlockScale<NV> &scale,
@@ -295,9 +301,10 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const T *x, const Qu
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     v[j] = DROP ? __fmul_rn(to_float(p[i].get(j)), a.drop.scale) : to_float(p[i].get(j));
-                uint32_t m = max_abs8(v);
+                uint32_t m = max_abs8(p[i]);
                 m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
                 if constexpr (!NV) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+                if constexpr (DROP) m = scaled_bits(m, a.drop.scale);
                 uint32_t byte;
                 const BlockScale<NV> scale = block_scale<NV, SR>(m, g, byte);
                 const uint32_t q = codes8<NV, SR>(v, m, scale, bits);
@@ -331,13 +338,27 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const T *x, const Qu
     struct alignas(2 * sizeof(T)) Two {
         T a, b;
     };
+    uint32_t both = 0;  // largest magnitudes of 16-bit elements, in pairs
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const Two t = *reinterpret_cast<const Two *>(xs + (16 * warp + i) * kTileC + 2 * lane);
         va[i] = DROP ? __fmul_rn(to_float(t.a), a.drop.scale) : to_float(t.a);
         vb[i] = DROP ? __fmul_rn(to_float(t.b), a.drop.scale) : to_float(t.b);
-        ma = max(ma, __float_as_uint(va[i]) & 0x7FFFFFFFu);
-        mb = max(mb, __float_as_uint(vb[i]) & 0x7FFFFFFFu);
+        if constexpr (sizeof(T) == 2) {
+            both = __vmaxu2(both, reinterpret_cast<const uint32_t &>(t) & 0x7FFF7FFFu);
+        } else {
+            ma = max(ma, __float_as_uint(va[i]) & 0x7FFFFFFFu);
+            mb = max(mb, __float_as_uint(vb[i]) & 0x7FFFFFFFu);
+        }
+    }
+    if constexpr (sizeof(T) == 2) {
+        const Two t = reinterpret_cast<const Two &>(both);
+        ma = __float_as_uint(to_float(t.a));
+        mb = __float_as_uint(to_float(t.b));
+        if constexpr (DROP) {
+            ma = scaled_bits(ma, a.drop.scale);
+            mb = scaled_bits(mb, a.drop.scale);
+        }
     }
     if constexpr (!NV) {
         top[warp * kTileC + 2 * lane] = ma;
