@@ -249,11 +249,13 @@ __global__ void __launch_bounds__(kTokThreads, 2)
         const uint32_t nv_pick = t < 2 ? 0x4420u : 0x4431u;  // this lane's half of a 32-code block: bytes 0, 2 or 1, 3
         // 16-byte piece 4 b + t (block b) of a token's stage lies at 4 (b ^ (token & 1)) + t.
         // (Tokens past the last read it again; their sums are dropped.)
-        uint32_t x_at[NT];
+        // Even blocks from x_at[n][0], odd ones from x_at[n][1], 128 bytes apart.
+        uint32_t x_at[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int tok = min(8 * n + gr, ntok - 1);
-            x_at[n] = uint32_t(share) * share_bytes + uint32_t(tok) * tok_bytes + (uint32_t(tok & 1) << 6) + uint32_t(t) * 16u;
+            x_at[n][0] = uint32_t(share) * share_bytes + uint32_t(tok) * tok_bytes + (uint32_t(tok & 1) << 6) + uint32_t(t) * 16u;
+            x_at[n][1] = x_at[n][0] ^ 64u;
         }
         // The activations of chunk `c` of every share: f(shared-memory offset of the
         // piece in buffer c & 1, offset of its block's power of two, source, valid
@@ -359,7 +361,7 @@ __global__ void __launch_bounds__(kTokThreads, 2)
                         }
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            const uint4 x = *reinterpret_cast<const uint4 *>(xs + (x_at[n] ^ (uint32_t(b) << 6)));
+                            const uint4 x = *reinterpret_cast<const uint4 *>(xs + x_at[n][b & 1] + (b >> 1) * 128);
                             if constexpr (NV && !BF16) {
                                 mma16816(acc[n], va[0], vb[0], va[1], vb[1], x.x, x.y, acc[n]);
                                 mma16816(acc[n], va[2], vb[2], va[3], vb[3], x.z, x.w, acc[n]);
