@@ -12,7 +12,11 @@
  *   gemm_s4   packed INT4 operands, INT32 accumulation, INT32 result
  *             (section IV-C, Listings 1-2: mma ... .s32.s4.s4.s32)
  *
- * All three compute C <- A.B exactly as the plain sum over k, with C
+ * and, beside the study, the 4-bit floating-point operators that language models
+ * train and decode with: gemm_fp4, gemm_a16_fp4, ptc_quantize_fp4,
+ * ptc_dequantize_fp4 and ptc_dropout (see "Microscaled 4-bit matrices" below).
+ *
+ * The first three compute C <- A.B exactly as the plain sum over k, with C
  * overwritten and no scaling, bias or dequantisation (section VI "Scope":
  * INT32 accumulations without in-kernel dequantization or scaling).  The
  * paper's problems are square (section III-B, N = 512 ... 8192); general

@@ -11,6 +11,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "ptc.h"
@@ -145,7 +146,8 @@ Matrix matrix(PyObject *codes, PyObject *scales, PyObject *k, PyObject *fmt, PyO
     m.k = integer(k);
     m.codes = r.p;
     m.rows = r.rows;
-    m.pitch = r.rows > 1 ? r.ld : std::max<int64_t>(16, (r.cols + 15) / 16 * 16);
+    // (One row, or rows of no values, have no pitch.)
+    m.pitch = r.rows > 1 && m.k > 0 ? r.ld : std::max<int64_t>(16, (r.cols + 15) / 16 * 16);
     if (m.k < 0 || r.cols < (m.k + 31) / 32 * 16 || m.pitch % 16)
         raise(PyExc_ValueError, "codes must hold 16 * ceil(K / 32) bytes per row, rows a multiple of 16 bytes apart");
     if (!s.is_cuda() || !s.is_contiguous() || s.numel() < scale_bytes(m.rows, m.k, m.fmt))

@@ -464,6 +464,50 @@ def test_few_tokens_placements_and_values_that_are_not_finite(fmt):
     assert ptc.matmul_a16_fp4(x[:0], W).shape == (0, 100)
 
 
+# ------------------------------------------------------------------ refusals of the tensor layer
+def test_tensor_layer_refusals_on_the_device():
+    A, _ = matrix(5, 64, "mxfp4", 1)
+    B, _ = matrix(9, 64, "mxfp4", 2)
+    x = torch.zeros(5, 64, dtype=torch.bfloat16, device=DEV)
+    one = torch.ones(1, device=DEV)
+    wide = torch.zeros(5, 64, 2, dtype=torch.bfloat16, device=DEV)
+    for bad in (lambda: ptc.matmul_fp4(A, matrix(9, 96, "mxfp4", 2)[0]),           # inner sizes
+                lambda: ptc.matmul_fp4(A, matrix(9, 64, "nvfp4", 2)[0]),           # formats
+                lambda: ptc.matmul_fp4(A, B, out=torch.zeros(5, 8, device=DEV)),   # out's shape
+                lambda: ptc.matmul_fp4(A, B, out=torch.zeros(5, 9)),               # out on the host
+                lambda: ptc.matmul_a16_fp4(x[:, :32], B),
+                lambda: ptc.matmul_a16_fp4(wide[..., 0], B),                       # column stride 2
+                lambda: ptc.matmul_a16_fp4(x, B, out=torch.zeros(5, 9, device=DEV)),
+                lambda: ptc.dropout(x, 0.1, 1, residual=x[:4]),
+                lambda: ptc.dropout(x, 0.1, 1, out=torch.zeros(5, 64, device=DEV)),
+                lambda: ptc.dropout(x[:1].expand(5, 64), 0.1, 1),                  # rows that overlap
+                lambda: ptc.dropout(x.view(-1), 0.1, 1),
+                lambda: ptc.quantize_fp4(x, "fp4"),
+                lambda: ptc.quantize_fp4(x, tensor_scale=one),                     # mxfp4 has none
+                lambda: ptc.quantize_fp4(x, "nvfp4", tensor_scale=torch.ones(1)),
+                lambda: ptc.quantize_fp4(x, "nvfp4", tensor_scale=one.double()),
+                lambda: ptc.dequantize_fp4(A, out=torch.zeros(5, 63, device=DEV)),
+                lambda: ptc.Fp4Matrix(A.codes, A.scales[:-1], 64),
+                lambda: ptc.Fp4Matrix(A.codes[:, :16], A.scales, 64),
+                lambda: ptc.Fp4Matrix(A.codes, A.scales, -1),
+                lambda: ptc.Fp4Matrix(torch.zeros(5, 40, dtype=torch.uint8, device=DEV), A.scales, 64)):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: ptc.matmul_fp4(A, x), lambda: ptc.matmul_fp4(A, B, out_dtype=torch.float64),
+                lambda: ptc.matmul_a16_fp4(x.float(), B), lambda: ptc.quantize_fp4(x.int()), lambda: ptc.dropout(3, 0.1, 1),
+                lambda: ptc.Fp4Matrix(A.codes.int(), A.scales, 64), lambda: ptc.matmul_fp4(A, B, out_dtype="bf16")):
+        with pytest.raises(TypeError):
+            bad()
+    for bad in (lambda: ptc.dropout(x, 1.5, 1), lambda: ptc.dropout(x, 0.1, 1, offset=-1),
+                lambda: ptc.dropout(x[:, :60], 0.1, 1, out=x[:, 4:])):
+        with pytest.raises(ptc.PtcError):
+            bad()
+    none = ptc.quantize_fp4(x[:, :0])
+    assert none.shape == (5, 0) and not ptc.matmul_fp4(none, ptc.quantize_fp4(x[:3, :0])).any()
+    assert not ptc.matmul_a16_fp4(x[:, :0], none).any() and ptc.dequantize_fp4(none).shape == (5, 0)
+    assert ptc.gemm_poll_device_error() == ptc.PTC_OK
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("tokens,inputs,outputs,p", [(1, 32, 16, 0.0), (65, 200, 130, 0.25), (256, 512, 384, 0.1)])
 def test_linear_step(tokens, inputs, outputs, p):
