@@ -221,38 +221,37 @@ __device__ __forceinline__ uint32_t codes_nearest(const float (&v)[8]) {
 }
 
 // One value rounded down or up to the neighbouring codes, up when its
-// remainder (in 1/65536 of the gap) plus r reaches 65536; the code in bits 16 ..
-// 19 of the result, other bits undefined.  With e the exponent of max(u, 1),
-// u = |v| at most 6, the gap is 2^(e - 1) and the range starts at code 2 e.  The
-// distance from 0 in 1/65536 of the gap, u 2^(17 - e), is rounded down to a
-// whole number T by an addition of 2^23 that rounds down; from there code
-// 2 e is 2 e (65536) further than in a uniform grid: (T + 2 e 65536 + r) / 65536
-// rounded down is the code.  `r2` is r + 2 * 65536, which makes up for the bias
-// 127 of the exponent field (2 * 127 = -2 modulo 8); the sum's higher bits, of
-// 2^23 and of the field, stay clear of bits 16 .. 18.
-__device__ __forceinline__ uint32_t code_stochastic(float v, uint32_t r2) {
+// remainder (in 1/65536 of the gap) plus r reaches 65536; the code in bits 22 ..
+// 25 of the result, the others zero.  From 1 up the codes are floats of one
+// mantissa bit, so bits 22 .. 24 of |v| are the code rounded down (plus a
+// constant) and the 22 bits below are the remainder: adding r << 6 carries
+// exactly where the code goes up.  Below 1 the grid is uniform with the gap of
+// [1, 2): (|v| + 1) / 2, the larger of the two only there, lies one binade lower,
+// which makes its first code 0; rounded down it keeps all 16 bits of the
+// remainder that count.  `r4` is r + 4 * 65536, which makes up for the exponent's
+// bias (2 * 126 = -4 modulo 8).
+__device__ __forceinline__ uint32_t code_stochastic(float v, uint32_t r4) {
     const float u = fminf(fabsf(v), 6.0f);
-    const uint32_t m = max(__float_as_uint(u), 0x3F800000u) & 0x7F800000u;  // e + 127 in the exponent field
-    const float t = __fmaf_rd(u, __uint_as_float(0x87800000u - m), 8388608.0f);
-    const uint32_t code = __float_as_uint(t) + (m >> 6) + r2;
-    return (code & 0x70000u) | ((__float_as_uint(v) >> 12) & 0x80000u);
+    const float w = fmaxf(u, __fmaf_rd(u, 0.5f, 0.5f));
+    const uint32_t code = __float_as_uint(w) + 64u * r4;
+    return (code & 0x01C00000u) | ((__float_as_uint(v) >> 6) & 0x02000000u);
 }
 
 // Eight codes of code_stochastic, value j in bits 4 j .. 4 j + 3 of the result.
 __device__ __forceinline__ uint32_t pack_stochastic(const uint32_t (&c)[8]) {
-    uint32_t p[4];  // two codes in bits 16 .. 23
+    uint32_t p[4];  // two codes in bits 22 .. 29
 #pragma unroll
     for (int i = 0; i < 4; ++i) p[i] = c[2 * i] + 16u * c[2 * i + 1];
-    return __byte_perm(__byte_perm(p[0], p[1], 0x0062), __byte_perm(p[2], p[3], 0x0062), 0x5410);
+    return (p[0] >> 22) | (p[1] >> 14) | (p[2] >> 6) | (p[3] << 2);
 }
 
-// r + 2 * 65536 of element j of eight (bits as random_bits8 gives them), and of
+// r + 4 * 65536 of element j of eight (bits as random_bits8 gives them), and of
 // the low and high half of a word.
-__device__ __forceinline__ uint32_t low_r2(uint32_t w) { return __byte_perm(w, 2u, 0x5410); }
-__device__ __forceinline__ uint32_t high_r2(uint32_t w) { return __byte_perm(w, 2u, 0x5432); }
-__device__ __forceinline__ uint32_t bits_r2(const uint4 &w, int j) {
+__device__ __forceinline__ uint32_t low_r4(uint32_t w) { return __byte_perm(w, 4u, 0x5410); }
+__device__ __forceinline__ uint32_t high_r4(uint32_t w) { return __byte_perm(w, 4u, 0x5432); }
+__device__ __forceinline__ uint32_t bits_r4(const uint4 &w, int j) {
     const uint32_t x = (j >> 1) == 0 ? w.x : (j >> 1) == 1 ? w.y : (j >> 1) == 2 ? w.z : w.w;
-    return (j & 1) ? high_r2(x) : low_r2(x);
+    return (j & 1) ? high_r4(x) : low_r4(x);
 }
 
 // Eight codes (a 32-bit word) as eight binary16 values, exactly: word i of the

@@ -143,7 +143,7 @@ __device__ __forceinline__ uint32_t codes8(const float (&v)[8], uint32_t amax, c
     if constexpr (SR) {
         uint32_t c[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) c[j] = code_stochastic(scale.apply(v[j]), bits_r2(bits, j));
+        for (int j = 0; j < 8; ++j) c[j] = code_stochastic(scale.apply(v[j]), bits_r4(bits, j));
         q = pack_stochastic(c);
     } else {
         float s[8];
@@ -377,8 +377,8 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const T *x, const Qu
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint32_t r = *reinterpret_cast<const uint32_t *>(rs + (16 * warp + 8 * w + j) * kTileC + 2 * lane);
-                ca[j] = code_stochastic(sa.apply(va[8 * w + j]), low_r2(r));
-                cb[j] = code_stochastic(sb.apply(vb[8 * w + j]), high_r2(r));
+                ca[j] = code_stochastic(sa.apply(va[8 * w + j]), low_r4(r));
+                cb[j] = code_stochastic(sb.apply(vb[8 * w + j]), high_r4(r));
             }
             qa[w] = pack_stochastic(ca);
             qb[w] = pack_stochastic(cb);
