@@ -93,7 +93,8 @@ def quantize(x, fmt, rounding="nearest", bits=None, g=None):
     else:
         gs = np.float32(1 if g is None else g)
         six = np.float32(gs * np.float32(6))
-        byte = e4m3_nearest((a / six).astype(np.float32))
+        with np.errstate(over="ignore"):
+            byte = e4m3_nearest((a / six).astype(np.float32))
         if rounding == "stochastic":
             byte = np.where((six * E4M3[byte].astype(np.float32) < a) & (byte < 0x7E), byte + 1, byte)
         d = E4M3[byte].astype(np.float32) * gs

@@ -464,6 +464,66 @@ def test_few_tokens_placements_and_values_that_are_not_finite(fmt):
     assert ptc.matmul_a16_fp4(x[:0], W).shape == (0, 100)
 
 
+# ------------------------------------------------------------------ random sizes
+@pytest.mark.parametrize("seed", range(24))
+def test_random_sizes(seed):
+    """Sizes spread over their logarithm, every format and type, by the shapes that the library chooses."""
+    rng = np.random.default_rng(100 + seed)
+
+    def size(lo, hi):
+        return int(np.exp(rng.uniform(np.log(lo), np.log(hi + 1))))
+
+    fmt = ("mxfp4", "nvfp4")[seed % 2]
+    dt = list(DT.values())[seed % 3]
+    M, N, K = size(1, 900), size(1, 1500), size(1, 3000)
+    A, a = matrix(M, K, fmt, seed)
+    B, b = matrix(N, K, fmt, seed + 1, g=0.7 if fmt == "nvfp4" else None)
+    check_product(ptc.matmul_fp4(A, B, out_dtype=dt), a, b, K)
+    x = normal(size(1, 20), K, seed, (torch.bfloat16, torch.float16)[seed % 4 // 2], 0.5)
+    check_product(ptc.matmul_a16_fp4(x, B), host(x), b, K)
+    rows, cols = size(1, 600), size(1, 600)
+    x = normal(rows, cols, seed, dt)
+    bits = ref.bits16(rows, cols, seed, 8, 1)
+    xd = ref.dropout(f32(x), 0.15, seed, 8)
+    q, t = ptc.quantize_fp4(x, fmt, transposed="both", rounding="stochastic", p=0.15, seed=seed, offset=8)
+    check_quantised(q, xd, fmt, "stochastic", bits, None)
+    check_quantised(t, np.ascontiguousarray(xd.T), fmt, "stochastic", bits.T, None)
+
+
+# ------------------------------------------------------------------ offsets past 32 bits
+def test_rows_further_apart_than_32_bits_reach():
+    """Row pitches that put the last rows more than 2^32 bytes from the first."""
+    rows, K = 66000, 64
+    A, a = matrix(rows, K, "mxfp4", 1)
+    B, b = matrix(48, K, "mxfp4", 2)
+    big = torch.empty(rows, 65536 + 64, dtype=torch.uint8, device=DEV)
+    codes = big[:, 64:64 + A.codes.shape[1]]
+    codes.copy_(A.codes)
+    assert codes.stride(0) * (rows - 1) > 2 ** 32
+    W = ptc.Fp4Matrix(codes, A.scales, K)
+    last = slice(rows - 300, rows)
+    out = torch.empty(rows, 32768 + 8, dtype=torch.bfloat16, device=DEV)[:, :48]
+    ptc.matmul_fp4(W, B, out=out)
+    check_product(out[last], a[last], b, K)
+    check_product(out[:300], a[:300], b, K)
+    x = normal(3, K, 3, torch.float16, 0.1)
+    check_product(ptc.matmul_a16_fp4(x, W)[:, last], host(x), a[last], K)
+    v = torch.empty(rows, 32768 + 8, dtype=torch.bfloat16, device=DEV)[:, 3:3 + K]
+    ptc.dequantize_fp4(W, out=v)
+    assert same(host(v[last]), a[last])
+    for q in (ptc.quantize_fp4(v), ptc.quantize_fp4(v, transposed="both")[0]):
+        check_quantised(ptc.Fp4Matrix(q.codes[-208:], ptc.Fp4Matrix.tile_scales(q.row_scales()[-208:]), K), f32(v[-208:]),
+                        "mxfp4", "nearest", None, None)
+    qt = ptc.quantize_fp4(v, transposed=True)
+    codes_t, byte_t = ref.quantize(np.ascontiguousarray(f32(v[-208:]).T), "mxfp4")  # 66000 - 208 is a whole block
+    assert (rows - 208) % 32 == 0
+    got = ref.unpack(qt.codes.cpu().numpy())[:, rows - 208:rows]
+    assert np.array_equal(np.where(got == 8, 0, got), np.where(codes_t == 8, 0, codes_t)[:, :208])
+    y = ptc.dropout(v, 0.5, 4, 5, out=torch.empty(rows, 32768 + 8, dtype=torch.bfloat16, device=DEV)[:, :K])
+    keep = ref.bits16(rows, K, 4, 5, 0)[last] < 32768
+    assert same(host(y[last]), np.where(keep, 2 * host(v[last]), 0.0))
+
+
 # ------------------------------------------------------------------ refusals of the tensor layer
 def test_tensor_layer_refusals_on_the_device():
     A, _ = matrix(5, 64, "mxfp4", 1)
