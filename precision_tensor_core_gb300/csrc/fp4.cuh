@@ -12,6 +12,7 @@
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <type_traits>
 
 namespace ptc {
 
@@ -106,6 +107,30 @@ struct Pack8 {
     __device__ __forceinline__ T get(int j) const { return reinterpret_cast<const T *>(v)[j]; }
     __device__ __forceinline__ void set(int j, T x) { reinterpret_cast<T *>(v)[j] = x; }
 };
+
+// Eight FP32 values rounded to the element type, two per conversion.
+template <typename T>
+__device__ __forceinline__ Pack8<T> round8(const float (&v)[8]) {
+    Pack8<T> r;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r.set(j, v[j]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (std::is_same_v<T, __half>) {
+                const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+                w[i] = reinterpret_cast<const uint32_t &>(h);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                w[i] = reinterpret_cast<const uint32_t &>(h);
+            }
+        }
+        r.v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return r;
+}
 
 // `n` (1 .. 8) elements at p; the others +0.  `vec`: p is 16-byte aligned.
 template <typename T>

@@ -61,7 +61,8 @@ __global__ void __launch_bounds__(256) dropout_kernel(const T *x, int64_t ldx, c
         const int64_t c = int64_t(w.group) * 8;
         const int n = int(min(int64_t(8), cols - c));
         const Pack8<T> a = load8(x + w.row * ldx + c, n, true);
-        Pack8<T> r, o;
+        Pack8<T> r;
+        float o[8];
         if constexpr (RES) r = load8(res + w.row * ldr + c, n, true);
         const uint4 bits = random_bits8(d.rng, kRngDropout, uint32_t(w.row), w.group);
 #pragma unroll
@@ -69,9 +70,9 @@ __global__ void __launch_bounds__(256) dropout_kernel(const T *x, int64_t ldx, c
             // Selected, not multiplied by zero: a dropped infinity or NaN leaves +0.
             float v = bits16(bits, j) < d.kept ? __fmul_rn(to_float(a.get(j)), d.scale) : 0.0f;
             if constexpr (RES) v = __fadd_rn(v, to_float(r.get(j)));
-            o.set(j, from_float<T>(v));
+            o[j] = v;
         }
-        store8(y + w.row * ldy + c, o, n, true);
+        store8(y + w.row * ldy + c, round8<T>(o), n, true);
     }
 }
 
@@ -501,15 +502,18 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *codes, i
             const float s = scale_value<NV>(b[u]);
             uint32_t h[4];
             codes_to_f16(q[u], h);
-            Pack8<T> o;
+            float v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float f =
-                    __half2float(__ushort_as_half(uint16_t((j & 1) ? h[j >> 1] >> 16 : h[j >> 1] & 0xFFFFu)));
-                float v = __fmul_rn(f, s);
-                if (has_g) v = __fmul_rn(v, g);
-                o.set(j, from_float<T>(v));
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = __half22float2(reinterpret_cast<const __half2 &>(h[i]));
+                v[2 * i] = __fmul_rn(f.x, s);
+                v[2 * i + 1] = __fmul_rn(f.y, s);
+                if (has_g) {
+                    v[2 * i] = __fmul_rn(v[2 * i], g);
+                    v[2 * i + 1] = __fmul_rn(v[2 * i + 1], g);
+                }
             }
+            const Pack8<T> o = round8<T>(v);
             if (vec != 0) {
                 if (c < cols) store8(y + w.row * ldy + c, o, int(min(int64_t(8), cols - c)), true);
             } else {
