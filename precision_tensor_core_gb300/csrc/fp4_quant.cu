@@ -47,9 +47,10 @@ struct DropArgs {
 
 // ------------------------------------------------------------ dropout
 // y = [r < kept] x * (65536 / kept) (+ residual), eight elements of a row per
-// step: 2 to 3 times 16 bytes of traffic and one generator call (ten rounds,
-// about 70 integer instructions, under the ~170 that eight 16-bit elements'
-// traffic leaves time for).
+// step: 2 to 3 times 16 bytes of traffic and one generator call, whose twenty
+// wide products (a quarter of the integer rate each) come close to the traffic's
+// time.  8192 x 8192 bfloat16: 60.6 us with a residual (6.6 TB/s, the copy
+// rate), 50.4 us without (5.3 TB/s, bound by the random numbers).
 template <typename T, bool RES>
 __global__ void __launch_bounds__(256) dropout_kernel(const T *x, int64_t ldx, const T *res, int64_t ldr, T *y,
                                                       int64_t ldy, int64_t rows, int64_t cols, DropArgs d) {
@@ -80,7 +81,8 @@ __global__ void __launch_bounds__(256) dropout_kernel(const T *x, int64_t ldx, c
 // row, each lane makes the eight keep bits of its group, and loads and stores
 // take 32 consecutive elements at a time, whose bits come from the lane that
 // made them.  (Eight elements per lane, one store each, touched every sector
-// eight times: 2047 x 1003 binary16 took 7.5 us.)
+// eight times: 2047 x 1003 binary16 took 7.5 us, and takes 3.9; 8191 x 8191
+// float32 84 us, 6.4 TB/s.)
 template <typename T, bool RES>
 __global__ void __launch_bounds__(256) dropout_ragged_kernel(const T *x, int64_t ldx, const T *res, int64_t ldr, T *y,
                                                              int64_t ldy, int64_t rows, int64_t cols, DropArgs d) {
@@ -199,7 +201,10 @@ __device__ __forceinline__ uint32_t codes8(const float (&v)[8], uint32_t amax, c
 // them, all loads before the first use: the block's maximum by one or two
 // shuffles, codes as 4 bytes per lane (128 contiguous bytes per warp), scales
 // gathered to one 4-byte store per tile.  Rows past the last one to the end of
-// the scale tile get zero scales.
+// the scale tile get zero scales.  8192 x 8192 bfloat16: 28.3 us to mxfp4 (6.0
+// TB/s, 90% of the copy rate) and 38.9 to nvfp4 to nearest, where the block's
+// division shows; 66 and 76 us stochastically, where the random numbers and the
+// rounding fill the integer pipe.
 template <typename T, bool NV, bool SR, bool DROP, int U>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *x, const QuantArgs a) {
     griddep_wait();
@@ -284,7 +289,11 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *x, const Qu
 // in, eight lanes per row.  For the columns a lane takes two adjacent columns
 // and a warp 16 rows: a block of nvfp4, half of one of mxfp4, whose maximum two
 // warps share.  Codes and scale bytes go through shared memory so that a
-// column's 64 bytes are written together.
+// column's 64 bytes are written together.  8192 x 8192 bfloat16 to mxfp4 both
+// ways: 53 us to nearest (30.6 us of traffic), 111 us stochastically, the
+// integer pipe at 83%.  (128 x 128 tiles of one column per thread took 33 us
+// for 2047 x 1003 both ways, these take 10: four times the CTAs.  Five or six
+// CTAs per SM instead of four made no difference.)
 constexpr int kTileR = 128, kTileC = 64;
 constexpr int kCodePitch = 80;  // of a column's 64 code bytes in shared memory
 
@@ -467,7 +476,8 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const T *x, const Qu
 // ------------------------------------------------------------ back to values
 // value = code x scale (x matrix scale), each product in FP32, rounded once
 // more to the output type.  A warp takes U x 256 columns of a row, a lane U
-// times eight of them, all loads before the first use.
+// times eight of them, all loads before the first use.  8192 x 8192 mxfp4 to
+// bfloat16: 31.0 us, 5.5 TB/s, bound by the writes.
 template <typename T, bool NV, int U>
 __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *codes, int64_t pitch, const uint8_t *scales,
                                                          const float *gp, int64_t rows, int64_t cols, T *y,

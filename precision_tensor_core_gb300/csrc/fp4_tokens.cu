@@ -37,6 +37,10 @@
 // The partial sums of the S shares are added in order in shared memory; where
 // that leaves SMs idle K is also shared by a cluster of up to eight CTAs, whose
 // sums are added in rank order through distributed shared memory.
+//
+// Rates (weights from HBM): one token 6.1 us with 4096 x 4096 mxfp4 weights and
+// 20 us with 16384 x 8192 (3.5 TB/s); 16 binary16 tokens 28 us with 16384 x 8192
+// nvfp4 (2.7 TB/s, bound by the instructions per weight), 16 bfloat16 tokens 42.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
