@@ -455,14 +455,18 @@ constexpr int kBufBytes = 28 * 1024;  // one buffer of activations (two per CTA,
 static_assert(16 * (kPieceBytes + 32) <= kBufBytes, "sixteen tokens fit with R = 8");
 
 // Row groups per CTA (log2) and CTAs per cluster of least estimated time, in
-// units of 0.01 us.  A wave of two CTAs per SM starts in 3.3 us, with a
-// cluster's barriers in 4.3; a stage takes 0.6 us plus 0.02 per token (0.05 for
-// bfloat16) where a CTA has its SM to itself and 1.6 times that where two share
-// one; a chunk of activations 0.6 us.  (Fitted to every shape at 11 sizes
-// between 512 x 512 and 16384 x 8192 weights with 1 to 16 tokens, of which it
-// takes the fastest or one close to it.)
-void choose_tokens(int64_t N, int groups, int toks, int token_bytes, bool bf16, int64_t chunks, int sms, int *r_log2,
-                   int *ks) {
+// units of 0.01 us.  A wave of two CTAs per SM starts in 2.2 us, 3.2 with clusters
+// of two, 3.6 and 0.02 per cluster of four, 5.5 and 0.11 per cluster of eight (few
+// of those fit a GPC).  A stage takes 0.54 us for eight tokens (bfloat16 0.6) and
+// 0.92 for sixteen, 1.8 times that where two CTAs share an SM, and 0.8 us more
+// where it is a whole chunk of the activations.  Their reading takes 0.02 us per KB
+// (bfloat16, which is converted, 0.1), 3.5 times that where rows are not aligned.
+// (Fitted to the times of every shape at 25 sizes between 128 x 8000 and 16384 x
+// 8192 weights with 1 to 16 tokens.  Its choice takes 1.02 times the fastest
+// shape's time there and at 15 other sizes, 1.13 at most.)
+void choose_tokens(int64_t N, int64_t K, int groups, int toks, int token_bytes, bool bf16, bool xvec, int64_t chunks,
+                   int sms, int *r_log2, int *ks) {
+    const int64_t per_stage = toks > 8 ? 92 : bf16 ? 60 : 54;
     int64_t best = INT64_MAX;
     for (int r = 3; r >= 0; --r) {
         const int S = 8 >> r, most = kBufBytes / (S * token_bytes);  // stages of a chunk
@@ -470,10 +474,12 @@ void choose_tokens(int64_t N, int groups, int toks, int token_bytes, bool bf16, 
         for (int k = 1; k <= 8; k *= 2) {
             if (groups < S * k && (r < 3 || k > 1)) continue;
             const int64_t ctas = (N + 127) / 128 * S * k * chunks;
-            const int64_t waves = (ctas + 2 * sms - 1) / (2 * sms);
+            const int64_t waves = (ctas + 2 * sms - 1) / (2 * sms), clusters = ctas / k / waves;
             const int64_t stages = (groups + S * k - 1) / (S * k);
-            const int64_t stage = (60 + (bf16 ? 5 : 2) * toks) * (ctas > sms ? 16 : 10) / 10;
-            const int64_t cost = waves * ((k > 1 ? 430 : 330) + stages * stage + (stages + most - 1) / most * 60);
+            const int64_t start = k == 1 ? 220 : k == 2 ? 320 : k == 4 ? 360 + 2 * clusters : 550 + 11 * clusters;
+            const int64_t read = toks * K / k * 2 * (bf16 ? 10 : 2) * (xvec ? 2 : 7) / 2048;
+            const int64_t cost = waves * (start + stages * per_stage * (ctas > sms ? 18 : 10) / 10 +
+                                          (most == 1 ? stages * 80 : 0) + read);
             if (cost < best) {
                 best = cost;
                 *r_log2 = r;
@@ -501,7 +507,7 @@ int launch_tokens(TokArgs a, const void *codes, int64_t pitch, const void *scale
     const int toks = std::min(a.M, TOK);
     // Bytes of a stage's activations and powers of two.
     const int token_bytes = toks * kPieceBytes + (BF16 ? 8 * TOK * 4 : 0);
-    choose_tokens(a.N, a.groups, toks, token_bytes, BF16, chunks, sms, &a.r_log2, &a.ks);
+    choose_tokens(a.N, a.K, a.groups, toks, token_bytes, BF16, a.xvec != 0, chunks, sms, &a.r_log2, &a.ks);
     const int ks = a.ks, S = kWarps >> a.r_log2;
     const int per = ((a.groups + ks - 1) / ks + S - 1) / S;         // stages of the longest share
     const int most = kBufBytes / (S * token_bytes);                // of a buffer
