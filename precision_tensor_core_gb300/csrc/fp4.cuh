@@ -195,6 +195,14 @@ struct BlockScale {
         // (Far above the largest code, where the remainder could overflow, q saturates as it is.)
         return fabsf(q) < 16.0f ? __fmaf_rn(__fmaf_rn(-q, d, x), inverse, q) : q;
     }
+    // The smaller of |x| / scale and 6 for stochastic rounding.  mxfp4's scale
+    // is then at least a sixth of the block's largest magnitude.  (nvfp4: a quotient
+    // so large that its remainder is NaN is 6 too.)
+    __device__ __forceinline__ float magnitude(float x) const {
+        const float q = __fmul_rn(NV ? x : fabsf(x), inverse);
+        if constexpr (!NV) return q;
+        return fminf(fabsf(__fmaf_rn(__fmaf_rn(-q, d, x), inverse, q)), 6.0f);
+    }
 };
 
 // Scale byte and scale of a block whose largest magnitude has the
@@ -245,38 +253,44 @@ __device__ __forceinline__ uint32_t codes_nearest(const float (&v)[8]) {
     return q;
 }
 
-// One value rounded down or up to the neighbouring codes, up when its
-// remainder (in 1/65536 of the gap) plus r reaches 65536; the code in bits 22 ..
-// 25 of the result, the others zero.  From 1 up the codes are floats of one
-// mantissa bit, so bits 22 .. 24 of |v| are the code rounded down (plus a
-// constant) and the 22 bits below are the remainder: adding r << 6 carries
-// exactly where the code goes up.  Below 1 the grid is uniform with the gap of
-// [1, 2): (|v| + 1) / 2, the larger of the two only there, lies one binade lower,
-// which makes its first code 0; rounded down it keeps all 16 bits of the
-// remainder that count.  `r4` is r + 4 * 65536, which makes up for the exponent's
-// bias (2 * 126 = -4 modulo 8).
-__device__ __forceinline__ uint32_t code_stochastic(float v, uint32_t r4) {
-    const float u = fminf(fabsf(v), 6.0f);
-    const float w = fmaxf(u, __fmaf_rd(u, 0.5f, 0.5f));
-    const uint32_t code = __float_as_uint(w) + 64u * r4;
-    return (code & 0x01C00000u) | ((__float_as_uint(v) >> 6) & 0x02000000u);
+// The magnitude u (at most 6) of a scaled value rounded down or up to the
+// neighbouring codes, up when its remainder (in 1/65536 of the gap) plus r
+// reaches 65536; the code in bits 24 .. 26 of the result, x's sign in bit 31, the
+// other bits of that byte zero.  From 1 up the codes are floats of one mantissa
+// bit, so bits 22 .. 24 of u are the code rounded down (plus a constant) and the 22
+// bits below are the remainder: adding r << 6 carries exactly where the code goes
+// up.  Below 1 the grid is uniform with the gap of [1, 2): (u + 1) / 2 lies one
+// binade lower, which makes its first code 0.  It is made as u + (1 - u) / 2, whose
+// second term saturates at 0 from 1 up, and rounded down keeps all 16 bits of the
+// remainder that count: the second term is rounded by at most 2^-26, and to the
+// nearest, so that the sum passes a multiple of 2^-18 only where the exact one
+// does.  `r8` is (r + 4 * 65536) * 256; the 4 makes up for the exponent's bias
+// (2 * 126 = -4 modulo 8) and the product by 4 takes the constant out at the top.
+// (All but the last step run beside the integer pipe, which bounds the kernels that
+// round stochastically.)
+__device__ __forceinline__ uint32_t code_stochastic(float u, float x, uint32_t r8) {
+    const float w = __fadd_rd(u, __saturatef(__fmaf_rn(u, -0.5f, 0.5f)));
+    const uint32_t code = 4u * __float_as_uint(w) + r8;
+    return (code & 0x7FFFFFFFu) | (__float_as_uint(x) & 0x80000000u);
 }
 
 // Eight codes of code_stochastic, value j in bits 4 j .. 4 j + 3 of the result.
 __device__ __forceinline__ uint32_t pack_stochastic(const uint32_t (&c)[8]) {
-    uint32_t p[4];  // two codes in bits 22 .. 29
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = c[2 * i] + 16u * c[2 * i + 1];
-    return (p[0] >> 22) | (p[1] >> 14) | (p[2] >> 6) | (p[3] << 2);
+    // Top bytes (sign in bit 7, code in bits 0 .. 2) of the even and the odd values.
+    const uint32_t e = __byte_perm(__byte_perm(c[0], c[2], 0x0073), __byte_perm(c[4], c[6], 0x0073), 0x5410);
+    const uint32_t o = __byte_perm(__byte_perm(c[1], c[3], 0x0073), __byte_perm(c[5], c[7], 0x0073), 0x5410);
+    const uint32_t low = (e & 0x07070707u) | ((e >> 4) & ~0x07070707u);   // of each byte
+    const uint32_t high = (o & 0x80808080u) | ((16u * o) & ~0x80808080u);
+    return (low & 0x0F0F0F0Fu) | (high & 0xF0F0F0F0u);
 }
 
-// r + 4 * 65536 of element j of eight (bits as random_bits8 gives them), and of
-// the low and high half of a word.
-__device__ __forceinline__ uint32_t low_r4(uint32_t w) { return __byte_perm(w, 4u, 0x5410); }
-__device__ __forceinline__ uint32_t high_r4(uint32_t w) { return __byte_perm(w, 4u, 0x5432); }
-__device__ __forceinline__ uint32_t bits_r4(const uint4 &w, int j) {
+// (r + 4 * 65536) * 256 of element j of eight (bits as random_bits8 gives them),
+// and of the low and high half of a word.
+__device__ __forceinline__ uint32_t low_r8(uint32_t w) { return __byte_perm(w, 4u, 0x4105); }
+__device__ __forceinline__ uint32_t high_r8(uint32_t w) { return __byte_perm(w, 4u, 0x4325); }
+__device__ __forceinline__ uint32_t bits_r8(const uint4 &w, int j) {
     const uint32_t x = (j >> 1) == 0 ? w.x : (j >> 1) == 1 ? w.y : (j >> 1) == 2 ? w.z : w.w;
-    return (j & 1) ? high_r4(x) : low_r4(x);
+    return (j & 1) ? high_r8(x) : low_r8(x);
 }
 
 // Eight codes (a 32-bit word) as eight binary16 values, exactly: word i of the

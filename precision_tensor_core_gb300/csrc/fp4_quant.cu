@@ -186,7 +186,7 @@ __device__ __forceinline__ uint32_t codes8(const float (&v)[8], uint32_t amax, c
     if constexpr (SR) {
         uint32_t c[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) c[j] = code_stochastic(scale.apply(v[j]), bits_r4(bits, j));
+        for (int j = 0; j < 8; ++j) c[j] = code_stochastic(scale.magnitude(v[j]), v[j], bits_r8(bits, j));
         q = pack_stochastic(c);
     } else {
         float s[8];
@@ -427,8 +427,8 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const T *x, const Qu
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint32_t r = *reinterpret_cast<const uint32_t *>(rs + (16 * warp + 8 * w + j) * kTileC + 2 * lane);
-                ca[j] = code_stochastic(sa.apply(va[8 * w + j]), low_r4(r));
-                cb[j] = code_stochastic(sb.apply(vb[8 * w + j]), high_r4(r));
+                ca[j] = code_stochastic(sa.magnitude(va[8 * w + j]), va[8 * w + j], low_r8(r));
+                cb[j] = code_stochastic(sb.magnitude(vb[8 * w + j]), vb[8 * w + j], high_r8(r));
             }
             qa[w] = pack_stochastic(ca);
             qb[w] = pack_stochastic(cb);
