@@ -269,7 +269,9 @@ __device__ __forceinline__ uint32_t codes_nearest(const float (&v)[8]) {
 // (All but the last step run beside the integer pipe, which bounds the kernels that
 // round stochastically.)
 __device__ __forceinline__ uint32_t code_stochastic(float u, float x, uint32_t r8) {
-    const float w = __fadd_rd(u, __saturatef(__fmaf_rn(u, -0.5f, 0.5f)));
+    float half_gap;  // (1 - u) / 2, or 0
+    asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(half_gap) : "f"(u), "f"(-0.5f), "f"(0.5f));
+    const float w = __fadd_rd(u, half_gap);
     const uint32_t code = 4u * __float_as_uint(w) + r8;
     return (code & 0x7FFFFFFFu) | (__float_as_uint(x) & 0x80000000u);
 }

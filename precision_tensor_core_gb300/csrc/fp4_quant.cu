@@ -319,29 +319,41 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const T *x, const Qu
     const int64_t r0 = blockIdx.x / tiles_c * kTileR, c0 = (blockIdx.x % tiles_c) * kTileC;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    {
-        const int grp = threadIdx.x & 7;
-        const int64_t c = c0 + grp * 8;
+    // Whole: all rows and columns of the tile exist, and rows are aligned.
+    auto rows_in = [&](auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        const int grp = threadIdx.x & 7, lr0 = threadIdx.x >> 3;
+        const int rows_left = WHOLE ? kTileR : int(min(int64_t(kTileR), a.rows - r0));
+        const int n_cols = WHOLE ? 8 : int(max(int64_t(0), min(int64_t(8), a.cols - c0 - grp * 8)));
+        const T *px = x + (r0 + lr0) * a.ldx + c0 + grp * 8;
+        const int64_t x_step = 32 * a.ldx, code_step = 32 * a.pitch;
+        uint8_t *code = nullptr, *scale_at = nullptr;
+        bool code_exists = true;
+        if constexpr (ROWS) {
+            code = a.codes + (r0 + lr0) * a.pitch + (c0 + grp * 8) / 2;
+            code_exists = WHOLE || c0 + grp * 8 < (a.cols + 31) / 32 * 32;
+            scale_at = a.scales + scale_word(r0 + lr0, c0 / KW, kt_rows);  // 32 rows further: 4 bytes
+        }
+        const uint32_t row = uint32_t(r0) + lr0, group = uint32_t(c0 / 8) + grp;
         Pack8<T> p[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t r = r0 + (threadIdx.x >> 3) + 32 * i;
-            const int n = r < a.rows ? int(max(int64_t(0), min(int64_t(8), a.cols - c))) : 0;
-            p[i] = load8(x + (n > 0 ? r * a.ldx + c : 0), n, a.vec != 0);
+            const int n = WHOLE || lr0 + 32 * i < rows_left ? n_cols : 0;
+            p[i] = load8(n > 0 ? px + i * x_step : x, n, WHOLE || a.vec != 0);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int lr = (threadIdx.x >> 3) + 32 * i;
-            const int64_t r = r0 + lr;
+            const int lr = lr0 + 32 * i;
+            const bool exists = WHOLE || lr < rows_left;
             if constexpr (DROP) {
-                const uint4 bits = random_bits8(a.drop.rng, kRngDropout, uint32_t(r), uint32_t(c / 8));
+                const uint4 bits = random_bits8(a.drop.rng, kRngDropout, row + 32 * i, group);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     if (bits16(bits, j) >= a.drop.kept) p[i].set(j, from_float<T>(0.0f));
             }
             uint4 bits = make_uint4(0, 0, 0, 0);
             if constexpr (SR) {
-                bits = random_bits8(a.drop.rng, kRngRounding, uint32_t(r), uint32_t(c / 8));
+                bits = random_bits8(a.drop.rng, kRngRounding, row + 32 * i, group);
                 *reinterpret_cast<uint4 *>(rs + lr * kTileC + grp * 8) = bits;
             }
 #pragma unroll
@@ -358,12 +370,11 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const T *x, const Qu
                 uint32_t byte;
                 const BlockScale<NV> scale = block_scale<NV, SR>(m, g, byte);
                 const uint32_t q = codes8<NV, SR>(v, m, scale, bits);
-                if (r < a.rows && c < (a.cols + 31) / 32 * 32)
-                    *reinterpret_cast<uint32_t *>(a.codes + r * a.pitch + c / 2) = q;
+                if (exists && code_exists) *reinterpret_cast<uint32_t *>(code + i * code_step) = q;
                 // The row's scale bytes of these 64 columns: a word (nvfp4), or half
                 // of one; a last first half also clears the other.
-                uint32_t word = r < a.rows ? byte : 0u;
-                uint8_t *dst = a.scales + scale_word(r, c0 / KW, kt_rows);
+                uint32_t word = exists ? byte : 0u;
+                uint8_t *dst = scale_at + 4 * i;
                 if constexpr (NV) {
                     word |= __shfl_down_sync(0xFFFFFFFFu, word, 2) << 8;
                     word |= __shfl_down_sync(0xFFFFFFFFu, word, 4) << 16;
@@ -380,35 +391,37 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const T *x, const Qu
                 }
             }
         }
-    }
+    };
+    if (a.vec != 0 && r0 + kTileR <= a.rows && c0 + kTileC <= a.cols)
+        rows_in(std::integral_constant<bool, true>());
+    else
+        rows_in(std::integral_constant<bool, false>());
     __syncthreads();
 
-    float va[16], vb[16];  // columns 2 lane and 2 lane + 1, rows 16 warp ..
-    uint32_t ma = 0, mb = 0;
     struct alignas(2 * sizeof(T)) Two {
         T a, b;
     };
+    Two t[16];  // columns 2 lane and 2 lane + 1, rows 16 warp ..
+    uint32_t ma = 0, mb = 0;
     uint32_t both = 0;  // largest magnitudes of 16-bit elements, in pairs
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        const Two t = *reinterpret_cast<const Two *>(xs + (16 * warp + i) * kTileC + 2 * lane);
-        va[i] = DROP ? __fmul_rn(to_float(t.a), a.drop.scale) : to_float(t.a);
-        vb[i] = DROP ? __fmul_rn(to_float(t.b), a.drop.scale) : to_float(t.b);
+        t[i] = *reinterpret_cast<const Two *>(xs + (16 * warp + i) * kTileC + 2 * lane);
         if constexpr (sizeof(T) == 2) {
-            both = __vmaxu2(both, reinterpret_cast<const uint32_t &>(t) & 0x7FFF7FFFu);
+            both = __vmaxu2(both, reinterpret_cast<const uint32_t &>(t[i]) & 0x7FFF7FFFu);
         } else {
-            ma = max(ma, __float_as_uint(va[i]) & 0x7FFFFFFFu);
-            mb = max(mb, __float_as_uint(vb[i]) & 0x7FFFFFFFu);
+            ma = max(ma, __float_as_uint(t[i].a) & 0x7FFFFFFFu);
+            mb = max(mb, __float_as_uint(t[i].b) & 0x7FFFFFFFu);
         }
     }
     if constexpr (sizeof(T) == 2) {
-        const Two t = reinterpret_cast<const Two &>(both);
-        ma = __float_as_uint(to_float(t.a));
-        mb = __float_as_uint(to_float(t.b));
-        if constexpr (DROP) {
-            ma = scaled_bits(ma, a.drop.scale);
-            mb = scaled_bits(mb, a.drop.scale);
-        }
+        const Two top2 = reinterpret_cast<const Two &>(both);
+        ma = __float_as_uint(to_float(top2.a));
+        mb = __float_as_uint(to_float(top2.b));
+    }
+    if constexpr (DROP) {
+        ma = scaled_bits(ma, a.drop.scale);
+        mb = scaled_bits(mb, a.drop.scale);
     }
     if constexpr (!NV) {
         top[warp * kTileC + 2 * lane] = ma;
@@ -422,24 +435,34 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const T *x, const Qu
     uint32_t qa[2] = {0u, 0u}, qb[2] = {0u, 0u};
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
+        float va[8], vb[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            va[j] = to_float(t[8 * w + j].a);
+            vb[j] = to_float(t[8 * w + j].b);
+            if constexpr (DROP) {
+                va[j] = __fmul_rn(va[j], a.drop.scale);
+                vb[j] = __fmul_rn(vb[j], a.drop.scale);
+            }
+        }
         if constexpr (SR) {
             uint32_t ca[8], cb[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint32_t r = *reinterpret_cast<const uint32_t *>(rs + (16 * warp + 8 * w + j) * kTileC + 2 * lane);
-                ca[j] = code_stochastic(sa.magnitude(va[8 * w + j]), va[8 * w + j], low_r8(r));
-                cb[j] = code_stochastic(sb.magnitude(vb[8 * w + j]), vb[8 * w + j], high_r8(r));
+                ca[j] = code_stochastic(sa.magnitude(va[j]), va[j], low_r8(r));
+                cb[j] = code_stochastic(sb.magnitude(vb[j]), vb[j], high_r8(r));
             }
             qa[w] = pack_stochastic(ca);
             qb[w] = pack_stochastic(cb);
         } else {
-            float s[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s[j] = sa.apply(va[8 * w + j]);
-            qa[w] = codes_nearest(s);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s[j] = sb.apply(vb[8 * w + j]);
-            qb[w] = codes_nearest(s);
+            for (int j = 0; j < 8; ++j) {
+                va[j] = sa.apply(va[j]);
+                vb[j] = sb.apply(vb[j]);
+            }
+            qa[w] = codes_nearest(va);
+            qb[w] = codes_nearest(vb);
         }
         qa[w] = ma < kInfBits ? qa[w] : 0u;
         qb[w] = mb < kInfBits ? qb[w] : 0u;
