@@ -255,8 +255,7 @@ __device__ __forceinline__ uint32_t codes_nearest(const float (&v)[8]) {
 
 // The magnitude u (at most 6) of a scaled value rounded down or up to the
 // neighbouring codes, up when its remainder (in 1/65536 of the gap) plus r
-// reaches 65536; the code in bits 24 .. 26 of the result, x's sign in bit 31, the
-// other bits of that byte zero.  From 1 up the codes are floats of one mantissa
+// reaches 65536; the code in the top byte of the result.  From 1 up the codes are floats of one mantissa
 // bit, so bits 22 .. 24 of u are the code rounded down (plus a constant) and the 22
 // bits below are the remainder: adding r << 6 carries exactly where the code goes
 // up.  Below 1 the grid is uniform with the gap of [1, 2): (u + 1) / 2 lies one
@@ -266,24 +265,67 @@ __device__ __forceinline__ uint32_t codes_nearest(const float (&v)[8]) {
 // nearest, so that the sum passes a multiple of 2^-18 only where the exact one
 // does.  `r8` is (r + 4 * 65536) * 256; the 4 makes up for the exponent's bias
 // (2 * 126 = -4 modulo 8) and the product by 4 takes the constant out at the top.
-// (All but the last step run beside the integer pipe, which bounds the kernels that
-// round stochastically.)
-__device__ __forceinline__ uint32_t code_stochastic(float u, float x, uint32_t r8) {
+__device__ __forceinline__ uint32_t code_stochastic(float u, uint32_t r8) {
     float half_gap;  // (1 - u) / 2, or 0
     asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(half_gap) : "f"(u), "f"(-0.5f), "f"(0.5f));
     const float w = __fadd_rd(u, half_gap);
-    const uint32_t code = 4u * __float_as_uint(w) + r8;
-    return (code & 0x7FFFFFFFu) | (__float_as_uint(x) & 0x80000000u);
+    return 4u * __float_as_uint(w) + r8;
 }
 
-// Eight codes of code_stochastic, value j in bits 4 j .. 4 j + 3 of the result.
-__device__ __forceinline__ uint32_t pack_stochastic(const uint32_t (&c)[8]) {
-    // Top bytes (sign in bit 7, code in bits 0 .. 2) of the even and the odd values.
-    const uint32_t e = __byte_perm(__byte_perm(c[0], c[2], 0x0073), __byte_perm(c[4], c[6], 0x0073), 0x5410);
-    const uint32_t o = __byte_perm(__byte_perm(c[1], c[3], 0x0073), __byte_perm(c[5], c[7], 0x0073), 0x5410);
-    const uint32_t low = (e & 0x07070707u) | ((e >> 4) & ~0x07070707u);   // of each byte
-    const uint32_t high = (o & 0x80808080u) | ((16u * o) & ~0x80808080u);
-    return (low & 0x0F0F0F0Fu) | (high & 0xF0F0F0F0u);
+// Bytes picked from two words; a selector's bit 3 spreads the byte's top bit.
+template <uint32_t SELECT>
+__device__ __forceinline__ uint32_t pick_bytes(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "n"(SELECT));
+    return r;
+}
+
+// Of eight values: byte j is 0xFF where value 2 j (`even`) or 2 j + 1 is negative.
+struct Signs8 {
+    uint32_t even, odd;
+};
+
+__device__ __forceinline__ Signs8 signs8(const float (&v)[8]) {
+    uint32_t p[4];  // values 0 and 2, 1 and 3, 4 and 6, 5 and 7
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int j = (i >> 1) * 4 + (i & 1);
+        p[i] = pick_bytes<0x00FB>(__float_as_uint(v[j]), __float_as_uint(v[j + 2]));
+    }
+    return {pick_bytes<0x5410>(p[0], p[2]), pick_bytes<0x5410>(p[1], p[3])};
+}
+
+// The top bytes' signs of the low (`low`) and high halves of four words: with the
+// words' order that of the values wanted.
+__device__ __forceinline__ void half_signs(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, uint32_t &low,
+                                           uint32_t &high) {
+    const uint32_t p = pick_bytes<0x7351>(w0, w1), q = pick_bytes<0x7351>(w2, w3);
+    low = pick_bytes<0xDC98>(p, q);
+    high = pick_bytes<0xFEBA>(p, q);
+}
+
+// The signs of eight elements as they came.
+template <typename T>
+__device__ __forceinline__ Signs8 signs8(const Pack8<T> &p) {
+    Signs8 s;
+    if constexpr (sizeof(T) == 2) {
+        const uint4 &w = p.v[0];
+        half_signs(w.x, w.y, w.z, w.w, s.even, s.odd);
+    } else {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = to_float(p.get(j));
+        s = signs8(v);
+    }
+    return s;
+}
+
+// Eight codes of code_stochastic with their signs, value j in bits 4 j .. 4 j + 3.
+__device__ __forceinline__ uint32_t pack_stochastic(const uint32_t (&c)[8], const Signs8 &s) {
+    const uint32_t e = pick_bytes<0x5410>(pick_bytes<0x0073>(c[0], c[2]), pick_bytes<0x0073>(c[4], c[6]));
+    const uint32_t o = pick_bytes<0x5410>(pick_bytes<0x0073>(c[1], c[3]), pick_bytes<0x0073>(c[5], c[7]));
+    const uint32_t sign = (s.even & 0x0F0F0F0Fu) | (s.odd & 0xF0F0F0F0u);
+    return (e + 16u * o) | (sign & 0x88888888u);
 }
 
 // (r + 4 * 65536) * 256 of element j of eight (bits as random_bits8 gives them),

@@ -178,16 +178,16 @@ __device__ __forceinline__ uint32_t scaled_bits(uint32_t m, float scale) {
     return __float_as_uint(__fmul_rn(__uint_as_float(m), scale)) & 0x7FFFFFFFu;
 }
 
-// Eight codes of values v with the block's scale.
-template <bool NV, bool SR>
-__device__ __forceinline__ uint32_t codes8(const float (&v)[8], uint32_t amax, const BlockScale<NV> &scale,
-                                           const uint4 &bits) {
+// Eight codes of values v, whose signs are those of `from`, with the block's scale.
+template <bool NV, bool SR, typename S>
+__device__ __forceinline__ uint32_t codes8(const float (&v)[8], const S &from, uint32_t amax,
+                                           const BlockScale<NV> &scale, const uint4 &bits) {
     uint32_t q = 0;
     if constexpr (SR) {
         uint32_t c[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) c[j] = code_stochastic(scale.magnitude(v[j]), v[j], bits_r8(bits, j));
-        q = pack_stochastic(c);
+        for (int j = 0; j < 8; ++j) c[j] = code_stochastic(scale.magnitude(v[j]), bits_r8(bits, j));
+        q = pack_stochastic(c, signs8(from));
     } else {
         float s[8];
 #pragma unroll
@@ -265,7 +265,11 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *x, const Qu
                 const BlockScale<NV> scale = block_scale<NV, SR>(m, g, byte);
                 uint4 bits = make_uint4(0, 0, 0, 0);
                 if constexpr (SR) bits = random_bits8(a.drop.rng, kRngRounding, uint32_t(w.row), uint32_t(c / 8));
-                const uint32_t q = codes8<NV, SR>(v, m, scale, bits);
+                uint32_t q;
+                if constexpr (DROP)
+                    q = codes8<NV, SR>(v, v, m, scale, bits);
+                else
+                    q = codes8<NV, SR>(v, p[u], m, scale, bits);
                 if (WHOLE || c < (cols + 31) / 32 * 32) *reinterpret_cast<uint32_t *>(code_row + c / 2) = q;
                 // Four blocks' bytes to one word (held by the first lane of the four).
                 uint32_t word = byte;
@@ -369,7 +373,7 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const T *x, const Qu
                 if constexpr (DROP) m = scaled_bits(m, a.drop.scale);
                 uint32_t byte;
                 const BlockScale<NV> scale = block_scale<NV, SR>(m, g, byte);
-                const uint32_t q = codes8<NV, SR>(v, m, scale, bits);
+                const uint32_t q = codes8<NV, SR>(v, p[i], m, scale, bits);
                 if (exists && code_exists) *reinterpret_cast<uint32_t *>(code + i * code_step) = q;
                 // The row's scale bytes of these 64 columns: a word (nvfp4), or half
                 // of one; a last first half also clears the other.
@@ -450,11 +454,20 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const T *x, const Qu
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint32_t r = *reinterpret_cast<const uint32_t *>(rs + (16 * warp + 8 * w + j) * kTileC + 2 * lane);
-                ca[j] = code_stochastic(sa.magnitude(va[j]), va[j], low_r8(r));
-                cb[j] = code_stochastic(sb.magnitude(vb[j]), vb[j], high_r8(r));
+                ca[j] = code_stochastic(sa.magnitude(va[j]), low_r8(r));
+                cb[j] = code_stochastic(sb.magnitude(vb[j]), high_r8(r));
             }
-            qa[w] = pack_stochastic(ca);
-            qb[w] = pack_stochastic(cb);
+            Signs8 na, nb;
+            if constexpr (sizeof(T) == 2) {
+                auto word = [&](int j) { return reinterpret_cast<const uint32_t &>(t[8 * w + j]); };
+                half_signs(word(0), word(2), word(4), word(6), na.even, nb.even);
+                half_signs(word(1), word(3), word(5), word(7), na.odd, nb.odd);
+            } else {
+                na = signs8(va);
+                nb = signs8(vb);
+            }
+            qa[w] = pack_stochastic(ca, na);
+            qb[w] = pack_stochastic(cb, nb);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
