@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *x, const Qu
     constexpr int LPB = NV ? 2 : 4;          // lanes per block
     constexpr int LPT = 4 * LPB;             // lanes per scale word
     const int lane = threadIdx.x & 31;
-    const float g = (NV && a.g != nullptr) ? __ldg(a.g) : 1.0f;
+    const MatrixScale<NV> g(a.g);
     const int64_t ktiles = (a.cols + 8 * LPT - 1) / (8 * LPT);
     const int64_t rows_p = (a.rows + 127) / 128 * 128;
     const int cols = int(a.cols);
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const T *x, const Qu
     griddep_wait();
     griddep_launch_dependents();
     constexpr int KW = NV ? 64 : 128;  // columns (rows) per scale word
-    const float g = (NV && a.g != nullptr) ? __ldg(a.g) : 1.0f;
+    const MatrixScale<NV> g(a.g);
     const int64_t tiles_c = (a.cols + kTileC - 1) / kTileC;
     const int64_t kt_rows = (a.cols + KW - 1) / KW, kt_cols = (a.rows + KW - 1) / KW;
     const int64_t r0 = blockIdx.x / tiles_c * kTileR, c0 = (blockIdx.x % tiles_c) * kTileC;
