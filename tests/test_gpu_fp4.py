@@ -234,6 +234,21 @@ def test_quantize_ties_of_nvfp4_scales():
     check_quantised(ptc.quantize_fp4(torch.from_numpy(x).to(DEV), "nvfp4"), x, "nvfp4", "nearest", None, None)
 
 
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_quantize_stochastic_thresholds(fmt):
+    """Values where the code goes up for the element's own random number, and their FP32 neighbours."""
+    bits = ref.bits16(128, 96, SEED, 5, 1)
+    rng = np.random.default_rng(3)
+    low = rng.integers(0, 7, bits.shape)
+    x = (ref.GRID[low] + (ref.GRID[low + 1] - ref.GRID[low]) * (65536 - bits) / 65536).astype(np.float32)
+    x = (x.view(np.int32) + rng.integers(-2, 3, x.shape).astype(np.int32)).view(np.float32)
+    x = np.minimum(x, np.float32(6)) * rng.choice(np.float32([-1, 1]), x.shape)
+    x[np.add.outer(np.arange(128), np.arange(96)) % 16 == 0] = 6  # in every block: its scale is 1
+    a, b = ptc.quantize_fp4(torch.from_numpy(x).to(DEV), fmt, transposed="both", rounding="stochastic", seed=SEED, offset=5)
+    check_quantised(a, x, fmt, "stochastic", bits, None)
+    check_quantised(b, np.ascontiguousarray(x.T), fmt, "stochastic", bits.T, None)
+
+
 def test_quantize_strided_input_and_empty():
     big = normal(40, 400, 12, torch.float16, 0.5)
     for x in (big[:, 5:205], big[::3, :64], big[7:8, 2:], big[:, 16:144]):
