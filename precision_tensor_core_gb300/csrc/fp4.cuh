@@ -291,6 +291,8 @@ __device__ __forceinline__ uint32_t codes_nearest(const float (&v)[8]) {
 // nearest, so that the sum passes a multiple of 2^-18 only where the exact one
 // does.  `r8` is (r + 4 * 65536) * 256; the 4 makes up for the exponent's bias
 // (2 * 126 = -4 modulo 8) and the product by 4 takes the constant out at the top.
+// The signs join the packed codes, four at a time (joined to each code: 8192 x 8192
+// bfloat16 to mxfp4 both ways 90 us instead of 81).
 __device__ __forceinline__ uint32_t code_stochastic(float u, uint32_t r8) {
     float half_gap;  // (1 - u) / 2, or 0
     asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(half_gap) : "f"(u), "f"(-0.5f), "f"(0.5f));
@@ -321,8 +323,8 @@ __device__ __forceinline__ Signs8 signs8(const float (&v)[8]) {
     return {pick_bytes<0x5410>(p[0], p[2]), pick_bytes<0x5410>(p[1], p[3])};
 }
 
-// The top bytes' signs of the low (`low`) and high halves of four words: with the
-// words' order that of the values wanted.
+// Of four words of two 16-bit values: byte j is 0xFF where word j's low (`low`) or
+// high value is negative.
 __device__ __forceinline__ void half_signs(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, uint32_t &low,
                                            uint32_t &high) {
     const uint32_t p = pick_bytes<0x7351>(w0, w1), q = pick_bytes<0x7351>(w2, w3);

@@ -201,10 +201,10 @@ __device__ __forceinline__ uint32_t codes8(const float (&v)[8], const S &from, u
 // them, all loads before the first use: the block's maximum by one or two
 // shuffles, codes as 4 bytes per lane (128 contiguous bytes per warp), scales
 // gathered to one 4-byte store per tile.  Rows past the last one to the end of
-// the scale tile get zero scales.  8192 x 8192 bfloat16: 28.3 us to mxfp4 (6.0
-// TB/s, 90% of the copy rate) and 38.9 to nvfp4 to nearest, where the block's
-// division shows; 66 and 76 us stochastically, where the random numbers and the
-// rounding fill the integer pipe.
+// the scale tile get zero scales.  8192 x 8192 bfloat16: 28.1 us to mxfp4 (6.0
+// TB/s, 90% of the copy rate) and 38.5 to nvfp4 to nearest, where the elements'
+// quotients show; 56 and 66 us stochastically, bound by the issue of
+// instructions (random numbers and rounding).
 template <typename T, bool NV, bool SR, bool DROP, int U>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *x, const QuantArgs a) {
     griddep_wait();
@@ -294,10 +294,13 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *x, const Qu
 // and a warp 16 rows: a block of nvfp4, half of one of mxfp4, whose maximum two
 // warps share.  Codes and scale bytes go through shared memory so that a
 // column's 64 bytes are written together.  8192 x 8192 bfloat16 to mxfp4 both
-// ways: 53 us to nearest (30.6 us of traffic), 111 us stochastically, the
-// integer pipe at 83%.  (128 x 128 tiles of one column per thread took 33 us
-// for 2047 x 1003 both ways, these take 10: four times the CTAs.  Five or six
-// CTAs per SM instead of four made no difference.)
+// ways: 44 us to nearest (30.6 us of traffic), 81 us stochastically, with an
+// instruction issued in 79% of the cycles (19 per code: 7.6 integer, 7.6 multiply).
+// Positions are 32-bit steps from the tile's corner and tiles that exist whole
+// test nothing: 64-bit ones and their tests took 53 and 105 us.  (128 x 128 tiles
+// of one column per thread took 33 us for 2047 x 1003 both ways, these take 6.7:
+// four times the CTAs.  Five or six CTAs per SM instead of four made no
+// difference.)
 constexpr int kTileR = 128, kTileC = 64;
 constexpr int kCodePitch = 80;  // of a column's 64 code bytes in shared memory
 
