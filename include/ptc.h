@@ -14,7 +14,7 @@
  *
  * and, beside the study, the 4-bit floating-point operators that language models
  * train and decode with: gemm_fp4, gemm_a16_fp4, ptc_quantize_fp4,
- * ptc_dequantize_fp4 and ptc_dropout (see "Microscaled 4-bit matrices" below).
+ * ptc_dequantize_fp4, ptc_dropout and ptc_dropout_to (see "Microscaled 4-bit matrices" below).
  *
  * The first three compute C <- A.B exactly as the plain sum over k, with C
  * overwritten and no scaling, bias or dequantisation (section VI "Scope":
@@ -358,6 +358,14 @@ int gemm_baseline(int variant, int64_t M, int64_t N, int64_t K,
  */
 int ptc_dropout(int64_t rows, int64_t cols, const void *x, int64_t ldx, const void *residual, int64_t ldr, void *y,
                 int64_t ldy, int type, double p, uint64_t seed, uint64_t offset, void *stream);
+
+/*
+ * The same with a type of its own for y (and the residual): out_type is x's type,
+ * or PTC_OUT_BF16 / PTC_OUT_F16 for PTC_OUT_F32 x without a residual.  A gradient
+ * that a product leaves in FP32 is so rounded once.  y may be x only in x's type.
+ */
+int ptc_dropout_to(int64_t rows, int64_t cols, const void *x, int64_t ldx, int type, const void *residual, int64_t ldr,
+                   void *y, int64_t ldy, int out_type, double p, uint64_t seed, uint64_t offset, void *stream);
 
 /*
  * Quantisation of x (rows x cols, ldx elements apart, type PTC_OUT_*) to a

@@ -11,7 +11,7 @@ library's CUDA kernels):
   ``gemm_s8_noalloc``, ``gemm_s8_b_rowmajor``, ``gemm_status_string``,
   ``gemm_poll_device_error``, ``ptc_kernel_launch_count``, ``ptc_last_launch``, ``ptc_last_conversion``, ``ptc_plan_shape``,
   ``ptc_debug_set_wait_limit``, ``ptc_set_tuning``, ``gemm_fp4``, ``gemm_a16_fp4``, ``ptc_dropout``,
-  ``ptc_quantize_fp4``, ``ptc_dequantize_fp4``: the C ABI of
+  ``ptc_dropout_to``, ``ptc_quantize_fp4``, ``ptc_dequantize_fp4``: the C ABI of
   ``include/ptc.h`` under the same names, taking integers (sizes, leading
   dimensions, device addresses, a cudaStream_t handle).  A nonzero status
   raises :class:`PtcError`.
@@ -97,6 +97,7 @@ def lib() -> ctypes.CDLL:
         _int, _u64, _f64 = ctypes.c_int, ctypes.c_uint64, ctypes.c_double
         for name, args in (
                 ("ptc_dropout", [_i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _int, _f64, _u64, _u64, _vp]),
+                ("ptc_dropout_to", [_i64, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64, _int, _f64, _u64, _u64, _vp]),
                 ("ptc_quantize_fp4", [_i64, _i64, _vp, _i64, _int, _int, _int, _vp, _vp, _i64, _vp, _vp, _i64, _vp,
                                       _f64, _u64, _u64, _vp]),
                 ("ptc_dequantize_fp4", [_i64, _i64, _vp, _i64, _vp, _int, _vp, _vp, _i64, _int, _vp]),
@@ -209,6 +210,12 @@ def gemm_baseline(variant, M, N, K, A, lda, B, ldb, C, ldc, stream=0) -> int:
 def ptc_dropout(rows, cols, x, ldx, residual, ldr, y, ldy, type, p, seed, offset, stream=0) -> int:
     """y = dropout(x) (+ residual), mask from (seed, offset); device addresses."""
     return _check(lib().ptc_dropout(rows, cols, x, ldx, residual, ldr, y, ldy, type, p, seed, offset, stream))
+
+
+def ptc_dropout_to(rows, cols, x, ldx, type, residual, ldr, y, ldy, out_type, p, seed, offset, stream=0) -> int:
+    """ptc_dropout with a type of its own for y; device addresses."""
+    return _check(lib().ptc_dropout_to(rows, cols, x, ldx, type, residual, ldr, y, ldy, out_type, p, seed, offset,
+                                       stream))
 
 
 def ptc_quantize_fp4(rows, cols, x, ldx, type, format, rounding, matrix_scale, codes, pitch, scales, codes_t, pitch_t,
@@ -457,8 +464,8 @@ def _load_native():
         raise RuntimeError(f"_native.so is not built ({path}); run __graft_entry__.build()")
     n = importlib.import_module(__name__ + "._native")
     L = lib()
-    n.init(*(ctypes.cast(getattr(L, f), _vp).value for f in ("ptc_dropout", "ptc_quantize_fp4", "ptc_dequantize_fp4",
-                                                             "gemm_fp4", "gemm_a16_fp4")),
+    n.init(*(ctypes.cast(getattr(L, f), _vp).value for f in ("ptc_dropout_to", "ptc_quantize_fp4",
+                                                             "ptc_dequantize_fp4", "gemm_fp4", "gemm_a16_fp4")),
            _check, _stream, Fp4Matrix)
     _native = n
     return n
@@ -517,13 +524,14 @@ class Fp4Matrix:
         return s.permute(0, 3, 2, 1, 4).reshape(-1, kt * 4)[:r, :b]
 
 
-def dropout(x, p, seed, offset=0, residual=None, out=None, stream=None):
+def dropout(x, p, seed, offset=0, residual=None, out=None, stream=None, out_dtype=None):
     """``x`` with each element dropped with probability ``p`` (kept ones scaled so
     that the expectation is x's), plus ``residual`` if given; float32, bfloat16
     or float16 (rows, cols).  The mask is a function of (seed, offset, row,
     column) and is never stored: the backward pass is the same call on the
-    gradient.  ``out`` may be ``x`` or ``residual``."""
-    return (_native or _load_native()).dropout(x, p, seed, offset, residual, out, stream)
+    gradient.  ``out`` may be ``x`` or ``residual``.  ``out_dtype`` is x's dtype;
+    float32 x without a residual may also give bfloat16 or float16, rounded once."""
+    return (_native or _load_native()).dropout(x, p, seed, offset, residual, out, stream, out_dtype)
 
 
 def quantize_fp4(x, fmt="mxfp4", transposed=False, rounding="nearest", tensor_scale=None, p=0.0, seed=0, offset=0,

@@ -18,7 +18,7 @@
 
 namespace {
 
-decltype(&ptc_dropout) f_dropout;
+decltype(&ptc_dropout_to) f_dropout;
 decltype(&ptc_quantize_fp4) f_quantize;
 decltype(&ptc_dequantize_fp4) f_dequantize;
 decltype(&gemm_fp4) f_gemm;
@@ -83,6 +83,11 @@ int type_of(at::ScalarType t) {
         case at::kHalf: return PTC_OUT_F16;
         default: raise(PyExc_TypeError, "tensors are float32, bfloat16 or float16");
     }
+}
+
+at::ScalarType dtype_of(PyObject *o) {
+    if (!THPDtype_Check(o)) raise(PyExc_TypeError, "a torch dtype is expected");
+    return reinterpret_cast<THPDtype *>(o)->scalar_type;
 }
 
 // A 2-D device tensor with unit column stride.
@@ -241,17 +246,19 @@ void expect(Py_ssize_t n, Py_ssize_t want) {
     }                    \
     END_HANDLE_TH_ERRORS
 
-// (x, p, seed, offset, residual, out, stream)
+// (x, p, seed, offset, residual, out, stream, out_dtype)
 PyObject *py_dropout(PyObject *, PyObject *const *a, Py_ssize_t n) {
     PTC_BODY_BEGIN
-    expect(n, 7);
+    expect(n, 8);
     const at::Tensor &x = tensor(a[0], "x");
     const int type = type_of(x.scalar_type());
+    const at::ScalarType st = a[7] == Py_None ? x.scalar_type() : dtype_of(a[7]);
+    const int out_type = type_of(st);
     const Rows rx = rows_of(x, "x");
     const c10::DeviceIndex index = x.get_device();
     auto like = [&](const at::Tensor &t, const char *name) {
-        if (t.scalar_type() != x.scalar_type() || t.sizes() != x.sizes() || !t.is_cuda() || t.get_device() != index) {
-            PyErr_Format(PyExc_ValueError, "%s must have x's shape, dtype and device", name);
+        if (t.scalar_type() != st || t.sizes() != x.sizes() || !t.is_cuda() || t.get_device() != index) {
+            PyErr_Format(PyExc_ValueError, "%s must have the result's shape, dtype and device", name);
             throw Bad();
         }
     };
@@ -262,12 +269,12 @@ PyObject *py_dropout(PyObject *, PyObject *const *a, Py_ssize_t n) {
         rr = rows_of(r, "residual");
     }
     if (a[5] != Py_None) like(tensor(a[5], "out"), "out");
-    at::Tensor y = result(a[5], rx.rows, rx.cols, x.scalar_type(), index, x.device());
+    at::Tensor y = result(a[5], rx.rows, rx.cols, st, index, x.device());
     const Rows ry = rows_of(y, "out");
     const double p = real(a[1]);
     const uint64_t seed = seed64(a[2]), offset = uint64_t(integer(a[3]));
     call(index, a[6], [&](void *s) {
-        return f_dropout(rx.rows, rx.cols, rx.p, rx.ld, rr.p, rr.ld, ry.p, ry.ld, type, p, seed, offset, s);
+        return f_dropout(rx.rows, rx.cols, rx.p, rx.ld, type, rr.p, rr.ld, ry.p, ry.ld, out_type, p, seed, offset, s);
     });
     return give(a[5], std::move(y));
     PTC_BODY_END
@@ -313,9 +320,7 @@ PyObject *py_quantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
 // dtype argument (None: `or_else`) or out's.
 at::ScalarType out_type(PyObject *dtype, PyObject *out, at::ScalarType or_else) {
     if (out != Py_None) return tensor(out, "out").scalar_type();
-    if (dtype == Py_None) return or_else;
-    if (!THPDtype_Check(dtype)) raise(PyExc_TypeError, "a torch dtype is expected");
-    return reinterpret_cast<THPDtype *>(dtype)->scalar_type;
+    return dtype == Py_None ? or_else : dtype_of(dtype);
 }
 
 // (q, dtype, out, stream)

@@ -51,8 +51,11 @@ struct DropArgs {
 // wide products (a quarter of the integer rate each) come close to the traffic's
 // time.  8192 x 8192 bfloat16: 60.6 us with a residual (6.6 TB/s, the copy
 // rate), 50.4 us without (5.3 TB/s, bound by the random numbers).
-template <typename T, bool RES>
-__global__ void __launch_bounds__(256) dropout_kernel(const T *x, int64_t ldx, const T *res, int64_t ldr, T *y,
+//
+// O is the type of y: T, or a 16-bit type for FP32 x (no residual then), so that
+// an FP32 product is dropped out and rounded once.
+template <typename T, typename O, bool RES>
+__global__ void __launch_bounds__(256) dropout_kernel(const T *x, int64_t ldx, const O *res, int64_t ldr, O *y,
                                                       int64_t ldy, int64_t rows, int64_t cols, DropArgs d) {
     griddep_wait();
     griddep_launch_dependents();
@@ -62,7 +65,7 @@ __global__ void __launch_bounds__(256) dropout_kernel(const T *x, int64_t ldx, c
         const int64_t c = int64_t(w.group) * 8;
         const int n = int(min(int64_t(8), cols - c));
         const Pack8<T> a = load8(x + w.row * ldx + c, n, true);
-        Pack8<T> r;
+        Pack8<O> r;
         float o[8];
         if constexpr (RES) r = load8(res + w.row * ldr + c, n, true);
         const uint4 bits = random_bits8(d.rng, kRngDropout, uint32_t(w.row), w.group);
@@ -73,7 +76,7 @@ __global__ void __launch_bounds__(256) dropout_kernel(const T *x, int64_t ldx, c
             if constexpr (RES) v = __fadd_rn(v, to_float(r.get(j)));
             o[j] = v;
         }
-        store8(y + w.row * ldy + c, round8<T>(o), n, true);
+        store8(y + w.row * ldy + c, round8<O>(o), n, true);
     }
 }
 
@@ -83,8 +86,8 @@ __global__ void __launch_bounds__(256) dropout_kernel(const T *x, int64_t ldx, c
 // made them.  (Eight elements per lane, one store each, touched every sector
 // eight times: 2047 x 1003 binary16 took 7.5 us, and takes 3.9; 8191 x 8191
 // float32 84 us, 6.4 TB/s.)
-template <typename T, bool RES>
-__global__ void __launch_bounds__(256) dropout_ragged_kernel(const T *x, int64_t ldx, const T *res, int64_t ldr, T *y,
+template <typename T, typename O, bool RES>
+__global__ void __launch_bounds__(256) dropout_ragged_kernel(const T *x, int64_t ldx, const O *res, int64_t ldr, O *y,
                                                              int64_t ldy, int64_t rows, int64_t cols, DropArgs d) {
     griddep_wait();
     griddep_launch_dependents();
@@ -94,14 +97,16 @@ __global__ void __launch_bounds__(256) dropout_ragged_kernel(const T *x, int64_t
     for (; w.row < rows; w.next()) {
         const int64_t c0 = int64_t(w.group) * 256;
         const int n = int(min(int64_t(256), cols - c0));
-        const T *xr = x + w.row * ldx + c0, *rr = RES ? res + w.row * ldr + c0 : nullptr;
-        T *yr = y + w.row * ldy + c0;
-        T a[8], r[8];
+        const T *xr = x + w.row * ldx + c0;
+        const O *rr = RES ? res + w.row * ldr + c0 : nullptr;
+        O *yr = y + w.row * ldy + c0;
+        T a[8];
+        O r[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int c = 32 * i + lane;
             a[i] = c < n ? xr[c] : from_float<T>(0.0f);
-            if constexpr (RES) r[i] = c < n ? rr[c] : from_float<T>(0.0f);
+            if constexpr (RES) r[i] = c < n ? rr[c] : from_float<O>(0.0f);
         }
         const uint4 bits = random_bits8(d.rng, kRngDropout, uint32_t(w.row), uint32_t(c0 / 8) + lane);
         uint32_t keep = 0;
@@ -113,7 +118,7 @@ __global__ void __launch_bounds__(256) dropout_ragged_kernel(const T *x, int64_t
             const uint32_t k = __shfl_sync(0xFFFFFFFFu, keep, 4 * i + (lane >> 3)) >> (lane & 7);
             float v = (k & 1u) ? __fmul_rn(to_float(a[i]), d.scale) : 0.0f;
             if constexpr (RES) v = __fadd_rn(v, to_float(r[i]));
-            if (c < n) yr[c] = from_float<T>(v);
+            if (c < n) yr[c] = from_float<O>(v);
         }
     }
 }
@@ -634,20 +639,24 @@ int check_random(double p, uint64_t offset) {
     return PTC_OK;
 }
 
-template <typename T>
+template <typename T, typename O>
 int run_dropout(int64_t rows, int64_t cols, const void *x, int64_t ldx, const void *res, int64_t ldr, void *y,
                 int64_t ldy, const DropArgs &d, int sms, cudaStream_t s) {
-    const int vec = wide_rows(x, ldx, sizeof(T)) && wide_rows(y, ldy, sizeof(T)) &&
-                    (res == nullptr || wide_rows(res, ldr, sizeof(T)));
-    const int64_t grid = grid_for(rows * ((cols + 7) / 8), sms);
-    const T *xp = static_cast<const T *>(x), *rp = static_cast<const T *>(res);
-    T *yp = static_cast<T *>(y);
-    auto go = [&](auto fn, int64_t blocks) {
-        return launch(fn, blocks, 256, 0, s, xp, ldx, rp, ldr, yp, ldy, rows, cols, d);
+    const int vec = wide_rows(x, ldx, sizeof(T)) && wide_rows(y, ldy, sizeof(O)) &&
+                    (res == nullptr || wide_rows(res, ldr, sizeof(O)));
+    const T *xp = static_cast<const T *>(x);
+    const O *rp = static_cast<const O *>(res);
+    O *yp = static_cast<O *>(y);
+    auto go = [&](auto wide, auto ragged) {
+        const int64_t threads = rows * (vec ? (cols + 7) / 8 : (cols + 255) / 256 * 32);
+        return launch(vec ? wide : ragged, grid_for(threads, sms), 256, 0, s, xp, ldx, rp, ldr, yp, ldy, rows, cols, d);
     };
-    const int64_t ragged = grid_for(rows * ((cols + 255) / 256) * 32, sms);
-    const cudaError_t e = vec ? (res ? go(dropout_kernel<T, true>, grid) : go(dropout_kernel<T, false>, grid))
-                              : (res ? go(dropout_ragged_kernel<T, true>, ragged) : go(dropout_ragged_kernel<T, false>, ragged));
+    cudaError_t e;
+    if constexpr (std::is_same_v<T, O>)
+        e = res ? go(dropout_kernel<T, O, true>, dropout_ragged_kernel<T, O, true>)
+                : go(dropout_kernel<T, O, false>, dropout_ragged_kernel<T, O, false>);
+    else
+        e = go(dropout_kernel<T, O, false>, dropout_ragged_kernel<T, O, false>);
     return e == cudaSuccess ? PTC_OK : fail_launch(e, "dropout launch");
 }
 
@@ -718,33 +727,43 @@ using namespace ptc;
 
 extern "C" {
 
-int ptc_dropout(int64_t rows, int64_t cols, const void *x, int64_t ldx, const void *residual, int64_t ldr, void *y,
-                int64_t ldy, int type, double p, uint64_t seed, uint64_t offset, void *stream) {
+int ptc_dropout_to(int64_t rows, int64_t cols, const void *x, int64_t ldx, int type, const void *residual, int64_t ldr,
+                   void *y, int64_t ldy, int out_type, double p, uint64_t seed, uint64_t offset, void *stream) {
     set_message("");
     if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim)
         return fail_status(PTC_ERR_INVALID, "sizes must satisfy 0 <= rows, cols <= 2^30");
-    if (!known_type(type)) return fail_status(PTC_ERR_INVALID, "unknown element type");
+    if (!known_type(type) || !known_type(out_type)) return fail_status(PTC_ERR_INVALID, "unknown element type");
+    if (out_type != type && (type != PTC_OUT_F32 || residual))
+        return fail_status(PTC_ERR_INVALID, "y has x's type, or a 16-bit type for float32 x without a residual");
     int rc = check_random(p, offset);
     if (rc) return rc;
     if (rows == 0 || cols == 0) return PTC_OK;
     if (!x || !y) return fail_status(PTC_ERR_INVALID, "x or y is NULL");
     if (ldx < cols || ldy < cols || (residual && ldr < cols) || ldx > kMaxLd || ldy > kMaxLd || (residual && ldr > kMaxLd))
         return fail_status(PTC_ERR_INVALID, "leading dimensions must be cols .. 2^36");
-    const int es = elem_bytes(type);
-    if (!multiple_of(x, es) || !multiple_of(y, es) || (residual && !multiple_of(residual, es)))
+    const int es = elem_bytes(type), os = elem_bytes(out_type);
+    if (!multiple_of(x, es) || !multiple_of(y, os) || (residual && !multiple_of(residual, os)))
         return fail_status(PTC_ERR_ALIGN, "pointers must be aligned to the element");
-    const uint64_t ybytes = span_of(rows, cols, ldy, es);
-    if ((y != x || ldy != ldx) && ranges_overlap(y, ybytes, x, span_of(rows, cols, ldx, es)))
+    const uint64_t ybytes = span_of(rows, cols, ldy, os);
+    if ((y != x || ldy != ldx || out_type != type) && ranges_overlap(y, ybytes, x, span_of(rows, cols, ldx, es)))
         return fail_status(PTC_ERR_OVERLAP, "y overlaps x without being x");
-    if (residual && (y != residual || ldy != ldr) && ranges_overlap(y, ybytes, residual, span_of(rows, cols, ldr, es)))
+    if (residual && (y != residual || ldy != ldr) && ranges_overlap(y, ybytes, residual, span_of(rows, cols, ldr, os)))
         return fail_status(PTC_ERR_OVERLAP, "y overlaps the residual without being it");
     int sms;
     if ((rc = usable_device(&sms))) return rc;
     const DropArgs d = drop_args(p, seed, offset);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (type == PTC_OUT_F32) return run_dropout<float>(rows, cols, x, ldx, residual, ldr, y, ldy, d, sms, s);
-    if (type == PTC_OUT_BF16) return run_dropout<__nv_bfloat16>(rows, cols, x, ldx, residual, ldr, y, ldy, d, sms, s);
-    return run_dropout<__half>(rows, cols, x, ldx, residual, ldr, y, ldy, d, sms, s);
+    auto go = [&](auto run) { return run(rows, cols, x, ldx, residual, ldr, y, ldy, d, sms, s); };
+    if (type == PTC_OUT_BF16) return go(run_dropout<__nv_bfloat16, __nv_bfloat16>);
+    if (type == PTC_OUT_F16) return go(run_dropout<__half, __half>);
+    return out_type == PTC_OUT_F32    ? go(run_dropout<float, float>)
+           : out_type == PTC_OUT_BF16 ? go(run_dropout<float, __nv_bfloat16>)
+                                      : go(run_dropout<float, __half>);
+}
+
+int ptc_dropout(int64_t rows, int64_t cols, const void *x, int64_t ldx, const void *residual, int64_t ldr, void *y,
+                int64_t ldy, int type, double p, uint64_t seed, uint64_t offset, void *stream) {
+    return ptc_dropout_to(rows, cols, x, ldx, type, residual, ldr, y, ldy, type, p, seed, offset, stream);
 }
 
 int ptc_quantize_fp4(int64_t rows, int64_t cols, const void *x, int64_t ldx, int type, int format, int rounding,

@@ -40,9 +40,10 @@ def backward(dy, saved):
     import torch
     xqt, wqt, p, seed, offset = saved
     dyq, dyqt = quantize_fp4(dy, FORMAT, transposed="both", rounding="stochastic", seed=seed, offset=offset)
-    dx = matmul_fp4(dyq, wqt, out_dtype=dy.dtype)
-    if p > 0.0:
-        dx = dropout(dx, p, seed, offset, out=dx)
+    if p > 0.0:  # (the product stays in FP32, so that dx is rounded once)
+        dx = dropout(matmul_fp4(dyq, wqt, out_dtype=torch.float32), p, seed, offset, out_dtype=dy.dtype)
+    else:
+        dx = matmul_fp4(dyq, wqt, out_dtype=dy.dtype)
     return dx, matmul_fp4(dyqt, xqt, out_dtype=torch.float32)
 
 
