@@ -32,7 +32,12 @@
 // multiplies the block's partial sum: exact for elements down to 2^-32 of the
 // largest, off by at most 2^-40 of the largest below that.  (bfloat16 MMAs
 // need no such step, but take three more integer instructions per two weights:
-// 16.8 us instead of 12.2 for one token and 8192 x 8192 mxfp4 weights.)
+// 16.8 us instead of 12.2 for one token and 8192 x 8192 mxfp4 weights.)  A block of
+// codes times bfloat16's largest values lies beyond FP32 before its mxfp4 scale
+// brings it back, so with those the sums are held 2^-8 times their size: the
+// powers of two carry the factor, and the output's rounding takes it out.  At
+// that size bfloat16's smallest number times the smallest code is still 2^-142,
+// which FP32 holds.
 //
 // The partial sums of the S shares are added in order in shared memory; where
 // that leaves SMs idle K is also shared by a cluster of up to eight CTAs, whose
@@ -124,6 +129,10 @@ __device__ __forceinline__ void load_scale_box(uint32_t dst, const CUtensorMap *
         "l"(reinterpret_cast<uint64_t>(map)), "r"(word), "r"(kt), "r"(rt), "r"(smem_u32(bar))
         : "memory");
 }
+
+// mxfp4 with bfloat16 tokens: the sums' size.  A block's sum of 32 codes of at most 6
+// and activations below 2^15 is below 2^23, its power of two at most 2^113.
+constexpr float kSumSize = 0x1p-8f;
 
 struct TokTail {
     uint64_t full[kWarps][kStages], empty[kWarps][kStages];  // per share
@@ -314,7 +323,9 @@ __global__ void __launch_bounds__(kTokThreads, 2)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) h.set(j, __float2half_rn(__fmul_rn(to_float(v.get(j)), down)));
                 *reinterpret_cast<uint4 *>(xs_base + dst) = h.v[0];
-                if (t == 0) *reinterpret_cast<float *>(xs_base + pw) = __uint_as_float(uint32_t(127 + e) << 23);
+                if (t == 0)
+                    *reinterpret_cast<float *>(xs_base + pw) =
+                        __fmul_rn(__uint_as_float(uint32_t(127 + e) << 23), NV ? 1.0f : kSumSize);
             });
         };
 
@@ -424,7 +435,7 @@ __global__ void __launch_bounds__(kTokThreads, 2)
         cluster_sync();
     else
         __syncthreads();
-    const float g = a.g ? __ldg(a.g) : 1.0f;
+    const float g = NV ? (a.g ? __ldg(a.g) : 1.0f) : BF16 ? 1.0f / kSumSize : 1.0f;
     const uint32_t base = smem_u32(xs_base);
     for (int i = krank * kTokThreads + int(threadIdx.x); i < R * 16 * TOK; i += a.ks * kTokThreads) {
         // Consecutive threads take consecutive rows of a row group.
