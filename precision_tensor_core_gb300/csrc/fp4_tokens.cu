@@ -28,7 +28,7 @@
 // significant bits within 2^-10 .. 2688).  mxfp4 scales exceed binary16, so
 // each block's FP32 partial sum is multiplied by its row's scale instead.
 // bfloat16 activations become binary16 relative to a power of two per token
-// and block of 32, which brings the block's largest to [2^14, 2^15) and
+// and block of 32, which brings the block's largest to [2^15, 2^16) and
 // multiplies the block's partial sum: exact for elements down to 2^-32 of the
 // largest, off by at most 2^-40 of the largest below that.  (bfloat16 MMAs
 // need no such step, but take three more integer instructions per two weights:
@@ -131,7 +131,7 @@ __device__ __forceinline__ void load_scale_box(uint32_t dst, const CUtensorMap *
 }
 
 // mxfp4 with bfloat16 tokens: the sums' size.  A block's sum of 32 codes of at most 6
-// and activations below 2^15 is below 2^23, its power of two at most 2^113.
+// and activations below 2^16 is below 2^24, its power of two at most 2^112.
 constexpr float kSumSize = 0x1p-8f;
 
 struct TokTail {
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kTokThreads, 2)
                 }
                 m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
                 m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-                const int e = max(int(m >> 23) - 127 - 14, -126);
+                const int e = max(int(m >> 23) - 127 - 15, -126);  // (the largest: 65280 of binary16's 65504)
                 const float down = __uint_as_float(uint32_t(127 - e) << 23);
                 Pack8<__half> h;
 #pragma unroll

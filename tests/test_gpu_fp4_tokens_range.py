@@ -59,3 +59,21 @@ def test_blocks_whose_exponents_cancel(M, N, K):
     codes[:, :K] = rng.integers(0, 16, (N, K))
     W, w = weights(codes, byte, K)
     check(ptc.matmul_a16_fp4(x, W), x.cpu().double().numpy(), w, K)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("top", [1.0, 1.5, 255 / 128])
+def test_small_activations_beside_a_large_one(fmt, top):
+    """Elements down to 2^-32 of the largest of their 32 are exact (eight significant bits each)."""
+    K, n = 256, ref.BLOCK[fmt]
+    rng = np.random.default_rng(1)
+    codes = rng.integers(0, 16, (64, K))
+    codes[:, ::32] = 0  # the large element's weight
+    W, w = weights(codes, np.full((64, K // n), 127 if fmt == "mxfp4" else 56), K, fmt)
+    x = np.zeros((4, K))
+    x[:, ::32] = top
+    x[np.arange(4)[:, None], np.arange(8) * 32 + 1 + rng.integers(0, 31, (4, 8))] = rng.integers(129, 256, (4, 8)) * 2.0 ** -39
+    x = x * np.array([1.0, 2.0 ** 60, 2.0 ** -60, -8.0])[:, None]
+    C = ptc.matmul_a16_fp4(torch.from_numpy(x.astype(np.float32)).bfloat16().to(DEV), W)
+    want = torch.from_numpy((x @ w.T).astype(np.float32)).bfloat16()  # few terms of 12 bits: exact in FP32
+    assert torch.equal(C.cpu(), want)
