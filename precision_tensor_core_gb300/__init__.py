@@ -448,7 +448,11 @@ _HOST_FN.update({gemm_f16: gemm_f16_host, gemm_s8: gemm_s8_host, gemm_s4: gemm_s
 # ---------------------------------------------------------------- 4-bit operators on tensors
 # These calls are a few microseconds on the device at decoding sizes, so their
 # marshalling is native: _native.so (csrc/binding.cpp) checks the tensors,
-# allocates results and calls the C ABI.
+# allocates results and calls the C ABI.  With `stream` (a torch stream or a
+# handle) a call runs as under torch.cuda.stream(stream): it is ordered after that
+# stream's work alone, so the caller waits for its inputs and for the result.
+# The tensors' memory needs no such care: results come from that stream's, and
+# inputs and results may be released while it runs.
 _FP4 = {"mxfp4": (PTC_FP4_MX, 32), "nvfp4": (PTC_FP4_NV, 16)}
 _ROUNDING = {"nearest": PTC_ROUND_NEAREST, "stochastic": PTC_ROUND_STOCHASTIC}
 _native = None

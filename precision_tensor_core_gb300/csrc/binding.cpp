@@ -196,25 +196,60 @@ struct NewMatrix {
     }
 };
 
-// Runs f(stream) with the device current, on the stream argument or the device's current stream.
-template <typename F>
-void call(c10::DeviceIndex index, PyObject *stream, F f) {
-    c10::cuda::OptionalCUDAGuard guard;
-    if (c10::cuda::current_device() != index) guard.set_index(index);
-    void *handle;
-    if (stream == Py_None) {
-        handle = c10::cuda::getCurrentCUDAStream(index).stream();
-    } else {
-        Ref h(PyObject_CallOneArg(g_stream, stream));
-        handle = reinterpret_cast<void *>(uintptr_t(seed64(h.p)));
+// Where a call runs: the tensors' device and the stream argument, or the device's
+// current stream.  While it lives both are current, so results come from that
+// stream's memory: a block that the caching allocator hands out again may still be
+// in use on the stream it belongs to, and on no other.  A call on another stream
+// than the caller's also tells the allocator so (used): the caller may release its
+// inputs, and results, without waiting for that stream.
+class Target {
+    c10::cuda::CUDAStream caller_;
+    void *handle_;
+    c10::cuda::OptionalCUDAGuard device_;
+    c10::cuda::OptionalCUDAStreamGuard stream_;
+
+  public:
+    Target(c10::DeviceIndex index, PyObject *stream) : caller_(c10::cuda::getCurrentCUDAStream(index)) {
+        handle_ = caller_.stream();
+        if (stream != Py_None) {
+            Ref h(PyObject_CallOneArg(g_stream, stream));
+            handle_ = reinterpret_cast<void *>(uintptr_t(seed64(h.p)));
+            if (handle_ == cudaStreamLegacy) handle_ = nullptr;  // (torch knows the default stream by that)
+        }
+        if (elsewhere())
+            stream_.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle_), index));
+        else if (c10::cuda::current_device() != index)
+            device_.set_index(index);
     }
-    const int status = f(handle);
-    if (status) {
-        Ref code(PyLong_FromLong(status));
-        Ref none(PyObject_CallOneArg(g_check, code.p));
-        throw Bad();
+    bool elsewhere() const { return handle_ != caller_.stream(); }
+    // f(stream), its status raised.
+    template <typename F>
+    void run(F f) const {
+        const int status = f(handle_);
+        if (status) {
+            Ref code(PyLong_FromLong(status));
+            Ref none(PyObject_CallOneArg(g_check, code.p));
+            throw Bad();
+        }
     }
-}
+    // Of a launched call: tensors of the caller's (a tensor, a 4-bit matrix or None),
+    // and results of this stream's memory.
+    void used(PyObject *o) const {
+        if (elsewhere()) record(o, c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle_), caller_.device_index()));
+    }
+    void made(PyObject *o) const {
+        if (elsewhere()) record(o, caller_);
+    }
+
+  private:
+    static void record(PyObject *o, c10::cuda::CUDAStream stream) {
+        if (THPVariable_Check(o)) {
+            THPVariable_Unpack(o).record_stream(stream);
+        } else if (o != Py_None) {
+            for (PyObject *name : {s_codes, s_scales, s_ts}) record(Ref(PyObject_GetAttr(o, name)).p, stream);
+        }
+    }
+};
 
 // The result tensor: `out`, or a new one.
 at::Tensor result(PyObject *out, int64_t rows, int64_t cols, at::ScalarType type, c10::DeviceIndex index, at::Device device) {
@@ -225,12 +260,15 @@ at::Tensor result(PyObject *out, int64_t rows, int64_t cols, at::ScalarType type
     return t;
 }
 
-PyObject *give(PyObject *out, at::Tensor t) {
+PyObject *give(const Target &target, PyObject *out, at::Tensor t) {
     if (out != Py_None) {
+        target.used(out);
         Py_INCREF(out);
         return out;
     }
-    return THPVariable_Wrap(std::move(t));
+    Ref made(THPVariable_Wrap(std::move(t)));
+    target.made(made.p);
+    return made.release();
 }
 
 void expect(Py_ssize_t n, Py_ssize_t want) {
@@ -269,14 +307,17 @@ PyObject *py_dropout(PyObject *, PyObject *const *a, Py_ssize_t n) {
         rr = rows_of(r, "residual");
     }
     if (a[5] != Py_None) like(tensor(a[5], "out"), "out");
+    const Target target(index, a[6]);
     at::Tensor y = result(a[5], rx.rows, rx.cols, st, index, x.device());
     const Rows ry = rows_of(y, "out");
     const double p = real(a[1]);
     const uint64_t seed = seed64(a[2]), offset = uint64_t(integer(a[3]));
-    call(index, a[6], [&](void *s) {
+    target.run([&](void *s) {
         return f_dropout(rx.rows, rx.cols, rx.p, rx.ld, type, rr.p, rr.ld, ry.p, ry.ld, out_type, p, seed, offset, s);
     });
-    return give(a[5], std::move(y));
+    target.used(a[0]);
+    target.used(a[4]);
+    return give(target, a[5], std::move(y));
     PTC_BODY_END
 }
 
@@ -294,12 +335,17 @@ PyObject *py_quantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int rounding = int(integer(a[3]));
     const double p = real(a[5]);
     const uint64_t seed = seed64(a[6]), offset = uint64_t(integer(a[7]));
+    const Target target(index, a[8]);
     auto run = [&](NewMatrix *q, NewMatrix *t) {
-        call(index, a[8], [&](void *s) {
+        target.run([&](void *s) {
             return f_quantize(rx.rows, rx.cols, rx.p, rx.ld, type, fmt, rounding, g, q ? q->codes : nullptr, q ? q->pitch : 0,
                               q ? q->scales : nullptr, t ? t->codes : nullptr, t ? t->pitch : 0, t ? t->scales : nullptr, p,
                               seed, offset, s);
         });
+        target.used(a[0]);
+        target.used(a[4]);
+        for (const NewMatrix *m : {q, t})
+            if (m) target.made(m->object.p);
     };
     if (which == 0) {
         NewMatrix q(rx.rows, rx.cols, fmt, a[1], a[4], x.device());
@@ -330,12 +376,14 @@ PyObject *py_dequantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Matrix m = matrix_of(a[0]);
     const at::ScalarType st = out_type(a[1], a[2], at::kBFloat16);
     const int type = type_of(st);
+    const Target target(m.index, a[3]);
     at::Tensor y = result(a[2], m.rows, m.k, st, m.index, m.device);
     const Rows ry = rows_of(y, "out");
-    call(m.index, a[3], [&](void *s) {
+    target.run([&](void *s) {
         return f_dequantize(m.rows, m.k, m.codes, m.pitch, m.scales, m.fmt, m.g, ry.p, ry.ld, type, s);
     });
-    return give(a[2], std::move(y));
+    target.used(a[0]);
+    return give(target, a[2], std::move(y));
     PTC_BODY_END
 }
 
@@ -349,13 +397,16 @@ PyObject *py_matmul(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (A.index != B.index) raise(PyExc_ValueError, "both matrices must be on one device");
     const at::ScalarType st = out_type(a[2], a[3], at::kBFloat16);
     const int type = type_of(st);
+    const Target target(A.index, a[4]);
     at::Tensor c = result(a[3], A.rows, B.rows, st, A.index, A.device);
     const Rows rc = rows_of(c, "out");
-    call(A.index, a[4], [&](void *s) {
+    target.run([&](void *s) {
         return f_gemm(A.rows, B.rows, A.k, A.fmt, A.codes, A.pitch, A.scales, A.g, B.codes, B.pitch, B.scales, B.g,
                       rc.p, rc.ld, type, s);
     });
-    return give(a[3], std::move(c));
+    target.used(a[0]);
+    target.used(a[1]);
+    return give(target, a[3], std::move(c));
     PTC_BODY_END
 }
 
@@ -371,12 +422,15 @@ PyObject *py_matmul_a16(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (rx.cols != W.k) raise(PyExc_ValueError, "inner dimensions differ");
     if (x.get_device() != W.index || (a[2] != Py_None && tensor(a[2], "out").scalar_type() != x.scalar_type()))
         raise(PyExc_ValueError, "x, the weights and out must share a device, x and out a dtype");
+    const Target target(W.index, a[3]);
     at::Tensor c = result(a[2], rx.rows, W.rows, x.scalar_type(), W.index, W.device);
     const Rows rc = rows_of(c, "out");
-    call(W.index, a[3], [&](void *s) {
+    target.run([&](void *s) {
         return f_gemm_a16(rx.rows, W.rows, W.k, type, rx.p, rx.ld, W.fmt, W.codes, W.pitch, W.scales, W.g, rc.p, rc.ld, s);
     });
-    return give(a[2], std::move(c));
+    target.used(a[0]);
+    target.used(a[1]);
+    return give(target, a[2], std::move(c));
     PTC_BODY_END
 }
 
