@@ -33,7 +33,8 @@
 // each take a third; 512^3 3.2 us.
 //
 // Every wait is bounded: on expiry the CTA raises its abort flag, records the
-// error word that gemm_poll_device_error reads, and every role runs out.
+// error word that gemm_poll_device_error reads, and every role runs out; the CTA
+// exits when its MMAs have ended and its copies in flight have landed.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -317,6 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_wait();
     griddep_launch_dependents();
 
+    uint32_t loaded = 0, loaded_phase = 0;  // producer: stages that hold or await a load, the phase of each
     if (warp == 0) {
         // ---------------------------------------------------------- TMA producer
         if (lane == 0) {
@@ -349,16 +351,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                             load_scales<2>(sa, &tmSA, bar, kb * C_::KAT, m0 / 128);
                             load_scales<2>(sa + C_::SFA_BYTES, &tmSB, bar, kb * C_::KAT, n0 / 128);
                         }
+                        loaded |= 1u << s;
+                        loaded_phase = (loaded_phase & ~(1u << s)) | (ph << s);
+                    } else {
+                        loaded &= ~(1u << s);
                     }
                     if (++s == nst) {
                         s = 0;
                         ph ^= 1u;
                     }
                 }
-            }
-            if (!ok) {  // abort: copies in flight land before the CTA exits
-                const uint64_t t0 = globaltimer_ns();
-                while (globaltimer_ns() - t0 < 200000) __nanosleep(1000);
             }
         }
         __syncwarp();
@@ -427,13 +429,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (!ok) {  // abort: the MMAs issued so far end before tensor memory is freed
+            // The MMAs issued so far end before tensor memory is freed, also where it is
+            // the epilogue that gave up.
+            if (ok) {
+                if (n > 0) mbar_wait(&st->acc_full, uint32_t(n - 1) & 1u, nullptr, nullptr, limit);
+            } else {
                 if (elect_one()) {
                     mma_commit<CTAS>(&st->drain);
                     mbar_wait(&st->drain, 0, nullptr, nullptr, limit);
                 }
-                __syncwarp();
             }
+            __syncwarp();
         }
     } else {
         // ---------------------------------------------------------- epilogue
@@ -538,6 +544,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
             __syncthreads();
         tc_fence_after_sync();
+    }
+    // Every role is done.  After an abort, of whichever role, copies in flight land
+    // before the CTA exits: a pair's complete on the first CTA's barriers and get 200 us
+    // (with one of its CTAs the other has given up too: its epilogue waits for the
+    // same MMAs).
+    if (warp == 0 && lane == 0 && st->abort.flag) {
+        if constexpr (CTAS == 1) {
+            for (int s = 0; s < STAGES; ++s)
+                if (loaded >> s & 1u) mbar_wait(&st->full[s], loaded_phase >> s & 1u, nullptr, nullptr, limit);
+        } else {
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 200000) __nanosleep(1000);
+        }
     }
     if (warp == 1) tmem_dealloc<CTAS>(tmem, C_::TMEM_COLS);
 }

@@ -207,6 +207,7 @@ __global__ void __launch_bounds__(kTokThreads, 2)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
 
+    int loaded = 0;  // stages that this lane of the ninth warp has asked for
     if (warp == kWarps) {
         // ---------------------------------------------------------- weights
         // Lane 4 s + q brings the 4 R rows 32 q + 4 rg0 .. of share s, lane
@@ -229,12 +230,9 @@ __global__ void __launch_bounds__(kTokThreads, 2)
                         load_scale_box(smem_u32(stage) + scale_at, &tmS, bar, 16 * rg0, (lo + i) * KAT, row0 / 128);
                     }
                     tma_load_2d(stage + code_at, &tmW, bar, (lo + i) * 128, row0 + 32 * q + 4 * rg0);
+                    loaded = i + 1;
                 }
             }
-        }
-        if (!ok) {  // abort: copies in flight land before the CTA exits
-            const uint64_t t0 = globaltimer_ns();
-            while (globaltimer_ns() - t0 < 200000) __nanosleep(1000);
         }
         __syncwarp();
     } else {
@@ -435,6 +433,10 @@ __global__ void __launch_bounds__(kTokThreads, 2)
         cluster_sync();
     else
         __syncthreads();
+    // After an abort, of whichever role, copies in flight land before the CTA exits.
+    if (warp == kWarps && st.abort.flag)
+        for (int i = max(0, loaded - kStages); i < loaded; ++i)
+            mbar_wait(&st.full[lane >> 2][i % kStages], uint32_t(i / kStages) & 1u, nullptr, nullptr, a.wait_limit);
     const float g = NV ? (a.g ? __ldg(a.g) : 1.0f) : BF16 ? 1.0f / kSumSize : 1.0f;
     const uint32_t base = smem_u32(xs_base);
     for (int i = krank * kTokThreads + int(threadIdx.x); i < R * 16 * TOK; i += a.ks * kTokThreads) {
