@@ -328,7 +328,7 @@ int gemm_baseline(int variant, int64_t M, int64_t N, int64_t K,
  *   PTC_FP4_MX  blocks of 32, scale 2^(byte - 127), 0xFF: the block is NaN
  *   PTC_FP4_NV  blocks of 16, E4M3 scale, 0x7F: the block is NaN; the whole
  *               matrix is also scaled by a float on the device (NULL: 1),
- *               which must lie in 2^-100 .. 2^100.
+ *               which must lie in 0 .. 2^100.
  * Codes and scales are 16-byte aligned.  (The study has no floating-point
  * 4-bit format; these are the ones the GB300 tensor cores multiply directly.)
  *
@@ -380,7 +380,8 @@ int ptc_dropout_to(int64_t rows, int64_t cols, const void *x, int64_t ldx, int t
  *               stochastic: the next one up where 6 G * scale < amax
  * and codes of x / scale (PTC_FP4_NV: x / rn(scale * G)), the quotient rounded
  * to FP32 and at most 6 in magnitude, rounded to nearest with ties to even, or (PTC_ROUND_STOCHASTIC)
- * up when remainder / gap >= 1 - r / 65536.  A block with an infinity or NaN
+ * up when remainder / gap >= 1 - r / 65536.  Where G or rn(scale * G) is 0 the
+ * codes are 0 (with G = 0 the scales too).  A block with an infinity or NaN
  * becomes NaN (codes 0).  x is aligned to its element.  Outputs must not
  * overlap each other or the inputs.
  */

@@ -489,7 +489,7 @@ class Fp4Matrix:
     scales: contiguous uint8 of ``fp4_scale_bytes(rows, K, fmt)`` bytes in the
         tiled layout of include/ptc.h (:meth:`tile_scales` makes it from rows)
     fmt: "mxfp4" or "nvfp4"; tensor_scale: None, or (nvfp4) a float32 device
-        tensor of one element that scales the whole matrix.
+        tensor of one element, 0 .. 2^100, that scales the whole matrix.
     """
 
     __slots__ = ("_codes", "_scales", "_K", "_fmt", "_ts")
@@ -546,6 +546,8 @@ def quantize_fp4(x, fmt="mxfp4", transposed=False, rounding="nearest", tensor_sc
         x's columns (cols, rows), which a product that contracts over x's rows
         takes; "both" for the pair (one pass over x).
     rounding: "nearest" (ties to even) or "stochastic" (bits from seed, offset).
+    tensor_scale: see :class:`Fp4Matrix`; the largest magnitude / 2688 uses the
+        whole range, and 0 (that of zeros) gives zeros.
     p: with p > 0 the values are ``dropout(x, p, seed, offset)`` in float32.
     """
     how = _ROUNDING.get(rounding)

@@ -189,31 +189,49 @@ __device__ __forceinline__ float quotient(float a, float b, float inverse) {
     return __fmaf_rn(__fmaf_rn(-q, b, a), inverse, q);
 }
 
-// The matrix scale G of an nvfp4 matrix, and 6 G by which blocks' largest
-// magnitudes are divided: both are taken times 2^64 where G is small, which keeps
-// the remainders above FP32's smallest number.  (One division per call of 6 G's
-// reciprocal in place of one per block: 8192 x 8192 bfloat16 both ways 64.0 -> 62.6 us.)
+// The matrix scale G (0 .. 2^100) of an nvfp4 matrix, and 6 G by which blocks' largest
+// magnitudes are divided.  (One division per call of 6 G's reciprocal in place of
+// one per block: 8192 x 8192 bfloat16 both ways 64.0 -> 62.6 us.)
+// Small: G is below 2^-20, and then 6 G, blocks' largest magnitudes, their scales and
+// elements are taken times 2^64 (LIFT below), which keeps remainders above FP32's
+// smallest number and reciprocals of the smallest scales below its largest.  An
+// element that this takes beyond FP32 is far above its block's largest code.  With
+// G = 0 scales and codes are 0.  (Kernels hold the two forms apart: a test per eight
+// elements costs a stochastic call 5%.)
 template <bool NV>
 struct MatrixScale {
-    float g = 1.0f, six = 6.0f, lift = 1.0f, inverse = 0.0f;
+    float g = 1.0f, six = 6.0f, inverse = 0.0f;
+    bool small = false;
     __device__ __forceinline__ explicit MatrixScale(const float *p) {
         if constexpr (NV) {
             if (p != nullptr) g = __ldg(p);
+            small = g < 0x1p-20f;
             six = __fmul_rn(g, 6.0f);
-            lift = g < 0x1p-20f ? 0x1p64f : 1.0f;
-            inverse = __frcp_rn(__fmul_rn(six, lift));
+            inverse = g > 0.0f ? __frcp_rn(small ? __fmul_rn(six, 0x1p64f) : six) : 0.0f;
         }
     }
-    // a / (6 G); at least 2^14 where that is beyond FP32.
+    // a / (6 G), or 0 where G is; at least 2^14 where the quotient is beyond FP32.
+    template <bool LIFT>
     __device__ __forceinline__ float sixths(float a) const {
-        return fminf(quotient(__fmul_rn(a, lift), __fmul_rn(six, lift), inverse), 0x1p14f);
+        if constexpr (LIFT)
+            return six > 0.0f ? fminf(quotient(__fmul_rn(a, 0x1p64f), __fmul_rn(six, 0x1p64f), inverse), 0x1p14f) : 0.0f;
+        return fminf(quotient(a, six, inverse), 0x1p14f);
     }
 };
 
-// A block's scale: the reciprocal it is applied by, and for nvfp4 the scale.
+// A block's scale: the reciprocal it is applied by, and for nvfp4 the scale, both
+// for lifted elements where G is small.
 template <bool NV>
 struct BlockScale {
     float inverse, d;
+    // Eight elements as the other functions take them.
+    template <bool LIFT>
+    __device__ __forceinline__ void lift8(float (&v)[8]) const {
+        if constexpr (LIFT) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = d > 0.0f ? __fmul_rn(v[j], 0x1p64f) : 0.0f;
+        }
+    }
     // x / scale rounded to FP32.  mxfp4 scales are powers of two, so the
     // product is exact.
     __device__ __forceinline__ float apply(float x) const {
@@ -239,7 +257,8 @@ struct BlockScale {
 //                      no element saturates and the rounding has no bias
 //   nvfp4:             amax / (6 G) rounded to E4M3 (stochastic: up to the next
 //                      one where amax would saturate), G the matrix scale
-template <bool NV, bool SR>
+// LIFT: the scale is that of lifted elements.
+template <bool NV, bool SR, bool LIFT>
 __device__ __forceinline__ BlockScale<NV> block_scale(uint32_t amax, const MatrixScale<NV> &g, uint32_t &byte) {
     BlockScale<NV> s{0.0f, 0.0f};
     const bool finite = amax < kInfBits;
@@ -252,11 +271,12 @@ __device__ __forceinline__ BlockScale<NV> block_scale(uint32_t amax, const Matri
     } else {
         const float a = __uint_as_float(amax);
         uint16_t q;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(q) : "f"(0.0f), "f"(g.sixths(a)));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(q) : "f"(0.0f), "f"(g.template sixths<LIFT>(a)));
         uint32_t b = q & 0x7Fu;
         if constexpr (SR)
-            if (__fmul_rn(g.six, scale_value<true>(b)) < a && b < 0x7Eu) ++b;
+            if (__fmul_rn(g.six, scale_value<true>(b)) < a && b < 0x7Eu && !(LIFT && g.six == 0.0f)) ++b;
         s.d = __fmul_rn(scale_value<true>(b), g.g);
+        if constexpr (LIFT) s.d = __fmul_rn(s.d, 0x1p64f);
         byte = finite ? b : 0x7Fu;
         s.inverse = s.d > 0.0f ? __frcp_rn(s.d) : 0.0f;
     }

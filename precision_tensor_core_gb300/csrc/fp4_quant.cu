@@ -39,6 +39,9 @@ struct Walk {
     }
 };
 
+using yes = std::integral_constant<bool, true>;
+using no = std::integral_constant<bool, false>;
+
 struct DropArgs {
     uint32_t kept;  // of 65536; 65536: nothing is dropped
     float scale;    // 65536 / kept
@@ -184,10 +187,12 @@ __device__ __forceinline__ uint32_t scaled_bits(uint32_t m, float scale) {
 }
 
 // Eight codes of values v, whose signs are those of `from`, with the block's scale.
-template <bool NV, bool SR, typename S>
-__device__ __forceinline__ uint32_t codes8(const float (&v)[8], const S &from, uint32_t amax,
-                                           const BlockScale<NV> &scale, const uint4 &bits) {
+// (v is lifted in place.)
+template <bool NV, bool SR, bool LIFT, typename S>
+__device__ __forceinline__ uint32_t codes8(float (&v)[8], const S &from, uint32_t amax, const BlockScale<NV> &scale,
+                                           const uint4 &bits) {
     uint32_t q = 0;
+    scale.template lift8<LIFT>(v);
     if constexpr (SR) {
         uint32_t c[8];
 #pragma unroll
@@ -236,9 +241,10 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *x, const Qu
         }
         const T *const row = x + w.row * a.ldx;
         uint8_t *const code_row = a.codes + w.row * a.pitch;
-        // Whole: 256 U aligned columns that all exist.
-        auto chunk = [&](auto whole) {
-            constexpr bool WHOLE = decltype(whole)::value;
+        // Whole: 256 U aligned columns that all exist.  Lifted:
+        // the matrix scale is small (MatrixScale).
+        auto chunk = [&](auto whole, auto lifted) {
+            constexpr bool WHOLE = decltype(whole)::value, LIFT = decltype(lifted)::value;
             Pack8<T> p[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -267,14 +273,14 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *x, const Qu
                 m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
                 if constexpr (!NV) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
                 uint32_t byte;
-                const BlockScale<NV> scale = block_scale<NV, SR>(m, g, byte);
+                const BlockScale<NV> scale = block_scale<NV, SR, LIFT>(m, g, byte);
                 uint4 bits = make_uint4(0, 0, 0, 0);
                 if constexpr (SR) bits = random_bits8(a.drop.rng, kRngRounding, uint32_t(w.row), uint32_t(c / 8));
                 uint32_t q;
                 if constexpr (DROP)
-                    q = codes8<NV, SR>(v, v, m, scale, bits);
+                    q = codes8<NV, SR, LIFT>(v, v, m, scale, bits);
                 else
-                    q = codes8<NV, SR>(v, p[u], m, scale, bits);
+                    q = codes8<NV, SR, LIFT>(v, p[u], m, scale, bits);
                 if (WHOLE || c < (cols + 31) / 32 * 32) *reinterpret_cast<uint32_t *>(code_row + c / 2) = q;
                 // Four blocks' bytes to one word (held by the first lane of the four).
                 uint32_t word = byte;
@@ -285,10 +291,12 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *x, const Qu
                     *reinterpret_cast<uint32_t *>(scale_row + kt * kScaleTile) = word;
             }
         };
-        if (a.vec != 0 && c0 + 256 * U <= cols)
-            chunk(std::integral_constant<bool, true>());
+        if (NV && __builtin_expect(g.small, 0))
+            chunk(no(), std::integral_constant<bool, NV>());
+        else if (a.vec != 0 && c0 + 256 * U <= cols)
+            chunk(yes(), no());
         else
-            chunk(std::integral_constant<bool, false>());
+            chunk(no(), no());
     }
 }
 
@@ -331,9 +339,9 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const T *x, const Qu
     const int64_t r0 = blockIdx.x / tiles_c * kTileR, c0 = (blockIdx.x % tiles_c) * kTileC;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    // Whole: all rows and columns of the tile exist, and rows are aligned.
-    auto rows_in = [&](auto whole) {
-        constexpr bool WHOLE = decltype(whole)::value;
+    // Whole: all rows and columns of the tile exist, and rows are aligned.  Lifted: as above.
+    auto rows_in = [&](auto whole, auto lifted) {
+        constexpr bool WHOLE = decltype(whole)::value, LIFT = decltype(lifted)::value;
         const int grp = threadIdx.x & 7, lr0 = threadIdx.x >> 3;
         const int rows_left = WHOLE ? kTileR : int(min(int64_t(kTileR), a.rows - r0));
         const int n_cols = WHOLE ? 8 : int(max(int64_t(0), min(int64_t(8), a.cols - c0 - grp * 8)));
@@ -380,8 +388,8 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const T *x, const Qu
                 if constexpr (!NV) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
                 if constexpr (DROP) m = scaled_bits(m, a.drop.scale);
                 uint32_t byte;
-                const BlockScale<NV> scale = block_scale<NV, SR>(m, g, byte);
-                const uint32_t q = codes8<NV, SR>(v, p[i], m, scale, bits);
+                const BlockScale<NV> scale = block_scale<NV, SR, LIFT>(m, g, byte);
+                const uint32_t q = codes8<NV, SR, LIFT>(v, p[i], m, scale, bits);
                 if (exists && code_exists) *reinterpret_cast<uint32_t *>(code + i * code_step) = q;
                 // The row's scale bytes of these 64 columns: a word (nvfp4), or half
                 // of one; a last first half also clears the other.
@@ -404,10 +412,12 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const T *x, const Qu
             }
         }
     };
-    if (a.vec != 0 && r0 + kTileR <= a.rows && c0 + kTileC <= a.cols)
-        rows_in(std::integral_constant<bool, true>());
+    if (NV && __builtin_expect(g.small, 0))
+        rows_in(no(), std::integral_constant<bool, NV>());
+    else if (a.vec != 0 && r0 + kTileR <= a.rows && c0 + kTileC <= a.cols)
+        rows_in(yes(), no());
     else
-        rows_in(std::integral_constant<bool, false>());
+        rows_in(no(), no());
     __syncthreads();
 
     struct alignas(2 * sizeof(T)) Two {
@@ -443,51 +453,60 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const T *x, const Qu
         mb = max(mb, top[(warp ^ 1) * kTileC + 2 * lane + 1]);
     }
     uint32_t ba, bb;
-    const BlockScale<NV> sa = block_scale<NV, SR>(ma, g, ba), sb = block_scale<NV, SR>(mb, g, bb);
     uint32_t qa[2] = {0u, 0u}, qb[2] = {0u, 0u};
+    auto columns = [&](auto lifted) {
+        constexpr bool LIFT = decltype(lifted)::value;
+        const BlockScale<NV> sa = block_scale<NV, SR, LIFT>(ma, g, ba), sb = block_scale<NV, SR, LIFT>(mb, g, bb);
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        float va[8], vb[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            va[j] = to_float(t[8 * w + j].a);
-            vb[j] = to_float(t[8 * w + j].b);
-            if constexpr (DROP) {
-                va[j] = __fmul_rn(va[j], a.drop.scale);
-                vb[j] = __fmul_rn(vb[j], a.drop.scale);
-            }
-        }
-        if constexpr (SR) {
-            uint32_t ca[8], cb[8];
+        for (int w = 0; w < 2; ++w) {
+            float va[8], vb[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const uint32_t r = *reinterpret_cast<const uint32_t *>(rs + (16 * warp + 8 * w + j) * kTileC + 2 * lane);
-                ca[j] = code_stochastic(sa.magnitude(va[j]), low_r8(r));
-                cb[j] = code_stochastic(sb.magnitude(vb[j]), high_r8(r));
+                va[j] = to_float(t[8 * w + j].a);
+                vb[j] = to_float(t[8 * w + j].b);
+                if constexpr (DROP) {
+                    va[j] = __fmul_rn(va[j], a.drop.scale);
+                    vb[j] = __fmul_rn(vb[j], a.drop.scale);
+                }
             }
-            Signs8 na, nb;
-            if constexpr (sizeof(T) == 2) {
-                auto word = [&](int j) { return reinterpret_cast<const uint32_t &>(t[8 * w + j]); };
-                half_signs(word(0), word(2), word(4), word(6), na.even, nb.even);
-                half_signs(word(1), word(3), word(5), word(7), na.odd, nb.odd);
+            sa.template lift8<LIFT>(va);
+            sb.template lift8<LIFT>(vb);
+            if constexpr (SR) {
+                uint32_t ca[8], cb[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t r = *reinterpret_cast<const uint32_t *>(rs + (16 * warp + 8 * w + j) * kTileC + 2 * lane);
+                    ca[j] = code_stochastic(sa.magnitude(va[j]), low_r8(r));
+                    cb[j] = code_stochastic(sb.magnitude(vb[j]), high_r8(r));
+                }
+                Signs8 na, nb;
+                if constexpr (sizeof(T) == 2) {
+                    auto word = [&](int j) { return reinterpret_cast<const uint32_t &>(t[8 * w + j]); };
+                    half_signs(word(0), word(2), word(4), word(6), na.even, nb.even);
+                    half_signs(word(1), word(3), word(5), word(7), na.odd, nb.odd);
+                } else {
+                    na = signs8(va);
+                    nb = signs8(vb);
+                }
+                qa[w] = pack_stochastic(ca, na);
+                qb[w] = pack_stochastic(cb, nb);
             } else {
-                na = signs8(va);
-                nb = signs8(vb);
-            }
-            qa[w] = pack_stochastic(ca, na);
-            qb[w] = pack_stochastic(cb, nb);
-        } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                va[j] = sa.apply(va[j]);
-                vb[j] = sb.apply(vb[j]);
+                for (int j = 0; j < 8; ++j) {
+                    va[j] = sa.apply(va[j]);
+                    vb[j] = sb.apply(vb[j]);
+                }
+                qa[w] = codes_nearest(va);
+                qb[w] = codes_nearest(vb);
             }
-            qa[w] = codes_nearest(va);
-            qb[w] = codes_nearest(vb);
+            qa[w] = ma < kInfBits ? qa[w] : 0u;
+            qb[w] = mb < kInfBits ? qb[w] : 0u;
         }
-        qa[w] = ma < kInfBits ? qa[w] : 0u;
-        qb[w] = mb < kInfBits ? qb[w] : 0u;
-    }
+    };
+    if (NV && __builtin_expect(g.small, 0))
+        columns(std::integral_constant<bool, NV>());
+    else
+        columns(no());
     *reinterpret_cast<uint2 *>(ct + (2 * lane) * kCodePitch + 8 * warp) = make_uint2(qa[0], qa[1]);
     *reinterpret_cast<uint2 *>(ct + (2 * lane + 1) * kCodePitch + 8 * warp) = make_uint2(qb[0], qb[1]);
     if (NV || (warp & 1) == 0) {
@@ -690,8 +709,6 @@ cudaError_t run_quantize(const void *x, const QuantArgs &a, bool nv, bool sr, in
         return drop ? launch_quantize<T, decltype(n)::value, decltype(r)::value, true>(p, a, sms, s)
                     : launch_quantize<T, decltype(n)::value, decltype(r)::value, false>(p, a, sms, s);
     };
-    using yes = std::integral_constant<bool, true>;
-    using no = std::integral_constant<bool, false>;
     if (nv) return sr ? go(yes(), yes()) : go(yes(), no());
     return sr ? go(no(), yes()) : go(no(), no());
 }
