@@ -18,6 +18,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "fp4.h"
 #include "internal.h"
 #include "ptc.h"
 

@@ -44,6 +44,7 @@
 #include <cstring>
 
 #include "fp4.cuh"
+#include "fp4.h"
 #include "internal.h"
 #include "ptc.h"
 #include "ptx.cuh"

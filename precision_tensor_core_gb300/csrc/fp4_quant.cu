@@ -11,6 +11,7 @@
 #include <type_traits>
 
 #include "fp4.cuh"
+#include "fp4.h"
 #include "internal.h"
 #include "ptc.h"
 #include "ptx.cuh"
