@@ -452,7 +452,8 @@ _HOST_FN.update({gemm_f16: gemm_f16_host, gemm_s8: gemm_s8_host, gemm_s4: gemm_s
 # handle) a call runs as under torch.cuda.stream(stream): it is ordered after that
 # stream's work alone, so the caller waits for its inputs and for the result.
 # The tensors' memory needs no such care: results come from that stream's, and
-# inputs and results may be released while it runs.
+# inputs and results may be released while it runs.  The operators are outside
+# autograd: a tensor that requires grad is refused unless gradients are off.
 _FP4 = {"mxfp4": (PTC_FP4_MX, 32), "nvfp4": (PTC_FP4_NV, 16)}
 _ROUNDING = {"nearest": PTC_ROUND_NEAREST, "stochastic": PTC_ROUND_STOCHASTIC}
 _native = None
@@ -533,7 +534,8 @@ def dropout(x, p, seed, offset=0, residual=None, out=None, stream=None, out_dtyp
     that the expectation is x's), plus ``residual`` if given; float32, bfloat16
     or float16 (rows, cols).  The mask is a function of (seed, offset, row,
     column) and is never stored: the backward pass is the same call on the
-    gradient.  ``out`` may be ``x`` or ``residual``.  ``out_dtype`` is x's dtype;
+    gradient (made by the caller: autograd does not see this call, and ``x`` must
+    not require grad while gradients are on).  ``out`` may be ``x`` or ``residual``.  ``out_dtype`` is x's dtype;
     float32 x without a residual may also give bfloat16 or float16, rounded once."""
     return (_native or _load_native()).dropout(x, p, seed, offset, residual, out, stream, out_dtype)
 

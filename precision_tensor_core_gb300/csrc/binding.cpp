@@ -9,6 +9,7 @@
 
 #include <ATen/Functions.h>
 #include <c10/cuda/CUDAGuard.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <algorithm>
@@ -56,6 +57,18 @@ const at::Tensor &tensor(PyObject *o, const char *name) {
         throw Bad();
     }
     return THPVariable_Unpack(o);
+}
+
+// The operators are outside autograd: a gradient is not lost without an error.
+const at::Tensor &outside_autograd(const at::Tensor &t, const char *name) {
+    if (t.requires_grad() && c10::GradMode::is_enabled()) {
+        PyErr_Format(PyExc_RuntimeError,
+                     "%s requires grad, and this operator gives no gradient: call it under torch.no_grad() or on a "
+                     "detached tensor, with the backward pass written out (as fp4_linear does)",
+                     name);
+        throw Bad();
+    }
+    return t;
 }
 
 int64_t integer(PyObject *o) {
@@ -254,7 +267,7 @@ class Target {
 // The result tensor: `out`, or a new one.
 at::Tensor result(PyObject *out, int64_t rows, int64_t cols, at::ScalarType type, c10::DeviceIndex index, at::Device device) {
     if (out == Py_None) return empty({rows, cols}, type, device);
-    const at::Tensor &t = tensor(out, "out");
+    const at::Tensor &t = outside_autograd(tensor(out, "out"), "out");
     if (t.dim() != 2 || t.size(0) != rows || t.size(1) != cols || !t.is_cuda() || t.get_device() != index)
         raise(PyExc_ValueError, "out must have the result's shape and device");
     return t;
@@ -263,6 +276,7 @@ at::Tensor result(PyObject *out, int64_t rows, int64_t cols, at::ScalarType type
 PyObject *give(const Target &target, PyObject *out, at::Tensor t) {
     if (out != Py_None) {
         target.used(out);
+        if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();  // (written in place)
         Py_INCREF(out);
         return out;
     }
@@ -288,7 +302,7 @@ void expect(Py_ssize_t n, Py_ssize_t want) {
 PyObject *py_dropout(PyObject *, PyObject *const *a, Py_ssize_t n) {
     PTC_BODY_BEGIN
     expect(n, 8);
-    const at::Tensor &x = tensor(a[0], "x");
+    const at::Tensor &x = outside_autograd(tensor(a[0], "x"), "x");
     const int type = type_of(x.scalar_type());
     const at::ScalarType st = a[7] == Py_None ? x.scalar_type() : dtype_of(a[7]);
     const int out_type = type_of(st);
@@ -302,7 +316,7 @@ PyObject *py_dropout(PyObject *, PyObject *const *a, Py_ssize_t n) {
     };
     Rows rr{nullptr, 0, 0, 0};
     if (a[4] != Py_None) {
-        const at::Tensor &r = tensor(a[4], "residual");
+        const at::Tensor &r = outside_autograd(tensor(a[4], "residual"), "residual");
         like(r, "residual");
         rr = rows_of(r, "residual");
     }
@@ -326,7 +340,7 @@ PyObject *py_quantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
     PTC_BODY_BEGIN
     expect(n, 9);
     const int fmt = format_of(a[1]);
-    const at::Tensor &x = tensor(a[0], "x");
+    const at::Tensor &x = outside_autograd(tensor(a[0], "x"), "x");
     const int type = type_of(x.scalar_type());
     const Rows rx = rows_of(x, "x");
     const c10::DeviceIndex index = x.get_device();
@@ -414,7 +428,7 @@ PyObject *py_matmul(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *py_matmul_a16(PyObject *, PyObject *const *a, Py_ssize_t n) {
     PTC_BODY_BEGIN
     expect(n, 4);
-    const at::Tensor &x = tensor(a[0], "x");
+    const at::Tensor &x = outside_autograd(tensor(a[0], "x"), "x");
     const int type = type_of(x.scalar_type());
     if (type == PTC_OUT_F32) raise(PyExc_TypeError, "matmul_a16_fp4 takes bfloat16 or float16 activations");
     const Rows rx = rows_of(x, "x");

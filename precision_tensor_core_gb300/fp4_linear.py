@@ -13,7 +13,8 @@ contract over different axes:
 x and W are rounded to nearest, dy stochastically, so that the rounding of the
 gradients has no bias.  decode() is the serving form of a few tokens: 16-bit
 activations with the 4-bit weights, read once.  The master weights stay with
-the caller.
+the caller.  Both passes are explicit and outside autograd: forward() and
+backward() take tensors that require grad as they are, and their results do not.
 """
 from __future__ import annotations
 
@@ -27,9 +28,11 @@ FORMAT = "mxfp4"
 def forward(x, w, p=0.0, seed=0, offset=0):
     """y (tokens, outputs) of x (tokens, inputs) and w (outputs, inputs), and what
     backward() needs."""
-    xq, xqt = quantize_fp4(x, FORMAT, transposed="both", p=p, seed=seed, offset=offset)
-    wq, wqt = quantize_fp4(w, FORMAT, transposed="both")
-    y = matmul_fp4(xq, wq, out_dtype=x.dtype)
+    import torch
+    with torch.no_grad():
+        xq, xqt = quantize_fp4(x, FORMAT, transposed="both", p=p, seed=seed, offset=offset)
+        wq, wqt = quantize_fp4(w, FORMAT, transposed="both")
+        y = matmul_fp4(xq, wq, out_dtype=x.dtype)
     return y, (xqt, wqt, p, seed, offset)
 
 
@@ -39,7 +42,8 @@ def backward(dy, saved):
     their own."""
     import torch
     xqt, wqt, p, seed, offset = saved
-    dyq, dyqt = quantize_fp4(dy, FORMAT, transposed="both", rounding="stochastic", seed=seed, offset=offset)
+    with torch.no_grad():
+        dyq, dyqt = quantize_fp4(dy, FORMAT, transposed="both", rounding="stochastic", seed=seed, offset=offset)
     if p > 0.0:  # (the product stays in FP32, so that dx is rounded once)
         dx = dropout(matmul_fp4(dyq, wqt, out_dtype=torch.float32), p, seed, offset, out_dtype=dy.dtype)
     else:
