@@ -166,7 +166,8 @@ Matrix matrix(PyObject *codes, PyObject *scales, PyObject *k, PyObject *fmt, PyO
     m.rows = r.rows;
     // (One row, or rows of no values, have no pitch.)
     m.pitch = r.rows > 1 && m.k > 0 ? r.ld : std::max<int64_t>(16, (r.cols + 15) / 16 * 16);
-    if (m.k < 0 || r.cols < (m.k + 31) / 32 * 16 || m.pitch % 16)
+    if (m.k < 0 || m.k > (int64_t(1) << 30)) raise(PyExc_ValueError, "K must be 0 .. 2^30");
+    if (r.cols < (m.k + 31) / 32 * 16 || m.pitch % 16)
         raise(PyExc_ValueError, "codes must hold 16 * ceil(K / 32) bytes per row, rows a multiple of 16 bytes apart");
     if (!s.is_cuda() || !s.is_contiguous() || s.numel() < scale_bytes(m.rows, m.k, m.fmt))
         raise(PyExc_ValueError, "scales must be contiguous and hold whole tiles of 128 rows x 4 blocks");

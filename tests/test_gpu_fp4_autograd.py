@@ -73,3 +73,10 @@ def test_the_linear_layer_takes_parameters():
     got = (y, *fp4_linear.backward(dy.clone().requires_grad_(), saved))
     for a, b in zip(got, want):
         assert torch.equal(a, b) and not a.requires_grad
+
+
+def test_a_matrix_of_more_values_than_any_call_takes_is_refused():
+    q = ptc.quantize_fp4(torch.ones(4, 64, device=DEV))
+    for K in (2 ** 30 + 1, 2 ** 62, 2 ** 63 - 1):
+        with pytest.raises(ValueError):
+            ptc.Fp4Matrix(q.codes, q.scales, K)
