@@ -332,6 +332,9 @@ int gemm_baseline(int variant, int64_t M, int64_t N, int64_t K,
  * Codes and scales are 16-byte aligned.  (The study has no floating-point
  * 4-bit format; these are the ones the GB300 tensor cores multiply directly.)
  *
+ * An output of the calls below must share no byte with an input (or another output);
+ * column slices of one buffer, whose rows lie side by side at one pitch, do not.
+ *
  * Random numbers: element (row, column) of a call with `seed` and `offset`
  * (below 2^63) has 16 bits of Philox4x32-10 (Salmon et al., "Parallel random
  * numbers: as easy as 1, 2, 3", SC 2011) with key = seed and counter (column / 8,

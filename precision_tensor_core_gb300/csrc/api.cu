@@ -470,8 +470,20 @@ int usable_device(int *sms) {
 bool pdl_enabled() { return g_pdl.load() != 0; }
 uint64_t wait_limit_ns() { return g_wait_ns.load(); }
 int take_stall_tile() { return int(g_stall_tile.exchange(-1)); }
-uint64_t span_of(int64_t rows, int64_t cols, int64_t ld, int esize) { return span_bytes(rows, cols, ld, esize, 1); }
-bool ranges_overlap(const void *a, uint64_t alen, const void *b, uint64_t blen) { return overlaps(a, alen, b, blen); }
+bool rows_overlap(const ByteRows &a, const ByteRows &b) {
+    if (!a.p || !b.p || a.rows < 1 || b.rows < 1 || !a.width || !b.width) return false;
+    using wide = unsigned __int128;
+    auto first = [](const ByteRows &r) { return wide(reinterpret_cast<uintptr_t>(r.p)); };
+    auto last = [&](const ByteRows &r) { return first(r) + wide(uint64_t(r.rows) - 1) * r.pitch + r.width; };
+    if (first(a) >= last(b) || first(b) >= last(a)) return false;
+    // A single row has any pitch that holds it.
+    uint64_t pitch = a.rows > 1 ? a.pitch : b.pitch;
+    if ((a.rows > 1 && b.rows > 1 && a.pitch != b.pitch) || a.width > pitch || b.width > pitch) return true;
+    // b's rows start `from` bytes into a's pitch.
+    const uint64_t from = first(b) >= first(a) ? uint64_t((first(b) - first(a)) % pitch)
+                                               : uint64_t((pitch - (first(a) - first(b)) % pitch) % pitch);
+    return from < a.width || from + b.width > pitch;
+}
 }  // namespace ptc
 
 namespace {

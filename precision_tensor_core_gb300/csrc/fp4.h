@@ -25,16 +25,28 @@ int usable_device(int *sms);
 bool pdl_enabled();
 uint64_t wait_limit_ns();
 int take_stall_tile();
-// Bytes spanned by `rows` rows of `cols` elements of `esize` bytes, `ld`
-// elements apart (saturating), and whether two byte ranges intersect.
-uint64_t span_of(int64_t rows, int64_t cols, int64_t ld, int esize);
-bool ranges_overlap(const void *a, uint64_t alen, const void *b, uint64_t blen);
+// Rows of `width` bytes, `pitch` bytes apart; what each argument of a call reads or
+// writes.  Two of them with one pitch that lie side by side in one buffer share no
+// byte although their spans intersect.
+struct ByteRows {
+    const void *p;  // NULL: none
+    int64_t rows;
+    uint64_t width, pitch;
+};
+// Whether they share a byte (for different pitches: whether their spans intersect).
+bool rows_overlap(const ByteRows &a, const ByteRows &b);
 
-// 4-bit matrices (fp4_quant.cu): bytes of the tiled scales and of the codes
-// of `rows` rows of `cols` values, and the argument checks of one.
-uint64_t fp4_scale_bytes(int64_t rows, int64_t cols, bool nv);
-uint64_t fp4_code_span(int64_t rows, int64_t cols, int64_t pitch);
-int check_fp4(const void *codes, int64_t pitch, const void *scales, const void *g, int64_t rows, int64_t cols, bool nv);
+// `rows` rows of `cols` elements of `esize` bytes, `ld` elements apart.
+inline ByteRows elem_rows(const void *p, int64_t rows, int64_t cols, int64_t ld, int esize) {
+    return {p, rows, uint64_t(cols) * uint64_t(esize), uint64_t(ld) * uint64_t(esize)};
+}
+inline ByteRows flat_bytes(const void *p, uint64_t n) { return {p, 1, n, n}; }
+
+// 4-bit matrices of `rows` rows of `cols` values (fp4_quant.cu): the bytes of the
+// codes and of the tiled scales, and the argument checks of one.
+ByteRows fp4_code_rows(const void *codes, int64_t rows, int64_t cols, int64_t pitch);
+ByteRows fp4_scale_rows(const void *scales, int64_t rows, int64_t cols, bool nv);
+int check_fp4(const void *codes, int64_t pitch, const void *scales, const void *g, int64_t cols, bool nv);
 
 // The 4-bit products' error words (fp4_gemm.cu, fp4_tokens.cu), read and cleared.
 cudaError_t read_and_clear_fp4_error_word(uint32_t *out);

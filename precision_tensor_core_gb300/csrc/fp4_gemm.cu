@@ -708,13 +708,12 @@ extern "C" int gemm_fp4(int64_t M, int64_t N, int64_t K, int format, const void 
     const int es = out_type == PTC_OUT_F32 ? 4 : 2;
     if (!C || ldc < N || ldc > kMaxLd4) return fail_status(PTC_ERR_INVALID, "C is NULL, or ldc is not N .. 2^36");
     int rc;
-    if (K > 0 && ((rc = check_fp4(A, lda, SA, GA, M, K, nv)) || (rc = check_fp4(B, ldb, SB, GB, N, K, nv)))) return rc;
+    if (K > 0 && ((rc = check_fp4(A, lda, SA, GA, K, nv)) || (rc = check_fp4(B, ldb, SB, GB, K, nv)))) return rc;
     if (reinterpret_cast<uintptr_t>(C) % es) return fail_status(PTC_ERR_ALIGN, "C must be aligned to its element");
-    const uint64_t cb = span_of(M, N, ldc, es);
-    if (K > 0 && (ranges_overlap(C, cb, A, fp4_code_span(M, K, lda)) || ranges_overlap(C, cb, B, fp4_code_span(N, K, ldb)) ||
-                  ranges_overlap(C, cb, SA, fp4_scale_bytes(M, K, nv)) ||
-                  ranges_overlap(C, cb, SB, fp4_scale_bytes(N, K, nv)) || (GA && ranges_overlap(C, cb, GA, 4)) ||
-                  (GB && ranges_overlap(C, cb, GB, 4))))
+    const ByteRows c = elem_rows(C, M, N, ldc, es);
+    if (K > 0 && (rows_overlap(c, fp4_code_rows(A, M, K, lda)) || rows_overlap(c, fp4_code_rows(B, N, K, ldb)) ||
+                  rows_overlap(c, fp4_scale_rows(SA, M, K, nv)) || rows_overlap(c, fp4_scale_rows(SB, N, K, nv)) ||
+                  rows_overlap(c, flat_bytes(GA, 4)) || rows_overlap(c, flat_bytes(GB, 4))))
         return fail_status(PTC_ERR_OVERLAP, "C overlaps an operand");
     int sms;
     if ((rc = usable_device(&sms))) return rc;

@@ -6,6 +6,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <cstring>
 #include <type_traits>
@@ -716,14 +717,17 @@ cudaError_t run_quantize(const void *x, const QuantArgs &a, bool nv, bool sr, in
 
 }  // namespace
 
-// Bytes of a matrix's tiled scales.
-uint64_t fp4_scale_bytes(int64_t rows, int64_t cols, bool nv) {
+ByteRows fp4_scale_rows(const void *scales, int64_t rows, int64_t cols, bool nv) {
     const int64_t block = nv ? 16 : 32, blocks = (cols + block - 1) / block;
-    return uint64_t((rows + 127) / 128) * uint64_t((blocks + 3) / 4) * kScaleTile;
+    return flat_bytes(scales, uint64_t((rows + 127) / 128) * uint64_t((blocks + 3) / 4) * kScaleTile);
 }
 
-// Checks of a 4-bit matrix of `rows` rows of `cols` values.
-int check_fp4(const void *codes, int64_t pitch, const void *scales, const void *g, int64_t rows, int64_t cols, bool nv) {
+ByteRows fp4_code_rows(const void *codes, int64_t rows, int64_t cols, int64_t pitch) {
+    return elem_rows(codes, rows, (cols + 31) / 32 * 16, pitch, 1);
+}
+
+// Checks of a 4-bit matrix with rows of `cols` values.
+int check_fp4(const void *codes, int64_t pitch, const void *scales, const void *g, int64_t cols, bool nv) {
     if (!codes || !scales) return fail_status(PTC_ERR_INVALID, "codes or scales is NULL");
     if (pitch < (cols + 31) / 32 * 16 || pitch > kMaxLd)
         return fail_status(PTC_ERR_INVALID, "the code pitch must hold whole 32-element blocks (16 bytes each)");
@@ -731,12 +735,7 @@ int check_fp4(const void *codes, int64_t pitch, const void *scales, const void *
     if (!multiple_of(codes, 16) || !multiple_of(scales, 16) || pitch % 16)
         return fail_status(PTC_ERR_ALIGN, "codes, scales must be 16-byte aligned with a code pitch that is a multiple of 16");
     if (g && !multiple_of(g, 4)) return fail_status(PTC_ERR_ALIGN, "matrix scales must be 4-byte aligned");
-    (void)rows;
     return PTC_OK;
-}
-
-uint64_t fp4_code_span(int64_t rows, int64_t cols, int64_t pitch) {
-    return span_of(rows, (cols + 31) / 32 * 16, pitch, 1);
 }
 
 }  // namespace ptc
@@ -762,10 +761,10 @@ int ptc_dropout_to(int64_t rows, int64_t cols, const void *x, int64_t ldx, int t
     const int es = elem_bytes(type), os = elem_bytes(out_type);
     if (!multiple_of(x, es) || !multiple_of(y, os) || (residual && !multiple_of(residual, os)))
         return fail_status(PTC_ERR_ALIGN, "pointers must be aligned to the element");
-    const uint64_t ybytes = span_of(rows, cols, ldy, os);
-    if ((y != x || ldy != ldx || out_type != type) && ranges_overlap(y, ybytes, x, span_of(rows, cols, ldx, es)))
+    const ByteRows yr = elem_rows(y, rows, cols, ldy, os);
+    if ((y != x || ldy != ldx || out_type != type) && rows_overlap(yr, elem_rows(x, rows, cols, ldx, es)))
         return fail_status(PTC_ERR_OVERLAP, "y overlaps x without being x");
-    if (residual && (y != residual || ldy != ldr) && ranges_overlap(y, ybytes, residual, span_of(rows, cols, ldr, os)))
+    if (residual && (y != residual || ldy != ldr) && rows_overlap(yr, elem_rows(residual, rows, cols, ldr, os)))
         return fail_status(PTC_ERR_OVERLAP, "y overlaps the residual without being it");
     int sms;
     if ((rc = usable_device(&sms))) return rc;
@@ -802,24 +801,18 @@ int ptc_quantize_fp4(int64_t rows, int64_t cols, const void *x, int64_t ldx, int
     if (ldx < cols || ldx > kMaxLd) return fail_status(PTC_ERR_INVALID, "ldx must be cols .. 2^36");
     const bool nv = format == PTC_FP4_NV;
     const int es = elem_bytes(type);
-    if (codes && (rc = check_fp4(codes, pitch, scales, matrix_scale, rows, cols, nv))) return rc;
-    if (codes_t && (rc = check_fp4(codes_t, pitch_t, scales_t, matrix_scale, cols, rows, nv))) return rc;
+    if (codes && (rc = check_fp4(codes, pitch, scales, matrix_scale, cols, nv))) return rc;
+    if (codes_t && (rc = check_fp4(codes_t, pitch_t, scales_t, matrix_scale, rows, nv))) return rc;
     if (!multiple_of(x, es)) return fail_status(PTC_ERR_ALIGN, "x must be aligned to its element");
-    struct Range {
-        const void *p;
-        uint64_t n;
-        bool out;
-    };
-    const Range r[6] = {{x, span_of(rows, cols, ldx, es), false},
-                        {matrix_scale, matrix_scale ? 4u : 0u, false},
-                        {codes, codes ? fp4_code_span(rows, cols, pitch) : 0, true},
-                        {codes ? scales : nullptr, codes ? fp4_scale_bytes(rows, cols, nv) : 0, true},
-                        {codes_t, codes_t ? fp4_code_span(cols, rows, pitch_t) : 0, true},
-                        {codes_t ? scales_t : nullptr, codes_t ? fp4_scale_bytes(cols, rows, nv) : 0, true}};
+    const ByteRows r[6] = {elem_rows(x, rows, cols, ldx, es),
+                           flat_bytes(matrix_scale, 4),
+                           fp4_code_rows(codes, rows, cols, pitch),
+                           fp4_scale_rows(codes ? scales : nullptr, rows, cols, nv),
+                           fp4_code_rows(codes_t, cols, rows, pitch_t),
+                           fp4_scale_rows(codes_t ? scales_t : nullptr, cols, rows, nv)};
     for (int i = 0; i < 6; ++i)
-        for (int j = i + 1; j < 6; ++j)
-            if (r[i].n && r[j].n && r[j].out && ranges_overlap(r[i].p, r[i].n, r[j].p, r[j].n))
-                return fail_status(PTC_ERR_OVERLAP, "an output overlaps another argument");
+        for (int j = std::max(i + 1, 2); j < 6; ++j)  // (the outputs)
+            if (rows_overlap(r[i], r[j])) return fail_status(PTC_ERR_OVERLAP, "an output overlaps another argument");
     int sms;
     if ((rc = usable_device(&sms))) return rc;
     QuantArgs a;
@@ -855,14 +848,13 @@ int ptc_dequantize_fp4(int64_t rows, int64_t cols, const void *codes, int64_t pi
     const bool nv = format == PTC_FP4_NV;
     if (!y) return fail_status(PTC_ERR_INVALID, "y is NULL");
     if (ldy < cols || ldy > kMaxLd) return fail_status(PTC_ERR_INVALID, "ldy must be cols .. 2^36");
-    int rc = check_fp4(codes, pitch, scales, matrix_scale, rows, cols, nv);
+    int rc = check_fp4(codes, pitch, scales, matrix_scale, cols, nv);
     if (rc) return rc;
     const int es = elem_bytes(type);
     if (!multiple_of(y, es)) return fail_status(PTC_ERR_ALIGN, "y must be aligned to its element");
-    const uint64_t yb = span_of(rows, cols, ldy, es);
-    if (ranges_overlap(y, yb, codes, fp4_code_span(rows, cols, pitch)) ||
-        ranges_overlap(y, yb, scales, fp4_scale_bytes(rows, cols, nv)) ||
-        (matrix_scale && ranges_overlap(y, yb, matrix_scale, 4)))
+    const ByteRows yr = elem_rows(y, rows, cols, ldy, es);
+    if (rows_overlap(yr, fp4_code_rows(codes, rows, cols, pitch)) || rows_overlap(yr, fp4_scale_rows(scales, rows, cols, nv)) ||
+        rows_overlap(yr, flat_bytes(matrix_scale, 4)))
         return fail_status(PTC_ERR_OVERLAP, "y overlaps an input");
     int sms;
     if ((rc = usable_device(&sms))) return rc;

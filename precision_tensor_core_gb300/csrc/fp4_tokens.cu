@@ -601,12 +601,12 @@ extern "C" int gemm_a16_fp4(int64_t M, int64_t N, int64_t K, int type, const voi
     if (K > 0 && (!X || ldx < K || ldx > kMaxLdT))
         return fail_status(PTC_ERR_INVALID, "X is NULL, or ldx is not K .. 2^36");
     int rc;
-    if (K > 0 && (rc = check_fp4(W, ldw, SW, GW, N, K, nv))) return rc;
+    if (K > 0 && (rc = check_fp4(W, ldw, SW, GW, K, nv))) return rc;
     if (reinterpret_cast<uintptr_t>(C) % 2 || (K > 0 && reinterpret_cast<uintptr_t>(X) % 2))
         return fail_status(PTC_ERR_ALIGN, "X and C must be aligned to their elements");
-    const uint64_t cb = span_of(M, N, ldc, 2);
-    if (K > 0 && (ranges_overlap(C, cb, X, span_of(M, K, ldx, 2)) || ranges_overlap(C, cb, W, fp4_code_span(N, K, ldw)) ||
-                  ranges_overlap(C, cb, SW, fp4_scale_bytes(N, K, nv)) || (GW && ranges_overlap(C, cb, GW, 4))))
+    const ByteRows c = elem_rows(C, M, N, ldc, 2);
+    if (K > 0 && (rows_overlap(c, elem_rows(X, M, K, ldx, 2)) || rows_overlap(c, fp4_code_rows(W, N, K, ldw)) ||
+                  rows_overlap(c, fp4_scale_rows(SW, N, K, nv)) || rows_overlap(c, flat_bytes(GW, 4))))
         return fail_status(PTC_ERR_OVERLAP, "C overlaps an operand");
     int sms;
     if ((rc = usable_device(&sms))) return rc;
