@@ -6,7 +6,8 @@ runtime linked statically (the driver API is reached at run time through the
 runtime's entry-point query, so the library loads on machines without a GPU
 driver).  ptxas register/shared-memory reports go to ``_build/ptxas.log``.
 Beside it ``_native.so``, the CPython module of the 4-bit operators' tensor layer
-(csrc/binding.cpp), compiles with g++ against the installed torch's headers.
+(csrc/binding.cpp), compiles with g++ against the installed torch's headers; without
+torch only the library is built, for users of its C ABI.
 """
 from __future__ import annotations
 
@@ -44,14 +45,16 @@ def _compile(src: str) -> tuple[str, str]:
     return obj, r.stderr
 
 
-def _compile_binding() -> None:
-    """_native.so, against the torch that `import torch` would load (not imported here)."""
+def _torch_dir() -> str | None:
+    """Where the torch that `import torch` would load lives (not imported here)."""
     import importlib.util
-    import sysconfig
     spec = importlib.util.find_spec("torch")
-    if spec is None or spec.origin is None:
-        raise RuntimeError("torch is not installed; the tensor layer of the 4-bit operators needs its headers")
-    torch = os.path.dirname(spec.origin)
+    return None if spec is None or spec.origin is None else os.path.dirname(spec.origin)
+
+
+def _compile_binding(torch: str) -> None:
+    """_native.so, against the torch in that directory."""
+    import sysconfig
     cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
     tmp = NATIVE + f".tmp{os.getpid()}"
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-I", INCLUDE, "-I", os.path.join(torch, "include"),
@@ -66,9 +69,10 @@ def _compile_binding() -> None:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(NATIVE):
+    made = [LIB, NATIVE] if _torch_dir() else [LIB]
+    if not all(os.path.exists(m) for m in made):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(NATIVE))
+    t = min(os.path.getmtime(m) for m in made)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "ptc.h"), __file__]
     return any(os.path.getmtime(d) > t for d in deps)
 
@@ -78,9 +82,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding)
+        torch = _torch_dir()
+        binding = ex.submit(_compile_binding, torch) if torch else None
         results = list(ex.map(_compile, SOURCES))
-        binding.result()
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         for (obj, log), src in zip(results, SOURCES):
             f.write(f"== {src}\n{log}\n")
@@ -90,6 +94,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}\n{r.stdout}")
     os.replace(tmp, LIB)
+    if binding is not None:
+        binding.result()  # (its errors come after the library, which does not need it)
     if verbose:
         sys.stdout.write(open(os.path.join(BUILD, "ptxas.log")).read())
     return LIB
