@@ -326,7 +326,7 @@ int gemm_baseline(int variant, int64_t M, int64_t N, int64_t K,
  *           The buffer holds whole tiles.  The bytes of blocks past K must not
  *           be NaN; those of rows past R may hold anything.
  *   PTC_FP4_MX  blocks of 32, scale 2^(byte - 127), 0xFF: the block is NaN
- *   PTC_FP4_NV  blocks of 16, E4M3 scale, 0x7F: the block is NaN; the whole
+ *   PTC_FP4_NV  blocks of 16, E4M3 scale (its sign bit clear), 0x7F: the block is NaN; the whole
  *               matrix is also scaled by a float on the device (NULL: 1),
  *               which must lie in 0 .. 2^100.
  * Codes and scales are 16-byte aligned.  (The study has no floating-point
@@ -375,7 +375,9 @@ int ptc_dropout_to(int64_t rows, int64_t cols, const void *x, int64_t ldx, int t
  * microscaled 4-bit matrix: of its rows (codes, pitch, scales: rows x cols),
  * of its columns (codes_t, pitch_t, scales_t: cols x rows, blocks along the
  * rows of x), or both in one pass; a NULL codes pointer leaves that one out.
- * With p > 0 the values are those of ptc_dropout(x) in FP32.
+ * With p > 0 the values are those of ptc_dropout(x) in FP32: kept ones are
+ * 65536 / T times x, and a matrix scale made from x's largest magnitude has to be
+ * taken times that too, or the largest blocks saturate.
  *   PTC_FP4_MX  scale 2^(floor(log2 amax) - 2), amax the block's largest
  *               magnitude; stochastic: the least power of two with
  *               amax <= 6 * scale
@@ -383,7 +385,8 @@ int ptc_dropout_to(int64_t rows, int64_t cols, const void *x, int64_t ldx, int t
  *               stochastic: the next one up where 6 G * scale < amax
  * and codes of x / scale (PTC_FP4_NV: x / rn(scale * G)), the quotient rounded
  * to FP32 and at most 6 in magnitude, rounded to nearest with ties to even, or (PTC_ROUND_STOCHASTIC)
- * up when remainder / gap >= 1 - r / 65536.  Where G or rn(scale * G) is 0 the
+ * up when remainder / gap >= 1 - r / 65536, which has the value as its mean down to
+ * 2^-16 of a gap (by which it may be too small).  Where G or rn(scale * G) is 0 the
  * codes are 0 (with G = 0 the scales too).  A block with an infinity or NaN
  * becomes NaN (codes 0).  x is aligned to its element.  Outputs must not
  * overlap each other or the inputs.

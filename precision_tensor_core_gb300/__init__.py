@@ -547,9 +547,12 @@ def quantize_fp4(x, fmt="mxfp4", transposed=False, rounding="nearest", tensor_sc
     transposed: False for blocks along the rows of x; True for the matrix of
         x's columns (cols, rows), which a product that contracts over x's rows
         takes; "both" for the pair (one pass over x).
-    rounding: "nearest" (ties to even) or "stochastic" (bits from seed, offset).
+    rounding: "nearest" (ties to even) or "stochastic" (16 bits per element from seed
+        and offset: the mean is the value, down to 2^-16 of the gap between codes).
     tensor_scale: see :class:`Fp4Matrix`; the largest magnitude / 2688 uses the
-        whole range, and 0 (that of zeros) gives zeros.
+        whole range, and 0 (that of zeros) gives zeros.  With p > 0 the largest
+        magnitude is that of the kept values, 1 / (1 - p) times x's: with x's own
+        the largest blocks saturate.
     p: with p > 0 the values are ``dropout(x, p, seed, offset)`` in float32.
     """
     how = _ROUNDING.get(rounding)

@@ -11,7 +11,7 @@ contract over different axes:
     dW = q(dy)^T . q(dropout(x))         over tokens: the columns of dy and x
 
 x and W are rounded to nearest, dy stochastically, so that the rounding of the
-gradients has no bias.  decode() is the serving form of a few tokens: 16-bit
+gradients has no bias (beyond 2^-16 of the gap between codes).  decode() is the serving form of a few tokens: 16-bit
 activations with the 4-bit weights, read once.  The master weights stay with
 the caller.  Both passes are explicit and outside autograd: forward() and
 backward() take tensors that require grad as they are, and their results do not.
