@@ -492,6 +492,11 @@ int ptc_plan_shape(int64_t M, int64_t N, int64_t K, int prec, int sms, int cap2,
  * work).  Returns PTC_OK, or PTC_ERR_INVALID when a pointer is NULL. */
 int ptc_last_launch(int *grid, int *cluster, int *ksplit, int *tile_n);
 
+/* The same of the calling thread's last 4-bit product: *tile = output columns per
+ * tile of gemm_fp4 (256: CTA pairs, 128, 64), or rows of the weights per CTA of
+ * gemm_a16_fp4 (128, 64, 32, 16). */
+int ptc_last_fp4_launch(int64_t *grid, int *cluster, int *ksplit, int *tile);
+
 /* Operand conversion of the calling thread's last GEMM call through this
  * library: *mode = 0 none (FP16 operands, a call that launched nothing, or no
  * call yet), 1 a separate conversion pass into a workspace, 2 conversion
@@ -636,6 +641,13 @@ int ptc_last_conversion(int *mode);
  *   "fp4_ksplit"   gemm_fp4's one-CTA tiles: CTAs of a cluster that share a
  *                  tile's K range: 0 (default) by size, 1, 2, 4 or 8.
  *   "fp4_group_m"  gemm_fp4's tile rows per raster group, default 8.
+ *   "fp4_tokens_rows" gemm_a16_fp4's row groups (16 rows of the weights) per CTA, whose
+ *                  8 / this many shares of K run beside each other: 0 (default) by
+ *                  size, 1, 2, 4 or 8.
+ *   "fp4_tokens_split" gemm_a16_fp4's CTAs of a cluster that share K: 0 (default) by
+ *                  size, 1, 2, 4 or 8.  A pair of these that the sizes do not allow
+ *                  (each share has at least 256 of K, and a share's activations fit
+ *                  their buffer) is not taken.
  * No accepted value of any key changes an INT8 or INT4 result. */
 int ptc_set_tuning(const char *key, int64_t value);
 

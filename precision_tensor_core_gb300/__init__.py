@@ -9,7 +9,7 @@ library's CUDA kernels):
 
 * ``gemm_f16``, ``gemm_f16_f16acc``, ``gemm_s8``, ``gemm_s4``, ``gemm_s8_scaled``, ``gemm_s4_scaled``,
   ``gemm_s8_noalloc``, ``gemm_s8_b_rowmajor``, ``gemm_status_string``,
-  ``gemm_poll_device_error``, ``ptc_kernel_launch_count``, ``ptc_last_launch``, ``ptc_last_conversion``, ``ptc_plan_shape``,
+  ``gemm_poll_device_error``, ``ptc_kernel_launch_count``, ``ptc_last_launch``, ``ptc_last_fp4_launch``, ``ptc_last_conversion``, ``ptc_plan_shape``,
   ``ptc_debug_set_wait_limit``, ``ptc_set_tuning``, ``gemm_fp4``, ``gemm_a16_fp4``, ``ptc_dropout``,
   ``ptc_dropout_to``, ``ptc_quantize_fp4``, ``ptc_dequantize_fp4``: the C ABI of
   ``include/ptc.h`` under the same names, taking integers (sizes, leading
@@ -122,6 +122,8 @@ def lib() -> ctypes.CDLL:
         _ip = ctypes.POINTER(ctypes.c_int)
         L.ptc_last_launch.restype = ctypes.c_int
         L.ptc_last_launch.argtypes = [_ip, _ip, _ip, _ip]
+        L.ptc_last_fp4_launch.restype = ctypes.c_int
+        L.ptc_last_fp4_launch.argtypes = [ctypes.POINTER(_i64), _ip, _ip, _ip]
         L.ptc_last_conversion.restype = ctypes.c_int
         L.ptc_last_conversion.argtypes = [_ip]
         _u64p = ctypes.POINTER(ctypes.c_uint64)
@@ -289,6 +291,14 @@ def ptc_last_launch() -> tuple[int, int, int, int]:
     width) of the calling thread's last GEMM kernel launch."""
     g, c, k, n = ctypes.c_int(0), ctypes.c_int(0), ctypes.c_int(0), ctypes.c_int(0)
     _check(lib().ptc_last_launch(ctypes.byref(g), ctypes.byref(c), ctypes.byref(k), ctypes.byref(n)))
+    return g.value, c.value, k.value, n.value
+
+
+def ptc_last_fp4_launch() -> tuple[int, int, int, int]:
+    """(grid CTAs, CTAs per cluster, CTAs sharing K, tile columns of gemm_fp4 or
+    weight rows per CTA of gemm_a16_fp4) of the calling thread's last 4-bit product."""
+    g, c, k, n = _i64(0), ctypes.c_int(0), ctypes.c_int(0), ctypes.c_int(0)
+    _check(lib().ptc_last_fp4_launch(ctypes.byref(g), ctypes.byref(c), ctypes.byref(k), ctypes.byref(n)))
     return g.value, c.value, k.value, n.value
 
 

@@ -470,6 +470,14 @@ int usable_device(int *sms) {
 bool pdl_enabled() { return g_pdl.load() != 0; }
 uint64_t wait_limit_ns() { return g_wait_ns.load(); }
 int take_stall_tile() { return int(g_stall_tile.exchange(-1)); }
+namespace {
+struct Fp4Launch {
+    int64_t grid;
+    int cluster, ksplit, tile;
+};
+thread_local Fp4Launch g_last_fp4{0, 0, 0, 0};
+}  // namespace
+void note_fp4_launch(int64_t grid, int cluster, int ksplit, int tile) { g_last_fp4 = {grid, cluster, ksplit, tile}; }
 bool rows_overlap(const ByteRows &a, const ByteRows &b) {
     if (!a.p || !b.p || a.rows < 1 || b.rows < 1 || !a.width || !b.width) return false;
     using wide = unsigned __int128;
@@ -1170,6 +1178,17 @@ int ptc_last_launch(int *grid, int *cluster, int *ksplit, int *tile_n) {
     return PTC_OK;
 }
 
+int ptc_last_fp4_launch(int64_t *grid, int *cluster, int *ksplit, int *tile) {
+    g_msg[0] = 0;
+    if (!grid || !cluster || !ksplit || !tile) return fail(PTC_ERR_INVALID, "NULL pointer");
+    const auto &l = ptc::g_last_fp4;
+    *grid = l.grid;
+    *cluster = l.cluster;
+    *ksplit = l.ksplit;
+    *tile = l.tile;
+    return PTC_OK;
+}
+
 int ptc_last_conversion(int *mode) {
     if (!mode) return fail(PTC_ERR_INVALID, "NULL pointer");
     *mode = g_last_conv;
@@ -1256,7 +1275,7 @@ int ptc_set_tuning(const char *key, int64_t value) {
         g_cta_pair.store(int(value));
         return PTC_OK;
     }
-    if (ptc::set_fp4_tuning(key, value)) return PTC_OK;
+    if (ptc::set_fp4_tuning(key, value) || ptc::set_tokens_tuning(key, value)) return PTC_OK;
     return fail(PTC_ERR_INVALID, "unknown tuning key or value out of range");
 }
 

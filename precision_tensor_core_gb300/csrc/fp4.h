@@ -51,8 +51,11 @@ int check_fp4(const void *codes, int64_t pitch, const void *scales, const void *
 // The 4-bit products' error words (fp4_gemm.cu, fp4_tokens.cu), read and cleared.
 cudaError_t read_and_clear_fp4_error_word(uint32_t *out);
 cudaError_t read_and_clear_tokens_error_word(uint32_t *out);
-// The keys "fp4_tile", "fp4_ksplit" and "fp4_group_m" of ptc_set_tuning;
-// false for another key or a value out of range.
+// The keys "fp4_tile", "fp4_ksplit" and "fp4_group_m", "fp4_tokens_rows" and
+// "fp4_tokens_split" of ptc_set_tuning; false for another key or a value out of range.
 bool set_fp4_tuning(const char *key, int64_t value);
+bool set_tokens_tuning(const char *key, int64_t value);
+// What ptc_last_fp4_launch reports (api.cu).
+void note_fp4_launch(int64_t grid, int cluster, int ksplit, int tile);
 
 }  // namespace ptc

@@ -657,7 +657,10 @@ cudaError_t launch4(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensor
     const int units = a.ks > 1 ? a.num_tiles : std::min(a.num_tiles, have);
     cfg.gridDim = dim3(unsigned(units * cl), 1, 1);
     e = cudaLaunchKernelEx(&cfg, fn, ta, tb, sa, sb, a);
-    if (e == cudaSuccess) note_launches(1);
+    if (e == cudaSuccess) {
+        note_launches(1);
+        note_fp4_launch(cfg.gridDim.x, cl, CTAS == 2 ? 1 : a.ks, BN);
+    }
     return e;
 }
 

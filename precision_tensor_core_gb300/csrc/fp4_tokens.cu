@@ -465,6 +465,8 @@ __global__ void __launch_bounds__(kTokThreads, 2)
 constexpr int64_t kMaxDimT = int64_t(1) << 30;
 constexpr int64_t kMaxLdT = int64_t(1) << 36;
 constexpr int kMaxDevT = 64;
+std::atomic<int> g_rows{0};   // "fp4_tokens_rows": 0 by size, 1, 2, 4, 8
+std::atomic<int> g_split{0};  // "fp4_tokens_split": 0 by size, 1, 2, 4, 8
 constexpr int kBufBytes = 28 * 1024;  // one buffer of activations (two per CTA, two CTAs per SM)
 static_assert(16 * (kPieceBytes + 32) <= kBufBytes, "sixteen tokens fit with R = 8");
 
@@ -478,28 +480,34 @@ static_assert(16 * (kPieceBytes + 32) <= kBufBytes, "sixteen tokens fit with R =
 // (Fitted to the times of every shape at 25 sizes between 128 x 8000 and 16384 x
 // 8192 weights with 1 to 16 tokens.  Its choice takes 1.02 times the fastest
 // shape's time there and at 15 other sizes, 1.13 at most.)
+// The keys take a part of the shapes, all of them where that leaves none.
 void choose_tokens(int64_t N, int64_t K, int groups, int toks, int token_bytes, bool bf16, bool xvec, int64_t chunks,
                    int sms, int *r_log2, int *ks) {
     const int64_t per_stage = toks > 8 ? 92 : bf16 ? 60 : 54;
+    const int rows = g_rows.load(), split = g_split.load();
     int64_t best = INT64_MAX;
-    for (int r = 3; r >= 0; --r) {
-        const int S = 8 >> r, most = kBufBytes / (S * token_bytes);  // stages of a chunk
-        if (most < 1) continue;                                      // (never with R = 8)
-        for (int k = 1; k <= 8; k *= 2) {
-            if (groups < S * k && (r < 3 || k > 1)) continue;
-            const int64_t ctas = (N + 127) / 128 * S * k * chunks;
-            const int64_t waves = (ctas + 2 * sms - 1) / (2 * sms), clusters = ctas / k / waves;
-            const int64_t stages = (groups + S * k - 1) / (S * k);
-            const int64_t start = k == 1 ? 220 : k == 2 ? 320 : k == 4 ? 360 + 2 * clusters : 550 + 11 * clusters;
-            const int64_t read = toks * K / k * 2 * (bf16 ? 10 : 2) * (xvec ? 2 : 7) / 2048;
-            const int64_t cost = waves * (start + stages * per_stage * (ctas > sms ? 18 : 10) / 10 +
-                                          (most == 1 ? stages * 80 : 0) + read);
-            if (cost < best) {
-                best = cost;
-                *r_log2 = r;
-                *ks = k;
+    for (bool any : {false, true}) {
+        for (int r = 3; r >= 0; --r) {
+            const int S = 8 >> r, most = kBufBytes / (S * token_bytes);  // stages of a chunk
+            if (most < 1) continue;                                      // (never with R = 8)
+            for (int k = 1; k <= 8; k *= 2) {
+                if (groups < S * k && (r < 3 || k > 1)) continue;
+                if (!any && ((rows != 0 && rows != 1 << r) || (split != 0 && split != k))) continue;
+                const int64_t ctas = (N + 127) / 128 * S * k * chunks;
+                const int64_t waves = (ctas + 2 * sms - 1) / (2 * sms), clusters = ctas / k / waves;
+                const int64_t stages = (groups + S * k - 1) / (S * k);
+                const int64_t start = k == 1 ? 220 : k == 2 ? 320 : k == 4 ? 360 + 2 * clusters : 550 + 11 * clusters;
+                const int64_t read = toks * K / k * 2 * (bf16 ? 10 : 2) * (xvec ? 2 : 7) / 2048;
+                const int64_t cost = waves * (start + stages * per_stage * (ctas > sms ? 18 : 10) / 10 +
+                                              (most == 1 ? stages * 80 : 0) + read);
+                if (cost < best) {
+                    best = cost;
+                    *r_log2 = r;
+                    *ks = k;
+                }
             }
         }
+        if (best != INT64_MAX) return;
     }
 }
 
@@ -561,6 +569,7 @@ int launch_tokens(TokArgs a, const void *codes, int64_t pitch, const void *scale
     e = cudaLaunchKernelEx(&cfg, fn, tw, ts, a);
     if (e != cudaSuccess) return fail_launch(e, "4-bit weight product launch");
     note_launches(1);
+    note_fp4_launch(int64_t(cfg.gridDim.x) * cfg.gridDim.y, ks, ks, 16 * R);
     return PTC_OK;
 }
 
@@ -571,6 +580,17 @@ int launch_width(const TokArgs &a, const void *codes, int64_t pitch, const void 
 }
 
 }  // namespace
+
+bool set_tokens_tuning(const char *key, int64_t v) {
+    if (v != 0 && v != 1 && v != 2 && v != 4 && v != 8) return false;
+    if (std::strcmp(key, "fp4_tokens_rows") == 0)
+        g_rows.store(int(v));
+    else if (std::strcmp(key, "fp4_tokens_split") == 0)
+        g_split.store(int(v));
+    else
+        return false;
+    return true;
+}
 
 cudaError_t read_and_clear_tokens_error_word(uint32_t *out) {
     uint32_t v = 0;
