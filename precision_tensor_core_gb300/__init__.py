@@ -528,15 +528,17 @@ class Fp4Matrix:
         """Row-major scale bytes (rows, blocks) to the tiled layout (laid out once, e.g. when weights are loaded)."""
         import torch
         r, b = scales.shape
+        if r == 0 or b == 0:
+            return scales.reshape(-1)
         s = torch.nn.functional.pad(scales, (0, -b % 4, 0, -r % 128))
         return s.view(s.shape[0] // 128, 4, 32, s.shape[1] // 4, 4).permute(0, 3, 2, 1, 4).reshape(-1)
 
     def row_scales(self):
         """Row-major scale bytes (rows, blocks)."""
         r, b = self._codes.shape[0], -(-self._K // _FP4[self._fmt][1])
-        kt = -(-b // 4)
-        s = self._scales.view(-1)[:fp4_scale_bytes(r, self._K, self._fmt)].view(-1, kt, 32, 4, 4)
-        return s.permute(0, 3, 2, 1, 4).reshape(-1, kt * 4)[:r, :b]
+        rt, kt = -(-r // 128), -(-b // 4)
+        s = self._scales.view(-1)[:fp4_scale_bytes(r, self._K, self._fmt)].view(rt, kt, 32, 4, 4)
+        return s.permute(0, 3, 2, 1, 4).reshape(rt * 128, kt * 4)[:r, :b]
 
 
 def dropout(x, p, seed, offset=0, residual=None, out=None, stream=None, out_dtype=None):
