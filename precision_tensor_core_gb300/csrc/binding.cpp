@@ -219,23 +219,25 @@ struct NewMatrix {
 class Target {
     c10::cuda::CUDAStream caller_;
     void *handle_;
+    bool elsewhere_ = false;  // on another stream than the caller's
     c10::cuda::OptionalCUDAGuard device_;
     c10::cuda::OptionalCUDAStreamGuard stream_;
 
   public:
     Target(c10::DeviceIndex index, PyObject *stream) : caller_(c10::cuda::getCurrentCUDAStream(index)) {
-        handle_ = caller_.stream();
+        void *const own = caller_.stream();
+        handle_ = own;
         if (stream != Py_None) {
             Ref h(PyObject_CallOneArg(g_stream, stream));
             handle_ = reinterpret_cast<void *>(uintptr_t(seed64(h.p)));
             if (handle_ == cudaStreamLegacy) handle_ = nullptr;  // (torch knows the default stream by that)
+            elsewhere_ = handle_ != own;
         }
-        if (elsewhere())
+        if (elsewhere_)
             stream_.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle_), index));
         else if (c10::cuda::current_device() != index)
             device_.set_index(index);
     }
-    bool elsewhere() const { return handle_ != caller_.stream(); }
     // f(stream), its status raised.
     template <typename F>
     void run(F f) const {
@@ -249,10 +251,10 @@ class Target {
     // Of a launched call: tensors of the caller's (a tensor, a 4-bit matrix or None),
     // and results of this stream's memory.
     void used(PyObject *o) const {
-        if (elsewhere()) record(o, c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle_), caller_.device_index()));
+        if (elsewhere_) record(o, c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle_), caller_.device_index()));
     }
     void made(PyObject *o) const {
-        if (elsewhere()) record(o, caller_);
+        if (elsewhere_) record(o, caller_);
     }
 
   private:
