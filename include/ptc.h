@@ -326,9 +326,9 @@ int gemm_baseline(int variant, int64_t M, int64_t N, int64_t K,
  *           The buffer holds whole tiles.  The bytes of blocks past K must not
  *           be NaN; those of rows past R may hold anything.
  *   PTC_FP4_MX  blocks of 32, scale 2^(byte - 127), 0xFF: the block is NaN
- *   PTC_FP4_NV  blocks of 16, E4M3 scale (its sign bit clear), 0x7F: the block is NaN; the whole
- *               matrix is also scaled by a float on the device (NULL: 1),
- *               which must lie in 0 .. 2^100.
+ *   PTC_FP4_NV  blocks of 16, E4M3 scale (its sign bit clear), 0x7F: the block
+ *               is NaN; the whole matrix is also scaled by a float on the
+ *               device (NULL: 1), which must lie in 0 .. 2^100.
  * Codes and scales are 16-byte aligned.  (The study has no floating-point
  * 4-bit format; these are the ones the GB300 tensor cores multiply directly.)
  *
@@ -404,10 +404,11 @@ int ptc_dequantize_fp4(int64_t rows, int64_t cols, const void *codes, int64_t pi
  * C[M x N] = out( rn(GA GB) * sum_k a_ik b_jk ) of two microscaled 4-bit
  * matrices of the same format: A of M rows of K, B of N rows of K (B's
  * columns as rows, like gemm_s4), lda and ldb the code pitches in BYTES, SA / SB
- * their scales, GA / GB their matrix scales (PTC_FP4_NV; NULL: 1).  Products
- * are exact, sums are the tensor cores' FP32 sums; C is float32, bfloat16 or
- * binary16 (PTC_OUT_*), ldc >= N elements apart, aligned to its element
- * (16-byte rows run faster).  K == 0 writes zeros.  No workspace is used.
+ * their scales, GA / GB their matrix scales (PTC_FP4_NV; NULL: 1), whose product
+ * has FP32's whole precision from 2^-126 up.  Products are exact, sums are the
+ * tensor cores' FP32 sums; C is float32, bfloat16 or binary16 (PTC_OUT_*),
+ * ldc >= N elements apart, aligned to its element (16-byte rows run faster).
+ * K == 0 writes zeros.  No workspace is used.
  * Results are the same from call to call; the summation order depends on the
  * sizes (and the keys fp4_tile, fp4_ksplit).
  */
