@@ -14,7 +14,8 @@
  *
  * and, beside the study, the 4-bit floating-point operators that language models
  * train and decode with: gemm_fp4, gemm_a16_fp4, ptc_quantize_fp4,
- * ptc_dequantize_fp4, ptc_dropout and ptc_dropout_to (see "Microscaled 4-bit matrices" below).
+ * ptc_dequantize_fp4, ptc_dropout and ptc_dropout_to (see "Microscaled 4-bit matrices" below),
+ * and the norm before a product, ptc_rms_norm, ptc_rms_norm_s8 and ptc_rms_norm_backward.
  *
  * The first three compute C <- A.B exactly as the plain sum over k, with C
  * overwritten and no scaling, bias or dequantisation (section VI "Scope":
@@ -428,6 +429,50 @@ int gemm_fp4(int64_t M, int64_t N, int64_t K, int format, const void *A, int64_t
  */
 int gemm_a16_fp4(int64_t M, int64_t N, int64_t K, int type, const void *X, int64_t ldx, int format, const void *W,
                  int64_t ldw, const void *SW, const float *GW, void *C, int64_t ldc, void *stream);
+
+/*
+ * Root-mean-square norm of rows
+ * -----------------------------
+ *   s = x, or x + residual in FP32 rounded to x's type, which is stored in `sum`
+ *       (the residual stream; without a residual `sum` is NULL)
+ *   r = 1 / sqrt(mean(s^2) + eps) of the row, in FP32
+ *   y = s r weight, rounded to x's type
+ * x, residual, sum, y: rows of `cols` elements of `type` (PTC_OUT_*), ld >= cols
+ * elements apart, aligned to the element (16-byte rows run faster).  weight: `cols`
+ * values of x's type or float32 (weight_type), or NULL for ones.  eps >= 0 (with 0 a
+ * row of zeros is NaN).  y or sum may be x or residual (same ld); other overlaps are
+ * refused.  Rows are independent: an infinity or NaN changes its own row alone.
+ */
+int ptc_rms_norm(int64_t rows, int64_t cols, const void *x, int64_t ldx, int type, const void *residual, int64_t ldr,
+                 void *sum, int64_t lds, const void *weight, int weight_type, float eps, void *y, int64_t ldy, void *stream);
+
+/*
+ * The same norm as 8-bit codes with a scale per row, the A and scale_a of
+ * gemm_s8_scaled.  With t = s weight in FP32 and a the largest |t| of the row:
+ * codes = 127 t / a rounded to nearest (ties to even; decided exactly), scale =
+ * a r / 127.  A row of zeros has codes and scale 0; a row in which some t is not
+ * finite has codes 0 and scale NaN.  codes: ldc >= cols bytes apart (gemm_s8_scaled takes
+ * multiples of 16).
+ */
+int ptc_rms_norm_s8(int64_t rows, int64_t cols, const void *x, int64_t ldx, int type, const void *residual, int64_t ldr,
+                    void *sum, int64_t lds, const void *weight, int weight_type, float eps, int8_t *codes, int64_t ldc,
+                    float *scale, void *stream);
+
+/*
+ * Gradients of ptc_rms_norm from dy, the gradient of y, and s, the matrix that was
+ * normalised (x or sum): with g = dy weight and u = s r
+ *   dx = r (g - u r mean(g s)) + ds      rounded once to the type of the matrices
+ *   dweight = sum over rows of dy u      float32, `cols` values
+ * ds (NULL: none) is the gradient that reaches s from elsewhere, as that of the
+ * residual stream; dx is the gradient of x and of the residual.  dx may be dy, s or ds
+ * (same ld).  The workspace holds partial sums of dweight, which are added in a fixed
+ * order: at least ptc_rms_norm_backward_workspace(rows, cols) bytes, 16-byte aligned,
+ * and no other call's until this one is done.
+ */
+int64_t ptc_rms_norm_backward_workspace(int64_t rows, int64_t cols);
+int ptc_rms_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t lddy, const void *s, int64_t lds, int type,
+                          const void *ds, int64_t ldds, const void *weight, int weight_type, float eps, void *dx, int64_t lddx,
+                          float *dweight, void *workspace, int64_t workspace_bytes, void *stream);
 
 /* Human-readable text of a status code.  For PTC_ERR_LAUNCH the text of the
  * failing CUDA call on the calling thread is appended.  Never NULL; the

@@ -11,7 +11,8 @@ library's CUDA kernels):
   ``gemm_s8_noalloc``, ``gemm_s8_b_rowmajor``, ``gemm_status_string``,
   ``gemm_poll_device_error``, ``ptc_kernel_launch_count``, ``ptc_last_launch``, ``ptc_last_fp4_launch``, ``ptc_last_conversion``, ``ptc_plan_shape``,
   ``ptc_debug_set_wait_limit``, ``ptc_set_tuning``, ``gemm_fp4``, ``gemm_a16_fp4``, ``ptc_dropout``,
-  ``ptc_dropout_to``, ``ptc_quantize_fp4``, ``ptc_dequantize_fp4``: the C ABI of
+  ``ptc_dropout_to``, ``ptc_quantize_fp4``, ``ptc_dequantize_fp4``, ``ptc_rms_norm``, ``ptc_rms_norm_s8``,
+  ``ptc_rms_norm_backward``, ``ptc_rms_norm_backward_workspace``: the C ABI of
   ``include/ptc.h`` under the same names, taking integers (sizes, leading
   dimensions, device addresses, a cudaStream_t handle).  A nonzero status
   raises :class:`PtcError`.
@@ -24,6 +25,8 @@ library's CUDA kernels):
   :class:`Fp4Matrix`: counter-based dropout and microscaled 4-bit matrices on
   torch tensors of the device; :mod:`precision_tensor_core_gb300.fp4_linear`
   puts them together as a linear layer's training and decoding steps.
+* ``rms_norm``, ``rms_norm_s8``, ``rms_norm_backward``: the norm before a product, also as
+  the 8-bit operand of ``matmul_s8_scaled``.
 
 There is no CPU fallback: if ``libptc.so`` has not been built the first call
 raises, and on a machine without a compute-capability 10.3 GPU every GEMM call
@@ -94,7 +97,7 @@ def lib() -> ctypes.CDLL:
             fn = getattr(L, name)
             fn.restype = ctypes.c_int
             fn.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, ctypes.c_int, _vp]
-        _int, _u64, _f64 = ctypes.c_int, ctypes.c_uint64, ctypes.c_double
+        _int, _u64, _f64, _f32 = ctypes.c_int, ctypes.c_uint64, ctypes.c_double, ctypes.c_float
         for name, args in (
                 ("ptc_dropout", [_i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _int, _f64, _u64, _u64, _vp]),
                 ("ptc_dropout_to", [_i64, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64, _int, _f64, _u64, _u64, _vp]),
@@ -103,10 +106,17 @@ def lib() -> ctypes.CDLL:
                 ("ptc_dequantize_fp4", [_i64, _i64, _vp, _i64, _vp, _int, _vp, _vp, _i64, _int, _vp]),
                 ("gemm_fp4", [_i64, _i64, _i64, _int, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _int,
                               _vp]),
-                ("gemm_a16_fp4", [_i64, _i64, _i64, _int, _vp, _i64, _int, _vp, _i64, _vp, _vp, _vp, _i64, _vp])):
+                ("gemm_a16_fp4", [_i64, _i64, _i64, _int, _vp, _i64, _int, _vp, _i64, _vp, _vp, _vp, _i64, _vp]),
+                ("ptc_rms_norm", [_i64, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64, _vp, _int, _f32, _vp, _i64, _vp]),
+                ("ptc_rms_norm_s8", [_i64, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64, _vp, _int, _f32, _vp, _i64, _vp,
+                                     _vp]),
+                ("ptc_rms_norm_backward", [_i64, _i64, _vp, _i64, _vp, _i64, _int, _vp, _i64, _vp, _int, _f32, _vp, _i64,
+                                           _vp, _vp, _i64, _vp])):
             fn = getattr(L, name)
             fn.restype = ctypes.c_int
             fn.argtypes = args
+        L.ptc_rms_norm_backward_workspace.restype = _i64
+        L.ptc_rms_norm_backward_workspace.argtypes = [_i64, _i64]
         L.gemm_baseline.restype = ctypes.c_int
         L.gemm_baseline.argtypes = [ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp]
         L.gemm_status_string.restype = ctypes.c_char_p
@@ -241,6 +251,31 @@ def gemm_fp4(M, N, K, format, A, lda, SA, GA, B, ldb, SB, GB, C, ldc, out_type, 
 def gemm_a16_fp4(M, N, K, type, X, ldx, format, W, ldw, SW, GW, C, ldc, stream=0) -> int:
     """C[MxN] = X[MxK] (bfloat16 / binary16) . W[NxK]^T, W microscaled 4-bit."""
     return _check(lib().gemm_a16_fp4(M, N, K, type, X, ldx, format, W, ldw, SW, GW, C, ldc, stream))
+
+
+def ptc_rms_norm(rows, cols, x, ldx, type, residual, ldr, sum, lds, weight, weight_type, eps, y, ldy, stream=0) -> int:
+    """Root-mean-square norm of rows, with the residual's addition (include/ptc.h)."""
+    return _check(lib().ptc_rms_norm(rows, cols, x, ldx, type, residual, ldr, sum, lds, weight, weight_type, eps, y, ldy,
+                                     stream))
+
+
+def ptc_rms_norm_s8(rows, cols, x, ldx, type, residual, ldr, sum, lds, weight, weight_type, eps, codes, ldc, scale,
+                    stream=0) -> int:
+    """The same as 8-bit codes with a scale per row (include/ptc.h)."""
+    return _check(lib().ptc_rms_norm_s8(rows, cols, x, ldx, type, residual, ldr, sum, lds, weight, weight_type, eps, codes,
+                                        ldc, scale, stream))
+
+
+def ptc_rms_norm_backward_workspace(rows, cols) -> int:
+    """Bytes of workspace that ptc_rms_norm_backward takes."""
+    return lib().ptc_rms_norm_backward_workspace(rows, cols)
+
+
+def ptc_rms_norm_backward(rows, cols, dy, lddy, s, lds, type, ds, ldds, weight, weight_type, eps, dx, lddx, dweight,
+                          workspace, workspace_bytes, stream=0) -> int:
+    """Gradients of the norm (include/ptc.h)."""
+    return _check(lib().ptc_rms_norm_backward(rows, cols, dy, lddy, s, lds, type, ds, ldds, weight, weight_type, eps, dx,
+                                              lddx, dweight, workspace, workspace_bytes, stream))
 
 
 def gemm_poll_device_error() -> int:
@@ -480,7 +515,10 @@ def _load_native():
     n = importlib.import_module(__name__ + "._native")
     L = lib()
     n.init(*(ctypes.cast(getattr(L, f), _vp).value for f in ("ptc_dropout_to", "ptc_quantize_fp4",
-                                                             "ptc_dequantize_fp4", "gemm_fp4", "gemm_a16_fp4")),
+                                                             "ptc_dequantize_fp4", "gemm_fp4", "gemm_a16_fp4",
+                                                             "ptc_rms_norm", "ptc_rms_norm_s8",
+                                                             "ptc_rms_norm_backward_workspace",
+                                                             "ptc_rms_norm_backward")),
            _check, _stream, Fp4Matrix)
     _native = n
     return n
@@ -594,3 +632,31 @@ def matmul_a16_fp4(x, Wt, out=None, stream=None):
     rows (more are taken 16 at a time; quantise x and use :func:`matmul_fp4`
     for many)."""
     return (_native or _load_native()).matmul_a16(x, Wt, out, stream)
+
+
+# ---------------------------------------------------------------- norms on tensors
+def rms_norm(x, weight=None, eps=1e-6, residual=None, out=None, sum_out=None, stream=None):
+    """``s / sqrt(mean(s^2) + eps) * weight`` of every row of x (rows, cols) float32,
+    bfloat16 or float16, computed in float32 and rounded once; s is x, or with a
+    ``residual`` x + residual rounded to x's dtype.  Returns y, or with a residual (y,
+    s).  ``weight`` (cols,): x's dtype or float32, None for ones.  ``out`` or
+    ``sum_out`` may be x or the residual.  Outside autograd, as the 4-bit operators;
+    :func:`rms_norm_backward` is the backward pass."""
+    return (_native or _load_native()).rms_norm(x, weight, eps, residual, out, sum_out, stream)
+
+
+def rms_norm_s8(x, weight=None, eps=1e-6, residual=None, sum_out=None, stream=None):
+    """:func:`rms_norm` as int8 codes (rows, cols) with a float32 scale per row, what
+    :func:`matmul_s8_scaled` takes as A and scale_a (the codes' rows are a multiple of
+    16 bytes apart).  Returns (codes, scale), or with a residual (codes, scale, s).  A
+    row with an infinity or NaN has codes 0 and scale NaN."""
+    return (_native or _load_native()).rms_norm_s8(x, weight, eps, residual, sum_out, stream)
+
+
+def rms_norm_backward(dy, s, weight=None, eps=1e-6, dsum=None, out=None, stream=None):
+    """(dx, dweight) of :func:`rms_norm` from the gradient dy of y and the s that was
+    normalised (x, or the returned sum).  ``dsum`` is the gradient that reaches s from
+    elsewhere (the residual stream's) and is added to dx, which is the gradient of x
+    and of the residual; dweight is float32 (cols,), added over the rows in a fixed
+    order.  ``out`` may be dy, s or dsum."""
+    return (_native or _load_native()).rms_norm_backward(dy, s, weight, eps, dsum, out, stream)

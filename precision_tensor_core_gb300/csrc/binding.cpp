@@ -1,5 +1,5 @@
-// binding.cpp -- CPython functions behind the 4-bit operators of the package's
-// tensor layer: they check torch tensors, allocate results, and call the C ABI of
+// binding.cpp -- CPython functions behind the 4-bit operators and the norms of the
+// package's tensor layer: they check torch tensors, allocate results, and call the C ABI of
 // include/ptc.h.  A decoding step's operators take a few microseconds on the
 // device; the same marshalling through ctypes took 9 to 14 us per call, this
 // takes 4 to 6.  The C entry points are passed in once as addresses (init), so
@@ -14,6 +14,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "ptc.h"
 
@@ -24,6 +25,10 @@ decltype(&ptc_quantize_fp4) f_quantize;
 decltype(&ptc_dequantize_fp4) f_dequantize;
 decltype(&gemm_fp4) f_gemm;
 decltype(&gemm_a16_fp4) f_gemm_a16;
+decltype(&ptc_rms_norm) f_norm;
+decltype(&ptc_rms_norm_s8) f_norm_s8;
+decltype(&ptc_rms_norm_backward_workspace) f_norm_workspace;
+decltype(&ptc_rms_norm_backward) f_norm_backward;
 PyObject *g_check;   // raises PtcError for a status
 PyObject *g_stream;  // a stream argument to its handle
 PyTypeObject *g_matrix;
@@ -451,6 +456,135 @@ PyObject *py_matmul_a16(PyObject *, PyObject *const *a, Py_ssize_t n) {
     PTC_BODY_END
 }
 
+// What the norms share: x, an optional tensor of x's shape, type and device, and the weight.
+const at::Tensor &same_as(const at::Tensor &x, const char *of, const at::Tensor &t, const char *name) {
+    if (t.scalar_type() != x.scalar_type() || t.sizes() != x.sizes() || !t.is_cuda() || t.get_device() != x.get_device()) {
+        PyErr_Format(PyExc_ValueError, "%s must have %s's shape, dtype and device", name, of);
+        throw Bad();
+    }
+    return t;
+}
+
+Rows optional_rows(const at::Tensor &x, const char *of, PyObject *o, const char *name) {
+    if (o == Py_None) return {nullptr, 0, 0, 0};
+    return rows_of(same_as(x, of, outside_autograd(tensor(o, name), name), name), name);
+}
+
+const void *norm_weight(const at::Tensor &x, PyObject *o, int type, int *w_type) {
+    *w_type = type;
+    if (o == Py_None) return nullptr;
+    const at::Tensor &w = outside_autograd(tensor(o, "weight"), "weight");
+    *w_type = type_of(w.scalar_type());
+    if (w.dim() != 1 || w.size(0) != x.size(1) || !w.is_contiguous() || !w.is_cuda() || w.get_device() != x.get_device() ||
+        (*w_type != type && *w_type != PTC_OUT_F32))
+        raise(PyExc_ValueError, "weight must be a contiguous vector of x's columns, of x's dtype or float32, on x's device");
+    return w.data_ptr();
+}
+
+float epsilon(PyObject *o) {
+    const double e = real(o);
+    if (!(e >= 0.0 && e <= 3.0e38)) raise(PyExc_ValueError, "eps must be finite and not negative");
+    return float(e);
+}
+
+// (x, weight, eps, residual, out, sum_out, stream)
+PyObject *py_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    PTC_BODY_BEGIN
+    expect(n, 7);
+    const at::Tensor &x = outside_autograd(tensor(a[0], "x"), "x");
+    const int type = type_of(x.scalar_type());
+    const Rows rx = rows_of(x, "x");
+    const c10::DeviceIndex index = x.get_device();
+    int wt;
+    const void *w = norm_weight(x, a[1], type, &wt);
+    const float eps = epsilon(a[2]);
+    const Rows rr = optional_rows(x, "x", a[3], "residual");
+    const bool res = a[3] != Py_None;
+    if (a[4] != Py_None) same_as(x, "x", tensor(a[4], "out"), "out");
+    if (a[5] != Py_None) {
+        if (!res) raise(PyExc_ValueError, "sum_out is written only with a residual");
+        same_as(x, "x", tensor(a[5], "sum_out"), "sum_out");
+    }
+    const Target target(index, a[6]);
+    at::Tensor y = result(a[4], rx.rows, rx.cols, x.scalar_type(), index, x.device());
+    at::Tensor sum = res ? result(a[5], rx.rows, rx.cols, x.scalar_type(), index, x.device()) : at::Tensor();
+    const Rows ry = rows_of(y, "out"), rs = res ? rows_of(sum, "sum_out") : Rows{nullptr, 0, 0, 0};
+    target.run([&](void *s) {
+        return f_norm(rx.rows, rx.cols, rx.p, rx.ld, type, rr.p, rr.ld, rs.p, rs.ld, w, wt, eps, ry.p, ry.ld, s);
+    });
+    for (int i : {0, 1, 3}) target.used(a[i]);
+    if (!res) return give(target, a[4], std::move(y));
+    Ref yo(give(target, a[4], std::move(y))), so(give(target, a[5], std::move(sum)));
+    return PyTuple_Pack(2, yo.p, so.p);
+    PTC_BODY_END
+}
+
+// (x, weight, eps, residual, sum_out, stream)
+PyObject *py_norm_s8(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    PTC_BODY_BEGIN
+    expect(n, 6);
+    const at::Tensor &x = outside_autograd(tensor(a[0], "x"), "x");
+    const int type = type_of(x.scalar_type());
+    const Rows rx = rows_of(x, "x");
+    const c10::DeviceIndex index = x.get_device();
+    int wt;
+    const void *w = norm_weight(x, a[1], type, &wt);
+    const float eps = epsilon(a[2]);
+    const Rows rr = optional_rows(x, "x", a[3], "residual");
+    const bool res = a[3] != Py_None;
+    if (a[4] != Py_None) {
+        if (!res) raise(PyExc_ValueError, "sum_out is written only with a residual");
+        same_as(x, "x", tensor(a[4], "sum_out"), "sum_out");
+    }
+    const Target target(index, a[5]);
+    // (rows of a multiple of 16 bytes, as the INT8 products take them)
+    at::Tensor wide = empty({rx.rows, (rx.cols + 15) / 16 * 16}, at::kChar, x.device());
+    at::Tensor codes = wide.size(1) == rx.cols ? wide : wide.narrow(1, 0, rx.cols);
+    at::Tensor scale = empty({rx.rows}, at::kFloat, x.device());
+    at::Tensor sum = res ? result(a[4], rx.rows, rx.cols, x.scalar_type(), index, x.device()) : at::Tensor();
+    const Rows rs = res ? rows_of(sum, "sum_out") : Rows{nullptr, 0, 0, 0};
+    target.run([&](void *s) {
+        return f_norm_s8(rx.rows, rx.cols, rx.p, rx.ld, type, rr.p, rr.ld, rs.p, rs.ld, w, wt, eps,
+                         static_cast<int8_t *>(wide.data_ptr()), wide.size(1), static_cast<float *>(scale.data_ptr()), s);
+    });
+    for (int i : {0, 1, 3}) target.used(a[i]);
+    Ref co(give(target, Py_None, std::move(codes))), sc(give(target, Py_None, std::move(scale)));
+    if (!res) return PyTuple_Pack(2, co.p, sc.p);
+    Ref so(give(target, a[4], std::move(sum)));
+    return PyTuple_Pack(3, co.p, sc.p, so.p);
+    PTC_BODY_END
+}
+
+// (dy, s, weight, eps, dsum, out, stream)
+PyObject *py_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    PTC_BODY_BEGIN
+    expect(n, 7);
+    const at::Tensor &dy = outside_autograd(tensor(a[0], "dy"), "dy");
+    const int type = type_of(dy.scalar_type());
+    const Rows rd = rows_of(dy, "dy");
+    const c10::DeviceIndex index = dy.get_device();
+    const Rows rs = rows_of(same_as(dy, "dy", outside_autograd(tensor(a[1], "s"), "s"), "s"), "s");
+    int wt;
+    const void *w = norm_weight(dy, a[2], type, &wt);
+    const float eps = epsilon(a[3]);
+    const Rows rr = optional_rows(dy, "dy", a[4], "dsum");
+    if (a[5] != Py_None) same_as(dy, "dy", tensor(a[5], "out"), "out");
+    const Target target(index, a[6]);
+    at::Tensor dx = result(a[5], rd.rows, rd.cols, dy.scalar_type(), index, dy.device());
+    at::Tensor dw = empty({rd.cols}, at::kFloat, dy.device());
+    const int64_t bytes = f_norm_workspace(rd.rows, rd.cols);
+    at::Tensor ws = empty({bytes}, at::kByte, dy.device());
+    const Rows rx = rows_of(dx, "out");
+    target.run([&](void *s) {
+        return f_norm_backward(rd.rows, rd.cols, rd.p, rd.ld, rs.p, rs.ld, type, rr.p, rr.ld, w, wt, eps, rx.p, rx.ld,
+                               static_cast<float *>(dw.data_ptr()), ws.data_ptr(), bytes, s);
+    });
+    for (int i : {0, 1, 2, 4}) target.used(a[i]);
+    Ref xo(give(target, a[5], std::move(dx))), wo(give(target, Py_None, std::move(dw)));
+    return PyTuple_Pack(2, xo.p, wo.p);
+    PTC_BODY_END
+}
+
 // (codes, scales, K, fmt, tensor_scale): raises what is wrong with them
 PyObject *py_check_matrix(PyObject *, PyObject *const *a, Py_ssize_t n) {
     PTC_BODY_BEGIN
@@ -460,20 +594,25 @@ PyObject *py_check_matrix(PyObject *, PyObject *const *a, Py_ssize_t n) {
     PTC_BODY_END
 }
 
-// (addresses of the five C entry points, status check, stream handle, Fp4Matrix)
+// (addresses of the nine C entry points, status check, stream handle, Fp4Matrix)
 PyObject *py_init(PyObject *, PyObject *const *a, Py_ssize_t n) {
     PTC_BODY_BEGIN
-    expect(n, 8);
-    f_dropout = reinterpret_cast<decltype(f_dropout)>(uintptr_t(seed64(a[0])));
-    f_quantize = reinterpret_cast<decltype(f_quantize)>(uintptr_t(seed64(a[1])));
-    f_dequantize = reinterpret_cast<decltype(f_dequantize)>(uintptr_t(seed64(a[2])));
-    f_gemm = reinterpret_cast<decltype(f_gemm)>(uintptr_t(seed64(a[3])));
-    f_gemm_a16 = reinterpret_cast<decltype(f_gemm_a16)>(uintptr_t(seed64(a[4])));
-    if (!PyType_Check(a[7])) raise(PyExc_TypeError, "a type is expected");
-    Py_XSETREF(g_check, Py_NewRef(a[5]));
-    Py_XSETREF(g_stream, Py_NewRef(a[6]));
+    expect(n, 12);
+    auto entry = [&](auto &f) { f = reinterpret_cast<std::decay_t<decltype(f)>>(uintptr_t(seed64(*a++))); };
+    entry(f_dropout);
+    entry(f_quantize);
+    entry(f_dequantize);
+    entry(f_gemm);
+    entry(f_gemm_a16);
+    entry(f_norm);
+    entry(f_norm_s8);
+    entry(f_norm_workspace);
+    entry(f_norm_backward);
+    if (!PyType_Check(a[2])) raise(PyExc_TypeError, "a type is expected");
+    Py_XSETREF(g_check, Py_NewRef(a[0]));
+    Py_XSETREF(g_stream, Py_NewRef(a[1]));
     PyTypeObject *old = g_matrix;
-    g_matrix = reinterpret_cast<PyTypeObject *>(Py_NewRef(a[7]));
+    g_matrix = reinterpret_cast<PyTypeObject *>(Py_NewRef(a[2]));
     Py_XDECREF(old);
     if (!s_codes) {
         s_codes = PyUnicode_InternFromString("_codes");
@@ -493,6 +632,9 @@ PyMethodDef g_methods[] = {PTC_METHOD("init", py_init),
                            PTC_METHOD("dequantize", py_dequantize),
                            PTC_METHOD("matmul", py_matmul),
                            PTC_METHOD("matmul_a16", py_matmul_a16),
+                           PTC_METHOD("rms_norm", py_norm),
+                           PTC_METHOD("rms_norm_s8", py_norm_s8),
+                           PTC_METHOD("rms_norm_backward", py_norm_backward),
                            PTC_METHOD("check_matrix", py_check_matrix),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

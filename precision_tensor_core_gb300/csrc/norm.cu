@@ -1,0 +1,731 @@
+// norm.cu -- root-mean-square norm of rows, with the residual's addition and an
+// output in the element type or in 8 bits with a scale per row, and its gradient
+// (ptc_rms_norm, ptc_rms_norm_s8, ptc_rms_norm_backward of include/ptc.h).
+//
+// Every byte is read and written once: rows of up to 16384 elements stay in
+// registers between the sum of squares and the output.  All of it is bound by
+// memory traffic; a row of one token by the start of a kernel and one reduction.
+//
+// In 8 bits the row's 1 / rms cancels out of the codes: with t = s w and a the
+// row's largest |t|, y / (max |y| / 127) = 127 t / a.  So the sum of squares and the
+// largest magnitude are reduced together, and a code depends on no sum's order.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include "fp4.cuh"
+#include "fp4.h"
+#include "internal.h"
+#include "ptc.h"
+#include "ptx.cuh"
+
+namespace ptc {
+namespace {
+
+struct NormArgs {
+    const void *x;
+    int64_t ldx;
+    const void *res;  // NULL: none
+    int64_t ldr;
+    void *sum;  // with a residual
+    int64_t lds;
+    const void *w;  // NULL: ones
+    int w_f32;      // w is float32 (else of x's type)
+    void *y;        // or the 8-bit codes
+    int64_t ldy;
+    float *scale;  // 8 bits: a scale per row
+    int64_t rows, cols;
+    float eps, inv_cols;
+};
+
+struct GradArgs {
+    const void *dy, *s, *ds;  // ds NULL: none
+    int64_t lddy, lds, ldds;
+    const void *w;
+    int w_f32;
+    void *dx;
+    int64_t lddx;
+    float *part;     // [gridDim.x][cols]: sums of dy s r
+    float2 *stat;    // long rows: r and r mean(g s) of every row
+    int64_t rows, cols;
+    float eps, inv_cols;
+};
+
+// Column of element e of this thread's chunk i of eight elements: eight consecutive
+// ones, or (rows that are not 16-byte aligned) one of each run of the row's threads,
+// so that a warp's accesses are consecutive either way.
+template <bool VEC>
+__device__ __forceinline__ int64_t column(int i, int e, int tid, int threads) {
+    return VEC ? (int64_t(i) * threads + tid) * 8 + e : (int64_t(i) * 8 + e) * threads + tid;
+}
+
+template <bool VEC, typename T>
+__device__ __forceinline__ Pack8<T> load_chunk(const T *p, int i, int tid, int threads, int64_t cols) {
+    Pack8<T> r;
+    if constexpr (VEC) {
+        const int64_t c = column<true>(i, 0, tid, threads);
+        if (c + 8 <= cols) return load8(p + c, 8, true);
+        return load8(c < cols ? p + c : p, c < cols ? int(cols - c) : 0, false);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int64_t c = column<false>(i, e, tid, threads);
+            r.set(e, c < cols ? p[c] : from_float<T>(0.0f));
+        }
+        return r;
+    }
+}
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_chunk(T *p, const Pack8<T> &v, int i, int tid, int threads, int64_t cols) {
+    if constexpr (VEC) {
+        const int64_t c = column<true>(i, 0, tid, threads);
+        if (c < cols) store8(p + c, v, int(min(int64_t(8), cols - c)), true);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int64_t c = column<false>(i, e, tid, threads);
+            if (c < cols) p[c] = v.get(e);
+        }
+    }
+}
+
+// Eight weights as FP32; 1 where there are none, anything past the row.
+template <bool VEC, typename T>
+__device__ __forceinline__ void load_weight(float (&o)[8], const void *w, int w_f32, int i, int tid, int threads, int64_t cols) {
+    if (w == nullptr) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = 1.0f;
+    } else if (w_f32) {
+        const Pack8<float> v = load_chunk<VEC>(static_cast<const float *>(w), i, tid, threads, cols);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = v.get(e);
+    } else {
+        const Pack8<T> v = load_chunk<VEC>(static_cast<const T *>(w), i, tid, threads, cols);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = to_float(v.get(e));
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// The sum of `a` and the largest `m` over the row's threads (a warp, or the CTA).
+// `buf`: 2 x 32 words that no thread still reads.
+template <bool WARP, bool MAX>
+__device__ __forceinline__ void reduce_row(float &a, uint32_t &m, uint32_t *buf) {
+    a = warp_sum(a);
+    if constexpr (MAX) m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if constexpr (!WARP) {
+        const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+        if (lane == 0) {
+            buf[warp] = __float_as_uint(a);
+            if constexpr (MAX) buf[32 + warp] = m;
+        }
+        __syncthreads();
+        a = warp_sum(lane < warps ? __uint_as_float(buf[lane]) : 0.0f);
+        if constexpr (MAX) m = __reduce_max_sync(0xFFFFFFFFu, lane < warps ? buf[32 + lane] : 0u);
+    }
+}
+
+__device__ __forceinline__ float inverse_rms(float squares, float inv_cols, float eps) {
+    return __frcp_rn(__fsqrt_rn(__fmaf_rn(squares, inv_cols, eps)));
+}
+
+// Row s of a chunk: x, or x + residual rounded to the type, which is also stored.
+template <bool VEC, typename T>
+__device__ __forceinline__ Pack8<T> sum_chunk(const NormArgs &a, int64_t row, int i, int tid, int threads) {
+    Pack8<T> v = load_chunk<VEC>(static_cast<const T *>(a.x) + row * a.ldx, i, tid, threads, a.cols);
+    if (a.res != nullptr) {
+        const Pack8<T> r = load_chunk<VEC>(static_cast<const T *>(a.res) + row * a.ldr, i, tid, threads, a.cols);
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = __fadd_rn(to_float(v.get(e)), to_float(r.get(e)));
+        v = round8<T>(f);
+    }
+    return v;
+}
+
+// 127 t / a rounded to nearest, ties to even: the FP32 quotient `v` (within 2^-15) is
+// decided in 64 bits, where both products are exact, when it lies next to a border.
+__device__ __forceinline__ int code_of(float t, float a, float inverse) {
+    const float v = __fmul_rn(t, inverse);
+    float q = rintf(v);
+    if (fabsf(v - q) > 0.49995f) {
+        const float low = floorf(v);
+        const double d = 127.0 * double(t) - (double(low) + 0.5) * double(a);
+        q = d > 0.0 ? low + 1.0f : d < 0.0 ? low : 2.0f * rintf(0.5f * low + 0.25f);
+    }
+    return int(q);
+}
+
+__device__ __forceinline__ float lift_of(float largest) { return largest < 0x1p-100f ? 0x1p100f : 1.0f; }
+
+// One chunk's outputs.  `r`: 1 / rms; 8 bits: `largest` the row's largest |t|.
+template <bool VEC, bool S8, typename T>
+__device__ __forceinline__ void put_chunk(const NormArgs &a, int64_t row, const Pack8<T> &s, float r, float largest,
+                                          float inverse, bool finite, int i, int tid, int threads) {
+    float w[8];
+    load_weight<VEC, T>(w, a.w, a.w_f32, i, tid, threads, a.cols);
+    if constexpr (!S8) {
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = __fmul_rn(__fmul_rn(to_float(s.get(e)), r), w[e]);
+        store_chunk<VEC>(static_cast<T *>(a.y) + row * a.ldy, round8<T>(o), i, tid, threads, a.cols);
+    } else {
+        // (The smallest rows are lifted, exactly, so that 127 / a is a number.)
+        const float lift = lift_of(largest), a_lifted = __fmul_rn(largest, lift);
+        int q[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            q[e] = finite && largest > 0.0f
+                       ? code_of(__fmul_rn(__fmul_rn(to_float(s.get(e)), w[e]), lift), a_lifted, inverse)
+                       : 0;
+        int8_t *p = static_cast<int8_t *>(a.y) + row * a.ldy;
+        if constexpr (VEC) {
+            const int64_t c = column<true>(i, 0, tid, threads);
+            if (c + 8 <= a.cols) {
+                uint32_t lo = 0, hi = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    lo |= (uint32_t(q[e]) & 255u) << (8 * e);
+                    hi |= (uint32_t(q[e + 4]) & 255u) << (8 * e);
+                }
+                *reinterpret_cast<uint2 *>(p + c) = make_uint2(lo, hi);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (c + e < a.cols) p[c + e] = int8_t(q[e]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int64_t c = column<false>(i, e, tid, threads);
+                if (c < a.cols) p[c] = int8_t(q[e]);
+            }
+        }
+    }
+}
+
+// A row per CTA, or (WARP) per warp; CH chunks of eight elements per thread.
+template <typename T, bool S8, bool VEC, int CH, bool WARP>
+__global__ void __launch_bounds__(CH == 1 ? 1024 : 512) norm_kernel(const NormArgs a) {
+    __shared__ uint32_t buf[64];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int threads = WARP ? 32 : int(blockDim.x), tid = WARP ? int(threadIdx.x) % 32 : int(threadIdx.x);
+    const int64_t row = WARP ? int64_t(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32 : int64_t(blockIdx.x);
+    if (row >= a.rows) return;  // (whole warps, and never with a CTA per row)
+    Pack8<T> s[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) s[i] = sum_chunk<VEC, T>(a, row, i, tid, threads);
+    float squares = 0.0f;
+    uint32_t largest = 0;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) squares = __fmaf_rn(to_float(s[i].get(e)), to_float(s[i].get(e)), squares);
+        if constexpr (S8) {
+            float w[8];
+            load_weight<VEC, T>(w, a.w, a.w_f32, i, tid, threads, a.cols);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                largest = max(largest, column<VEC>(i, e, tid, threads) < a.cols
+                                           ? __float_as_uint(__fmul_rn(to_float(s[i].get(e)), w[e])) & 0x7FFFFFFFu
+                                           : 0u);
+        }
+        if (a.res != nullptr)
+            store_chunk<VEC>(static_cast<T *>(a.sum) + row * a.lds, s[i], i, tid, threads, a.cols);
+    }
+    reduce_row<WARP, S8>(squares, largest, buf);
+    const float r = inverse_rms(squares, a.inv_cols, a.eps);
+    const float big = __uint_as_float(largest);
+    const bool finite = largest < kInfBits;
+    const float inverse = S8 ? __fdiv_rn(127.0f, __fmul_rn(big, lift_of(big))) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) put_chunk<VEC, S8>(a, row, s[i], r, big, inverse, finite, i, tid, threads);
+    if (S8 && tid == 0)
+        a.scale[row] = finite ? __fdiv_rn(__fmul_rn(big, r), 127.0f) : __uint_as_float(0x7FC00000u);
+}
+
+// Rows beyond the registers: s is read again after the sums (by the thread that
+// stored it).
+template <typename T, bool S8, bool VEC>
+__global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
+    __shared__ uint32_t buf[64];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int threads = int(blockDim.x), tid = int(threadIdx.x);
+    const int64_t row = blockIdx.x;
+    const int chunks = int((a.cols + int64_t(8) * threads - 1) / (int64_t(8) * threads));
+    float squares = 0.0f;
+    uint32_t largest = 0;
+    for (int i = 0; i < chunks; ++i) {
+        const Pack8<T> s = sum_chunk<VEC, T>(a, row, i, tid, threads);
+        float part = 0.0f;  // (chunk by chunk: long sums stay exact to a few ulps)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) part = __fmaf_rn(to_float(s.get(e)), to_float(s.get(e)), part);
+        squares += part;
+        if constexpr (S8) {
+            float w[8];
+            load_weight<VEC, T>(w, a.w, a.w_f32, i, tid, threads, a.cols);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                largest = max(largest, column<VEC>(i, e, tid, threads) < a.cols
+                                           ? __float_as_uint(__fmul_rn(to_float(s.get(e)), w[e])) & 0x7FFFFFFFu
+                                           : 0u);
+        }
+        if (a.res != nullptr) store_chunk<VEC>(static_cast<T *>(a.sum) + row * a.lds, s, i, tid, threads, a.cols);
+    }
+    reduce_row<false, S8>(squares, largest, buf);
+    const float r = inverse_rms(squares, a.inv_cols, a.eps);
+    const float big = __uint_as_float(largest);
+    const bool finite = largest < kInfBits;
+    const float inverse = S8 ? __fdiv_rn(127.0f, __fmul_rn(big, lift_of(big))) : 0.0f;
+    const T *again = a.res != nullptr ? static_cast<const T *>(a.sum) + row * a.lds : static_cast<const T *>(a.x) + row * a.ldx;
+    for (int i = 0; i < chunks; ++i) {
+        const Pack8<T> s = load_chunk<VEC>(again, i, tid, threads, a.cols);
+        put_chunk<VEC, S8>(a, row, s, r, big, inverse, finite, i, tid, threads);
+    }
+    if (S8 && tid == 0)
+        a.scale[row] = finite ? __fdiv_rn(__fmul_rn(big, r), 127.0f) : __uint_as_float(0x7FC00000u);
+}
+
+// ------------------------------------------------------------ gradient
+// With g = dy w, n columns and u = s r: dx = r (g - u m) (+ ds), m = r sum(g s) / n, dw =
+// sum over rows of dy u.  Both row sums are reduced together.
+__device__ __forceinline__ void reduce_two(float &p, float &q, float2 *buf) {
+    p = warp_sum(p);
+    q = warp_sum(q);
+    const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (lane == 0) buf[warp] = make_float2(p, q);
+    __syncthreads();
+    const float2 v = lane < warps ? buf[lane] : make_float2(0.0f, 0.0f);
+    p = warp_sum(v.x);
+    q = warp_sum(v.y);
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void grad_chunk(const GradArgs &a, int64_t row, const Pack8<T> &s, const Pack8<T> &dy, float r,
+                                           float m, float (&acc)[8], int i, int tid, int threads) {
+    float w[8], o[8];
+    load_weight<VEC, T>(w, a.w, a.w_f32, i, tid, threads, a.cols);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float sv = to_float(s.get(e)), dv = to_float(dy.get(e));
+        const float u = __fmul_rn(sv, r);
+        o[e] = __fmul_rn(r, __fmaf_rn(-u, m, __fmul_rn(dv, w[e])));
+        acc[e] = __fmaf_rn(dv, u, acc[e]);
+    }
+    if (a.ds != nullptr) {
+        const Pack8<T> d = load_chunk<VEC>(static_cast<const T *>(a.ds) + row * a.ldds, i, tid, threads, a.cols);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = __fadd_rn(o[e], to_float(d.get(e)));
+    }
+    store_chunk<VEC>(static_cast<T *>(a.dx) + row * a.lddx, round8<T>(o), i, tid, threads, a.cols);
+}
+
+// A CTA takes rows blockIdx.x, + gridDim.x, ... and holds its columns' sums of the
+// weight's gradient in registers; they leave as one row of partial sums per CTA,
+// which column_sums_kernel adds in order.
+template <typename T, bool VEC, int CH>
+__global__ void __launch_bounds__(512) grad_kernel(const GradArgs a) {
+    __shared__ float2 buf[2][32];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int threads = int(blockDim.x), tid = int(threadIdx.x);
+    float acc[CH][8];
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[i][e] = 0.0f;
+    int b = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, b ^= 1) {
+        Pack8<T> s[CH], dy[CH];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            s[i] = load_chunk<VEC>(static_cast<const T *>(a.s) + row * a.lds, i, tid, threads, a.cols);
+            dy[i] = load_chunk<VEC>(static_cast<const T *>(a.dy) + row * a.lddy, i, tid, threads, a.cols);
+        }
+        float squares = 0.0f, gs = 0.0f;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            float w[8];
+            load_weight<VEC, T>(w, a.w, a.w_f32, i, tid, threads, a.cols);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float sv = to_float(s[i].get(e));
+                squares = __fmaf_rn(sv, sv, squares);
+                gs = __fmaf_rn(__fmul_rn(to_float(dy[i].get(e)), w[e]), sv, gs);
+            }
+        }
+        reduce_two(squares, gs, buf[b]);
+        const float r = inverse_rms(squares, a.inv_cols, a.eps);
+        const float m = __fmul_rn(r, __fmul_rn(gs, a.inv_cols));
+#pragma unroll
+        for (int i = 0; i < CH; ++i) grad_chunk<T, VEC>(a, row, s[i], dy[i], r, m, acc[i], i, tid, threads);
+    }
+    float *part = a.part + int64_t(blockIdx.x) * a.cols;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int64_t c = column<VEC>(i, e, tid, threads);
+            if (c < a.cols) part[c] = acc[i][e];
+        }
+}
+
+// Longer rows: the sums of every row first, then columns in pieces of 8 per thread
+// (blockIdx.x) for the rows of each blockIdx.y.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(1024) grad_stats_kernel(const GradArgs a) {
+    __shared__ float2 buf[32];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int threads = int(blockDim.x), tid = int(threadIdx.x);
+    const int64_t row = blockIdx.x;
+    const int chunks = int((a.cols + int64_t(8) * threads - 1) / (int64_t(8) * threads));
+    float squares = 0.0f, gs = 0.0f;
+    for (int i = 0; i < chunks; ++i) {
+        const Pack8<T> s = load_chunk<VEC>(static_cast<const T *>(a.s) + row * a.lds, i, tid, threads, a.cols);
+        const Pack8<T> dy = load_chunk<VEC>(static_cast<const T *>(a.dy) + row * a.lddy, i, tid, threads, a.cols);
+        float w[8], p = 0.0f, q = 0.0f;
+        load_weight<VEC, T>(w, a.w, a.w_f32, i, tid, threads, a.cols);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float sv = to_float(s.get(e));
+            p = __fmaf_rn(sv, sv, p);
+            q = __fmaf_rn(__fmul_rn(to_float(dy.get(e)), w[e]), sv, q);
+        }
+        squares += p;
+        gs += q;
+    }
+    reduce_two(squares, gs, buf);
+    const float r = inverse_rms(squares, a.inv_cols, a.eps);
+    if (tid == 0) a.stat[row] = make_float2(r, __fmul_rn(r, __fmul_rn(gs, a.inv_cols)));
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) grad_columns_kernel(const GradArgs a) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int threads = int(blockDim.x), tid = int(threadIdx.x), i = int(blockIdx.x);
+    float acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+    for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+        const Pack8<T> s = load_chunk<VEC>(static_cast<const T *>(a.s) + row * a.lds, i, tid, threads, a.cols);
+        const Pack8<T> dy = load_chunk<VEC>(static_cast<const T *>(a.dy) + row * a.lddy, i, tid, threads, a.cols);
+        const float2 st = a.stat[row];
+        grad_chunk<T, VEC>(a, row, s, dy, st.x, st.y, acc, i, tid, threads);
+    }
+    float *part = a.part + int64_t(blockIdx.y) * a.cols;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int64_t c = column<VEC>(i, e, tid, threads);
+        if (c < a.cols) part[c] = acc[e];
+    }
+}
+
+// dw[c] = sum over p of part[p][c]: 32 columns per CTA, eight warps a share of p each,
+// added in order.
+__global__ void __launch_bounds__(256) column_sums_kernel(const float *part, int parts, int64_t cols, float *dw) {
+    __shared__ float sums[8][32];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int64_t c = int64_t(blockIdx.x) * 32 + lane;
+    float v = 0.0f;
+    if (c < cols) {
+#pragma unroll 8
+        for (int p = warp; p < parts; p += 8) v += part[int64_t(p) * cols + c];
+    }
+    sums[warp][lane] = v;
+    __syncthreads();
+    if (warp == 0 && c < cols) {
+        float t = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t += sums[k][lane];
+        dw[c] = t;
+    }
+}
+
+// ------------------------------------------------------------ host side
+constexpr int64_t kMaxDimN = int64_t(1) << 30;
+constexpr int64_t kMaxLdN = int64_t(1) << 36;
+
+int bytes_of(int type) { return type == PTC_OUT_F32 ? 4 : 2; }
+bool type_known(int type) { return type == PTC_OUT_F32 || type == PTC_OUT_BF16 || type == PTC_OUT_F16; }
+bool aligned_to(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+bool wide(const void *p, int64_t ld, int esize) { return aligned_to(p, 16) && (ld * esize) % 16 == 0; }
+
+template <typename... P, typename... A>
+cudaError_t launch_norm(void (*fn)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[1];
+    std::memset(&cfg, 0, sizeof(cfg));
+    std::memset(attr, 0, sizeof(attr));
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(unsigned(threads), 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    if (pdl_enabled()) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.numAttrs = 1;
+    }
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
+    if (e == cudaSuccess) note_launches(1);
+    return e;
+}
+
+int round32(int64_t n) { return int((n + 31) / 32 * 32); }
+
+// A few rows take a thread per eight elements, so that a row is one round of loads; many
+// take four rounds per thread, whose loads are in flight together; rows of up to 1024
+// elements a warp each.
+template <typename T, bool S8, bool VEC>
+cudaError_t run_norm(const NormArgs &a, int sms, cudaStream_t s) {
+    const int64_t chunks = (a.cols + 7) / 8;
+    if (chunks > 4 * 512 && !(chunks <= 1024 && a.rows <= sms))
+        return launch_norm(norm_long_kernel<T, S8, VEC>, dim3(unsigned(a.rows)), 1024, s, a);
+    if (a.rows > 2 * sms && chunks <= 128) {
+        const dim3 grid(unsigned((a.rows + 7) / 8));
+        return chunks <= 32 ? launch_norm(norm_kernel<T, S8, VEC, 1, true>, grid, 256, s, a)
+                            : launch_norm(norm_kernel<T, S8, VEC, 4, true>, grid, 256, s, a);
+    }
+    const dim3 grid = dim3(unsigned(a.rows));
+    if ((a.rows <= sms && chunks <= 1024) || chunks <= 32)
+        return launch_norm(norm_kernel<T, S8, VEC, 1, false>, grid, round32(chunks), s, a);
+    return launch_norm(norm_kernel<T, S8, VEC, 4, false>, grid, round32((chunks + 3) / 4), s, a);
+}
+
+template <bool S8>
+int start_norm(NormArgs a, int type, int out_esize, cudaStream_t s) {
+    int sms;
+    const int rc = usable_device(&sms);
+    if (rc) return rc;
+    const int es = bytes_of(type);
+    if (a.rows == 1) a.ldx = a.ldr = a.lds = a.ldy = 0;  // (one row has no pitch)
+    const bool vec = wide(a.x, a.ldx, es) && (!a.res || (wide(a.res, a.ldr, es) && wide(a.sum, a.lds, es))) &&
+                     (S8 ? aligned_to(a.y, 8) && a.ldy % 8 == 0 : wide(a.y, a.ldy, out_esize)) && aligned_to(a.w, 16);
+    auto go = [&](auto t) {
+        using T = decltype(t);
+        return vec ? run_norm<T, S8, true>(a, sms, s) : run_norm<T, S8, false>(a, sms, s);
+    };
+    const cudaError_t e = type == PTC_OUT_F32 ? go(float()) : type == PTC_OUT_BF16 ? go(__nv_bfloat16()) : go(__half());
+    return e == cudaSuccess ? PTC_OK : fail_launch(e, "norm launch");
+}
+
+int check_sizes_n(int64_t rows, int64_t cols, int type, int w_type, float eps) {
+    if (rows < 0 || cols < 0 || rows > kMaxDimN || cols > kMaxDimN)
+        return fail_status(PTC_ERR_INVALID, "sizes must satisfy 0 <= rows, cols <= 2^30");
+    if (!type_known(type) || (w_type != type && w_type != PTC_OUT_F32))
+        return fail_status(PTC_ERR_INVALID, "unknown element type, or a weight that is neither float32 nor of x's type");
+    if (!(eps >= 0.0f) || eps > 3.0e38f) return fail_status(PTC_ERR_INVALID, "eps must be finite and not negative");
+    return PTC_OK;
+}
+
+int check_rows(const void *p, int64_t cols, int64_t ld, int esize) {
+    if (!p || ld < cols || ld > kMaxLdN)
+        return fail_status(PTC_ERR_INVALID, "a matrix is NULL, or its leading dimension is not cols .. 2^36");
+    if (!aligned_to(p, uintptr_t(esize))) return fail_status(PTC_ERR_ALIGN, "matrices must be aligned to their elements");
+    return PTC_OK;
+}
+
+// `same`: an output may be exactly this input (a thread reads what it writes first).
+bool clashes(const ByteRows &out, const ByteRows &in, bool same) {
+    return rows_overlap(out, in) && !(same && out.p == in.p && (out.pitch == in.pitch || out.rows == 1));
+}
+
+// The checks that both forms share; `y` the output's bytes.
+int check_norm(int64_t rows, int64_t cols, const void *x, int64_t ldx, int type, const void *res, int64_t ldr, void *sum,
+               int64_t lds, const void *w, int w_type, const ByteRows &y, bool same) {
+    const int es = bytes_of(type);
+    int rc = check_rows(x, cols, ldx, es);
+    if (!rc && res) rc = check_rows(res, cols, ldr, es);
+    if (!rc && res) rc = check_rows(sum, cols, lds, es);
+    if (rc) return rc;
+    if (!res && sum) return fail_status(PTC_ERR_INVALID, "a sum is written only with a residual");
+    if (w && !aligned_to(w, uintptr_t(bytes_of(w_type)))) return fail_status(PTC_ERR_ALIGN, "weight must be aligned to its elements");
+    const ByteRows bx = elem_rows(x, rows, cols, ldx, es), br = elem_rows(res, rows, cols, ldr, es),
+                   bs = elem_rows(sum, rows, cols, lds, es), bw = flat_bytes(w, uint64_t(cols) * uint64_t(bytes_of(w_type)));
+    if (clashes(y, bx, same) || clashes(y, br, same) || rows_overlap(y, bs) || rows_overlap(y, bw) || clashes(bs, bx, true) ||
+        clashes(bs, br, true) || rows_overlap(bs, bw))
+        return fail_status(PTC_ERR_OVERLAP, "an output overlaps another argument");
+    return PTC_OK;
+}
+
+NormArgs norm_args(int64_t rows, int64_t cols, const void *x, int64_t ldx, const void *res, int64_t ldr, void *sum,
+                   int64_t lds, const void *w, int w_type, float eps, void *y, int64_t ldy, float *scale) {
+    NormArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = x;
+    a.ldx = ldx;
+    a.res = res;
+    a.ldr = ldr;
+    a.sum = sum;
+    a.lds = lds;
+    a.w = w;
+    a.w_f32 = w_type == PTC_OUT_F32;
+    a.y = y;
+    a.ldy = ldy;
+    a.scale = scale;
+    a.rows = rows;
+    a.cols = cols;
+    a.eps = eps;
+    a.inv_cols = float(1.0 / double(cols));
+    return a;
+}
+
+// Partial sums of the weight's gradient: rows of them, and of the row pieces of long rows.
+constexpr int kMaxParts = 512;
+bool grad_long(int64_t cols) { return cols > 16384; }
+int64_t grad_parts(int64_t rows) { return std::min<int64_t>(rows, kMaxParts); }
+
+template <typename T, bool VEC>
+cudaError_t run_grad(GradArgs a, int sms, float *dw, cudaStream_t s) {
+    const int64_t chunks = (a.cols + 7) / 8;
+    int parts;
+    cudaError_t e;
+    if (grad_long(a.cols)) {
+        const int64_t pieces = (chunks + 255) / 256;
+        parts = int(std::min<int64_t>(grad_parts(a.rows), std::max<int64_t>(1, 8 * int64_t(sms) / pieces)));
+        e = launch_norm(grad_stats_kernel<T, VEC>, dim3(unsigned(a.rows)), 1024, s, a);
+        if (e == cudaSuccess) e = launch_norm(grad_columns_kernel<T, VEC>, dim3(unsigned(pieces), unsigned(parts)), 256, s, a);
+    } else {
+        const int ch = chunks <= 256 ? 1 : chunks <= 1024 ? 2 : 4;
+        const int threads = round32((chunks + ch - 1) / ch);
+        const int per_sm = std::max(1, (sizeof(T) == 2 && ch <= 2 ? 1024 : 512) / threads);
+        parts = int(std::min<int64_t>(grad_parts(a.rows), int64_t(sms) * std::min(per_sm, 3)));
+        const dim3 grid = dim3(unsigned(parts));
+        e = ch == 1   ? launch_norm(grad_kernel<T, VEC, 1>, grid, threads, s, a)
+            : ch == 2 ? launch_norm(grad_kernel<T, VEC, 2>, grid, threads, s, a)
+                      : launch_norm(grad_kernel<T, VEC, 4>, grid, threads, s, a);
+    }
+    if (e == cudaSuccess)
+        e = launch_norm(column_sums_kernel, dim3(unsigned((a.cols + 31) / 32)), 256, s, static_cast<const float *>(a.part), parts,
+                        a.cols, dw);
+    return e;
+}
+
+}  // namespace
+}  // namespace ptc
+
+using namespace ptc;
+
+extern "C" {
+
+int ptc_rms_norm(int64_t rows, int64_t cols, const void *x, int64_t ldx, int type, const void *residual, int64_t ldr,
+                 void *sum, int64_t lds, const void *weight, int weight_type, float eps, void *y, int64_t ldy, void *stream) {
+    set_message("");
+    int rc = check_sizes_n(rows, cols, type, weight_type, eps);
+    if (rc || rows == 0 || cols == 0) return rc;
+    rc = check_rows(y, cols, ldy, bytes_of(type));
+    if (!rc)
+        rc = check_norm(rows, cols, x, ldx, type, residual, ldr, sum, lds, weight, weight_type,
+                        elem_rows(y, rows, cols, ldy, bytes_of(type)), true);
+    if (rc) return rc;
+    return start_norm<false>(norm_args(rows, cols, x, ldx, residual, ldr, sum, lds, weight, weight_type, eps, y, ldy, nullptr),
+                             type, bytes_of(type), static_cast<cudaStream_t>(stream));
+}
+
+int ptc_rms_norm_s8(int64_t rows, int64_t cols, const void *x, int64_t ldx, int type, const void *residual, int64_t ldr,
+                    void *sum, int64_t lds, const void *weight, int weight_type, float eps, int8_t *codes, int64_t ldc,
+                    float *scale, void *stream) {
+    set_message("");
+    int rc = check_sizes_n(rows, cols, type, weight_type, eps);
+    if (rc || rows == 0 || cols == 0) return rc;
+    rc = check_rows(codes, cols, ldc, 1);
+    if (rc) return rc;
+    if (!scale) return fail_status(PTC_ERR_INVALID, "scale is NULL");
+    if (!aligned_to(scale, 4)) return fail_status(PTC_ERR_ALIGN, "scale must be 4-byte aligned");
+    const ByteRows c = elem_rows(codes, rows, cols, ldc, 1), sc = flat_bytes(scale, uint64_t(rows) * 4);
+    const int es = bytes_of(type);
+    rc = check_norm(rows, cols, x, ldx, type, residual, ldr, sum, lds, weight, weight_type, c, false);
+    if (rc) return rc;
+    if (rows_overlap(sc, c) || rows_overlap(sc, elem_rows(x, rows, cols, ldx, es)) ||
+        rows_overlap(sc, elem_rows(residual, rows, cols, ldr, es)) || rows_overlap(sc, elem_rows(sum, rows, cols, lds, es)) ||
+        rows_overlap(sc, flat_bytes(weight, uint64_t(cols) * uint64_t(bytes_of(weight_type)))))
+        return fail_status(PTC_ERR_OVERLAP, "an output overlaps another argument");
+    return start_norm<true>(norm_args(rows, cols, x, ldx, residual, ldr, sum, lds, weight, weight_type, eps, codes, ldc, scale),
+                            type, 1, static_cast<cudaStream_t>(stream));
+}
+
+int64_t ptc_rms_norm_backward_workspace(int64_t rows, int64_t cols) {
+    if (rows <= 0 || cols <= 0 || rows > kMaxDimN || cols > kMaxDimN) return 0;
+    return grad_parts(rows) * cols * 4 + (grad_long(cols) ? rows * 8 + 16 : 0);
+}
+
+int ptc_rms_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t lddy, const void *s, int64_t lds, int type,
+                          const void *ds, int64_t ldds, const void *weight, int weight_type, float eps, void *dx, int64_t lddx,
+                          float *dweight, void *workspace, int64_t workspace_bytes, void *stream) {
+    set_message("");
+    int rc = check_sizes_n(rows, cols, type, weight_type, eps);
+    if (rc || cols == 0) return rc;
+    if (!dweight) return fail_status(PTC_ERR_INVALID, "dweight is NULL");
+    if (!aligned_to(dweight, 4)) return fail_status(PTC_ERR_ALIGN, "dweight must be 4-byte aligned");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int sms;
+    if (rows == 0) {  // the empty sum
+        if ((rc = usable_device(&sms))) return rc;
+        const cudaError_t e = launch_norm(column_sums_kernel, dim3(unsigned((cols + 31) / 32)), 256, st,
+                                          static_cast<const float *>(nullptr), 0, cols, dweight);
+        return e == cudaSuccess ? PTC_OK : fail_launch(e, "norm gradient launch");
+    }
+    const int es = bytes_of(type);
+    rc = check_rows(dy, cols, lddy, es);
+    if (!rc) rc = check_rows(s, cols, lds, es);
+    if (!rc && ds) rc = check_rows(ds, cols, ldds, es);
+    if (!rc) rc = check_rows(dx, cols, lddx, es);
+    if (rc) return rc;
+    if (weight && !aligned_to(weight, uintptr_t(bytes_of(weight_type))))
+        return fail_status(PTC_ERR_ALIGN, "weight must be aligned to its elements");
+    const int64_t need = ptc_rms_norm_backward_workspace(rows, cols);
+    if (!workspace || workspace_bytes < need) return fail_status(PTC_ERR_INVALID, "the workspace is too small");
+    if (!aligned_to(workspace, 16)) return fail_status(PTC_ERR_ALIGN, "the workspace must be 16-byte aligned");
+    const ByteRows in[4] = {elem_rows(dy, rows, cols, lddy, es), elem_rows(s, rows, cols, lds, es),
+                            elem_rows(ds, rows, cols, ldds, es), flat_bytes(weight, uint64_t(cols) * uint64_t(bytes_of(weight_type)))};
+    const ByteRows bx = elem_rows(dx, rows, cols, lddx, es), bw = flat_bytes(dweight, uint64_t(cols) * 4),
+                   bk = flat_bytes(workspace, uint64_t(need));
+    bool bad = rows_overlap(bx, bw) || rows_overlap(bx, bk) || rows_overlap(bw, bk);
+    for (int i = 0; i < 4; ++i)  // (with long rows dy and s are read by other threads than those that write dx)
+        bad = bad || clashes(bx, in[i], i < 3) || rows_overlap(bw, in[i]) || rows_overlap(bk, in[i]);
+    if (bad) return fail_status(PTC_ERR_OVERLAP, "an output overlaps another argument");
+    if ((rc = usable_device(&sms))) return rc;
+    GradArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.dy = dy;
+    a.lddy = lddy;
+    a.s = s;
+    a.lds = lds;
+    a.ds = ds;
+    a.ldds = ldds;
+    a.w = weight;
+    a.w_f32 = weight_type == PTC_OUT_F32;
+    a.dx = dx;
+    a.lddx = lddx;
+    a.part = static_cast<float *>(workspace);
+    a.stat = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + (grad_parts(rows) * cols * 4 + 15) / 16 * 16);
+    a.rows = rows;
+    a.cols = cols;
+    a.eps = eps;
+    a.inv_cols = float(1.0 / double(cols));
+    if (rows == 1) a.lddy = a.lds = a.ldds = a.lddx = 0;  // (one row has no pitch)
+    const bool vec = wide(dy, a.lddy, es) && wide(s, a.lds, es) && wide(dx, a.lddx, es) && (!ds || wide(ds, a.ldds, es)) &&
+                     aligned_to(weight, 16);
+    auto go = [&](auto t) {
+        using T = decltype(t);
+        return vec ? run_grad<T, true>(a, sms, dweight, st) : run_grad<T, false>(a, sms, dweight, st);
+    };
+    const cudaError_t e = type == PTC_OUT_F32 ? go(float()) : type == PTC_OUT_BF16 ? go(__nv_bfloat16()) : go(__half());
+    return e == cudaSuccess ? PTC_OK : fail_launch(e, "norm gradient launch");
+}
+
+}  // extern "C"
