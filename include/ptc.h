@@ -15,6 +15,7 @@
  * and, beside the study, the 4-bit floating-point operators that language models
  * train and decode with: gemm_fp4, gemm_a16_fp4, ptc_quantize_fp4,
  * ptc_dequantize_fp4, ptc_dropout and ptc_dropout_to (see "Microscaled 4-bit matrices" below),
+ * the product of a few tokens with 4-bit integer weights that have group scales, gemm_a16_s4,
  * and the norm before a product, ptc_rms_norm, ptc_rms_norm_s8 and ptc_rms_norm_backward.
  *
  * The first three compute C <- A.B exactly as the plain sum over k, with C
@@ -431,6 +432,36 @@ int gemm_a16_fp4(int64_t M, int64_t N, int64_t K, int type, const void *X, int64
                  int64_t ldw, const void *SW, const float *GW, void *C, int64_t ldc, void *stream);
 
 /*
+ * 4-bit integer weights with group scales
+ * ---------------------------------------
+ * A matrix of R rows of K weights w = (c - z) s:
+ *   codes   c in -8 .. 7, the packed INT4 of gemm_s4 (two's complement, two per byte, the
+ *           even element in the low nibble).  Row r starts at byte r * pitch; pitch is a
+ *           multiple of 16 and at least ceil(K / 2).  A nibble past K may hold anything.
+ *   group   consecutive codes of a row that share s and z: 32, 64 or a multiple of 128
+ *           (at least K: one per row); the last group may be shorter
+ *   scales  s, bfloat16 or binary16 (scale_type, PTC_OUT_*), in tiles of 16 rows: that of
+ *           row r and group g at element ((r / 16) * ceil(K / group) + g) * 16 + r % 16.
+ *           The buffer holds whole tiles; those of rows past R may hold anything.
+ *   zeros   z, of the scales' type and layout, any numbers (NULL: 0)
+ * Codes, scales and zeros are 16-byte aligned.
+ *
+ * C[M x N] = out( sum over groups g of s_jg sum_{k in g} x_ik (c_jk - z_jg) ): a few rows
+ * (tokens) of bfloat16 or binary16 activations X (`type`, ldx elements apart) with such a
+ * matrix W of N rows of K (ldw bytes apart); C has X's type.  Products are exact and sums
+ * FP32: a group's is taken of x (c + 8) less (8 + z) times that of x.  Activations are
+ * taken as binary16 relative to a power of two per token and 32, 64 or 128 elements, which
+ * is exact down to 2^-28 of the largest of them and off by at most 2^-35 of it below.
+ * A token with an infinity or NaN gives NaN; other tokens do not see it.
+ * Meant for M up to 16, where W is read once; more rows are taken 16 at a time.  X and C
+ * are aligned to the element.  K == 0 writes zeros.  No workspace is used.  Results are the
+ * same from call to call; the summation order depends on the sizes (and the keys
+ * s4_tokens_rows, s4_tokens_split, s4_tokens_tiles).
+ */
+int gemm_a16_s4(int64_t M, int64_t N, int64_t K, int type, const void *X, int64_t ldx, const void *W, int64_t ldw,
+                int64_t group, int scale_type, const void *scales, const void *zeros, void *C, int64_t ldc, void *stream);
+
+/*
  * Root-mean-square norm of rows
  * -----------------------------
  *   s = x, or x + residual in FP32 rounded to x's type, which is stored in `sum`
@@ -540,7 +571,7 @@ int ptc_last_launch(int *grid, int *cluster, int *ksplit, int *tile_n);
 
 /* The same of the calling thread's last 4-bit product: *tile = output columns per
  * tile of gemm_fp4 (256: CTA pairs, 128, 64), or rows of the weights per CTA of
- * gemm_a16_fp4 (128, 64, 32, 16). */
+ * gemm_a16_fp4 (128, 64, 32, 16) and gemm_a16_s4 (256 to 16). */
 int ptc_last_fp4_launch(int64_t *grid, int *cluster, int *ksplit, int *tile);
 
 /* Operand conversion of the calling thread's last GEMM call through this
@@ -694,6 +725,10 @@ int ptc_last_conversion(int *mode);
  *                  size, 1, 2, 4 or 8.  A pair of these that the sizes do not allow
  *                  (each share has at least 256 of K, and a share's activations fit
  *                  their buffer) is not taken.
+ *   "s4_tokens_rows", "s4_tokens_split" the same of gemm_a16_s4, whose shares of K take
+ *                  at least 128.
+ *   "s4_tokens_tiles" gemm_a16_s4's tiles of 16 rows per row group: 0 (default) by size,
+ *                  1 or 2.
  * No accepted value of any key changes an INT8 or INT4 result. */
 int ptc_set_tuning(const char *key, int64_t value);
 

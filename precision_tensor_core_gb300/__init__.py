@@ -11,7 +11,7 @@ library's CUDA kernels):
   ``gemm_s8_noalloc``, ``gemm_s8_b_rowmajor``, ``gemm_status_string``,
   ``gemm_poll_device_error``, ``ptc_kernel_launch_count``, ``ptc_last_launch``, ``ptc_last_fp4_launch``, ``ptc_last_conversion``, ``ptc_plan_shape``,
   ``ptc_debug_set_wait_limit``, ``ptc_set_tuning``, ``gemm_fp4``, ``gemm_a16_fp4``, ``ptc_dropout``,
-  ``ptc_dropout_to``, ``ptc_quantize_fp4``, ``ptc_dequantize_fp4``, ``ptc_rms_norm``, ``ptc_rms_norm_s8``,
+  ``ptc_dropout_to``, ``ptc_quantize_fp4``, ``ptc_dequantize_fp4``, ``gemm_a16_s4``, ``ptc_rms_norm``, ``ptc_rms_norm_s8``,
   ``ptc_rms_norm_backward``, ``ptc_rms_norm_backward_workspace``: the C ABI of
   ``include/ptc.h`` under the same names, taking integers (sizes, leading
   dimensions, device addresses, a cudaStream_t handle).  A nonzero status
@@ -25,6 +25,8 @@ library's CUDA kernels):
   :class:`Fp4Matrix`: counter-based dropout and microscaled 4-bit matrices on
   torch tensors of the device; :mod:`precision_tensor_core_gb300.fp4_linear`
   puts them together as a linear layer's training and decoding steps.
+* ``matmul_a16_s4`` and :class:`S4Matrix`: a few tokens with 4-bit integer weights that have
+  group scales.
 * ``rms_norm``, ``rms_norm_s8``, ``rms_norm_backward``: the norm before a product, also as
   the 8-bit operand of ``matmul_s8_scaled``.
 
@@ -107,6 +109,7 @@ def lib() -> ctypes.CDLL:
                 ("gemm_fp4", [_i64, _i64, _i64, _int, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _int,
                               _vp]),
                 ("gemm_a16_fp4", [_i64, _i64, _i64, _int, _vp, _i64, _int, _vp, _i64, _vp, _vp, _vp, _i64, _vp]),
+                ("gemm_a16_s4", [_i64, _i64, _i64, _int, _vp, _i64, _vp, _i64, _i64, _int, _vp, _vp, _vp, _i64, _vp]),
                 ("ptc_rms_norm", [_i64, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64, _vp, _int, _f32, _vp, _i64, _vp]),
                 ("ptc_rms_norm_s8", [_i64, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64, _vp, _int, _f32, _vp, _i64, _vp,
                                      _vp]),
@@ -251,6 +254,11 @@ def gemm_fp4(M, N, K, format, A, lda, SA, GA, B, ldb, SB, GB, C, ldc, out_type, 
 def gemm_a16_fp4(M, N, K, type, X, ldx, format, W, ldw, SW, GW, C, ldc, stream=0) -> int:
     """C[MxN] = X[MxK] (bfloat16 / binary16) . W[NxK]^T, W microscaled 4-bit."""
     return _check(lib().gemm_a16_fp4(M, N, K, type, X, ldx, format, W, ldw, SW, GW, C, ldc, stream))
+
+
+def gemm_a16_s4(M, N, K, type, X, ldx, W, ldw, group, scale_type, scales, zeros, C, ldc, stream=0) -> int:
+    """Few 16-bit tokens times 4-bit integer weights with group scales (include/ptc.h)."""
+    return _check(lib().gemm_a16_s4(M, N, K, type, X, ldx, W, ldw, group, scale_type, scales, zeros, C, ldc, stream))
 
 
 def ptc_rms_norm(rows, cols, x, ldx, type, residual, ldr, sum, lds, weight, weight_type, eps, y, ldy, stream=0) -> int:
@@ -516,10 +524,10 @@ def _load_native():
     L = lib()
     n.init(*(ctypes.cast(getattr(L, f), _vp).value for f in ("ptc_dropout_to", "ptc_quantize_fp4",
                                                              "ptc_dequantize_fp4", "gemm_fp4", "gemm_a16_fp4",
-                                                             "ptc_rms_norm", "ptc_rms_norm_s8",
+                                                             "gemm_a16_s4", "ptc_rms_norm", "ptc_rms_norm_s8",
                                                              "ptc_rms_norm_backward_workspace",
                                                              "ptc_rms_norm_backward")),
-           _check, _stream, Fp4Matrix)
+           _check, _stream, Fp4Matrix, S4Matrix)
     _native = n
     return n
 
@@ -632,6 +640,82 @@ def matmul_a16_fp4(x, Wt, out=None, stream=None):
     rows (more are taken 16 at a time; quantise x and use :func:`matmul_fp4`
     for many)."""
     return (_native or _load_native()).matmul_a16(x, Wt, out, stream)
+
+
+# ---------------------------------------------------------------- grouped 4-bit integer weights
+class S4Matrix:
+    """A matrix of rows of ``K`` weights (c - z) s: 4-bit integer codes c with a scale s,
+    and a zero z if given, per row and group of ``group`` codes; or several such matrices
+    of one size (the experts of :func:`moe_a16_s4`).
+
+    codes: uint8 (rows, >= ceil(K / 2)) or (experts, rows, >= ceil(K / 2)), the packed INT4
+        of :func:`matmul_s4`: two's complement, two per byte, the low nibble first, unit
+        column stride, rows (and experts) a multiple of 16 bytes apart
+    scales: contiguous bfloat16 or float16 in tiles of 16 rows (:meth:`tile_scales` makes
+        them from (rows, groups))
+    group: 32, 64 or a multiple of 128; at least K for one scale per row
+    zeros: None, or like the scales
+    """
+
+    __slots__ = ("_codes", "_scales", "_K", "_group", "_zeros")
+
+    def __init__(self, codes, scales, K, group=128, zeros=None):
+        (_native or _load_native()).check_s4(codes, scales, K, group, zeros)
+        self._codes, self._scales, self._K, self._group, self._zeros = codes, scales, K, group, zeros
+
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
+    zeros = property(lambda self: self._zeros)
+    K = property(lambda self: self._K)
+    group = property(lambda self: self._group)
+    shape = property(lambda self: (*self._codes.shape[:-1], self._K))
+    device = property(lambda self: self._codes.device)
+
+    def record_stream(self, stream):
+        """As torch.Tensor.record_stream, for every tensor of the matrix."""
+        for t in (self._codes, self._scales, self._zeros):
+            if t is not None:
+                t.record_stream(stream)
+
+    @staticmethod
+    def tile_scales(scales):
+        """(..., rows, groups) to the tiled layout (laid out once, e.g. when weights are loaded)."""
+        import torch
+        r, n = scales.shape[-2:]
+        if scales.numel() == 0:
+            return scales.reshape(-1)
+        t = torch.nn.functional.pad(scales, (0, 0, 0, -r % 16))
+        return t.reshape(*scales.shape[:-2], -1, 16, n).transpose(-1, -2).reshape(-1).contiguous()
+
+    @classmethod
+    def quantize(cls, w, group=128, zeros=False, dtype=None):
+        """Weights (rows, K) or (experts, rows, K) rounded to nearest, when they are loaded: scales
+        max |w| / 7 of a group, or with zeros (max - min) / 15 about a whole zero.  ``dtype`` of
+        the scales: w's, or bfloat16 for float32."""
+        import torch
+        dtype = dtype or (w.dtype if w.dtype in (torch.bfloat16, torch.float16) else torch.bfloat16)
+        K, groups = w.shape[-1], -(-w.shape[-1] // group)
+        v = torch.nn.functional.pad(w.detach().float(), (0, groups * group - K))
+        v = v.reshape(*w.shape[:-1], groups, group)
+        if zeros:
+            low, high = v.amin(-1).clamp(max=0), v.amax(-1).clamp(min=0)
+            scale = ((high - low) / 15).to(dtype)
+            zero = torch.where(scale > 0, -8 - low / scale.float(), 0.0).round().clamp(-8, 7).to(dtype)
+        else:
+            scale, zero = (v.abs().amax(-1) / 7).to(dtype), None
+        code = torch.where(scale.float().unsqueeze(-1) > 0, v / scale.float().unsqueeze(-1), 0.0)
+        code = code if zero is None else code + zero.float().unsqueeze(-1)
+        code = code.round().clamp(-8, 7).to(torch.int8).reshape(*w.shape[:-1], -1)[..., :K].view(torch.uint8) & 15
+        code = torch.nn.functional.pad(code, (0, -K % 32))
+        return cls((code[..., 0::2] | (code[..., 1::2] << 4)).contiguous(), cls.tile_scales(scale), K, group,
+                   None if zero is None else cls.tile_scales(zero))
+
+
+def matmul_a16_s4(x, Wt, out=None, stream=None):
+    """x (M,K) bfloat16 or float16 @ W given as Wt (N,K) :class:`S4Matrix` -> x's dtype (M,N),
+    summed in FP32: the product of a decoding step, for M up to 16 rows (more are taken 16
+    at a time)."""
+    return (_native or _load_native()).matmul_a16_s4(x, Wt, out, stream)
 
 
 # ---------------------------------------------------------------- norms on tensors

@@ -21,6 +21,7 @@
 #include "fp4.h"
 #include "internal.h"
 #include "ptc.h"
+#include "s4.h"
 
 namespace {
 
@@ -1275,7 +1276,7 @@ int ptc_set_tuning(const char *key, int64_t value) {
         g_cta_pair.store(int(value));
         return PTC_OK;
     }
-    if (ptc::set_fp4_tuning(key, value) || ptc::set_tokens_tuning(key, value)) return PTC_OK;
+    if (ptc::set_fp4_tuning(key, value) || ptc::set_tokens_tuning(key, value) || ptc::set_s4_tuning(key, value)) return PTC_OK;
     return fail(PTC_ERR_INVALID, "unknown tuning key or value out of range");
 }
 

@@ -25,14 +25,15 @@ decltype(&ptc_quantize_fp4) f_quantize;
 decltype(&ptc_dequantize_fp4) f_dequantize;
 decltype(&gemm_fp4) f_gemm;
 decltype(&gemm_a16_fp4) f_gemm_a16;
+decltype(&gemm_a16_s4) f_gemm_a16_s4;
 decltype(&ptc_rms_norm) f_norm;
 decltype(&ptc_rms_norm_s8) f_norm_s8;
 decltype(&ptc_rms_norm_backward_workspace) f_norm_workspace;
 decltype(&ptc_rms_norm_backward) f_norm_backward;
 PyObject *g_check;   // raises PtcError for a status
 PyObject *g_stream;  // a stream argument to its handle
-PyTypeObject *g_matrix;
-PyObject *s_codes, *s_scales, *s_k, *s_fmt, *s_ts;
+PyTypeObject *g_matrix, *g_s4;  // Fp4Matrix, S4Matrix
+PyObject *s_codes, *s_scales, *s_k, *s_fmt, *s_ts, *s_group, *s_zeros;
 
 struct Bad {};  // a Python exception has been set
 
@@ -191,6 +192,65 @@ Matrix matrix_of(PyObject *o) {
     return matrix(c.p, s.p, k.p, f.p, t.p);
 }
 
+// Grouped 4-bit integer weights, of one matrix or of several (experts), checked every
+// time they are used.
+struct S4 {
+    void *codes, *scales, *zeros;
+    int64_t experts, rows, pitch, expert, k, group;
+    int type;
+    bool many;
+    c10::DeviceIndex index;
+    at::Device device{at::kCPU};
+};
+
+S4 s4(PyObject *codes, PyObject *scales, PyObject *k, PyObject *group, PyObject *zeros) {
+    S4 m;
+    const at::Tensor &c = tensor(codes, "codes"), &s = tensor(scales, "scales");
+    if (c.scalar_type() != at::kByte) raise(PyExc_TypeError, "codes are uint8");
+    if (s.scalar_type() != at::kBFloat16 && s.scalar_type() != at::kHalf)
+        raise(PyExc_TypeError, "scales are bfloat16 or float16");
+    if (!c.is_cuda() || (c.dim() != 2 && c.dim() != 3)) raise(PyExc_ValueError, "codes must be a 2-D or 3-D device tensor");
+    m.many = c.dim() == 3;
+    m.experts = m.many ? c.size(0) : 1;
+    m.rows = c.size(-2);
+    m.k = integer(k);
+    m.group = integer(group);
+    if (m.k < 0 || m.k > (int64_t(1) << 30)) raise(PyExc_ValueError, "K must be 0 .. 2^30");
+    if (m.group != 32 && m.group != 64 && (m.group <= 0 || m.group % 128))
+        raise(PyExc_ValueError, "group is 32, 64 or a multiple of 128");
+    // (One row, or rows of no values, have no pitch; nor has one expert.)
+    const int64_t least = std::max<int64_t>(16, (c.size(-1) + 15) / 16 * 16);
+    m.pitch = m.rows > 1 && m.k > 0 ? c.stride(-2) : least;
+    m.expert = m.experts > 1 ? c.stride(0) : 0;
+    if (c.size(-1) < (m.k + 1) / 2 || (c.size(-1) > 1 && c.stride(-1) != 1) || m.pitch < c.size(-1) || m.pitch % 16 ||
+        m.expert % 16 || (m.experts > 1 && m.rows > 0 && m.expert < (m.rows - 1) * m.pitch + c.size(-1)))
+        raise(PyExc_ValueError, "codes must hold ceil(K / 2) bytes per row, rows (and experts) a multiple of 16 bytes apart");
+    const int64_t count = m.experts * ((m.rows + 15) / 16) * ((m.k + m.group - 1) / m.group) * 16;
+    auto tiles = [&](const at::Tensor &t, const char *name) {
+        if (t.scalar_type() != s.scalar_type() || !t.is_cuda() || t.get_device() != c.get_device() || !t.is_contiguous() ||
+            t.numel() < count) {
+            PyErr_Format(PyExc_ValueError, "%s must be contiguous, of the scales' dtype on the codes' device, and hold whole "
+                         "tiles of 16 rows", name);
+            throw Bad();
+        }
+        return t.data_ptr();
+    };
+    m.scales = tiles(s, "scales");
+    m.zeros = zeros == Py_None ? nullptr : tiles(tensor(zeros, "zeros"), "zeros");
+    m.codes = c.data_ptr();
+    m.type = s.scalar_type() == at::kHalf ? PTC_OUT_F16 : PTC_OUT_BF16;
+    m.device = c.device();
+    m.index = c.get_device();
+    return m;
+}
+
+S4 s4_of(PyObject *o) {
+    if (Py_TYPE(o) != g_s4 && !PyObject_TypeCheck(o, g_s4)) raise(PyExc_TypeError, "an S4Matrix is expected");
+    Ref c(PyObject_GetAttr(o, s_codes)), s(PyObject_GetAttr(o, s_scales)), k(PyObject_GetAttr(o, s_k)),
+        g(PyObject_GetAttr(o, s_group)), z(PyObject_GetAttr(o, s_zeros));
+    return s4(c.p, s.p, k.p, g.p, z.p);
+}
+
 at::Tensor empty(at::IntArrayRef size, at::ScalarType type, at::Device device) {
     return at::empty(size, at::TensorOptions().dtype(type).device(device));
 }
@@ -253,7 +313,7 @@ class Target {
             throw Bad();
         }
     }
-    // Of a launched call: tensors of the caller's (a tensor, a 4-bit matrix or None),
+    // Of a launched call: tensors of the caller's (a tensor, a matrix object or None),
     // and results of this stream's memory.
     void used(PyObject *o) const {
         if (elsewhere_) record(o, c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle_), caller_.device_index()));
@@ -267,7 +327,7 @@ class Target {
         if (THPVariable_Check(o)) {
             THPVariable_Unpack(o).record_stream(stream);
         } else if (o != Py_None) {
-            for (PyObject *name : {s_codes, s_scales, s_ts}) record(Ref(PyObject_GetAttr(o, name)).p, stream);
+            for (PyObject *name : {s_codes, s_scales, PyObject_TypeCheck(o, g_s4) ? s_zeros : s_ts}) record(Ref(PyObject_GetAttr(o, name)).p, stream);
         }
     }
 };
@@ -456,6 +516,32 @@ PyObject *py_matmul_a16(PyObject *, PyObject *const *a, Py_ssize_t n) {
     PTC_BODY_END
 }
 
+// (x, Wt, out, stream)
+PyObject *py_matmul_a16_s4(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    PTC_BODY_BEGIN
+    expect(n, 4);
+    const at::Tensor &x = outside_autograd(tensor(a[0], "x"), "x");
+    const int type = type_of(x.scalar_type());
+    if (type == PTC_OUT_F32) raise(PyExc_TypeError, "matmul_a16_s4 takes bfloat16 or float16 activations");
+    const Rows rx = rows_of(x, "x");
+    const S4 W = s4_of(a[1]);
+    if (W.many) raise(PyExc_ValueError, "the weights are several matrices (experts)");
+    if (rx.cols != W.k) raise(PyExc_ValueError, "inner dimensions differ");
+    if (x.get_device() != W.index || (a[2] != Py_None && tensor(a[2], "out").scalar_type() != x.scalar_type()))
+        raise(PyExc_ValueError, "x, the weights and out must share a device, x and out a dtype");
+    const Target target(W.index, a[3]);
+    at::Tensor c = result(a[2], rx.rows, W.rows, x.scalar_type(), W.index, W.device);
+    const Rows rc = rows_of(c, "out");
+    target.run([&](void *s) {
+        return f_gemm_a16_s4(rx.rows, W.rows, W.k, type, rx.p, rx.ld, W.codes, W.pitch, W.group, W.type, W.scales, W.zeros,
+                             rc.p, rc.ld, s);
+    });
+    target.used(a[0]);
+    target.used(a[1]);
+    return give(target, a[2], std::move(c));
+    PTC_BODY_END
+}
+
 // What the norms share: x, an optional tensor of x's shape, type and device, and the weight.
 const at::Tensor &same_as(const at::Tensor &x, const char *of, const at::Tensor &t, const char *name) {
     if (t.scalar_type() != x.scalar_type() || t.sizes() != x.sizes() || !t.is_cuda() || t.get_device() != x.get_device()) {
@@ -594,32 +680,48 @@ PyObject *py_check_matrix(PyObject *, PyObject *const *a, Py_ssize_t n) {
     PTC_BODY_END
 }
 
-// (addresses of the nine C entry points, status check, stream handle, Fp4Matrix)
+// (codes, scales, K, group, zeros): raises what is wrong with them
+PyObject *py_check_s4(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    PTC_BODY_BEGIN
+    expect(n, 5);
+    s4(a[0], a[1], a[2], a[3], a[4]);
+    Py_RETURN_NONE;
+    PTC_BODY_END
+}
+
+// (addresses of the ten C entry points, status check, stream handle, Fp4Matrix, S4Matrix)
 PyObject *py_init(PyObject *, PyObject *const *a, Py_ssize_t n) {
     PTC_BODY_BEGIN
-    expect(n, 12);
+    expect(n, 14);
     auto entry = [&](auto &f) { f = reinterpret_cast<std::decay_t<decltype(f)>>(uintptr_t(seed64(*a++))); };
     entry(f_dropout);
     entry(f_quantize);
     entry(f_dequantize);
     entry(f_gemm);
     entry(f_gemm_a16);
+    entry(f_gemm_a16_s4);
     entry(f_norm);
     entry(f_norm_s8);
     entry(f_norm_workspace);
     entry(f_norm_backward);
-    if (!PyType_Check(a[2])) raise(PyExc_TypeError, "a type is expected");
+    if (!PyType_Check(a[2]) || !PyType_Check(a[3])) raise(PyExc_TypeError, "a type is expected");
     Py_XSETREF(g_check, Py_NewRef(a[0]));
     Py_XSETREF(g_stream, Py_NewRef(a[1]));
-    PyTypeObject *old = g_matrix;
-    g_matrix = reinterpret_cast<PyTypeObject *>(Py_NewRef(a[2]));
-    Py_XDECREF(old);
+    auto type = [](PyTypeObject *&to, PyObject *o) {
+        PyTypeObject *old = to;
+        to = reinterpret_cast<PyTypeObject *>(Py_NewRef(o));
+        Py_XDECREF(old);
+    };
+    type(g_matrix, a[2]);
+    type(g_s4, a[3]);
     if (!s_codes) {
         s_codes = PyUnicode_InternFromString("_codes");
         s_scales = PyUnicode_InternFromString("_scales");
         s_k = PyUnicode_InternFromString("_K");
         s_fmt = PyUnicode_InternFromString("_fmt");
         s_ts = PyUnicode_InternFromString("_ts");
+        s_group = PyUnicode_InternFromString("_group");
+        s_zeros = PyUnicode_InternFromString("_zeros");
     }
     Py_RETURN_NONE;
     PTC_BODY_END
@@ -632,6 +734,8 @@ PyMethodDef g_methods[] = {PTC_METHOD("init", py_init),
                            PTC_METHOD("dequantize", py_dequantize),
                            PTC_METHOD("matmul", py_matmul),
                            PTC_METHOD("matmul_a16", py_matmul_a16),
+                           PTC_METHOD("matmul_a16_s4", py_matmul_a16_s4),
+                           PTC_METHOD("check_s4", py_check_s4),
                            PTC_METHOD("rms_norm", py_norm),
                            PTC_METHOD("rms_norm_s8", py_norm_s8),
                            PTC_METHOD("rms_norm_backward", py_norm_backward),

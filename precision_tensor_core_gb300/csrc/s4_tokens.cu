@@ -1,0 +1,418 @@
+// s4_tokens.cu -- product of a few rows of 16-bit activations with 4-bit integer
+// weights that have group scales (gemm_a16_s4 of include/ptc.h).
+//
+// The weights are read once and bound the call: 0.5 bytes each and their scales.  The
+// products run on mma.sync m16n8k16 with 16 rows of the weights as one operand and eight
+// tokens as the other (s4.cuh); sums stay in FP32.
+//
+// Layout.  The eight warps of a CTA are R row groups x S shares of K; a warp owns 16 MT
+// rows and every S-th stage of 128 codes, and brings them to its own ring in shared memory
+// by asynchronous copies, kStages deep, with no other warp to wait for.  The tokens'
+// activations are made operands once per CTA, in chunks of K that fit, two of them in
+// shared memory.  The shares' sums are added in order there, and where that leaves SMs
+// idle K is also shared by a cluster of up to eight CTAs, whose sums are added in rank
+// order through distributed shared memory.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+#include <cstring>
+#include <type_traits>
+
+#include "fp4.cuh"
+#include "fp4.h"
+#include "internal.h"
+#include "ptc.h"
+#include "ptx.cuh"
+#include "s4.cuh"
+#include "s4.h"
+
+namespace ptc {
+namespace {
+
+constexpr int kWarps4 = 8, kThreads4 = 32 * kWarps4;
+__host__ __device__ constexpr int stages_of(int mt) { return mt == 1 ? 6 : 4; }
+
+struct S4Args {
+    const void *x;
+    int64_t ldx;
+    const uint8_t *codes;
+    int64_t pitch;
+    const uint8_t *scales, *zeros;  // tiles
+    void *C;
+    int64_t ldc;
+    int M, N, K;
+    int row_bytes;       // of codes
+    int groups;          // per row
+    int per_group;       // stages per group (1 for groups of up to 128)
+    int stages;          // of K
+    int chunk;           // stages of the CTA's K range whose activations are held at once
+    int buffers;         // of activations
+    int r_log2, ks;
+    int xvec, bf16_scales;
+    int stage_bytes;     // of a warp's ring
+};
+
+template <typename X, int MT, int NT, int UNIT>
+__global__ void __launch_bounds__(kThreads4, 2) s4_kernel(const S4Args a) {
+    constexpr int TOK = 8 * NT, GROUPS = 4 / UNIT, D = stages_of(MT);
+    extern __shared__ __align__(128) uint8_t smem4[];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int gr = lane >> 2, t = lane & 3;
+    const int krank = a.ks == 1 ? 0 : int(cluster_ctarank());
+    const int R = 1 << a.r_log2, S = kWarps4 >> a.r_log2;
+    const int rg = warp & (R - 1), share = warp >> a.r_log2;
+    const int row0 = (int(blockIdx.x) / a.ks * R + rg) * (16 * MT);
+    const int tok0 = int(blockIdx.y) * TOK, ntok = min(TOK, a.M - tok0);
+    // This CTA's stages of K.
+    const int q = a.stages / a.ks, rest = a.stages % a.ks;
+    const int c0 = krank * q + min(krank, rest), c1 = c0 + q + (krank < rest ? 1 : 0);
+    uint8_t *ring = smem4 + warp * D * a.stage_bytes;
+    uint8_t *xs_base = smem4 + kWarps4 * D * a.stage_bytes;
+    const uint32_t tok_bytes = uint32_t(a.chunk) * kS4XBytes, ps_at = tok_bytes * uint32_t(ntok);
+    const uint32_t buf_bytes = ps_at + uint32_t(a.chunk) * (GROUPS * TOK * 8);
+
+    griddep_wait();
+    griddep_launch_dependents();
+
+    // Copies of stage i of this warp's share, c0 + share + i S: the rows' codes (two
+    // copies per tile, a lane 16 bytes) and the tiles' scales and zeros.
+    const int crow = lane >> 2, piece = lane & 3;
+    const uint8_t *src[2 * MT];
+#pragma unroll
+    for (int j = 0; j < 2 * MT; ++j) src[j] = a.codes + int64_t(min(row0 + 8 * j + crow, a.N - 1)) * a.pitch + piece * 16;
+    constexpr int PIECES = MT * GROUPS * 2;  // of scales
+    const uint8_t *scale_src = nullptr;
+    const int sp = lane % PIECES, sm = sp / (2 * GROUPS), sg = sp / 2 % GROUPS;
+    const bool scale_lane = lane < PIECES * (a.zeros ? 2 : 1);
+    if (scale_lane) {
+        const int64_t tile = min(row0 / 16 + sm, (a.N + 15) / 16 - 1);
+        scale_src = (lane < PIECES ? a.scales : a.zeros) + tile * a.groups * 32 + (sp & 1) * 16;
+    }
+    auto issue = [&](int i) {
+        const int st = c0 + share + i * S;
+        if (st < c1) {
+            const uint32_t dst = smem_u32(ring + (i % D) * a.stage_bytes);
+            const int n = min(16, max(0, a.row_bytes - st * kS4RowBytes - piece * 16));
+#pragma unroll
+            for (int j = 0; j < 2 * MT; ++j)
+                copy16(dst + (j >> 1) * kS4TileBytes + s4_piece(8 * (j & 1) + crow, piece),
+                       n > 0 ? src[j] + int64_t(st) * kS4RowBytes : a.codes, n);
+            if (scale_lane) {
+                const int g = GROUPS == 1 ? st / a.per_group : st * GROUPS + sg;
+                copy16(dst + MT * kS4TileBytes + lane * 16, g < a.groups ? scale_src + int64_t(g) * 32 : a.scales,
+                       g < a.groups ? 16 : 0);
+            }
+        }
+        copies_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i) issue(i);
+
+    // Activations of chunk c to its buffer: 4 UNIT lanes a block, a warp 32 / (4 UNIT).
+    auto load_x = [&](int c) {
+        constexpr int LANES = 4 * UNIT, PER = 32 / LANES;
+        uint8_t *buf = xs_base + (a.buffers == 2 && (c & 1) ? buf_bytes : 0u);
+        const int first = c0 + c * a.chunk, n = min(a.chunk, c1 - first);   // stages
+        const int blocks = n * GROUPS;
+        for (int u = warp * PER; u < blocks * ntok; u += kWarps4 * PER) {
+            const int mine = u + lane / LANES;
+            const bool ok = mine < blocks * ntok;
+            const int tok = ok ? mine / blocks : 0, blk = ok ? mine - tok * blocks : 0;
+            const int k = first * kS4Stage + blk * (32 * UNIT) + (lane % LANES) * 8;
+            const int have = ok ? max(0, min(8, a.K - k)) : 0;
+            const X *p = static_cast<const X *>(a.x) + int64_t(tok0 + tok) * a.ldx + (have > 0 ? k : 0);
+            const Pack8<X> raw = load8(p, have, a.xvec != 0);
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = to_float(raw.get(j));
+            uint4 hi, lo;
+            float2 ps;
+            s4_operands<UNIT, false>(v, hi, lo, ps);
+            if (ok) {
+                const int st = blk / GROUPS, g = blk % GROUPS;
+                const int pc = g * (4 * UNIT) + lane % LANES;  // piece of the token's stage
+                *reinterpret_cast<uint4 *>(buf + uint32_t(tok) * tok_bytes + uint32_t(st) * kS4XBytes + s4_x_piece(tok, pc)) = hi;
+                if (lane % LANES == 0) *reinterpret_cast<float2 *>(buf + ps_at + uint32_t((st * GROUPS + g) * TOK + tok) * 8u) = ps;
+            }
+        }
+    };
+    load_x(0);
+
+    float tot[MT][NT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tot[m][n][i] = 0.0f;
+    const uint32_t code_at = s4_code_at(lane);
+    int i = 0;
+    for (int c = 0; c * a.chunk < c1 - c0; ++c) {
+        __syncthreads();  // chunk c is there, and everyone is done with the other buffer
+        if (a.buffers == 2 && (c + 1) * a.chunk < c1 - c0) load_x(c + 1);
+        const uint8_t *buf = xs_base + (a.buffers == 2 && (c & 1) ? buf_bytes : 0u);
+        const int end = min(c1, c0 + (c + 1) * a.chunk);
+        for (int st = c0 + share + i * S; st < end; st += S, ++i) {
+            copies_wait<D - 2>();
+            __syncwarp();
+            issue(i + D - 1);
+            const uint8_t *stage = ring + (i % D) * a.stage_bytes;
+            const uint32_t local = uint32_t(st - c0 - c * a.chunk);
+            const uint8_t *x[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)  // (tokens past the last read it again; their sums are dropped)
+                x[n] = buf + uint32_t(min(8 * n + gr, ntok - 1)) * tok_bytes + local * kS4XBytes + uint32_t(t) * 16u;
+            s4_stage<MT, NT, UNIT, 1>(tot, stage + code_at, stage + MT * kS4TileBytes,
+                                      a.zeros ? stage + MT * kS4TileBytes + PIECES * 16 : nullptr, a.bf16_scales != 0, x, 0u,
+                                      buf + ps_at + local * (GROUPS * TOK * 8), lane);
+        }
+    }
+    copies_wait<0>();
+    __syncthreads();
+
+    // Sums: [warp][row][token] in the ring's place, added over the shares and then over
+    // the cluster's ranks, both in order.
+    float *part = reinterpret_cast<float *>(smem4) + warp * (16 * MT * TOK);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int r = 16 * m + gr, tk = 8 * n + 2 * t;
+            *reinterpret_cast<float2 *>(part + r * TOK + tk) = make_float2(tot[m][n][0], tot[m][n][1]);
+            *reinterpret_cast<float2 *>(part + (r + 8) * TOK + tk) = make_float2(tot[m][n][2], tot[m][n][3]);
+        }
+    if (a.ks > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    const uint32_t base = smem_u32(smem4);
+    const int rows = R * 16 * MT, first = int(blockIdx.x) / a.ks * rows;
+    for (int o = krank * kThreads4 + int(threadIdx.x); o < rows * TOK; o += a.ks * kThreads4) {
+        const int tk = o / rows, r = o - tk * rows, w = r / (16 * MT), lr = r % (16 * MT);
+        float v = 0.0f;
+        for (int k = 0; k < a.ks; ++k)
+            for (int sh = 0; sh < S; ++sh) {
+                const uint32_t at = base + uint32_t(((sh << a.r_log2) + w) * (16 * MT * TOK) + lr * TOK + tk) * 4u;
+                float f;
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(a.ks == 1 ? at : mapa_shared(at, uint32_t(k))) : "memory");
+                v = __fadd_rn(v, f);
+            }
+        if (tk < ntok && first + r < a.N)
+            static_cast<X *>(a.C)[int64_t(tok0 + tk) * a.ldc + first + r] = from_float<X>(__fmul_rn(v, kS4Out));
+    }
+    if (a.ks > 1) cluster_sync();
+}
+
+// ------------------------------------------------------------ host side
+constexpr int64_t kMaxDim4 = int64_t(1) << 30;
+constexpr int64_t kMaxLd4 = int64_t(1) << 36;
+constexpr int kMaxDev4 = 64;
+std::atomic<int> g_s4_rows{0};   // "s4_tokens_rows": 0 by size, 1, 2, 4, 8
+std::atomic<int> g_s4_split{0};  // "s4_tokens_split": 0 by size, 1, 2, 4, 8
+std::atomic<int> g_s4_tiles{0};  // "s4_tokens_tiles": 0 by size, 1, 2
+
+constexpr int kSmem4 = 226 * 1024, kSmem4Half = 113 * 1024;  // one CTA per SM, two
+
+// Rows and K shares of a launch, and how the activations are held.
+struct S4Shape {
+    int mt, r_log2, ks;
+    int chunk, buffers;
+    size_t smem;
+};
+
+// Shared memory of a shape; false where a buffer does not hold a stage of every share.
+bool fit_s4(S4Shape &sh, const S4Args &a, int groups_per_stage, int toks, int tok, int64_t ctas, int sms) {
+    const int S = kWarps4 >> sh.r_log2, most = ctas <= sms ? kSmem4 : kSmem4Half;
+    const int ring = kWarps4 * stages_of(sh.mt) * sh.mt * (kS4TileBytes + groups_per_stage * 32 * (a.zeros ? 2 : 1));
+    const int per_stage = toks * kS4XBytes + groups_per_stage * tok * 8;
+    const int range = (a.stages + sh.ks - 1) / sh.ks, fit = (most - ring) / per_stage;
+    sh.buffers = range <= fit ? 1 : 2;
+    sh.chunk = sh.buffers == 1 ? range : fit / 2 / S * S;
+    sh.smem = size_t(ring) + size_t(sh.buffers) * sh.chunk * per_stage;
+    return sh.chunk > 0;
+}
+
+S4Shape choose_s4(const S4Args &a, int unit, int sms) {
+    const int64_t N = a.N, chunks = (a.M + 15) / 16;
+    const int stages = a.stages, toks = std::min(a.M, 16), tok = a.M > 8 ? 16 : 8;
+    S4Shape best{1, 0, 1, 0, 0, 0};
+    const int rows = g_s4_rows.load(), split = g_s4_split.load(), tiles = g_s4_tiles.load();
+    int64_t cost_best = INT64_MAX;
+    for (bool any : {false, true}) {
+        for (int mt = 1; mt <= 2; ++mt)
+            for (int r = 0; r <= 3; ++r)
+                for (int k = 1; k <= 8; k *= 2) {
+                    const int S = 8 >> r;
+                    if (stages < S * k && (r < 3 || k > 1)) continue;
+                    if (!any && ((rows && rows != 1 << r) || (split && split != k) || (tiles && tiles != mt))) continue;
+                    const int64_t per = int64_t(16) * mt << r, ctas = (N + per - 1) / per * k * chunks;
+                    S4Shape sh{mt, r, k, 0, 0, 0};
+                    if (!fit_s4(sh, a, 4 / unit, toks, tok, ctas, sms)) continue;
+                    const int64_t waves = (ctas + 2 * sms - 1) / (2 * sms);
+                    const int64_t st = (stages + S * k - 1) / (S * k);
+                    const int64_t start = k == 1 ? 220 : k == 2 ? 320 : k == 4 ? 400 : 600;
+                    const int64_t read = int64_t(toks) * stages / k * 3;
+                    const int64_t cost = waves * (start + st * (mt == 1 ? 30 : 50) * (toks > 8 ? 3 : 2) / 2 * (ctas > sms ? 17 : 10) / 10 + read);
+                    if (cost < cost_best) {
+                        cost_best = cost;
+                        best = sh;
+                    }
+                }
+        if (cost_best != INT64_MAX) return best;
+    }
+    return best;
+}
+
+template <typename X, int MT, int NT, int UNIT>
+int launch_s4(S4Args a, const S4Shape &sh, cudaStream_t stream) {
+    constexpr int TOK = 8 * NT, GROUPS = 4 / UNIT;
+    auto *fn = s4_kernel<X, MT, NT, UNIT>;
+    static std::atomic<int> ready[kMaxDev4];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return fail_launch(e, "cudaGetDevice");
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem4);
+        if (e != cudaSuccess) return fail_launch(e, "grouped 4-bit product set-up");
+        ready[dev].store(1, std::memory_order_release);
+    }
+    a.r_log2 = sh.r_log2;
+    a.ks = sh.ks;
+    a.stage_bytes = MT * (kS4TileBytes + GROUPS * 32 * (a.zeros ? 2 : 1));
+    a.buffers = sh.buffers;
+    a.chunk = sh.chunk;
+    const size_t smem = sh.smem;
+    const int R = 1 << sh.r_log2;
+    const int64_t per = int64_t(16) * MT * R, blocks = (a.N + per - 1) / per * sh.ks, chunks = (a.M + TOK - 1) / TOK;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    std::memset(&cfg, 0, sizeof(cfg));
+    std::memset(attr, 0, sizeof(attr));
+    cfg.gridDim = dim3(unsigned(blocks), unsigned(chunks), 1);
+    cfg.blockDim = dim3(kThreads4, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    if (sh.ks > 1) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = unsigned(sh.ks);
+        attr[cfg.numAttrs].val.clusterDim.y = 1;
+        attr[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
+    if (pdl_enabled()) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+        ++cfg.numAttrs;
+    }
+    e = cudaLaunchKernelEx(&cfg, fn, a);
+    if (e != cudaSuccess) return fail_launch(e, "grouped 4-bit product launch");
+    note_launches(1);
+    note_fp4_launch(int64_t(cfg.gridDim.x) * cfg.gridDim.y, sh.ks, sh.ks, 16 * MT * R);
+    return PTC_OK;
+}
+
+template <typename X>
+int run_s4(const S4Args &a, int64_t group, int sms, cudaStream_t s) {
+    const bool wide = a.M > 8;
+    const S4Shape sh = choose_s4(a, s4_unit(group), sms);
+    auto unit = [&](auto u) {
+        constexpr int U = decltype(u)::value;
+        if (sh.mt == 1) return wide ? launch_s4<X, 1, 2, U>(a, sh, s) : launch_s4<X, 1, 1, U>(a, sh, s);
+        return wide ? launch_s4<X, 2, 2, U>(a, sh, s) : launch_s4<X, 2, 1, U>(a, sh, s);
+    };
+    switch (s4_unit(group)) {
+        case 1: return unit(std::integral_constant<int, 1>());
+        case 2: return unit(std::integral_constant<int, 2>());
+        default: return unit(std::integral_constant<int, 4>());
+    }
+}
+
+bool at_multiple(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+}  // namespace
+
+bool set_s4_tuning(const char *key, int64_t v) {
+    const bool power = v == 0 || v == 1 || v == 2 || v == 4 || v == 8;
+    if (std::strcmp(key, "s4_tokens_rows") == 0 && power)
+        g_s4_rows.store(int(v));
+    else if (std::strcmp(key, "s4_tokens_split") == 0 && power)
+        g_s4_split.store(int(v));
+    else if (std::strcmp(key, "s4_tokens_tiles") == 0 && v >= 0 && v <= 2)
+        g_s4_tiles.store(int(v));
+    else
+        return false;
+    return true;
+}
+
+int check_s4(const S4Weights &w) {
+    if (!w.codes || !w.scales) return fail_status(PTC_ERR_INVALID, "codes or scales is NULL");
+    if (w.group != 32 && w.group != 64 && (w.group <= 0 || w.group % 128 || w.group > kMaxDim4))
+        return fail_status(PTC_ERR_INVALID, "groups are of 32, 64 or a multiple of 128 codes");
+    if (w.pitch < (w.cols + 1) / 2 || w.pitch > kMaxLd4)
+        return fail_status(PTC_ERR_INVALID, "the code pitch must hold a row's codes, two per byte");
+    if (!at_multiple(w.codes, 16) || !at_multiple(w.scales, 16) || !at_multiple(w.zeros, 16) || w.pitch % 16 || w.expert % 16)
+        return fail_status(PTC_ERR_ALIGN, "codes, scales and zeros must be 16-byte aligned, with pitches that are multiples of 16");
+    return PTC_OK;
+}
+
+}  // namespace ptc
+
+using namespace ptc;
+
+extern "C" int gemm_a16_s4(int64_t M, int64_t N, int64_t K, int type, const void *X, int64_t ldx, const void *W, int64_t ldw,
+                           int64_t group, int scale_type, const void *scales, const void *zeros, void *C, int64_t ldc,
+                           void *stream) {
+    set_message("");
+    if (M < 0 || N < 0 || K < 0 || M > kMaxDim4 || N > kMaxDim4 || K > kMaxDim4)
+        return fail_status(PTC_ERR_INVALID, "sizes must satisfy 0 <= M, N, K <= 2^30");
+    if (M > 65535 * 16) return fail_status(PTC_ERR_INVALID, "at most 1048560 rows of activations");
+    if (type != PTC_OUT_BF16 && type != PTC_OUT_F16)
+        return fail_status(PTC_ERR_INVALID, "activations are PTC_OUT_BF16 or PTC_OUT_F16");
+    if (scale_type != PTC_OUT_BF16 && scale_type != PTC_OUT_F16)
+        return fail_status(PTC_ERR_INVALID, "scales are PTC_OUT_BF16 or PTC_OUT_F16");
+    if (M == 0 || N == 0) return PTC_OK;
+    if (!C || ldc < N || ldc > kMaxLd4) return fail_status(PTC_ERR_INVALID, "C is NULL, or ldc is not N .. 2^36");
+    if (K > 0 && (!X || ldx < K || ldx > kMaxLd4)) return fail_status(PTC_ERR_INVALID, "X is NULL, or ldx is not K .. 2^36");
+    const S4Weights w{W, ldw, 0, scales, zeros, N, K, group, 1};
+    int rc;
+    if (K > 0 && (rc = check_s4(w))) return rc;
+    if (!at_multiple(C, 2) || (K > 0 && !at_multiple(X, 2)))
+        return fail_status(PTC_ERR_ALIGN, "X and C must be aligned to their elements");
+    const ByteRows c = elem_rows(C, M, N, ldc, 2);
+    if (K > 0 && (rows_overlap(c, elem_rows(X, M, K, ldx, 2)) || rows_overlap(c, elem_rows(W, N, (K + 1) / 2, ldw, 1)) ||
+                  rows_overlap(c, flat_bytes(scales, w.scale_bytes())) || rows_overlap(c, flat_bytes(zeros, w.scale_bytes()))))
+        return fail_status(PTC_ERR_OVERLAP, "C overlaps an operand");
+    int sms;
+    if ((rc = usable_device(&sms))) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (K == 0) {
+        const cudaError_t e = launch_zero_fill(C, ldc, int(M), int(N), 2, sms * 4, s);
+        if (e != cudaSuccess) return fail_launch(e, "zero-fill launch");
+        note_launches(1);
+        return PTC_OK;
+    }
+    S4Args a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = X;
+    a.ldx = ldx;
+    a.codes = static_cast<const uint8_t *>(W);
+    a.pitch = ldw;
+    a.scales = static_cast<const uint8_t *>(scales);
+    a.zeros = static_cast<const uint8_t *>(zeros);
+    a.C = C;
+    a.ldc = ldc;
+    a.M = int(M);
+    a.N = int(N);
+    a.K = int(K);
+    a.row_bytes = int((K + 1) / 2);
+    a.groups = int(w.groups());
+    a.per_group = int(group >= 128 ? group / 128 : 1);
+    a.stages = int((K + kS4Stage - 1) / kS4Stage);
+    a.xvec = at_multiple(X, 16) && (M == 1 || ldx % 8 == 0);
+    a.bf16_scales = scale_type == PTC_OUT_BF16;
+    return type == PTC_OUT_BF16 ? run_s4<__nv_bfloat16>(a, group, sms, s) : run_s4<__half>(a, group, sms, s);
+}
