@@ -24,6 +24,7 @@
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <type_traits>
 
 #include "fp4.cuh"
 #include "ptx.cuh"
@@ -40,42 +41,62 @@ constexpr float kS4Out = 0x1p12f;    // the output's factor
 __host__ __device__ constexpr int s4_unit(int64_t group) { return group == 32 ? 1 : group == 64 ? 2 : 4; }
 
 // ------------------------------------------------------------ activations
-// Eight consecutive activations of a block that 4 UNIT consecutive lanes hold, as
-// operands (a word of 16 bytes, see above), and the block's factor and sum (in every
-// lane).  LO also gives the operands of what the rounding to binary16 left, for FP32
-// values: 22 bits in all.
-template <int UNIT, bool LO>
-__device__ __forceinline__ void s4_operands(const float (&v)[8], uint4 &hi, uint4 &lo, float2 &factor_sum) {
-    uint32_t m = 0;  // largest finite magnitude, as FP32 bits
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t u = __float_as_uint(v[j]) & 0x7FFFFFFFu;
-        m = max(m, u < kInfBits ? u : 0u);
-    }
+// The power of two of a block whose largest magnitude has the FP32 bits m (at least
+// kInfBits: the token is NaN anyway), as the factor that brings it to [2^14, 2^15) and
+// the block's factor.
+__device__ __forceinline__ void s4_powers(uint32_t m, float &down, float &factor) {
+    const int e = min(max(int(m >> 23) - 127 - 14, -126), 113);
+    down = __uint_as_float(uint32_t(127 - e) << 23);
+    factor = __uint_as_float(uint32_t(127 + 12 + e) << 23);
+}
+
+__device__ __forceinline__ uint32_t s4_pair(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return reinterpret_cast<const uint32_t &>(h);
+}
+
+// Eight consecutive 16-bit activations of a block that 4 UNIT consecutive lanes hold, as
+// operands (16 bytes, see above), and the block's factor and sum (in every lane).  The
+// sum is that of the elements before they are held, which differ by 2^-35 of the largest
+// at most.
+template <int UNIT, typename X>
+__device__ __forceinline__ uint4 s4_operands(const uint4 &raw, float2 &factor_sum) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+    m = max(m & 0xFFFFu, m >> 16);
 #pragma unroll
     for (int o = 1; o < 4 * UNIT; o *= 2) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    const int e = max(int(m >> 23) - 127 - 14, -126);
-    const float down = __uint_as_float(uint32_t(127 - e) << 23);
-    __half h[8], l[8];
+    float v[8];
+    if constexpr (std::is_same_v<X, __half>) {
+        m = __float_as_uint(__half2float(__ushort_as_half(uint16_t(m))));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = __half22float2(reinterpret_cast<const __half2 &>(w[j]));
+            v[2 * j] = f.x;
+            v[2 * j + 1] = f.y;
+        }
+    } else {
+        m <<= 16;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(w[j] << 16);
+            v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+    }
+    float down, factor;
+    s4_powers(m, down, factor);
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float part = (j & 1) ? 0x1p-4f : 1.0f;
-        const float x = __fmul_rn(__fmul_rn(v[j], down), part);
-        h[j] = __float2half_rn(x);
-        float held = __half2float(h[j]);
-        if constexpr (LO) {
-            l[j] = __float2half_rn(__fsub_rn(x, held));
-            held = __fadd_rn(held, __half2float(l[j]));
-        }
-        sum = __fmaf_rn(held, (j & 1) ? 0x1p4f : 1.0f, sum);
+        v[j] = __fmul_rn(v[j], down);
+        sum = __fadd_rn(sum, v[j]);
     }
 #pragma unroll
     for (int o = 1; o < 4 * UNIT; o *= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    factor_sum = make_float2(__uint_as_float(uint32_t(127 + 12 + e) << 23), __fmul_rn(sum, 0x1p-24f));
-    auto pair = [](__half a, __half b) { return uint32_t(__half_as_ushort(a)) | uint32_t(__half_as_ushort(b)) << 16; };
-    hi = make_uint4(pair(h[0], h[4]), pair(h[2], h[6]), pair(h[1], h[5]), pair(h[3], h[7]));
-    if constexpr (LO) lo = make_uint4(pair(l[0], l[4]), pair(l[2], l[6]), pair(l[1], l[5]), pair(l[3], l[7]));
+    factor_sum = make_float2(factor, __fmul_rn(sum, 0x1p-24f));
+#pragma unroll
+    for (int j = 1; j < 8; j += 2) v[j] = __fmul_rn(v[j], 0x1p-4f);
+    return make_uint4(s4_pair(v[0], v[4]), s4_pair(v[2], v[6]), s4_pair(v[1], v[5]), s4_pair(v[3], v[7]));
 }
 
 // ------------------------------------------------------------ copies
@@ -92,17 +113,33 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
-// Where 16-byte piece c (0 .. 3) of row r of a tile of 16 rows lies: rows that are read
-// together differ in their banks.
-__device__ __forceinline__ uint32_t s4_piece(int r, int c) { return uint32_t(r) * kS4RowBytes + (uint32_t(c ^ ((r >> 1) & 3)) << 4); }
+// In a stage the lanes of a quad take the words of a row's four 16-byte pieces in one of
+// two ways.  With UNIT 4, where the whole stage is one block, lane t takes piece t by one
+// load, and the i-th pair of MMAs multiplies its word i: codes 32 t + 8 i .. + 7.
+// Otherwise lane t takes word t of each piece, and the i-th pair multiplies block i.
 
-// Where 16-byte piece c (block c / 4, lane c % 4) of token j's stage lies, from the token's start.
-__device__ __forceinline__ uint32_t s4_x_piece(int j, int c) { return uint32_t(c ^ ((j & 1) << 2)) << 4; }
+// Where 16-byte piece c (0 .. 3) of MMA row i of a tile of 16 rows lies: rows that are read
+// together differ in their banks.  MMA rows i and i + 8 are the tile's rows 2 i and 2 i + 1,
+// whose scales one load takes.
+template <int UNIT>
+__device__ __forceinline__ uint32_t s4_piece(int i, int c) {
+    return uint32_t(i) * kS4RowBytes + (uint32_t(UNIT == 4 ? c : c ^ ((i >> 1) & 3)) << 4);
+}
+__device__ __forceinline__ int s4_row(int i) { return 2 * (i & 7) + (i >> 3); }
 
-// A scale or zero of either 16-bit type.
-__device__ __forceinline__ float s4_scale(const uint8_t *p, bool bf16) {
-    const uint16_t u = *reinterpret_cast<const uint16_t *>(p);
-    return bf16 ? __uint_as_float(uint32_t(u) << 16) : __half2float(__ushort_as_half(u));
+// Where the operands of activations 8 c .. 8 c + 7 of token j's stage lie, from the
+// token's start: 64 bytes for each pair of MMAs, odd tokens in the other order.
+template <int UNIT>
+__device__ __forceinline__ uint32_t s4_x_piece(int j, int c) {
+    const int at = UNIT == 4 ? (c & 3) * 4 + (c >> 2) : c;
+    return uint32_t(at ^ ((j & 1) << 2)) << 4;
+}
+
+// Two scales or zeros of either 16-bit type.
+__device__ __forceinline__ float2 s4_scales(const uint8_t *p, bool bf16) {
+    const uint32_t u = *reinterpret_cast<const uint32_t *>(p);
+    return bf16 ? make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u))
+                : __half22float2(reinterpret_cast<const __half2 &>(u));
 }
 
 // ------------------------------------------------------------ products
@@ -113,85 +150,110 @@ __device__ __forceinline__ void s4_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
+// (a & b) ^ c in one instruction (written out as C++ it became two: 23.1 us instead of 19.6 for
+// one token with 16384 x 8192 weights).
+__device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+
 // Eight codes as four operands (see the top).
 __device__ __forceinline__ void s4_codes(uint32_t w, uint32_t (&a)[4]) {
     const uint32_t w8 = w >> 8;
-    a[0] = (w & 0x000F000Fu) ^ 0x00080008u;
-    a[1] = (w8 & 0x000F000Fu) ^ 0x00080008u;
-    a[2] = (w & 0x00F000F0u) ^ 0x00800080u;
-    a[3] = (w8 & 0x00F000F0u) ^ 0x00800080u;
+    a[0] = and_xor(w, 0x000F000Fu, 0x00080008u);
+    a[1] = and_xor(w8, 0x000F000Fu, 0x00080008u);
+    a[2] = and_xor(w, 0x00F000F0u, 0x00800080u);
+    a[3] = and_xor(w8, 0x00F000F0u, 0x00800080u);
 }
 
-// One stage: MT tiles of 16 rows of codes (`codes`: of this lane's word of row 0, see
-// code_at) with NT sets of eight tokens.  `scales` (and `zeros`, or NULL): [tile][group][16]
-// of this stage; x[n]: this lane's operands of token set n (of block 0), x_lo: those of
-// the low parts, PARTS 2; ps: factors and sums, [block of activations][8 NT tokens].
+// One stage: MT tiles of 16 rows of codes with NT sets of eight tokens.  Offsets in
+// shared memory (`smem`): codes s4_code_at<UNIT> past a multiple of 64; scales, and zeros
+// that many bytes behind (0: none), [tile][group][16]; x[n]: this lane's token of set n,
+// 16 t past a multiple of 256 (odd tokens: 64 more), x_lo: from it to the operands of the
+// low parts (PARTS 2); ps: factors and sums, [block of activations][8 NT tokens].
 // tot += s factor (sum of n x - (8 + z) sum of x).
 template <int MT, int NT, int UNIT, int PARTS>
-__device__ __forceinline__ void s4_stage(float (&tot)[MT][NT][4], const uint8_t *codes, const uint8_t *scales,
-                                         const uint8_t *zeros, bool bf16, const uint8_t *const (&x)[NT], uint32_t x_lo,
-                                         const uint8_t *ps, int lane) {
+__device__ __forceinline__ void s4_stage(float (&tot)[MT][NT][4], const uint8_t *smem, uint32_t codes, uint32_t scales,
+                                         uint32_t zeros, bool bf16, const uint32_t (&x)[NT], uint32_t x_lo, uint32_t ps,
+                                         int lane) {
     constexpr int GROUPS = 4 / UNIT;
     const int gr = lane >> 2, t = lane & 3;
-    const uint32_t turn = uint32_t((gr >> 1) & 3);   // the same for rows gr and gr + 8
-    const uint32_t x_turn = uint32_t(gr & 1);
+    uint4 wide[MT][2];
+    if constexpr (UNIT == 4) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                wide[m][h] = *reinterpret_cast<const uint4 *>(smem + codes + m * kS4TileBytes + h * (8 * kS4RowBytes));
+    }
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) {
         float d[MT][NT][4];
 #pragma unroll
         for (int u = 0; u < UNIT; ++u) {
-            const int b = g * UNIT + u;
+            const int i = g * UNIT + u;
             uint4 xv[NT][PARTS];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int p = 0; p < PARTS; ++p)
-                    xv[n][p] = *reinterpret_cast<const uint4 *>(x[n] + ((uint32_t(b) ^ x_turn) << 6) + uint32_t(p) * x_lo);
+                    xv[n][p] = *reinterpret_cast<const uint4 *>(smem + (x[n] ^ (uint32_t(i) << 6)) + uint32_t(p) * x_lo);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                const uint8_t *row = codes + m * kS4TileBytes + ((uint32_t(b) ^ turn) << 4);
-                uint32_t a[4], c[4];
-                s4_codes(*reinterpret_cast<const uint32_t *>(row), a);
-                s4_codes(*reinterpret_cast<const uint32_t *>(row + 8 * kS4RowBytes), c);
+                uint32_t w[2], a[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if constexpr (UNIT == 4)
+                        w[h] = i == 0 ? wide[m][h].x : i == 1 ? wide[m][h].y : i == 2 ? wide[m][h].z : wide[m][h].w;
+                    else
+                        w[h] = *reinterpret_cast<const uint32_t *>(smem + (codes ^ (uint32_t(i) << 4)) + m * kS4TileBytes +
+                                                                   h * (8 * kS4RowBytes));
+                    s4_codes(w[h], a[h]);
+                }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int p = 0; p < PARTS; ++p) {
                         if (u == 0 && p == 0)
-                            s4_mma(d[m][n], a[0], c[0], a[1], c[1], xv[n][p].x, xv[n][p].y, zero);
+                            s4_mma(d[m][n], a[0][0], a[1][0], a[0][1], a[1][1], xv[n][p].x, xv[n][p].y, zero);
                         else
-                            s4_mma(d[m][n], a[0], c[0], a[1], c[1], xv[n][p].x, xv[n][p].y, d[m][n]);
-                        s4_mma(d[m][n], a[2], c[2], a[3], c[3], xv[n][p].z, xv[n][p].w, d[m][n]);
+                            s4_mma(d[m][n], a[0][0], a[1][0], a[0][1], a[1][1], xv[n][p].x, xv[n][p].y, d[m][n]);
+                        s4_mma(d[m][n], a[0][2], a[1][2], a[0][3], a[1][3], xv[n][p].z, xv[n][p].w, d[m][n]);
                     }
                 }
             }
         }
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            const uint32_t at = uint32_t((m * GROUPS + g) * 16 + gr) * 2u;
-            const float s0 = s4_scale(scales + at, bf16), s1 = s4_scale(scales + at + 16, bf16);
-            float z0 = 8.0f, z1 = 8.0f;
-            if (zeros != nullptr) {
-                z0 = __fadd_rn(z0, s4_scale(zeros + at, bf16));
-                z1 = __fadd_rn(z1, s4_scale(zeros + at + 16, bf16));
+            const uint8_t *at = smem + scales + uint32_t(m * GROUPS + g) * 32u + uint32_t(gr) * 4u;
+            const float2 s = s4_scales(at, bf16);
+            float2 z = make_float2(8.0f, 8.0f);
+            if (zeros != 0) {
+                const float2 more = s4_scales(at + zeros, bf16);
+                z = make_float2(__fadd_rn(z.x, more.x), __fadd_rn(z.y, more.y));
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const float4 q = *reinterpret_cast<const float4 *>(ps + (g * 8 * NT + 8 * n + 2 * t) * 8);
+                const float4 q = *reinterpret_cast<const float4 *>(smem + ps + (g * 8 * NT + 8 * n + 2 * t) * 8);
                 float(&o)[4] = tot[m][n];
                 const float(&v)[4] = d[m][n];
-                o[0] = __fmaf_rn(s0, __fmul_rn(q.x, __fmaf_rn(-z0, q.y, v[0])), o[0]);
-                o[1] = __fmaf_rn(s0, __fmul_rn(q.z, __fmaf_rn(-z0, q.w, v[1])), o[1]);
-                o[2] = __fmaf_rn(s1, __fmul_rn(q.x, __fmaf_rn(-z1, q.y, v[2])), o[2]);
-                o[3] = __fmaf_rn(s1, __fmul_rn(q.z, __fmaf_rn(-z1, q.w, v[3])), o[3]);
+                o[0] = __fmaf_rn(s.x, __fmul_rn(q.x, __fmaf_rn(-z.x, q.y, v[0])), o[0]);
+                o[1] = __fmaf_rn(s.x, __fmul_rn(q.z, __fmaf_rn(-z.x, q.w, v[1])), o[1]);
+                o[2] = __fmaf_rn(s.y, __fmul_rn(q.x, __fmaf_rn(-z.y, q.y, v[2])), o[2]);
+                o[3] = __fmaf_rn(s.y, __fmul_rn(q.z, __fmaf_rn(-z.y, q.w, v[3])), o[3]);
             }
         }
     }
 }
 
-// This lane's word of row lane / 4 in a stage's codes.
-__device__ __forceinline__ uint32_t s4_code_at(int lane) { return uint32_t(lane >> 2) * kS4RowBytes + uint32_t(lane & 3) * 4u; }
+// This lane's piece (UNIT 4) or word of row lane / 4 in a stage's codes.
+template <int UNIT>
+__device__ __forceinline__ uint32_t s4_code_at(int lane) {
+    const int gr = lane >> 2, t = lane & 3;
+    return UNIT == 4 ? s4_piece<4>(gr, t) : s4_piece<1>(gr, 0) + uint32_t(t) * 4u;
+}
 
 // ------------------------------------------------------------ host side
 // Weights of one matrix (or of the experts') as the C entry points take them.

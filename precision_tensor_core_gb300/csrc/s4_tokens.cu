@@ -33,7 +33,7 @@ namespace ptc {
 namespace {
 
 constexpr int kWarps4 = 8, kThreads4 = 32 * kWarps4;
-__host__ __device__ constexpr int stages_of(int mt) { return mt == 1 ? 6 : 4; }
+constexpr int kStages4 = 4;  // of a warp's ring
 
 struct S4Args {
     const void *x;
@@ -56,9 +56,9 @@ struct S4Args {
 };
 
 template <typename X, int MT, int NT, int UNIT>
-__global__ void __launch_bounds__(kThreads4, 2) s4_kernel(const S4Args a) {
-    constexpr int TOK = 8 * NT, GROUPS = 4 / UNIT, D = stages_of(MT);
-    extern __shared__ __align__(128) uint8_t smem4[];
+__global__ void __launch_bounds__(kThreads4, MT == 1 ? 3 : 2) s4_kernel(const S4Args a) {
+    constexpr int TOK = 8 * NT, GROUPS = 4 / UNIT, D = kStages4;
+    extern __shared__ __align__(256) uint8_t smem4[];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int gr = lane >> 2, t = lane & 3;
     const int krank = a.ks == 1 ? 0 : int(cluster_ctarank());
@@ -69,10 +69,9 @@ __global__ void __launch_bounds__(kThreads4, 2) s4_kernel(const S4Args a) {
     // This CTA's stages of K.
     const int q = a.stages / a.ks, rest = a.stages % a.ks;
     const int c0 = krank * q + min(krank, rest), c1 = c0 + q + (krank < rest ? 1 : 0);
-    uint8_t *ring = smem4 + warp * D * a.stage_bytes;
-    uint8_t *xs_base = smem4 + kWarps4 * D * a.stage_bytes;
+    const uint32_t ring = uint32_t(warp * D * a.stage_bytes), xs_base = uint32_t(kWarps4 * D * a.stage_bytes);
     const uint32_t tok_bytes = uint32_t(a.chunk) * kS4XBytes, ps_at = tok_bytes * uint32_t(ntok);
-    const uint32_t buf_bytes = ps_at + uint32_t(a.chunk) * (GROUPS * TOK * 8);
+    const uint32_t buf_bytes = (ps_at + uint32_t(a.chunk) * (GROUPS * TOK * 8) + 255u) & ~255u;  // (tokens' places rest on 256)
 
     griddep_wait();
     griddep_launch_dependents();
@@ -82,7 +81,8 @@ __global__ void __launch_bounds__(kThreads4, 2) s4_kernel(const S4Args a) {
     const int crow = lane >> 2, piece = lane & 3;
     const uint8_t *src[2 * MT];
 #pragma unroll
-    for (int j = 0; j < 2 * MT; ++j) src[j] = a.codes + int64_t(min(row0 + 8 * j + crow, a.N - 1)) * a.pitch + piece * 16;
+    for (int j = 0; j < 2 * MT; ++j)  // (MMA rows crow and crow + 8 of each tile)
+        src[j] = a.codes + int64_t(min(row0 + 16 * (j >> 1) + s4_row(crow + 8 * (j & 1)), a.N - 1)) * a.pitch + piece * 16;
     constexpr int PIECES = MT * GROUPS * 2;  // of scales
     const uint8_t *scale_src = nullptr;
     const int sp = lane % PIECES, sm = sp / (2 * GROUPS), sg = sp / 2 % GROUPS;
@@ -91,51 +91,70 @@ __global__ void __launch_bounds__(kThreads4, 2) s4_kernel(const S4Args a) {
         const int64_t tile = min(row0 / 16 + sm, (a.N + 15) / 16 - 1);
         scale_src = (lane < PIECES ? a.scales : a.zeros) + tile * a.groups * 32 + (sp & 1) * 16;
     }
-    auto issue = [&](int i) {
-        const int st = c0 + share + i * S;
-        if (st < c1) {
-            const uint32_t dst = smem_u32(ring + (i % D) * a.stage_bytes);
-            const int n = min(16, max(0, a.row_bytes - st * kS4RowBytes - piece * 16));
+    // The next stage to bring, its place in the ring and its group.
+    int next = c0 + share, into = 0, group = GROUPS == 1 ? next / a.per_group : 0, in_group = GROUPS == 1 ? next % a.per_group : 0;
+    const uint32_t ring_at = smem_u32(smem4) + ring;
+    const uint32_t dst_at = ring_at + s4_piece<UNIT>(crow, piece), dst_at8 = ring_at + s4_piece<UNIT>(crow + 8, piece);
+    auto issue = [&]() {
+        if (next < c1) {
+            const uint32_t slot = uint32_t(into * a.stage_bytes);
+            const int n = min(16, a.row_bytes - next * kS4RowBytes - piece * 16);
 #pragma unroll
             for (int j = 0; j < 2 * MT; ++j)
-                copy16(dst + (j >> 1) * kS4TileBytes + s4_piece(8 * (j & 1) + crow, piece),
-                       n > 0 ? src[j] + int64_t(st) * kS4RowBytes : a.codes, n);
+                copy16((j & 1 ? dst_at8 : dst_at) + slot + (j >> 1) * kS4TileBytes,
+                       n > 0 ? src[j] + int64_t(next) * kS4RowBytes : a.codes, max(n, 0));
             if (scale_lane) {
-                const int g = GROUPS == 1 ? st / a.per_group : st * GROUPS + sg;
-                copy16(dst + MT * kS4TileBytes + lane * 16, g < a.groups ? scale_src + int64_t(g) * 32 : a.scales,
+                const int g = GROUPS == 1 ? group : next * GROUPS + sg;
+                copy16(ring_at + slot + MT * kS4TileBytes + lane * 16, g < a.groups ? scale_src + int64_t(g) * 32 : a.scales,
                        g < a.groups ? 16 : 0);
+            }
+            next += S;
+            if (++into == D) into = 0;
+            if constexpr (GROUPS == 1) {
+                in_group += S;
+                while (in_group >= a.per_group) {
+                    in_group -= a.per_group;
+                    ++group;
+                }
             }
         }
         copies_commit();
     };
 #pragma unroll
-    for (int i = 0; i < D - 1; ++i) issue(i);
+    for (int i = 0; i < D - 1; ++i) issue();
 
-    // Activations of chunk c to its buffer: 4 UNIT lanes a block, a warp 32 / (4 UNIT).
+    // Activations of chunk c to its buffer: 4 UNIT lanes a block, a warp 32 / (4 UNIT),
+    // four loads in flight per lane.
     auto load_x = [&](int c) {
         constexpr int LANES = 4 * UNIT, PER = 32 / LANES;
-        uint8_t *buf = xs_base + (a.buffers == 2 && (c & 1) ? buf_bytes : 0u);
-        const int first = c0 + c * a.chunk, n = min(a.chunk, c1 - first);   // stages
-        const int blocks = n * GROUPS;
-        for (int u = warp * PER; u < blocks * ntok; u += kWarps4 * PER) {
-            const int mine = u + lane / LANES;
-            const bool ok = mine < blocks * ntok;
-            const int tok = ok ? mine / blocks : 0, blk = ok ? mine - tok * blocks : 0;
-            const int k = first * kS4Stage + blk * (32 * UNIT) + (lane % LANES) * 8;
-            const int have = ok ? max(0, min(8, a.K - k)) : 0;
-            const X *p = static_cast<const X *>(a.x) + int64_t(tok0 + tok) * a.ldx + (have > 0 ? k : 0);
-            const Pack8<X> raw = load8(p, have, a.xvec != 0);
-            float v[8];
+        const uint32_t buf = xs_base + (a.buffers == 2 && (c & 1) ? buf_bytes : 0u);
+        const int first = c0 + c * a.chunk, blocks = min(a.chunk, c1 - first) * GROUPS;
+        const int part = lane % LANES, k0 = first * kS4Stage + part * 8;
+        const int rounds = (blocks + PER - 1) / PER, all = rounds * ntok;
+        for (int u0 = warp; u0 < all; u0 += 4 * kWarps4) {
+            uint4 raw[4];
+            int at[4], tk[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = to_float(raw.get(j));
-            uint4 hi, lo;
-            float2 ps;
-            s4_operands<UNIT, false>(v, hi, lo, ps);
-            if (ok) {
-                const int st = blk / GROUPS, g = blk % GROUPS;
-                const int pc = g * (4 * UNIT) + lane % LANES;  // piece of the token's stage
-                *reinterpret_cast<uint4 *>(buf + uint32_t(tok) * tok_bytes + uint32_t(st) * kS4XBytes + s4_x_piece(tok, pc)) = hi;
-                if (lane % LANES == 0) *reinterpret_cast<float2 *>(buf + ps_at + uint32_t((st * GROUPS + g) * TOK + tok) * 8u) = ps;
+            for (int j = 0; j < 4; ++j) {
+                const int u = u0 + j * kWarps4;
+                tk[j] = u / rounds;
+                at[j] = (u - tk[j] * rounds) * PER + lane / LANES;  // block
+                const int k = k0 + at[j] * (32 * UNIT);
+                const int have = u < all && at[j] < blocks ? max(0, min(8, a.K - k)) : 0;
+                const X *p = static_cast<const X *>(a.x) + (have > 0 ? int64_t(tok0 + tk[j]) * a.ldx + k : 0);
+                raw[j] = load8(p, have, a.xvec != 0).v[0];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (u0 + j * kWarps4 >= all) break;
+                float2 ps;
+                const uint4 op = s4_operands<UNIT, X>(raw[j], ps);
+                if (at[j] < blocks) {
+                    const int st = at[j] / GROUPS, g = at[j] % GROUPS;
+                    *reinterpret_cast<uint4 *>(smem4 + buf + uint32_t(tk[j]) * tok_bytes + uint32_t(st) * kS4XBytes +
+                                               s4_x_piece<UNIT>(tk[j], g * LANES + part)) = op;
+                    if (part == 0) *reinterpret_cast<float2 *>(smem4 + buf + ps_at + uint32_t(at[j] * TOK + tk[j]) * 8u) = ps;
+                }
             }
         }
     };
@@ -148,25 +167,30 @@ __global__ void __launch_bounds__(kThreads4, 2) s4_kernel(const S4Args a) {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) tot[m][n][i] = 0.0f;
-    const uint32_t code_at = s4_code_at(lane);
-    int i = 0;
-    for (int c = 0; c * a.chunk < c1 - c0; ++c) {
+    const uint32_t code_at = ring + s4_code_at<UNIT>(lane), scale_at = ring + MT * kS4TileBytes;
+    const uint32_t zeros = a.zeros ? PIECES * 16 : 0;
+    uint32_t tok_at[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {  // (tokens past the last read it again; their sums are dropped)
+        const int tok = min(8 * n + gr, ntok - 1);
+        tok_at[n] = uint32_t(tok) * tok_bytes + uint32_t(t) * 16u + uint32_t(tok & 1) * 64u;
+    }
+    int from = 0;  // place in the ring
+    for (int c = 0, st = c0 + share; c * a.chunk < c1 - c0; ++c) {
         __syncthreads();  // chunk c is there, and everyone is done with the other buffer
         if (a.buffers == 2 && (c + 1) * a.chunk < c1 - c0) load_x(c + 1);
-        const uint8_t *buf = xs_base + (a.buffers == 2 && (c & 1) ? buf_bytes : 0u);
-        const int end = min(c1, c0 + (c + 1) * a.chunk);
-        for (int st = c0 + share + i * S; st < end; st += S, ++i) {
+        const uint32_t buf = xs_base + (a.buffers == 2 && (c & 1) ? buf_bytes : 0u);
+        const int first = c0 + c * a.chunk, end = min(c1, first + a.chunk);
+        for (; st < end; st += S) {
             copies_wait<D - 2>();
             __syncwarp();
-            issue(i + D - 1);
-            const uint8_t *stage = ring + (i % D) * a.stage_bytes;
-            const uint32_t local = uint32_t(st - c0 - c * a.chunk);
-            const uint8_t *x[NT];
+            issue();
+            const uint32_t slot = uint32_t(from * a.stage_bytes), local = uint32_t(st - first);
+            if (++from == D) from = 0;
+            uint32_t x[NT];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)  // (tokens past the last read it again; their sums are dropped)
-                x[n] = buf + uint32_t(min(8 * n + gr, ntok - 1)) * tok_bytes + local * kS4XBytes + uint32_t(t) * 16u;
-            s4_stage<MT, NT, UNIT, 1>(tot, stage + code_at, stage + MT * kS4TileBytes,
-                                      a.zeros ? stage + MT * kS4TileBytes + PIECES * 16 : nullptr, a.bf16_scales != 0, x, 0u,
+            for (int n = 0; n < NT; ++n) x[n] = buf + tok_at[n] + local * kS4XBytes;
+            s4_stage<MT, NT, UNIT, 1>(tot, smem4, code_at + slot, scale_at + slot, zeros, a.bf16_scales != 0, x, 0u,
                                       buf + ps_at + local * (GROUPS * TOK * 8), lane);
         }
     }
@@ -180,9 +204,9 @@ __global__ void __launch_bounds__(kThreads4, 2) s4_kernel(const S4Args a) {
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int r = 16 * m + gr, tk = 8 * n + 2 * t;
+            const int r = 16 * m + 2 * gr, tk = 8 * n + 2 * t;  // rows 2 gr and 2 gr + 1 of the tile
             *reinterpret_cast<float2 *>(part + r * TOK + tk) = make_float2(tot[m][n][0], tot[m][n][1]);
-            *reinterpret_cast<float2 *>(part + (r + 8) * TOK + tk) = make_float2(tot[m][n][2], tot[m][n][3]);
+            *reinterpret_cast<float2 *>(part + (r + 1) * TOK + tk) = make_float2(tot[m][n][2], tot[m][n][3]);
         }
     if (a.ks > 1)
         cluster_sync();
@@ -214,7 +238,7 @@ std::atomic<int> g_s4_rows{0};   // "s4_tokens_rows": 0 by size, 1, 2, 4, 8
 std::atomic<int> g_s4_split{0};  // "s4_tokens_split": 0 by size, 1, 2, 4, 8
 std::atomic<int> g_s4_tiles{0};  // "s4_tokens_tiles": 0 by size, 1, 2
 
-constexpr int kSmem4 = 226 * 1024, kSmem4Half = 113 * 1024;  // one CTA per SM, two
+constexpr int kSmem4 = 227 * 1024, kSmemSm = 228 * 1024;  // of a CTA, of an SM (1 KB per CTA is the system's)
 
 // Rows and K shares of a launch, and how the activations are held.
 struct S4Shape {
@@ -223,15 +247,20 @@ struct S4Shape {
     size_t smem;
 };
 
+// Of a stage: codes, scales, zeros; in whole 64 bytes, on which the codes' places rest.
+int stage_bytes4(int mt, int groups, const void *zeros) { return (mt * (kS4TileBytes + groups * 32 * (zeros ? 2 : 1)) + 63) / 64 * 64; }
+
 // Shared memory of a shape; false where a buffer does not hold a stage of every share.
 bool fit_s4(S4Shape &sh, const S4Args &a, int groups_per_stage, int toks, int tok, int64_t ctas, int sms) {
-    const int S = kWarps4 >> sh.r_log2, most = ctas <= sms ? kSmem4 : kSmem4Half;
-    const int ring = kWarps4 * stages_of(sh.mt) * sh.mt * (kS4TileBytes + groups_per_stage * 32 * (a.zeros ? 2 : 1));
+    const int S = kWarps4 >> sh.r_log2;
+    const int per_sm = int(std::min<int64_t>(sh.mt == 1 ? 3 : 2, (ctas + sms - 1) / sms));
+    const int most = std::min(kSmem4, kSmemSm / per_sm - 1024) / 256 * 256;
+    const int ring = kWarps4 * kStages4 * stage_bytes4(sh.mt, groups_per_stage, a.zeros);
     const int per_stage = toks * kS4XBytes + groups_per_stage * tok * 8;
-    const int range = (a.stages + sh.ks - 1) / sh.ks, fit = (most - ring) / per_stage;
-    sh.buffers = range <= fit ? 1 : 2;
-    sh.chunk = sh.buffers == 1 ? range : fit / 2 / S * S;
-    sh.smem = size_t(ring) + size_t(sh.buffers) * sh.chunk * per_stage;
+    const int range = (a.stages + sh.ks - 1) / sh.ks;  // the longest of a CTA
+    sh.buffers = range * per_stage <= most - ring ? 1 : 2;
+    sh.chunk = sh.buffers == 1 ? range : (most - ring) / 2 / 256 * 256 / per_stage / S * S;
+    sh.smem = size_t(ring) + size_t(sh.buffers) * size_t((sh.chunk * per_stage + 255) / 256 * 256);
     return sh.chunk > 0;
 }
 
@@ -281,7 +310,7 @@ int launch_s4(S4Args a, const S4Shape &sh, cudaStream_t stream) {
     }
     a.r_log2 = sh.r_log2;
     a.ks = sh.ks;
-    a.stage_bytes = MT * (kS4TileBytes + GROUPS * 32 * (a.zeros ? 2 : 1));
+    a.stage_bytes = stage_bytes4(MT, GROUPS, a.zeros);
     a.buffers = sh.buffers;
     a.chunk = sh.chunk;
     const size_t smem = sh.smem;
