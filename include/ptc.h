@@ -16,6 +16,7 @@
  * train and decode with: gemm_fp4, gemm_a16_fp4, ptc_quantize_fp4,
  * ptc_dequantize_fp4, ptc_dropout and ptc_dropout_to (see "Microscaled 4-bit matrices" below),
  * the product of a few tokens with 4-bit integer weights that have group scales, gemm_a16_s4,
+ * a mixture-of-experts layer with such weights, ptc_moe_a16_s4,
  * and the norm before a product, ptc_rms_norm, ptc_rms_norm_s8 and ptc_rms_norm_backward.
  *
  * The first three compute C <- A.B exactly as the plain sum over k, with C
@@ -460,6 +461,33 @@ int gemm_a16_fp4(int64_t M, int64_t N, int64_t K, int type, const void *X, int64
  */
 int gemm_a16_s4(int64_t M, int64_t N, int64_t K, int type, const void *X, int64_t ldx, const void *W, int64_t ldw,
                 int64_t group, int scale_type, const void *scales, const void *zeros, void *C, int64_t ldc, void *stream);
+
+/*
+ * A mixture-of-experts layer for a few tokens, with grouped 4-bit integer weights:
+ *   logits = X router^T in FP32; the top_k largest of a token are its experts, in falling
+ *     order (equal ones: the lowest index first; NaN counts as the smallest)
+ *   p = softmax of a token's logits over all experts, or (renormalize) over the chosen
+ *   h = silu(gate x) (up x),  Y = out( sum over the chosen of p down h )
+ * X: `tokens` rows of `hidden` bfloat16 or binary16 elements (`type`), at most 64 rows and
+ * 512 / top_k.  router: a row of `hidden` per expert, of X's type or float32.  gate_up:
+ * an expert's 2 `inner` rows of `hidden` weights, the gate's first; down: its `hidden`
+ * rows of `inner`; both in the layout above with one `group`, rows ld_... bytes apart and
+ * experts expert_... bytes apart (multiples of 16), the experts' scale tiles one after
+ * another.  Y has X's type.  ids and weights ([tokens][top_k], or NULL) receive the chosen
+ * experts and their p.  Sizes: hidden and inner 1 .. 2^20, experts up to 512, top_k up to 32.
+ * Only the chosen experts' weights are read, once per eight of an expert's tokens.  Products and
+ * activations as gemm_a16_s4; h is not rounded to 16 bits (22 bits are kept).  Results
+ * are the same from call to call.  The workspace has at least
+ * ptc_moe_a16_s4_workspace(...) bytes (0: the sizes are refused), 256-byte aligned, and is
+ * no other call's until this one is done.
+ */
+int64_t ptc_moe_a16_s4_workspace(int64_t tokens, int64_t hidden, int64_t inner, int64_t experts, int64_t top_k);
+int ptc_moe_a16_s4(int64_t tokens, int64_t hidden, int64_t inner, int64_t experts, int64_t top_k, int renormalize, int type,
+                   const void *X, int64_t ldx, const void *router, int64_t ldr, int router_type, int64_t group, int scale_type,
+                   const void *gate_up, int64_t ld_gate_up, int64_t expert_gate_up, const void *gate_up_scales,
+                   const void *gate_up_zeros, const void *down, int64_t ld_down, int64_t expert_down, const void *down_scales,
+                   const void *down_zeros, void *Y, int64_t ldy, int32_t *ids, float *weights, void *workspace,
+                   int64_t workspace_bytes, void *stream);
 
 /*
  * Root-mean-square norm of rows

@@ -11,7 +11,8 @@ library's CUDA kernels):
   ``gemm_s8_noalloc``, ``gemm_s8_b_rowmajor``, ``gemm_status_string``,
   ``gemm_poll_device_error``, ``ptc_kernel_launch_count``, ``ptc_last_launch``, ``ptc_last_fp4_launch``, ``ptc_last_conversion``, ``ptc_plan_shape``,
   ``ptc_debug_set_wait_limit``, ``ptc_set_tuning``, ``gemm_fp4``, ``gemm_a16_fp4``, ``ptc_dropout``,
-  ``ptc_dropout_to``, ``ptc_quantize_fp4``, ``ptc_dequantize_fp4``, ``gemm_a16_s4``, ``ptc_rms_norm``, ``ptc_rms_norm_s8``,
+  ``ptc_dropout_to``, ``ptc_quantize_fp4``, ``ptc_dequantize_fp4``, ``gemm_a16_s4``, ``ptc_moe_a16_s4``,
+  ``ptc_moe_a16_s4_workspace``, ``ptc_rms_norm``, ``ptc_rms_norm_s8``,
   ``ptc_rms_norm_backward``, ``ptc_rms_norm_backward_workspace``: the C ABI of
   ``include/ptc.h`` under the same names, taking integers (sizes, leading
   dimensions, device addresses, a cudaStream_t handle).  A nonzero status
@@ -25,8 +26,8 @@ library's CUDA kernels):
   :class:`Fp4Matrix`: counter-based dropout and microscaled 4-bit matrices on
   torch tensors of the device; :mod:`precision_tensor_core_gb300.fp4_linear`
   puts them together as a linear layer's training and decoding steps.
-* ``matmul_a16_s4`` and :class:`S4Matrix`: a few tokens with 4-bit integer weights that have
-  group scales.
+* ``matmul_a16_s4``, ``moe_a16_s4`` and :class:`S4Matrix`: a few tokens with 4-bit integer
+  weights that have group scales, in one matrix or as a mixture of experts.
 * ``rms_norm``, ``rms_norm_s8``, ``rms_norm_backward``: the norm before a product, also as
   the 8-bit operand of ``matmul_s8_scaled``.
 
@@ -110,6 +111,8 @@ def lib() -> ctypes.CDLL:
                               _vp]),
                 ("gemm_a16_fp4", [_i64, _i64, _i64, _int, _vp, _i64, _int, _vp, _i64, _vp, _vp, _vp, _i64, _vp]),
                 ("gemm_a16_s4", [_i64, _i64, _i64, _int, _vp, _i64, _vp, _i64, _i64, _int, _vp, _vp, _vp, _i64, _vp]),
+                ("ptc_moe_a16_s4", [_i64] * 5 + [_int, _int, _vp, _i64, _vp, _i64, _int, _i64, _int]
+                 + [_vp, _i64, _i64, _vp, _vp] * 2 + [_vp, _i64, _vp, _vp, _vp, _i64, _vp]),
                 ("ptc_rms_norm", [_i64, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64, _vp, _int, _f32, _vp, _i64, _vp]),
                 ("ptc_rms_norm_s8", [_i64, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64, _vp, _int, _f32, _vp, _i64, _vp,
                                      _vp]),
@@ -118,6 +121,8 @@ def lib() -> ctypes.CDLL:
             fn = getattr(L, name)
             fn.restype = ctypes.c_int
             fn.argtypes = args
+        L.ptc_moe_a16_s4_workspace.restype = _i64
+        L.ptc_moe_a16_s4_workspace.argtypes = [_i64] * 5
         L.ptc_rms_norm_backward_workspace.restype = _i64
         L.ptc_rms_norm_backward_workspace.argtypes = [_i64, _i64]
         L.gemm_baseline.restype = ctypes.c_int
@@ -259,6 +264,21 @@ def gemm_a16_fp4(M, N, K, type, X, ldx, format, W, ldw, SW, GW, C, ldc, stream=0
 def gemm_a16_s4(M, N, K, type, X, ldx, W, ldw, group, scale_type, scales, zeros, C, ldc, stream=0) -> int:
     """Few 16-bit tokens times 4-bit integer weights with group scales (include/ptc.h)."""
     return _check(lib().gemm_a16_s4(M, N, K, type, X, ldx, W, ldw, group, scale_type, scales, zeros, C, ldc, stream))
+
+
+def ptc_moe_a16_s4_workspace(tokens, hidden, inner, experts, top_k) -> int:
+    """Bytes of workspace that ptc_moe_a16_s4 takes; 0 for sizes that it refuses."""
+    return lib().ptc_moe_a16_s4_workspace(tokens, hidden, inner, experts, top_k)
+
+
+def ptc_moe_a16_s4(tokens, hidden, inner, experts, top_k, renormalize, type, X, ldx, router, ldr, router_type, group,
+                   scale_type, gate_up, ld_gate_up, expert_gate_up, gate_up_scales, gate_up_zeros, down, ld_down,
+                   expert_down, down_scales, down_zeros, Y, ldy, ids, weights, workspace, workspace_bytes, stream=0) -> int:
+    """A mixture-of-experts layer for a few tokens (include/ptc.h)."""
+    return _check(lib().ptc_moe_a16_s4(tokens, hidden, inner, experts, top_k, renormalize, type, X, ldx, router, ldr,
+                                       router_type, group, scale_type, gate_up, ld_gate_up, expert_gate_up, gate_up_scales,
+                                       gate_up_zeros, down, ld_down, expert_down, down_scales, down_zeros, Y, ldy, ids,
+                                       weights, workspace, workspace_bytes, stream))
 
 
 def ptc_rms_norm(rows, cols, x, ldx, type, residual, ldr, sum, lds, weight, weight_type, eps, y, ldy, stream=0) -> int:
@@ -524,7 +544,8 @@ def _load_native():
     L = lib()
     n.init(*(ctypes.cast(getattr(L, f), _vp).value for f in ("ptc_dropout_to", "ptc_quantize_fp4",
                                                              "ptc_dequantize_fp4", "gemm_fp4", "gemm_a16_fp4",
-                                                             "gemm_a16_s4", "ptc_rms_norm", "ptc_rms_norm_s8",
+                                                             "gemm_a16_s4", "ptc_moe_a16_s4_workspace",
+                                                             "ptc_moe_a16_s4", "ptc_rms_norm", "ptc_rms_norm_s8",
                                                              "ptc_rms_norm_backward_workspace",
                                                              "ptc_rms_norm_backward")),
            _check, _stream, Fp4Matrix, S4Matrix)
@@ -716,6 +737,22 @@ def matmul_a16_s4(x, Wt, out=None, stream=None):
     summed in FP32: the product of a decoding step, for M up to 16 rows (more are taken 16
     at a time)."""
     return (_native or _load_native()).matmul_a16_s4(x, Wt, out, stream)
+
+
+def moe_a16_s4(x, router, gate_up, down, top_k, renormalize=True, out=None, return_routing=False, stream=None):
+    """A mixture-of-experts layer for up to 64 tokens x (tokens, hidden) bfloat16 or float16
+    -> x's dtype: each token's ``top_k`` experts of the largest logits x router^T, their
+    weights p the softmax over the chosen (``renormalize``) or over all experts, and the
+    sum of p * down(silu(gate(x)) * up(x)).
+
+    router: (experts, hidden), x's dtype or float32
+    gate_up: :class:`S4Matrix` of (experts, 2 inner, hidden), the gate's rows first; down: of
+        (experts, hidden, inner), with the same group and scales' dtype
+    return_routing: also give the chosen experts (tokens, top_k) int32, in falling order
+        of their logits (equal ones: the lowest first), and their weights p in float32
+
+    tokens * top_k is at most 512.  Outside autograd, as the other products."""
+    return (_native or _load_native()).moe_a16_s4(x, router, gate_up, down, top_k, renormalize, out, return_routing, stream)
 
 
 # ---------------------------------------------------------------- norms on tensors

@@ -24,7 +24,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libptc.so")
 SOURCES = ["gemm_tc.cu", "convert.cu", "api.cu", "gemm_s8_noalloc.cu", "baseline.cu", "fp4_quant.cu",
-           "fp4_gemm.cu", "fp4_tokens.cu", "norm.cu", "s4_tokens.cu"]
+           "fp4_gemm.cu", "fp4_tokens.cu", "norm.cu", "s4_tokens.cu",
+           "s4_experts.cu"]
 BINDING = "binding.cpp"
 NATIVE = os.path.join(HERE, "_native.so")
 GENCODE = "-gencode=arch=compute_103a,code=sm_103a"

@@ -1112,11 +1112,12 @@ int gemm_poll_device_error(void) {
     uint32_t w = 0;
     cudaError_t e = ptc::read_and_clear_error_word(&w);
     if (e != cudaSuccess) return fail_cuda(e, "reading the device error word");
-    uint32_t w4 = 0, wt = 0;
+    uint32_t w4 = 0, wt = 0, wm = 0;
     e = ptc::read_and_clear_fp4_error_word(&w4);
     if (e == cudaSuccess) e = ptc::read_and_clear_tokens_error_word(&wt);
+    if (e == cudaSuccess) e = ptc::read_and_clear_moe_error_word(&wm);
     if (e != cudaSuccess) return fail_cuda(e, "reading the device error word");
-    return (w | w4 | wt) ? PTC_ERR_TIMEOUT : PTC_OK;
+    return (w | w4 | wt | wm) ? PTC_ERR_TIMEOUT : PTC_OK;
 }
 
 uint64_t ptc_kernel_launch_count(void) { return g_launches.load(); }

@@ -26,6 +26,8 @@ decltype(&ptc_dequantize_fp4) f_dequantize;
 decltype(&gemm_fp4) f_gemm;
 decltype(&gemm_a16_fp4) f_gemm_a16;
 decltype(&gemm_a16_s4) f_gemm_a16_s4;
+decltype(&ptc_moe_a16_s4_workspace) f_moe_workspace;
+decltype(&ptc_moe_a16_s4) f_moe;
 decltype(&ptc_rms_norm) f_norm;
 decltype(&ptc_rms_norm_s8) f_norm_s8;
 decltype(&ptc_rms_norm_backward_workspace) f_norm_workspace;
@@ -542,6 +544,51 @@ PyObject *py_matmul_a16_s4(PyObject *, PyObject *const *a, Py_ssize_t n) {
     PTC_BODY_END
 }
 
+// (x, router, gate_up, down, top_k, renormalize, out, return_routing, stream)
+PyObject *py_moe(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    PTC_BODY_BEGIN
+    expect(n, 9);
+    const at::Tensor &x = outside_autograd(tensor(a[0], "x"), "x"), &router = outside_autograd(tensor(a[1], "router"), "router");
+    const int type = type_of(x.scalar_type()), router_type = type_of(router.scalar_type());
+    if (type == PTC_OUT_F32) raise(PyExc_TypeError, "moe_a16_s4 takes bfloat16 or float16 activations");
+    if (router_type != type && router_type != PTC_OUT_F32) raise(PyExc_TypeError, "router is of x's dtype or float32");
+    const Rows rx = rows_of(x, "x"), rr = rows_of(router, "router");
+    const S4 gu = s4_of(a[2]), dn = s4_of(a[3]);
+    const int64_t top_k = integer(a[4]);
+    const int renormalize = PyObject_IsTrue(a[5]), routing = PyObject_IsTrue(a[7]);
+    if (renormalize < 0 || routing < 0) throw Bad();
+    if (!gu.many || !dn.many) raise(PyExc_ValueError, "gate_up and down hold several matrices (experts)");
+    if (gu.experts != dn.experts || gu.experts != rr.rows || gu.k != rx.cols || rr.cols != rx.cols || gu.rows != 2 * dn.k ||
+        dn.rows != rx.cols)
+        raise(PyExc_ValueError, "sizes differ: x (tokens, hidden), router (experts, hidden), gate_up (experts, 2 inner, hidden), "
+                                "down (experts, hidden, inner)");
+    if (gu.group != dn.group || gu.type != dn.type) raise(PyExc_ValueError, "gate_up and down must share their group and scales' dtype");
+    const c10::DeviceIndex index = x.get_device();
+    if (gu.index != index || dn.index != index || router.get_device() != index ||
+        (a[6] != Py_None && tensor(a[6], "out").scalar_type() != x.scalar_type()))
+        raise(PyExc_ValueError, "x, router, the weights and out must share a device, x and out a dtype");
+    const int64_t bytes = rx.rows ? f_moe_workspace(rx.rows, rx.cols, dn.k, gu.experts, top_k) : 0;
+    const Target target(index, a[8]);
+    at::Tensor y = result(a[6], rx.rows, rx.cols, x.scalar_type(), index, x.device());
+    const Rows ry = rows_of(y, "out");
+    at::Tensor ids, weights, ws = empty({bytes}, at::kByte, x.device());
+    if (routing && top_k >= 0) {
+        ids = empty({rx.rows, top_k}, at::kInt, x.device());
+        weights = empty({rx.rows, top_k}, at::kFloat, x.device());
+    }
+    target.run([&](void *s) {
+        return f_moe(rx.rows, rx.cols, dn.k, gu.experts, top_k, renormalize, type, rx.p, rx.ld, rr.p, rr.ld, router_type, gu.group,
+                     gu.type, gu.codes, gu.pitch, gu.expert, gu.scales, gu.zeros, dn.codes, dn.pitch, dn.expert, dn.scales, dn.zeros,
+                     ry.p, ry.ld, ids.defined() ? static_cast<int32_t *>(ids.data_ptr()) : nullptr,
+                     weights.defined() ? static_cast<float *>(weights.data_ptr()) : nullptr, ws.data_ptr(), bytes, s);
+    });
+    for (int i : {0, 1, 2, 3}) target.used(a[i]);
+    if (!routing) return give(target, a[6], std::move(y));
+    Ref yo(give(target, a[6], std::move(y))), io(give(target, Py_None, std::move(ids))), wo(give(target, Py_None, std::move(weights)));
+    return PyTuple_Pack(3, yo.p, io.p, wo.p);
+    PTC_BODY_END
+}
+
 // What the norms share: x, an optional tensor of x's shape, type and device, and the weight.
 const at::Tensor &same_as(const at::Tensor &x, const char *of, const at::Tensor &t, const char *name) {
     if (t.scalar_type() != x.scalar_type() || t.sizes() != x.sizes() || !t.is_cuda() || t.get_device() != x.get_device()) {
@@ -689,10 +736,10 @@ PyObject *py_check_s4(PyObject *, PyObject *const *a, Py_ssize_t n) {
     PTC_BODY_END
 }
 
-// (addresses of the ten C entry points, status check, stream handle, Fp4Matrix, S4Matrix)
+// (addresses of the twelve C entry points, status check, stream handle, Fp4Matrix, S4Matrix)
 PyObject *py_init(PyObject *, PyObject *const *a, Py_ssize_t n) {
     PTC_BODY_BEGIN
-    expect(n, 14);
+    expect(n, 16);
     auto entry = [&](auto &f) { f = reinterpret_cast<std::decay_t<decltype(f)>>(uintptr_t(seed64(*a++))); };
     entry(f_dropout);
     entry(f_quantize);
@@ -700,6 +747,8 @@ PyObject *py_init(PyObject *, PyObject *const *a, Py_ssize_t n) {
     entry(f_gemm);
     entry(f_gemm_a16);
     entry(f_gemm_a16_s4);
+    entry(f_moe_workspace);
+    entry(f_moe);
     entry(f_norm);
     entry(f_norm_s8);
     entry(f_norm_workspace);
@@ -735,6 +784,7 @@ PyMethodDef g_methods[] = {PTC_METHOD("init", py_init),
                            PTC_METHOD("matmul", py_matmul),
                            PTC_METHOD("matmul_a16", py_matmul_a16),
                            PTC_METHOD("matmul_a16_s4", py_matmul_a16_s4),
+                           PTC_METHOD("moe_a16_s4", py_moe),
                            PTC_METHOD("check_s4", py_check_s4),
                            PTC_METHOD("rms_norm", py_norm),
                            PTC_METHOD("rms_norm_s8", py_norm_s8),

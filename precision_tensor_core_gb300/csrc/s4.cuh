@@ -99,6 +99,22 @@ __device__ __forceinline__ uint4 s4_operands(const uint4 &raw, float2 &factor_su
     return make_uint4(s4_pair(v[0], v[4]), s4_pair(v[2], v[6]), s4_pair(v[1], v[5]), s4_pair(v[3], v[7]));
 }
 
+// One FP32 activation of a block that a warp's 32 lanes hold, as two operands whose sum
+// has 22 bits (hi: rounded to binary16, lo: what that left), and the block's factor and sum.
+__device__ __forceinline__ void s4_operand32(float v, int lane, __half &hi, __half &lo, float2 &factor_sum) {
+    float down, factor;
+    s4_powers(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu), down, factor);
+    const float x = __fmul_rn(v, down), part = __fmul_rn(x, (lane & 1) ? 0x1p-4f : 1.0f);
+    hi = __float2half_rn(part);
+    lo = __float2half_rn(__fsub_rn(part, __half2float(hi)));
+    float sum = x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    factor_sum = make_float2(factor, __fmul_rn(sum, 0x1p-24f));
+}
+// Where element e (0 .. 7) of a word lies among its operands' halves: 0, 4, 2, 6, 1, 5, 3, 7.
+__device__ __forceinline__ int s4_half(int e) { return ((e & 1) << 2) | (e & 2) | (e >> 2); }
+
 // ------------------------------------------------------------ copies
 // 16 (8) bytes to shared memory, `n` of them from global memory and zeros after them.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, int n) {
@@ -135,13 +151,6 @@ __device__ __forceinline__ uint32_t s4_x_piece(int j, int c) {
     return uint32_t(at ^ ((j & 1) << 2)) << 4;
 }
 
-// Two scales or zeros of either 16-bit type.
-__device__ __forceinline__ float2 s4_scales(const uint8_t *p, bool bf16) {
-    const uint32_t u = *reinterpret_cast<const uint32_t *>(p);
-    return bf16 ? make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u))
-                : __half22float2(reinterpret_cast<const __half2 &>(u));
-}
-
 // ------------------------------------------------------------ products
 __device__ __forceinline__ void s4_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                        uint32_t b1, const float (&c)[4]) {
@@ -167,16 +176,30 @@ __device__ __forceinline__ void s4_codes(uint32_t w, uint32_t (&a)[4]) {
     a[3] = and_xor(w8, 0x00F000F0u, 0x00800080u);
 }
 
+// The scales (zeros) of rows 2 gr and 2 gr + 1 of a tile, `p` those of its 16 rows; ODD:
+// these start at any row of two tiles, 2 bytes aligned.
+template <bool ODD>
+__device__ __forceinline__ float2 s4_row_scales(const uint8_t *p, int gr, bool bf16) {
+    uint32_t u;
+    if constexpr (ODD)
+        u = uint32_t(*reinterpret_cast<const uint16_t *>(p + gr * 4)) | uint32_t(*reinterpret_cast<const uint16_t *>(p + gr * 4 + 2)) << 16;
+    else
+        u = *reinterpret_cast<const uint32_t *>(p + gr * 4);
+    return bf16 ? make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u))
+                : __half22float2(reinterpret_cast<const __half2 &>(u));
+}
+
 // One stage: MT tiles of 16 rows of codes with NT sets of eight tokens.  Offsets in
-// shared memory (`smem`): codes s4_code_at<UNIT> past a multiple of 64; scales, and zeros
-// that many bytes behind (0: none), [tile][group][16]; x[n]: this lane's token of set n,
-// 16 t past a multiple of 256 (odd tokens: 64 more), x_lo: from it to the operands of the
-// low parts (PARTS 2); ps: factors and sums, [block of activations][8 NT tokens].
+// shared memory (`smem`): codes s4_code_at<UNIT> past a multiple of 64; scales[m], and
+// zeros that many bytes behind (0: none), [group][16] or (ODD) [group][32] of which 16
+// count; x[n]: this lane's token of set n, 16 t past a multiple of 256 (odd tokens: 64
+// more), x_lo: from it to the operands of the low parts (PARTS 2); ps: factors and sums,
+// [block of activations][8 NT tokens].  The stage has 4 / UNIT blocks and SG groups.
 // tot += s factor (sum of n x - (8 + z) sum of x).
-template <int MT, int NT, int UNIT, int PARTS>
-__device__ __forceinline__ void s4_stage(float (&tot)[MT][NT][4], const uint8_t *smem, uint32_t codes, uint32_t scales,
-                                         uint32_t zeros, bool bf16, const uint32_t (&x)[NT], uint32_t x_lo, uint32_t ps,
-                                         int lane) {
+template <int MT, int NT, int UNIT, int SG, int PARTS, bool ODD>
+__device__ __forceinline__ void s4_stage(float (&tot)[MT][NT][4], const uint8_t *smem, uint32_t codes,
+                                         const uint32_t (&scales)[MT], uint32_t zeros, bool bf16, const uint32_t (&x)[NT],
+                                         uint32_t x_lo, uint32_t ps, int lane) {
     constexpr int GROUPS = 4 / UNIT;
     const int gr = lane >> 2, t = lane & 3;
     uint4 wide[MT][2];
@@ -227,11 +250,11 @@ __device__ __forceinline__ void s4_stage(float (&tot)[MT][NT][4], const uint8_t 
         }
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            const uint8_t *at = smem + scales + uint32_t(m * GROUPS + g) * 32u + uint32_t(gr) * 4u;
-            const float2 s = s4_scales(at, bf16);
+            const uint8_t *at = smem + scales[m] + uint32_t(g * SG / GROUPS) * (ODD ? 64u : 32u);
+            const float2 s = s4_row_scales<ODD>(at, gr, bf16);
             float2 z = make_float2(8.0f, 8.0f);
             if (zeros != 0) {
-                const float2 more = s4_scales(at + zeros, bf16);
+                const float2 more = s4_row_scales<ODD>(at + zeros, gr, bf16);
                 z = make_float2(__fadd_rn(z.x, more.x), __fadd_rn(z.y, more.y));
             }
 #pragma unroll

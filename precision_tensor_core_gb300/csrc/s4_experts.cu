@@ -1,0 +1,736 @@
+// s4_experts.cu -- a whole mixture-of-experts layer for a few tokens, the experts' weights
+// 4-bit integers with group scales (ptc_moe_a16_s4 of include/ptc.h), in two kernels.
+//
+//   logits = x R^T, the top_k largest of each token, p their softmax
+//   h = silu(gate_e x) * (up_e x),  y = sum over the token's experts of p down_e h
+//
+// The active experts' weights are read once per eight of an expert's tokens and bound the
+// call.  router_kernel makes the logits and the tokens' operands (s4.cuh).  Every CTA of
+// experts_kernel finds the experts and their tokens from the logits, which is less than
+// handing them over, then takes items by tickets: first 32 rows of h of an expert (32 rows
+// of gate and 32 of up, the eight warps two row halves by four shares of K), then 16 rows of y
+// of all experts (the warps share the experts' codes evenly).  The second kind waits until
+// every item of the first kind is done: their tickets are lower, so they are in the hands of CTAs that
+// run, whatever else holds the GPU.  h passes through memory as two binary16 numbers
+// relative to a power of two per 32, 22 bits in all.  No sum's order depends on which
+// CTA takes what.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+#include <cstring>
+#include <type_traits>
+
+#include "fp4.cuh"
+#include "fp4.h"
+#include "internal.h"
+#include "ptc.h"
+#include "ptx.cuh"
+#include "s4.cuh"
+#include "s4.h"
+
+namespace ptc {
+namespace {
+
+constexpr int kMoeWarps = 8, kMoeThreads = 32 * kMoeWarps;
+constexpr int kMaxTokens = 64, kMaxExperts = 512, kMaxTopK = 32, kMaxPairs = 512;
+constexpr int kTile = 8;  // tokens of an expert per item
+
+__device__ uint32_t g_moe_error = 0;
+
+struct Experts {  // one of the two weight matrices
+    const uint8_t *codes;
+    int64_t pitch, expert;
+    const uint8_t *scales, *zeros;
+    int rows, row_bytes, groups, tiles;
+};
+
+struct MoeArgs {
+    const void *x, *router;
+    int64_t ldx, ldr;
+    int router_f32, xvec, rvec;
+    void *y;
+    int64_t ldy;
+    int *ids;        // NULL, or [tokens][top_k]
+    float *weights;  // NULL, or the same
+    int tokens, hidden, inner, experts, top_k, renormalize;
+    int bf16_scales, per_group;
+    Experts gate_up, down;
+    int stages, h_stages, h_blocks;  // stages of hidden and inner, blocks of 32 of inner
+    int stage_bytes;                 // of a warp's ring
+    // Workspace.
+    uint32_t *counters;   // tickets, items of the first kind that are done
+    float *logits;        // [tokens][experts]
+    uint8_t *xs;          // [token][stage] operands
+    float2 *xps;          // [token][block] factors and sums
+    uint8_t *hs;          // [pair][stage] operands, high parts and low parts
+    float2 *hps;          // [pair][block of 32]
+    int stall;            // test hook: this item is never done (-1: none)
+    uint64_t wait_limit;
+};
+
+// ------------------------------------------------------------ router
+// A CTA per expert: its logits of all tokens, eight tokens at a time, every thread eight
+// columns of each 2048; after them CTAs that make the tokens' operands.
+template <typename X, int UNIT>
+__global__ void __launch_bounds__(kMoeThreads) router_kernel(const MoeArgs a) {
+    __shared__ float part[kMoeWarps][kTile];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (int(blockIdx.x) >= a.experts) {
+        const int first = int(blockIdx.x) - a.experts, ctas = int(gridDim.x) - a.experts;
+        if (first == 0 && threadIdx.x < 2) a.counters[threadIdx.x] = 0;
+        constexpr int LANES = 4 * UNIT, PER = 32 / LANES, GROUPS = 4 / UNIT;
+        const int blocks = a.stages * GROUPS, rounds = (blocks + PER - 1) / PER, lane8 = lane % LANES;
+        for (int u = first * kMoeWarps + warp; u < rounds * a.tokens; u += ctas * kMoeWarps) {
+            const int tok = u / rounds, blk = (u - tok * rounds) * PER + lane / LANES;
+            const int k = blk * (32 * UNIT) + lane8 * 8, have = max(0, min(8, a.hidden - k));
+            const X *p = static_cast<const X *>(a.x) + (have > 0 ? int64_t(tok) * a.ldx + k : 0);
+            float2 ps;
+            const uint4 op = s4_operands<UNIT, X>(load8(p, have, a.xvec != 0).v[0], ps);
+            if (blk >= blocks) continue;
+            const int st = blk / GROUPS, g = blk % GROUPS;
+            *reinterpret_cast<uint4 *>(a.xs + (int64_t(tok) * a.stages + st) * kS4XBytes + s4_x_piece<UNIT>(0, g * LANES + lane8)) = op;
+            if (lane8 == 0) a.xps[int64_t(tok) * blocks + blk] = ps;
+        }
+        return;
+    }
+    const int e = int(blockIdx.x);
+    for (int t0 = 0; t0 < a.tokens; t0 += kTile) {
+        const int n = min(kTile, a.tokens - t0);
+        float acc[kTile];
+#pragma unroll
+        for (int j = 0; j < kTile; ++j) acc[j] = 0.0f;
+        for (int k = int(threadIdx.x) * 8; k < a.hidden; k += kMoeThreads * 8) {
+            const int have = min(8, a.hidden - k);
+            float w[8];
+            if (a.router_f32) {
+                const Pack8<float> r = load8(static_cast<const float *>(a.router) + int64_t(e) * a.ldr + k, have, a.rvec != 0);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = r.get(i);
+            } else {
+                const Pack8<X> r = load8(static_cast<const X *>(a.router) + int64_t(e) * a.ldr + k, have, a.rvec != 0);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = to_float(r.get(i));
+            }
+#pragma unroll
+            for (int j = 0; j < kTile; ++j) {
+                if (j < n) {
+                    const Pack8<X> v = load8(static_cast<const X *>(a.x) + int64_t(t0 + j) * a.ldx + k, have, a.xvec != 0);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[j] = __fmaf_rn(to_float(v.get(i)), w[i], acc[j]);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kTile; ++j) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], o);
+            if (lane == 0) part[warp][j] = acc[j];
+        }
+        __syncthreads();
+        if (int(threadIdx.x) < n) {
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kMoeWarps; ++w) v += part[w][threadIdx.x];
+            a.logits[int64_t(t0 + threadIdx.x) * a.experts + e] = v;
+        }
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------ routing
+// What every CTA finds from the logits.  A pair is a token and one of its experts; pairs
+// lie by expert, then by token, and each expert's in tiles of up to eight.
+struct Routing {
+    uint32_t mask[kMaxExperts][2];   // tokens of an expert
+    uint16_t first[kMaxExperts];     // its first pair
+    uint16_t id[kMaxPairs];          // [token][slot]
+    float slot_weight[kMaxPairs];
+    uint8_t pair_token[kMaxPairs];
+    float pair_weight[kMaxPairs];
+    uint16_t tile_expert[kMaxPairs], tile_first[kMaxPairs];
+    uint8_t tile_count[kMaxPairs];
+    int tiles;
+    uint32_t ticket[2];
+    int abort;
+};
+
+// Order of logits as integers: NaN below every number, 0 for what is taken already.
+__device__ __forceinline__ uint32_t logit_key(float v) {
+    const uint32_t u = __float_as_uint(v);
+    if ((u & 0x7FFFFFFFu) > kInfBits) return 1u;
+    return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ void route(const MoeArgs &a, Routing &r) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    for (int i = threadIdx.x; i < a.experts; i += kMoeThreads) r.mask[i][0] = r.mask[i][1] = 0;
+    __syncthreads();
+    constexpr int PER = kMaxExperts / 32;
+    for (int tok = warp; tok < a.tokens; tok += kMoeWarps) {
+        const float *l = a.logits + int64_t(tok) * a.experts;
+        float v[PER];
+        uint32_t key[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = lane + 32 * i;
+            v[i] = e < a.experts ? __ldcg(l + e) : 0.0f;
+            key[i] = e < a.experts ? logit_key(v[i]) : 0u;
+        }
+        float largest = 0.0f, mine = 0.0f;  // of the logits; this lane's slot's
+        int my_id = 0;
+        for (int j = 0; j < a.top_k; ++j) {
+            uint32_t k = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) k = max(k, key[i]);
+            const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, k);
+            int at = kMaxExperts;
+#pragma unroll
+            for (int i = PER - 1; i >= 0; --i)
+                if (key[i] == best) at = lane + 32 * i;
+            const int e = __reduce_min_sync(0xFFFFFFFFu, at);
+            float value = 0.0f;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (lane + 32 * i == e) {
+                    key[i] = 0u;
+                    value = v[i];
+                }
+            value = __shfl_sync(0xFFFFFFFFu, value, e & 31);
+            if (j == 0) largest = value;
+            if (lane == j) {
+                mine = value;
+                my_id = e;
+            }
+        }
+        float sum = 0.0f;
+        const float p = lane < a.top_k ? expf(mine - largest) : 0.0f;
+        if (a.renormalize) {
+            sum = p;
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (lane + 32 * i < a.experts) sum += expf(v[i] - largest);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (lane < a.top_k) {
+            const int s = tok * a.top_k + lane;
+            const float w = __fdiv_rn(p, sum);
+            r.id[s] = uint16_t(my_id);
+            r.slot_weight[s] = w;
+            atomicOr(&r.mask[my_id][tok >> 5], 1u << (tok & 31));
+            if (blockIdx.x == 0) {
+                if (a.ids) a.ids[s] = my_id;
+                if (a.weights) a.weights[s] = w;
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {  // pairs and tiles of the experts, in order
+        int pairs = 0, tiles = 0;
+        for (int e0 = 0; e0 < a.experts; e0 += 32) {
+            const int e = e0 + lane;
+            const int c = e < a.experts ? __popc(r.mask[e][0]) + __popc(r.mask[e][1]) : 0, t = (c + kTile - 1) / kTile;
+            int sum = c | t << 16;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const int up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+                if (lane >= o) sum += up;
+            }
+            const int p0 = pairs + (sum & 0xFFFF) - c, t0 = tiles + (sum >> 16) - t;
+            if (e < a.experts) r.first[e] = uint16_t(p0);
+            for (int i = 0; i < t; ++i) {
+                r.tile_expert[t0 + i] = uint16_t(e);
+                r.tile_first[t0 + i] = uint16_t(p0 + kTile * i);
+                r.tile_count[t0 + i] = uint8_t(min(kTile, c - kTile * i));
+            }
+            const int total = __shfl_sync(0xFFFFFFFFu, sum, 31);
+            pairs += total & 0xFFFF;
+            tiles += total >> 16;
+        }
+        if (lane == 0) r.tiles = tiles;
+    }
+    __syncthreads();
+    for (int s = threadIdx.x; s < a.tokens * a.top_k; s += kMoeThreads) {
+        const int tok = s / a.top_k, e = r.id[s];
+        const uint32_t lo = r.mask[e][0], hi = r.mask[e][1];
+        const int rank = tok < 32 ? __popc(lo & ((1u << tok) - 1u)) : __popc(lo) + __popc(hi & ((1u << (tok - 32)) - 1u));
+        r.pair_token[r.first[e] + rank] = uint8_t(tok);
+        r.pair_weight[r.first[e] + rank] = r.slot_weight[s];
+    }
+    __syncthreads();
+}
+
+// Waits until `count` items of the first kind are done; false after the limit.
+__device__ __forceinline__ bool wait_done(const MoeArgs &a, uint32_t count) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t n = 1;; ++n) {
+        uint32_t v;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(a.counters + 1) : "memory");
+        if (v >= count) return true;
+        if ((n & 15u) == 0 && globaltimer_ns() - t0 > a.wait_limit) {
+            atomicCAS(&g_moe_error, 0u, kErrTimeout);
+            return false;
+        }
+        __nanosleep(64);
+    }
+}
+
+// ------------------------------------------------------------ experts
+template <typename X, int UNIT, bool ODD, int D>
+__global__ void __launch_bounds__(kMoeThreads, 2) experts_kernel(const MoeArgs a) {
+    constexpr int SG = 4 / UNIT;  // scale groups (and, of x, blocks) per stage
+    extern __shared__ __align__(256) uint8_t moe_smem[];
+    __shared__ Routing r;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int gr = lane >> 2, t = lane & 3, crow = gr, piece = t;
+    const uint32_t ring = uint32_t(warp * D * a.stage_bytes), ring_at = smem_u32(moe_smem) + ring;
+    float *const sums = reinterpret_cast<float *>(moe_smem + kMoeWarps * D * a.stage_bytes);
+    griddep_wait();
+    griddep_launch_dependents();
+    if (threadIdx.x == 0) {
+        r.ticket[0] = atomicAdd(a.counters, 1u);
+        r.abort = 0;
+    }
+    route(a, r);
+
+    const int first_items = r.tiles * a.h_blocks, items = first_items + (a.hidden + 15) / 16;
+    bool ready = false;  // every item of the first kind is done
+    for (int round = 0;; ++round) {
+        const int item = int(min(r.ticket[round & 1], 0x7FFFFFFFu));
+        if (item >= items) break;
+        if (threadIdx.x == 0) r.ticket[(round + 1) & 1] = atomicAdd(a.counters, 1u);
+        if (item < first_items) {
+            // ------------------------------------------------ rows of h
+            const int tile = item / a.h_blocks, ib = item - tile * a.h_blocks;
+            const int e = r.tile_expert[tile], pair0 = r.tile_first[tile], n = r.tile_count[tile];
+            const int half = warp & 1, share = warp >> 1, row0 = ib * 32 + half * 16;
+            const Experts &w = a.gate_up;
+            const uint32_t x_bytes = uint32_t(n) * kS4XBytes;
+            // Codes: MMA rows crow and crow + 8 of the gate's tile and of up's.
+            const uint8_t *src[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                src[j] = w.codes + int64_t(e) * w.expert +
+                         int64_t((j >> 1) * a.inner + min(row0 + s4_row(crow + 8 * (j & 1)), a.inner - 1)) * w.pitch + piece * 16;
+            // Scales: of each tile and group 32 bytes (ODD: of two tiles), then the zeros.
+            constexpr int PIECES = 2 * SG * (ODD ? 4 : 2);
+            const uint32_t codes_at = uint32_t(min(kTile, a.tokens)) * kS4XBytes, scales_at = codes_at + 2 * kS4TileBytes;
+            const uint32_t ps_at = scales_at + PIECES * 16 * (w.zeros ? 2 : 1);
+            const int64_t expert_scales = int64_t(e) * w.tiles * w.groups * 32;
+            auto issue = [&](int st, int slot) {
+                const uint32_t dst = ring_at + uint32_t(slot * a.stage_bytes);
+                for (int q = lane; q < n * 16; q += 32) {
+                    const int j = q >> 4, c = q & 15;
+                    copy16(dst + uint32_t(j) * kS4XBytes + (uint32_t(c ^ ((j & 1) << 2)) << 4),
+                           a.xs + (int64_t(r.pair_token[pair0 + j]) * a.stages + st) * kS4XBytes + c * 16, 16);
+                }
+                for (int q = lane; q < n * SG; q += 32) {
+                    const int j = q / SG, g = q % SG;
+                    copy8(dst + ps_at + uint32_t(g * kTile + j) * 8u,
+                          a.xps + (int64_t(r.pair_token[pair0 + j]) * a.stages + st) * SG + g, 8);
+                }
+                const int have = min(16, w.row_bytes - st * kS4RowBytes - piece * 16);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    copy16(dst + codes_at + (j >> 1) * kS4TileBytes + s4_piece<UNIT>(crow + 8 * (j & 1), piece),
+                           have > 0 ? src[j] + int64_t(st) * kS4RowBytes : w.codes, max(have, 0));
+                for (int q = lane; q < PIECES * (w.zeros ? 2 : 1); q += 32) {
+                    const int z = q >= PIECES, p = q - (z ? PIECES : 0);
+                    const int m = p / (PIECES / 2), g = p % (PIECES / 2) / (ODD ? 4 : 2), i = p % (ODD ? 4 : 2);
+                    const int tl = (m * a.inner + row0) / 16 + (i >> 1), group = SG == 1 ? st / a.per_group : st * SG + g;
+                    const bool in = tl < w.tiles && group < w.groups;
+                    copy16(dst + scales_at + uint32_t(q) * 16u,
+                           in ? (z ? w.zeros : w.scales) + expert_scales + (int64_t(tl) * w.groups + group) * 32 + (i & 1) * 16 : w.scales,
+                           in ? 16 : 0);
+                }
+            };
+            float tot[2][1][4];
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tot[m][0][i] = 0.0f;
+            const int mine = (a.stages - share + 3) / 4;  // stages share, share + 4, ...
+            for (int i = 0; i < D - 1; ++i) {
+                if (i < mine) issue(share + 4 * i, i);
+                copies_commit();
+            }
+            const int tok = min(gr, n - 1);
+            for (int i = 0; i < mine; ++i) {
+                copies_wait<D - 2>();
+                __syncwarp();
+                if (i + D - 1 < mine) issue(share + 4 * (i + D - 1), (i + D - 1) % D);
+                copies_commit();
+                const uint32_t at = ring + uint32_t((i % D) * a.stage_bytes);
+                const uint32_t x[1] = {at + uint32_t(tok) * kS4XBytes + uint32_t(t) * 16u + uint32_t(tok & 1) * 64u};
+                // (up's first row may lie anywhere in its tile)
+                const uint32_t scales[2] = {at + scales_at, at + scales_at + PIECES * 8 + (ODD ? uint32_t((a.inner + row0) % 16) * 2u : 0u)};
+                s4_stage<2, 1, UNIT, SG, 1, ODD>(tot, moe_smem, at + codes_at + s4_code_at<UNIT>(lane), scales,
+                                                 w.zeros ? PIECES * 16 : 0, a.bf16_scales != 0, x, x_bytes, at + ps_at, lane);
+            }
+            copies_wait<0>();
+            // Sums of the shares: [share][half][gate, up][row][token].
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                float *p = sums + ((warp * 2 + m) * 16 + 2 * gr) * kTile + 2 * t;
+                *reinterpret_cast<float2 *>(p) = make_float2(tot[m][0][0], tot[m][0][1]);
+                *reinterpret_cast<float2 *>(p + kTile) = make_float2(tot[m][0][2], tot[m][0][3]);
+            }
+            __syncthreads();
+            if (warp < n) {  // token `warp`, a lane a row
+                float gate = 0.0f, up = 0.0f;
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const float *p = sums + ((s * 2 + (lane >> 4)) * 2 * 16 + (lane & 15)) * kTile + warp;
+                    gate = __fadd_rn(gate, p[0]);
+                    up = __fadd_rn(up, p[16 * kTile]);
+                }
+                gate = __fmul_rn(gate, kS4Out);
+                up = __fmul_rn(up, kS4Out);
+                const float h = ib * 32 + lane < a.inner ? __fmul_rn(__fdiv_rn(gate, __fadd_rn(1.0f, expf(-gate))), up) : 0.0f;
+                __half hi, lo;
+                float2 ps;
+                s4_operand32(h, lane, hi, lo, ps);
+                const int64_t pair = pair0 + warp;
+                __half *p = reinterpret_cast<__half *>(a.hs + (pair * a.h_stages + ib / 4) * (2 * kS4XBytes)) + (ib & 3) * 32 +
+                            (lane >> 3) * 8 + s4_half(lane & 7);
+                p[0] = hi;
+                p[kS4XBytes / 2] = lo;
+                if (lane == 0) a.hps[pair * a.h_blocks + ib] = ps;
+            }
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0 && item != a.stall)
+                asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.counters + 1) : "memory");
+        } else {
+            // ------------------------------------------------ rows of y
+            if (!ready) {
+                if (threadIdx.x == 0 && !wait_done(a, uint32_t(first_items))) r.abort = 1;
+                __syncthreads();
+                if (r.abort) break;
+                ready = true;
+            }
+            const int row0 = (item - first_items) * 16;
+            const Experts &w = a.down;
+            const uint32_t most_x = uint32_t(min(kTile, a.tokens)) * kS4XBytes;
+            const uint32_t codes_at = 2 * most_x, scales_at = codes_at + kS4TileBytes;
+            constexpr int PIECES = SG * 2;
+            const uint32_t ps_at = scales_at + PIECES * 16 * (w.zeros ? 2 : 1);
+            for (int i = lane; i < a.tokens * 16; i += 32) sums[warp * (a.tokens * 16) + i] = 0.0f;
+            __syncwarp();
+            const int units = r.tiles * a.h_stages;
+            const int u0 = int(int64_t(units) * warp / kMoeWarps), u1 = int(int64_t(units) * (warp + 1) / kMoeWarps);
+            int64_t row_at[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) row_at[j] = int64_t(min(row0 + s4_row(crow + 8 * j), w.rows - 1)) * w.pitch + piece * 16;
+            // The next unit to bring: tile and stage.
+            int b_tile = u0 / a.h_stages, b_st = u0 - b_tile * a.h_stages, b_left = u1 - u0;
+            auto issue = [&](int slot) {
+                const uint32_t dst = ring_at + uint32_t(slot * a.stage_bytes);
+                const int e = r.tile_expert[b_tile], pair0 = r.tile_first[b_tile], n = r.tile_count[b_tile], st = b_st;
+                for (int q = lane; q < n * 32; q += 32) {
+                    const int j = q >> 5, lo = (q >> 4) & 1, c = q & 15;
+                    const bool in = st * 4 + (c >> 2) < a.h_blocks;
+                    copy16(dst + uint32_t(lo) * most_x + uint32_t(j) * kS4XBytes + (uint32_t(c ^ ((j & 1) << 2)) << 4),
+                           a.hs + (int64_t(pair0 + j) * a.h_stages + st) * (2 * kS4XBytes) + lo * kS4XBytes + c * 16, in ? 16 : 0);
+                }
+                if (lane < n * 4) {
+                    const int j = lane >> 2, g = lane & 3;
+                    const bool in = st * 4 + g < a.h_blocks;
+                    copy8(dst + ps_at + uint32_t(g * kTile + j) * 8u, a.hps + int64_t(pair0 + j) * a.h_blocks + (in ? st * 4 + g : 0),
+                          in ? 8 : 0);
+                }
+                const int have = min(16, w.row_bytes - st * kS4RowBytes - piece * 16);
+                const uint8_t *codes = w.codes + int64_t(e) * w.expert;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    copy16(dst + codes_at + s4_piece<1>(crow + 8 * j, piece),
+                           have > 0 ? codes + row_at[j] + int64_t(st) * kS4RowBytes : w.codes, max(have, 0));
+                if (lane < PIECES * (w.zeros ? 2 : 1)) {
+                    const int z = lane >= PIECES, p = lane - (z ? PIECES : 0), group = SG == 1 ? st / a.per_group : st * SG + (p >> 1);
+                    const bool in = group < w.groups;
+                    copy16(dst + scales_at + uint32_t(lane) * 16u,
+                           in ? (z ? w.zeros : w.scales) + ((int64_t(e) * w.tiles + row0 / 16) * w.groups + group) * 32 + (p & 1) * 16 : w.scales,
+                           in ? 16 : 0);
+                }
+                if (++b_st == a.h_stages) {
+                    b_st = 0;
+                    ++b_tile;
+                }
+                --b_left;
+            };
+            for (int i = 0; i < D - 1; ++i) {
+                if (b_left > 0) issue(i);
+                copies_commit();
+            }
+            float tot[1][1][4] = {{{0.0f, 0.0f, 0.0f, 0.0f}}};
+            int tile = u0 / a.h_stages, st = u0 - tile * a.h_stages;
+            for (int u = u0, i = 0; u < u1; ++u, ++i) {
+                copies_wait<D - 2>();
+                __syncwarp();
+                if (b_left > 0) issue((i + D - 1) % D);
+                copies_commit();
+                const int n = r.tile_count[tile], tok = min(gr, n - 1);
+                const uint32_t at = ring + uint32_t((i % D) * a.stage_bytes);
+                const uint32_t x[1] = {at + uint32_t(tok) * kS4XBytes + uint32_t(t) * 16u + uint32_t(tok & 1) * 64u};
+                const uint32_t scales[1] = {at + scales_at};
+                s4_stage<1, 1, 1, SG, 2, false>(tot, moe_smem, at + codes_at + s4_code_at<1>(lane), scales, w.zeros ? PIECES * 16 : 0,
+                                                a.bf16_scales != 0, x, most_x, at + ps_at, lane);
+                if (++st == a.h_stages || u + 1 == u1) {
+                    // The tile's sums to its tokens, this warp's.
+#pragma unroll
+                    for (int i2 = 0; i2 < 2; ++i2) {
+                        const int j = 2 * t + i2;
+                        if (j < n) {
+                            const int pair = r.tile_first[tile] + j;
+                            float *p = sums + warp * (a.tokens * 16) + r.pair_token[pair] * 16 + 2 * gr;
+                            const float pw = r.pair_weight[pair];
+                            p[0] = __fmaf_rn(pw, tot[0][0][i2], p[0]);
+                            p[1] = __fmaf_rn(pw, tot[0][0][2 + i2], p[1]);
+                        }
+                    }
+#pragma unroll
+                    for (int i2 = 0; i2 < 4; ++i2) tot[0][0][i2] = 0.0f;
+                    if (st == a.h_stages) {
+                        st = 0;
+                        ++tile;
+                    }
+                }
+            }
+            copies_wait<0>();
+            __syncthreads();
+            for (int o = threadIdx.x; o < a.tokens * 16; o += kMoeThreads) {
+                float v = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kMoeWarps; ++k) v = __fadd_rn(v, sums[k * (a.tokens * 16) + o]);
+                const int row = row0 + (o & 15);
+                if (row < a.hidden) static_cast<X *>(a.y)[int64_t(o >> 4) * a.ldy + row] = from_float<X>(__fmul_rn(v, kS4Out));
+            }
+        }
+        __syncthreads();  // the next ticket is there, and the sums are read
+    }
+}
+
+// ------------------------------------------------------------ host side
+constexpr int64_t kMaxSize = 1 << 20;  // of hidden and inner
+constexpr int64_t kMaxLdM = int64_t(1) << 36;
+constexpr int kMaxDevM = 64;
+
+int64_t up_to(int64_t v, int64_t n) { return (v + n - 1) / n * n; }
+bool lies_on(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+struct MoeSpace {
+    int64_t logits, xs, xps, hs, hps, bytes;
+};
+
+MoeSpace moe_space(int64_t tokens, int64_t hidden, int64_t inner, int64_t experts, int64_t top_k) {
+    const int64_t stages = (hidden + 127) / 128, h_stages = (inner + 127) / 128, pairs = tokens * top_k;
+    MoeSpace s;
+    s.logits = 256;
+    s.xs = s.logits + up_to(tokens * experts * 4, 256);
+    s.xps = s.xs + tokens * stages * kS4XBytes;
+    s.hs = s.xps + up_to(tokens * stages * 4 * 8, 256);
+    s.hps = s.hs + pairs * h_stages * 2 * kS4XBytes;
+    s.bytes = s.hps + up_to(pairs * ((inner + 31) / 32) * 8, 256);
+    return s;
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_moe(void (*fn)(P...), int64_t blocks, size_t smem, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[1];
+    std::memset(&cfg, 0, sizeof(cfg));
+    std::memset(attr, 0, sizeof(attr));
+    cfg.gridDim = dim3(unsigned(blocks), 1, 1);
+    cfg.blockDim = dim3(kMoeThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    if (pdl_enabled()) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.numAttrs = 1;
+    }
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
+    if (e == cudaSuccess) note_launches(1);
+    return e;
+}
+
+template <typename X, int UNIT, bool ODD, int D>
+int launch_experts(MoeArgs a, int sms, cudaStream_t s) {
+    constexpr int SG = 4 / UNIT;
+    auto *fn = experts_kernel<X, UNIT, ODD, D>;
+    const int most = std::min(a.tokens, kTile);
+    const int one = most * kS4XBytes + 2 * kS4TileBytes + 2 * SG * (ODD ? 4 : 2) * 16 * (a.gate_up.zeros ? 2 : 1) + SG * kTile * 8;
+    const int two = 2 * most * kS4XBytes + kS4TileBytes + SG * 2 * 16 * (a.down.zeros ? 2 : 1) + 4 * kTile * 8;
+    a.stage_bytes = int(up_to(std::max(one, two), 256));
+    const size_t smem = size_t(kMoeWarps) * D * a.stage_bytes + std::max<size_t>(kMoeWarps * 32 * kTile * 4, size_t(kMoeWarps) * a.tokens * 16 * 4);
+    static std::atomic<int> ready[kMaxDevM];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return fail_launch(e, "cudaGetDevice");
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 212 * 1024);
+        if (e != cudaSuccess) return fail_launch(e, "experts set-up");
+        ready[dev].store(1, std::memory_order_release);
+    }
+    const int64_t waves = up_to(int64_t(a.tokens) * a.stages * SG, kMoeWarps * (32 / (4 * UNIT))) / (kMoeWarps * (32 / (4 * UNIT)));
+    e = launch_moe(router_kernel<X, UNIT>, a.experts + std::min<int64_t>(std::max<int64_t>(waves, 1), sms), 0, s, a);
+    if (e == cudaSuccess) {
+        const int per_sm = smem + sizeof(Routing) + 1024 <= 114 * 1024 ? 2 : 1;
+        e = launch_moe(fn, int64_t(sms) * per_sm, smem, s, a);
+    }
+    return e == cudaSuccess ? PTC_OK : fail_launch(e, "experts launch");
+}
+
+template <typename X>
+int run_moe(const MoeArgs &a, int64_t group, int sms, cudaStream_t s) {
+    auto unit = [&](auto u) {
+        constexpr int U = decltype(u)::value;
+        const bool odd = a.inner % 16 != 0;
+        if (a.tokens <= 2) return odd ? launch_experts<X, U, true, 4>(a, sms, s) : launch_experts<X, U, false, 4>(a, sms, s);
+        return odd ? launch_experts<X, U, true, 3>(a, sms, s) : launch_experts<X, U, false, 3>(a, sms, s);
+    };
+    switch (s4_unit(group)) {
+        case 1: return unit(std::integral_constant<int, 1>());
+        case 2: return unit(std::integral_constant<int, 2>());
+        default: return unit(std::integral_constant<int, 4>());
+    }
+}
+
+Experts experts_of(const S4Weights &w) {
+    Experts e;
+    e.codes = static_cast<const uint8_t *>(w.codes);
+    e.pitch = w.pitch;
+    e.expert = w.expert;
+    e.scales = static_cast<const uint8_t *>(w.scales);
+    e.zeros = static_cast<const uint8_t *>(w.zeros);
+    e.rows = int(w.rows);
+    e.row_bytes = int((w.cols + 1) / 2);
+    e.groups = int(w.groups());
+    e.tiles = int(w.tiles());
+    return e;
+}
+
+}  // namespace
+
+cudaError_t read_and_clear_moe_error_word(uint32_t *out) {
+    uint32_t v = 0;
+    const uint32_t zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_moe_error, sizeof(v));
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_moe_error, &zero, sizeof(zero));
+    *out = v;
+    return e;
+}
+
+}  // namespace ptc
+
+using namespace ptc;
+
+extern "C" {
+
+int64_t ptc_moe_a16_s4_workspace(int64_t tokens, int64_t hidden, int64_t inner, int64_t experts, int64_t top_k) {
+    if (tokens <= 0 || hidden <= 0 || inner <= 0 || experts <= 0 || top_k <= 0 || tokens > kMaxTokens || hidden > kMaxSize ||
+        inner > kMaxSize || experts > kMaxExperts || top_k > std::min<int64_t>(experts, kMaxTopK) || tokens * top_k > kMaxPairs)
+        return 0;
+    return moe_space(tokens, hidden, inner, experts, top_k).bytes;
+}
+
+int ptc_moe_a16_s4(int64_t tokens, int64_t hidden, int64_t inner, int64_t experts, int64_t top_k, int renormalize, int type,
+                   const void *X, int64_t ldx, const void *router, int64_t ldr, int router_type, int64_t group, int scale_type,
+                   const void *gate_up, int64_t ld_gate_up, int64_t expert_gate_up, const void *gate_up_scales,
+                   const void *gate_up_zeros, const void *down, int64_t ld_down, int64_t expert_down, const void *down_scales,
+                   const void *down_zeros, void *Y, int64_t ldy, int32_t *ids, float *weights, void *workspace,
+                   int64_t workspace_bytes, void *stream) {
+    set_message("");
+    if (tokens < 0 || tokens > kMaxTokens || hidden < 1 || hidden > kMaxSize || inner < 1 || inner > kMaxSize || experts < 1 ||
+        experts > kMaxExperts)
+        return fail_status(PTC_ERR_INVALID, "sizes must satisfy 0 <= tokens <= 64, 1 <= hidden, inner <= 2^20, 1 <= experts <= 512");
+    if (top_k < 1 || top_k > experts || top_k > kMaxTopK || tokens * top_k > kMaxPairs)
+        return fail_status(PTC_ERR_INVALID, "top_k must be 1 .. min(experts, 32), and tokens * top_k at most 512");
+    if (type != PTC_OUT_BF16 && type != PTC_OUT_F16)
+        return fail_status(PTC_ERR_INVALID, "activations are PTC_OUT_BF16 or PTC_OUT_F16");
+    if (router_type != type && router_type != PTC_OUT_F32)
+        return fail_status(PTC_ERR_INVALID, "the router is of the activations' type or float32");
+    if (scale_type != PTC_OUT_BF16 && scale_type != PTC_OUT_F16)
+        return fail_status(PTC_ERR_INVALID, "scales are PTC_OUT_BF16 or PTC_OUT_F16");
+    if (tokens == 0) return PTC_OK;
+    if (!X || ldx < hidden || ldx > kMaxLdM || !Y || ldy < hidden || ldy > kMaxLdM || !router || ldr < hidden || ldr > kMaxLdM)
+        return fail_status(PTC_ERR_INVALID, "X, Y or router is NULL, or its leading dimension is not hidden .. 2^36");
+    const S4Weights gu{gate_up, ld_gate_up, expert_gate_up, gate_up_scales, gate_up_zeros, 2 * inner, hidden, group, experts};
+    const S4Weights dn{down, ld_down, expert_down, down_scales, down_zeros, hidden, inner, group, experts};
+    int rc = check_s4(gu);
+    if (!rc) rc = check_s4(dn);
+    if (rc) return rc;
+    for (const S4Weights *w : {&gu, &dn})
+        if (experts > 1 && (w->expert < (w->rows - 1) * w->pitch + (w->cols + 1) / 2 || w->expert > kMaxLdM))
+            return fail_status(PTC_ERR_INVALID, "experts' matrices overlap, or lie over 2^36 bytes apart");
+    const int64_t need = ptc_moe_a16_s4_workspace(tokens, hidden, inner, experts, top_k);
+    if (!workspace || workspace_bytes < need) return fail_status(PTC_ERR_INVALID, "the workspace is too small");
+    const int rs = router_type == PTC_OUT_F32 ? 4 : 2;
+    if (!lies_on(X, 2) || !lies_on(Y, 2) || !lies_on(router, uintptr_t(rs)) || !lies_on(ids, 4) || !lies_on(weights, 4))
+        return fail_status(PTC_ERR_ALIGN, "X, Y, router, ids and weights must be aligned to their elements");
+    if (!lies_on(workspace, 256)) return fail_status(PTC_ERR_ALIGN, "the workspace must be 256-byte aligned");
+    auto span = [&](const S4Weights &w) {
+        return flat_bytes(w.codes, uint64_t(w.experts > 1 ? w.experts - 1 : 0) * uint64_t(w.expert) + uint64_t(w.rows - 1) * uint64_t(w.pitch) +
+                                       uint64_t((w.cols + 1) / 2));
+    };
+    const ByteRows in[] = {elem_rows(X, tokens, hidden, ldx, 2), elem_rows(router, experts, hidden, ldr, rs), span(gu),
+                           flat_bytes(gu.scales, gu.scale_bytes()), flat_bytes(gu.zeros, gu.scale_bytes()), span(dn),
+                           flat_bytes(dn.scales, dn.scale_bytes()), flat_bytes(dn.zeros, dn.scale_bytes())};
+    const ByteRows out[] = {elem_rows(Y, tokens, hidden, ldy, 2), flat_bytes(ids, uint64_t(tokens * top_k) * 4),
+                            flat_bytes(weights, uint64_t(tokens * top_k) * 4), flat_bytes(workspace, uint64_t(need))};
+    for (int i = 0; i < 4; ++i) {
+        for (const ByteRows &b : in)
+            if (rows_overlap(out[i], b)) return fail_status(PTC_ERR_OVERLAP, "an output overlaps another argument");
+        for (int j = 0; j < i; ++j)
+            if (rows_overlap(out[i], out[j])) return fail_status(PTC_ERR_OVERLAP, "an output overlaps another argument");
+    }
+    int sms;
+    if ((rc = usable_device(&sms))) return rc;
+    const MoeSpace at = moe_space(tokens, hidden, inner, experts, top_k);
+    char *ws = static_cast<char *>(workspace);
+    MoeArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = X;
+    a.ldx = ldx;
+    a.router = router;
+    a.ldr = ldr;
+    a.router_f32 = router_type == PTC_OUT_F32;
+    a.xvec = lies_on(X, 16) && (tokens == 1 || ldx % 8 == 0);
+    a.rvec = lies_on(router, 16) && (experts == 1 || ldr * rs % 16 == 0);
+    a.y = Y;
+    a.ldy = ldy;
+    a.ids = ids;
+    a.weights = weights;
+    a.tokens = int(tokens);
+    a.hidden = int(hidden);
+    a.inner = int(inner);
+    a.experts = int(experts);
+    a.top_k = int(top_k);
+    a.renormalize = renormalize != 0;
+    a.bf16_scales = scale_type == PTC_OUT_BF16;
+    a.per_group = int(group >= 128 ? group / 128 : 1);
+    a.gate_up = experts_of(gu);
+    a.down = experts_of(dn);
+    a.stages = int((hidden + 127) / 128);
+    a.h_stages = int((inner + 127) / 128);
+    a.h_blocks = int((inner + 31) / 32);
+    a.counters = reinterpret_cast<uint32_t *>(ws);
+    a.logits = reinterpret_cast<float *>(ws + at.logits);
+    a.xs = reinterpret_cast<uint8_t *>(ws + at.xs);
+    a.xps = reinterpret_cast<float2 *>(ws + at.xps);
+    a.hs = reinterpret_cast<uint8_t *>(ws + at.hs);
+    a.hps = reinterpret_cast<float2 *>(ws + at.hps);
+    a.stall = take_stall_tile();
+    a.wait_limit = wait_limit_ns();
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return type == PTC_OUT_BF16 ? run_moe<__nv_bfloat16>(a, group, sms, s) : run_moe<__half>(a, group, sms, s);
+}
+
+}  // extern "C"

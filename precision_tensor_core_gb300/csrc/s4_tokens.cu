@@ -190,8 +190,11 @@ __global__ void __launch_bounds__(kThreads4, MT == 1 ? 3 : 2) s4_kernel(const S4
             uint32_t x[NT];
 #pragma unroll
             for (int n = 0; n < NT; ++n) x[n] = buf + tok_at[n] + local * kS4XBytes;
-            s4_stage<MT, NT, UNIT, 1>(tot, smem4, code_at + slot, scale_at + slot, zeros, a.bf16_scales != 0, x, 0u,
-                                      buf + ps_at + local * (GROUPS * TOK * 8), lane);
+            uint32_t scales[MT];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) scales[m] = scale_at + slot + uint32_t(m * GROUPS) * 32u;
+            s4_stage<MT, NT, UNIT, GROUPS, 1, false>(tot, smem4, code_at + slot, scales, zeros, a.bf16_scales != 0, x, 0u,
+                                                     buf + ps_at + local * (GROUPS * TOK * 8), lane);
         }
     }
     copies_wait<0>();

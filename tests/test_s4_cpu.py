@@ -66,3 +66,37 @@ def test_keys(L):
         assert [L.ptc_set_tuning(key, v) for v in (1, 2, 4, 8, 0)] == [0] * 5
         assert L.ptc_set_tuning(key, 3) == INVALID and L.ptc_set_tuning(key, -1) == INVALID
     assert [L.ptc_set_tuning(b"s4_tokens_tiles", v) for v in (1, 2, 0, 3)] == [0, 0, 0, INVALID]
+
+
+def moe(L, tokens=4, hidden=200, inner=100, experts=5, top_k=2, type=1, X=BASE, ldx=200, router=BASE + GB, ldr=200, rt=1, group=64,
+        st=1, gu=BASE + 2 * GB, ldg=112, eg=200 * 112, gs=BASE + 3 * GB, gz=None, dn=BASE + 4 * GB, ldd=64, ed=200 * 64,
+        ds=BASE + 5 * GB, dz=None, Y=BASE + 6 * GB, ldy=200, ids=None, weights=None, ws=BASE + 7 * GB, bytes=None):
+    if bytes is None:
+        bytes = L.ptc_moe_a16_s4_workspace(tokens, hidden, inner, experts, top_k)
+    return L.ptc_moe_a16_s4(tokens, hidden, inner, experts, top_k, 1, type, X, ldx, router, ldr, rt, group, st, gu, ldg, eg, gs, gz,
+                            dn, ldd, ed, ds, dz, Y, ldy, ids, weights, ws, bytes, None)
+
+
+@no_gpu
+@pytest.mark.parametrize("change, status", [
+    (dict(), DEVICE), (dict(tokens=0, X=None), 0), (dict(tokens=65), INVALID), (dict(tokens=-1), INVALID), (dict(hidden=0), INVALID),
+    (dict(inner=0), INVALID), (dict(experts=513), INVALID), (dict(top_k=0), INVALID), (dict(top_k=6), INVALID),
+    (dict(experts=64, top_k=33), INVALID), (dict(tokens=64, experts=64, top_k=9), INVALID), (dict(tokens=64, experts=64, top_k=8), DEVICE),
+    (dict(type=0), INVALID), (dict(rt=2), INVALID), (dict(rt=0), DEVICE), (dict(st=0), INVALID), (dict(st=2), DEVICE),
+    (dict(group=48), INVALID), (dict(ldx=199), INVALID), (dict(ldy=199), INVALID), (dict(ldr=199), INVALID), (dict(ldg=96), INVALID),
+    (dict(ldd=48), INVALID), (dict(eg=200 * 112 - 16), INVALID), (dict(ed=16), INVALID), (dict(ed=200 * 64 + 8), ALIGN),
+    (dict(gu=None), INVALID), (dict(ds=None), INVALID), (dict(gu=BASE + 2 * GB + 8), ALIGN), (dict(dz=BASE + 8 * GB + 2), ALIGN),
+    (dict(X=BASE + 1), ALIGN), (dict(ids=BASE + 8 * GB + 2), ALIGN), (dict(ids=BASE + 8 * GB, weights=BASE + 9 * GB), DEVICE),
+    (dict(ws=None), INVALID), (dict(ws=BASE + 7 * GB + 128), ALIGN), (dict(bytes=1000), INVALID), (dict(Y=BASE), OVERLAP),
+    (dict(Y=BASE + 4 * GB + 64), OVERLAP), (dict(weights=BASE + 7 * GB), OVERLAP), (dict(ids=BASE + 8 * GB, weights=BASE + 8 * GB), OVERLAP),
+    (dict(Y=BASE + 2 * GB + 5 * 200 * 112 - 16), OVERLAP), (dict(ws=BASE + 5 * GB), OVERLAP),
+])
+def test_moe_statuses(L, change, status):
+    assert moe(L, **change) == status
+
+
+def test_moe_workspace():
+    f = ptc.ptc_moe_a16_s4_workspace
+    assert f(0, 1, 1, 1, 1) == f(65, 1, 1, 1, 1) == f(1, 0, 1, 1, 1) == f(1, 1, 1, 1, 2) == f(64, 1, 1, 64, 9) == 0
+    # counters, logits, operands of x and their factors, of h and theirs
+    assert f(3, 300, 200, 10, 2) == 256 + 256 + 3 * 3 * 256 + 512 + 6 * 2 * 512 + 512
