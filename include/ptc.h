@@ -753,8 +753,7 @@ int ptc_last_conversion(int *mode);
  *                  size, 1, 2, 4 or 8.  A pair of these that the sizes do not allow
  *                  (each share has at least 256 of K, and a share's activations fit
  *                  their buffer) is not taken.
- *   "s4_tokens_rows", "s4_tokens_split" the same of gemm_a16_s4, whose shares of K take
- *                  at least 128.
+ *   "s4_tokens_rows", "s4_tokens_split" the same of gemm_a16_s4.
  *   "s4_tokens_tiles" gemm_a16_s4's tiles of 16 rows per row group: 0 (default) by size,
  *                  1 or 2.
  * No accepted value of any key changes an INT8 or INT4 result. */

@@ -459,6 +459,23 @@ int encode_tmap_scales(CUtensorMap *map, const void *base, uint64_t ktiles, uint
     }
     return PTC_OK;
 }
+int encode_tmap_codes(CUtensorMap *map, const void *base, uint64_t row_bytes, uint64_t rows, uint64_t experts, uint64_t pitch,
+                      uint64_t expert, uint32_t box_rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return fail(PTC_ERR_LAUNCH, "cuTensorMapEncodeTiled unavailable");
+    cuuint64_t dims[3] = {row_bytes, rows, experts};
+    cuuint64_t strides[2] = {pitch, expert};
+    cuuint32_t box[3] = {128, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        std::snprintf(g_msg, sizeof(g_msg), "cuTensorMapEncodeTiled failed (CUresult %d)", int(r));
+        return PTC_ERR_LAUNCH;
+    }
+    return PTC_OK;
+}
 int fail_status(int code, const char *text) { return fail(code, text); }
 int fail_launch(cudaError_t e, const char *what) { return fail_cuda(e, what); }
 int usable_device(int *sms) {
@@ -1112,12 +1129,13 @@ int gemm_poll_device_error(void) {
     uint32_t w = 0;
     cudaError_t e = ptc::read_and_clear_error_word(&w);
     if (e != cudaSuccess) return fail_cuda(e, "reading the device error word");
-    uint32_t w4 = 0, wt = 0, wm = 0;
+    uint32_t w4 = 0, wt = 0, ws = 0, wm = 0;
     e = ptc::read_and_clear_fp4_error_word(&w4);
     if (e == cudaSuccess) e = ptc::read_and_clear_tokens_error_word(&wt);
+    if (e == cudaSuccess) e = ptc::read_and_clear_s4_error_word(&ws);
     if (e == cudaSuccess) e = ptc::read_and_clear_moe_error_word(&wm);
     if (e != cudaSuccess) return fail_cuda(e, "reading the device error word");
-    return (w | w4 | wt | wm) ? PTC_ERR_TIMEOUT : PTC_OK;
+    return (w | w4 | wt | ws | wm) ? PTC_ERR_TIMEOUT : PTC_OK;
 }
 
 uint64_t ptc_kernel_launch_count(void) { return g_launches.load(); }

@@ -22,6 +22,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <type_traits>
@@ -31,10 +32,11 @@
 
 namespace ptc {
 
-constexpr int kS4Stage = 128;        // codes of a row per stage
-constexpr int kS4RowBytes = 64;      // their bytes
-constexpr int kS4TileBytes = 1024;   // of 16 rows
-constexpr int kS4XBytes = 256;       // a token's activations of a stage
+constexpr int kS4Half = 128;         // codes of a row that one call of s4_half multiplies
+constexpr int kS4Stage = 256;        // codes of a row per stage of a ring
+constexpr int kS4RowBytes = 128;     // their bytes
+constexpr int kS4TileBytes = 2048;   // of 16 rows
+constexpr int kS4XBytes = 256;       // a token's activations of half a stage
 constexpr float kS4Out = 0x1p12f;    // the output's factor
 
 // Codes per block of activations, in units of 32, for a group size; groups per stage.
@@ -116,39 +118,46 @@ __device__ __forceinline__ void s4_operand32(float v, int lane, __half &hi, __ha
 __device__ __forceinline__ int s4_half(int e) { return ((e & 1) << 2) | (e & 2) | (e >> 2); }
 
 // ------------------------------------------------------------ copies
-// 16 (8) bytes to shared memory, `n` of them from global memory and zeros after them.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int n) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void copy8(uint32_t dst, const void *src, int n) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LEFT>
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+// `bytes` (a multiple of 16) from 16-byte aligned global to shared memory, signalled on `bar`.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
 }
 
-// In a stage the lanes of a quad take the words of a row's four 16-byte pieces in one of
-// two ways.  With UNIT 4, where the whole stage is one block, lane t takes piece t by one
-// load, and the i-th pair of MMAs multiplies its word i: codes 32 t + 8 i .. + 7.
+// Box of a 3-D tensor: bytes of a row, rows, experts.
+__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// A stage's rows of 128 bytes lie in the 128-byte swizzle: 16-byte piece c of row r at
+// c ^ (r & 7), on 1024 bytes.  In half a stage (four pieces) the lanes of a quad take the
+// words in one of two ways.  With UNIT 4, where all of it is one block, lane t takes piece
+// t by one load, and the i-th pair of MMAs multiplies its word i: codes 32 t + 8 i .. + 7.
 // Otherwise lane t takes word t of each piece, and the i-th pair multiplies block i.
+//
+// MMA rows gr and gr + 8 are the tile's rows 2 f and 2 f + 1, whose scales one load takes;
+// f is such that rows whose pieces are read together differ in the swizzle's top bit.
+__device__ __forceinline__ int s4_pair_of(int gr) { return ((gr & 1) << 1) | ((gr >> 1) & 1) | (gr & 4); }
 
-// Where 16-byte piece c (0 .. 3) of MMA row i of a tile of 16 rows lies: rows that are read
-// together differ in their banks.  MMA rows i and i + 8 are the tile's rows 2 i and 2 i + 1,
-// whose scales one load takes.
+// This lane's piece (UNIT 4) or word (of piece 0) of row 2 f in the first half of a stage's
+// codes; the second half is 64 further by exclusive or, row 2 f + 1 at s4_next_row.
 template <int UNIT>
-__device__ __forceinline__ uint32_t s4_piece(int i, int c) {
-    return uint32_t(i) * kS4RowBytes + (uint32_t(UNIT == 4 ? c : c ^ ((i >> 1) & 3)) << 4);
+__device__ __forceinline__ uint32_t s4_code_at(int lane) {
+    const int r = 2 * s4_pair_of(lane >> 2), t = lane & 3;
+    return uint32_t(r) * kS4RowBytes + (UNIT == 4 ? uint32_t(t ^ (r & 7)) << 4 : uint32_t(r & 7) << 4 | uint32_t(t) << 2);
 }
-__device__ __forceinline__ int s4_row(int i) { return 2 * (i & 7) + (i >> 3); }
+__device__ __forceinline__ uint32_t s4_next_row(uint32_t at) { return (at ^ 16u) + kS4RowBytes; }
 
-// Where the operands of activations 8 c .. 8 c + 7 of token j's stage lie, from the
-// token's start: 64 bytes for each pair of MMAs, odd tokens in the other order.
+// Where the operands of activations 8 c .. 8 c + 7 of half a stage lie: 64 bytes for each
+// pair of MMAs, 16 for each lane of a quad.
 template <int UNIT>
-__device__ __forceinline__ uint32_t s4_x_piece(int j, int c) {
-    const int at = UNIT == 4 ? (c & 3) * 4 + (c >> 2) : c;
-    return uint32_t(at ^ ((j & 1) << 2)) << 4;
+__device__ __forceinline__ uint32_t s4_x_piece(int c) {
+    return uint32_t(UNIT == 4 ? (c & 3) * 4 + (c >> 2) : c) << 4;
 }
 
 // ------------------------------------------------------------ products
@@ -176,42 +185,42 @@ __device__ __forceinline__ void s4_codes(uint32_t w, uint32_t (&a)[4]) {
     a[3] = and_xor(w8, 0x00F000F0u, 0x00800080u);
 }
 
-// The scales (zeros) of rows 2 gr and 2 gr + 1 of a tile, `p` those of its 16 rows; ODD:
-// these start at any row of two tiles, 2 bytes aligned.
+// The scales (zeros) of two rows that lie side by side at p, or (ODD) at p and `second` on.
 template <bool ODD>
-__device__ __forceinline__ float2 s4_row_scales(const uint8_t *p, int gr, bool bf16) {
+__device__ __forceinline__ float2 s4_row_scales(const uint8_t *p, uint32_t second, bool bf16) {
     uint32_t u;
     if constexpr (ODD)
-        u = uint32_t(*reinterpret_cast<const uint16_t *>(p + gr * 4)) | uint32_t(*reinterpret_cast<const uint16_t *>(p + gr * 4 + 2)) << 16;
+        u = uint32_t(*reinterpret_cast<const uint16_t *>(p)) | uint32_t(*reinterpret_cast<const uint16_t *>(p + second)) << 16;
     else
-        u = *reinterpret_cast<const uint32_t *>(p + gr * 4);
+        u = *reinterpret_cast<const uint32_t *>(p);
     return bf16 ? make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u))
                 : __half22float2(reinterpret_cast<const __half2 &>(u));
 }
 
-// One stage: MT tiles of 16 rows of codes with NT sets of eight tokens.  Offsets in
-// shared memory (`smem`): codes s4_code_at<UNIT> past a multiple of 64; scales[m], and
-// zeros that many bytes behind (0: none), [group][16] or (ODD) [group][32] of which 16
-// count; x[n]: this lane's token of set n, 16 t past a multiple of 256 (odd tokens: 64
-// more), x_lo: from it to the operands of the low parts (PARTS 2); ps: factors and sums,
-// [block of activations][8 NT tokens].  The stage has 4 / UNIT blocks and SG groups.
+// Half a stage: MT tiles of 16 rows of codes with NT sets of eight tokens.  Offsets in
+// shared memory (`smem`): codes, this lane's s4_code_at of the half; scales[m], those of this
+// lane's row 2 f in the half's first group (ODD: that of row 2 f + 1 is second[m] on), `step` bytes
+// from group to group, the zeros `zeros` bytes behind (0: none).  x(i, n, p): the operands
+// of this lane's token of set n for the i-th pair of MMAs, p 1 those of the low parts (PARTS
+// 2); ps(g, n): factor and sum of block g of this lane's two tokens of set n.  The half has
+// 4 / UNIT blocks, of which `blocks` are there, in SG groups.
 // tot += s factor (sum of n x - (8 + z) sum of x).
-template <int MT, int NT, int UNIT, int SG, int PARTS, bool ODD>
-__device__ __forceinline__ void s4_stage(float (&tot)[MT][NT][4], const uint8_t *smem, uint32_t codes,
-                                         const uint32_t (&scales)[MT], uint32_t zeros, bool bf16, const uint32_t (&x)[NT],
-                                         uint32_t x_lo, uint32_t ps, int lane) {
-    constexpr int GROUPS = 4 / UNIT;
-    const int gr = lane >> 2, t = lane & 3;
+template <int MT, int NT, int UNIT, int SG, int PARTS, bool ODD, typename OPERANDS, typename SUMS>
+__device__ __forceinline__ void s4_half_stage(float (&tot)[MT][NT][4], const uint8_t *smem, uint32_t codes,
+                                              const uint32_t (&scales)[MT], const uint32_t (&second)[MT], uint32_t step,
+                                              uint32_t zeros, bool bf16, OPERANDS x, SUMS ps, int blocks) {
+    constexpr int BLOCKS = 4 / UNIT;
     uint4 wide[MT][2];
     if constexpr (UNIT == 4) {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                wide[m][h] = *reinterpret_cast<const uint4 *>(smem + codes + m * kS4TileBytes + h * (8 * kS4RowBytes));
+                wide[m][h] = *reinterpret_cast<const uint4 *>(smem + (h ? s4_next_row(codes) : codes) + m * kS4TileBytes);
     }
 #pragma unroll
-    for (int g = 0; g < GROUPS; ++g) {
+    for (int g = 0; g < BLOCKS; ++g) {
+        if (BLOCKS > 1 && g >= blocks) break;
         float d[MT][NT][4];
 #pragma unroll
         for (int u = 0; u < UNIT; ++u) {
@@ -221,7 +230,7 @@ __device__ __forceinline__ void s4_stage(float (&tot)[MT][NT][4], const uint8_t 
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int p = 0; p < PARTS; ++p)
-                    xv[n][p] = *reinterpret_cast<const uint4 *>(smem + (x[n] ^ (uint32_t(i) << 6)) + uint32_t(p) * x_lo);
+                    xv[n][p] = x(i, n, p);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 uint32_t w[2], a[2][4];
@@ -230,8 +239,8 @@ __device__ __forceinline__ void s4_stage(float (&tot)[MT][NT][4], const uint8_t 
                     if constexpr (UNIT == 4)
                         w[h] = i == 0 ? wide[m][h].x : i == 1 ? wide[m][h].y : i == 2 ? wide[m][h].z : wide[m][h].w;
                     else
-                        w[h] = *reinterpret_cast<const uint32_t *>(smem + (codes ^ (uint32_t(i) << 4)) + m * kS4TileBytes +
-                                                                   h * (8 * kS4RowBytes));
+                        w[h] = *reinterpret_cast<const uint32_t *>(smem + ((h ? s4_next_row(codes) : codes) ^ (uint32_t(i) << 4)) +
+                                                                   m * kS4TileBytes);
                     s4_codes(w[h], a[h]);
                 }
 #pragma unroll
@@ -250,16 +259,16 @@ __device__ __forceinline__ void s4_stage(float (&tot)[MT][NT][4], const uint8_t 
         }
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            const uint8_t *at = smem + scales[m] + uint32_t(g * SG / GROUPS) * (ODD ? 64u : 32u);
-            const float2 s = s4_row_scales<ODD>(at, gr, bf16);
+            const uint8_t *at = smem + scales[m] + uint32_t(g * SG / BLOCKS) * step;
+            const float2 s = s4_row_scales<ODD>(at, second[m], bf16);
             float2 z = make_float2(8.0f, 8.0f);
             if (zeros != 0) {
-                const float2 more = s4_row_scales<ODD>(at + zeros, gr, bf16);
+                const float2 more = s4_row_scales<ODD>(at + zeros, second[m], bf16);
                 z = make_float2(__fadd_rn(z.x, more.x), __fadd_rn(z.y, more.y));
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const float4 q = *reinterpret_cast<const float4 *>(smem + ps + (g * 8 * NT + 8 * n + 2 * t) * 8);
+                const float4 q = ps(g, n);
                 float(&o)[4] = tot[m][n];
                 const float(&v)[4] = d[m][n];
                 o[0] = __fmaf_rn(s.x, __fmul_rn(q.x, __fmaf_rn(-z.x, q.y, v[0])), o[0]);
@@ -269,13 +278,6 @@ __device__ __forceinline__ void s4_stage(float (&tot)[MT][NT][4], const uint8_t 
             }
         }
     }
-}
-
-// This lane's piece (UNIT 4) or word of row lane / 4 in a stage's codes.
-template <int UNIT>
-__device__ __forceinline__ uint32_t s4_code_at(int lane) {
-    const int gr = lane >> 2, t = lane & 3;
-    return UNIT == 4 ? s4_piece<4>(gr, t) : s4_piece<1>(gr, 0) + uint32_t(t) * 4u;
 }
 
 // ------------------------------------------------------------ host side

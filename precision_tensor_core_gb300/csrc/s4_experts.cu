@@ -37,14 +37,13 @@ namespace {
 constexpr int kMoeWarps = 8, kMoeThreads = 32 * kMoeWarps;
 constexpr int kMaxTokens = 64, kMaxExperts = 512, kMaxTopK = 32, kMaxPairs = 512;
 constexpr int kTile = 8;  // tokens of an expert per item
+constexpr int kRing = 2;  // stages of a warp's ring
 
 __device__ uint32_t g_moe_error = 0;
 
-struct Experts {  // one of the two weight matrices
-    const uint8_t *codes;
-    int64_t pitch, expert;
+struct Experts {  // scales of one of the two weight matrices
     const uint8_t *scales, *zeros;
-    int rows, row_bytes, groups, tiles;
+    int groups, tiles;
 };
 
 struct MoeArgs {
@@ -56,17 +55,18 @@ struct MoeArgs {
     int *ids;        // NULL, or [tokens][top_k]
     float *weights;  // NULL, or the same
     int tokens, hidden, inner, experts, top_k, renormalize;
-    int bf16_scales, per_group;
+    int bf16_scales, per_group;  // halves of a stage per group (1 for groups of up to 128)
     Experts gate_up, down;
-    int stages, h_stages, h_blocks;  // stages of hidden and inner, blocks of 32 of inner
-    int stage_bytes;                 // of a warp's ring
+    int halves, stages;              // of hidden
+    int h_halves, h_stages, h_blocks;  // of inner; blocks of 32
+    int ring_bytes, scale_bytes;     // of all warps' codes; of a stage's scales and zeros
     // Workspace.
     uint32_t *counters;   // tickets, items of the first kind that are done
     float *logits;        // [tokens][experts]
     uint8_t *xs;          // [token][stage] operands
     float2 *xps;          // [token][block] factors and sums
     uint8_t *hs;          // [pair][stage] operands, high parts and low parts
-    float2 *hps;          // [pair][block of 32]
+    float2 *hps;          // [pair][block of 32, eight per stage]
     int stall;            // test hook: this item is never done (-1: none)
     uint64_t wait_limit;
 };
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kMoeThreads) router_kernel(const MoeArgs a) {
         const int first = int(blockIdx.x) - a.experts, ctas = int(gridDim.x) - a.experts;
         if (first == 0 && threadIdx.x < 2) a.counters[threadIdx.x] = 0;
         constexpr int LANES = 4 * UNIT, PER = 32 / LANES, GROUPS = 4 / UNIT;
-        const int blocks = a.stages * GROUPS, rounds = (blocks + PER - 1) / PER, lane8 = lane % LANES;
+        const int blocks = a.stages * 2 * GROUPS, rounds = (blocks + PER - 1) / PER, lane8 = lane % LANES;
         for (int u = first * kMoeWarps + warp; u < rounds * a.tokens; u += ctas * kMoeWarps) {
             const int tok = u / rounds, blk = (u - tok * rounds) * PER + lane / LANES;
             const int k = blk * (32 * UNIT) + lane8 * 8, have = max(0, min(8, a.hidden - k));
@@ -92,8 +92,8 @@ __global__ void __launch_bounds__(kMoeThreads) router_kernel(const MoeArgs a) {
             float2 ps;
             const uint4 op = s4_operands<UNIT, X>(load8(p, have, a.xvec != 0).v[0], ps);
             if (blk >= blocks) continue;
-            const int st = blk / GROUPS, g = blk % GROUPS;
-            *reinterpret_cast<uint4 *>(a.xs + (int64_t(tok) * a.stages + st) * kS4XBytes + s4_x_piece<UNIT>(0, g * LANES + lane8)) = op;
+            const int half = blk / GROUPS, g = blk % GROUPS;
+            *reinterpret_cast<uint4 *>(a.xs + (int64_t(tok) * a.stages * 2 + half) * kS4XBytes + s4_x_piece<UNIT>(g * LANES + lane8)) = op;
             if (lane8 == 0) a.xps[int64_t(tok) * blocks + blk] = ps;
         }
         return;
@@ -155,8 +155,12 @@ struct Routing {
     uint16_t tile_expert[kMaxPairs], tile_first[kMaxPairs];
     uint8_t tile_count[kMaxPairs];
     int tiles;
-    uint32_t ticket[2];
-    int abort;
+    uint32_t ticket[4];
+};
+
+struct MoeTail {
+    uint64_t full[kMoeWarps][kRing];
+    AbortState abort;
 };
 
 // Order of logits as integers: NaN below every number, 0 for what is taken already.
@@ -277,111 +281,207 @@ __device__ __forceinline__ bool wait_done(const MoeArgs &a, uint32_t count) {
             atomicCAS(&g_moe_error, 0u, kErrTimeout);
             return false;
         }
-        __nanosleep(64);
+        __nanosleep(32);
     }
 }
 
 // ------------------------------------------------------------ experts
-template <typename X, int UNIT, bool ODD, int D>
-__global__ void __launch_bounds__(kMoeThreads, 2) experts_kernel(const MoeArgs a) {
-    constexpr int SG = 4 / UNIT;  // scale groups (and, of x, blocks) per stage
-    extern __shared__ __align__(256) uint8_t moe_smem[];
+// What a warp brings next: stages of one item, in the order in which it takes them.
+struct Bring {
+    int left;         // stages of the item
+    int second_kind;  // rows of y
+    int tile, st;     // the next stage's tile of pairs and stage
+    int row;          // the warp's first row of h, or the item's of y
+};
+
+template <typename X, int UNIT, bool ODD>
+__global__ void __launch_bounds__(kMoeThreads, 2)
+    experts_kernel(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CUtensorMap tm_down, const MoeArgs a) {
+    constexpr int SG = 4 / UNIT;            // scale groups (and, of x, blocks) per half stage
+    constexpr int SCALES = 2 * SG * 32;     // bytes of a tile's scales in a stage
+    constexpr int UP = SCALES;              // up's from the gate's
+    constexpr int ZEROS = SCALES * (ODD ? 3 : 2);  // zeros from scales, of either kind
+    constexpr int CODES = 2 * kS4TileBytes;
+    extern __shared__ uint8_t moe_raw[];
+    uint8_t *const smem = moe_raw + ((1024u - (smem_u32(moe_raw) & 1023u)) & 1023u);
     __shared__ Routing r;
+    __shared__ MoeTail st;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int gr = lane >> 2, t = lane & 3, crow = gr, piece = t;
-    const uint32_t ring = uint32_t(warp * D * a.stage_bytes), ring_at = smem_u32(moe_smem) + ring;
-    float *const sums = reinterpret_cast<float *>(moe_smem + kMoeWarps * D * a.stage_bytes);
+    const int f = s4_pair_of(lane >> 2), gr = lane >> 2, t = lane & 3;
+    const int half = warp & 1, share = warp >> 1;  // of rows of h
+    const uint32_t ring = uint32_t(warp * kRing * CODES), scale_ring = uint32_t(a.ring_bytes + warp * kRing * a.scale_bytes);
+    float *const sums = reinterpret_cast<float *>(smem + a.ring_bytes + kMoeWarps * kRing * a.scale_bytes);
+    if (lane == 0)
+        for (int i = 0; i < kRing; ++i) mbar_init(&st.full[warp][i], 1);
+    if (threadIdx.x == 0) {
+        st.abort.flag = 0;
+        tma_prefetch_desc(&tm_up);
+        tma_prefetch_desc(&tm_down);
+    }
+    fence_barrier_init();
     griddep_wait();
     griddep_launch_dependents();
     if (threadIdx.x == 0) {
         r.ticket[0] = atomicAdd(a.counters, 1u);
-        r.abort = 0;
+        r.ticket[1] = atomicAdd(a.counters, 1u);
     }
     route(a, r);
 
     const int first_items = r.tiles * a.h_blocks, items = first_items + (a.hidden + 15) / 16;
+    const int units = r.tiles * a.h_stages;  // stages of all tiles' rows of y, shared by the warps
+    const int u0 = int(int64_t(units) * warp / kMoeWarps), u1 = int(int64_t(units) * (warp + 1) / kMoeWarps);
+    auto ticket = [&](int round) { return int(min(r.ticket[round & 3], 0x7FFFFFFFu)); };
+    // The stages of the item of a round; none past the last item.
+    auto begin = [&](int round) {
+        const int item = ticket(round);
+        Bring b{0, 0, 0, 0, 0};
+        if (item < first_items) {
+            b.tile = item / a.h_blocks;
+            b.row = (item - b.tile * a.h_blocks) * 32 + half * 16;
+            b.st = share;
+            b.left = (a.stages - share + 3) / 4;  // share, share + 4, ...
+        } else if (item < items) {
+            b.second_kind = 1;
+            b.row = (item - first_items) * 16;
+            b.tile = u0 / a.h_stages;
+            b.st = u0 - b.tile * a.h_stages;
+            b.left = u1 - u0;
+        }
+        return b;
+    };
+    // Lane 0 brings one stage: its codes (zeros past the matrix) and its tiles' scales and
+    // zeros.  When the item's are all asked for, the next item's follow: the weights do
+    // not depend on h.
+    Bring b = begin(0);
+    int bring_round = 0, into = 0, asked = 0, taken = 0;
+    auto issue = [&](int round) {
+        if (b.left == 0 && bring_round == round) b = begin(++bring_round);
+        if (b.left == 0) return;
+        if (lane == 0) {
+            const Experts &w = b.second_kind ? a.down : a.gate_up;
+            const int e = r.tile_expert[b.tile];
+            uint64_t *bar = &st.full[warp][into];
+            const int g0 = a.per_group == 1 ? 2 * b.st * SG : 2 * b.st / a.per_group;
+            const uint32_t bytes = uint32_t(min(2 * SG, w.groups - g0)) * 32u, both = w.zeros ? 2u : 1u;
+            const uint32_t dst = smem_u32(smem) + ring + into * CODES, sdst = smem_u32(smem) + scale_ring + into * a.scale_bytes;
+            auto scales = [&](int tile, uint32_t at) {
+                const int64_t from = ((int64_t(e) * w.tiles + tile) * w.groups + g0) * 32;
+                bulk_copy(sdst + at, w.scales + from, bytes, bar);
+                if (w.zeros) bulk_copy(sdst + ZEROS + at, w.zeros + from, bytes, bar);
+            };
+            if (b.second_kind) {
+                mbar_arrive_expect_tx(bar, kS4TileBytes + bytes * both);
+                tma_load_rows(dst, &tm_down, bar, b.st * kS4RowBytes, b.row, e);
+                scales(b.row / 16, 0);
+            } else {
+                // (up's rows may begin in the middle of a tile and end in the next one)
+                const int up = (a.inner + b.row) / 16, gate = min(b.row / 16, w.tiles - 1);
+                const bool next = ODD && up + 1 < w.tiles;
+                mbar_arrive_expect_tx(bar, 2 * kS4TileBytes + bytes * both * (next ? 3u : 2u));
+                tma_load_rows(dst, &tm_up, bar, b.st * kS4RowBytes, b.row, e);
+                tma_load_rows(dst + kS4TileBytes, &tm_up, bar, b.st * kS4RowBytes, a.inner + b.row, e);
+                scales(gate, 0);
+                scales(min(up, w.tiles - 1), UP);
+                if (next) scales(up + 1, UP + SCALES);
+            }
+        }
+        if (b.second_kind) {
+            if (++b.st == a.h_stages) {
+                b.st = 0;
+                ++b.tile;
+            }
+        } else {
+            b.st += 4;
+        }
+        --b.left;
+        ++asked;
+        if (++into == kRing) into = 0;
+    };
+    // Waits for the next stage to take; its place in the ring.
+    bool ok = true;
+    auto arrived = [&](int &from) {
+        from = taken % kRing;
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&st.full[warp][from], uint32_t(taken / kRing) & 1u, &st.abort, &g_moe_error, a.wait_limit));
+        return ok;
+    };
+    // Offset in a stage's scales of this lane's two rows, for the gate (and y) and up; from
+    // the first to the second row.
+    uint32_t row_at[2], row_more[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        auto at = [&](int i) { return uint32_t(i >> 4) * SCALES + uint32_t(i & 15) * 2u; };
+        const int i = 2 * f + (ODD && m ? a.inner % 16 : 0);
+        row_at[m] = at(i) + (m ? UP : 0);
+        row_more[m] = at(i + 1) - at(i);
+    }
+    // From the first to the second half of a stage: that of its scales.
+    auto second_half = [&](int s) {
+        return a.per_group == 1 ? SG * 32u : uint32_t((2 * s + 1) / a.per_group - 2 * s / a.per_group) * 32u;
+    };
+
+    __syncwarp();
+    for (int i = 0; i < kRing; ++i) issue(0);
     bool ready = false;  // every item of the first kind is done
     for (int round = 0;; ++round) {
-        const int item = int(min(r.ticket[round & 1], 0x7FFFFFFFu));
+        const int item = ticket(round);
         if (item >= items) break;
-        if (threadIdx.x == 0) r.ticket[(round + 1) & 1] = atomicAdd(a.counters, 1u);
+        if (threadIdx.x == 0) r.ticket[(round + 2) & 3] = atomicAdd(a.counters, 1u);
         if (item < first_items) {
             // ------------------------------------------------ rows of h
             const int tile = item / a.h_blocks, ib = item - tile * a.h_blocks;
-            const int e = r.tile_expert[tile], pair0 = r.tile_first[tile], n = r.tile_count[tile];
-            const int half = warp & 1, share = warp >> 1, row0 = ib * 32 + half * 16;
-            const Experts &w = a.gate_up;
-            const uint32_t x_bytes = uint32_t(n) * kS4XBytes;
-            // Codes: MMA rows crow and crow + 8 of the gate's tile and of up's.
-            const uint8_t *src[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                src[j] = w.codes + int64_t(e) * w.expert +
-                         int64_t((j >> 1) * a.inner + min(row0 + s4_row(crow + 8 * (j & 1)), a.inner - 1)) * w.pitch + piece * 16;
-            // Scales: of each tile and group 32 bytes (ODD: of two tiles), then the zeros.
-            constexpr int PIECES = 2 * SG * (ODD ? 4 : 2);
-            const uint32_t codes_at = uint32_t(min(kTile, a.tokens)) * kS4XBytes, scales_at = codes_at + 2 * kS4TileBytes;
-            const uint32_t ps_at = scales_at + PIECES * 16 * (w.zeros ? 2 : 1);
-            const int64_t expert_scales = int64_t(e) * w.tiles * w.groups * 32;
-            auto issue = [&](int st, int slot) {
-                const uint32_t dst = ring_at + uint32_t(slot * a.stage_bytes);
-                for (int q = lane; q < n * 16; q += 32) {
-                    const int j = q >> 4, c = q & 15;
-                    copy16(dst + uint32_t(j) * kS4XBytes + (uint32_t(c ^ ((j & 1) << 2)) << 4),
-                           a.xs + (int64_t(r.pair_token[pair0 + j]) * a.stages + st) * kS4XBytes + c * 16, 16);
-                }
-                for (int q = lane; q < n * SG; q += 32) {
-                    const int j = q / SG, g = q % SG;
-                    copy8(dst + ps_at + uint32_t(g * kTile + j) * 8u,
-                          a.xps + (int64_t(r.pair_token[pair0 + j]) * a.stages + st) * SG + g, 8);
-                }
-                const int have = min(16, w.row_bytes - st * kS4RowBytes - piece * 16);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    copy16(dst + codes_at + (j >> 1) * kS4TileBytes + s4_piece<UNIT>(crow + 8 * (j & 1), piece),
-                           have > 0 ? src[j] + int64_t(st) * kS4RowBytes : w.codes, max(have, 0));
-                for (int q = lane; q < PIECES * (w.zeros ? 2 : 1); q += 32) {
-                    const int z = q >= PIECES, p = q - (z ? PIECES : 0);
-                    const int m = p / (PIECES / 2), g = p % (PIECES / 2) / (ODD ? 4 : 2), i = p % (ODD ? 4 : 2);
-                    const int tl = (m * a.inner + row0) / 16 + (i >> 1), group = SG == 1 ? st / a.per_group : st * SG + g;
-                    const bool in = tl < w.tiles && group < w.groups;
-                    copy16(dst + scales_at + uint32_t(q) * 16u,
-                           in ? (z ? w.zeros : w.scales) + expert_scales + (int64_t(tl) * w.groups + group) * 32 + (i & 1) * 16 : w.scales,
-                           in ? 16 : 0);
-                }
-            };
+            const int pair0 = r.tile_first[tile], n = r.tile_count[tile];
             float tot[2][1][4];
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) tot[m][0][i] = 0.0f;
-            const int mine = (a.stages - share + 3) / 4;  // stages share, share + 4, ...
-            for (int i = 0; i < D - 1; ++i) {
-                if (i < mine) issue(share + 4 * i, i);
-                copies_commit();
+            const uint8_t *const xs = a.xs + int64_t(r.pair_token[pair0 + min(gr, n - 1)]) * a.stages * (2 * kS4XBytes) + t * 16;
+            const float2 *const ps0 = a.xps + int64_t(r.pair_token[pair0 + min(2 * t, n - 1)]) * a.stages * (2 * SG);
+            const float2 *const ps1 = a.xps + int64_t(r.pair_token[pair0 + min(2 * t + 1, n - 1)]) * a.stages * (2 * SG);
+            for (int s = share; s < a.stages && ok; s += 4) {
+                uint4 x[2][4];
+                float2 p[2][SG][2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[h][i] = *reinterpret_cast<const uint4 *>(xs + (2 * s + h) * kS4XBytes + i * 64);
+                    if constexpr (SG == 1) {
+                        p[h][0][0] = ps0[2 * s + h];
+                        p[h][0][1] = ps1[2 * s + h];
+                    }
+                }
+                int from;
+                if (!arrived(from)) break;
+                const uint32_t more = second_half(s);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (2 * s + h < a.halves) {
+                        const uint32_t at = scale_ring + uint32_t(from * a.scale_bytes) + uint32_t(h) * more;
+                        const uint32_t scales[2] = {at + row_at[0], at + row_at[1]};
+                        s4_half_stage<2, 1, UNIT, SG, 1, ODD>(
+                            tot, smem, (ring + uint32_t(from) * CODES + s4_code_at<UNIT>(lane)) ^ (uint32_t(h) << 6), scales, row_more,
+                            32u, a.gate_up.zeros ? ZEROS : 0u, a.bf16_scales != 0, [&](int i, int, int) { return x[h][i]; },
+                            [&](int g, int) {
+                                const float2 u = SG == 1 ? p[h][0][0] : ps0[(2 * s + h) * SG + g];
+                                const float2 v = SG == 1 ? p[h][0][1] : ps1[(2 * s + h) * SG + g];
+                                return make_float4(u.x, u.y, v.x, v.y);
+                            },
+                            (a.hidden - (2 * s + h) * kS4Half + 32 * UNIT - 1) / (32 * UNIT));
+                    }
+                }
+                __syncwarp();  // (every lane has read the stage)
+                ++taken;
+                issue(round);
             }
-            const int tok = min(gr, n - 1);
-            for (int i = 0; i < mine; ++i) {
-                copies_wait<D - 2>();
-                __syncwarp();
-                if (i + D - 1 < mine) issue(share + 4 * (i + D - 1), (i + D - 1) % D);
-                copies_commit();
-                const uint32_t at = ring + uint32_t((i % D) * a.stage_bytes);
-                const uint32_t x[1] = {at + uint32_t(tok) * kS4XBytes + uint32_t(t) * 16u + uint32_t(tok & 1) * 64u};
-                // (up's first row may lie anywhere in its tile)
-                const uint32_t scales[2] = {at + scales_at, at + scales_at + PIECES * 8 + (ODD ? uint32_t((a.inner + row0) % 16) * 2u : 0u)};
-                s4_stage<2, 1, UNIT, SG, 1, ODD>(tot, moe_smem, at + codes_at + s4_code_at<UNIT>(lane), scales,
-                                                 w.zeros ? PIECES * 16 : 0, a.bf16_scales != 0, x, x_bytes, at + ps_at, lane);
-            }
-            copies_wait<0>();
             // Sums of the shares: [share][half][gate, up][row][token].
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-                float *p = sums + ((warp * 2 + m) * 16 + 2 * gr) * kTile + 2 * t;
+                float *p = sums + ((warp * 2 + m) * 16 + 2 * f) * kTile + 2 * t;
                 *reinterpret_cast<float2 *>(p) = make_float2(tot[m][0][0], tot[m][0][1]);
                 *reinterpret_cast<float2 *>(p + kTile) = make_float2(tot[m][0][2], tot[m][0][3]);
             }
             __syncthreads();
+            if (st.abort.flag) break;
             if (warp < n) {  // token `warp`, a lane a row
                 float gate = 0.0f, up = 0.0f;
 #pragma unroll
@@ -397,11 +497,12 @@ __global__ void __launch_bounds__(kMoeThreads, 2) experts_kernel(const MoeArgs a
                 float2 ps;
                 s4_operand32(h, lane, hi, lo, ps);
                 const int64_t pair = pair0 + warp;
-                __half *p = reinterpret_cast<__half *>(a.hs + (pair * a.h_stages + ib / 4) * (2 * kS4XBytes)) + (ib & 3) * 32 +
+                // [pair][stage][high parts of 256, low parts]
+                __half *p = reinterpret_cast<__half *>(a.hs + (pair * a.h_stages + ib / 8) * (4 * kS4XBytes)) + (ib & 7) * 32 +
                             (lane >> 3) * 8 + s4_half(lane & 7);
                 p[0] = hi;
-                p[kS4XBytes / 2] = lo;
-                if (lane == 0) a.hps[pair * a.h_blocks + ib] = ps;
+                p[kS4XBytes] = lo;
+                if (lane == 0) a.hps[pair * a.h_stages * 8 + ib] = ps;
             }
             __threadfence();
             __syncthreads();
@@ -410,100 +511,72 @@ __global__ void __launch_bounds__(kMoeThreads, 2) experts_kernel(const MoeArgs a
         } else {
             // ------------------------------------------------ rows of y
             if (!ready) {
-                if (threadIdx.x == 0 && !wait_done(a, uint32_t(first_items))) r.abort = 1;
+                if (threadIdx.x == 0 && !wait_done(a, uint32_t(first_items))) st.abort.flag = 1;
                 __syncthreads();
-                if (r.abort) break;
+                if (st.abort.flag) break;
                 ready = true;
             }
             const int row0 = (item - first_items) * 16;
-            const Experts &w = a.down;
-            const uint32_t most_x = uint32_t(min(kTile, a.tokens)) * kS4XBytes;
-            const uint32_t codes_at = 2 * most_x, scales_at = codes_at + kS4TileBytes;
-            constexpr int PIECES = SG * 2;
-            const uint32_t ps_at = scales_at + PIECES * 16 * (w.zeros ? 2 : 1);
             for (int i = lane; i < a.tokens * 16; i += 32) sums[warp * (a.tokens * 16) + i] = 0.0f;
             __syncwarp();
-            const int units = r.tiles * a.h_stages;
-            const int u0 = int(int64_t(units) * warp / kMoeWarps), u1 = int(int64_t(units) * (warp + 1) / kMoeWarps);
-            int64_t row_at[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) row_at[j] = int64_t(min(row0 + s4_row(crow + 8 * j), w.rows - 1)) * w.pitch + piece * 16;
-            // The next unit to bring: tile and stage.
-            int b_tile = u0 / a.h_stages, b_st = u0 - b_tile * a.h_stages, b_left = u1 - u0;
-            auto issue = [&](int slot) {
-                const uint32_t dst = ring_at + uint32_t(slot * a.stage_bytes);
-                const int e = r.tile_expert[b_tile], pair0 = r.tile_first[b_tile], n = r.tile_count[b_tile], st = b_st;
-                for (int q = lane; q < n * 32; q += 32) {
-                    const int j = q >> 5, lo = (q >> 4) & 1, c = q & 15;
-                    const bool in = st * 4 + (c >> 2) < a.h_blocks;
-                    copy16(dst + uint32_t(lo) * most_x + uint32_t(j) * kS4XBytes + (uint32_t(c ^ ((j & 1) << 2)) << 4),
-                           a.hs + (int64_t(pair0 + j) * a.h_stages + st) * (2 * kS4XBytes) + lo * kS4XBytes + c * 16, in ? 16 : 0);
-                }
-                if (lane < n * 4) {
-                    const int j = lane >> 2, g = lane & 3;
-                    const bool in = st * 4 + g < a.h_blocks;
-                    copy8(dst + ps_at + uint32_t(g * kTile + j) * 8u, a.hps + int64_t(pair0 + j) * a.h_blocks + (in ? st * 4 + g : 0),
-                          in ? 8 : 0);
-                }
-                const int have = min(16, w.row_bytes - st * kS4RowBytes - piece * 16);
-                const uint8_t *codes = w.codes + int64_t(e) * w.expert;
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    copy16(dst + codes_at + s4_piece<1>(crow + 8 * j, piece),
-                           have > 0 ? codes + row_at[j] + int64_t(st) * kS4RowBytes : w.codes, max(have, 0));
-                if (lane < PIECES * (w.zeros ? 2 : 1)) {
-                    const int z = lane >= PIECES, p = lane - (z ? PIECES : 0), group = SG == 1 ? st / a.per_group : st * SG + (p >> 1);
-                    const bool in = group < w.groups;
-                    copy16(dst + scales_at + uint32_t(lane) * 16u,
-                           in ? (z ? w.zeros : w.scales) + ((int64_t(e) * w.tiles + row0 / 16) * w.groups + group) * 32 + (p & 1) * 16 : w.scales,
-                           in ? 16 : 0);
-                }
-                if (++b_st == a.h_stages) {
-                    b_st = 0;
-                    ++b_tile;
-                }
-                --b_left;
-            };
-            for (int i = 0; i < D - 1; ++i) {
-                if (b_left > 0) issue(i);
-                copies_commit();
-            }
             float tot[1][1][4] = {{{0.0f, 0.0f, 0.0f, 0.0f}}};
-            int tile = u0 / a.h_stages, st = u0 - tile * a.h_stages;
-            for (int u = u0, i = 0; u < u1; ++u, ++i) {
-                copies_wait<D - 2>();
-                __syncwarp();
-                if (b_left > 0) issue((i + D - 1) % D);
-                copies_commit();
-                const int n = r.tile_count[tile], tok = min(gr, n - 1);
-                const uint32_t at = ring + uint32_t((i % D) * a.stage_bytes);
-                const uint32_t x[1] = {at + uint32_t(tok) * kS4XBytes + uint32_t(t) * 16u + uint32_t(tok & 1) * 64u};
-                const uint32_t scales[1] = {at + scales_at};
-                s4_stage<1, 1, 1, SG, 2, false>(tot, moe_smem, at + codes_at + s4_code_at<1>(lane), scales, w.zeros ? PIECES * 16 : 0,
-                                                a.bf16_scales != 0, x, most_x, at + ps_at, lane);
-                if (++st == a.h_stages || u + 1 == u1) {
+            int tile = u0 / a.h_stages, s = u0 - tile * a.h_stages;
+            for (int u = u0; u < u1 && ok; ++u) {
+                const int pair0 = r.tile_first[tile], n = r.tile_count[tile];
+                const uint8_t *const xs = a.hs + (int64_t(pair0 + min(gr, n - 1)) * a.h_stages + s) * (4 * kS4XBytes) + t * 16;
+                const float2 *const ps0 = a.hps + (int64_t(pair0 + min(2 * t, n - 1)) * a.h_stages + s) * 8;
+                const float2 *const ps1 = a.hps + (int64_t(pair0 + min(2 * t + 1, n - 1)) * a.h_stages + s) * 8;
+                uint4 x[4][2];
+                auto load = [&](int h) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) x[i][p] = __ldcg(reinterpret_cast<const uint4 *>(xs + h * kS4XBytes + i * 64 + p * 2 * kS4XBytes));
+                };
+                load(0);
+                int from;
+                if (!arrived(from)) break;
+                const uint32_t more = second_half(s);
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    if (2 * s + h >= a.h_halves) break;
+                    if (h) load(1);
+                    const uint32_t scales[1] = {scale_ring + uint32_t(from * a.scale_bytes) + uint32_t(h) * more + row_at[0]};
+                    const uint32_t next_row[1] = {2u};
+                    s4_half_stage<1, 1, 1, SG, 2, false>(
+                        tot, smem, (ring + uint32_t(from) * CODES + s4_code_at<1>(lane)) ^ (uint32_t(h) << 6), scales, next_row, 32u,
+                        a.down.zeros ? ZEROS : 0u, a.bf16_scales != 0, [&](int i, int, int p) { return x[i][p]; },
+                        [&](int g, int) {
+                            const float2 v = __ldcg(ps0 + h * 4 + g), w = __ldcg(ps1 + h * 4 + g);
+                            return make_float4(v.x, v.y, w.x, w.y);
+                        },
+                        a.h_blocks - (2 * s + h) * 4);
+                }
+                __syncwarp();  // (every lane has read the stage)
+                ++taken;
+                issue(round);
+                if (++s == a.h_stages || u + 1 == u1) {
                     // The tile's sums to its tokens, this warp's.
 #pragma unroll
-                    for (int i2 = 0; i2 < 2; ++i2) {
-                        const int j = 2 * t + i2;
+                    for (int i = 0; i < 2; ++i) {
+                        const int j = 2 * t + i;
                         if (j < n) {
-                            const int pair = r.tile_first[tile] + j;
-                            float *p = sums + warp * (a.tokens * 16) + r.pair_token[pair] * 16 + 2 * gr;
-                            const float pw = r.pair_weight[pair];
-                            p[0] = __fmaf_rn(pw, tot[0][0][i2], p[0]);
-                            p[1] = __fmaf_rn(pw, tot[0][0][2 + i2], p[1]);
+                            float *p = sums + warp * (a.tokens * 16) + r.pair_token[pair0 + j] * 16 + 2 * f;
+                            const float pw = r.pair_weight[pair0 + j];
+                            p[0] = __fmaf_rn(pw, tot[0][0][i], p[0]);
+                            p[1] = __fmaf_rn(pw, tot[0][0][2 + i], p[1]);
                         }
                     }
 #pragma unroll
-                    for (int i2 = 0; i2 < 4; ++i2) tot[0][0][i2] = 0.0f;
-                    if (st == a.h_stages) {
-                        st = 0;
+                    for (int i = 0; i < 4; ++i) tot[0][0][i] = 0.0f;
+                    if (s == a.h_stages) {
+                        s = 0;
                         ++tile;
                     }
                 }
             }
-            copies_wait<0>();
             __syncthreads();
+            if (st.abort.flag) break;
             for (int o = threadIdx.x; o < a.tokens * 16; o += kMoeThreads) {
                 float v = 0.0f;
 #pragma unroll
@@ -512,8 +585,17 @@ __global__ void __launch_bounds__(kMoeThreads, 2) experts_kernel(const MoeArgs a
                 if (row < a.hidden) static_cast<X *>(a.y)[int64_t(o >> 4) * a.ldy + row] = from_float<X>(__fmul_rn(v, kS4Out));
             }
         }
-        __syncthreads();  // the next ticket is there, and the sums are read
+        __syncthreads();  // the tickets are there, and the sums are read
+        // (A warp that has no stage of this item brings the next one's here.)
+        while (asked - taken < kRing && (b.left > 0 || bring_round == round)) {
+            const int before = asked;
+            issue(round);
+            if (asked == before) break;
+        }
     }
+    // After an abort copies in flight land before the CTA exits.
+    for (; taken < asked; ++taken)
+        mbar_wait(&st.full[warp][taken % kRing], uint32_t(taken / kRing) & 1u, nullptr, nullptr, a.wait_limit);
 }
 
 // ------------------------------------------------------------ host side
@@ -529,14 +611,14 @@ struct MoeSpace {
 };
 
 MoeSpace moe_space(int64_t tokens, int64_t hidden, int64_t inner, int64_t experts, int64_t top_k) {
-    const int64_t stages = (hidden + 127) / 128, h_stages = (inner + 127) / 128, pairs = tokens * top_k;
+    const int64_t stages = (hidden + 255) / 256, h_stages = (inner + 255) / 256, pairs = tokens * top_k;
     MoeSpace s;
     s.logits = 256;
     s.xs = s.logits + up_to(tokens * experts * 4, 256);
-    s.xps = s.xs + tokens * stages * kS4XBytes;
-    s.hs = s.xps + up_to(tokens * stages * 4 * 8, 256);
-    s.hps = s.hs + pairs * h_stages * 2 * kS4XBytes;
-    s.bytes = s.hps + up_to(pairs * ((inner + 31) / 32) * 8, 256);
+    s.xps = s.xs + tokens * stages * 2 * kS4XBytes;
+    s.hs = s.xps + up_to(tokens * stages * 8 * 8, 256);
+    s.hps = s.hs + pairs * h_stages * 4 * kS4XBytes;
+    s.bytes = s.hps + up_to(pairs * h_stages * 8 * 8, 256);
     return s;
 }
 
@@ -561,42 +643,47 @@ cudaError_t launch_moe(void (*fn)(P...), int64_t blocks, size_t smem, cudaStream
     return e;
 }
 
-template <typename X, int UNIT, bool ODD, int D>
-int launch_experts(MoeArgs a, int sms, cudaStream_t s) {
+template <typename X, int UNIT, bool ODD>
+int launch_experts(MoeArgs a, const S4Weights &gu, const S4Weights &dn, int sms, cudaStream_t s) {
     constexpr int SG = 4 / UNIT;
-    auto *fn = experts_kernel<X, UNIT, ODD, D>;
-    const int most = std::min(a.tokens, kTile);
-    const int one = most * kS4XBytes + 2 * kS4TileBytes + 2 * SG * (ODD ? 4 : 2) * 16 * (a.gate_up.zeros ? 2 : 1) + SG * kTile * 8;
-    const int two = 2 * most * kS4XBytes + kS4TileBytes + SG * 2 * 16 * (a.down.zeros ? 2 : 1) + 4 * kTile * 8;
-    a.stage_bytes = int(up_to(std::max(one, two), 256));
-    const size_t smem = size_t(kMoeWarps) * D * a.stage_bytes + std::max<size_t>(kMoeWarps * 32 * kTile * 4, size_t(kMoeWarps) * a.tokens * 16 * 4);
+    auto *fn = experts_kernel<X, UNIT, ODD>;
+    a.ring_bytes = kMoeWarps * kRing * 2 * kS4TileBytes;
+    a.scale_bytes = 2 * SG * 32 * (ODD ? 3 : 2) * (a.gate_up.zeros || a.down.zeros ? 2 : 1);
+    const size_t sums = size_t(kMoeWarps) * std::max(32 * kTile, a.tokens * 16) * 4;
+    const size_t smem = size_t(a.ring_bytes) + size_t(kMoeWarps) * kRing * a.scale_bytes + sums + 1024;
     static std::atomic<int> ready[kMaxDevM];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return fail_launch(e, "cudaGetDevice");
     if (!ready[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 212 * 1024);
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
         if (e != cudaSuccess) return fail_launch(e, "experts set-up");
         ready[dev].store(1, std::memory_order_release);
     }
-    const int64_t waves = up_to(int64_t(a.tokens) * a.stages * SG, kMoeWarps * (32 / (4 * UNIT))) / (kMoeWarps * (32 / (4 * UNIT)));
-    e = launch_moe(router_kernel<X, UNIT>, a.experts + std::min<int64_t>(std::max<int64_t>(waves, 1), sms), 0, s, a);
+    CUtensorMap up, down;
+    int rc = encode_tmap_codes(&up, gu.codes, uint64_t(gu.cols + 1) / 2, uint64_t(gu.rows), uint64_t(gu.experts), uint64_t(gu.pitch),
+                               uint64_t(gu.expert), 16);
+    if (!rc)
+        rc = encode_tmap_codes(&down, dn.codes, uint64_t(dn.cols + 1) / 2, uint64_t(dn.rows), uint64_t(dn.experts), uint64_t(dn.pitch),
+                               uint64_t(dn.expert), 16);
+    if (rc) return rc;
+    const int64_t blocks = int64_t(a.tokens) * a.stages * 2 * SG, per_cta = kMoeWarps * (32 / (4 * UNIT));
+    const int64_t makers = std::min<int64_t>((blocks + per_cta - 1) / per_cta, sms);  // CTAs that make the operands
+    e = launch_moe(router_kernel<X, UNIT>, a.experts + makers, 0, s, a);
     if (e == cudaSuccess) {
-        const int per_sm = smem + sizeof(Routing) + 1024 <= 114 * 1024 ? 2 : 1;
-        e = launch_moe(fn, int64_t(sms) * per_sm, smem, s, a);
+        const int per_sm = smem + sizeof(Routing) + sizeof(MoeTail) + 1024 <= 114 * 1024 ? 2 : 1;
+        e = launch_moe(fn, int64_t(sms) * per_sm, smem, s, up, down, a);
     }
     return e == cudaSuccess ? PTC_OK : fail_launch(e, "experts launch");
 }
 
 template <typename X>
-int run_moe(const MoeArgs &a, int64_t group, int sms, cudaStream_t s) {
+int run_moe(const MoeArgs &a, const S4Weights &gu, const S4Weights &dn, int sms, cudaStream_t s) {
     auto unit = [&](auto u) {
         constexpr int U = decltype(u)::value;
-        const bool odd = a.inner % 16 != 0;
-        if (a.tokens <= 2) return odd ? launch_experts<X, U, true, 4>(a, sms, s) : launch_experts<X, U, false, 4>(a, sms, s);
-        return odd ? launch_experts<X, U, true, 3>(a, sms, s) : launch_experts<X, U, false, 3>(a, sms, s);
+        return a.inner % 16 ? launch_experts<X, U, true>(a, gu, dn, sms, s) : launch_experts<X, U, false>(a, gu, dn, sms, s);
     };
-    switch (s4_unit(group)) {
+    switch (s4_unit(gu.group)) {
         case 1: return unit(std::integral_constant<int, 1>());
         case 2: return unit(std::integral_constant<int, 2>());
         default: return unit(std::integral_constant<int, 4>());
@@ -605,13 +692,8 @@ int run_moe(const MoeArgs &a, int64_t group, int sms, cudaStream_t s) {
 
 Experts experts_of(const S4Weights &w) {
     Experts e;
-    e.codes = static_cast<const uint8_t *>(w.codes);
-    e.pitch = w.pitch;
-    e.expert = w.expert;
     e.scales = static_cast<const uint8_t *>(w.scales);
     e.zeros = static_cast<const uint8_t *>(w.zeros);
-    e.rows = int(w.rows);
-    e.row_bytes = int((w.cols + 1) / 2);
     e.groups = int(w.groups());
     e.tiles = int(w.tiles());
     return e;
@@ -662,6 +744,8 @@ int ptc_moe_a16_s4(int64_t tokens, int64_t hidden, int64_t inner, int64_t expert
     if (tokens == 0) return PTC_OK;
     if (!X || ldx < hidden || ldx > kMaxLdM || !Y || ldy < hidden || ldy > kMaxLdM || !router || ldr < hidden || ldr > kMaxLdM)
         return fail_status(PTC_ERR_INVALID, "X, Y or router is NULL, or its leading dimension is not hidden .. 2^36");
+    // (One expert has no distance to the next; a tensor map wants one.)
+    if (experts == 1) expert_gate_up = 2 * inner * ld_gate_up, expert_down = hidden * ld_down;
     const S4Weights gu{gate_up, ld_gate_up, expert_gate_up, gate_up_scales, gate_up_zeros, 2 * inner, hidden, group, experts};
     const S4Weights dn{down, ld_down, expert_down, down_scales, down_zeros, hidden, inner, group, experts};
     int rc = check_s4(gu);
@@ -718,8 +802,10 @@ int ptc_moe_a16_s4(int64_t tokens, int64_t hidden, int64_t inner, int64_t expert
     a.per_group = int(group >= 128 ? group / 128 : 1);
     a.gate_up = experts_of(gu);
     a.down = experts_of(dn);
-    a.stages = int((hidden + 127) / 128);
-    a.h_stages = int((inner + 127) / 128);
+    a.halves = int((hidden + kS4Half - 1) / kS4Half);
+    a.stages = int((hidden + kS4Stage - 1) / kS4Stage);
+    a.h_halves = int((inner + kS4Half - 1) / kS4Half);
+    a.h_stages = int((inner + kS4Stage - 1) / kS4Stage);
     a.h_blocks = int((inner + 31) / 32);
     a.counters = reinterpret_cast<uint32_t *>(ws);
     a.logits = reinterpret_cast<float *>(ws + at.logits);
@@ -730,7 +816,7 @@ int ptc_moe_a16_s4(int64_t tokens, int64_t hidden, int64_t inner, int64_t expert
     a.stall = take_stall_tile();
     a.wait_limit = wait_limit_ns();
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return type == PTC_OUT_BF16 ? run_moe<__nv_bfloat16>(a, group, sms, s) : run_moe<__half>(a, group, sms, s);
+    return type == PTC_OUT_BF16 ? run_moe<__nv_bfloat16>(a, gu, dn, sms, s) : run_moe<__half>(a, gu, dn, sms, s);
 }
 
 }  // extern "C"

@@ -6,11 +6,12 @@
 // tokens as the other (s4.cuh); sums stay in FP32.
 //
 // Layout.  The eight warps of a CTA are R row groups x S shares of K; a warp owns 16 MT
-// rows and every S-th stage of 128 codes, and brings them to its own ring in shared memory
-// by asynchronous copies, kStages deep, with no other warp to wait for.  The tokens'
-// activations are made operands once per CTA, in chunks of K that fit, two of them in
-// shared memory.  The shares' sums are added in order there, and where that leaves SMs
-// idle K is also shared by a cluster of up to eight CTAs, whose sums are added in rank
+// rows and every S-th stage of 256 codes.  One of its lanes brings them to the warp's own
+// ring in shared memory: the rows by TMA, whole 128-byte lines, and their scales by bulk
+// copies, so that no warp waits for another and the others spend no instruction on it.
+// The tokens' activations are made operands once per CTA, in chunks of K that fit, two of
+// them in shared memory.  The shares' sums are added in order there, and where that leaves
+// SMs idle K is also shared by a cluster of up to eight CTAs, whose sums are added in rank
 // order through distributed shared memory.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -33,32 +34,42 @@ namespace ptc {
 namespace {
 
 constexpr int kWarps4 = 8, kThreads4 = 32 * kWarps4;
-constexpr int kStages4 = 4;  // of a warp's ring
+__host__ __device__ constexpr int ring_of(int mt) { return mt == 1 ? 4 : 2; }  // stages of a warp's ring
+
+__device__ uint32_t g_s4_error = 0;
 
 struct S4Args {
     const void *x;
     int64_t ldx;
-    const uint8_t *codes;
-    int64_t pitch;
     const uint8_t *scales, *zeros;  // tiles
     void *C;
     int64_t ldc;
     int M, N, K;
-    int row_bytes;       // of codes
     int groups;          // per row
-    int per_group;       // stages per group (1 for groups of up to 128)
+    int per_group;       // halves of a stage per group (1 for groups of up to 128)
+    int halves;          // of stages, in K
     int stages;          // of K
     int chunk;           // stages of the CTA's K range whose activations are held at once
     int buffers;         // of activations
     int r_log2, ks;
     int xvec, bf16_scales;
-    int stage_bytes;     // of a warp's ring
+    int ring_bytes;      // of all warps
+    int stall;           // test hook: this CTA's weights never arrive (-1: none)
+    uint64_t wait_limit;
+};
+
+struct S4Tail {
+    uint64_t full[kWarps4][4];
+    AbortState abort;
 };
 
 template <typename X, int MT, int NT, int UNIT>
-__global__ void __launch_bounds__(kThreads4, MT == 1 ? 3 : 2) s4_kernel(const S4Args a) {
-    constexpr int TOK = 8 * NT, GROUPS = 4 / UNIT, D = kStages4;
-    extern __shared__ __align__(256) uint8_t smem4[];
+__global__ void __launch_bounds__(kThreads4, MT == 1 ? 3 : 2) s4_kernel(const __grid_constant__ CUtensorMap tm, const S4Args a) {
+    constexpr int TOK = 8 * NT, BLOCKS = 4 / UNIT, D = ring_of(MT), CODES = MT * kS4TileBytes;
+    constexpr int SCALES = 2 * BLOCKS * 32;  // bytes of a tile's scales in a stage: two halves' groups
+    extern __shared__ uint8_t smem4_raw[];
+    uint8_t *const smem4 = smem4_raw + ((1024u - (smem_u32(smem4_raw) & 1023u)) & 1023u);
+    __shared__ S4Tail st4;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int gr = lane >> 2, t = lane & 3;
     const int krank = a.ks == 1 ? 0 : int(cluster_ctarank());
@@ -69,66 +80,56 @@ __global__ void __launch_bounds__(kThreads4, MT == 1 ? 3 : 2) s4_kernel(const S4
     // This CTA's stages of K.
     const int q = a.stages / a.ks, rest = a.stages % a.ks;
     const int c0 = krank * q + min(krank, rest), c1 = c0 + q + (krank < rest ? 1 : 0);
-    const uint32_t ring = uint32_t(warp * D * a.stage_bytes), xs_base = uint32_t(kWarps4 * D * a.stage_bytes);
-    const uint32_t tok_bytes = uint32_t(a.chunk) * kS4XBytes, ps_at = tok_bytes * uint32_t(ntok);
-    const uint32_t buf_bytes = (ps_at + uint32_t(a.chunk) * (GROUPS * TOK * 8) + 255u) & ~255u;  // (tokens' places rest on 256)
+    // Shared memory: every warp's codes (on 1024 bytes), every warp's scales and zeros, activations.
+    const uint32_t scale_bytes = MT * SCALES * (a.zeros ? 2u : 1u);
+    const uint32_t ring = uint32_t(warp * D * CODES), scale_ring = uint32_t(kWarps4 * D * CODES) + uint32_t(warp * D) * scale_bytes;
+    const uint32_t xs_base = uint32_t(a.ring_bytes);
+    // (Tokens lie an odd number of 64 bytes apart, so that two of them are read at once.)
+    const uint32_t tok_bytes = uint32_t(a.chunk) * (2 * kS4XBytes) + 64u, ps_at = tok_bytes * uint32_t(ntok);
+    const uint32_t buf_bytes = ps_at + uint32_t(a.chunk) * (2 * BLOCKS * TOK * 8);
 
+    if (lane == 0)
+        for (int i = 0; i < D; ++i) mbar_init(&st4.full[warp][i], 1);
+    if (threadIdx.x == 0) {
+        st4.abort.flag = 0;
+        tma_prefetch_desc(&tm);
+    }
+    fence_barrier_init();
     griddep_wait();
     griddep_launch_dependents();
 
-    // Copies of stage i of this warp's share, c0 + share + i S: the rows' codes (two
-    // copies per tile, a lane 16 bytes) and the tiles' scales and zeros.
-    const int crow = lane >> 2, piece = lane & 3;
-    const uint8_t *src[2 * MT];
-#pragma unroll
-    for (int j = 0; j < 2 * MT; ++j)  // (MMA rows crow and crow + 8 of each tile)
-        src[j] = a.codes + int64_t(min(row0 + 16 * (j >> 1) + s4_row(crow + 8 * (j & 1)), a.N - 1)) * a.pitch + piece * 16;
-    constexpr int PIECES = MT * GROUPS * 2;  // of scales
-    const uint8_t *scale_src = nullptr;
-    const int sp = lane % PIECES, sm = sp / (2 * GROUPS), sg = sp / 2 % GROUPS;
-    const bool scale_lane = lane < PIECES * (a.zeros ? 2 : 1);
-    if (scale_lane) {
-        const int64_t tile = min(row0 / 16 + sm, (a.N + 15) / 16 - 1);
-        scale_src = (lane < PIECES ? a.scales : a.zeros) + tile * a.groups * 32 + (sp & 1) * 16;
-    }
-    // The next stage to bring, its place in the ring and its group.
-    int next = c0 + share, into = 0, group = GROUPS == 1 ? next / a.per_group : 0, in_group = GROUPS == 1 ? next % a.per_group : 0;
-    const uint32_t ring_at = smem_u32(smem4) + ring;
-    const uint32_t dst_at = ring_at + s4_piece<UNIT>(crow, piece), dst_at8 = ring_at + s4_piece<UNIT>(crow + 8, piece);
+    // Lane 0 brings this warp's stages c0 + share, + S, ...: the codes of its rows (zeros
+    // past the matrix) and its tiles' scales and zeros.
+    int next = c0 + share, into = 0;
     auto issue = [&]() {
-        if (next < c1) {
-            const uint32_t slot = uint32_t(into * a.stage_bytes);
-            const int n = min(16, a.row_bytes - next * kS4RowBytes - piece * 16);
+        if (lane == 0 && next < c1 && int(blockIdx.x) != a.stall) {
+            uint64_t *bar = &st4.full[warp][into];
+            const int g0 = a.per_group == 1 ? 2 * next * BLOCKS : 2 * next / a.per_group;
+            const uint32_t bytes = uint32_t(min(2 * BLOCKS, a.groups - g0)) * 32u;
+            mbar_arrive_expect_tx(bar, uint32_t(CODES) + MT * bytes * (a.zeros ? 2u : 1u));
+            tma_load_2d(smem4 + ring + into * CODES, &tm, bar, next * kS4RowBytes, row0);
 #pragma unroll
-            for (int j = 0; j < 2 * MT; ++j)
-                copy16((j & 1 ? dst_at8 : dst_at) + slot + (j >> 1) * kS4TileBytes,
-                       n > 0 ? src[j] + int64_t(next) * kS4RowBytes : a.codes, max(n, 0));
-            if (scale_lane) {
-                const int g = GROUPS == 1 ? group : next * GROUPS + sg;
-                copy16(ring_at + slot + MT * kS4TileBytes + lane * 16, g < a.groups ? scale_src + int64_t(g) * 32 : a.scales,
-                       g < a.groups ? 16 : 0);
-            }
-            next += S;
-            if (++into == D) into = 0;
-            if constexpr (GROUPS == 1) {
-                in_group += S;
-                while (in_group >= a.per_group) {
-                    in_group -= a.per_group;
-                    ++group;
-                }
+            for (int m = 0; m < MT; ++m) {
+                // (rows past the last tile read it again; what they give is dropped)
+                const int64_t at = (int64_t(min(row0 / 16 + m, (a.N + 15) / 16 - 1)) * a.groups + g0) * 32;
+                const uint32_t dst = smem_u32(smem4) + scale_ring + uint32_t(into) * scale_bytes + m * SCALES;
+                bulk_copy(dst, a.scales + at, bytes, bar);
+                if (a.zeros) bulk_copy(dst + MT * SCALES, a.zeros + at, bytes, bar);
             }
         }
-        copies_commit();
+        next += S;
+        if (++into == D) into = 0;
     };
+    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < D - 1; ++i) issue();
+    for (int i = 0; i < D; ++i) issue();
 
     // Activations of chunk c to its buffer: 4 UNIT lanes a block, a warp 32 / (4 UNIT),
     // four loads in flight per lane.
     auto load_x = [&](int c) {
         constexpr int LANES = 4 * UNIT, PER = 32 / LANES;
         const uint32_t buf = xs_base + (a.buffers == 2 && (c & 1) ? buf_bytes : 0u);
-        const int first = c0 + c * a.chunk, blocks = min(a.chunk, c1 - first) * GROUPS;
+        const int first = c0 + c * a.chunk, blocks = min(2 * min(a.chunk, c1 - first), a.halves - 2 * first) * BLOCKS;
         const int part = lane % LANES, k0 = first * kS4Stage + part * 8;
         const int rounds = (blocks + PER - 1) / PER, all = rounds * ntok;
         for (int u0 = warp; u0 < all; u0 += 4 * kWarps4) {
@@ -150,9 +151,9 @@ __global__ void __launch_bounds__(kThreads4, MT == 1 ? 3 : 2) s4_kernel(const S4
                 float2 ps;
                 const uint4 op = s4_operands<UNIT, X>(raw[j], ps);
                 if (at[j] < blocks) {
-                    const int st = at[j] / GROUPS, g = at[j] % GROUPS;
-                    *reinterpret_cast<uint4 *>(smem4 + buf + uint32_t(tk[j]) * tok_bytes + uint32_t(st) * kS4XBytes +
-                                               s4_x_piece<UNIT>(tk[j], g * LANES + part)) = op;
+                    const int hf = at[j] / BLOCKS, g = at[j] % BLOCKS;
+                    *reinterpret_cast<uint4 *>(smem4 + buf + uint32_t(tk[j]) * tok_bytes + uint32_t(hf) * kS4XBytes +
+                                               s4_x_piece<UNIT>(g * LANES + part)) = op;
                     if (part == 0) *reinterpret_cast<float2 *>(smem4 + buf + ps_at + uint32_t(at[j] * TOK + tk[j]) * 8u) = ps;
                 }
             }
@@ -167,47 +168,70 @@ __global__ void __launch_bounds__(kThreads4, MT == 1 ? 3 : 2) s4_kernel(const S4
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) tot[m][n][i] = 0.0f;
-    const uint32_t code_at = ring + s4_code_at<UNIT>(lane), scale_at = ring + MT * kS4TileBytes;
-    const uint32_t zeros = a.zeros ? PIECES * 16 : 0;
+    const uint32_t code_at = ring + s4_code_at<UNIT>(lane);
+    const uint32_t zeros = a.zeros ? MT * SCALES : 0, scale_at = scale_ring + uint32_t(s4_pair_of(gr)) * 4u;
     uint32_t tok_at[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {  // (tokens past the last read it again; their sums are dropped)
         const int tok = min(8 * n + gr, ntok - 1);
-        tok_at[n] = uint32_t(tok) * tok_bytes + uint32_t(t) * 16u + uint32_t(tok & 1) * 64u;
+        tok_at[n] = uint32_t(tok) * tok_bytes + uint32_t(t) * 16u;
     }
-    int from = 0;  // place in the ring
+    int from = 0, done = 0;  // place in the ring, stages taken
+    uint32_t parity = 0;
+    bool ok = true;
     for (int c = 0, st = c0 + share; c * a.chunk < c1 - c0; ++c) {
         __syncthreads();  // chunk c is there, and everyone is done with the other buffer
         if (a.buffers == 2 && (c + 1) * a.chunk < c1 - c0) load_x(c + 1);
         const uint32_t buf = xs_base + (a.buffers == 2 && (c & 1) ? buf_bytes : 0u);
         const int first = c0 + c * a.chunk, end = min(c1, first + a.chunk);
-        for (; st < end; st += S) {
-            copies_wait<D - 2>();
-            __syncwarp();
+        for (; ok && st < end; st += S, ++done) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&st4.full[warp][from], parity, &st4.abort, &g_s4_error, a.wait_limit));
+            if (!ok) break;  // (the sums are not used)
+            const uint32_t local = uint32_t(st - first) * 2;
+            // (groups of more than 128: the second half's may be the first's)
+            const uint32_t second = a.per_group == 1 ? BLOCKS * 32u : uint32_t((2 * st + 1) / a.per_group - 2 * st / a.per_group) * 32u;
+#pragma unroll 1
+            for (uint32_t h = 0; h < 2; ++h) {
+                if (2 * st + int(h) >= a.halves) break;
+                uint32_t scales[MT];
+                const uint32_t second_row[MT] = {};
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    scales[m] = scale_at + uint32_t(from) * scale_bytes + uint32_t(m) * SCALES + h * second;
+                const uint8_t *xp = smem4 + buf + (local + h) * kS4XBytes;
+                const uint8_t *pp = smem4 + buf + ps_at + (local + h) * (BLOCKS * TOK * 8) + uint32_t(t) * 16u;
+                s4_half_stage<MT, NT, UNIT, BLOCKS, 1, false>(
+                    tot, smem4, (code_at + uint32_t(from) * CODES) ^ (h << 6), scales, second_row, 32u, zeros, a.bf16_scales != 0,
+                    [&](int i, int n, int) { return *reinterpret_cast<const uint4 *>(xp + tok_at[n] + i * 64); },
+                    [&](int g, int n) { return *reinterpret_cast<const float4 *>(pp + (g * TOK + 8 * n) * 8); },
+                    (a.K - (2 * st + int(h)) * kS4Half + 32 * UNIT - 1) / (32 * UNIT));
+            }
+            __syncwarp();  // (every lane has read the stage)
             issue();
-            const uint32_t slot = uint32_t(from * a.stage_bytes), local = uint32_t(st - first);
-            if (++from == D) from = 0;
-            uint32_t x[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) x[n] = buf + tok_at[n] + local * kS4XBytes;
-            uint32_t scales[MT];
-#pragma unroll
-            for (int m = 0; m < MT; ++m) scales[m] = scale_at + slot + uint32_t(m * GROUPS) * 32u;
-            s4_stage<MT, NT, UNIT, GROUPS, 1, false>(tot, smem4, code_at + slot, scales, zeros, a.bf16_scales != 0, x, 0u,
-                                                     buf + ps_at + local * (GROUPS * TOK * 8), lane);
+            if (++from == D) {
+                from = 0;
+                parity ^= 1u;
+            }
         }
     }
-    copies_wait<0>();
     __syncthreads();
+    // After an abort copies in flight land before the ring is written, or the CTA exits.
+    if (st4.abort.flag) {
+        if (!ok)
+            for (int i = done; i < done + D; ++i)
+                if (c0 + share + i * S < c1 && int(blockIdx.x) != a.stall)
+                    mbar_wait(&st4.full[warp][i % D], uint32_t(i / D) & 1u, nullptr, nullptr, a.wait_limit);
+        __syncthreads();
+    }
 
-    // Sums: [warp][row][token] in the ring's place, added over the shares and then over
+    // Sums: [warp][row][token] in the rings' place, added over the shares and then over
     // the cluster's ranks, both in order.
     float *part = reinterpret_cast<float *>(smem4) + warp * (16 * MT * TOK);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int r = 16 * m + 2 * gr, tk = 8 * n + 2 * t;  // rows 2 gr and 2 gr + 1 of the tile
+            const int r = 16 * m + 2 * s4_pair_of(gr), tk = 8 * n + 2 * t;
             *reinterpret_cast<float2 *>(part + r * TOK + tk) = make_float2(tot[m][n][0], tot[m][n][1]);
             *reinterpret_cast<float2 *>(part + (r + 1) * TOK + tk) = make_float2(tot[m][n][2], tot[m][n][3]);
         }
@@ -241,7 +265,7 @@ std::atomic<int> g_s4_rows{0};   // "s4_tokens_rows": 0 by size, 1, 2, 4, 8
 std::atomic<int> g_s4_split{0};  // "s4_tokens_split": 0 by size, 1, 2, 4, 8
 std::atomic<int> g_s4_tiles{0};  // "s4_tokens_tiles": 0 by size, 1, 2
 
-constexpr int kSmem4 = 227 * 1024, kSmemSm = 228 * 1024;  // of a CTA, of an SM (1 KB per CTA is the system's)
+constexpr int kSmem4 = 227 * 1024, kSmemSm = 228 * 1024;  // of a CTA, of an SM
 
 // Rows and K shares of a launch, and how the activations are held.
 struct S4Shape {
@@ -250,20 +274,21 @@ struct S4Shape {
     size_t smem;
 };
 
-// Of a stage: codes, scales, zeros; in whole 64 bytes, on which the codes' places rest.
-int stage_bytes4(int mt, int groups, const void *zeros) { return (mt * (kS4TileBytes + groups * 32 * (zeros ? 2 : 1)) + 63) / 64 * 64; }
+// Bytes of all warps' rings: codes, scales, zeros.
+int ring_bytes4(int mt, int blocks, const void *zeros) {
+    return kWarps4 * ring_of(mt) * mt * (kS4TileBytes + 2 * blocks * 32 * (zeros ? 2 : 1));
+}
 
 // Shared memory of a shape; false where a buffer does not hold a stage of every share.
-bool fit_s4(S4Shape &sh, const S4Args &a, int groups_per_stage, int toks, int tok, int64_t ctas, int sms) {
-    const int S = kWarps4 >> sh.r_log2;
+bool fit_s4(S4Shape &sh, const S4Args &a, int blocks, int toks, int tok, int64_t ctas, int sms) {
+    const int S = kWarps4 >> sh.r_log2, ring = ring_bytes4(sh.mt, blocks, a.zeros);
     const int per_sm = int(std::min<int64_t>(sh.mt == 1 ? 3 : 2, (ctas + sms - 1) / sms));
-    const int most = std::min(kSmem4, kSmemSm / per_sm - 1024) / 256 * 256;
-    const int ring = kWarps4 * kStages4 * stage_bytes4(sh.mt, groups_per_stage, a.zeros);
-    const int per_stage = toks * kS4XBytes + groups_per_stage * tok * 8;
+    const int most = std::min(kSmem4 - 2048, kSmemSm / per_sm - 3072) / 256 * 256;  // (alignment, barriers, the system's 1 KB)
+    const int per_stage = 2 * (toks * kS4XBytes + blocks * tok * 8), more = toks * 64;
     const int range = (a.stages + sh.ks - 1) / sh.ks;  // the longest of a CTA
-    sh.buffers = range * per_stage <= most - ring ? 1 : 2;
-    sh.chunk = sh.buffers == 1 ? range : (most - ring) / 2 / 256 * 256 / per_stage / S * S;
-    sh.smem = size_t(ring) + size_t(sh.buffers) * size_t((sh.chunk * per_stage + 255) / 256 * 256);
+    sh.buffers = range * per_stage + more <= most - ring ? 1 : 2;
+    sh.chunk = sh.buffers == 1 ? range : ((most - ring) / 2 - more) / per_stage / S * S;
+    sh.smem = size_t(ring) + size_t(sh.buffers) * size_t(sh.chunk * per_stage + more);
     return sh.chunk > 0;
 }
 
@@ -299,24 +324,24 @@ S4Shape choose_s4(const S4Args &a, int unit, int sms) {
 }
 
 template <typename X, int MT, int NT, int UNIT>
-int launch_s4(S4Args a, const S4Shape &sh, cudaStream_t stream) {
-    constexpr int TOK = 8 * NT, GROUPS = 4 / UNIT;
+int launch_s4(S4Args a, const void *codes, int64_t pitch, const S4Shape &sh, cudaStream_t stream) {
+    constexpr int TOK = 8 * NT, BLOCKS = 4 / UNIT;
     auto *fn = s4_kernel<X, MT, NT, UNIT>;
     static std::atomic<int> ready[kMaxDev4];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return fail_launch(e, "cudaGetDevice");
     if (!ready[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem4);
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem4 - 1024);
         if (e != cudaSuccess) return fail_launch(e, "grouped 4-bit product set-up");
         ready[dev].store(1, std::memory_order_release);
     }
     a.r_log2 = sh.r_log2;
     a.ks = sh.ks;
-    a.stage_bytes = stage_bytes4(MT, GROUPS, a.zeros);
+    a.ring_bytes = ring_bytes4(MT, BLOCKS, a.zeros);
     a.buffers = sh.buffers;
     a.chunk = sh.chunk;
-    const size_t smem = sh.smem;
+    const size_t smem = sh.smem + 1024;
     const int R = 1 << sh.r_log2;
     const int64_t per = int64_t(16) * MT * R, blocks = (a.N + per - 1) / per * sh.ks, chunks = (a.M + TOK - 1) / TOK;
     cudaLaunchConfig_t cfg;
@@ -340,7 +365,10 @@ int launch_s4(S4Args a, const S4Shape &sh, cudaStream_t stream) {
         attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
         ++cfg.numAttrs;
     }
-    e = cudaLaunchKernelEx(&cfg, fn, a);
+    CUtensorMap tm;
+    const int rc = encode_tmap_2d(&tm, true, codes, uint64_t(a.K + 1) / 2, uint64_t(a.N), uint64_t(pitch), kS4RowBytes, 16 * MT);
+    if (rc) return rc;
+    e = cudaLaunchKernelEx(&cfg, fn, tm, a);
     if (e != cudaSuccess) return fail_launch(e, "grouped 4-bit product launch");
     note_launches(1);
     note_fp4_launch(int64_t(cfg.gridDim.x) * cfg.gridDim.y, sh.ks, sh.ks, 16 * MT * R);
@@ -348,13 +376,13 @@ int launch_s4(S4Args a, const S4Shape &sh, cudaStream_t stream) {
 }
 
 template <typename X>
-int run_s4(const S4Args &a, int64_t group, int sms, cudaStream_t s) {
+int run_s4(const S4Args &a, const void *codes, int64_t pitch, int64_t group, int sms, cudaStream_t s) {
     const bool wide = a.M > 8;
     const S4Shape sh = choose_s4(a, s4_unit(group), sms);
     auto unit = [&](auto u) {
         constexpr int U = decltype(u)::value;
-        if (sh.mt == 1) return wide ? launch_s4<X, 1, 2, U>(a, sh, s) : launch_s4<X, 1, 1, U>(a, sh, s);
-        return wide ? launch_s4<X, 2, 2, U>(a, sh, s) : launch_s4<X, 2, 1, U>(a, sh, s);
+        if (sh.mt == 1) return wide ? launch_s4<X, 1, 2, U>(a, codes, pitch, sh, s) : launch_s4<X, 1, 1, U>(a, codes, pitch, sh, s);
+        return wide ? launch_s4<X, 2, 2, U>(a, codes, pitch, sh, s) : launch_s4<X, 2, 1, U>(a, codes, pitch, sh, s);
     };
     switch (s4_unit(group)) {
         case 1: return unit(std::integral_constant<int, 1>());
@@ -366,6 +394,15 @@ int run_s4(const S4Args &a, int64_t group, int sms, cudaStream_t s) {
 bool at_multiple(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 }  // namespace
+
+cudaError_t read_and_clear_s4_error_word(uint32_t *out) {
+    uint32_t v = 0;
+    const uint32_t zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_s4_error, sizeof(v));
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_s4_error, &zero, sizeof(zero));
+    *out = v;
+    return e;
+}
 
 bool set_s4_tuning(const char *key, int64_t v) {
     const bool power = v == 0 || v == 1 || v == 2 || v == 4 || v == 8;
@@ -431,8 +468,6 @@ extern "C" int gemm_a16_s4(int64_t M, int64_t N, int64_t K, int type, const void
     std::memset(&a, 0, sizeof(a));
     a.x = X;
     a.ldx = ldx;
-    a.codes = static_cast<const uint8_t *>(W);
-    a.pitch = ldw;
     a.scales = static_cast<const uint8_t *>(scales);
     a.zeros = static_cast<const uint8_t *>(zeros);
     a.C = C;
@@ -440,11 +475,13 @@ extern "C" int gemm_a16_s4(int64_t M, int64_t N, int64_t K, int type, const void
     a.M = int(M);
     a.N = int(N);
     a.K = int(K);
-    a.row_bytes = int((K + 1) / 2);
     a.groups = int(w.groups());
     a.per_group = int(group >= 128 ? group / 128 : 1);
+    a.halves = int((K + kS4Half - 1) / kS4Half);
     a.stages = int((K + kS4Stage - 1) / kS4Stage);
+    a.stall = take_stall_tile();
+    a.wait_limit = wait_limit_ns();
     a.xvec = at_multiple(X, 16) && (M == 1 || ldx % 8 == 0);
     a.bf16_scales = scale_type == PTC_OUT_BF16;
-    return type == PTC_OUT_BF16 ? run_s4<__nv_bfloat16>(a, group, sms, s) : run_s4<__half>(a, group, sms, s);
+    return type == PTC_OUT_BF16 ? run_s4<__nv_bfloat16>(a, W, ldw, group, sms, s) : run_s4<__half>(a, W, ldw, group, sms, s);
 }

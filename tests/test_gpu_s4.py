@@ -47,10 +47,10 @@ SHAPES = list(itertools.product([1, 2, 4, 8], [1, 2, 4, 8], [1, 2]))
 @pytest.mark.parametrize("rows, split, tiles", SHAPES)
 @pytest.mark.parametrize("group", [32, 128])
 def test_every_launch_shape(rows, split, tiles, group):
-    """K of 64 stages and a part: every share has its stages; the shape is the one that was asked for."""
-    for M, K in ((1, 8200), (7, 8200), (16, 8200), (16, 16500)):
-        N = 530 if K < 10000 else 200
-        w = weights(3, (), N, K, group, True, HF)
+    """K of 64 stages and a part: every share has its stages, and its activations fit; the shape is the one asked for."""
+    N, K = 200, 16500
+    w = weights(3, (), N, K, group, True, HF)
+    for M in (1, 7, 12):
         x = rand(4, M, K, dtype=HF)
         for k, v in (("rows", rows), ("split", split), ("tiles", tiles)):
             ptc.ptc_set_tuning("s4_tokens_" + k, v)
@@ -219,6 +219,27 @@ def test_codes_past_32_bit_offsets():
     x = rand(23, 3, 200, dtype=BF)
     got = ptc.matmul_a16_s4(x, ptc.S4Matrix(v, ptc.S4Matrix.tile_scales(w["scales"]), 200, 64))
     check(got, x, w, BF)
+
+
+def test_weights_that_never_arrive_are_reported():
+    """A wait that runs out ends the call and is reported; the next call is whole."""
+    w = weights(30, (), 300, 4000, 128, False, BF)
+    m, x = matrix(w), rand(31, 3, 4000, dtype=BF)
+    for split in (1, 2):
+        ptc.ptc_set_tuning("s4_tokens_split", split)
+        want = ptc.matmul_a16_s4(x, m)
+        torch.cuda.synchronize()
+        ptc.ptc_debug_set_wait_limit(20_000_000, 1)
+        try:
+            ptc.matmul_a16_s4(x, m)
+            torch.cuda.synchronize()
+            assert ptc.lib().gemm_poll_device_error() == ptc.PTC_ERR_TIMEOUT
+        finally:
+            ptc.ptc_debug_set_wait_limit(0, -1)
+            ptc.ptc_set_tuning("s4_tokens_split", 0)
+        ptc.ptc_set_tuning("s4_tokens_split", split)
+        assert torch.equal(ptc.matmul_a16_s4(x, m), want)
+        ptc.ptc_set_tuning("s4_tokens_split", 0)
 
 
 def test_refusals():
