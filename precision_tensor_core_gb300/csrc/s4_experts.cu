@@ -37,6 +37,7 @@ namespace {
 constexpr int kMoeWarps = 8, kMoeThreads = 32 * kMoeWarps;
 constexpr int kMaxTokens = 64, kMaxExperts = 512, kMaxTopK = 32, kMaxPairs = 512;
 constexpr int kTile = 8;  // tokens of an expert per item
+constexpr int kLogits = 4;  // tokens per CTA of the router
 constexpr int kRing = 2;  // stages of a warp's ring
 
 __device__ uint32_t g_moe_error = 0;
@@ -72,16 +73,17 @@ struct MoeArgs {
 };
 
 // ------------------------------------------------------------ router
-// A CTA per expert: its logits of all tokens, eight tokens at a time, every thread eight
-// columns of each 2048; after them CTAs that make the tokens' operands.
+// A CTA per expert and four tokens: their logits, every thread eight columns of each 2048;
+// after them CTAs that make the tokens' operands.
 template <typename X, int UNIT>
 __global__ void __launch_bounds__(kMoeThreads) router_kernel(const MoeArgs a) {
-    __shared__ float part[kMoeWarps][kTile];
+    __shared__ float part[kMoeWarps][kLogits];
     griddep_wait();
     griddep_launch_dependents();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (int(blockIdx.x) >= a.experts) {
-        const int first = int(blockIdx.x) - a.experts, ctas = int(gridDim.x) - a.experts;
+    const int logits = (a.tokens + kLogits - 1) / kLogits * a.experts;  // CTAs
+    if (int(blockIdx.x) >= logits) {
+        const int first = int(blockIdx.x) - logits, ctas = int(gridDim.x) - logits;
         if (first == 0 && threadIdx.x < 2) a.counters[threadIdx.x] = 0;
         constexpr int LANES = 4 * UNIT, PER = 32 / LANES, GROUPS = 4 / UNIT;
         const int blocks = a.stages * 2 * GROUPS, rounds = (blocks + PER - 1) / PER, lane8 = lane % LANES;
@@ -98,47 +100,47 @@ __global__ void __launch_bounds__(kMoeThreads) router_kernel(const MoeArgs a) {
         }
         return;
     }
-    const int e = int(blockIdx.x);
-    for (int t0 = 0; t0 < a.tokens; t0 += kTile) {
-        const int n = min(kTile, a.tokens - t0);
-        float acc[kTile];
+    const int e = int(blockIdx.x) % a.experts, t0 = int(blockIdx.x) / a.experts * kLogits;
+    const X *x[kLogits];
+    float acc[kLogits];
 #pragma unroll
-        for (int j = 0; j < kTile; ++j) acc[j] = 0.0f;
-        for (int k = int(threadIdx.x) * 8; k < a.hidden; k += kMoeThreads * 8) {
-            const int have = min(8, a.hidden - k);
-            float w[8];
-            if (a.router_f32) {
-                const Pack8<float> r = load8(static_cast<const float *>(a.router) + int64_t(e) * a.ldr + k, have, a.rvec != 0);
+    for (int j = 0; j < kLogits; ++j) {  // (tokens past the last are the last again)
+        x[j] = static_cast<const X *>(a.x) + int64_t(min(t0 + j, a.tokens - 1)) * a.ldx;
+        acc[j] = 0.0f;
+    }
+#pragma unroll 2
+    for (int k = int(threadIdx.x) * 8; k < a.hidden; k += kMoeThreads * 8) {
+        const int have = min(8, a.hidden - k);
+        float w[8];
+        Pack8<X> v[kLogits];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = r.get(i);
-            } else {
-                const Pack8<X> r = load8(static_cast<const X *>(a.router) + int64_t(e) * a.ldr + k, have, a.rvec != 0);
+        for (int j = 0; j < kLogits; ++j) v[j] = load8(x[j] + k, have, a.xvec != 0);
+        if (a.router_f32) {
+            const Pack8<float> r = load8(static_cast<const float *>(a.router) + int64_t(e) * a.ldr + k, have, a.rvec != 0);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = to_float(r.get(i));
-            }
+            for (int i = 0; i < 8; ++i) w[i] = r.get(i);
+        } else {
+            const Pack8<X> r = load8(static_cast<const X *>(a.router) + int64_t(e) * a.ldr + k, have, a.rvec != 0);
 #pragma unroll
-            for (int j = 0; j < kTile; ++j) {
-                if (j < n) {
-                    const Pack8<X> v = load8(static_cast<const X *>(a.x) + int64_t(t0 + j) * a.ldx + k, have, a.xvec != 0);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) acc[j] = __fmaf_rn(to_float(v.get(i)), w[i], acc[j]);
-                }
-            }
+            for (int i = 0; i < 8; ++i) w[i] = to_float(r.get(i));
         }
 #pragma unroll
-        for (int j = 0; j < kTile; ++j) {
+        for (int j = 0; j < kLogits; ++j)
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], o);
-            if (lane == 0) part[warp][j] = acc[j];
-        }
-        __syncthreads();
-        if (int(threadIdx.x) < n) {
-            float v = 0.0f;
+            for (int i = 0; i < 8; ++i) acc[j] = __fmaf_rn(to_float(v[j].get(i)), w[i], acc[j]);
+    }
 #pragma unroll
-            for (int w = 0; w < kMoeWarps; ++w) v += part[w][threadIdx.x];
-            a.logits[int64_t(t0 + threadIdx.x) * a.experts + e] = v;
-        }
-        __syncthreads();
+    for (int j = 0; j < kLogits; ++j) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], o);
+        if (lane == 0) part[warp][j] = acc[j];
+    }
+    __syncthreads();
+    if (int(threadIdx.x) < min(kLogits, a.tokens - t0)) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kMoeWarps; ++w) v += part[w][threadIdx.x];
+        a.logits[int64_t(t0 + threadIdx.x) * a.experts + e] = v;
     }
 }
 
@@ -321,16 +323,21 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     fence_barrier_init();
     griddep_wait();
     griddep_launch_dependents();
-    if (threadIdx.x == 0) {
-        r.ticket[0] = atomicAdd(a.counters, 1u);
-        r.ticket[1] = atomicAdd(a.counters, 1u);
-    }
+    if (threadIdx.x == 0) r.ticket[0] = atomicAdd(a.counters, 1u);
     route(a, r);
 
     const int first_items = r.tiles * a.h_blocks, items = first_items + (a.hidden + 15) / 16;
+    // With many items per CTA tickets are taken two items ahead, so that the next item's weights
+    // are asked for before this one's end; with few that would leave CTAs without, and they are
+    // taken when the item before begins.
+    const bool early = first_items >= 4 * int(gridDim.x);
+    if (early) {
+        if (threadIdx.x == 0) r.ticket[1] = atomicAdd(a.counters, 1u);
+        __syncthreads();
+    }
     const int units = r.tiles * a.h_stages;  // stages of all tiles' rows of y, shared by the warps
     const int u0 = int(int64_t(units) * warp / kMoeWarps), u1 = int(int64_t(units) * (warp + 1) / kMoeWarps);
-    auto ticket = [&](int round) { return int(min(r.ticket[round & 3], 0x7FFFFFFFu)); };
+    auto ticket = [&](int round) { return int(r.ticket[round & 3]); };
     // The stages of the item of a round; none past the last item.
     auto begin = [&](int round) {
         const int item = ticket(round);
@@ -354,8 +361,8 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     // not depend on h.
     Bring b = begin(0);
     int bring_round = 0, into = 0, asked = 0, taken = 0;
-    auto issue = [&](int round) {
-        if (b.left == 0 && bring_round == round) b = begin(++bring_round);
+    auto issue = [&](int round, bool ahead) {
+        if (b.left == 0 && bring_round == round && ahead) b = begin(++bring_round);
         if (b.left == 0) return;
         if (lane == 0) {
             const Experts &w = b.second_kind ? a.down : a.gate_up;
@@ -420,12 +427,13 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     };
 
     __syncwarp();
-    for (int i = 0; i < kRing; ++i) issue(0);
+    for (int i = 0; i < kRing; ++i) issue(0, early);
     bool ready = false;  // every item of the first kind is done
     for (int round = 0;; ++round) {
         const int item = ticket(round);
         if (item >= items) break;
-        if (threadIdx.x == 0) r.ticket[(round + 2) & 3] = atomicAdd(a.counters, 1u);
+        const int later = (round + (early ? 2 : 1)) & 3;
+        if (threadIdx.x == 0 && (early || item < first_items)) r.ticket[later] = atomicAdd(a.counters, 1u);
         if (item < first_items) {
             // ------------------------------------------------ rows of h
             const int tile = item / a.h_blocks, ib = item - tile * a.h_blocks;
@@ -471,7 +479,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                 }
                 __syncwarp();  // (every lane has read the stage)
                 ++taken;
-                issue(round);
+                issue(round, early);
             }
             // Sums of the shares: [share][half][gate, up][row][token].
 #pragma unroll
@@ -516,6 +524,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                 if (st.abort.flag) break;
                 ready = true;
             }
+            if (threadIdx.x == 0 && !early) r.ticket[later] = atomicAdd(a.counters, 1u);
             const int row0 = (item - first_items) * 16;
             for (int i = lane; i < a.tokens * 16; i += 32) sums[warp * (a.tokens * 16) + i] = 0.0f;
             __syncwarp();
@@ -554,7 +563,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                 }
                 __syncwarp();  // (every lane has read the stage)
                 ++taken;
-                issue(round);
+                issue(round, early);
                 if (++s == a.h_stages || u + 1 == u1) {
                     // The tile's sums to its tokens, this warp's.
 #pragma unroll
@@ -589,7 +598,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
         // (A warp that has no stage of this item brings the next one's here.)
         while (asked - taken < kRing && (b.left > 0 || bring_round == round)) {
             const int before = asked;
-            issue(round);
+            issue(round, true);
             if (asked == before) break;
         }
     }
@@ -669,7 +678,7 @@ int launch_experts(MoeArgs a, const S4Weights &gu, const S4Weights &dn, int sms,
     if (rc) return rc;
     const int64_t blocks = int64_t(a.tokens) * a.stages * 2 * SG, per_cta = kMoeWarps * (32 / (4 * UNIT));
     const int64_t makers = std::min<int64_t>((blocks + per_cta - 1) / per_cta, sms);  // CTAs that make the operands
-    e = launch_moe(router_kernel<X, UNIT>, a.experts + makers, 0, s, a);
+    e = launch_moe(router_kernel<X, UNIT>, int64_t(a.tokens + kLogits - 1) / kLogits * a.experts + makers, 0, s, a);
     if (e == cudaSuccess) {
         const int per_sm = smem + sizeof(Routing) + sizeof(MoeTail) + 1024 <= 114 * 1024 ? 2 : 1;
         e = launch_moe(fn, int64_t(sms) * per_sm, smem, s, up, down, a);

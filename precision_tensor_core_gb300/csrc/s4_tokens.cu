@@ -34,7 +34,7 @@ namespace ptc {
 namespace {
 
 constexpr int kWarps4 = 8, kThreads4 = 32 * kWarps4;
-__host__ __device__ constexpr int ring_of(int mt) { return mt == 1 ? 4 : 2; }  // stages of a warp's ring
+__host__ __device__ constexpr int ring_of(int mt) { return mt == 1 ? 3 : 2; }  // stages of a warp's ring
 
 __device__ uint32_t g_s4_error = 0;
 
@@ -54,6 +54,7 @@ struct S4Args {
     int r_log2, ks;
     int xvec, bf16_scales;
     int ring_bytes;      // of all warps
+    int sums_at;
     int stall;           // test hook: this CTA's weights never arrive (-1: none)
     uint64_t wait_limit;
 };
@@ -75,7 +76,9 @@ __global__ void __launch_bounds__(kThreads4, MT == 1 ? 3 : 2) s4_kernel(const __
     const int krank = a.ks == 1 ? 0 : int(cluster_ctarank());
     const int R = 1 << a.r_log2, S = kWarps4 >> a.r_log2;
     const int rg = warp & (R - 1), share = warp >> a.r_log2;
-    const int row0 = (int(blockIdx.x) / a.ks * R + rg) * (16 * MT);
+    // Row tiles of R 16 MT rows: this cluster's first, and from one to its next.
+    const int tile0 = int(blockIdx.x) / a.ks, tile_step = int(gridDim.x) / a.ks;
+    const int tile_rows = 16 * MT * R, tiles = (a.N + tile_rows - 1) / tile_rows;
     const int tok0 = int(blockIdx.y) * TOK, ntok = min(TOK, a.M - tok0);
     // This CTA's stages of K.
     const int q = a.stages / a.ks, rest = a.stages % a.ks;
@@ -98,11 +101,14 @@ __global__ void __launch_bounds__(kThreads4, MT == 1 ? 3 : 2) s4_kernel(const __
     griddep_wait();
     griddep_launch_dependents();
 
-    // Lane 0 brings this warp's stages c0 + share, + S, ...: the codes of its rows (zeros
-    // past the matrix) and its tiles' scales and zeros.
-    int next = c0 + share, into = 0;
+    // Lane 0 brings this warp's stages c0 + share, + S, ... of tile after tile: the codes of
+    // its rows (zeros past the matrix) and its tiles' scales and zeros.
+    int asked = 0, taken = 0;
+    int next = c0 + share, next_tile = next < c1 ? tile0 : tiles, into = 0;
     auto issue = [&]() {
-        if (lane == 0 && next < c1 && int(blockIdx.x) != a.stall) {
+        if (next_tile >= tiles) return;
+        if (lane == 0 && int(blockIdx.x) != a.stall) {
+            const int row0 = next_tile * tile_rows + rg * (16 * MT);
             uint64_t *bar = &st4.full[warp][into];
             const int g0 = a.per_group == 1 ? 2 * next * BLOCKS : 2 * next / a.per_group;
             const uint32_t bytes = uint32_t(min(2 * BLOCKS, a.groups - g0)) * 32u;
@@ -118,17 +124,23 @@ __global__ void __launch_bounds__(kThreads4, MT == 1 ? 3 : 2) s4_kernel(const __
             }
         }
         next += S;
+        if (next >= c1) {
+            next = c0 + share;
+            next_tile += tile_step;
+        }
+        ++asked;
         if (++into == D) into = 0;
     };
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < D; ++i) issue();
 
-    // Activations of chunk c to its buffer: 4 UNIT lanes a block, a warp 32 / (4 UNIT),
+    // Activations of chunk c to the buffer of the place-th chunk: 4 UNIT lanes a block, a warp 32 / (4 UNIT),
     // four loads in flight per lane.
-    auto load_x = [&](int c) {
+    int chunks_done = 0;
+    auto load_x = [&](int c, int place) {
         constexpr int LANES = 4 * UNIT, PER = 32 / LANES;
-        const uint32_t buf = xs_base + (a.buffers == 2 && (c & 1) ? buf_bytes : 0u);
+        const uint32_t buf = xs_base + (a.buffers == 2 && (place & 1) ? buf_bytes : 0u);
         const int first = c0 + c * a.chunk, blocks = min(2 * min(a.chunk, c1 - first), a.halves - 2 * first) * BLOCKS;
         const int part = lane % LANES, k0 = first * kS4Stage + part * 8;
         const int rounds = (blocks + PER - 1) / PER, all = rounds * ntok;
@@ -159,15 +171,8 @@ __global__ void __launch_bounds__(kThreads4, MT == 1 ? 3 : 2) s4_kernel(const __
             }
         }
     };
-    load_x(0);
+    load_x(0, 0);
 
-    float tot[MT][NT][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tot[m][n][i] = 0.0f;
     const uint32_t code_at = ring + s4_code_at<UNIT>(lane);
     const uint32_t zeros = a.zeros ? MT * SCALES : 0, scale_at = scale_ring + uint32_t(s4_pair_of(gr)) * 4u;
     uint32_t tok_at[NT];
@@ -176,85 +181,95 @@ __global__ void __launch_bounds__(kThreads4, MT == 1 ? 3 : 2) s4_kernel(const __
         const int tok = min(8 * n + gr, ntok - 1);
         tok_at[n] = uint32_t(tok) * tok_bytes + uint32_t(t) * 16u;
     }
-    int from = 0, done = 0;  // place in the ring, stages taken
+    int from = 0;  // place in the ring
     uint32_t parity = 0;
     bool ok = true;
-    for (int c = 0, st = c0 + share; c * a.chunk < c1 - c0; ++c) {
-        __syncthreads();  // chunk c is there, and everyone is done with the other buffer
-        if (a.buffers == 2 && (c + 1) * a.chunk < c1 - c0) load_x(c + 1);
-        const uint32_t buf = xs_base + (a.buffers == 2 && (c & 1) ? buf_bytes : 0u);
-        const int first = c0 + c * a.chunk, end = min(c1, first + a.chunk);
-        for (; ok && st < end; st += S, ++done) {
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&st4.full[warp][from], parity, &st4.abort, &g_s4_error, a.wait_limit));
-            if (!ok) break;  // (the sums are not used)
-            const uint32_t local = uint32_t(st - first) * 2;
-            // (groups of more than 128: the second half's may be the first's)
-            const uint32_t second = a.per_group == 1 ? BLOCKS * 32u : uint32_t((2 * st + 1) / a.per_group - 2 * st / a.per_group) * 32u;
+    // Sums [warp][row][token], of this tile and the one before: written, joined after one
+    // synchronisation, and written again after the next.
+    float *sums = reinterpret_cast<float *>(smem4 + a.sums_at);
+    for (int tile = tile0, flip = 0; tile < tiles; tile += tile_step, flip ^= 1) {
+        float tot[MT][NT][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tot[m][n][i] = 0.0f;
+        for (int c = 0, st = c0 + share; c * a.chunk < c1 - c0; ++c) {
+            if (a.buffers == 2 || tile == tile0) __syncthreads();  // chunk c is there, and everyone is done with the other buffer
+            if (a.buffers == 2) {  // (the next tile begins with the first chunk again)
+                const bool last = (c + 1) * a.chunk >= c1 - c0;
+                if (!last || tile + tile_step < tiles) load_x(last ? 0 : c + 1, chunks_done + 1);
+            }
+            const uint32_t buf = xs_base + (a.buffers == 2 && (chunks_done & 1) ? buf_bytes : 0u);
+            ++chunks_done;
+            const int first = c0 + c * a.chunk, end = min(c1, first + a.chunk);
+            for (; ok && st < end; st += S) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&st4.full[warp][from], parity, &st4.abort, &g_s4_error, a.wait_limit));
+                if (!ok) break;  // (the sums are not used)
+                const uint32_t local = uint32_t(st - first) * 2;
+                // (groups of more than 128: the second half's may be the first's)
+                const uint32_t second = a.per_group == 1 ? BLOCKS * 32u : uint32_t((2 * st + 1) / a.per_group - 2 * st / a.per_group) * 32u;
 #pragma unroll 1
-            for (uint32_t h = 0; h < 2; ++h) {
-                if (2 * st + int(h) >= a.halves) break;
-                uint32_t scales[MT];
-                const uint32_t second_row[MT] = {};
+                for (uint32_t h = 0; h < 2; ++h) {
+                    if (2 * st + int(h) >= a.halves) break;
+                    uint32_t scales[MT];
+                    const uint32_t second_row[MT] = {};
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-                    scales[m] = scale_at + uint32_t(from) * scale_bytes + uint32_t(m) * SCALES + h * second;
-                const uint8_t *xp = smem4 + buf + (local + h) * kS4XBytes;
-                const uint8_t *pp = smem4 + buf + ps_at + (local + h) * (BLOCKS * TOK * 8) + uint32_t(t) * 16u;
-                s4_half_stage<MT, NT, UNIT, BLOCKS, 1, false>(
-                    tot, smem4, (code_at + uint32_t(from) * CODES) ^ (h << 6), scales, second_row, 32u, zeros, a.bf16_scales != 0,
-                    [&](int i, int n, int) { return *reinterpret_cast<const uint4 *>(xp + tok_at[n] + i * 64); },
-                    [&](int g, int n) { return *reinterpret_cast<const float4 *>(pp + (g * TOK + 8 * n) * 8); },
-                    (a.K - (2 * st + int(h)) * kS4Half + 32 * UNIT - 1) / (32 * UNIT));
-            }
-            __syncwarp();  // (every lane has read the stage)
-            issue();
-            if (++from == D) {
-                from = 0;
-                parity ^= 1u;
+                    for (int m = 0; m < MT; ++m)
+                        scales[m] = scale_at + uint32_t(from) * scale_bytes + uint32_t(m) * SCALES + h * second;
+                    const uint8_t *xp = smem4 + buf + (local + h) * kS4XBytes;
+                    const uint8_t *pp = smem4 + buf + ps_at + (local + h) * (BLOCKS * TOK * 8) + uint32_t(t) * 16u;
+                    s4_half_stage<MT, NT, UNIT, BLOCKS, 1, false>(
+                        tot, smem4, (code_at + uint32_t(from) * CODES) ^ (h << 6), scales, second_row, 32u, zeros, a.bf16_scales != 0,
+                        [&](int i, int n, int) { return *reinterpret_cast<const uint4 *>(xp + tok_at[n] + i * 64); },
+                        [&](int g, int n) { return *reinterpret_cast<const float4 *>(pp + (g * TOK + 8 * n) * 8); },
+                        (a.K - (2 * st + int(h)) * kS4Half + 32 * UNIT - 1) / (32 * UNIT));
+                }
+                __syncwarp();  // (every lane has read the stage)
+                ++taken;
+                issue();
+                if (++from == D) {
+                    from = 0;
+                    parity ^= 1u;
+                }
             }
         }
-    }
-    __syncthreads();
-    // After an abort copies in flight land before the ring is written, or the CTA exits.
-    if (st4.abort.flag) {
-        if (!ok)
-            for (int i = done; i < done + D; ++i)
-                if (c0 + share + i * S < c1 && int(blockIdx.x) != a.stall)
-                    mbar_wait(&st4.full[warp][i % D], uint32_t(i / D) & 1u, nullptr, nullptr, a.wait_limit);
-        __syncthreads();
-    }
-
-    // Sums: [warp][row][token] in the rings' place, added over the shares and then over
-    // the cluster's ranks, both in order.
-    float *part = reinterpret_cast<float *>(smem4) + warp * (16 * MT * TOK);
+        // Added over the shares and then over the cluster's ranks, both in order.
+        float *part = sums + flip * (kWarps4 * 16 * MT * TOK) + warp * (16 * MT * TOK);
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int r = 16 * m + 2 * s4_pair_of(gr), tk = 8 * n + 2 * t;
-            *reinterpret_cast<float2 *>(part + r * TOK + tk) = make_float2(tot[m][n][0], tot[m][n][1]);
-            *reinterpret_cast<float2 *>(part + (r + 1) * TOK + tk) = make_float2(tot[m][n][2], tot[m][n][3]);
-        }
-    if (a.ks > 1)
-        cluster_sync();
-    else
-        __syncthreads();
-    const uint32_t base = smem_u32(smem4);
-    const int rows = R * 16 * MT, first = int(blockIdx.x) / a.ks * rows;
-    for (int o = krank * kThreads4 + int(threadIdx.x); o < rows * TOK; o += a.ks * kThreads4) {
-        const int tk = o / rows, r = o - tk * rows, w = r / (16 * MT), lr = r % (16 * MT);
-        float v = 0.0f;
-        for (int k = 0; k < a.ks; ++k)
-            for (int sh = 0; sh < S; ++sh) {
-                const uint32_t at = base + uint32_t(((sh << a.r_log2) + w) * (16 * MT * TOK) + lr * TOK + tk) * 4u;
-                float f;
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(a.ks == 1 ? at : mapa_shared(at, uint32_t(k))) : "memory");
-                v = __fadd_rn(v, f);
+            for (int n = 0; n < NT; ++n) {
+                const int r = 16 * m + 2 * s4_pair_of(gr), tk = 8 * n + 2 * t;
+                *reinterpret_cast<float2 *>(part + r * TOK + tk) = make_float2(tot[m][n][0], tot[m][n][1]);
+                *reinterpret_cast<float2 *>(part + (r + 1) * TOK + tk) = make_float2(tot[m][n][2], tot[m][n][3]);
             }
-        if (tk < ntok && first + r < a.N)
-            static_cast<X *>(a.C)[int64_t(tok0 + tk) * a.ldc + first + r] = from_float<X>(__fmul_rn(v, kS4Out));
+        if (a.ks > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+        const uint32_t base = smem_u32(sums + flip * (kWarps4 * 16 * MT * TOK));
+        for (int o = krank * kThreads4 + int(threadIdx.x); o < tile_rows * TOK; o += a.ks * kThreads4) {
+            const int tk = o / tile_rows, r = o - tk * tile_rows, w = r / (16 * MT), lr = r % (16 * MT);
+            if (tk >= ntok) break;
+            float v = 0.0f;
+            for (int k = 0; k < a.ks; ++k)
+                for (int sh = 0; sh < S; ++sh) {
+                    const uint32_t at = base + uint32_t(((sh << a.r_log2) + w) * (16 * MT * TOK) + lr * TOK + tk) * 4u;
+                    float f;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(a.ks == 1 ? at : mapa_shared(at, uint32_t(k))) : "memory");
+                    v = __fadd_rn(v, f);
+                }
+            const int row = tile * tile_rows + r;
+            if (row < a.N) static_cast<X *>(a.C)[int64_t(tok0 + tk) * a.ldc + row] = from_float<X>(__fmul_rn(v, kS4Out));
+        }
     }
-    if (a.ks > 1) cluster_sync();
+    // After an abort copies in flight land before the CTA exits.
+    if (int(blockIdx.x) != a.stall)
+        for (; taken < asked; ++taken)
+            mbar_wait(&st4.full[warp][taken % D], uint32_t(taken / D) & 1u, nullptr, nullptr, a.wait_limit);
+    if (a.ks > 1) cluster_sync();  // (the sums are read)
 }
 
 // ------------------------------------------------------------ host side
@@ -271,7 +286,9 @@ constexpr int kSmem4 = 227 * 1024, kSmemSm = 228 * 1024;  // of a CTA, of an SM
 struct S4Shape {
     int mt, r_log2, ks;
     int chunk, buffers;
+    int sums_at;  // offset of the sums
     size_t smem;
+    int per_sm;   // CTAs that fit an SM
 };
 
 // Bytes of all warps' rings: codes, scales, zeros.
@@ -281,21 +298,28 @@ int ring_bytes4(int mt, int blocks, const void *zeros) {
 
 // Shared memory of a shape; false where a buffer does not hold a stage of every share.
 bool fit_s4(S4Shape &sh, const S4Args &a, int blocks, int toks, int tok, int64_t ctas, int sms) {
-    const int S = kWarps4 >> sh.r_log2, ring = ring_bytes4(sh.mt, blocks, a.zeros);
-    const int per_sm = int(std::min<int64_t>(sh.mt == 1 ? 3 : 2, (ctas + sms - 1) / sms));
-    const int most = std::min(kSmem4 - 2048, kSmemSm / per_sm - 3072) / 256 * 256;  // (alignment, barriers, the system's 1 KB)
+    const int S = kWarps4 >> sh.r_log2, ring = ring_bytes4(sh.mt, blocks, a.zeros), sums = 2 * kWarps4 * 16 * sh.mt * tok * 4;
     const int per_stage = 2 * (toks * kS4XBytes + blocks * tok * 8), more = toks * 64;
     const int range = (a.stages + sh.ks - 1) / sh.ks;  // the longest of a CTA
-    sh.buffers = range * per_stage + more <= most - ring ? 1 : 2;
-    sh.chunk = sh.buffers == 1 ? range : ((most - ring) / 2 - more) / per_stage / S * S;
-    sh.smem = size_t(ring) + size_t(sh.buffers) * size_t(sh.chunk * per_stage + more);
+    // As many CTAs per SM as hold the whole range; one whose buffers are as large as can be where none does.
+    sh.chunk = 0;
+    for (int per_sm = int(std::min<int64_t>(sh.mt == 1 ? 3 : 2, (ctas + sms - 1) / sms)); per_sm >= 1; --per_sm) {
+        const int most = std::min(kSmem4 - 2048, kSmemSm / per_sm - 3072) / 256 * 256 - ring - sums;  // (alignment, barriers, the system's 1 KB)
+        sh.buffers = range * per_stage + more <= most ? 1 : 2;
+        if (sh.buffers == 2 && per_sm > 1) continue;
+        sh.chunk = sh.buffers == 1 ? range : (most / 2 - more) / per_stage / S * S;
+        sh.sums_at = ring + sh.buffers * (sh.chunk * per_stage + more);
+        sh.smem = size_t(sh.sums_at + sums);
+        sh.per_sm = per_sm;
+        break;
+    }
     return sh.chunk > 0;
 }
 
 S4Shape choose_s4(const S4Args &a, int unit, int sms) {
     const int64_t N = a.N, chunks = (a.M + 15) / 16;
     const int stages = a.stages, toks = std::min(a.M, 16), tok = a.M > 8 ? 16 : 8;
-    S4Shape best{1, 0, 1, 0, 0, 0};
+    S4Shape best{1, 0, 1, 0, 0, 0, 0, 0};
     const int rows = g_s4_rows.load(), split = g_s4_split.load(), tiles = g_s4_tiles.load();
     int64_t cost_best = INT64_MAX;
     for (bool any : {false, true}) {
@@ -306,7 +330,7 @@ S4Shape choose_s4(const S4Args &a, int unit, int sms) {
                     if (stages < S * k && (r < 3 || k > 1)) continue;
                     if (!any && ((rows && rows != 1 << r) || (split && split != k) || (tiles && tiles != mt))) continue;
                     const int64_t per = int64_t(16) * mt << r, ctas = (N + per - 1) / per * k * chunks;
-                    S4Shape sh{mt, r, k, 0, 0, 0};
+                    S4Shape sh{mt, r, k, 0, 0, 0, 0, 0};
                     if (!fit_s4(sh, a, 4 / unit, toks, tok, ctas, sms)) continue;
                     const int64_t waves = (ctas + 2 * sms - 1) / (2 * sms);
                     const int64_t st = (stages + S * k - 1) / (S * k);
@@ -324,7 +348,7 @@ S4Shape choose_s4(const S4Args &a, int unit, int sms) {
 }
 
 template <typename X, int MT, int NT, int UNIT>
-int launch_s4(S4Args a, const void *codes, int64_t pitch, const S4Shape &sh, cudaStream_t stream) {
+int launch_s4(S4Args a, const void *codes, int64_t pitch, const S4Shape &sh, int sms, cudaStream_t stream) {
     constexpr int TOK = 8 * NT, BLOCKS = 4 / UNIT;
     auto *fn = s4_kernel<X, MT, NT, UNIT>;
     static std::atomic<int> ready[kMaxDev4];
@@ -341,9 +365,11 @@ int launch_s4(S4Args a, const void *codes, int64_t pitch, const S4Shape &sh, cud
     a.ring_bytes = ring_bytes4(MT, BLOCKS, a.zeros);
     a.buffers = sh.buffers;
     a.chunk = sh.chunk;
+    a.sums_at = sh.sums_at;
     const size_t smem = sh.smem + 1024;
     const int R = 1 << sh.r_log2;
-    const int64_t per = int64_t(16) * MT * R, blocks = (a.N + per - 1) / per * sh.ks, chunks = (a.M + TOK - 1) / TOK;
+    const int64_t per = int64_t(16) * MT * R, chunks = (a.M + TOK - 1) / TOK;
+    const int64_t blocks = std::min((a.N + per - 1) / per, std::max<int64_t>(1, int64_t(sms) * sh.per_sm / sh.ks)) * sh.ks;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
     std::memset(&cfg, 0, sizeof(cfg));
@@ -381,8 +407,8 @@ int run_s4(const S4Args &a, const void *codes, int64_t pitch, int64_t group, int
     const S4Shape sh = choose_s4(a, s4_unit(group), sms);
     auto unit = [&](auto u) {
         constexpr int U = decltype(u)::value;
-        if (sh.mt == 1) return wide ? launch_s4<X, 1, 2, U>(a, codes, pitch, sh, s) : launch_s4<X, 1, 1, U>(a, codes, pitch, sh, s);
-        return wide ? launch_s4<X, 2, 2, U>(a, codes, pitch, sh, s) : launch_s4<X, 2, 1, U>(a, codes, pitch, sh, s);
+        if (sh.mt == 1) return wide ? launch_s4<X, 1, 2, U>(a, codes, pitch, sh, sms, s) : launch_s4<X, 1, 1, U>(a, codes, pitch, sh, sms, s);
+        return wide ? launch_s4<X, 2, 2, U>(a, codes, pitch, sh, sms, s) : launch_s4<X, 2, 1, U>(a, codes, pitch, sh, sms, s);
     };
     switch (s4_unit(group)) {
         case 1: return unit(std::integral_constant<int, 1>());

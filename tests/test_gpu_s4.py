@@ -47,16 +47,18 @@ SHAPES = list(itertools.product([1, 2, 4, 8], [1, 2, 4, 8], [1, 2]))
 @pytest.mark.parametrize("rows, split, tiles", SHAPES)
 @pytest.mark.parametrize("group", [32, 128])
 def test_every_launch_shape(rows, split, tiles, group):
-    """K of 64 stages and a part: every share has its stages, and its activations fit; the shape is the one asked for."""
+    """K of 64 stages and a part: every share has its stages.  The shape is the one asked for where its
+    activations fit, up to seven tokens in all of them."""
     N, K = 200, 16500
     w = weights(3, (), N, K, group, True, HF)
-    for M in (1, 7, 12):
+    for M in (1, 7, 16):
         x = rand(4, M, K, dtype=HF)
         for k, v in (("rows", rows), ("split", split), ("tiles", tiles)):
             ptc.ptc_set_tuning("s4_tokens_" + k, v)
         got = ptc.matmul_a16_s4(x, matrix(w))
         grid, cluster, ks, tile = ptc.ptc_last_fp4_launch()
-        assert (cluster, ks, tile) == (split, split, 16 * rows * tiles) and grid == -(-N // tile) * split
+        if M <= 7:
+            assert (cluster, ks, tile) == (split, split, 16 * rows * tiles) and grid == -(-N // tile) * split
         check(got, x, w, HF)
     for k in ("rows", "split", "tiles"):
         ptc.ptc_set_tuning("s4_tokens_" + k, 0)
@@ -67,6 +69,21 @@ def test_larger(M, N, K):
     w = weights(5, (), N, K, 128, False, BF)
     x = rand(6, M, K, dtype=BF)
     check(ptc.matmul_a16_s4(x, matrix(w)), x, w, BF)
+
+
+@pytest.mark.parametrize("rows, split, tiles", [(1, 1, 1), (1, 1, 2), (4, 2, 1), (8, 4, 2), (8, 1, 1)])
+@pytest.mark.parametrize("M, K, group", [(1, 2100, 128), (3, 2048, 32), (16, 4096, 256), (40, 2100, 64)])
+def test_many_row_tiles_per_cta(rows, split, tiles, M, K, group):
+    """Every CTA walks over several tiles of rows, the last ones partial."""
+    N = 30011
+    w = weights(32, (), N, K, group, group == 32, BF)
+    x = rand(33, M, K, dtype=BF)
+    for k, v in (("rows", rows), ("split", split), ("tiles", tiles)):
+        ptc.ptc_set_tuning("s4_tokens_" + k, v)
+    got = ptc.matmul_a16_s4(x, matrix(w))
+    for k in ("rows", "split", "tiles"):
+        ptc.ptc_set_tuning("s4_tokens_" + k, 0)
+    check(got, x, w, BF)
 
 
 def test_codes_one_by_one():
