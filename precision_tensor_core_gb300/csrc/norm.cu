@@ -331,10 +331,15 @@ __device__ __forceinline__ void grad_chunk(const GradArgs &a, int64_t row, const
     store_chunk<VEC>(static_cast<T *>(a.dx) + row * a.lddx, round8<T>(o), i, tid, threads, a.cols);
 }
 
-// A CTA takes rows blockIdx.x, + gridDim.x, ... and holds its columns' sums of the
+// 16 bytes to shared memory, `n` of them from global memory and zeros after them.
+__device__ __forceinline__ void copy16_or_zero(void *dst, const void *src, int n) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+}
+
+// Rows that are not aligned: a CTA takes rows blockIdx.x, + gridDim.x, ... and holds its columns' sums of the
 // weight's gradient in registers; they leave as one row of partial sums per CTA,
 // which column_sums_kernel adds in order.
-template <typename T, bool VEC, int CH>
+template <typename T, int CH>
 __global__ void __launch_bounds__(512) grad_kernel(const GradArgs a) {
     __shared__ float2 buf[2][32];
     griddep_wait();
@@ -350,14 +355,14 @@ __global__ void __launch_bounds__(512) grad_kernel(const GradArgs a) {
         Pack8<T> s[CH], dy[CH];
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            s[i] = load_chunk<VEC>(static_cast<const T *>(a.s) + row * a.lds, i, tid, threads, a.cols);
-            dy[i] = load_chunk<VEC>(static_cast<const T *>(a.dy) + row * a.lddy, i, tid, threads, a.cols);
+            s[i] = load_chunk<false>(static_cast<const T *>(a.s) + row * a.lds, i, tid, threads, a.cols);
+            dy[i] = load_chunk<false>(static_cast<const T *>(a.dy) + row * a.lddy, i, tid, threads, a.cols);
         }
         float squares = 0.0f, gs = 0.0f;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             float w[8];
-            load_weight<VEC, T>(w, a.w, a.w_f32, i, tid, threads, a.cols);
+            load_weight<false, T>(w, a.w, a.w_f32, i, tid, threads, a.cols);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float sv = to_float(s[i].get(e));
@@ -369,14 +374,122 @@ __global__ void __launch_bounds__(512) grad_kernel(const GradArgs a) {
         const float r = inverse_rms(squares, a.inv_cols, a.eps);
         const float m = __fmul_rn(r, __fmul_rn(gs, a.inv_cols));
 #pragma unroll
-        for (int i = 0; i < CH; ++i) grad_chunk<T, VEC>(a, row, s[i], dy[i], r, m, acc[i], i, tid, threads);
+        for (int i = 0; i < CH; ++i) grad_chunk<T, false>(a, row, s[i], dy[i], r, m, acc[i], i, tid, threads);
     }
     float *part = a.part + int64_t(blockIdx.x) * a.cols;
 #pragma unroll
     for (int i = 0; i < CH; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int64_t c = column<VEC>(i, e, tid, threads);
+            const int64_t c = column<false>(i, e, tid, threads);
+            if (c < a.cols) part[c] = acc[i][e];
+        }
+}
+
+// The same for aligned rows, which come through shared memory: every thread copies its own
+// elements of the next rows there, `slots` rows deep, and waits for nobody else's.  (Loads
+// at the row's beginning left the memory idle during the reduction and the stores: 8192 x
+// 8192 bfloat16 with ds XX us.)
+template <typename T, int CH>
+__global__ void __launch_bounds__(1024) grad_ring_kernel(const GradArgs a, int slots) {
+    constexpr int W = Pack8<T>::W;
+    extern __shared__ uint4 ring[];  // [slot][s, dy, ds][chunk][16 bytes][thread], then the weights [chunk][2][thread]
+    __shared__ float2 buf[2][32];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int threads = int(blockDim.x), tid = int(threadIdx.x);
+    const int arrays = a.ds != nullptr ? 3 : 2, slot_size = arrays * CH * W * threads;
+    uint4 *const weights = ring + slots * slot_size + tid;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        float w[8];
+        load_weight<true, T>(w, a.w, a.w_f32, i, tid, threads, a.cols);
+        weights[(2 * i) * threads] = *reinterpret_cast<const uint4 *>(&w[0]);
+        weights[(2 * i + 1) * threads] = *reinterpret_cast<const uint4 *>(&w[4]);
+    }
+    auto issue = [&](int64_t row, int slot) {
+        if (row < a.rows) {
+            const T *from[3] = {static_cast<const T *>(a.s) + row * a.lds, static_cast<const T *>(a.dy) + row * a.lddy,
+                                static_cast<const T *>(a.ds) + row * a.ldds};
+            uint4 *to = ring + slot * slot_size + tid;
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                if (k < arrays)
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) {
+                        const int64_t c = column<true>(i, 0, tid, threads);
+#pragma unroll
+                        for (int w = 0; w < W; ++w) {
+                            constexpr int PER = 16 / int(sizeof(T));
+                            const int have = c < a.cols ? int(max(int64_t(0), min(int64_t(PER), a.cols - c - w * PER))) : 0;
+                            copy16_or_zero(to + ((k * CH + i) * W + w) * threads, from[k] + (have > 0 ? c + w * PER : 0), have * int(sizeof(T)));
+                        }
+                    }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto taken = [&](int slot, int array, int i) {
+        Pack8<T> v;
+#pragma unroll
+        for (int w = 0; w < W; ++w) v.v[w] = ring[slot * slot_size + ((array * CH + i) * W + w) * threads + tid];
+        return v;
+    };
+    auto weight = [&](int i, int e) { return reinterpret_cast<const float *>(weights + (2 * i + (e >> 2)) * threads)[e & 3]; };
+    float acc[CH][8];
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[i][e] = 0.0f;
+    for (int k = 0; k < slots; ++k) issue(int64_t(blockIdx.x) + int64_t(k) * gridDim.x, k);
+    int slot = 0, b = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, b ^= 1) {
+        switch (slots) {  // (all but the copies of the last slots - 1 rows)
+            case 1: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+            case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+            case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+            default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+        }
+        Pack8<T> s[CH], dy[CH];
+        float squares = 0.0f, gs = 0.0f;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            s[i] = taken(slot, 0, i);
+            dy[i] = taken(slot, 1, i);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float sv = to_float(s[i].get(e));
+                squares = __fmaf_rn(sv, sv, squares);
+                gs = __fmaf_rn(__fmul_rn(to_float(dy[i].get(e)), weight(i, e)), sv, gs);
+            }
+        }
+        reduce_two(squares, gs, buf[b]);
+        const float r = inverse_rms(squares, a.inv_cols, a.eps);
+        const float m = __fmul_rn(r, __fmul_rn(gs, a.inv_cols));
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            float o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float dv = to_float(dy[i].get(e)), u = __fmul_rn(to_float(s[i].get(e)), r);
+                o[e] = __fmul_rn(r, __fmaf_rn(-u, m, __fmul_rn(dv, weight(i, e))));
+                acc[i][e] = __fmaf_rn(dv, u, acc[i][e]);
+            }
+            if (a.ds != nullptr) {
+                const Pack8<T> d = taken(slot, 2, i);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = __fadd_rn(o[e], to_float(d.get(e)));
+            }
+            store_chunk<true>(static_cast<T *>(a.dx) + row * a.lddx, round8<T>(o), i, tid, threads, a.cols);
+        }
+        issue(row + int64_t(slots) * gridDim.x, slot);
+        if (++slot == slots) slot = 0;
+    }
+    float *part = a.part + int64_t(blockIdx.x) * a.cols;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int64_t c = column<true>(i, e, tid, threads);
             if (c < a.cols) part[c] = acc[i][e];
         }
 }
@@ -466,13 +579,14 @@ bool aligned_to(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>
 bool wide(const void *p, int64_t ld, int esize) { return aligned_to(p, 16) && (ld * esize) % 16 == 0; }
 
 template <typename... P, typename... A>
-cudaError_t launch_norm(void (*fn)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+cudaError_t launch_norm_smem(void (*fn)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
     std::memset(&cfg, 0, sizeof(cfg));
     std::memset(attr, 0, sizeof(attr));
     cfg.gridDim = grid;
     cfg.blockDim = dim3(unsigned(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
     if (pdl_enabled()) {
@@ -483,6 +597,11 @@ cudaError_t launch_norm(void (*fn)(P...), dim3 grid, int threads, cudaStream_t s
     const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
     if (e == cudaSuccess) note_launches(1);
     return e;
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_norm(void (*fn)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+    return launch_norm_smem(fn, grid, threads, 0, stream, args...);
 }
 
 int round32(int64_t n) { return int((n + 31) / 32 * 32); }
@@ -589,6 +708,22 @@ constexpr int kMaxParts = 512;
 bool grad_long(int64_t cols) { return cols > 16384; }
 int64_t grad_parts(int64_t rows) { return std::min<int64_t>(rows, kMaxParts); }
 
+// Of grad_ring_kernel: threads and their chunks, bytes of a row in flight and of the weights.
+struct RingShape {
+    int ch, threads;
+    size_t row, weights;
+};
+constexpr size_t kRingMost = 225 * 1024;  // of an SM, and of a CTA
+
+RingShape ring_shape(int64_t chunks, int arrays, size_t esize) {
+    RingShape g;
+    g.ch = chunks <= 1024 ? 1 : 2;
+    g.threads = round32((chunks + g.ch - 1) / g.ch);
+    g.row = size_t(arrays) * size_t(g.ch) * esize * 8 * size_t(g.threads);
+    g.weights = size_t(g.ch) * 32 * size_t(g.threads);
+    return g;
+}
+
 template <typename T, bool VEC>
 cudaError_t run_grad(GradArgs a, int sms, float *dw, cudaStream_t s) {
     const int64_t chunks = (a.cols + 7) / 8;
@@ -599,15 +734,25 @@ cudaError_t run_grad(GradArgs a, int sms, float *dw, cudaStream_t s) {
         parts = int(std::min<int64_t>(grad_parts(a.rows), std::max<int64_t>(1, 8 * int64_t(sms) / pieces)));
         e = launch_norm(grad_stats_kernel<T, VEC>, dim3(unsigned(a.rows)), 1024, s, a);
         if (e == cudaSuccess) e = launch_norm(grad_columns_kernel<T, VEC>, dim3(unsigned(pieces), unsigned(parts)), 256, s, a);
+    } else if (const RingShape g = ring_shape(chunks, a.ds ? 3 : 2, sizeof(T)); VEC && g.weights + g.row <= kRingMost) {
+        // Four rows in flight per CTA, fewer where they do not fit; up to three CTAs per SM.
+        const int slots = int(std::min<size_t>(4, (kRingMost - g.weights) / g.row));
+        const size_t smem = slots * g.row + g.weights;
+        const int per_sm = int(std::max<size_t>(1, std::min<size_t>({3, size_t(2048 / g.threads), kRingMost / (smem + 2048)})));
+        auto *fn = g.ch == 1 ? grad_ring_kernel<T, 1> : grad_ring_kernel<T, 2>;
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kRingMost));
+        if (e != cudaSuccess) return e;
+        parts = int(std::min<int64_t>(grad_parts(a.rows), int64_t(sms) * per_sm));
+        e = launch_norm_smem(fn, dim3(unsigned(parts)), g.threads, smem, s, a, slots);
     } else {
         const int ch = chunks <= 256 ? 1 : chunks <= 1024 ? 2 : 4;
         const int threads = round32((chunks + ch - 1) / ch);
         const int per_sm = std::max(1, (sizeof(T) == 2 && ch <= 2 ? 1024 : 512) / threads);
         parts = int(std::min<int64_t>(grad_parts(a.rows), int64_t(sms) * std::min(per_sm, 3)));
         const dim3 grid = dim3(unsigned(parts));
-        e = ch == 1   ? launch_norm(grad_kernel<T, VEC, 1>, grid, threads, s, a)
-            : ch == 2 ? launch_norm(grad_kernel<T, VEC, 2>, grid, threads, s, a)
-                      : launch_norm(grad_kernel<T, VEC, 4>, grid, threads, s, a);
+        e = ch == 1   ? launch_norm(grad_kernel<T, 1>, grid, threads, s, a)
+            : ch == 2 ? launch_norm(grad_kernel<T, 2>, grid, threads, s, a)
+                      : launch_norm(grad_kernel<T, 4>, grid, threads, s, a);
     }
     if (e == cudaSuccess)
         e = launch_norm(column_sums_kernel, dim3(unsigned((a.cols + 31) / 32)), 256, s, static_cast<const float *>(a.part), parts,
