@@ -455,12 +455,19 @@ int gemm_a16_fp4(int64_t M, int64_t N, int64_t K, int type, const void *X, int64
  * is exact down to 2^-28 of the largest of them and off by at most 2^-35 of it below.
  * A token with an infinity or NaN gives NaN; other tokens do not see it.
  * Meant for M up to 16, where W is read once; more rows are taken 16 at a time.  X and C
- * are aligned to the element.  K == 0 writes zeros.  No workspace is used.  Results are the
- * same from call to call; the summation order depends on the sizes (and the keys
- * s4_tokens_rows, s4_tokens_split, s4_tokens_tiles).
+ * are aligned to the element.  K == 0 writes zeros.  Results are the same from call to
+ * call; the summation order depends on the sizes (and the keys s4_tokens_rows,
+ * s4_tokens_split, s4_tokens_tiles).
+ *
+ * The workspace holds the activations as the tensor cores take them, made once for all
+ * CTAs: gemm_a16_s4_workspace(M, K) bytes, 16-byte aligned, and no other call's until this
+ * one is done.  With NULL (or for sizes of which that gives 0, up to two tokens) every CTA makes
+ * its own, with the same result.
  */
+int64_t gemm_a16_s4_workspace(int64_t M, int64_t K);
 int gemm_a16_s4(int64_t M, int64_t N, int64_t K, int type, const void *X, int64_t ldx, const void *W, int64_t ldw,
-                int64_t group, int scale_type, const void *scales, const void *zeros, void *C, int64_t ldc, void *stream);
+                int64_t group, int scale_type, const void *scales, const void *zeros, void *C, int64_t ldc, void *workspace,
+                int64_t workspace_bytes, void *stream);
 
 /*
  * A mixture-of-experts layer for a few tokens, with grouped 4-bit integer weights:
@@ -599,7 +606,7 @@ int ptc_last_launch(int *grid, int *cluster, int *ksplit, int *tile_n);
 
 /* The same of the calling thread's last 4-bit product: *tile = output columns per
  * tile of gemm_fp4 (256: CTA pairs, 128, 64), or rows of the weights per CTA of
- * gemm_a16_fp4 (128, 64, 32, 16) and gemm_a16_s4 (256 to 16). */
+ * gemm_a16_fp4 (128, 64, 32, 16) and gemm_a16_s4 (512 to 16). */
 int ptc_last_fp4_launch(int64_t *grid, int *cluster, int *ksplit, int *tile);
 
 /* Operand conversion of the calling thread's last GEMM call through this

@@ -11,7 +11,7 @@ library's CUDA kernels):
   ``gemm_s8_noalloc``, ``gemm_s8_b_rowmajor``, ``gemm_status_string``,
   ``gemm_poll_device_error``, ``ptc_kernel_launch_count``, ``ptc_last_launch``, ``ptc_last_fp4_launch``, ``ptc_last_conversion``, ``ptc_plan_shape``,
   ``ptc_debug_set_wait_limit``, ``ptc_set_tuning``, ``gemm_fp4``, ``gemm_a16_fp4``, ``ptc_dropout``,
-  ``ptc_dropout_to``, ``ptc_quantize_fp4``, ``ptc_dequantize_fp4``, ``gemm_a16_s4``, ``ptc_moe_a16_s4``,
+  ``ptc_dropout_to``, ``ptc_quantize_fp4``, ``ptc_dequantize_fp4``, ``gemm_a16_s4``, ``gemm_a16_s4_workspace``, ``ptc_moe_a16_s4``,
   ``ptc_moe_a16_s4_workspace``, ``ptc_rms_norm``, ``ptc_rms_norm_s8``,
   ``ptc_rms_norm_backward``, ``ptc_rms_norm_backward_workspace``: the C ABI of
   ``include/ptc.h`` under the same names, taking integers (sizes, leading
@@ -110,7 +110,8 @@ def lib() -> ctypes.CDLL:
                 ("gemm_fp4", [_i64, _i64, _i64, _int, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _int,
                               _vp]),
                 ("gemm_a16_fp4", [_i64, _i64, _i64, _int, _vp, _i64, _int, _vp, _i64, _vp, _vp, _vp, _i64, _vp]),
-                ("gemm_a16_s4", [_i64, _i64, _i64, _int, _vp, _i64, _vp, _i64, _i64, _int, _vp, _vp, _vp, _i64, _vp]),
+                ("gemm_a16_s4", [_i64, _i64, _i64, _int, _vp, _i64, _vp, _i64, _i64, _int, _vp, _vp, _vp, _i64, _vp, _i64,
+                                 _vp]),
                 ("ptc_moe_a16_s4", [_i64] * 5 + [_int, _int, _vp, _i64, _vp, _i64, _int, _i64, _int]
                  + [_vp, _i64, _i64, _vp, _vp] * 2 + [_vp, _i64, _vp, _vp, _vp, _i64, _vp]),
                 ("ptc_rms_norm", [_i64, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64, _vp, _int, _f32, _vp, _i64, _vp]),
@@ -121,6 +122,8 @@ def lib() -> ctypes.CDLL:
             fn = getattr(L, name)
             fn.restype = ctypes.c_int
             fn.argtypes = args
+        L.gemm_a16_s4_workspace.restype = _i64
+        L.gemm_a16_s4_workspace.argtypes = [_i64, _i64]
         L.ptc_moe_a16_s4_workspace.restype = _i64
         L.ptc_moe_a16_s4_workspace.argtypes = [_i64] * 5
         L.ptc_rms_norm_backward_workspace.restype = _i64
@@ -261,9 +264,16 @@ def gemm_a16_fp4(M, N, K, type, X, ldx, format, W, ldw, SW, GW, C, ldc, stream=0
     return _check(lib().gemm_a16_fp4(M, N, K, type, X, ldx, format, W, ldw, SW, GW, C, ldc, stream))
 
 
-def gemm_a16_s4(M, N, K, type, X, ldx, W, ldw, group, scale_type, scales, zeros, C, ldc, stream=0) -> int:
+def gemm_a16_s4_workspace(M, K) -> int:
+    """Bytes of workspace with which gemm_a16_s4 is fastest."""
+    return lib().gemm_a16_s4_workspace(M, K)
+
+
+def gemm_a16_s4(M, N, K, type, X, ldx, W, ldw, group, scale_type, scales, zeros, C, ldc, workspace=None,
+                workspace_bytes=0, stream=0) -> int:
     """Few 16-bit tokens times 4-bit integer weights with group scales (include/ptc.h)."""
-    return _check(lib().gemm_a16_s4(M, N, K, type, X, ldx, W, ldw, group, scale_type, scales, zeros, C, ldc, stream))
+    return _check(lib().gemm_a16_s4(M, N, K, type, X, ldx, W, ldw, group, scale_type, scales, zeros, C, ldc, workspace,
+                                    workspace_bytes, stream))
 
 
 def ptc_moe_a16_s4_workspace(tokens, hidden, inner, experts, top_k) -> int:
@@ -544,7 +554,7 @@ def _load_native():
     L = lib()
     n.init(*(ctypes.cast(getattr(L, f), _vp).value for f in ("ptc_dropout_to", "ptc_quantize_fp4",
                                                              "ptc_dequantize_fp4", "gemm_fp4", "gemm_a16_fp4",
-                                                             "gemm_a16_s4", "ptc_moe_a16_s4_workspace",
+                                                             "gemm_a16_s4_workspace", "gemm_a16_s4", "ptc_moe_a16_s4_workspace",
                                                              "ptc_moe_a16_s4", "ptc_rms_norm", "ptc_rms_norm_s8",
                                                              "ptc_rms_norm_backward_workspace",
                                                              "ptc_rms_norm_backward")),

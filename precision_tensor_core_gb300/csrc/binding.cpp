@@ -25,6 +25,7 @@ decltype(&ptc_quantize_fp4) f_quantize;
 decltype(&ptc_dequantize_fp4) f_dequantize;
 decltype(&gemm_fp4) f_gemm;
 decltype(&gemm_a16_fp4) f_gemm_a16;
+decltype(&gemm_a16_s4_workspace) f_gemm_a16_s4_workspace;
 decltype(&gemm_a16_s4) f_gemm_a16_s4;
 decltype(&ptc_moe_a16_s4_workspace) f_moe_workspace;
 decltype(&ptc_moe_a16_s4) f_moe;
@@ -534,9 +535,12 @@ PyObject *py_matmul_a16_s4(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Target target(W.index, a[3]);
     at::Tensor c = result(a[2], rx.rows, W.rows, x.scalar_type(), W.index, W.device);
     const Rows rc = rows_of(c, "out");
+    const int64_t bytes = f_gemm_a16_s4_workspace(rx.rows, W.k);
+    at::Tensor ws;
+    if (bytes > 0) ws = empty({bytes}, at::kByte, W.device);
     target.run([&](void *s) {
         return f_gemm_a16_s4(rx.rows, W.rows, W.k, type, rx.p, rx.ld, W.codes, W.pitch, W.group, W.type, W.scales, W.zeros,
-                             rc.p, rc.ld, s);
+                             rc.p, rc.ld, bytes > 0 ? ws.data_ptr() : nullptr, bytes, s);
     });
     target.used(a[0]);
     target.used(a[1]);
@@ -736,16 +740,17 @@ PyObject *py_check_s4(PyObject *, PyObject *const *a, Py_ssize_t n) {
     PTC_BODY_END
 }
 
-// (addresses of the twelve C entry points, status check, stream handle, Fp4Matrix, S4Matrix)
+// (addresses of the thirteen C entry points, status check, stream handle, Fp4Matrix, S4Matrix)
 PyObject *py_init(PyObject *, PyObject *const *a, Py_ssize_t n) {
     PTC_BODY_BEGIN
-    expect(n, 16);
+    expect(n, 17);
     auto entry = [&](auto &f) { f = reinterpret_cast<std::decay_t<decltype(f)>>(uintptr_t(seed64(*a++))); };
     entry(f_dropout);
     entry(f_quantize);
     entry(f_dequantize);
     entry(f_gemm);
     entry(f_gemm_a16);
+    entry(f_gemm_a16_s4_workspace);
     entry(f_gemm_a16_s4);
     entry(f_moe_workspace);
     entry(f_moe);

@@ -33,8 +33,8 @@
 namespace ptc {
 namespace {
 
-constexpr int kWarps4 = 8, kThreads4 = 32 * kWarps4;
-__host__ __device__ constexpr int ring_of(int mt) { return mt == 1 ? 3 : 2; }  // stages of a warp's ring
+constexpr int kWarps4 = 16, kThreads4 = 32 * kWarps4, kShares4Log2 = 4;
+constexpr int kRing4 = 2;  // stages of a warp's ring
 
 __device__ uint32_t g_s4_error = 0;
 
@@ -55,18 +55,44 @@ struct S4Args {
     int xvec, bf16_scales;
     int ring_bytes;      // of all warps
     int sums_at;
+    // Operands made by s4_operands_kernel: [token][stage][512 bytes], and factors and sums
+    // [tile of tokens][block][token]; NULL: every CTA makes its own.
+    uint8_t *xs;
+    float2 *xps;
     int stall;           // test hook: this CTA's weights never arrive (-1: none)
     uint64_t wait_limit;
 };
 
 struct S4Tail {
-    uint64_t full[kWarps4][4];
+    uint64_t full[kWarps4][kRing4], operands[2];
     AbortState abort;
 };
 
+// The tokens' operands, once for all CTAs (whole stages, zeros past K): 4 UNIT lanes a block.
+// With more than a few tokens making them in every CTA costs as much as the products.
+template <typename X, int UNIT>
+__global__ void __launch_bounds__(256) s4_operands_kernel(const S4Args a, int tok_tile) {
+    constexpr int LANES = 4 * UNIT, PER = 32 / LANES, BLOCKS = 4 / UNIT;
+    griddep_wait();
+    griddep_launch_dependents();  // (after the wait: what runs before this kernel is done when the product starts)
+    const int lane = threadIdx.x % 32, part = lane % LANES;
+    const int blocks = a.stages * 2 * BLOCKS, rounds = (blocks + PER - 1) / PER;
+    for (int64_t u = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) / 32; u < int64_t(rounds) * a.M; u += int64_t(gridDim.x) * 8) {
+        const int tok = int(u / rounds), blk = int(u - int64_t(tok) * rounds) * PER + lane / LANES;
+        const int k = blk * (32 * UNIT) + part * 8, have = max(0, min(8, a.K - k));
+        const X *p = static_cast<const X *>(a.x) + (have > 0 ? int64_t(tok) * a.ldx + k : 0);
+        float2 ps;
+        const uint4 op = s4_operands<UNIT, X>(load8(p, have, a.xvec != 0).v[0], ps);
+        if (blk >= blocks) continue;
+        const int hf = blk / BLOCKS, g = blk % BLOCKS;
+        *reinterpret_cast<uint4 *>(a.xs + (int64_t(tok) * a.stages * 2 + hf) * kS4XBytes + s4_x_piece<UNIT>(g * LANES + part)) = op;
+        if (part == 0) a.xps[(int64_t(tok / tok_tile) * blocks + blk) * tok_tile + tok % tok_tile] = ps;
+    }
+}
+
 template <typename X, int MT, int NT, int UNIT>
-__global__ void __launch_bounds__(kThreads4, MT == 1 ? 3 : 2) s4_kernel(const __grid_constant__ CUtensorMap tm, const S4Args a) {
-    constexpr int TOK = 8 * NT, BLOCKS = 4 / UNIT, D = ring_of(MT), CODES = MT * kS4TileBytes;
+__global__ void __launch_bounds__(kThreads4, 1) s4_kernel(const __grid_constant__ CUtensorMap tm, const S4Args a) {
+    constexpr int TOK = 8 * NT, BLOCKS = 4 / UNIT, D = kRing4, CODES = MT * kS4TileBytes;
     constexpr int SCALES = 2 * BLOCKS * 32;  // bytes of a tile's scales in a stage: two halves' groups
     extern __shared__ uint8_t smem4_raw[];
     uint8_t *const smem4 = smem4_raw + ((1024u - (smem_u32(smem4_raw) & 1023u)) & 1023u);
@@ -94,12 +120,13 @@ __global__ void __launch_bounds__(kThreads4, MT == 1 ? 3 : 2) s4_kernel(const __
     if (lane == 0)
         for (int i = 0; i < D; ++i) mbar_init(&st4.full[warp][i], 1);
     if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) mbar_init(&st4.operands[i], 1);
         st4.abort.flag = 0;
         tma_prefetch_desc(&tm);
     }
     fence_barrier_init();
-    griddep_wait();
-    griddep_launch_dependents();
+    // (After s4_operands_kernel the weights may be read before it is done: see there.)
+    if (a.xs == nullptr) griddep_wait();
 
     // Lane 0 brings this warp's stages c0 + share, + S, ... of tile after tile: the codes of
     // its rows (zeros past the matrix) and its tiles' scales and zeros.
@@ -134,6 +161,8 @@ __global__ void __launch_bounds__(kThreads4, MT == 1 ? 3 : 2) s4_kernel(const __
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < D; ++i) issue();
+    if (a.xs != nullptr) griddep_wait();
+    griddep_launch_dependents();
 
     // Activations of chunk c to the buffer of the place-th chunk: 4 UNIT lanes a block, a warp 32 / (4 UNIT),
     // four loads in flight per lane.
@@ -141,7 +170,21 @@ __global__ void __launch_bounds__(kThreads4, MT == 1 ? 3 : 2) s4_kernel(const __
     auto load_x = [&](int c, int place) {
         constexpr int LANES = 4 * UNIT, PER = 32 / LANES;
         const uint32_t buf = xs_base + (a.buffers == 2 && (place & 1) ? buf_bytes : 0u);
-        const int first = c0 + c * a.chunk, blocks = min(2 * min(a.chunk, c1 - first), a.halves - 2 * first) * BLOCKS;
+        const int first = c0 + c * a.chunk;
+        if (a.xs != nullptr) {  // a copy per token, and one of the factors and sums
+            if (threadIdx.x == 0) {
+                const int n = min(a.chunk, c1 - first);
+                uint64_t *bar = &st4.operands[place & 1];
+                const uint32_t bytes = uint32_t(n) * (2 * kS4XBytes), sums = uint32_t(n) * (2 * BLOCKS * TOK * 8), to = smem_u32(smem4) + buf;
+                fence_proxy_async_all();  // (what was read there before)
+                mbar_arrive_expect_tx(bar, bytes * uint32_t(ntok) + sums);
+                for (int j = 0; j < ntok; ++j)
+                    bulk_copy(to + uint32_t(j) * tok_bytes, a.xs + (int64_t(tok0 + j) * a.stages + first) * (2 * kS4XBytes), bytes, bar);
+                bulk_copy(to + ps_at, a.xps + (int64_t(blockIdx.y) * a.stages + first) * (2 * BLOCKS * TOK), sums, bar);
+            }
+            return;
+        }
+        const int blocks = min(2 * min(a.chunk, c1 - first), a.halves - 2 * first) * BLOCKS;
         const int part = lane % LANES, k0 = first * kS4Stage + part * 8;
         const int rounds = (blocks + PER - 1) / PER, all = rounds * ntok;
         for (int u0 = warp; u0 < all; u0 += 4 * kWarps4) {
@@ -184,10 +227,9 @@ __global__ void __launch_bounds__(kThreads4, MT == 1 ? 3 : 2) s4_kernel(const __
     int from = 0;  // place in the ring
     uint32_t parity = 0;
     bool ok = true;
-    // Sums [warp][row][token], of this tile and the one before: written, joined after one
-    // synchronisation, and written again after the next.
+    // Sums [warp][row][token].
     float *sums = reinterpret_cast<float *>(smem4 + a.sums_at);
-    for (int tile = tile0, flip = 0; tile < tiles; tile += tile_step, flip ^= 1) {
+    for (int tile = tile0; tile < tiles; tile += tile_step) {
         float tot[MT][NT][4];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -202,6 +244,9 @@ __global__ void __launch_bounds__(kThreads4, MT == 1 ? 3 : 2) s4_kernel(const __
                 if (!last || tile + tile_step < tiles) load_x(last ? 0 : c + 1, chunks_done + 1);
             }
             const uint32_t buf = xs_base + (a.buffers == 2 && (chunks_done & 1) ? buf_bytes : 0u);
+            if (a.xs != nullptr && (a.buffers == 2 || tile == tile0))
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&st4.operands[chunks_done & 1], uint32_t(chunks_done >> 1) & 1u, &st4.abort,
+                                                       &g_s4_error, a.wait_limit)) && ok;
             ++chunks_done;
             const int first = c0 + c * a.chunk, end = min(c1, first + a.chunk);
             for (; ok && st < end; st += S) {
@@ -236,7 +281,7 @@ __global__ void __launch_bounds__(kThreads4, MT == 1 ? 3 : 2) s4_kernel(const __
             }
         }
         // Added over the shares and then over the cluster's ranks, both in order.
-        float *part = sums + flip * (kWarps4 * 16 * MT * TOK) + warp * (16 * MT * TOK);
+        float *part = sums + warp * (16 * MT * TOK);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -249,7 +294,7 @@ __global__ void __launch_bounds__(kThreads4, MT == 1 ? 3 : 2) s4_kernel(const __
             cluster_sync();
         else
             __syncthreads();
-        const uint32_t base = smem_u32(sums + flip * (kWarps4 * 16 * MT * TOK));
+        const uint32_t base = smem_u32(sums);
         for (int o = krank * kThreads4 + int(threadIdx.x); o < tile_rows * TOK; o += a.ks * kThreads4) {
             const int tk = o / tile_rows, r = o - tk * tile_rows, w = r / (16 * MT), lr = r % (16 * MT);
             if (tk >= ntok) break;
@@ -264,19 +309,27 @@ __global__ void __launch_bounds__(kThreads4, MT == 1 ? 3 : 2) s4_kernel(const __
             const int row = tile * tile_rows + r;
             if (row < a.N) static_cast<X *>(a.C)[int64_t(tok0 + tk) * a.ldc + row] = from_float<X>(__fmul_rn(v, kS4Out));
         }
+        if (tile + tile_step < tiles || a.ks > 1) {  // (the sums are read)
+            if (a.ks > 1)
+                cluster_sync();
+            else
+                __syncthreads();
+        }
     }
     // After an abort copies in flight land before the CTA exits.
+    if (st4.abort.flag && a.xs != nullptr && chunks_done > 0)
+        mbar_wait(&st4.operands[(chunks_done - 1) & 1], uint32_t((chunks_done - 1) >> 1) & 1u, nullptr, nullptr, a.wait_limit);
     if (int(blockIdx.x) != a.stall)
         for (; taken < asked; ++taken)
             mbar_wait(&st4.full[warp][taken % D], uint32_t(taken / D) & 1u, nullptr, nullptr, a.wait_limit);
-    if (a.ks > 1) cluster_sync();  // (the sums are read)
 }
 
 // ------------------------------------------------------------ host side
 constexpr int64_t kMaxDim4 = int64_t(1) << 30;
 constexpr int64_t kMaxLd4 = int64_t(1) << 36;
 constexpr int kMaxDev4 = 64;
-std::atomic<int> g_s4_rows{0};   // "s4_tokens_rows": 0 by size, 1, 2, 4, 8
+constexpr int64_t kAlone4 = 2;  // up to so many tokens every CTA makes their operands itself
+std::atomic<int> g_s4_rows{0};   // "s4_tokens_rows": 0 by size, 1, 2, 4, 8, 16
 std::atomic<int> g_s4_split{0};  // "s4_tokens_split": 0 by size, 1, 2, 4, 8
 std::atomic<int> g_s4_tiles{0};  // "s4_tokens_tiles": 0 by size, 1, 2
 
@@ -293,21 +346,22 @@ struct S4Shape {
 
 // Bytes of all warps' rings: codes, scales, zeros.
 int ring_bytes4(int mt, int blocks, const void *zeros) {
-    return kWarps4 * ring_of(mt) * mt * (kS4TileBytes + 2 * blocks * 32 * (zeros ? 2 : 1));
+    return kWarps4 * kRing4 * mt * (kS4TileBytes + 2 * blocks * 32 * (zeros ? 2 : 1));
 }
 
 // Shared memory of a shape; false where a buffer does not hold a stage of every share.
 bool fit_s4(S4Shape &sh, const S4Args &a, int blocks, int toks, int tok, int64_t ctas, int sms) {
-    const int S = kWarps4 >> sh.r_log2, ring = ring_bytes4(sh.mt, blocks, a.zeros), sums = 2 * kWarps4 * 16 * sh.mt * tok * 4;
+    const int S = kWarps4 >> sh.r_log2, ring = ring_bytes4(sh.mt, blocks, a.zeros), sums = kWarps4 * 16 * sh.mt * tok * 4;
     const int per_stage = 2 * (toks * kS4XBytes + blocks * tok * 8), more = toks * 64;
     const int range = (a.stages + sh.ks - 1) / sh.ks;  // the longest of a CTA
     // As many CTAs per SM as hold the whole range; one whose buffers are as large as can be where none does.
     sh.chunk = 0;
-    for (int per_sm = int(std::min<int64_t>(sh.mt == 1 ? 3 : 2, (ctas + sms - 1) / sms)); per_sm >= 1; --per_sm) {
+    for (int per_sm = int(std::min<int64_t>(1, (ctas + sms - 1) / sms)); per_sm >= 1; --per_sm) {
         const int most = std::min(kSmem4 - 2048, kSmemSm / per_sm - 3072) / 256 * 256 - ring - sums;  // (alignment, barriers, the system's 1 KB)
         sh.buffers = range * per_stage + more <= most ? 1 : 2;
         if (sh.buffers == 2 && per_sm > 1) continue;
-        sh.chunk = sh.buffers == 1 ? range : (most / 2 - more) / per_stage / S * S;
+        sh.chunk = sh.buffers == 1 ? range : (most / 2 - more) / per_stage;
+        if (sh.buffers == 2 && sh.chunk > S) sh.chunk = sh.chunk / S * S;  // (whole rounds of the shares)
         sh.sums_at = ring + sh.buffers * (sh.chunk * per_stage + more);
         sh.smem = size_t(sh.sums_at + sums);
         sh.per_sm = per_sm;
@@ -324,10 +378,10 @@ S4Shape choose_s4(const S4Args &a, int unit, int sms) {
     int64_t cost_best = INT64_MAX;
     for (bool any : {false, true}) {
         for (int mt = 1; mt <= 2; ++mt)
-            for (int r = 0; r <= 3; ++r)
+            for (int r = 0; r <= kShares4Log2; ++r)
                 for (int k = 1; k <= 8; k *= 2) {
-                    const int S = 8 >> r;
-                    if (stages < S * k && (r < 3 || k > 1)) continue;
+                    const int S = kWarps4 >> r;
+                    if (stages < S * k && (r < kShares4Log2 || k > 1)) continue;
                     if (!any && ((rows && rows != 1 << r) || (split && split != k) || (tiles && tiles != mt))) continue;
                     const int64_t per = int64_t(16) * mt << r, ctas = (N + per - 1) / per * k * chunks;
                     S4Shape sh{mt, r, k, 0, 0, 0, 0, 0};
@@ -394,6 +448,25 @@ int launch_s4(S4Args a, const void *codes, int64_t pitch, const S4Shape &sh, int
     CUtensorMap tm;
     const int rc = encode_tmap_2d(&tm, true, codes, uint64_t(a.K + 1) / 2, uint64_t(a.N), uint64_t(pitch), kS4RowBytes, 16 * MT);
     if (rc) return rc;
+    if (a.xs) {
+        cudaLaunchConfig_t first = cfg;  // (no cluster)
+        cudaLaunchAttribute alone[1];
+        std::memset(alone, 0, sizeof(alone));
+        const int64_t warps = (int64_t(a.stages) * 2 * BLOCKS * a.M + 8 / UNIT - 1) / (8 / UNIT);
+        first.gridDim = dim3(unsigned(std::min<int64_t>((warps + 7) / 8, 4 * int64_t(sms))), 1, 1);
+        first.blockDim = dim3(256, 1, 1);
+        first.dynamicSmemBytes = 0;
+        first.attrs = alone;
+        first.numAttrs = 0;
+        if (pdl_enabled()) {
+            alone[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            alone[0].val.programmaticStreamSerializationAllowed = 1;
+            first.numAttrs = 1;
+        }
+        e = cudaLaunchKernelEx(&first, s4_operands_kernel<X, UNIT>, a, TOK);
+        if (e != cudaSuccess) return fail_launch(e, "grouped 4-bit product launch");
+        note_launches(1);
+    }
     e = cudaLaunchKernelEx(&cfg, fn, tm, a);
     if (e != cudaSuccess) return fail_launch(e, "grouped 4-bit product launch");
     note_launches(1);
@@ -432,7 +505,7 @@ cudaError_t read_and_clear_s4_error_word(uint32_t *out) {
 
 bool set_s4_tuning(const char *key, int64_t v) {
     const bool power = v == 0 || v == 1 || v == 2 || v == 4 || v == 8;
-    if (std::strcmp(key, "s4_tokens_rows") == 0 && power)
+    if (std::strcmp(key, "s4_tokens_rows") == 0 && (power || v == 16))
         g_s4_rows.store(int(v));
     else if (std::strcmp(key, "s4_tokens_split") == 0 && power)
         g_s4_split.store(int(v));
@@ -458,9 +531,16 @@ int check_s4(const S4Weights &w) {
 
 using namespace ptc;
 
+// Operands of every token, and factors and sums of whole tiles of tokens, eight per stage at most.
+extern "C" int64_t gemm_a16_s4_workspace(int64_t M, int64_t K) {
+    if (M <= kAlone4 || K <= 0 || M > 65535 * 16 || K > kMaxDim4) return 0;
+    const int64_t stages = (K + kS4Stage - 1) / kS4Stage, tile = M > 8 ? 16 : 8;
+    return M * stages * (2 * kS4XBytes) + (M + tile - 1) / tile * tile * stages * 8 * 8;
+}
+
 extern "C" int gemm_a16_s4(int64_t M, int64_t N, int64_t K, int type, const void *X, int64_t ldx, const void *W, int64_t ldw,
                            int64_t group, int scale_type, const void *scales, const void *zeros, void *C, int64_t ldc,
-                           void *stream) {
+                           void *workspace, int64_t workspace_bytes, void *stream) {
     set_message("");
     if (M < 0 || N < 0 || K < 0 || M > kMaxDim4 || N > kMaxDim4 || K > kMaxDim4)
         return fail_status(PTC_ERR_INVALID, "sizes must satisfy 0 <= M, N, K <= 2^30");
@@ -481,6 +561,15 @@ extern "C" int gemm_a16_s4(int64_t M, int64_t N, int64_t K, int type, const void
     if (K > 0 && (rows_overlap(c, elem_rows(X, M, K, ldx, 2)) || rows_overlap(c, elem_rows(W, N, (K + 1) / 2, ldw, 1)) ||
                   rows_overlap(c, flat_bytes(scales, w.scale_bytes())) || rows_overlap(c, flat_bytes(zeros, w.scale_bytes()))))
         return fail_status(PTC_ERR_OVERLAP, "C overlaps an operand");
+    const int64_t need = gemm_a16_s4_workspace(M, K);
+    if (workspace && need > 0) {
+        if (workspace_bytes < need) return fail_status(PTC_ERR_INVALID, "the workspace is too small");
+        if (!at_multiple(workspace, 16)) return fail_status(PTC_ERR_ALIGN, "the workspace must be 16-byte aligned");
+        const ByteRows b = flat_bytes(workspace, uint64_t(need));
+        if (rows_overlap(b, c) || rows_overlap(b, elem_rows(X, M, K, ldx, 2)) || rows_overlap(b, elem_rows(W, N, (K + 1) / 2, ldw, 1)) ||
+            rows_overlap(b, flat_bytes(scales, w.scale_bytes())) || rows_overlap(b, flat_bytes(zeros, w.scale_bytes())))
+            return fail_status(PTC_ERR_OVERLAP, "the workspace overlaps another argument");
+    }
     int sms;
     if ((rc = usable_device(&sms))) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -509,5 +598,9 @@ extern "C" int gemm_a16_s4(int64_t M, int64_t N, int64_t K, int type, const void
     a.wait_limit = wait_limit_ns();
     a.xvec = at_multiple(X, 16) && (M == 1 || ldx % 8 == 0);
     a.bf16_scales = scale_type == PTC_OUT_BF16;
+    if (workspace && need > 0) {
+        a.xs = static_cast<uint8_t *>(workspace);
+        a.xps = reinterpret_cast<float2 *>(a.xs + M * a.stages * (2 * kS4XBytes));
+    }
     return type == PTC_OUT_BF16 ? run_s4<__nv_bfloat16>(a, W, ldw, group, sms, s) : run_s4<__half>(a, W, ldw, group, sms, s);
 }

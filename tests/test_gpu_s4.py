@@ -41,23 +41,23 @@ def test_scales_of_the_other_type(xt, st):
     check(ptc.matmul_a16_s4(x, matrix(w)), x, w, xt)
 
 
-SHAPES = list(itertools.product([1, 2, 4, 8], [1, 2, 4, 8], [1, 2]))
+SHAPES = list(itertools.product([1, 2, 4, 8, 16], [1, 2, 4, 8], [1, 2]))
 
 
 @pytest.mark.parametrize("rows, split, tiles", SHAPES)
 @pytest.mark.parametrize("group", [32, 128])
 def test_every_launch_shape(rows, split, tiles, group):
-    """K of 64 stages and a part: every share has its stages.  The shape is the one asked for where its
-    activations fit, up to seven tokens in all of them."""
-    N, K = 200, 16500
+    """K of 128 stages and a part: every share has its stages.  The shape is the one asked for where its
+    activations fit, up to four tokens in all of them."""
+    N, K = 200, 33000
     w = weights(3, (), N, K, group, True, HF)
-    for M in (1, 7, 16):
+    for M in (1, 4, 16):
         x = rand(4, M, K, dtype=HF)
         for k, v in (("rows", rows), ("split", split), ("tiles", tiles)):
             ptc.ptc_set_tuning("s4_tokens_" + k, v)
         got = ptc.matmul_a16_s4(x, matrix(w))
         grid, cluster, ks, tile = ptc.ptc_last_fp4_launch()
-        if M <= 7:
+        if M <= 4:
             assert (cluster, ks, tile) == (split, split, 16 * rows * tiles) and grid == -(-N // tile) * split
         check(got, x, w, HF)
     for k in ("rows", "split", "tiles"):
@@ -84,6 +84,19 @@ def test_many_row_tiles_per_cta(rows, split, tiles, M, K, group):
     for k in ("rows", "split", "tiles"):
         ptc.ptc_set_tuning("s4_tokens_" + k, 0)
     check(got, x, w, BF)
+
+
+@pytest.mark.parametrize("M, N, K", [(3, 500, 2090), (16, 2000, 4096), (16, 64, 40000), (23, 300, 900)])
+def test_without_workspace(M, N, K):
+    """Every CTA making the operands itself gives the same bits."""
+    w = weights(34, (), N, K, 64, True, HF)
+    x, m = rand(35, M, K, dtype=HF), matrix(w)
+    want = ptc.matmul_a16_s4(x, m)
+    got = torch.empty_like(want)
+    assert ptc.gemm_a16_s4_workspace(M, K) > 0 and ptc.gemm_a16_s4_workspace(2, K) == 0
+    ptc.gemm_a16_s4(M, N, K, ptc.PTC_OUT_F16, x.data_ptr(), K, m.codes.data_ptr(), m.codes.stride(0), 64, ptc.PTC_OUT_F16,
+                    m.scales.data_ptr(), m.zeros.data_ptr(), got.data_ptr(), N, stream=torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(got, want)
 
 
 def test_codes_one_by_one():

@@ -18,8 +18,8 @@ def L():
 
 
 def product(L, M=4, N=40, K=200, type=1, X=BASE, ldx=200, W=BASE + GB, ldw=112, group=64, st=1, scales=BASE + 2 * GB,
-            zeros=None, C=BASE + 4 * GB, ldc=40):
-    return L.gemm_a16_s4(M, N, K, type, X, ldx, W, ldw, group, st, scales, zeros, C, ldc, None)
+            zeros=None, C=BASE + 4 * GB, ldc=40, ws=None, bytes=0):
+    return L.gemm_a16_s4(M, N, K, type, X, ldx, W, ldw, group, st, scales, zeros, C, ldc, ws, bytes, None)
 
 
 @no_gpu
@@ -34,6 +34,9 @@ def product(L, M=4, N=40, K=200, type=1, X=BASE, ldx=200, W=BASE + GB, ldw=112, 
     (dict(C=BASE), OVERLAP), (dict(C=BASE + GB + 64), OVERLAP), (dict(C=BASE + 2 * GB + 3 * 4 * 32 - 2), OVERLAP),
     (dict(C=BASE + 2 * GB + 3 * 4 * 32), DEVICE), (dict(C=BASE + 3 * GB, zeros=BASE + 3 * GB), OVERLAP),
     (dict(K=0, X=None, W=None, scales=None), DEVICE), (dict(C=BASE + 400, ldx=240, ldc=240), DEVICE),
+    (dict(ws=BASE + 5 * GB, bytes=4 * 512 + 8 * 64), DEVICE), (dict(ws=BASE + 5 * GB, bytes=4 * 512 + 8 * 64 - 1), INVALID),
+    (dict(ws=BASE + 5 * GB + 8, bytes=1 << 20), ALIGN), (dict(ws=BASE, bytes=1 << 20), OVERLAP), (dict(ws=BASE + 4 * GB, bytes=1 << 20), OVERLAP),
+    (dict(M=2, ws=BASE + 8, bytes=0), DEVICE),  # (not used)
 ])
 def test_statuses(L, change, status):
     assert product(L, **change) == status
@@ -62,6 +65,7 @@ def test_host_tensors_are_refused():
 
 
 def test_keys(L):
+    assert [L.ptc_set_tuning(b"s4_tokens_rows", v) for v in (16, 0)] == [0, 0] and L.ptc_set_tuning(b"s4_tokens_split", 16) == INVALID
     for key in (b"s4_tokens_rows", b"s4_tokens_split"):
         assert [L.ptc_set_tuning(key, v) for v in (1, 2, 4, 8, 0)] == [0] * 5
         assert L.ptc_set_tuning(key, 3) == INVALID and L.ptc_set_tuning(key, -1) == INVALID
