@@ -294,19 +294,29 @@ __global__ void __launch_bounds__(kThreads4, 1) s4_kernel(const __grid_constant_
             cluster_sync();
         else
             __syncthreads();
+        // (Rows of a tile and of a row group are powers of two.)
+        constexpr int GROUP_LOG2 = MT == 1 ? 4 : 5;
+        const int rows_log2 = a.r_log2 + GROUP_LOG2, outs = ntok << rows_log2;
+        const int from_share = (16 * MT * TOK) << a.r_log2;  // from a share's sums to the next one's
         const uint32_t base = smem_u32(sums);
-        for (int o = krank * kThreads4 + int(threadIdx.x); o < tile_rows * TOK; o += a.ks * kThreads4) {
-            const int tk = o / tile_rows, r = o - tk * tile_rows, w = r / (16 * MT), lr = r % (16 * MT);
-            if (tk >= ntok) break;
+        for (int o = krank * kThreads4 + int(threadIdx.x); o < outs; o += a.ks * kThreads4) {
+            const int tk = o >> rows_log2, r = o & ((1 << rows_log2) - 1), row = tile * tile_rows + r;
+            const int at = (r >> GROUP_LOG2) * (16 * MT * TOK) + (r & (16 * MT - 1)) * TOK + tk;
             float v = 0.0f;
-            for (int k = 0; k < a.ks; ++k)
-                for (int sh = 0; sh < S; ++sh) {
-                    const uint32_t at = base + uint32_t(((sh << a.r_log2) + w) * (16 * MT * TOK) + lr * TOK + tk) * 4u;
-                    float f;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(a.ks == 1 ? at : mapa_shared(at, uint32_t(k))) : "memory");
-                    v = __fadd_rn(v, f);
+            if (a.ks == 1) {
+#pragma unroll 4
+                for (int sh = 0; sh < S; ++sh) v = __fadd_rn(v, sums[at + sh * from_share]);
+            } else {
+                for (int k = 0; k < a.ks; ++k) {
+                    const uint32_t peer = mapa_shared(base + uint32_t(at) * 4u, uint32_t(k));
+#pragma unroll 4
+                    for (int sh = 0; sh < S; ++sh) {
+                        float f;
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(peer + uint32_t(sh * from_share) * 4u) : "memory");
+                        v = __fadd_rn(v, f);
+                    }
                 }
-            const int row = tile * tile_rows + r;
+            }
             if (row < a.N) static_cast<X *>(a.C)[int64_t(tok0 + tk) * a.ldc + row] = from_float<X>(__fmul_rn(v, kS4Out));
         }
         if (tile + tile_step < tiles || a.ks > 1) {  // (the sums are read)
@@ -333,7 +343,7 @@ std::atomic<int> g_s4_rows{0};   // "s4_tokens_rows": 0 by size, 1, 2, 4, 8, 16
 std::atomic<int> g_s4_split{0};  // "s4_tokens_split": 0 by size, 1, 2, 4, 8
 std::atomic<int> g_s4_tiles{0};  // "s4_tokens_tiles": 0 by size, 1, 2
 
-constexpr int kSmem4 = 227 * 1024, kSmemSm = 228 * 1024;  // of a CTA, of an SM
+constexpr int kSmem4 = 227 * 1024;
 
 // Rows and K shares of a launch, and how the activations are held.
 struct S4Shape {
@@ -341,7 +351,6 @@ struct S4Shape {
     int chunk, buffers;
     int sums_at;  // offset of the sums
     size_t smem;
-    int per_sm;   // CTAs that fit an SM
 };
 
 // Bytes of all warps' rings: codes, scales, zeros.
@@ -349,32 +358,35 @@ int ring_bytes4(int mt, int blocks, const void *zeros) {
     return kWarps4 * kRing4 * mt * (kS4TileBytes + 2 * blocks * 32 * (zeros ? 2 : 1));
 }
 
-// Shared memory of a shape; false where a buffer does not hold a stage of every share.
-bool fit_s4(S4Shape &sh, const S4Args &a, int blocks, int toks, int tok, int64_t ctas, int sms) {
+// Shared memory of a shape; false where a buffer does not hold a stage.
+bool fit_s4(S4Shape &sh, const S4Args &a, int blocks, int toks, int tok) {
     const int S = kWarps4 >> sh.r_log2, ring = ring_bytes4(sh.mt, blocks, a.zeros), sums = kWarps4 * 16 * sh.mt * tok * 4;
     const int per_stage = 2 * (toks * kS4XBytes + blocks * tok * 8), more = toks * 64;
     const int range = (a.stages + sh.ks - 1) / sh.ks;  // the longest of a CTA
-    // As many CTAs per SM as hold the whole range; one whose buffers are as large as can be where none does.
-    sh.chunk = 0;
-    for (int per_sm = int(std::min<int64_t>(1, (ctas + sms - 1) / sms)); per_sm >= 1; --per_sm) {
-        const int most = std::min(kSmem4 - 2048, kSmemSm / per_sm - 3072) / 256 * 256 - ring - sums;  // (alignment, barriers, the system's 1 KB)
-        sh.buffers = range * per_stage + more <= most ? 1 : 2;
-        if (sh.buffers == 2 && per_sm > 1) continue;
-        sh.chunk = sh.buffers == 1 ? range : (most / 2 - more) / per_stage;
-        if (sh.buffers == 2 && sh.chunk > S) sh.chunk = sh.chunk / S * S;  // (whole rounds of the shares)
-        sh.sums_at = ring + sh.buffers * (sh.chunk * per_stage + more);
-        sh.smem = size_t(sh.sums_at + sums);
-        sh.per_sm = per_sm;
-        break;
-    }
+    const int most = (kSmem4 - 2048) / 256 * 256 - ring - sums;  // (alignment, barriers)
+    sh.buffers = int64_t(range) * per_stage + more <= most ? 1 : 2;
+    sh.chunk = sh.buffers == 1 ? range : (most / 2 - more) / per_stage;
+    if (sh.buffers == 2 && sh.chunk > S) sh.chunk = sh.chunk / S * S;  // (whole rounds of the shares)
+    sh.sums_at = ring + sh.buffers * (sh.chunk * per_stage + more);
+    sh.smem = size_t(sh.sums_at + sums);
     return sh.chunk > 0;
 }
 
+// The shape of least estimated time, in units of 0.01 us.  A warp takes 1.1 us for a stage
+// of 16 rows and up to eight tokens, 1.4 for sixteen, 1.9 and 3.0 for 32 rows; an eighth
+// more with groups of 32, a tenth with 64.  A tile of rows takes 0.8 to 1.1 us more,
+// 2.0 for 16 rows and sixteen tokens, its sums over a cluster 1.6, clusters of four 0.8 to
+// start, of eight 2.0.  Operands that a CTA makes itself cost 0.03 us per stage and token, ones
+// that do not fit 1.1 per chunk and tile.  (Fitted to the times of every shape at 44 sizes
+// between 64 x 64 and 16384 x 8192 weights with 1 to 16 tokens; its choice takes 1.004
+// times the fastest shape's time there, 1.07 at most.)
+// The keys take a part of the shapes, all of them where that leaves none.
 S4Shape choose_s4(const S4Args &a, int unit, int sms) {
-    const int64_t N = a.N, chunks = (a.M + 15) / 16;
-    const int stages = a.stages, toks = std::min(a.M, 16), tok = a.M > 8 ? 16 : 8;
-    S4Shape best{1, 0, 1, 0, 0, 0, 0, 0};
+    const int64_t chunks = (a.M + 15) / 16;
+    const int stages = a.stages, toks = std::min(a.M, 16), nt = a.M > 8 ? 2 : 1;
+    S4Shape best{1, 0, 1, 0, 0, 0, 0};
     const int rows = g_s4_rows.load(), split = g_s4_split.load(), tiles = g_s4_tiles.load();
+    constexpr int kStage[2][2] = {{111, 139}, {188, 297}}, kTile4[2][2] = {{96, 203}, {84, 108}};
     int64_t cost_best = INT64_MAX;
     for (bool any : {false, true}) {
         for (int mt = 1; mt <= 2; ++mt)
@@ -383,14 +395,17 @@ S4Shape choose_s4(const S4Args &a, int unit, int sms) {
                     const int S = kWarps4 >> r;
                     if (stages < S * k && (r < kShares4Log2 || k > 1)) continue;
                     if (!any && ((rows && rows != 1 << r) || (split && split != k) || (tiles && tiles != mt))) continue;
-                    const int64_t per = int64_t(16) * mt << r, ctas = (N + per - 1) / per * k * chunks;
-                    S4Shape sh{mt, r, k, 0, 0, 0, 0, 0};
-                    if (!fit_s4(sh, a, 4 / unit, toks, tok, ctas, sms)) continue;
-                    const int64_t waves = (ctas + 2 * sms - 1) / (2 * sms);
-                    const int64_t st = (stages + S * k - 1) / (S * k);
-                    const int64_t start = k == 1 ? 220 : k == 2 ? 320 : k == 4 ? 400 : 600;
-                    const int64_t read = int64_t(toks) * stages / k * 3;
-                    const int64_t cost = waves * (start + st * (mt == 1 ? 30 : 50) * (toks > 8 ? 3 : 2) / 2 * (ctas > sms ? 17 : 10) / 10 + read);
+                    S4Shape sh{mt, r, k, 0, 0, 0, 0};
+                    if (!fit_s4(sh, a, 4 / unit, toks, 8 * nt)) continue;
+                    const int64_t per = int64_t(16) * mt << r, count = (a.N + per - 1) / per;
+                    const int64_t clusters = std::min<int64_t>(count, std::max(1, sms / k));
+                    const int64_t walk = (count + clusters - 1) / clusters * chunks;  // tiles of a CTA
+                    const int range = (stages + k - 1) / k;
+                    const int64_t stage = kStage[mt - 1][nt - 1] * (unit == 1 ? 113 : unit == 2 ? 109 : 100) / 100;
+                    int64_t tile = kTile4[mt - 1][nt - 1] + (range + S - 1) / S * stage + (k > 1 ? 156 : 0);
+                    if (sh.buffers == 2) tile += 111 * int64_t((range + sh.chunk - 1) / sh.chunk);
+                    const int64_t start = (k == 4 ? 84 : k == 8 ? 203 : 0) + (a.xs ? 0 : 3 * int64_t(toks) * range) + ((nt * mt) << r) * 8 / 5;
+                    const int64_t cost = start + walk * tile;
                     if (cost < cost_best) {
                         cost_best = cost;
                         best = sh;
@@ -423,7 +438,7 @@ int launch_s4(S4Args a, const void *codes, int64_t pitch, const S4Shape &sh, int
     const size_t smem = sh.smem + 1024;
     const int R = 1 << sh.r_log2;
     const int64_t per = int64_t(16) * MT * R, chunks = (a.M + TOK - 1) / TOK;
-    const int64_t blocks = std::min((a.N + per - 1) / per, std::max<int64_t>(1, int64_t(sms) * sh.per_sm / sh.ks)) * sh.ks;
+    const int64_t blocks = std::min((a.N + per - 1) / per, int64_t(std::max(1, sms / sh.ks))) * sh.ks;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
     std::memset(&cfg, 0, sizeof(cfg));
