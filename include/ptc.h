@@ -483,7 +483,8 @@ int gemm_a16_s4(int64_t M, int64_t N, int64_t K, int type, const void *X, int64_
  * another.  Y has X's type.  ids and weights ([tokens][top_k], or NULL) receive the chosen
  * experts and their p.  Sizes: hidden and inner 1 .. 2^20, experts up to 512, top_k up to 32.
  * Only the chosen experts' weights are read, once per eight of an expert's tokens.  Products and
- * activations as gemm_a16_s4; h is not rounded to 16 bits (22 bits are kept).  Results
+ * activations as gemm_a16_s4; of h 22 bits are kept, for bfloat16 X 11, and at least 2^-24
+ * of the largest of 128.  Results
  * are the same from call to call.  The workspace has at least
  * ptc_moe_a16_s4_workspace(...) bytes (0: the sizes are refused), 256-byte aligned, and is
  * no other call's until this one is done.

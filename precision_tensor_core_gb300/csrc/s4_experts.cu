@@ -39,6 +39,7 @@ constexpr int kMaxTokens = 64, kMaxExperts = 512, kMaxTopK = 32, kMaxPairs = 512
 constexpr int kTile = 8;  // tokens of an expert per item
 constexpr int kLogits = 4;  // tokens per CTA of the router
 constexpr int kRing = 2;  // stages of a warp's ring
+constexpr int kMaxParts4 = 2048;  // shares of all tiles of 16 rows of y, where they are shared
 
 __device__ uint32_t g_moe_error = 0;
 
@@ -62,7 +63,8 @@ struct MoeArgs {
     int h_halves, h_stages, h_blocks;  // of inner; blocks of 32
     int ring_bytes, scale_bytes;     // of all warps' codes; of a stage's scales and zeros
     // Workspace.
-    uint32_t *counters;   // tickets, items of the first kind that are done
+    uint32_t *counters;   // tickets, items of the first kind that are done; shares of 16 rows of y that are
+    float *parts;         // sums of shares of rows of y: [share][tile of rows][token][16]
     float *logits;        // [tokens][experts]
     uint8_t *xs;          // [token][stage] operands
     float2 *xps;          // [token][block] factors and sums
@@ -84,7 +86,8 @@ __global__ void __launch_bounds__(kMoeThreads) router_kernel(const MoeArgs a) {
     const int logits = (a.tokens + kLogits - 1) / kLogits * a.experts;  // CTAs
     if (int(blockIdx.x) >= logits) {
         const int first = int(blockIdx.x) - logits, ctas = int(gridDim.x) - logits;
-        if (first == 0 && threadIdx.x < 2) a.counters[threadIdx.x] = 0;
+        if (first == 0)
+            for (int i = threadIdx.x; i < 2 + kMaxParts4 / 2; i += kMoeThreads) a.counters[i] = 0;
         constexpr int LANES = 4 * UNIT, PER = 32 / LANES, GROUPS = 4 / UNIT;
         const int blocks = a.stages * 2 * GROUPS, rounds = (blocks + PER - 1) / PER, lane8 = lane % LANES;
         for (int u = first * kMoeWarps + warp; u < rounds * a.tokens; u += ctas * kMoeWarps) {
@@ -158,6 +161,7 @@ struct Routing {
     uint8_t tile_count[kMaxPairs];
     int tiles;
     uint32_t ticket[4];
+    bool last;  // of the shares of 16 rows of y
 };
 
 struct MoeTail {
@@ -172,11 +176,9 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ void route(const MoeArgs &a, Routing &r) {
+template <int PER>
+__device__ __forceinline__ void choose_experts(const MoeArgs &a, Routing &r) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    for (int i = threadIdx.x; i < a.experts; i += kMoeThreads) r.mask[i][0] = r.mask[i][1] = 0;
-    __syncthreads();
-    constexpr int PER = kMaxExperts / 32;
     for (int tok = warp; tok < a.tokens; tok += kMoeWarps) {
         const float *l = a.logits + int64_t(tok) * a.experts;
         float v[PER];
@@ -236,6 +238,18 @@ __device__ __forceinline__ void route(const MoeArgs &a, Routing &r) {
             }
         }
     }
+}
+
+__device__ __forceinline__ void route(const MoeArgs &a, Routing &r) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    for (int i = threadIdx.x; i < a.experts; i += kMoeThreads) r.mask[i][0] = r.mask[i][1] = 0;
+    __syncthreads();
+    if (a.experts <= 64)
+        choose_experts<2>(a, r);
+    else if (a.experts <= 128)
+        choose_experts<4>(a, r);
+    else
+        choose_experts<kMaxExperts / 32>(a, r);
     __syncthreads();
     if (warp == 0) {  // pairs and tiles of the experts, in order
         int pairs = 0, tiles = 0;
@@ -304,11 +318,19 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     constexpr int UP = SCALES;              // up's from the gate's
     constexpr int ZEROS = SCALES * (ODD ? 3 : 2);  // zeros from scales, of either kind
     constexpr int CODES = 2 * kS4TileBytes;
+    // Rows of y: with groups of 128 and more half a stage is one block, whose four blocks of
+    // 32 of h are brought to one power of two as they are loaded.
+    constexpr int UNIT_H = UNIT == 4 ? 4 : 1;
+    // h as one binary16 number where y is bfloat16 (2^-12 of an element, an eighth of y's own
+    // rounding: 1.01 times its error), two where it is binary16.
+    constexpr int PARTS = std::is_same_v<X, __half> ? 2 : 1;
     extern __shared__ uint8_t moe_raw[];
     uint8_t *const smem = moe_raw + ((1024u - (smem_u32(moe_raw) & 1023u)) & 1023u);
     __shared__ Routing r;
     __shared__ MoeTail st;
+    __shared__ __align__(16) float2 factors[kMoeWarps][2][32];  // of half a stage, [block][token]
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    float2 *const mine = &factors[warp][0][0];
     const int f = s4_pair_of(lane >> 2), gr = lane >> 2, t = lane & 3;
     const int half = warp & 1, share = warp >> 1;  // of rows of h
     const uint32_t ring = uint32_t(warp * kRing * CODES), scale_ring = uint32_t(a.ring_bytes + warp * kRing * a.scale_bytes);
@@ -326,7 +348,17 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     if (threadIdx.x == 0) r.ticket[0] = atomicAdd(a.counters, 1u);
     route(a, r);
 
-    const int first_items = r.tiles * a.h_blocks, items = first_items + (a.hidden + 15) / 16;
+    const int units = r.tiles * a.h_stages;  // stages of 16 rows of y, of all tiles of pairs
+    const int row_tiles = (a.hidden + 15) / 16;
+    // Shares of these stages that are items of their own: as many as keep every CTA busy
+    // once, where tiles are fewer than half the CTAs; otherwise for three rounds, so that none
+    // is left with one item more than the others for long (256 tiles on 304 CTAs, two of them in the hands
+    // of some: 172 us instead of XX).
+    int shares = 1;
+    while (shares < 8 && row_tiles * shares * 2 <= kMaxParts4 && units >= 16 * shares &&
+           (2 * row_tiles <= int(gridDim.x) ? row_tiles * shares * 2 <= int(gridDim.x) : row_tiles * shares < 3 * int(gridDim.x)))
+        shares *= 2;
+    const int first_items = r.tiles * a.h_blocks, items = first_items + row_tiles * shares;
     // With many items per CTA tickets are taken two items ahead, so that the next item's weights
     // are asked for before this one's end; with few that would leave CTAs without, and they are
     // taken when the item before begins.
@@ -335,8 +367,12 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
         if (threadIdx.x == 0) r.ticket[1] = atomicAdd(a.counters, 1u);
         __syncthreads();
     }
-    const int units = r.tiles * a.h_stages;  // stages of all tiles' rows of y, shared by the warps
-    const int u0 = int(int64_t(units) * warp / kMoeWarps), u1 = int(int64_t(units) * (warp + 1) / kMoeWarps);
+    // This warp's of a share.
+    auto units_of = [&](int part, int &u0, int &u1) {
+        const int first = int(int64_t(units) * part / shares), n = int(int64_t(units) * (part + 1) / shares) - first;
+        u0 = first + n * warp / kMoeWarps;
+        u1 = first + n * (warp + 1) / kMoeWarps;
+    };
     auto ticket = [&](int round) { return int(r.ticket[round & 3]); };
     // The stages of the item of a round; none past the last item.
     auto begin = [&](int round) {
@@ -348,8 +384,10 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
             b.st = share;
             b.left = (a.stages - share + 3) / 4;  // share, share + 4, ...
         } else if (item < items) {
+            int u0, u1;
+            units_of((item - first_items) / row_tiles, u0, u1);
             b.second_kind = 1;
-            b.row = (item - first_items) * 16;
+            b.row = (item - first_items) % row_tiles * 16;
             b.tile = u0 / a.h_stages;
             b.st = u0 - b.tile * a.h_stages;
             b.left = u1 - u0;
@@ -443,37 +481,37 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
             for (int m = 0; m < 2; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) tot[m][0][i] = 0.0f;
+            // Operands and factors of half a stage ahead: 16 bytes per pair of MMAs of this lane's
+            // token, and an entry of the warp's [block][token].
             const uint8_t *const xs = a.xs + int64_t(r.pair_token[pair0 + min(gr, n - 1)]) * a.stages * (2 * kS4XBytes) + t * 16;
-            const float2 *const ps0 = a.xps + int64_t(r.pair_token[pair0 + min(2 * t, n - 1)]) * a.stages * (2 * SG);
-            const float2 *const ps1 = a.xps + int64_t(r.pair_token[pair0 + min(2 * t + 1, n - 1)]) * a.stages * (2 * SG);
+            const float2 *const ps = a.xps + int64_t(r.pair_token[pair0 + min(lane & 7, n - 1)]) * a.stages * (2 * SG) + min(lane >> 3, SG - 1);
+            uint4 x[2][4];
+            float2 p[2];
+            auto load = [&](int hf, int at) {  // (the workspace holds whole stages)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[at][i] = *reinterpret_cast<const uint4 *>(xs + hf * kS4XBytes + i * 64);
+                p[at] = ps[hf * SG];
+            };
+            if (share < a.stages) load(2 * share, 0);
             for (int s = share; s < a.stages && ok; s += 4) {
-                uint4 x[2][4];
-                float2 p[2][SG][2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[h][i] = *reinterpret_cast<const uint4 *>(xs + (2 * s + h) * kS4XBytes + i * 64);
-                    if constexpr (SG == 1) {
-                        p[h][0][0] = ps0[2 * s + h];
-                        p[h][0][1] = ps1[2 * s + h];
-                    }
-                }
                 int from;
                 if (!arrived(from)) break;
                 const uint32_t more = second_half(s);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
+                    if (h == 0)
+                        load(2 * s + 1, 1);
+                    else if (s + 4 < a.stages)
+                        load(2 * (s + 4), 0);
                     if (2 * s + h < a.halves) {
+                        if (lane < 8 * SG) mine[h * 32 + lane] = p[h];
+                        __syncwarp();
                         const uint32_t at = scale_ring + uint32_t(from * a.scale_bytes) + uint32_t(h) * more;
                         const uint32_t scales[2] = {at + row_at[0], at + row_at[1]};
                         s4_half_stage<2, 1, UNIT, SG, 1, ODD>(
                             tot, smem, (ring + uint32_t(from) * CODES + s4_code_at<UNIT>(lane)) ^ (uint32_t(h) << 6), scales, row_more,
                             32u, a.gate_up.zeros ? ZEROS : 0u, a.bf16_scales != 0, [&](int i, int, int) { return x[h][i]; },
-                            [&](int g, int) {
-                                const float2 u = SG == 1 ? p[h][0][0] : ps0[(2 * s + h) * SG + g];
-                                const float2 v = SG == 1 ? p[h][0][1] : ps1[(2 * s + h) * SG + g];
-                                return make_float4(u.x, u.y, v.x, v.y);
-                            },
+                            [&](int g, int) { return *reinterpret_cast<const float4 *>(mine + h * 32 + g * 8 + 2 * t); },
                             (a.hidden - (2 * s + h) * kS4Half + 32 * UNIT - 1) / (32 * UNIT));
                     }
                 }
@@ -506,10 +544,10 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                 s4_operand32(h, lane, hi, lo, ps);
                 const int64_t pair = pair0 + warp;
                 // [pair][stage][high parts of 256, low parts]
-                __half *p = reinterpret_cast<__half *>(a.hs + (pair * a.h_stages + ib / 8) * (4 * kS4XBytes)) + (ib & 7) * 32 +
-                            (lane >> 3) * 8 + s4_half(lane & 7);
-                p[0] = hi;
-                p[kS4XBytes] = lo;
+                uint8_t *p = a.hs + (pair * a.h_stages + ib / 8) * (4 * kS4XBytes) + ((ib >> 2) & 1) * kS4XBytes +
+                             s4_x_piece<UNIT_H>((ib & 3) * 4 + (lane >> 3)) + s4_half(lane & 7) * 2;
+                *reinterpret_cast<__half *>(p) = hi;
+                if (PARTS == 2) *reinterpret_cast<__half *>(p + 2 * kS4XBytes) = lo;
                 if (lane == 0) a.hps[pair * a.h_stages * 8 + ib] = ps;
             }
             __threadfence();
@@ -525,41 +563,73 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                 ready = true;
             }
             if (threadIdx.x == 0 && !early) r.ticket[later] = atomicAdd(a.counters, 1u);
-            const int row0 = (item - first_items) * 16;
+            const int part = (item - first_items) / row_tiles, row_tile = (item - first_items) % row_tiles, row0 = row_tile * 16;
+            int u0, u1;
+            units_of(part, u0, u1);
             for (int i = lane; i < a.tokens * 16; i += 32) sums[warp * (a.tokens * 16) + i] = 0.0f;
             __syncwarp();
             float tot[1][1][4] = {{{0.0f, 0.0f, 0.0f, 0.0f}}};
             int tile = u0 / a.h_stages, s = u0 - tile * a.h_stages;
+            uint4 x[2][4][PARTS];
+            float2 p[2];
+            // Half stages ahead, of the pairs of a tile (h comes from other SMs): operands, and the
+            // factor and sum of one block of one token: UNIT_H 4 those of this lane's operands.
+            auto load = [&](int tl, int hf, int at) {
+                const int pair0 = r.tile_first[tl], n = r.tile_count[tl];
+                const uint8_t *const xs =
+                    a.hs + (int64_t(pair0 + min(gr, n - 1)) * a.h_stages + (hf >> 1)) * (4 * kS4XBytes) + (hf & 1) * kS4XBytes + t * 16;
+                const bool there = UNIT_H == 1 || hf * 4 + t < a.h_blocks;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part)
+                        x[at][i][part] = there ? __ldcg(reinterpret_cast<const uint4 *>(xs + i * 64 + part * 2 * kS4XBytes)) : make_uint4(0, 0, 0, 0);
+                const int token = UNIT_H == 4 ? gr : lane & 7, block = UNIT_H == 4 ? t : lane >> 3;
+                p[at] = there ? __ldcg(a.hps + (int64_t(pair0 + min(token, n - 1)) * a.h_stages * 2 + hf) * 4 + block) : make_float2(0x1p-114f, 0.0f);
+            };
+            if (u0 < u1) load(tile, 2 * s, 0);
             for (int u = u0; u < u1 && ok; ++u) {
                 const int pair0 = r.tile_first[tile], n = r.tile_count[tile];
-                const uint8_t *const xs = a.hs + (int64_t(pair0 + min(gr, n - 1)) * a.h_stages + s) * (4 * kS4XBytes) + t * 16;
-                const float2 *const ps0 = a.hps + (int64_t(pair0 + min(2 * t, n - 1)) * a.h_stages + s) * 8;
-                const float2 *const ps1 = a.hps + (int64_t(pair0 + min(2 * t + 1, n - 1)) * a.h_stages + s) * 8;
-                uint4 x[4][2];
-                auto load = [&](int h) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int p = 0; p < 2; ++p) x[i][p] = __ldcg(reinterpret_cast<const uint4 *>(xs + h * kS4XBytes + i * 64 + p * 2 * kS4XBytes));
-                };
-                load(0);
                 int from;
                 if (!arrived(from)) break;
                 const uint32_t more = second_half(s);
-#pragma unroll 1
+#pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (2 * s + h >= a.h_halves) break;
-                    if (h) load(1);
-                    const uint32_t scales[1] = {scale_ring + uint32_t(from * a.scale_bytes) + uint32_t(h) * more + row_at[0]};
-                    const uint32_t next_row[1] = {2u};
-                    s4_half_stage<1, 1, 1, SG, 2, false>(
-                        tot, smem, (ring + uint32_t(from) * CODES + s4_code_at<1>(lane)) ^ (uint32_t(h) << 6), scales, next_row, 32u,
-                        a.down.zeros ? ZEROS : 0u, a.bf16_scales != 0, [&](int i, int, int p) { return x[i][p]; },
-                        [&](int g, int) {
-                            const float2 v = __ldcg(ps0 + h * 4 + g), w = __ldcg(ps1 + h * 4 + g);
-                            return make_float4(v.x, v.y, w.x, w.y);
-                        },
-                        a.h_blocks - (2 * s + h) * 4);
+                    if (h == 0)
+                        load(tile, 2 * s + 1, 1);
+                    else if (u + 1 < u1)
+                        load(s + 1 == a.h_stages ? tile + 1 : tile, s + 1 == a.h_stages ? 0 : 2 * (s + 1), 0);
+                    if (2 * s + h < a.h_halves) {
+                        if constexpr (UNIT_H == 4) {
+                            float most = fmaxf(p[h].x, __shfl_xor_sync(0xFFFFFFFFu, p[h].x, 1));
+                            most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+                            // (powers of two: the inverse and the quotient are exact)
+                            const float rel = __fmul_rn(p[h].x, __uint_as_float((254u << 23) - __float_as_uint(most)));
+                            float sum = __fmul_rn(p[h].y, rel);
+                            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+                            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+                            if (t == 0) mine[h * 32 + gr] = make_float2(most, sum);
+                            const __half2 by = __float2half2_rn(rel);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int part = 0; part < PARTS; ++part) {
+                                    __half2 *v = reinterpret_cast<__half2 *>(&x[h][i][part]);
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) v[k] = __hmul2(v[k], by);
+                                }
+                        } else {
+                            mine[h * 32 + lane] = p[h];
+                        }
+                        __syncwarp();
+                        const uint32_t scales[1] = {scale_ring + uint32_t(from * a.scale_bytes) + uint32_t(h) * more + row_at[0]};
+                        const uint32_t next_row[1] = {2u};
+                        s4_half_stage<1, 1, UNIT_H, SG, PARTS, false>(
+                            tot, smem, (ring + uint32_t(from) * CODES + s4_code_at<UNIT_H>(lane)) ^ (uint32_t(h) << 6), scales, next_row, 32u,
+                            a.down.zeros ? ZEROS : 0u, a.bf16_scales != 0, [&](int i, int, int part) { return x[h][i][part]; },
+                            [&](int g, int) { return *reinterpret_cast<const float4 *>(mine + h * 32 + g * 8 + 2 * t); },
+                            a.h_blocks - (2 * s + h) * 4);
+                    }
                 }
                 __syncwarp();  // (every lane has read the stage)
                 ++taken;
@@ -586,12 +656,34 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
             }
             __syncthreads();
             if (st.abort.flag) break;
-            for (int o = threadIdx.x; o < a.tokens * 16; o += kMoeThreads) {
-                float v = 0.0f;
-#pragma unroll
-                for (int k = 0; k < kMoeWarps; ++k) v = __fadd_rn(v, sums[k * (a.tokens * 16) + o]);
+            auto put = [&](int o, float v) {
                 const int row = row0 + (o & 15);
                 if (row < a.hidden) static_cast<X *>(a.y)[int64_t(o >> 4) * a.ldy + row] = from_float<X>(__fmul_rn(v, kS4Out));
+            };
+            const int outs = a.tokens * 16;
+            for (int o = threadIdx.x; o < outs; o += kMoeThreads) {
+                float v = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kMoeWarps; ++k) v = __fadd_rn(v, sums[k * outs + o]);
+                if (shares == 1)
+                    put(o, v);
+                else
+                    a.parts[(int64_t(part) * row_tiles + row_tile) * outs + o] = v;
+            }
+            if (shares > 1) {  // the last share to end adds all of them, in order
+                __threadfence();
+                __syncthreads();
+                if (threadIdx.x == 0) {
+                    r.last = atomicAdd(a.counters + 2 + row_tile, 1u) == uint32_t(shares - 1);
+                    __threadfence();
+                }
+                __syncthreads();
+                if (r.last)
+                    for (int o = threadIdx.x; o < outs; o += kMoeThreads) {
+                        float v = 0.0f;
+                        for (int k = 0; k < shares; ++k) v = __fadd_rn(v, __ldcg(a.parts + (int64_t(k) * row_tiles + row_tile) * outs + o));
+                        put(o, v);
+                    }
             }
         }
         __syncthreads();  // the tickets are there, and the sums are read
@@ -616,18 +708,19 @@ int64_t up_to(int64_t v, int64_t n) { return (v + n - 1) / n * n; }
 bool lies_on(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 struct MoeSpace {
-    int64_t logits, xs, xps, hs, hps, bytes;
+    int64_t logits, xs, xps, hs, hps, parts, bytes;
 };
 
 MoeSpace moe_space(int64_t tokens, int64_t hidden, int64_t inner, int64_t experts, int64_t top_k) {
     const int64_t stages = (hidden + 255) / 256, h_stages = (inner + 255) / 256, pairs = tokens * top_k;
     MoeSpace s;
-    s.logits = 256;
+    s.logits = up_to((2 + kMaxParts4 / 2) * 4, 256);
     s.xs = s.logits + up_to(tokens * experts * 4, 256);
     s.xps = s.xs + tokens * stages * 2 * kS4XBytes;
     s.hs = s.xps + up_to(tokens * stages * 8 * 8, 256);
     s.hps = s.hs + pairs * h_stages * 4 * kS4XBytes;
-    s.bytes = s.hps + up_to(pairs * h_stages * 8 * 8, 256);
+    s.parts = s.hps + up_to(pairs * h_stages * 8 * 8, 256);
+    s.bytes = s.parts + int64_t(kMaxParts4) * tokens * 16 * 4;
     return s;
 }
 
@@ -666,6 +759,9 @@ int launch_experts(MoeArgs a, const S4Weights &gu, const S4Weights &dn, int sms,
     if (e != cudaSuccess) return fail_launch(e, "cudaGetDevice");
     if (!ready[dev].load(std::memory_order_acquire)) {
         e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+        // (An SM changes its split between shared memory and cache only when it is idle.)
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(router_kernel<X, UNIT>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
         if (e != cudaSuccess) return fail_launch(e, "experts set-up");
         ready[dev].store(1, std::memory_order_release);
     }
@@ -680,7 +776,7 @@ int launch_experts(MoeArgs a, const S4Weights &gu, const S4Weights &dn, int sms,
     const int64_t makers = std::min<int64_t>((blocks + per_cta - 1) / per_cta, sms);  // CTAs that make the operands
     e = launch_moe(router_kernel<X, UNIT>, int64_t(a.tokens + kLogits - 1) / kLogits * a.experts + makers, 0, s, a);
     if (e == cudaSuccess) {
-        const int per_sm = smem + sizeof(Routing) + sizeof(MoeTail) + 1024 <= 114 * 1024 ? 2 : 1;
+        const int per_sm = smem + sizeof(Routing) + sizeof(MoeTail) + kMoeWarps * 512 + 1024 <= 114 * 1024 ? 2 : 1;
         e = launch_moe(fn, int64_t(sms) * per_sm, smem, s, up, down, a);
     }
     return e == cudaSuccess ? PTC_OK : fail_launch(e, "experts launch");
@@ -822,6 +918,7 @@ int ptc_moe_a16_s4(int64_t tokens, int64_t hidden, int64_t inner, int64_t expert
     a.xps = reinterpret_cast<float2 *>(ws + at.xps);
     a.hs = reinterpret_cast<uint8_t *>(ws + at.hs);
     a.hps = reinterpret_cast<float2 *>(ws + at.hps);
+    a.parts = reinterpret_cast<float *>(ws + at.parts);
     a.stall = take_stall_tile();
     a.wait_limit = wait_limit_ns();
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -426,6 +426,9 @@ int launch_s4(S4Args a, const void *codes, int64_t pitch, const S4Shape &sh, int
     if (e != cudaSuccess) return fail_launch(e, "cudaGetDevice");
     if (!ready[dev].load(std::memory_order_acquire)) {
         e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem4 - 1024);
+        // (An SM changes its split between shared memory and cache only when it is idle.)
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(s4_operands_kernel<X, UNIT>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
         if (e != cudaSuccess) return fail_launch(e, "grouped 4-bit product set-up");
         ready[dev].store(1, std::memory_order_release);
     }

@@ -102,5 +102,5 @@ def test_moe_statuses(L, change, status):
 def test_moe_workspace():
     f = ptc.ptc_moe_a16_s4_workspace
     assert f(0, 1, 1, 1, 1) == f(65, 1, 1, 1, 1) == f(1, 0, 1, 1, 1) == f(1, 1, 1, 1, 2) == f(64, 1, 1, 64, 9) == 0
-    # counters, logits, operands of x and their factors, of h and theirs
-    assert f(3, 300, 200, 10, 2) == 256 + 256 + 3 * 2 * 512 + 512 + 6 * 1024 + 512
+    # counters, logits, operands of x and their factors, of h and theirs, shares of y
+    assert f(3, 300, 200, 10, 2) == 4352 + 256 + 3 * 2 * 512 + 512 + 6 * 1024 + 512 + 2048 * 3 * 64
