@@ -38,7 +38,7 @@ constexpr int kMoeWarps = 8, kMoeThreads = 32 * kMoeWarps;
 constexpr int kMaxTokens = 64, kMaxExperts = 512, kMaxTopK = 32, kMaxPairs = 512;
 constexpr int kTile = 8;  // tokens of an expert per item
 constexpr int kLogits = 4;  // tokens per CTA of the router
-constexpr int kRing = 2;  // stages of a warp's ring
+constexpr int kMaxRing = 6;  // places of a warp's ring, each a stage of 16 rows: two for rows of h, one for rows of y
 constexpr int kMaxParts4 = 2048;  // shares of all tiles of 16 rows of y, where they are shared
 
 __device__ uint32_t g_moe_error = 0;
@@ -61,7 +61,7 @@ struct MoeArgs {
     Experts gate_up, down;
     int halves, stages;              // of hidden
     int h_halves, h_stages, h_blocks;  // of inner; blocks of 32
-    int ring_bytes, scale_bytes;     // of all warps' codes; of a stage's scales and zeros
+    int places, ring_bytes, scale_bytes;  // of a warp's ring (even); of all warps' codes; of a place's scales and zeros
     // Workspace.
     uint32_t *counters;   // tickets, items of the first kind that are done; shares of 16 rows of y that are
     float *parts;         // sums of shares of rows of y: [share][tile of rows][token][16]
@@ -151,10 +151,6 @@ __global__ void __launch_bounds__(kMoeThreads) router_kernel(const MoeArgs a) {
 // What every CTA finds from the logits.  A pair is a token and one of its experts; pairs
 // lie by expert, then by token, and each expert's in tiles of up to eight.
 struct Routing {
-    uint32_t mask[kMaxExperts][2];   // tokens of an expert
-    uint16_t first[kMaxExperts];     // its first pair
-    uint16_t id[kMaxPairs];          // [token][slot]
-    float slot_weight[kMaxPairs];
     uint8_t pair_token[kMaxPairs];
     float pair_weight[kMaxPairs];
     uint16_t tile_expert[kMaxPairs], tile_first[kMaxPairs];
@@ -163,9 +159,15 @@ struct Routing {
     uint32_t ticket[4];
     bool last;  // of the shares of 16 rows of y
 };
+struct RoutingWork {  // in the ring's place, before it is used
+    uint32_t mask[kMaxExperts][2];   // tokens of an expert
+    uint16_t first[kMaxExperts];     // its first pair
+    uint16_t id[kMaxPairs];          // [token][slot]
+    float slot_weight[kMaxPairs];
+};
 
 struct MoeTail {
-    uint64_t full[kMoeWarps][kRing];
+    uint64_t full[kMoeWarps][kMaxRing];
     AbortState abort;
 };
 
@@ -177,7 +179,7 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
 }
 
 template <int PER>
-__device__ __forceinline__ void choose_experts(const MoeArgs &a, Routing &r) {
+__device__ __forceinline__ void choose_experts(const MoeArgs &a, RoutingWork &w) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     for (int tok = warp; tok < a.tokens; tok += kMoeWarps) {
         const float *l = a.logits + int64_t(tok) * a.experts;
@@ -228,34 +230,34 @@ __device__ __forceinline__ void choose_experts(const MoeArgs &a, Routing &r) {
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
         if (lane < a.top_k) {
             const int s = tok * a.top_k + lane;
-            const float w = __fdiv_rn(p, sum);
-            r.id[s] = uint16_t(my_id);
-            r.slot_weight[s] = w;
-            atomicOr(&r.mask[my_id][tok >> 5], 1u << (tok & 31));
+            const float share = __fdiv_rn(p, sum);
+            w.id[s] = uint16_t(my_id);
+            w.slot_weight[s] = share;
+            atomicOr(&w.mask[my_id][tok >> 5], 1u << (tok & 31));
             if (blockIdx.x == 0) {
                 if (a.ids) a.ids[s] = my_id;
-                if (a.weights) a.weights[s] = w;
+                if (a.weights) a.weights[s] = share;
             }
         }
     }
 }
 
-__device__ __forceinline__ void route(const MoeArgs &a, Routing &r) {
+__device__ __forceinline__ void route(const MoeArgs &a, Routing &r, RoutingWork &w) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    for (int i = threadIdx.x; i < a.experts; i += kMoeThreads) r.mask[i][0] = r.mask[i][1] = 0;
+    for (int i = threadIdx.x; i < a.experts; i += kMoeThreads) w.mask[i][0] = w.mask[i][1] = 0;
     __syncthreads();
     if (a.experts <= 64)
-        choose_experts<2>(a, r);
+        choose_experts<2>(a, w);
     else if (a.experts <= 128)
-        choose_experts<4>(a, r);
+        choose_experts<4>(a, w);
     else
-        choose_experts<kMaxExperts / 32>(a, r);
+        choose_experts<kMaxExperts / 32>(a, w);
     __syncthreads();
     if (warp == 0) {  // pairs and tiles of the experts, in order
         int pairs = 0, tiles = 0;
         for (int e0 = 0; e0 < a.experts; e0 += 32) {
             const int e = e0 + lane;
-            const int c = e < a.experts ? __popc(r.mask[e][0]) + __popc(r.mask[e][1]) : 0, t = (c + kTile - 1) / kTile;
+            const int c = e < a.experts ? __popc(w.mask[e][0]) + __popc(w.mask[e][1]) : 0, t = (c + kTile - 1) / kTile;
             int sum = c | t << 16;
 #pragma unroll
             for (int o = 1; o < 32; o *= 2) {
@@ -263,7 +265,7 @@ __device__ __forceinline__ void route(const MoeArgs &a, Routing &r) {
                 if (lane >= o) sum += up;
             }
             const int p0 = pairs + (sum & 0xFFFF) - c, t0 = tiles + (sum >> 16) - t;
-            if (e < a.experts) r.first[e] = uint16_t(p0);
+            if (e < a.experts) w.first[e] = uint16_t(p0);
             for (int i = 0; i < t; ++i) {
                 r.tile_expert[t0 + i] = uint16_t(e);
                 r.tile_first[t0 + i] = uint16_t(p0 + kTile * i);
@@ -277,12 +279,13 @@ __device__ __forceinline__ void route(const MoeArgs &a, Routing &r) {
     }
     __syncthreads();
     for (int s = threadIdx.x; s < a.tokens * a.top_k; s += kMoeThreads) {
-        const int tok = s / a.top_k, e = r.id[s];
-        const uint32_t lo = r.mask[e][0], hi = r.mask[e][1];
+        const int tok = s / a.top_k, e = w.id[s];
+        const uint32_t lo = w.mask[e][0], hi = w.mask[e][1];
         const int rank = tok < 32 ? __popc(lo & ((1u << tok) - 1u)) : __popc(lo) + __popc(hi & ((1u << (tok - 32)) - 1u));
-        r.pair_token[r.first[e] + rank] = uint8_t(tok);
-        r.pair_weight[r.first[e] + rank] = r.slot_weight[s];
+        r.pair_token[w.first[e] + rank] = uint8_t(tok);
+        r.pair_weight[w.first[e] + rank] = w.slot_weight[s];
     }
+    fence_proxy_async_all();  // (bulk copies write where this was held)
     __syncthreads();
 }
 
@@ -315,9 +318,8 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     experts_kernel(const __grid_constant__ CUtensorMap tm_up, const __grid_constant__ CUtensorMap tm_down, const MoeArgs a) {
     constexpr int SG = 4 / UNIT;            // scale groups (and, of x, blocks) per half stage
     constexpr int SCALES = 2 * SG * 32;     // bytes of a tile's scales in a stage
-    constexpr int UP = SCALES;              // up's from the gate's
-    constexpr int ZEROS = SCALES * (ODD ? 3 : 2);  // zeros from scales, of either kind
-    constexpr int CODES = 2 * kS4TileBytes;
+    constexpr int ZEROS = SCALES * (ODD ? 2 : 1);  // zeros from scales
+    constexpr int CODES = kS4TileBytes;
     // Rows of y: with groups of 128 and more half a stage is one block, whose four blocks of
     // 32 of h are brought to one power of two as they are loaded.
     constexpr int UNIT_H = UNIT == 4 ? 4 : 1;
@@ -333,10 +335,10 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     float2 *const mine = &factors[warp][0][0];
     const int f = s4_pair_of(lane >> 2), gr = lane >> 2, t = lane & 3;
     const int half = warp & 1, share = warp >> 1;  // of rows of h
-    const uint32_t ring = uint32_t(warp * kRing * CODES), scale_ring = uint32_t(a.ring_bytes + warp * kRing * a.scale_bytes);
-    float *const sums = reinterpret_cast<float *>(smem + a.ring_bytes + kMoeWarps * kRing * a.scale_bytes);
+    const uint32_t ring = uint32_t(warp * a.places * CODES), scale_ring = uint32_t(a.ring_bytes + warp * a.places * a.scale_bytes);
+    float *const sums = reinterpret_cast<float *>(smem + a.ring_bytes + kMoeWarps * a.places * a.scale_bytes);
     if (lane == 0)
-        for (int i = 0; i < kRing; ++i) mbar_init(&st.full[warp][i], 1);
+        for (int i = 0; i < a.places; ++i) mbar_init(&st.full[warp][i], 1);
     if (threadIdx.x == 0) {
         st.abort.flag = 0;
         tma_prefetch_desc(&tm_up);
@@ -345,8 +347,11 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     fence_barrier_init();
     griddep_wait();
     griddep_launch_dependents();
-    if (threadIdx.x == 0) r.ticket[0] = atomicAdd(a.counters, 1u);
-    route(a, r);
+    // (Tickets are asked for where they are due and looked at later.)
+    uint32_t asked_ticket = 0;
+    if (threadIdx.x == 0) asked_ticket = atomicAdd(a.counters, 1u);
+    route(a, r, *reinterpret_cast<RoutingWork *>(smem));
+    if (threadIdx.x == 0) r.ticket[0] = asked_ticket;
 
     const int units = r.tiles * a.h_stages;  // stages of 16 rows of y, of all tiles of pairs
     const int row_tiles = (a.hidden + 15) / 16;
@@ -363,10 +368,8 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     // are asked for before this one's end; with few that would leave CTAs without, and they are
     // taken when the item before begins.
     const bool early = first_items >= 4 * int(gridDim.x);
-    if (early) {
-        if (threadIdx.x == 0) r.ticket[1] = atomicAdd(a.counters, 1u);
-        __syncthreads();
-    }
+    if (early && threadIdx.x == 0) r.ticket[1] = atomicAdd(a.counters, 1u);
+    __syncthreads();
     // This warp's of a share.
     auto units_of = [&](int part, int &u0, int &u1) {
         const int first = int(int64_t(units) * part / shares), n = int(int64_t(units) * (part + 1) / shares) - first;
@@ -398,36 +401,34 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     // zeros.  When the item's are all asked for, the next item's follow: the weights do
     // not depend on h.
     Bring b = begin(0);
-    int bring_round = 0, into = 0, asked = 0, taken = 0;
+    int bring_round = 0, into = 0, asked = 0, taken = 0;  // (in places)
     auto issue = [&](int round, bool ahead) {
         if (b.left == 0 && bring_round == round && ahead) b = begin(++bring_round);
-        if (b.left == 0) return;
+        const int need = b.second_kind ? 1 : 2;
+        if (b.left == 0 || asked - taken + need > a.places) return false;
         if (lane == 0) {
             const Experts &w = b.second_kind ? a.down : a.gate_up;
             const int e = r.tile_expert[b.tile];
-            uint64_t *bar = &st.full[warp][into];
             const int g0 = a.per_group == 1 ? 2 * b.st * SG : 2 * b.st / a.per_group;
             const uint32_t bytes = uint32_t(min(2 * SG, w.groups - g0)) * 32u, both = w.zeros ? 2u : 1u;
-            const uint32_t dst = smem_u32(smem) + ring + into * CODES, sdst = smem_u32(smem) + scale_ring + into * a.scale_bytes;
-            auto scales = [&](int tile, uint32_t at) {
-                const int64_t from = ((int64_t(e) * w.tiles + tile) * w.groups + g0) * 32;
-                bulk_copy(sdst + at, w.scales + from, bytes, bar);
-                if (w.zeros) bulk_copy(sdst + ZEROS + at, w.zeros + from, bytes, bar);
+            // One place: rows from `row`, the scales of their tile and (next) of the one after it.
+            auto place = [&](int at, const CUtensorMap *map, int row, int tile, bool next) {
+                uint64_t *bar = &st.full[warp][at];
+                const uint32_t scales = smem_u32(smem) + scale_ring + at * a.scale_bytes;
+                mbar_arrive_expect_tx(bar, kS4TileBytes + bytes * both * (next ? 2u : 1u));
+                tma_load_rows(smem_u32(smem) + ring + at * CODES, map, bar, b.st * kS4RowBytes, row, e);
+                for (int i = 0; i <= int(next); ++i) {
+                    const int64_t from = ((int64_t(e) * w.tiles + min(tile + i, w.tiles - 1)) * w.groups + g0) * 32;
+                    bulk_copy(scales + i * SCALES, w.scales + from, bytes, bar);
+                    if (w.zeros) bulk_copy(scales + ZEROS + i * SCALES, w.zeros + from, bytes, bar);
+                }
             };
             if (b.second_kind) {
-                mbar_arrive_expect_tx(bar, kS4TileBytes + bytes * both);
-                tma_load_rows(dst, &tm_down, bar, b.st * kS4RowBytes, b.row, e);
-                scales(b.row / 16, 0);
+                place(into, &tm_down, b.row, b.row / 16, false);
             } else {
                 // (up's rows may begin in the middle of a tile and end in the next one)
-                const int up = (a.inner + b.row) / 16, gate = min(b.row / 16, w.tiles - 1);
-                const bool next = ODD && up + 1 < w.tiles;
-                mbar_arrive_expect_tx(bar, 2 * kS4TileBytes + bytes * both * (next ? 3u : 2u));
-                tma_load_rows(dst, &tm_up, bar, b.st * kS4RowBytes, b.row, e);
-                tma_load_rows(dst + kS4TileBytes, &tm_up, bar, b.st * kS4RowBytes, a.inner + b.row, e);
-                scales(gate, 0);
-                scales(min(up, w.tiles - 1), UP);
-                if (next) scales(up + 1, UP + SCALES);
+                place(into, &tm_up, b.row, b.row / 16, false);
+                place(into + 1, &tm_up, a.inner + b.row, (a.inner + b.row) / 16, ODD && (a.inner + b.row) / 16 + 1 < w.tiles);
             }
         }
         if (b.second_kind) {
@@ -439,15 +440,29 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
             b.st += 4;
         }
         --b.left;
-        ++asked;
-        if (++into == kRing) into = 0;
+        asked += need;
+        into += need;
+        if (into == a.places) into = 0;
+        return true;
     };
     // Waits for the next stage to take; its place in the ring.
     bool ok = true;
-    auto arrived = [&](int &from) {
-        from = taken % kRing;
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&st.full[warp][from], uint32_t(taken / kRing) & 1u, &st.abort, &g_moe_error, a.wait_limit));
+    int from = 0;          // the place
+    uint32_t parity = 0;
+    auto arrived = [&](int places) {
+        for (int i = 0; i < places; ++i)
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&st.full[warp][from + i], parity, &st.abort, &g_moe_error, a.wait_limit)) && ok;
         return ok;
+    };
+    // A stage has been read by every lane: its places are free.
+    auto release = [&](int places) {
+        __syncwarp();
+        taken += places;
+        from += places;
+        if (from == a.places) {
+            from = 0;
+            parity ^= 1u;
+        }
     };
     // Offset in a stage's scales of this lane's two rows, for the gate (and y) and up; from
     // the first to the second row.
@@ -456,7 +471,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     for (int m = 0; m < 2; ++m) {
         auto at = [&](int i) { return uint32_t(i >> 4) * SCALES + uint32_t(i & 15) * 2u; };
         const int i = 2 * f + (ODD && m ? a.inner % 16 : 0);
-        row_at[m] = at(i) + (m ? UP : 0);
+        row_at[m] = at(i) + (m ? uint32_t(a.scale_bytes) : 0u);  // (up's are in the next place)
         row_more[m] = at(i + 1) - at(i);
     }
     // From the first to the second half of a stage: that of its scales.
@@ -465,13 +480,13 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     };
 
     __syncwarp();
-    for (int i = 0; i < kRing; ++i) issue(0, early);
+    while (issue(0, early)) {}
     bool ready = false;  // every item of the first kind is done
     for (int round = 0;; ++round) {
         const int item = ticket(round);
         if (item >= items) break;
         const int later = (round + (early ? 2 : 1)) & 3;
-        if (threadIdx.x == 0 && (early || item < first_items)) r.ticket[later] = atomicAdd(a.counters, 1u);
+        if (threadIdx.x == 0 && (early || item < first_items)) asked_ticket = atomicAdd(a.counters, 1u);
         if (item < first_items) {
             // ------------------------------------------------ rows of h
             const int tile = item / a.h_blocks, ib = item - tile * a.h_blocks;
@@ -494,8 +509,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
             };
             if (share < a.stages) load(2 * share, 0);
             for (int s = share; s < a.stages && ok; s += 4) {
-                int from;
-                if (!arrived(from)) break;
+                if (!arrived(2)) break;
                 const uint32_t more = second_half(s);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -515,8 +529,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                             (a.hidden - (2 * s + h) * kS4Half + 32 * UNIT - 1) / (32 * UNIT));
                     }
                 }
-                __syncwarp();  // (every lane has read the stage)
-                ++taken;
+                release(2);
                 issue(round, early);
             }
             // Sums of the shares: [share][half][gate, up][row][token].
@@ -562,7 +575,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                 if (st.abort.flag) break;
                 ready = true;
             }
-            if (threadIdx.x == 0 && !early) r.ticket[later] = atomicAdd(a.counters, 1u);
+            if (threadIdx.x == 0 && !early) asked_ticket = atomicAdd(a.counters, 1u);
             const int part = (item - first_items) / row_tiles, row_tile = (item - first_items) % row_tiles, row0 = row_tile * 16;
             int u0, u1;
             units_of(part, u0, u1);
@@ -590,8 +603,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
             if (u0 < u1) load(tile, 2 * s, 0);
             for (int u = u0; u < u1 && ok; ++u) {
                 const int pair0 = r.tile_first[tile], n = r.tile_count[tile];
-                int from;
-                if (!arrived(from)) break;
+                if (!arrived(1)) break;
                 const uint32_t more = second_half(s);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -631,8 +643,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                             a.h_blocks - (2 * s + h) * 4);
                     }
                 }
-                __syncwarp();  // (every lane has read the stage)
-                ++taken;
+                release(1);
                 issue(round, early);
                 if (++s == a.h_stages || u + 1 == u1) {
                     // The tile's sums to its tokens, this warp's.
@@ -686,17 +697,12 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                     }
             }
         }
+        if (threadIdx.x == 0) r.ticket[later] = asked_ticket;
         __syncthreads();  // the tickets are there, and the sums are read
-        // (A warp that has no stage of this item brings the next one's here.)
-        while (asked - taken < kRing && (b.left > 0 || bring_round == round)) {
-            const int before = asked;
-            issue(round, true);
-            if (asked == before) break;
-        }
+        while (issue(round, true)) {}  // (what the item's end left room for)
     }
     // After an abort copies in flight land before the CTA exits.
-    for (; taken < asked; ++taken)
-        mbar_wait(&st.full[warp][taken % kRing], uint32_t(taken / kRing) & 1u, nullptr, nullptr, a.wait_limit);
+    for (; taken < asked; release(1)) mbar_wait(&st.full[warp][from], parity, nullptr, nullptr, a.wait_limit);
 }
 
 // ------------------------------------------------------------ host side
@@ -749,10 +755,14 @@ template <typename X, int UNIT, bool ODD>
 int launch_experts(MoeArgs a, const S4Weights &gu, const S4Weights &dn, int sms, cudaStream_t s) {
     constexpr int SG = 4 / UNIT;
     auto *fn = experts_kernel<X, UNIT, ODD>;
-    a.ring_bytes = kMoeWarps * kRing * 2 * kS4TileBytes;
-    a.scale_bytes = 2 * SG * 32 * (ODD ? 3 : 2) * (a.gate_up.zeros || a.down.zeros ? 2 : 1);
+    a.scale_bytes = 2 * SG * 32 * (ODD ? 2 : 1) * (a.gate_up.zeros || a.down.zeros ? 2 : 1);
+    // As many places as leave two CTAs on an SM, at least four.
     const size_t sums = size_t(kMoeWarps) * std::max(32 * kTile, a.tokens * 16) * 4;
-    const size_t smem = size_t(a.ring_bytes) + size_t(kMoeWarps) * kRing * a.scale_bytes + sums + 1024;
+    const size_t fixed = sums + sizeof(Routing) + sizeof(MoeTail) + kMoeWarps * 512 + 3072;  // (alignment, the system's 1 KB)
+    const size_t place = size_t(kMoeWarps) * (kS4TileBytes + a.scale_bytes);
+    a.places = fixed + kMaxRing * place <= 114 * 1024 ? kMaxRing : 4;
+    a.ring_bytes = kMoeWarps * a.places * kS4TileBytes;
+    const size_t smem = a.places * place + sums + 1024;
     static std::atomic<int> ready[kMaxDevM];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -776,7 +786,7 @@ int launch_experts(MoeArgs a, const S4Weights &gu, const S4Weights &dn, int sms,
     const int64_t makers = std::min<int64_t>((blocks + per_cta - 1) / per_cta, sms);  // CTAs that make the operands
     e = launch_moe(router_kernel<X, UNIT>, int64_t(a.tokens + kLogits - 1) / kLogits * a.experts + makers, 0, s, a);
     if (e == cudaSuccess) {
-        const int per_sm = smem + sizeof(Routing) + sizeof(MoeTail) + kMoeWarps * 512 + 1024 <= 114 * 1024 ? 2 : 1;
+        const int per_sm = fixed + a.places * place <= 114 * 1024 ? 2 : 1;
         e = launch_moe(fn, int64_t(sms) * per_sm, smem, s, up, down, a);
     }
     return e == cudaSuccess ? PTC_OK : fail_launch(e, "experts launch");
