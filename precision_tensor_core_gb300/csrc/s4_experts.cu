@@ -7,13 +7,17 @@
 // The active experts' weights are read once per eight of an expert's tokens and bound the
 // call.  router_kernel makes the logits and the tokens' operands (s4.cuh).  Every CTA of
 // experts_kernel finds the experts and their tokens from the logits, which is less than
-// handing them over, then takes items by tickets: first 32 rows of h of an expert (32 rows
-// of gate and 32 of up, the eight warps two row halves by four shares of K), then 16 rows of y
-// of all experts (the warps share the experts' codes evenly).  The second kind waits until
-// every item of the first kind is done: their tickets are lower, so they are in the hands of CTAs that
-// run, whatever else holds the GPU.  h passes through memory as two binary16 numbers
-// relative to a power of two per 32, 22 bits in all.  No sum's order depends on which
-// CTA takes what.
+// handing them over.  It then takes items: first, by tickets, 32 rows of h of an expert (32
+// rows of gate and 32 of up, the eight warps two row halves by four shares of K), and when
+// those are gone 16 rows of y of all experts, or of a share of their codes, which the warps share
+// evenly.  The second kind waits until every item of the first kind is done.  A ticket is
+// taken by a CTA that runs, and a CTA that waits holds no item of the first kind, so the wait
+// ends whatever else holds the GPU.  h passes through memory as one or two binary16 numbers
+// relative to a power of two per 32.  No sum's order depends on which CTA takes what.
+//
+// Each warp brings its rows itself, by TMA, to a ring of its own in shared memory, and the
+// next item's while it ends one.  The activations come from L2 into registers, half a stage
+// ahead: an expert has few of them.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -311,6 +315,8 @@ struct Bring {
     int second_kind;  // rows of y
     int tile, st;     // the next stage's tile of pairs and stage
     int row;          // the warp's first row of h, or the item's of y
+    int expert;       // the tile's
+    const uint8_t *scales, *up_scales;  // of the rows' tiles, from group 0
 };
 
 template <typename X, int UNIT, bool ODD>
@@ -355,15 +361,16 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
 
     const int units = r.tiles * a.h_stages;  // stages of 16 rows of y, of all tiles of pairs
     const int row_tiles = (a.hidden + 15) / 16;
-    // Shares of these stages that are items of their own: as many as keep every CTA busy
-    // once, where tiles are fewer than half the CTAs; otherwise for three rounds, so that none
-    // is left with one item more than the others for long (256 tiles on 304 CTAs, two of them in the hands
-    // of some: 172 us instead of XX).
+    // Shares of these stages that are items of their own: as many as give every CTA one where
+    // there are CTAs enough; otherwise (or with 60% of a round's CTAs idle) for three rounds.
     int shares = 1;
+    const int grid = int(gridDim.x);
     while (shares < 8 && row_tiles * shares * 2 <= kMaxParts4 && units >= 16 * shares &&
-           (2 * row_tiles <= int(gridDim.x) ? row_tiles * shares * 2 <= int(gridDim.x) : row_tiles * shares < 3 * int(gridDim.x)))
+           (row_tiles <= grid ? row_tiles * shares * 2 <= grid : row_tiles * shares < 3 * grid))
         shares *= 2;
-    const int first_items = r.tiles * a.h_blocks, items = first_items + row_tiles * shares;
+    // Items of the first kind are taken by tickets, which end the wait for them: whoever waits has
+    // none that is not done.  Those of the second kind are every grid-th from this CTA's own number.
+    const int first_items = r.tiles * a.h_blocks, second_items = row_tiles * shares;
     // With many items per CTA tickets are taken two items ahead, so that the next item's weights
     // are asked for before this one's end; with few that would leave CTAs without, and they are
     // taken when the item before begins.
@@ -376,17 +383,39 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
         u0 = first + n * warp / kMoeWarps;
         u1 = first + n * (warp + 1) / kMoeWarps;
     };
-    auto ticket = [&](int round) { return int(r.ticket[round & 3]); };
+    // The item of a round: one of the first kind by its ticket, then those of the second kind; -1
+    // after the last.  (Tickets rise, so that the rounds of the first kind come first;
+    // `second_round` is the round of the first ticket past them, where it is known.)
+    int second_round = 1 << 30;
+    auto item_of = [&](int round) {
+        if (round < second_round) {
+            const uint32_t t = r.ticket[round & 3];
+            if (t < uint32_t(first_items)) return int(t);
+            second_round = round;
+        }
+        const int64_t second = int(blockIdx.x) + int64_t(round - second_round) * grid;
+        return second < second_items ? first_items + int(second) : -1;
+    };
+    // From scales to zeros, of either matrix (0: it has none).
+    const int64_t up_zeros = a.gate_up.zeros ? a.gate_up.zeros - a.gate_up.scales : 0;
+    const int64_t down_zeros = a.down.zeros ? a.down.zeros - a.down.scales : 0;
+    auto tile_scales = [](const Experts &w, int e, int tile) {  // (rows past the last tile read it again)
+        return w.scales + (int64_t(e) * w.tiles + min(tile, w.tiles - 1)) * w.groups * 32;
+    };
     // The stages of the item of a round; none past the last item.
     auto begin = [&](int round) {
-        const int item = ticket(round);
-        Bring b{0, 0, 0, 0, 0};
+        const int item = item_of(round);
+        Bring b{0, 0, 0, 0, 0, 0, nullptr, nullptr};
+        if (item < 0) return b;
         if (item < first_items) {
             b.tile = item / a.h_blocks;
             b.row = (item - b.tile * a.h_blocks) * 32 + half * 16;
             b.st = share;
             b.left = (a.stages - share + 3) / 4;  // share, share + 4, ...
-        } else if (item < items) {
+            b.expert = r.tile_expert[b.tile];
+            b.scales = tile_scales(a.gate_up, b.expert, b.row / 16);
+            b.up_scales = tile_scales(a.gate_up, b.expert, (a.inner + b.row) / 16);
+        } else {
             int u0, u1;
             units_of((item - first_items) / row_tiles, u0, u1);
             b.second_kind = 1;
@@ -394,6 +423,8 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
             b.tile = u0 / a.h_stages;
             b.st = u0 - b.tile * a.h_stages;
             b.left = u1 - u0;
+            b.expert = r.tile_expert[min(b.tile, r.tiles - 1)];
+            b.scales = tile_scales(a.down, b.expert, b.row / 16);
         }
         return b;
     };
@@ -407,39 +438,46 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
         const int need = b.second_kind ? 1 : 2;
         if (b.left == 0 || asked - taken + need > a.places) return false;
         if (lane == 0) {
-            const Experts &w = b.second_kind ? a.down : a.gate_up;
-            const int e = r.tile_expert[b.tile];
+            const int groups = b.second_kind ? a.down.groups : a.gate_up.groups;
+            const int64_t zeros = b.second_kind ? down_zeros : up_zeros;
             const int g0 = a.per_group == 1 ? 2 * b.st * SG : 2 * b.st / a.per_group;
-            const uint32_t bytes = uint32_t(min(2 * SG, w.groups - g0)) * 32u, both = w.zeros ? 2u : 1u;
-            // One place: rows from `row`, the scales of their tile and (next) of the one after it.
-            auto place = [&](int at, const CUtensorMap *map, int row, int tile, bool next) {
-                uint64_t *bar = &st.full[warp][at];
-                const uint32_t scales = smem_u32(smem) + scale_ring + at * a.scale_bytes;
-                mbar_arrive_expect_tx(bar, kS4TileBytes + bytes * both * (next ? 2u : 1u));
-                tma_load_rows(smem_u32(smem) + ring + at * CODES, map, bar, b.st * kS4RowBytes, row, e);
-                for (int i = 0; i <= int(next); ++i) {
-                    const int64_t from = ((int64_t(e) * w.tiles + min(tile + i, w.tiles - 1)) * w.groups + g0) * 32;
-                    bulk_copy(scales + i * SCALES, w.scales + from, bytes, bar);
-                    if (w.zeros) bulk_copy(scales + ZEROS + i * SCALES, w.zeros + from, bytes, bar);
-                }
-            };
-            if (b.second_kind) {
-                place(into, &tm_down, b.row, b.row / 16, false);
-            } else {
+            const uint32_t bytes = uint32_t(min(2 * SG, groups - g0)) * 32u, both = zeros ? 2u * bytes : bytes;
+            const uint32_t codes = smem_u32(smem) + ring + into * CODES, scales = smem_u32(smem) + scale_ring + into * a.scale_bytes;
+            uint64_t *const bar = &st.full[warp][into];
+            const uint8_t *const from = b.scales + g0 * 32;
+            mbar_arrive_expect_tx(bar, kS4TileBytes + both);
+            tma_load_rows(codes, b.second_kind ? &tm_down : &tm_up, bar, b.st * kS4RowBytes, b.row, b.expert);
+            bulk_copy(scales, from, bytes, bar);
+            if (zeros) bulk_copy(scales + ZEROS, from + zeros, bytes, bar);
+            if (!b.second_kind) {
                 // (up's rows may begin in the middle of a tile and end in the next one)
-                place(into, &tm_up, b.row, b.row / 16, false);
-                place(into + 1, &tm_up, a.inner + b.row, (a.inner + b.row) / 16, ODD && (a.inner + b.row) / 16 + 1 < w.tiles);
+                const uint32_t up = scales + a.scale_bytes;
+                const uint8_t *const more = b.up_scales + g0 * 32;
+                const bool next = ODD && (a.inner + b.row) / 16 + 1 < a.gate_up.tiles;
+                mbar_arrive_expect_tx(bar + 1, kS4TileBytes + (next ? 2 * both : both));
+                tma_load_rows(codes + CODES, &tm_up, bar + 1, b.st * kS4RowBytes, a.inner + b.row, b.expert);
+                bulk_copy(up, more, bytes, bar + 1);
+                if (zeros) bulk_copy(up + ZEROS, more + zeros, bytes, bar + 1);
+                if (next) {
+                    bulk_copy(up + SCALES, more + groups * 32, bytes, bar + 1);
+                    if (zeros) bulk_copy(up + ZEROS + SCALES, more + groups * 32 + zeros, bytes, bar + 1);
+                }
             }
         }
+        --b.left;
         if (b.second_kind) {
             if (++b.st == a.h_stages) {
                 b.st = 0;
                 ++b.tile;
+                if (b.left > 0) {
+                    const int e = r.tile_expert[b.tile];
+                    b.scales += int64_t(e - b.expert) * a.down.tiles * a.down.groups * 32;
+                    b.expert = e;
+                }
             }
         } else {
             b.st += 4;
         }
-        --b.left;
         asked += need;
         into += need;
         if (into == a.places) into = 0;
@@ -483,10 +521,10 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     while (issue(0, early)) {}
     bool ready = false;  // every item of the first kind is done
     for (int round = 0;; ++round) {
-        const int item = ticket(round);
-        if (item >= items) break;
+        const int item = item_of(round);
+        if (item < 0) break;
         const int later = (round + (early ? 2 : 1)) & 3;
-        if (threadIdx.x == 0 && (early || item < first_items)) asked_ticket = atomicAdd(a.counters, 1u);
+        if (threadIdx.x == 0 && item < first_items) asked_ticket = atomicAdd(a.counters, 1u);
         if (item < first_items) {
             // ------------------------------------------------ rows of h
             const int tile = item / a.h_blocks, ib = item - tile * a.h_blocks;
@@ -575,7 +613,6 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                 if (st.abort.flag) break;
                 ready = true;
             }
-            if (threadIdx.x == 0 && !early) asked_ticket = atomicAdd(a.counters, 1u);
             const int part = (item - first_items) / row_tiles, row_tile = (item - first_items) % row_tiles, row0 = row_tile * 16;
             int u0, u1;
             units_of(part, u0, u1);
@@ -587,30 +624,40 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
             float2 p[2];
             // Half stages ahead, of the pairs of a tile (h comes from other SMs): operands, and the
             // factor and sum of one block of one token: UNIT_H 4 those of this lane's operands.
-            auto load = [&](int tl, int hf, int at) {
+            const uint8_t *xs = nullptr;
+            const float2 *ps = nullptr;
+            auto point = [&](int tl) {  // to a tile's pairs
                 const int pair0 = r.tile_first[tl], n = r.tile_count[tl];
-                const uint8_t *const xs =
-                    a.hs + (int64_t(pair0 + min(gr, n - 1)) * a.h_stages + (hf >> 1)) * (4 * kS4XBytes) + (hf & 1) * kS4XBytes + t * 16;
+                const int token = UNIT_H == 4 ? gr : lane & 7, block = UNIT_H == 4 ? t : lane >> 3;
+                xs = a.hs + int64_t(pair0 + min(gr, n - 1)) * a.h_stages * (4 * kS4XBytes) + t * 16;
+                ps = a.hps + int64_t(pair0 + min(token, n - 1)) * a.h_stages * 8 + block;
+            };
+            auto load = [&](int hf, int at) {
+                const uint8_t *const from = xs + (hf >> 1) * (4 * kS4XBytes) + (hf & 1) * kS4XBytes;
                 const bool there = UNIT_H == 1 || hf * 4 + t < a.h_blocks;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int part = 0; part < PARTS; ++part)
-                        x[at][i][part] = there ? __ldcg(reinterpret_cast<const uint4 *>(xs + i * 64 + part * 2 * kS4XBytes)) : make_uint4(0, 0, 0, 0);
-                const int token = UNIT_H == 4 ? gr : lane & 7, block = UNIT_H == 4 ? t : lane >> 3;
-                p[at] = there ? __ldcg(a.hps + (int64_t(pair0 + min(token, n - 1)) * a.h_stages * 2 + hf) * 4 + block) : make_float2(0x1p-114f, 0.0f);
+                        x[at][i][part] = there ? __ldcg(reinterpret_cast<const uint4 *>(from + i * 64 + part * 2 * kS4XBytes)) : make_uint4(0, 0, 0, 0);
+                p[at] = there ? __ldcg(ps + hf * 4) : make_float2(0x1p-114f, 0.0f);
             };
-            if (u0 < u1) load(tile, 2 * s, 0);
+            if (u0 < u1) {
+                point(tile);
+                load(2 * s, 0);
+            }
             for (int u = u0; u < u1 && ok; ++u) {
-                const int pair0 = r.tile_first[tile], n = r.tile_count[tile];
                 if (!arrived(1)) break;
                 const uint32_t more = second_half(s);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (h == 0)
-                        load(tile, 2 * s + 1, 1);
-                    else if (u + 1 < u1)
-                        load(s + 1 == a.h_stages ? tile + 1 : tile, s + 1 == a.h_stages ? 0 : 2 * (s + 1), 0);
+                    if (h == 0) {
+                        load(2 * s + 1, 1);
+                    } else if (u + 1 < u1) {
+                        const bool over = s + 1 == a.h_stages;
+                        if (over) point(tile + 1);
+                        load(over ? 0 : 2 * (s + 1), 0);
+                    }
                     if (2 * s + h < a.h_halves) {
                         if constexpr (UNIT_H == 4) {
                             float most = fmaxf(p[h].x, __shfl_xor_sync(0xFFFFFFFFu, p[h].x, 1));
@@ -647,6 +694,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                 issue(round, early);
                 if (++s == a.h_stages || u + 1 == u1) {
                     // The tile's sums to its tokens, this warp's.
+                    const int pair0 = r.tile_first[tile], n = r.tile_count[tile];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int j = 2 * t + i;
@@ -697,7 +745,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                     }
             }
         }
-        if (threadIdx.x == 0) r.ticket[later] = asked_ticket;
+        if (threadIdx.x == 0 && item < first_items) r.ticket[later] = asked_ticket;
         __syncthreads();  // the tickets are there, and the sums are read
         while (issue(round, true)) {}  // (what the item's end left room for)
     }
