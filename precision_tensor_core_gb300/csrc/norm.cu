@@ -54,57 +54,92 @@ struct GradArgs {
     float eps, inv_cols;
 };
 
-// Column of element e of this thread's chunk i of eight elements: eight consecutive
-// ones, or (rows that are not 16-byte aligned) one of each run of the row's threads,
-// so that a warp's accesses are consecutive either way.
-template <bool VEC>
+// How a thread meets its chunk i of eight elements of a row: eight consecutive ones, of
+// rows that are 16-byte aligned, or (kShifted, loads only) of any; or one of each run of the
+// row's threads (kSpread).  A warp's accesses are consecutive either way.
+constexpr int kSpread = 0, kWide = 1, kShifted = 2;
+
+template <int HOW>
 __device__ __forceinline__ int64_t column(int i, int e, int tid, int threads) {
-    return VEC ? (int64_t(i) * threads + tid) * 8 + e : (int64_t(i) * 8 + e) * threads + tid;
+    return HOW != kSpread ? (int64_t(i) * threads + tid) * 8 + e : (int64_t(i) * 8 + e) * threads + tid;
 }
 
-template <bool VEC, typename T>
+// Eight elements at p, which is aligned to them alone, from the aligned words around them;
+// `before`, `after`: elements of the row before p, and from p on.  (A word that reaches past
+// the row is not read: those at the row's ends come one by one.)
+template <typename T>
+__device__ __forceinline__ Pack8<T> load_shifted(const T *p, int64_t before, int64_t after) {
+    constexpr int W = Pack8<T>::W, PER = 16 / int(sizeof(T));
+    const int m = int((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
+    if (m > before || after < 8 + (m ? PER - m : 0)) return load8(p, int(min(int64_t(8), after)), false);
+    const uint4 *from = reinterpret_cast<const uint4 *>(p - m);
+    uint4 words[W + 1];
+#pragma unroll
+    for (int i = 0; i < W; ++i) words[i] = from[i];
+    words[W] = m ? from[W] : make_uint4(0, 0, 0, 0);
+    uint32_t r[4 * W + 4];
+#pragma unroll
+    for (int i = 0; i <= W; ++i) r[4 * i] = words[i].x, r[4 * i + 1] = words[i].y, r[4 * i + 2] = words[i].z, r[4 * i + 3] = words[i].w;
+    const int bytes = m * int(sizeof(T));
+#pragma unroll
+    for (int i = 0; i < 4 * W + 2; ++i) r[i] = bytes & 8 ? r[i + 2] : r[i];
+#pragma unroll
+    for (int i = 0; i < 4 * W + 1; ++i) r[i] = bytes & 4 ? r[i + 1] : r[i];
+    if constexpr (sizeof(T) == 2)
+#pragma unroll
+        for (int i = 0; i < 4 * W; ++i) r[i] = __funnelshift_r(r[i], r[i + 1], bytes & 2 ? 16 : 0);
+    Pack8<T> o;
+#pragma unroll
+    for (int i = 0; i < W; ++i) o.v[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+    return o;
+}
+
+// (Elements past the row are +0.)
+template <int HOW, typename T>
 __device__ __forceinline__ Pack8<T> load_chunk(const T *p, int i, int tid, int threads, int64_t cols) {
-    Pack8<T> r;
-    if constexpr (VEC) {
-        const int64_t c = column<true>(i, 0, tid, threads);
+    const int64_t c = column<HOW>(i, 0, tid, threads);
+    if constexpr (HOW == kWide) {
         if (c + 8 <= cols) return load8(p + c, 8, true);
         return load8(c < cols ? p + c : p, c < cols ? int(cols - c) : 0, false);
+    } else if constexpr (HOW == kShifted) {
+        return c < cols ? load_shifted(p + c, c, cols - c) : load8(p, 0, false);
     } else {
+        Pack8<T> r;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int64_t c = column<false>(i, e, tid, threads);
-            r.set(e, c < cols ? p[c] : from_float<T>(0.0f));
+            const int64_t at = column<kSpread>(i, e, tid, threads);
+            r.set(e, at < cols ? p[at] : from_float<T>(0.0f));
         }
         return r;
     }
 }
 
-template <bool VEC, typename T>
+template <int HOW, typename T>
 __device__ __forceinline__ void store_chunk(T *p, const Pack8<T> &v, int i, int tid, int threads, int64_t cols) {
-    if constexpr (VEC) {
-        const int64_t c = column<true>(i, 0, tid, threads);
-        if (c < cols) store8(p + c, v, int(min(int64_t(8), cols - c)), true);
+    if constexpr (HOW != kSpread) {
+        const int64_t c = column<HOW>(i, 0, tid, threads);
+        if (c < cols) store8(p + c, v, int(min(int64_t(8), cols - c)), HOW == kWide);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int64_t c = column<false>(i, e, tid, threads);
+            const int64_t c = column<kSpread>(i, e, tid, threads);
             if (c < cols) p[c] = v.get(e);
         }
     }
 }
 
-// Eight weights as FP32; 1 where there are none, anything past the row.
-template <bool VEC, typename T>
+// Eight weights as FP32; 1 where there are none, +0 or 1 past the row.
+template <int HOW, typename T>
 __device__ __forceinline__ void load_weight(float (&o)[8], const void *w, int w_f32, int i, int tid, int threads, int64_t cols) {
     if (w == nullptr) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = 1.0f;
     } else if (w_f32) {
-        const Pack8<float> v = load_chunk<VEC>(static_cast<const float *>(w), i, tid, threads, cols);
+        const Pack8<float> v = load_chunk<HOW>(static_cast<const float *>(w), i, tid, threads, cols);
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = v.get(e);
     } else {
-        const Pack8<T> v = load_chunk<VEC>(static_cast<const T *>(w), i, tid, threads, cols);
+        const Pack8<T> v = load_chunk<HOW>(static_cast<const T *>(w), i, tid, threads, cols);
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = to_float(v.get(e));
     }
@@ -114,6 +149,13 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
+}
+
+// The larger of `m` and |t| as bits; a NaN is the largest.
+__device__ __forceinline__ uint32_t larger(uint32_t m, float t) {
+    float o;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(o) : "f"(__uint_as_float(m)), "f"(fabsf(t)));
+    return __float_as_uint(o);
 }
 
 // The sum of `a` and the largest `m` over the row's threads (a warp, or the CTA).
@@ -139,11 +181,11 @@ __device__ __forceinline__ float inverse_rms(float squares, float inv_cols, floa
 }
 
 // Row s of a chunk: x, or x + residual rounded to the type, which is also stored.
-template <bool VEC, typename T>
+template <int HOW, typename T>
 __device__ __forceinline__ Pack8<T> sum_chunk(const NormArgs &a, int64_t row, int i, int tid, int threads) {
-    Pack8<T> v = load_chunk<VEC>(static_cast<const T *>(a.x) + row * a.ldx, i, tid, threads, a.cols);
+    Pack8<T> v = load_chunk<HOW>(static_cast<const T *>(a.x) + row * a.ldx, i, tid, threads, a.cols);
     if (a.res != nullptr) {
-        const Pack8<T> r = load_chunk<VEC>(static_cast<const T *>(a.res) + row * a.ldr, i, tid, threads, a.cols);
+        const Pack8<T> r = load_chunk<HOW>(static_cast<const T *>(a.res) + row * a.ldr, i, tid, threads, a.cols);
         float f[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = __fadd_rn(to_float(v.get(e)), to_float(r.get(e)));
@@ -152,69 +194,98 @@ __device__ __forceinline__ Pack8<T> sum_chunk(const NormArgs &a, int64_t row, in
     return v;
 }
 
-// 127 t / a rounded to nearest, ties to even: the FP32 quotient `v` (within 2^-15) is
-// decided in 64 bits, where both products are exact, when it lies next to a border.
-__device__ __forceinline__ int code_of(float t, float a, float inverse) {
-    const float v = __fmul_rn(t, inverse);
-    float q = rintf(v);
-    if (fabsf(v - q) > 0.49995f) {
-        const float low = floorf(v);
-        const double d = 127.0 * double(t) - (double(low) + 0.5) * double(a);
-        q = d > 0.0 ? low + 1.0f : d < 0.0 ? low : 2.0f * rintf(0.5f * low + 0.25f);
-    }
-    return int(q);
+constexpr float kNear = 0.49999f;
+
+// 127 t / a rounded to nearest, ties to even, for a quotient next to a border: decided in 64
+// bits, where both products are exact.
+__device__ __noinline__ int border_code(float t, float a, float inverse) {
+    const float low = floorf(__fmul_rn(t, inverse));
+    const double d = 127.0 * double(t) - (double(low) + 0.5) * double(a);
+    return int(d > 0.0 ? low + 1.0f : d < 0.0 ? low : 2.0f * rintf(0.5f * low + 0.25f));
 }
 
-__device__ __forceinline__ float lift_of(float largest) { return largest < 0x1p-100f ? 0x1p100f : 1.0f; }
-
-// One chunk's outputs.  `r`: 1 / rms; 8 bits: `largest` the row's largest |t|.
-template <bool VEC, bool S8, typename T>
-__device__ __forceinline__ void put_chunk(const NormArgs &a, int64_t row, const Pack8<T> &s, float r, float largest,
-                                          float inverse, bool finite, int i, int tid, int threads) {
-    float w[8];
-    load_weight<VEC, T>(w, a.w, a.w_f32, i, tid, threads, a.cols);
-    if constexpr (!S8) {
-        float o[8];
+// One chunk's output in the element type; `r`: 1 / rms.
+template <int HOW, typename T>
+__device__ __forceinline__ void put_chunk(const NormArgs &a, int64_t row, const Pack8<T> &s, float r, int i, int tid, int threads) {
+    float w[8], o[8];
+    load_weight<HOW, T>(w, a.w, a.w_f32, i, tid, threads, a.cols);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = __fmul_rn(__fmul_rn(to_float(s.get(e)), r), w[e]);
-        store_chunk<VEC>(static_cast<T *>(a.y) + row * a.ldy, round8<T>(o), i, tid, threads, a.cols);
-    } else {
-        // (The smallest rows are lifted, exactly, so that 127 / a is a number.)
-        const float lift = lift_of(largest), a_lifted = __fmul_rn(largest, lift);
-        int q[8];
+    for (int e = 0; e < 8; ++e) o[e] = __fmul_rn(__fmul_rn(to_float(s.get(e)), r), w[e]);
+    store_chunk<HOW>(static_cast<T *>(a.y) + row * a.ldy, round8<T>(o), i, tid, threads, a.cols);
+}
+
+// One chunk's t = s w.
+template <int HOW, typename T>
+__device__ __forceinline__ void products(float (&t)[8], const NormArgs &a, const Pack8<T> &s, int i, int tid, int threads) {
+    load_weight<HOW, T>(t, a.w, a.w_f32, i, tid, threads, a.cols);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = __fmul_rn(to_float(s.get(e)), t[e]);
+}
+
+// Of a row in 8 bits: its largest |t|, 127 of which one is a code's step.  The smallest rows
+// are lifted, exactly, so that 127 / |t| is a number.
+struct CodeScale {
+    float largest, lift, inverse;  // (lifted)
+    bool blank;  // an infinity or NaN in the row, or nothing but zeros
+    __device__ __forceinline__ explicit CodeScale(uint32_t bits) {
+        const float a = __uint_as_float(bits);
+        lift = a < 0x1p-100f ? 0x1p100f : 1.0f;
+        largest = __fmul_rn(a, lift);
+        inverse = __fdiv_rn(127.0f, largest);
+        blank = bits >= kInfBits || bits == 0;
+    }
+};
+
+// One chunk's codes of t (lifted).  With 3 2^22 added the sum's low byte is the code of the
+// FP32 quotient, which is within 127 2^-24 of the quotient: its own code but for 2 in 10^5,
+// next to a border.
+template <int HOW>
+__device__ __forceinline__ void put_codes(const NormArgs &a, int64_t row, const float (&t)[8], const CodeScale &c, int i, int tid, int threads) {
+    uint32_t q[8];
+    float near = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float u = __fmaf_rn(t[e], c.inverse, 0x1.8p23f);
+        near = fmaxf(near, fabsf(__fmaf_rn(t[e], c.inverse, -__fsub_rn(u, 0x1.8p23f))));
+        q[e] = __float_as_uint(u);
+    }
+    if (c.blank) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] = 0;
+    } else if (near > kNear) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            q[e] = finite && largest > 0.0f
-                       ? code_of(__fmul_rn(__fmul_rn(to_float(s.get(e)), w[e]), lift), a_lifted, inverse)
-                       : 0;
-        int8_t *p = static_cast<int8_t *>(a.y) + row * a.ldy;
-        if constexpr (VEC) {
-            const int64_t c = column<true>(i, 0, tid, threads);
-            if (c + 8 <= a.cols) {
-                uint32_t lo = 0, hi = 0;
+            if (fabsf(__fmaf_rn(t[e], c.inverse, -rintf(__fmul_rn(t[e], c.inverse)))) > kNear)
+                q[e] = uint32_t(border_code(t[e], c.largest, c.inverse));
+    }
+    int8_t *p = static_cast<int8_t *>(a.y) + row * a.ldy;
+    if constexpr (HOW != kSpread) {
+        const int64_t at = column<HOW>(i, 0, tid, threads);
+        if (at + 8 <= a.cols) {
+            uint32_t two[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    lo |= (uint32_t(q[e]) & 255u) << (8 * e);
-                    hi |= (uint32_t(q[e + 4]) & 255u) << (8 * e);
-                }
-                *reinterpret_cast<uint2 *>(p + c) = make_uint2(lo, hi);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (c + e < a.cols) p[c + e] = int8_t(q[e]);
-            }
+            for (int e = 0; e < 4; ++e) two[e] = __byte_perm(q[2 * e], q[2 * e + 1], 0x0040);
+            *reinterpret_cast<uint2 *>(p + at) = make_uint2(__byte_perm(two[0], two[1], 0x5410), __byte_perm(two[2], two[3], 0x5410));
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int64_t c = column<false>(i, e, tid, threads);
-                if (c < a.cols) p[c] = int8_t(q[e]);
-            }
+            for (int e = 0; e < 8; ++e)
+                if (at + e < a.cols) p[at + e] = int8_t(q[e]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int64_t at = column<HOW>(i, e, tid, threads);
+            if (at < a.cols) p[at] = int8_t(q[e]);
         }
     }
 }
 
+__device__ __forceinline__ float scale_of(uint32_t largest, float r) {
+    return largest < kInfBits ? __fdiv_rn(__fmul_rn(__uint_as_float(largest), r), 127.0f) : __uint_as_float(0x7FC00000u);
+}
+
 // A row per CTA, or (WARP) per warp; CH chunks of eight elements per thread.
-template <typename T, bool S8, bool VEC, int CH, bool WARP>
+template <typename T, bool S8, int HOW, int CH, bool WARP>
 __global__ void __launch_bounds__(CH == 1 ? 1024 : 512) norm_kernel(const NormArgs a) {
     __shared__ uint32_t buf[64];
     griddep_wait();
@@ -223,8 +294,9 @@ __global__ void __launch_bounds__(CH == 1 ? 1024 : 512) norm_kernel(const NormAr
     const int64_t row = WARP ? int64_t(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32 : int64_t(blockIdx.x);
     if (row >= a.rows) return;  // (whole warps, and never with a CTA per row)
     Pack8<T> s[CH];
+    float t[CH][8];  // 8 bits: what is coded
 #pragma unroll
-    for (int i = 0; i < CH; ++i) s[i] = sum_chunk<VEC, T>(a, row, i, tid, threads);
+    for (int i = 0; i < CH; ++i) s[i] = sum_chunk<HOW, T>(a, row, i, tid, threads);
     float squares = 0.0f;
     uint32_t largest = 0;
 #pragma unroll
@@ -232,31 +304,34 @@ __global__ void __launch_bounds__(CH == 1 ? 1024 : 512) norm_kernel(const NormAr
 #pragma unroll
         for (int e = 0; e < 8; ++e) squares = __fmaf_rn(to_float(s[i].get(e)), to_float(s[i].get(e)), squares);
         if constexpr (S8) {
-            float w[8];
-            load_weight<VEC, T>(w, a.w, a.w_f32, i, tid, threads, a.cols);
+            products<HOW, T>(t[i], a, s[i], i, tid, threads);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                largest = max(largest, column<VEC>(i, e, tid, threads) < a.cols
-                                           ? __float_as_uint(__fmul_rn(to_float(s[i].get(e)), w[e])) & 0x7FFFFFFFu
-                                           : 0u);
+            for (int e = 0; e < 8; ++e) largest = larger(largest, t[i][e]);
         }
         if (a.res != nullptr)
-            store_chunk<VEC>(static_cast<T *>(a.sum) + row * a.lds, s[i], i, tid, threads, a.cols);
+            store_chunk<HOW>(static_cast<T *>(a.sum) + row * a.lds, s[i], i, tid, threads, a.cols);
     }
     reduce_row<WARP, S8>(squares, largest, buf);
     const float r = inverse_rms(squares, a.inv_cols, a.eps);
-    const float big = __uint_as_float(largest);
-    const bool finite = largest < kInfBits;
-    const float inverse = S8 ? __fdiv_rn(127.0f, __fmul_rn(big, lift_of(big))) : 0.0f;
+    if constexpr (S8) {
+        const CodeScale c(largest);
+        if (c.lift != 1.0f)
 #pragma unroll
-    for (int i = 0; i < CH; ++i) put_chunk<VEC, S8>(a, row, s[i], r, big, inverse, finite, i, tid, threads);
-    if (S8 && tid == 0)
-        a.scale[row] = finite ? __fdiv_rn(__fmul_rn(big, r), 127.0f) : __uint_as_float(0x7FC00000u);
+            for (int i = 0; i < CH; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t[i][e] = __fmul_rn(t[i][e], c.lift);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) put_codes<HOW>(a, row, t[i], c, i, tid, threads);
+        if (tid == 0) a.scale[row] = scale_of(largest, r);
+    } else {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) put_chunk<HOW>(a, row, s[i], r, i, tid, threads);
+    }
 }
 
 // Rows beyond the registers: s is read again after the sums (by the thread that
 // stored it).
-template <typename T, bool S8, bool VEC>
+template <typename T, bool S8, int HOW>
 __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
     __shared__ uint32_t buf[64];
     griddep_wait();
@@ -267,34 +342,36 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
     float squares = 0.0f;
     uint32_t largest = 0;
     for (int i = 0; i < chunks; ++i) {
-        const Pack8<T> s = sum_chunk<VEC, T>(a, row, i, tid, threads);
+        const Pack8<T> s = sum_chunk<HOW, T>(a, row, i, tid, threads);
         float part = 0.0f;  // (chunk by chunk: long sums stay exact to a few ulps)
 #pragma unroll
         for (int e = 0; e < 8; ++e) part = __fmaf_rn(to_float(s.get(e)), to_float(s.get(e)), part);
         squares += part;
         if constexpr (S8) {
-            float w[8];
-            load_weight<VEC, T>(w, a.w, a.w_f32, i, tid, threads, a.cols);
+            float t[8];
+            products<HOW, T>(t, a, s, i, tid, threads);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                largest = max(largest, column<VEC>(i, e, tid, threads) < a.cols
-                                           ? __float_as_uint(__fmul_rn(to_float(s.get(e)), w[e])) & 0x7FFFFFFFu
-                                           : 0u);
+            for (int e = 0; e < 8; ++e) largest = larger(largest, t[e]);
         }
-        if (a.res != nullptr) store_chunk<VEC>(static_cast<T *>(a.sum) + row * a.lds, s, i, tid, threads, a.cols);
+        if (a.res != nullptr) store_chunk<HOW>(static_cast<T *>(a.sum) + row * a.lds, s, i, tid, threads, a.cols);
     }
     reduce_row<false, S8>(squares, largest, buf);
     const float r = inverse_rms(squares, a.inv_cols, a.eps);
-    const float big = __uint_as_float(largest);
-    const bool finite = largest < kInfBits;
-    const float inverse = S8 ? __fdiv_rn(127.0f, __fmul_rn(big, lift_of(big))) : 0.0f;
+    const CodeScale c(largest);
     const T *again = a.res != nullptr ? static_cast<const T *>(a.sum) + row * a.lds : static_cast<const T *>(a.x) + row * a.ldx;
     for (int i = 0; i < chunks; ++i) {
-        const Pack8<T> s = load_chunk<VEC>(again, i, tid, threads, a.cols);
-        put_chunk<VEC, S8>(a, row, s, r, big, inverse, finite, i, tid, threads);
+        const Pack8<T> s = load_chunk<HOW>(again, i, tid, threads, a.cols);
+        if constexpr (S8) {
+            float t[8];
+            products<HOW, T>(t, a, s, i, tid, threads);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] = __fmul_rn(t[e], c.lift);
+            put_codes<HOW>(a, row, t, c, i, tid, threads);
+        } else {
+            put_chunk<HOW>(a, row, s, r, i, tid, threads);
+        }
     }
-    if (S8 && tid == 0)
-        a.scale[row] = finite ? __fdiv_rn(__fmul_rn(big, r), 127.0f) : __uint_as_float(0x7FC00000u);
+    if (S8 && tid == 0) a.scale[row] = scale_of(largest, r);
 }
 
 // ------------------------------------------------------------ gradient
@@ -311,11 +388,11 @@ __device__ __forceinline__ void reduce_two(float &p, float &q, float2 *buf) {
     q = warp_sum(v.y);
 }
 
-template <typename T, bool VEC>
+template <typename T, int HOW>
 __device__ __forceinline__ void grad_chunk(const GradArgs &a, int64_t row, const Pack8<T> &s, const Pack8<T> &dy, float r,
                                            float m, float (&acc)[8], int i, int tid, int threads) {
     float w[8], o[8];
-    load_weight<VEC, T>(w, a.w, a.w_f32, i, tid, threads, a.cols);
+    load_weight<HOW, T>(w, a.w, a.w_f32, i, tid, threads, a.cols);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const float sv = to_float(s.get(e)), dv = to_float(dy.get(e));
@@ -324,11 +401,11 @@ __device__ __forceinline__ void grad_chunk(const GradArgs &a, int64_t row, const
         acc[e] = __fmaf_rn(dv, u, acc[e]);
     }
     if (a.ds != nullptr) {
-        const Pack8<T> d = load_chunk<VEC>(static_cast<const T *>(a.ds) + row * a.ldds, i, tid, threads, a.cols);
+        const Pack8<T> d = load_chunk<HOW>(static_cast<const T *>(a.ds) + row * a.ldds, i, tid, threads, a.cols);
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = __fadd_rn(o[e], to_float(d.get(e)));
     }
-    store_chunk<VEC>(static_cast<T *>(a.dx) + row * a.lddx, round8<T>(o), i, tid, threads, a.cols);
+    store_chunk<HOW>(static_cast<T *>(a.dx) + row * a.lddx, round8<T>(o), i, tid, threads, a.cols);
 }
 
 // 16 bytes to shared memory, `n` of them from global memory and zeros after them.
@@ -496,7 +573,7 @@ __global__ void __launch_bounds__(1024) grad_ring_kernel(const GradArgs a, int s
 
 // Longer rows: the sums of every row first, then columns in pieces of 8 per thread
 // (blockIdx.x) for the rows of each blockIdx.y.
-template <typename T, bool VEC>
+template <typename T, int HOW>
 __global__ void __launch_bounds__(1024) grad_stats_kernel(const GradArgs a) {
     __shared__ float2 buf[32];
     griddep_wait();
@@ -506,10 +583,10 @@ __global__ void __launch_bounds__(1024) grad_stats_kernel(const GradArgs a) {
     const int chunks = int((a.cols + int64_t(8) * threads - 1) / (int64_t(8) * threads));
     float squares = 0.0f, gs = 0.0f;
     for (int i = 0; i < chunks; ++i) {
-        const Pack8<T> s = load_chunk<VEC>(static_cast<const T *>(a.s) + row * a.lds, i, tid, threads, a.cols);
-        const Pack8<T> dy = load_chunk<VEC>(static_cast<const T *>(a.dy) + row * a.lddy, i, tid, threads, a.cols);
+        const Pack8<T> s = load_chunk<HOW>(static_cast<const T *>(a.s) + row * a.lds, i, tid, threads, a.cols);
+        const Pack8<T> dy = load_chunk<HOW>(static_cast<const T *>(a.dy) + row * a.lddy, i, tid, threads, a.cols);
         float w[8], p = 0.0f, q = 0.0f;
-        load_weight<VEC, T>(w, a.w, a.w_f32, i, tid, threads, a.cols);
+        load_weight<HOW, T>(w, a.w, a.w_f32, i, tid, threads, a.cols);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float sv = to_float(s.get(e));
@@ -524,7 +601,7 @@ __global__ void __launch_bounds__(1024) grad_stats_kernel(const GradArgs a) {
     if (tid == 0) a.stat[row] = make_float2(r, __fmul_rn(r, __fmul_rn(gs, a.inv_cols)));
 }
 
-template <typename T, bool VEC>
+template <typename T, int HOW>
 __global__ void __launch_bounds__(256) grad_columns_kernel(const GradArgs a) {
     griddep_wait();
     griddep_launch_dependents();
@@ -533,15 +610,15 @@ __global__ void __launch_bounds__(256) grad_columns_kernel(const GradArgs a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
     for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
-        const Pack8<T> s = load_chunk<VEC>(static_cast<const T *>(a.s) + row * a.lds, i, tid, threads, a.cols);
-        const Pack8<T> dy = load_chunk<VEC>(static_cast<const T *>(a.dy) + row * a.lddy, i, tid, threads, a.cols);
+        const Pack8<T> s = load_chunk<HOW>(static_cast<const T *>(a.s) + row * a.lds, i, tid, threads, a.cols);
+        const Pack8<T> dy = load_chunk<HOW>(static_cast<const T *>(a.dy) + row * a.lddy, i, tid, threads, a.cols);
         const float2 st = a.stat[row];
-        grad_chunk<T, VEC>(a, row, s, dy, st.x, st.y, acc, i, tid, threads);
+        grad_chunk<T, HOW>(a, row, s, dy, st.x, st.y, acc, i, tid, threads);
     }
     float *part = a.part + int64_t(blockIdx.y) * a.cols;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const int64_t c = column<VEC>(i, e, tid, threads);
+        const int64_t c = column<HOW>(i, e, tid, threads);
         if (c < a.cols) part[c] = acc[e];
     }
 }
@@ -609,20 +686,20 @@ int round32(int64_t n) { return int((n + 31) / 32 * 32); }
 // A few rows take a thread per eight elements, so that a row is one round of loads; many
 // take four rounds per thread, whose loads are in flight together; rows of up to 1024
 // elements a warp each.
-template <typename T, bool S8, bool VEC>
+template <typename T, bool S8, int HOW>
 cudaError_t run_norm(const NormArgs &a, int sms, cudaStream_t s) {
     const int64_t chunks = (a.cols + 7) / 8;
     if (chunks > 4 * 512 && !(chunks <= 1024 && a.rows <= sms))
-        return launch_norm(norm_long_kernel<T, S8, VEC>, dim3(unsigned(a.rows)), 1024, s, a);
+        return launch_norm(norm_long_kernel<T, S8, HOW>, dim3(unsigned(a.rows)), 1024, s, a);
     if (a.rows > 2 * sms && chunks <= 128) {
         const dim3 grid(unsigned((a.rows + 7) / 8));
-        return chunks <= 32 ? launch_norm(norm_kernel<T, S8, VEC, 1, true>, grid, 256, s, a)
-                            : launch_norm(norm_kernel<T, S8, VEC, 4, true>, grid, 256, s, a);
+        return chunks <= 32 ? launch_norm(norm_kernel<T, S8, HOW, 1, true>, grid, 256, s, a)
+                            : launch_norm(norm_kernel<T, S8, HOW, 4, true>, grid, 256, s, a);
     }
     const dim3 grid = dim3(unsigned(a.rows));
     if ((a.rows <= sms && chunks <= 1024) || chunks <= 32)
-        return launch_norm(norm_kernel<T, S8, VEC, 1, false>, grid, round32(chunks), s, a);
-    return launch_norm(norm_kernel<T, S8, VEC, 4, false>, grid, round32((chunks + 3) / 4), s, a);
+        return launch_norm(norm_kernel<T, S8, HOW, 1, false>, grid, round32(chunks), s, a);
+    return launch_norm(norm_kernel<T, S8, HOW, 4, false>, grid, round32((chunks + 3) / 4), s, a);
 }
 
 template <bool S8>
@@ -632,11 +709,14 @@ int start_norm(NormArgs a, int type, int out_esize, cudaStream_t s) {
     if (rc) return rc;
     const int es = bytes_of(type);
     if (a.rows == 1) a.ldx = a.ldr = a.lds = a.ldy = 0;  // (one row has no pitch)
-    const bool vec = wide(a.x, a.ldx, es) && (!a.res || (wide(a.res, a.ldr, es) && wide(a.sum, a.lds, es))) &&
-                     (S8 ? aligned_to(a.y, 8) && a.ldy % 8 == 0 : wide(a.y, a.ldy, out_esize)) && aligned_to(a.w, 16);
+    const bool out = S8 ? aligned_to(a.y, 8) && a.ldy % 8 == 0 : wide(a.y, a.ldy, out_esize);
+    const bool vec = out && wide(a.x, a.ldx, es) && (!a.res || (wide(a.res, a.ldr, es) && wide(a.sum, a.lds, es))) && aligned_to(a.w, 16);
     auto go = [&](auto t) {
         using T = decltype(t);
-        return vec ? run_norm<T, S8, true>(a, sms, s) : run_norm<T, S8, false>(a, sms, s);
+        if (vec) return run_norm<T, S8, kWide>(a, sms, s);
+        if constexpr (S8)  // codes are stored eight at a time, and nothing else is
+            if (out && !a.res) return run_norm<T, S8, kShifted>(a, sms, s);
+        return run_norm<T, S8, kSpread>(a, sms, s);
     };
     const cudaError_t e = type == PTC_OUT_F32 ? go(float()) : type == PTC_OUT_BF16 ? go(__nv_bfloat16()) : go(__half());
     return e == cudaSuccess ? PTC_OK : fail_launch(e, "norm launch");
@@ -724,7 +804,7 @@ RingShape ring_shape(int64_t chunks, int arrays, size_t esize) {
     return g;
 }
 
-template <typename T, bool VEC>
+template <typename T, int HOW>
 cudaError_t run_grad(GradArgs a, int sms, float *dw, cudaStream_t s) {
     const int64_t chunks = (a.cols + 7) / 8;
     int parts;
@@ -732,9 +812,9 @@ cudaError_t run_grad(GradArgs a, int sms, float *dw, cudaStream_t s) {
     if (grad_long(a.cols)) {
         const int64_t pieces = (chunks + 255) / 256;
         parts = int(std::min<int64_t>(grad_parts(a.rows), std::max<int64_t>(1, 8 * int64_t(sms) / pieces)));
-        e = launch_norm(grad_stats_kernel<T, VEC>, dim3(unsigned(a.rows)), 1024, s, a);
-        if (e == cudaSuccess) e = launch_norm(grad_columns_kernel<T, VEC>, dim3(unsigned(pieces), unsigned(parts)), 256, s, a);
-    } else if (const RingShape g = ring_shape(chunks, a.ds ? 3 : 2, sizeof(T)); VEC && g.weights + g.row <= kRingMost) {
+        e = launch_norm(grad_stats_kernel<T, HOW>, dim3(unsigned(a.rows)), 1024, s, a);
+        if (e == cudaSuccess) e = launch_norm(grad_columns_kernel<T, HOW>, dim3(unsigned(pieces), unsigned(parts)), 256, s, a);
+    } else if (const RingShape g = ring_shape(chunks, a.ds ? 3 : 2, sizeof(T)); HOW == kWide && g.weights + g.row <= kRingMost) {
         // Four rows in flight per CTA, fewer where they do not fit; up to three CTAs per SM.
         const int slots = int(std::min<size_t>(4, (kRingMost - g.weights) / g.row));
         const size_t smem = slots * g.row + g.weights;
