@@ -462,7 +462,8 @@ int gemm_a16_fp4(int64_t M, int64_t N, int64_t K, int type, const void *X, int64
  * The workspace holds the activations as the tensor cores take them, made once for all
  * CTAs: gemm_a16_s4_workspace(M, K) bytes, 16-byte aligned, and no other call's until this
  * one is done.  With NULL (or for sizes of which that gives 0, up to two tokens) every CTA makes
- * its own, with the same result.
+ * its own, with the same result; so it does where a few tokens have few codes, whose
+ * workspace is not touched.
  */
 int64_t gemm_a16_s4_workspace(int64_t M, int64_t K);
 int gemm_a16_s4(int64_t M, int64_t N, int64_t K, int type, const void *X, int64_t ldx, const void *W, int64_t ldw,
@@ -761,7 +762,10 @@ int ptc_last_conversion(int *mode);
  *                  size, 1, 2, 4 or 8.  A pair of these that the sizes do not allow
  *                  (each share has at least 256 of K, and a share's activations fit
  *                  their buffer) is not taken.
- *   "s4_tokens_rows", "s4_tokens_split" the same of gemm_a16_s4.
+ *   "s4_tokens_rows" gemm_a16_s4's row groups per CTA, whose 16 / this many shares of K
+ *                  run beside each other: 0 (default) by size, 1, 2, 4, 8 or 16.
+ *   "s4_tokens_split" gemm_a16_s4's CTAs of a cluster that share K: 0 (default) by size,
+ *                  1, 2, 4 or 8.
  *   "s4_tokens_tiles" gemm_a16_s4's tiles of 16 rows per row group: 0 (default) by size,
  *                  1 or 2.
  * No accepted value of any key changes an INT8 or INT4 result. */

@@ -5,14 +5,18 @@
 // products run on mma.sync m16n8k16 with 16 rows of the weights as one operand and eight
 // tokens as the other (s4.cuh); sums stay in FP32.
 //
-// Layout.  The eight warps of a CTA are R row groups x S shares of K; a warp owns 16 MT
+// Layout.  The sixteen warps of a CTA are R row groups x S shares of K; a warp owns 16 MT
 // rows and every S-th stage of 256 codes.  One of its lanes brings them to the warp's own
 // ring in shared memory: the rows by TMA, whole 128-byte lines, and their scales by bulk
 // copies, so that no warp waits for another and the others spend no instruction on it.
-// The tokens' activations are made operands once per CTA, in chunks of K that fit, two of
-// them in shared memory.  The shares' sums are added in order there, and where that leaves
+// A few activations are made operands by every CTA; more by s4_operands_kernel once, and
+// every CTA copies them, in chunks of K that fit, two of them in
+// shared memory.  The shares' sums are added in order there, and where that leaves
 // SMs idle K is also shared by a cluster of up to eight CTAs, whose sums are added in rank
 // order through distributed shared memory.
+//
+// What bounds it is the issue of instructions, not the weights' bytes, but for large
+// matrices and one token; @TOK@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -338,7 +342,10 @@ __global__ void __launch_bounds__(kThreads4, 1) s4_kernel(const __grid_constant_
 constexpr int64_t kMaxDim4 = int64_t(1) << 30;
 constexpr int64_t kMaxLd4 = int64_t(1) << 36;
 constexpr int kMaxDev4 = 64;
-constexpr int64_t kAlone4 = 2;  // up to so many tokens every CTA makes their operands itself
+// Up to so many tokens, or stages of all tokens, every CTA makes the operands itself.  (A kernel
+// for them takes 0.5 us, and 0.7 of the caller's time: 1024 codes of 8 tokens 4.6 us instead of
+// 5.1, 4096 of 4 5.9 either way, 4096 of 5 6.9 instead of 5.9, 8192 of 16 51 instead of 12.)
+constexpr int64_t kAlone4 = 2, kAloneStages4 = 64;
 std::atomic<int> g_s4_rows{0};   // "s4_tokens_rows": 0 by size, 1, 2, 4, 8, 16
 std::atomic<int> g_s4_split{0};  // "s4_tokens_split": 0 by size, 1, 2, 4, 8
 std::atomic<int> g_s4_tiles{0};  // "s4_tokens_tiles": 0 by size, 1, 2
@@ -616,7 +623,7 @@ extern "C" int gemm_a16_s4(int64_t M, int64_t N, int64_t K, int type, const void
     a.wait_limit = wait_limit_ns();
     a.xvec = at_multiple(X, 16) && (M == 1 || ldx % 8 == 0);
     a.bf16_scales = scale_type == PTC_OUT_BF16;
-    if (workspace && need > 0) {
+    if (workspace && need > 0 && M * a.stages > kAloneStages4) {
         a.xs = static_cast<uint8_t *>(workspace);
         a.xps = reinterpret_cast<float2 *>(a.xs + M * a.stages * (2 * kS4XBytes));
     }

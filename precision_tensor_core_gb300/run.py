@@ -10,7 +10,10 @@ to profile beside ours; it is not part of the library.  `mxfp4` and `nvfp4` run
 the product of two quantised 4-bit matrices, `quant_mxfp4` / `quant_nvfp4` the
 quantisation of an N x N bfloat16 matrix by rows, `quant_both` by rows and columns
 with stochastic rounding, `dropout` dropout with a residual, `tokens_mxfp4` /
-`tokens_nvfp4` 16 tokens of bfloat16 / binary16 with 2N x N 4-bit weights.  `--tune key=value`
+`tokens_nvfp4` 16 tokens of bfloat16 / binary16 with 2N x N 4-bit weights.  `norm`,
+`norm_s8` and `norm_gradient` run the norm of an N x N bfloat16 matrix (the first and last
+with a residual), `tokens_s4` 16 tokens with 2N x N 4-bit integer weights, `experts_s4` 16
+tokens of width N / 2 through 4 each of 32 experts of N / 4.  `--tune key=value`
 (repeatable) sets a library tuning knob first (ptc_set_tuning), e.g.
 `--tune in_ring=0` to profile the separate operand-conversion pass.
 """
@@ -56,9 +59,43 @@ def fp4_workload(prec, n):
     return lambda: ptc.quantize_fp4(x, fmt)
 
 
+S4 = ["norm", "norm_s8", "norm_gradient", "tokens_s4", "experts_s4"]
+
+
+def s4_workload(prec, n):
+    """The call of one of the norm and 4-bit integer weight workloads on seeded data."""
+    import torch
+
+    import precision_tensor_core_gb300 as ptc
+    g = torch.Generator(device="cuda").manual_seed(n)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g, device="cuda").to(torch.bfloat16)
+
+    def weights(rows, k, *experts):
+        codes = torch.randint(0, 256, (*experts, rows, -(-k // 32) * 16), generator=g, device="cuda", dtype=torch.uint8)
+        scales = torch.rand(*experts, rows, -(-k // 128), generator=g, device="cuda").to(torch.bfloat16)
+        return ptc.S4Matrix(codes, ptc.S4Matrix.tile_scales(scales), k, 128)
+
+    if prec == "tokens_s4":
+        w, x = weights(2 * n, n), normal(16, n)
+        return lambda: ptc.matmul_a16_s4(x, w)
+    if prec == "experts_s4":
+        hidden, inner, experts = n // 2, n // 4, 32
+        gate_up, down = weights(2 * inner, hidden, experts), weights(hidden, inner, experts)
+        x, router = normal(16, hidden), normal(experts, hidden)
+        return lambda: ptc.moe_a16_s4(x, router, gate_up, down, 4)
+    x, r, w = normal(n, n), normal(n, n), normal(n)
+    if prec == "norm":
+        return lambda: ptc.rms_norm(x, w, residual=r)
+    if prec == "norm_s8":
+        return lambda: ptc.rms_norm_s8(x, w)
+    return lambda: ptc.rms_norm_backward(r, x, w, dsum=r)
+
+
 def main():
     p = argparse.ArgumentParser()
-    p.add_argument("--prec", choices=["f16", "s8", "s4", "s8_noalloc", "cublas_f16", *FP4], default="f16")
+    p.add_argument("--prec", choices=["f16", "s8", "s4", "s8_noalloc", "cublas_f16", *FP4, *S4], default="f16")
     p.add_argument("--n", type=int, default=8192)
     p.add_argument("--reps", type=int, default=2)
     p.add_argument("--tune", action="append", default=[], metavar="KEY=VALUE")
@@ -79,6 +116,8 @@ def main():
     n = a.n
     if a.prec in FP4:
         run = fp4_workload(a.prec, n)
+    elif a.prec in S4:
+        run = s4_workload(a.prec, n)
     elif a.prec == "cublas_f16":
         A, B = datagen.f16_operands(n, "normal")
         Ad = torch.from_numpy(A.view(np.float16)).to(dev)
