@@ -9,7 +9,7 @@
 // experts_kernel finds the experts and their tokens from the logits, which is less than
 // handing them over.  It then takes items: first, by tickets, 32 rows of h of an expert (32
 // rows of gate and 32 of up, the eight warps two row halves by four shares of K), and when
-// those are gone 16 rows of y of all experts, or of a share of their codes, which the warps share
+// those are gone 32 rows of y of all experts, or of a share of their codes, which the warps share
 // evenly.  The second kind waits until every item of the first kind is done.  A ticket is
 // taken by a CTA that runs, and a CTA that waits holds no item of the first kind, so the wait
 // ends whatever else holds the GPU.  h passes through memory as one or two binary16 numbers
@@ -42,8 +42,8 @@ constexpr int kMoeWarps = 8, kMoeThreads = 32 * kMoeWarps;
 constexpr int kMaxTokens = 64, kMaxExperts = 512, kMaxTopK = 32, kMaxPairs = 512;
 constexpr int kTile = 8;  // tokens of an expert per item
 constexpr int kLogits = 4;  // tokens per CTA of the router
-constexpr int kMaxRing = 6;  // places of a warp's ring, each a stage of 16 rows: two for rows of h, one for rows of y
-constexpr int kMaxParts4 = 2048;  // shares of all tiles of 16 rows of y, where they are shared
+constexpr int kMaxRing = 6;  // places of a warp's ring, each a stage of 16 rows; taken in pairs
+constexpr int kMaxParts4 = 1024;  // shares of all tiles of 32 rows of y, where they are shared
 
 __device__ uint32_t g_moe_error = 0;
 
@@ -67,8 +67,8 @@ struct MoeArgs {
     int h_halves, h_stages, h_blocks;  // of inner; blocks of 32
     int places, ring_bytes, scale_bytes;  // of a warp's ring (even); of all warps' codes; of a place's scales and zeros
     // Workspace.
-    uint32_t *counters;   // tickets, items of the first kind that are done; shares of 16 rows of y that are
-    float *parts;         // sums of shares of rows of y: [share][tile of rows][token][16]
+    uint32_t *counters;   // tickets, items of the first kind that are done; shares of 32 rows of y that are
+    float *parts;         // sums of shares of rows of y: [share][tile of rows][token][32]
     float *logits;        // [tokens][experts]
     uint8_t *xs;          // [token][stage] operands
     float2 *xps;          // [token][block] factors and sums
@@ -161,7 +161,7 @@ struct Routing {
     uint8_t tile_count[kMaxPairs];
     int tiles;
     uint32_t ticket[4];
-    bool last;  // of the shares of 16 rows of y
+    bool last;  // of the shares of 32 rows of y
 };
 struct RoutingWork {  // in the ring's place, before it is used
     uint32_t mask[kMaxExperts][2];   // tokens of an expert
@@ -316,7 +316,7 @@ struct Bring {
     int tile, st;     // the next stage's tile of pairs and stage
     int row;          // the warp's first row of h, or the item's of y
     int expert;       // the tile's
-    const uint8_t *scales, *up_scales;  // of the rows' tiles, from group 0
+    const uint8_t *scales, *more_scales;  // of the tiles of the first and second 16 rows, from group 0
 };
 
 template <typename X, int UNIT, bool ODD>
@@ -359,15 +359,18 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     route(a, r, *reinterpret_cast<RoutingWork *>(smem));
     if (threadIdx.x == 0) r.ticket[0] = asked_ticket;
 
-    const int units = r.tiles * a.h_stages;  // stages of 16 rows of y, of all tiles of pairs
-    const int row_tiles = (a.hidden + 15) / 16;
-    // Shares of these stages that are items of their own: as many as give every CTA one where
-    // there are CTAs enough; otherwise (or with 60% of a round's CTAs idle) for three rounds.
-    int shares = 1;
+    const int units = r.tiles * a.h_stages;  // stages of 32 rows of y, of all tiles of pairs
+    const int row_tiles = (a.hidden + 31) / 32;
+    // Shares of these stages that are items of their own: what takes the least stages of a warp
+    // in all rounds, two more per item.
     const int grid = int(gridDim.x);
-    while (shares < 8 && row_tiles * shares * 2 <= kMaxParts4 && units >= 16 * shares &&
-           (row_tiles <= grid ? row_tiles * shares * 2 <= grid : row_tiles * shares < 3 * grid))
-        shares *= 2;
+    int shares = 1;
+    {
+        const int n = (lane & 7) + 1, items = row_tiles * n, warps = n * kMoeWarps;
+        const uint32_t cost = uint32_t((items + grid - 1) / grid) * uint32_t((units + warps - 1) / warps + 2);
+        const bool may = n == 1 || (items <= kMaxParts4 && cost < 1u << 28);
+        shares = int(__reduce_min_sync(0xFFFFFFFFu, may ? min(cost, (1u << 28) - 1) * 8u + uint32_t(n - 1) : ~0u) & 7u) + 1;
+    }
     // Items of the first kind are taken by tickets, which end the wait for them: whoever waits has
     // none that is not done.  Those of the second kind are every grid-th from this CTA's own number.
     const int first_items = r.tiles * a.h_blocks, second_items = row_tiles * shares;
@@ -414,17 +417,18 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
             b.left = (a.stages - share + 3) / 4;  // share, share + 4, ...
             b.expert = r.tile_expert[b.tile];
             b.scales = tile_scales(a.gate_up, b.expert, b.row / 16);
-            b.up_scales = tile_scales(a.gate_up, b.expert, (a.inner + b.row) / 16);
+            b.more_scales = tile_scales(a.gate_up, b.expert, (a.inner + b.row) / 16);
         } else {
             int u0, u1;
             units_of((item - first_items) / row_tiles, u0, u1);
             b.second_kind = 1;
-            b.row = (item - first_items) % row_tiles * 16;
+            b.row = (item - first_items) % row_tiles * 32;
             b.tile = u0 / a.h_stages;
             b.st = u0 - b.tile * a.h_stages;
             b.left = u1 - u0;
             b.expert = r.tile_expert[min(b.tile, r.tiles - 1)];
             b.scales = tile_scales(a.down, b.expert, b.row / 16);
+            b.more_scales = tile_scales(a.down, b.expert, b.row / 16 + 1);
         }
         return b;
     };
@@ -435,9 +439,9 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     int bring_round = 0, into = 0, asked = 0, taken = 0;  // (in places)
     auto issue = [&](int round, bool ahead) {
         if (b.left == 0 && bring_round == round && ahead) b = begin(++bring_round);
-        const int need = b.second_kind ? 1 : 2;
-        if (b.left == 0 || asked - taken + need > a.places) return false;
+        if (b.left == 0 || asked - taken + 2 > a.places) return false;
         if (lane == 0) {
+            const CUtensorMap *const tm = b.second_kind ? &tm_down : &tm_up;
             const int groups = b.second_kind ? a.down.groups : a.gate_up.groups;
             const int64_t zeros = b.second_kind ? down_zeros : up_zeros;
             const int g0 = a.per_group == 1 ? 2 * b.st * SG : 2 * b.st / a.per_group;
@@ -446,22 +450,21 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
             uint64_t *const bar = &st.full[warp][into];
             const uint8_t *const from = b.scales + g0 * 32;
             mbar_arrive_expect_tx(bar, kS4TileBytes + both);
-            tma_load_rows(codes, b.second_kind ? &tm_down : &tm_up, bar, b.st * kS4RowBytes, b.row, b.expert);
+            tma_load_rows(codes, tm, bar, b.st * kS4RowBytes, b.row, b.expert);
             bulk_copy(scales, from, bytes, bar);
             if (zeros) bulk_copy(scales + ZEROS, from + zeros, bytes, bar);
-            if (!b.second_kind) {
-                // (up's rows may begin in the middle of a tile and end in the next one)
-                const uint32_t up = scales + a.scale_bytes;
-                const uint8_t *const more = b.up_scales + g0 * 32;
-                const bool next = ODD && (a.inner + b.row) / 16 + 1 < a.gate_up.tiles;
-                mbar_arrive_expect_tx(bar + 1, kS4TileBytes + (next ? 2 * both : both));
-                tma_load_rows(codes + CODES, &tm_up, bar + 1, b.st * kS4RowBytes, a.inner + b.row, b.expert);
-                bulk_copy(up, more, bytes, bar + 1);
-                if (zeros) bulk_copy(up + ZEROS, more + zeros, bytes, bar + 1);
-                if (next) {
-                    bulk_copy(up + SCALES, more + groups * 32, bytes, bar + 1);
-                    if (zeros) bulk_copy(up + ZEROS + SCALES, more + groups * 32 + zeros, bytes, bar + 1);
-                }
+            // (up's rows may begin in the middle of a tile and end in the next one)
+            const uint32_t second = scales + a.scale_bytes;
+            const uint8_t *const more = b.more_scales + g0 * 32;
+            const int row = b.second_kind ? b.row + 16 : a.inner + b.row;
+            const bool next = ODD && !b.second_kind && row / 16 + 1 < a.gate_up.tiles;
+            mbar_arrive_expect_tx(bar + 1, kS4TileBytes + (next ? 2 * both : both));
+            tma_load_rows(codes + CODES, tm, bar + 1, b.st * kS4RowBytes, row, b.expert);
+            bulk_copy(second, more, bytes, bar + 1);
+            if (zeros) bulk_copy(second + ZEROS, more + zeros, bytes, bar + 1);
+            if (next) {
+                bulk_copy(second + SCALES, more + groups * 32, bytes, bar + 1);
+                if (zeros) bulk_copy(second + ZEROS + SCALES, more + groups * 32 + zeros, bytes, bar + 1);
             }
         }
         --b.left;
@@ -471,15 +474,17 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                 ++b.tile;
                 if (b.left > 0) {
                     const int e = r.tile_expert[b.tile];
-                    b.scales += int64_t(e - b.expert) * a.down.tiles * a.down.groups * 32;
+                    const int64_t to = int64_t(e - b.expert) * a.down.tiles * a.down.groups * 32;
+                    b.scales += to;
+                    b.more_scales += to;
                     b.expert = e;
                 }
             }
         } else {
             b.st += 4;
         }
-        asked += need;
-        into += need;
+        asked += 2;
+        into += 2;
         if (into == a.places) into = 0;
         return true;
     };
@@ -601,9 +606,8 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                 if (PARTS == 2) *reinterpret_cast<__half *>(p + 2 * kS4XBytes) = lo;
                 if (lane == 0) a.hps[pair * a.h_stages * 8 + ib] = ps;
             }
-            __threadfence();
             __syncthreads();
-            if (threadIdx.x == 0 && item != a.stall)
+            if (threadIdx.x == 0 && item != a.stall)  // (released for the whole CTA)
                 asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.counters + 1) : "memory");
         } else {
             // ------------------------------------------------ rows of y
@@ -613,17 +617,19 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                 if (st.abort.flag) break;
                 ready = true;
             }
-            const int part = (item - first_items) / row_tiles, row_tile = (item - first_items) % row_tiles, row0 = row_tile * 16;
+            const int part = (item - first_items) / row_tiles, row_tile = (item - first_items) % row_tiles, row0 = row_tile * 32;
             int u0, u1;
             units_of(part, u0, u1);
-            for (int i = lane; i < a.tokens * 16; i += 32) sums[warp * (a.tokens * 16) + i] = 0.0f;
+            for (int i = lane; i < a.tokens * 32; i += 32) sums[warp * (a.tokens * 32) + i] = 0.0f;
             __syncwarp();
-            float tot[1][1][4] = {{{0.0f, 0.0f, 0.0f, 0.0f}}};
+            float tot[2][1][4] = {{{0.0f, 0.0f, 0.0f, 0.0f}}, {{0.0f, 0.0f, 0.0f, 0.0f}}};
             int tile = u0 / a.h_stages, s = u0 - tile * a.h_stages;
-            uint4 x[2][4][PARTS];
-            float2 p[2];
-            // Half stages ahead, of the pairs of a tile (h comes from other SMs): operands, and the
-            // factor and sum of one block of one token: UNIT_H 4 those of this lane's operands.
+            // Half a stage ahead where the registers hold it (not with two parts), of the pairs of
+            // a tile (h comes from other SMs): operands, and the factor and sum of one block of one
+            // token: UNIT_H 4 those of this lane's operands.
+            constexpr int AHEAD = PARTS == 1 ? 1 : 0;
+            uint4 x[1 + AHEAD][4][PARTS];
+            float2 p[1 + AHEAD];
             const uint8_t *xs = nullptr;
             const float2 *ps = nullptr;
             auto point = [&](int tl) {  // to a tile's pairs
@@ -647,11 +653,14 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                 load(2 * s, 0);
             }
             for (int u = u0; u < u1 && ok; ++u) {
-                if (!arrived(1)) break;
+                if (!arrived(2)) break;
                 const uint32_t more = second_half(s);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (h == 0) {
+                    const int now = h * AHEAD;
+                    if (!AHEAD) {
+                        if (h == 1) load(2 * s + 1, 0);
+                    } else if (h == 0) {
                         load(2 * s + 1, 1);
                     } else if (u + 1 < u1) {
                         const bool over = s + 1 == a.h_stages;
@@ -660,11 +669,11 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                     }
                     if (2 * s + h < a.h_halves) {
                         if constexpr (UNIT_H == 4) {
-                            float most = fmaxf(p[h].x, __shfl_xor_sync(0xFFFFFFFFu, p[h].x, 1));
+                            float most = fmaxf(p[now].x, __shfl_xor_sync(0xFFFFFFFFu, p[now].x, 1));
                             most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
                             // (powers of two: the inverse and the quotient are exact)
-                            const float rel = __fmul_rn(p[h].x, __uint_as_float((254u << 23) - __float_as_uint(most)));
-                            float sum = __fmul_rn(p[h].y, rel);
+                            const float rel = __fmul_rn(p[now].x, __uint_as_float((254u << 23) - __float_as_uint(most)));
+                            float sum = __fmul_rn(p[now].y, rel);
                             sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
                             sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
                             if (t == 0) mine[h * 32 + gr] = make_float2(most, sum);
@@ -673,24 +682,24 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                             for (int i = 0; i < 4; ++i)
 #pragma unroll
                                 for (int part = 0; part < PARTS; ++part) {
-                                    __half2 *v = reinterpret_cast<__half2 *>(&x[h][i][part]);
+                                    __half2 *v = reinterpret_cast<__half2 *>(&x[now][i][part]);
 #pragma unroll
                                     for (int k = 0; k < 4; ++k) v[k] = __hmul2(v[k], by);
                                 }
                         } else {
-                            mine[h * 32 + lane] = p[h];
+                            mine[h * 32 + lane] = p[now];
                         }
                         __syncwarp();
-                        const uint32_t scales[1] = {scale_ring + uint32_t(from * a.scale_bytes) + uint32_t(h) * more + row_at[0]};
-                        const uint32_t next_row[1] = {2u};
-                        s4_half_stage<1, 1, UNIT_H, SG, PARTS, false>(
+                        const uint32_t at = scale_ring + uint32_t(from * a.scale_bytes) + uint32_t(h) * more + row_at[0];
+                        const uint32_t scales[2] = {at, at + uint32_t(a.scale_bytes)}, next_row[2] = {2u, 2u};
+                        s4_half_stage<2, 1, UNIT_H, SG, PARTS, false>(
                             tot, smem, (ring + uint32_t(from) * CODES + s4_code_at<UNIT_H>(lane)) ^ (uint32_t(h) << 6), scales, next_row, 32u,
-                            a.down.zeros ? ZEROS : 0u, a.bf16_scales != 0, [&](int i, int, int part) { return x[h][i][part]; },
+                            a.down.zeros ? ZEROS : 0u, a.bf16_scales != 0, [&](int i, int, int part) { return x[now][i][part]; },
                             [&](int g, int) { return *reinterpret_cast<const float4 *>(mine + h * 32 + g * 8 + 2 * t); },
                             a.h_blocks - (2 * s + h) * 4);
                     }
                 }
-                release(1);
+                release(2);
                 issue(round, early);
                 if (++s == a.h_stages || u + 1 == u1) {
                     // The tile's sums to its tokens, this warp's.
@@ -699,27 +708,34 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                     for (int i = 0; i < 2; ++i) {
                         const int j = 2 * t + i;
                         if (j < n) {
-                            float *p = sums + warp * (a.tokens * 16) + r.pair_token[pair0 + j] * 16 + 2 * f;
+                            float *p = sums + (warp * a.tokens + r.pair_token[pair0 + j]) * 32 + 2 * f;
                             const float pw = r.pair_weight[pair0 + j];
-                            p[0] = __fmaf_rn(pw, tot[0][0][i], p[0]);
-                            p[1] = __fmaf_rn(pw, tot[0][0][2 + i], p[1]);
+#pragma unroll
+                            for (int m = 0; m < 2; ++m) {
+                                p[m * 16] = __fmaf_rn(pw, tot[m][0][i], p[m * 16]);
+                                p[m * 16 + 1] = __fmaf_rn(pw, tot[m][0][2 + i], p[m * 16 + 1]);
+                            }
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) tot[0][0][i] = 0.0f;
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) tot[m][0][i] = 0.0f;
                     if (s == a.h_stages) {
                         s = 0;
                         ++tile;
+                        if (!AHEAD && u + 1 < u1) point(tile);
                     }
                 }
+                if (!AHEAD && u + 1 < u1) load(2 * s, 0);
             }
             __syncthreads();
             if (st.abort.flag) break;
             auto put = [&](int o, float v) {
-                const int row = row0 + (o & 15);
-                if (row < a.hidden) static_cast<X *>(a.y)[int64_t(o >> 4) * a.ldy + row] = from_float<X>(__fmul_rn(v, kS4Out));
+                const int row = row0 + (o & 31);
+                if (row < a.hidden) static_cast<X *>(a.y)[int64_t(o >> 5) * a.ldy + row] = from_float<X>(__fmul_rn(v, kS4Out));
             };
-            const int outs = a.tokens * 16;
+            const int outs = a.tokens * 32;
             for (int o = threadIdx.x; o < outs; o += kMoeThreads) {
                 float v = 0.0f;
 #pragma unroll
@@ -730,9 +746,9 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                     a.parts[(int64_t(part) * row_tiles + row_tile) * outs + o] = v;
             }
             if (shares > 1) {  // the last share to end adds all of them, in order
-                __threadfence();
                 __syncthreads();
                 if (threadIdx.x == 0) {
+                    __threadfence();
                     r.last = atomicAdd(a.counters + 2 + row_tile, 1u) == uint32_t(shares - 1);
                     __threadfence();
                 }
@@ -768,13 +784,13 @@ struct MoeSpace {
 MoeSpace moe_space(int64_t tokens, int64_t hidden, int64_t inner, int64_t experts, int64_t top_k) {
     const int64_t stages = (hidden + 255) / 256, h_stages = (inner + 255) / 256, pairs = tokens * top_k;
     MoeSpace s;
-    s.logits = up_to((2 + kMaxParts4 / 2) * 4, 256);
+    s.logits = up_to((2 + kMaxParts4) * 4, 256);
     s.xs = s.logits + up_to(tokens * experts * 4, 256);
     s.xps = s.xs + tokens * stages * 2 * kS4XBytes;
     s.hs = s.xps + up_to(tokens * stages * 8 * 8, 256);
     s.hps = s.hs + pairs * h_stages * 4 * kS4XBytes;
     s.parts = s.hps + up_to(pairs * h_stages * 8 * 8, 256);
-    s.bytes = s.parts + int64_t(kMaxParts4) * tokens * 16 * 4;
+    s.bytes = s.parts + int64_t(kMaxParts4) * tokens * 32 * 4;
     return s;
 }
 
@@ -804,11 +820,13 @@ int launch_experts(MoeArgs a, const S4Weights &gu, const S4Weights &dn, int sms,
     constexpr int SG = 4 / UNIT;
     auto *fn = experts_kernel<X, UNIT, ODD>;
     a.scale_bytes = 2 * SG * 32 * (ODD ? 2 : 1) * (a.gate_up.zeros || a.down.zeros ? 2 : 1);
-    // As many places as leave two CTAs on an SM, at least four.
-    const size_t sums = size_t(kMoeWarps) * std::max(32 * kTile, a.tokens * 16) * 4;
+    // As many places as leave two CTAs on an SM, four where none do.
+    const size_t sums = size_t(kMoeWarps) * std::max(32 * kTile, a.tokens * 32) * 4;
     const size_t fixed = sums + sizeof(Routing) + sizeof(MoeTail) + kMoeWarps * 512 + 3072;  // (alignment, the system's 1 KB)
     const size_t place = size_t(kMoeWarps) * (kS4TileBytes + a.scale_bytes);
-    a.places = fixed + kMaxRing * place <= 114 * 1024 ? kMaxRing : 4;
+    a.places = kMaxRing;
+    while (a.places > 0 && fixed + a.places * place > 114 * 1024) a.places -= 2;
+    if (a.places == 0) a.places = 4;
     a.ring_bytes = kMoeWarps * a.places * kS4TileBytes;
     const size_t smem = a.places * place + sums + 1024;
     static std::atomic<int> ready[kMaxDevM];
@@ -816,7 +834,7 @@ int launch_experts(MoeArgs a, const S4Weights &gu, const S4Weights &dn, int sms,
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return fail_launch(e, "cudaGetDevice");
     if (!ready[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 176 * 1024);
         // (An SM changes its split between shared memory and cache only when it is idle.)
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(router_kernel<X, UNIT>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
