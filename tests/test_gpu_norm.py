@@ -302,3 +302,30 @@ def test_rows_past_32_bit_offsets():
     assert torch.equal(ptc.rms_norm(v), ptc.rms_norm(x))
     out = buf.as_strided((3, 512), (1 << 31, 1), 1024)
     assert torch.equal(ptc.rms_norm(x, out=out), ptc.rms_norm(x))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("cols", [1, 7, 8, 9, 33, 250, 1000, 5003, 20001])
+def test_s8_rows_at_any_element(cols, dtype):
+    """Rows that begin at every element of a 16-byte word, with weights that do too: the codes are
+    those of the same numbers in aligned rows, bit for bit (no code depends on a sum's order).
+    The scale's 1 / rms may: either is within F32 of the formula's."""
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    rows = 5
+    # (numbers around the ones that are read: none of them may count)
+    wide = torch.full((rows, cols + 24), 1e4, device="cuda").to(dtype)
+    wide_w = torch.full((cols + 24,), 1e3, device="cuda").to(dtype)
+    x = torch.randn(rows, cols, generator=g, device="cuda").to(dtype)
+    w = torch.randn(cols, generator=g, device="cuda").to(dtype)
+    aligned = torch.zeros(rows, -(-cols // 8) * 8, device="cuda", dtype=dtype)[:, :cols]
+    aligned.copy_(x)
+    want, want_scale = ptc.rms_norm_s8(aligned, w)
+    for off in range(9):
+        part, part_w = wide[:, off:off + cols], wide_w[off:off + cols]
+        part.copy_(x)
+        part_w.copy_(w)
+        got, scale = ptc.rms_norm_s8(part, part_w)
+        assert torch.equal(got, want), off
+        assert ((scale - want_scale).abs() <= 2 * F32 * want_scale.abs()).all(), off
+        wide.fill_(1e4)
+        wide_w.fill_(1e3)
