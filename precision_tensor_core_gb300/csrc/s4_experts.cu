@@ -18,6 +18,11 @@
 // Each warp brings its rows itself, by TMA, to a ring of its own in shared memory, and the
 // next item's while it ends one.  The activations come from L2 into registers, half a stage
 // ahead: an expert has few of them.
+//
+// Times: 16 tokens through 4 each of 32 experts of 4096 x 2048 in bfloat16 138 us (367 MB, 2.7 TB/s),
+// bound by the issue of instructions (about 410 per 16 rows x 256 codes); one token through 8 of 64
+// experts of 2048 x 1024 22 us, a chain of waits: router 3.3, routing 2.6, rows of h 8, all of them
+// 3, rows of y 4, their shares 2.  With 16 rows of y per item instead of 32 the first took 155.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -15,8 +15,9 @@
 // SMs idle K is also shared by a cluster of up to eight CTAs, whose sums are added in rank
 // order through distributed shared memory.
 //
-// What bounds it is the issue of instructions, not the weights' bytes, but for large
-// matrices and one token; @TOK@
+// Rates (weights from HBM): one token 5.1 us with 4096 x 4096 weights in groups of 128 and 17.4
+// with 16384 x 8192 (3.9 TB/s); sixteen 8.3 and 29 (2.4 TB/s): those are bound by the issue
+// of instructions, 409 per 16 rows x 256 codes and sixteen tokens.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
