@@ -57,9 +57,14 @@ struct GradArgs {
 };
 
 // How a thread meets its chunk i of eight elements of a row: eight consecutive ones, of
-// rows that are 16-byte aligned, or (kShifted, loads only) of any; or one of each run of the
-// row's threads (kSpread).  A warp's accesses are consecutive either way.
-constexpr int kSpread = 0, kWide = 1, kShifted = 2;
+// rows that are 16-byte aligned, or (kShifted, loads only) of any; eight of a 16-byte word (32
+// bytes of float32) of rows that all lie alike within one (kAlike, the weights shifted); or one of
+// each run of the row's threads (kSpread).  A warp's accesses are consecutive in all of them.
+constexpr int kSpread = 0, kWide = 1, kShifted = 2, kAlike = 3;
+
+// Elements of a row's first word that lie before the row.
+template <typename T>
+__device__ __forceinline__ int row_shift(const T *p) { return int((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T)); }
 
 template <int HOW>
 __device__ __forceinline__ int64_t column(int i, int e, int tid, int threads) {
@@ -105,6 +110,13 @@ __device__ __forceinline__ Pack8<T> load_chunk(const T *p, int i, int tid, int t
         return load8(c < cols ? p + c : p, c < cols ? int(cols - c) : 0, false);
     } else if constexpr (HOW == kShifted) {
         return c < cols ? load_shifted(p + c, c, cols - c) : load8(p, 0, false);
+    } else if constexpr (HOW == kAlike) {
+        const int64_t at = c - row_shift(p);
+        if (at >= 0 && at + 8 <= cols) return load8(p + at, 8, true);
+        Pack8<T> r;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r.set(e, at + e >= 0 && at + e < cols ? p[at + e] : from_float<T>(0.0f));
+        return r;
     } else {
         Pack8<T> r;
 #pragma unroll
@@ -118,7 +130,16 @@ __device__ __forceinline__ Pack8<T> load_chunk(const T *p, int i, int tid, int t
 
 template <int HOW, typename T>
 __device__ __forceinline__ void store_chunk(T *p, const Pack8<T> &v, int i, int tid, int threads, int64_t cols) {
-    if constexpr (HOW != kSpread) {
+    if constexpr (HOW == kAlike) {
+        const int64_t at = column<HOW>(i, 0, tid, threads) - row_shift(p);
+        if (at >= 0 && at + 8 <= cols) {
+            store8(p + at, v, 8, true);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (at + e >= 0 && at + e < cols) p[at + e] = v.get(e);
+        }
+    } else if constexpr (HOW != kSpread) {
         const int64_t c = column<HOW>(i, 0, tid, threads);
         if (c < cols) store8(p + c, v, int(min(int64_t(8), cols - c)), HOW == kWide);
     } else {
@@ -130,18 +151,34 @@ __device__ __forceinline__ void store_chunk(T *p, const Pack8<T> &v, int i, int 
     }
 }
 
+// Weights of a chunk; `shift`: the row's (kAlike).
+template <int HOW, typename W>
+__device__ __forceinline__ Pack8<W> weight_chunk(const W *w, int i, int tid, int threads, int64_t cols, int shift) {
+    if constexpr (HOW == kAlike) {
+        const int64_t at = column<HOW>(i, 0, tid, threads) - shift;
+        if (at >= 0) return at < cols ? load_shifted(w + at, at, cols - at) : load8(w, 0, false);
+        Pack8<W> r;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r.set(e, at + e >= 0 && at + e < cols ? w[at + e] : from_float<W>(0.0f));
+        return r;
+    } else {
+        return load_chunk<HOW>(w, i, tid, threads, cols);
+    }
+}
+
 // Eight weights as FP32; 1 where there are none, +0 or 1 past the row.
 template <int HOW, typename T>
-__device__ __forceinline__ void load_weight(float (&o)[8], const void *w, int w_f32, int i, int tid, int threads, int64_t cols) {
+__device__ __forceinline__ void load_weight(float (&o)[8], const void *w, int w_f32, int i, int tid, int threads, int64_t cols,
+                                            int shift = 0) {
     if (w == nullptr) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = 1.0f;
     } else if (w_f32) {
-        const Pack8<float> v = load_chunk<HOW>(static_cast<const float *>(w), i, tid, threads, cols);
+        const Pack8<float> v = weight_chunk<HOW>(static_cast<const float *>(w), i, tid, threads, cols, shift);
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = v.get(e);
     } else {
-        const Pack8<T> v = load_chunk<HOW>(static_cast<const T *>(w), i, tid, threads, cols);
+        const Pack8<T> v = weight_chunk<HOW>(static_cast<const T *>(w), i, tid, threads, cols, shift);
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = to_float(v.get(e));
     }
@@ -209,11 +246,12 @@ __device__ __noinline__ int border_code(float t, float a, float inverse) {
 // One chunk's output in the element type; `r`: 1 / rms.
 template <int HOW, typename T>
 __device__ __forceinline__ void put_chunk(const NormArgs &a, int64_t row, const Pack8<T> &s, float r, int i, int tid, int threads) {
+    T *const y = static_cast<T *>(a.y) + row * a.ldy;
     float w[8], o[8];
-    load_weight<HOW, T>(w, a.w, a.w_f32, i, tid, threads, a.cols);
+    load_weight<HOW, T>(w, a.w, a.w_f32, i, tid, threads, a.cols, HOW == kAlike ? row_shift(y) : 0);
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] = __fmul_rn(__fmul_rn(to_float(s.get(e)), r), w[e]);
-    store_chunk<HOW>(static_cast<T *>(a.y) + row * a.ldy, round8<T>(o), i, tid, threads, a.cols);
+    store_chunk<HOW>(y, round8<T>(o), i, tid, threads, a.cols);
 }
 
 // One chunk's t = s w.
@@ -340,7 +378,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
     griddep_launch_dependents();
     const int threads = int(blockDim.x), tid = int(threadIdx.x);
     const int64_t row = blockIdx.x;
-    const int chunks = int((a.cols + int64_t(8) * threads - 1) / (int64_t(8) * threads));
+    const int chunks = int((a.cols + (HOW == kAlike ? 7 : 0) + int64_t(8) * threads - 1) / (int64_t(8) * threads));
     float squares = 0.0f;
     uint32_t largest = 0;
     for (int i = 0; i < chunks; ++i) {
@@ -690,7 +728,7 @@ int round32(int64_t n) { return int((n + 31) / 32 * 32); }
 // elements a warp each.
 template <typename T, bool S8, int HOW>
 cudaError_t run_norm(const NormArgs &a, int sms, cudaStream_t s) {
-    const int64_t chunks = (a.cols + 7) / 8;
+    const int64_t chunks = (a.cols + 7) / 8 + (HOW == kAlike ? 1 : 0);
     if (chunks > 4 * 512 && !(chunks <= 1024 && a.rows <= sms))
         return launch_norm(norm_long_kernel<T, S8, HOW>, dim3(unsigned(a.rows)), 1024, s, a);
     if (a.rows > 2 * sms && chunks <= 128) {
@@ -713,11 +751,17 @@ int start_norm(NormArgs a, int type, int out_esize, cudaStream_t s) {
     if (a.rows == 1) a.ldx = a.ldr = a.lds = a.ldy = 0;  // (one row has no pitch)
     const bool out = S8 ? aligned_to(a.y, 8) && a.ldy % 8 == 0 : wide(a.y, a.ldy, out_esize);
     const bool vec = out && wide(a.x, a.ldx, es) && (!a.res || (wide(a.res, a.ldr, es) && wide(a.sum, a.lds, es))) && aligned_to(a.w, 16);
+    // Rows that lie as x's do within 16 bytes.
+    auto alike = [&](const void *p, int64_t ld) {
+        return (reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(a.x)) % 16 == 0 && (ld - a.ldx) * es % 16 == 0;
+    };
     auto go = [&](auto t) {
         using T = decltype(t);
         if (vec) return run_norm<T, S8, kWide>(a, sms, s);
         if constexpr (S8)  // codes are stored eight at a time, and nothing else is
             if (out && !a.res) return run_norm<T, S8, kShifted>(a, sms, s);
+        if constexpr (!S8)  // (2047 x 5003 f16 11.1 us instead of 15.8)
+            if (alike(a.y, a.ldy) && (!a.res || (alike(a.res, a.ldr) && alike(a.sum, a.lds)))) return run_norm<T, S8, kAlike>(a, sms, s);
         return run_norm<T, S8, kSpread>(a, sms, s);
     };
     const cudaError_t e = type == PTC_OUT_F32 ? go(float()) : type == PTC_OUT_BF16 ? go(__nv_bfloat16()) : go(__half());

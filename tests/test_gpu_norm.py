@@ -329,3 +329,27 @@ def test_s8_rows_at_any_element(cols, dtype):
         assert ((scale - want_scale).abs() <= 2 * F32 * want_scale.abs()).all(), off
         wide.fill_(1e4)
         wide_w.fill_(1e3)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("rows", [5, 400])
+@pytest.mark.parametrize("cols", [1, 7, 8, 9, 33, 250, 1001, 5003, 20001])
+def test_rows_that_lie_alike(cols, rows, dtype):
+    """Every matrix of a call begins at the same element of a 16-byte word, each of them in turn, in
+    rows of any pitch: the formula's values, and nothing written beside them."""
+    pitch = cols + 24
+    x, r, w = rand(1, rows, cols, dtype=dtype), rand(2, rows, cols, dtype=dtype), rand(3, cols, dtype=dtype)
+    s = x + r
+    v = s.double()
+    want = v / (v.square().mean(1, keepdim=True) + 1e-6).sqrt() * w.double()
+    for off in range(8) if rows == 5 else (0, 3):
+        for weight in (w, torch.cat([w[:1], w])[1:]):
+            wide = [torch.full((rows, pitch), 7.0, device=DEV).to(dtype) for _ in range(4)]
+            px, pr, py, ps = (b[:, off:off + cols] for b in wide)
+            px.copy_(x)
+            pr.copy_(r)
+            ptc.rms_norm(px, weight, 1e-6, residual=pr, out=py, sum_out=ps)
+            assert torch.equal(ps, s) and torch.equal(px, x), off
+            near(py, want, dtype)
+            for b in wide[2:]:
+                assert (b[:, :off] == 7).all() and (b[:, off + cols:] == 7).all(), off
