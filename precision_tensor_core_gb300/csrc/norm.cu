@@ -506,8 +506,10 @@ __global__ void __launch_bounds__(512) grad_kernel(const GradArgs a) {
 // The same for aligned rows, which come through shared memory: every thread copies its own
 // elements of the next rows there, `slots` rows deep, and waits for nobody else's.  (Loads
 // at the row's beginning left the memory idle during the reduction and the stores: 8192 x
-// 8192 bfloat16 with ds 259 us instead of 101.)
-template <typename T, int CH>
+// 8192 bfloat16 with ds 259 us instead of 101.)  With rows that lie alike (kAlike) the grid is a
+// multiple of eight wherever a CTA has several, so that all of a CTA's begin at the same
+// element of a word and its columns stay where they are.
+template <typename T, int CH, int HOW>
 __global__ void __launch_bounds__(1024) grad_ring_kernel(const GradArgs a, int slots) {
     constexpr int W = Pack8<T>::W;
     extern __shared__ uint4 ring[];  // [slot][s, dy, ds][chunk][16 bytes][thread], then the weights [chunk][2][thread]
@@ -516,11 +518,12 @@ __global__ void __launch_bounds__(1024) grad_ring_kernel(const GradArgs a, int s
     griddep_launch_dependents();
     const int threads = int(blockDim.x), tid = int(threadIdx.x);
     const int arrays = a.ds != nullptr ? 3 : 2, slot_size = arrays * CH * W * threads;
+    const int shift = HOW == kAlike ? row_shift(static_cast<const T *>(a.s) + int64_t(blockIdx.x) * a.lds) : 0;
     uint4 *const weights = ring + slots * slot_size + tid;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         float w[8];
-        load_weight<true, T>(w, a.w, a.w_f32, i, tid, threads, a.cols);
+        load_weight<HOW, T>(w, a.w, a.w_f32, i, tid, threads, a.cols, shift);
         weights[(2 * i) * threads] = *reinterpret_cast<const uint4 *>(&w[0]);
         weights[(2 * i + 1) * threads] = *reinterpret_cast<const uint4 *>(&w[4]);
     }
@@ -534,10 +537,24 @@ __global__ void __launch_bounds__(1024) grad_ring_kernel(const GradArgs a, int s
                 if (k < arrays)
 #pragma unroll
                     for (int i = 0; i < CH; ++i) {
-                        const int64_t c = column<true>(i, 0, tid, threads);
+                        const int64_t c = column<HOW>(i, 0, tid, threads) - shift;
 #pragma unroll
                         for (int w = 0; w < W; ++w) {
                             constexpr int PER = 16 / int(sizeof(T));
+                            if (HOW == kAlike && w == 0 && c < 0) {
+                                // The word that the row begins in: whole, with the end of the row
+                                // before it (which `taken` clears), or where none is its elements.
+                                uint4 *const at = to + ((k * CH + i) * W) * threads;
+                                if (row > 0 && a.cols >= 8) {
+                                    copy16_or_zero(at, from[k] + c, 16);
+                                } else {
+                                    Pack8<T> v;
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) v.set(e, c + e >= 0 && c + e < a.cols ? from[k][c + e] : from_float<T>(0.0f));
+                                    *at = v.v[0];
+                                }
+                                continue;
+                            }
                             const int have = c < a.cols ? int(max(int64_t(0), min(int64_t(PER), a.cols - c - w * PER))) : 0;
                             copy16_or_zero(to + ((k * CH + i) * W + w) * threads, from[k] + (have > 0 ? c + w * PER : 0), have * int(sizeof(T)));
                         }
@@ -549,6 +566,10 @@ __global__ void __launch_bounds__(1024) grad_ring_kernel(const GradArgs a, int s
         Pack8<T> v;
 #pragma unroll
         for (int w = 0; w < W; ++w) v.v[w] = ring[slot * slot_size + ((array * CH + i) * W + w) * threads + tid];
+        if (HOW == kAlike && i == 0 && tid == 0)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < shift) v.set(e, from_float<T>(0.0f));
         return v;
     };
     auto weight = [&](int i, int e) { return reinterpret_cast<const float *>(weights + (2 * i + (e >> 2)) * threads)[e & 3]; };
@@ -596,7 +617,7 @@ __global__ void __launch_bounds__(1024) grad_ring_kernel(const GradArgs a, int s
 #pragma unroll
                 for (int e = 0; e < 8; ++e) o[e] = __fadd_rn(o[e], to_float(d.get(e)));
             }
-            store_chunk<true>(static_cast<T *>(a.dx) + row * a.lddx, round8<T>(o), i, tid, threads, a.cols);
+            store_chunk<HOW>(static_cast<T *>(a.dx) + row * a.lddx, round8<T>(o), i, tid, threads, a.cols);
         }
         issue(row + int64_t(slots) * gridDim.x, slot);
         if (++slot == slots) slot = 0;
@@ -606,8 +627,8 @@ __global__ void __launch_bounds__(1024) grad_ring_kernel(const GradArgs a, int s
     for (int i = 0; i < CH; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int64_t c = column<true>(i, e, tid, threads);
-            if (c < a.cols) part[c] = acc[i][e];
+            const int64_t c = column<HOW>(i, e, tid, threads) - shift;
+            if (c >= 0 && c < a.cols) part[c] = acc[i][e];
         }
 }
 
@@ -855,20 +876,24 @@ cudaError_t run_grad(GradArgs a, int sms, float *dw, cudaStream_t s) {
     const int64_t chunks = (a.cols + 7) / 8;
     int parts;
     cudaError_t e;
+    constexpr int WIDE = HOW == kWide ? kWide : kSpread;
     if (grad_long(a.cols)) {
         const int64_t pieces = (chunks + 255) / 256;
         parts = int(std::min<int64_t>(grad_parts(a.rows), std::max<int64_t>(1, 8 * int64_t(sms) / pieces)));
-        e = launch_norm(grad_stats_kernel<T, HOW>, dim3(unsigned(a.rows)), 1024, s, a);
-        if (e == cudaSuccess) e = launch_norm(grad_columns_kernel<T, HOW>, dim3(unsigned(pieces), unsigned(parts)), 256, s, a);
-    } else if (const RingShape g = ring_shape(chunks, a.ds ? 3 : 2, sizeof(T)); HOW == kWide && g.weights + g.row <= kRingMost) {
+        e = launch_norm(grad_stats_kernel<T, WIDE>, dim3(unsigned(a.rows)), 1024, s, a);
+        if (e == cudaSuccess) e = launch_norm(grad_columns_kernel<T, WIDE>, dim3(unsigned(pieces), unsigned(parts)), 256, s, a);
+    } else if (const RingShape g = ring_shape(chunks + (HOW == kAlike ? 1 : 0), a.ds ? 3 : 2, sizeof(T));
+               HOW != kSpread && g.weights + g.row <= kRingMost) {
         // Four rows in flight per CTA, fewer where they do not fit; up to three CTAs per SM.
         const int slots = int(std::min<size_t>(4, (kRingMost - g.weights) / g.row));
         const size_t smem = slots * g.row + g.weights;
         const int per_sm = int(std::max<size_t>(1, std::min<size_t>({3, size_t(2048 / g.threads), kRingMost / (smem + 2048)})));
-        auto *fn = g.ch == 1 ? grad_ring_kernel<T, 1> : grad_ring_kernel<T, 2>;
+        constexpr int RING = HOW == kAlike ? kAlike : kWide;
+        auto *fn = g.ch == 1 ? grad_ring_kernel<T, 1, RING> : grad_ring_kernel<T, 2, RING>;
         e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kRingMost));
         if (e != cudaSuccess) return e;
         parts = int(std::min<int64_t>(grad_parts(a.rows), int64_t(sms) * per_sm));
+        if (HOW == kAlike && parts < a.rows) parts = std::max(8, parts / 8 * 8);
         e = launch_norm_smem(fn, dim3(unsigned(parts)), g.threads, smem, s, a, slots);
     } else {
         const int ch = chunks <= 256 ? 1 : chunks <= 1024 ? 2 : 4;
@@ -991,9 +1016,17 @@ int ptc_rms_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t ld
     if (rows == 1) a.lddy = a.lds = a.ldds = a.lddx = 0;  // (one row has no pitch)
     const bool vec = wide(dy, a.lddy, es) && wide(s, a.lds, es) && wide(dx, a.lddx, es) && (!ds || wide(ds, a.ldds, es)) &&
                      aligned_to(weight, 16);
+    // Rows that lie as those of s do within 16 bytes.
+    auto alike = [&](const void *p, int64_t ld) {
+        return (reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(s)) % 16 == 0 && (ld - a.lds) * es % 16 == 0;
+    };
     auto go = [&](auto t) {
         using T = decltype(t);
-        return vec ? run_grad<T, true>(a, sms, dweight, st) : run_grad<T, false>(a, sms, dweight, st);
+        if (vec) return run_grad<T, kWide>(a, sms, dweight, st);
+        // (2047 x 5003 f16 33 us instead of 50, 8192 x 8191 bf16 139 instead of 212; but with few rows
+        // per SM there is nothing to copy ahead: 333 x 777 f32 7.4 instead of 6.1)
+        if (rows > 4 * int64_t(sms) && alike(dy, a.lddy) && alike(dx, a.lddx) && (!ds || alike(ds, a.ldds))) return run_grad<T, kAlike>(a, sms, dweight, st);
+        return run_grad<T, kSpread>(a, sms, dweight, st);
     };
     const cudaError_t e = type == PTC_OUT_F32 ? go(float()) : type == PTC_OUT_BF16 ? go(__nv_bfloat16()) : go(__half());
     return e == cudaSuccess ? PTC_OK : fail_launch(e, "norm gradient launch");

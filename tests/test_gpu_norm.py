@@ -353,3 +353,37 @@ def test_rows_that_lie_alike(cols, rows, dtype):
             near(py, want, dtype)
             for b in wide[2:]:
                 assert (b[:, :off] == 7).all() and (b[:, off + cols:] == 7).all(), off
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [5, 700])
+@pytest.mark.parametrize("cols", [1, 7, 9, 33, 250, 1001, 5003, 9001])
+def test_gradient_of_rows_that_lie_alike(cols, rows, dtype):
+    """The same for the gradient, whose rows of odd length begin at other elements one after the
+    other: NaN beside the rows counts nowhere, and the values are those of separate rows."""
+    s, dy, ds, w = (rand(k, *shape, dtype=dtype) for k, shape in enumerate([(rows, cols)] * 3 + [(cols,)]))
+    pad = torch.full((rows, -(-cols // 8) * 8 + 8), float("nan"), device=DEV).to(dtype)
+
+    def apart(t):  # 16-byte aligned rows
+        b = pad.clone()
+        b[:, :cols].copy_(t)
+        return b[:, :cols]
+
+    want, want_w = ptc.rms_norm_backward(apart(dy), apart(s), w, 1e-6, dsum=apart(ds), out=apart(dy))
+    for off in range(8) if rows == 5 else (0, 3):
+        for pitch in (cols + 8, cols + 9):
+            wide = [torch.full((rows, pitch), float("nan"), device=DEV).to(dtype) for _ in range(4)]
+            part = [b[:, off:off + cols] for b in wide]
+            for to, t in zip(part, (s, dy, ds)):
+                to.copy_(t)
+            got, got_w = ptc.rms_norm_backward(part[1], part[0], w, 1e-6, dsum=part[2], out=part[3])
+            assert got.data_ptr() == part[3].data_ptr()
+            # Both are within the type's rounding and 2 F32 of terms no larger than these.
+            v, g = s.double(), dy.double() * w.double()
+            r = (v.square().mean(1, keepdim=True) + 1e-6).rsqrt()
+            size = r * (g.abs() + (v * r).abs() * (g * v * r).abs().mean(1, keepdim=True)) + ds.double().abs()
+            bound = 2 * (ulp(dtype) * (want.double().abs() + 2 * F32 * size) + 2 * F32 * size + least(dtype))
+            assert bool(((got.double() - want.double()).abs() <= bound).all()), off
+            bound = 2 * (2 * F32 + (rows + 40) * 2.0 ** -24) * (dy.double() * v * r).abs().sum(0)
+            assert bool(((got_w.double() - want_w.double()).abs() <= bound + 1e-30).all()), off
+            assert bool(wide[3][:, :off].isnan().all()) and bool(wide[3][:, off + cols:].isnan().all())
