@@ -827,7 +827,7 @@ int launch_experts(MoeArgs a, const S4Weights &gu, const S4Weights &dn, int sms,
     a.scale_bytes = 2 * SG * 32 * (ODD ? 2 : 1) * (a.gate_up.zeros || a.down.zeros ? 2 : 1);
     // As many places as leave two CTAs on an SM, four where none do.
     const size_t sums = size_t(kMoeWarps) * std::max(32 * kTile, a.tokens * 32) * 4;
-    const size_t fixed = sums + sizeof(Routing) + sizeof(MoeTail) + kMoeWarps * 512 + 3072;  // (alignment, the system's 1 KB)
+    const size_t fixed = sums + sizeof(Routing) + sizeof(MoeTail) + kMoeWarps * 512 + 3 * 1024;  // (alignment, the system's 1 KB)
     const size_t place = size_t(kMoeWarps) * (kS4TileBytes + a.scale_bytes);
     a.places = kMaxRing;
     while (a.places > 0 && fixed + a.places * place > 114 * 1024) a.places -= 2;
