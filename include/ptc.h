@@ -486,7 +486,8 @@ int gemm_a16_s4(int64_t M, int64_t N, int64_t K, int type, const void *X, int64_
  * Only the chosen experts' weights are read, once per eight of an expert's tokens.  Products and
  * activations as gemm_a16_s4; of h 22 bits are kept, for bfloat16 X 11, and at least 2^-24
  * of the largest of 128.  Results
- * are the same from call to call.  The workspace has at least
+ * are the same from call to call, and a token's do not depend on what the other tokens are
+ * (the order of its sums goes by the sizes alone).  The workspace has at least
  * ptc_moe_a16_s4_workspace(...) bytes (0: the sizes are refused), 256-byte aligned, and is
  * no other call's until this one is done.
  */

@@ -13,7 +13,9 @@
 // evenly.  The second kind waits until every item of the first kind is done.  A ticket is
 // taken by a CTA that runs, and a CTA that waits holds no item of the first kind, so the wait
 // ends whatever else holds the GPU.  h passes through memory as one or two binary16 numbers
-// relative to a power of two per 32.  No sum's order depends on which CTA takes what.
+// relative to a power of two per 32.  No sum's order depends on which CTA or warp takes what, nor
+// on the other tokens: a token's products with an expert are summed in chunks of the expert's codes,
+// whose sums pass through memory (L2) and are added by slot and chunk.
 //
 // Each warp brings its rows itself, by TMA, to a ring of its own in shared memory, and the
 // next item's while it ends one.  The activations come from L2 into registers, half a stage
@@ -49,6 +51,11 @@ constexpr int kTile = 8;  // tokens of an expert per item
 constexpr int kLogits = 4;  // tokens per CTA of the router
 constexpr int kMaxRing = 6;  // places of a warp's ring, each a stage of 16 rows; taken in pairs
 constexpr int kMaxParts4 = 1024;  // shares of all tiles of 32 rows of y, where they are shared
+constexpr int kPlaces = 512;  // sets of chunks' sums: of a tile of 32 rows each, or (more tiles) of a CTA each
+// Chunks of all pairs' codes, at least, where their codes have as many stages: enough for an even
+// share of warps, few enough for their sums (16 tokens of 4 experts of 2048: 4 of two stages; twice
+// as many chunks take the same time within 2%).
+constexpr int kChunks = 256;
 
 __device__ uint32_t g_moe_error = 0;
 
@@ -70,10 +77,11 @@ struct MoeArgs {
     Experts gate_up, down;
     int halves, stages;              // of hidden
     int h_halves, h_stages, h_blocks;  // of inner; blocks of 32
+    int chunk, chunks;               // stages per chunk of inner, and chunks
     int places, ring_bytes, scale_bytes;  // of a warp's ring (even); of all warps' codes; of a place's scales and zeros
     // Workspace.
     uint32_t *counters;   // tickets, items of the first kind that are done; shares of 32 rows of y that are
-    float *parts;         // sums of shares of rows of y: [share][tile of rows][token][32]
+    float *parts;         // chunks' sums of rows of y: [place][token][slot][chunk][32]
     float *logits;        // [tokens][experts]
     uint8_t *xs;          // [token][stage] operands
     float2 *xps;          // [token][block] factors and sums
@@ -161,6 +169,7 @@ __global__ void __launch_bounds__(kMoeThreads) router_kernel(const MoeArgs a) {
 // lie by expert, then by token, and each expert's in tiles of up to eight.
 struct Routing {
     uint8_t pair_token[kMaxPairs];
+    uint16_t pair_slot[kMaxPairs];  // [token][slot]
     float pair_weight[kMaxPairs];
     uint16_t tile_expert[kMaxPairs], tile_first[kMaxPairs];
     uint8_t tile_count[kMaxPairs];
@@ -292,6 +301,7 @@ __device__ __forceinline__ void route(const MoeArgs &a, Routing &r, RoutingWork 
         const uint32_t lo = w.mask[e][0], hi = w.mask[e][1];
         const int rank = tok < 32 ? __popc(lo & ((1u << tok) - 1u)) : __popc(lo) + __popc(hi & ((1u << (tok - 32)) - 1u));
         r.pair_token[w.first[e] + rank] = uint8_t(tok);
+        r.pair_slot[w.first[e] + rank] = uint16_t(s);
         r.pair_weight[w.first[e] + rank] = w.slot_weight[s];
     }
     fence_proxy_async_all();  // (bulk copies write where this was held)
@@ -364,15 +374,15 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     route(a, r, *reinterpret_cast<RoutingWork *>(smem));
     if (threadIdx.x == 0) r.ticket[0] = asked_ticket;
 
-    const int units = r.tiles * a.h_stages;  // stages of 32 rows of y, of all tiles of pairs
+    const int units = r.tiles * a.chunks;  // chunks of 32 rows of y, of all tiles of pairs
     const int row_tiles = (a.hidden + 31) / 32;
-    // Shares of these stages that are items of their own: what takes the least stages of a warp
+    // Shares of these chunks that are items of their own: what takes the least stages of a warp
     // in all rounds, two more per item.
     const int grid = int(gridDim.x);
     int shares = 1;
     {
         const int n = (lane & 7) + 1, items = row_tiles * n, warps = n * kMoeWarps;
-        const uint32_t cost = uint32_t((items + grid - 1) / grid) * uint32_t((units + warps - 1) / warps + 2);
+        const uint32_t cost = uint32_t((items + grid - 1) / grid) * uint32_t((units + warps - 1) / warps * a.chunk + 2);
         const bool may = n == 1 || (items <= kMaxParts4 && cost < 1u << 28);
         shares = int(__reduce_min_sync(0xFFFFFFFFu, may ? min(cost, (1u << 28) - 1) * 8u + uint32_t(n - 1) : ~0u) & 7u) + 1;
     }
@@ -385,11 +395,12 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     const bool early = first_items >= 4 * int(gridDim.x);
     if (early && threadIdx.x == 0) r.ticket[1] = atomicAdd(a.counters, 1u);
     __syncthreads();
-    // This warp's of a share.
+    // This warp's chunks of a share, as stages of all tiles.
     auto units_of = [&](int part, int &u0, int &u1) {
         const int first = int(int64_t(units) * part / shares), n = int(int64_t(units) * (part + 1) / shares) - first;
-        u0 = first + n * warp / kMoeWarps;
-        u1 = first + n * (warp + 1) / kMoeWarps;
+        auto stage = [&](int u) { return u / a.chunks * a.h_stages + u % a.chunks * a.chunk; };
+        u0 = stage(first + n * warp / kMoeWarps);
+        u1 = stage(first + n * (warp + 1) / kMoeWarps);
     };
     // The item of a round: one of the first kind by its ticket, then those of the second kind; -1
     // after the last.  (Tickets rise, so that the rounds of the first kind come first;
@@ -625,10 +636,10 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
             const int part = (item - first_items) / row_tiles, row_tile = (item - first_items) % row_tiles, row0 = row_tile * 32;
             int u0, u1;
             units_of(part, u0, u1);
-            for (int i = lane; i < a.tokens * 32; i += 32) sums[warp * (a.tokens * 32) + i] = 0.0f;
-            __syncwarp();
+            // (32 bits: 512 places of at most 767 sums)
+            const int place = (row_tiles <= kPlaces ? row_tile : int(blockIdx.x)) * (a.tokens * a.top_k * a.chunks);
             float tot[2][1][4] = {{{0.0f, 0.0f, 0.0f, 0.0f}}, {{0.0f, 0.0f, 0.0f, 0.0f}}};
-            int tile = u0 / a.h_stages, s = u0 - tile * a.h_stages;
+            int tile = u0 / a.h_stages, s = u0 - tile * a.h_stages, chunk = s / a.chunk;
             // Half a stage ahead where the registers hold it (not with two parts), of the pairs of
             // a tile (h comes from other SMs): operands, and the factor and sum of one block of one
             // token: UNIT_H 4 those of this lane's operands.
@@ -706,28 +717,27 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                 }
                 release(2);
                 issue(round, early);
-                if (++s == a.h_stages || u + 1 == u1) {
-                    // The tile's sums to its tokens, this warp's.
+                if (++s == a.h_stages || s == (chunk + 1) * a.chunk) {
+                    // The chunk's sums to their places, of the tile's pairs.
                     const int pair0 = r.tile_first[tile], n = r.tile_count[tile];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int j = 2 * t + i;
                         if (j < n) {
-                            float *p = sums + (warp * a.tokens + r.pair_token[pair0 + j]) * 32 + 2 * f;
+                            float *p = a.parts + (place + int(r.pair_slot[pair0 + j]) * a.chunks + chunk) * 32 + 2 * f;
                             const float pw = r.pair_weight[pair0 + j];
 #pragma unroll
-                            for (int m = 0; m < 2; ++m) {
-                                p[m * 16] = __fmaf_rn(pw, tot[m][0][i], p[m * 16]);
-                                p[m * 16 + 1] = __fmaf_rn(pw, tot[m][0][2 + i], p[m * 16 + 1]);
-                            }
+                            for (int m = 0; m < 2; ++m)
+                                *reinterpret_cast<float2 *>(p + m * 16) = make_float2(__fmul_rn(pw, tot[m][0][i]), __fmul_rn(pw, tot[m][0][2 + i]));
                         }
                     }
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) tot[m][0][i] = 0.0f;
+                    ++chunk;
                     if (s == a.h_stages) {
-                        s = 0;
+                        s = chunk = 0;
                         ++tile;
                         if (!AHEAD && u + 1 < u1) point(tile);
                     }
@@ -736,34 +746,29 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
             }
             __syncthreads();
             if (st.abort.flag) break;
-            auto put = [&](int o, float v) {
-                const int row = row0 + (o & 31);
-                if (row < a.hidden) static_cast<X *>(a.y)[int64_t(o >> 5) * a.ldy + row] = from_float<X>(__fmul_rn(v, kS4Out));
-            };
-            const int outs = a.tokens * 32;
-            for (int o = threadIdx.x; o < outs; o += kMoeThreads) {
-                float v = 0.0f;
-#pragma unroll
-                for (int k = 0; k < kMoeWarps; ++k) v = __fadd_rn(v, sums[k * outs + o]);
-                if (shares == 1)
-                    put(o, v);
-                else
-                    a.parts[(int64_t(part) * row_tiles + row_tile) * outs + o] = v;
-            }
-            if (shares > 1) {  // the last share to end adds all of them, in order
-                __syncthreads();
+            if (shares > 1) {  // the last share to end adds the chunks of all
                 if (threadIdx.x == 0) {
                     __threadfence();
                     r.last = atomicAdd(a.counters + 2 + row_tile, 1u) == uint32_t(shares - 1);
                     __threadfence();
                 }
                 __syncthreads();
-                if (r.last)
-                    for (int o = threadIdx.x; o < outs; o += kMoeThreads) {
-                        float v = 0.0f;
-                        for (int k = 0; k < shares; ++k) v = __fadd_rn(v, __ldcg(a.parts + (int64_t(k) * row_tiles + row_tile) * outs + o));
-                        put(o, v);
+            }
+            if (shares == 1 || r.last) {  // token by token, a lane a row, in the slots' order
+                const int n = a.top_k * a.chunks;
+                for (int o = threadIdx.x; o < a.tokens * 32; o += kMoeThreads) {
+                    const float *p = a.parts + (place + (o >> 5) * n) * 32 + (o & 31);
+                    float v = 0.0f;
+                    for (int k = 0; k < n; k += 24) {  // (24 loads in flight)
+                        float c[24];
+#pragma unroll
+                        for (int i = 0; i < 24; ++i) c[i] = k + i < n ? __ldcg(p + (k + i) * 32) : 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 24; ++i) v = __fadd_rn(v, c[i]);
                     }
+                    const int row = row0 + (o & 31);
+                    if (row < a.hidden) static_cast<X *>(a.y)[int64_t(o >> 5) * a.ldy + row] = from_float<X>(__fmul_rn(v, kS4Out));
+                }
             }
         }
         if (threadIdx.x == 0 && item < first_items) r.ticket[later] = asked_ticket;
@@ -784,6 +789,7 @@ bool lies_on(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p)
 
 struct MoeSpace {
     int64_t logits, xs, xps, hs, hps, parts, bytes;
+    int chunk, chunks;
 };
 
 MoeSpace moe_space(int64_t tokens, int64_t hidden, int64_t inner, int64_t experts, int64_t top_k) {
@@ -795,7 +801,10 @@ MoeSpace moe_space(int64_t tokens, int64_t hidden, int64_t inner, int64_t expert
     s.hs = s.xps + up_to(tokens * stages * 8 * 8, 256);
     s.hps = s.hs + pairs * h_stages * 4 * kS4XBytes;
     s.parts = s.hps + up_to(pairs * h_stages * 8 * 8, 256);
-    s.bytes = s.parts + int64_t(kMaxParts4) * tokens * 32 * 4;
+    const int64_t most = std::min(h_stages, (kChunks + pairs - 1) / pairs);
+    s.chunk = int((h_stages + most - 1) / most);
+    s.chunks = int((h_stages + s.chunk - 1) / s.chunk);
+    s.bytes = s.parts + std::min<int64_t>((hidden + 31) / 32, kPlaces) * pairs * s.chunks * 32 * 4;
     return s;
 }
 
@@ -826,7 +835,7 @@ int launch_experts(MoeArgs a, const S4Weights &gu, const S4Weights &dn, int sms,
     auto *fn = experts_kernel<X, UNIT, ODD>;
     a.scale_bytes = 2 * SG * 32 * (ODD ? 2 : 1) * (a.gate_up.zeros || a.down.zeros ? 2 : 1);
     // As many places as leave two CTAs on an SM, four where none do.
-    const size_t sums = size_t(kMoeWarps) * std::max(32 * kTile, a.tokens * 32) * 4;
+    const size_t sums = size_t(kMoeWarps) * 32 * kTile * 4;
     const size_t fixed = sums + sizeof(Routing) + sizeof(MoeTail) + kMoeWarps * 512 + 3 * 1024;  // (alignment, the system's 1 KB)
     const size_t place = size_t(kMoeWarps) * (kS4TileBytes + a.scale_bytes);
     a.places = kMaxRing;
@@ -858,7 +867,7 @@ int launch_experts(MoeArgs a, const S4Weights &gu, const S4Weights &dn, int sms,
     e = launch_moe(router_kernel<X, UNIT>, int64_t(a.tokens + kLogits - 1) / kLogits * a.experts + makers, 0, s, a);
     if (e == cudaSuccess) {
         const int per_sm = fixed + a.places * place <= 114 * 1024 ? 2 : 1;
-        e = launch_moe(fn, int64_t(sms) * per_sm, smem, s, up, down, a);
+        e = launch_moe(fn, std::min(sms * per_sm, kPlaces), smem, s, up, down, a);
     }
     return e == cudaSuccess ? PTC_OK : fail_launch(e, "experts launch");
 }
@@ -993,6 +1002,8 @@ int ptc_moe_a16_s4(int64_t tokens, int64_t hidden, int64_t inner, int64_t expert
     a.h_halves = int((inner + kS4Half - 1) / kS4Half);
     a.h_stages = int((inner + kS4Stage - 1) / kS4Stage);
     a.h_blocks = int((inner + 31) / 32);
+    a.chunk = at.chunk;
+    a.chunks = at.chunks;
     a.counters = reinterpret_cast<uint32_t *>(ws);
     a.logits = reinterpret_cast<float *>(ws + at.logits);
     a.xs = reinterpret_cast<uint8_t *>(ws + at.xs);
