@@ -804,7 +804,9 @@ MoeSpace moe_space(int64_t tokens, int64_t hidden, int64_t inner, int64_t expert
     const int64_t most = std::min(h_stages, (kChunks + pairs - 1) / pairs);
     s.chunk = int((h_stages + most - 1) / most);
     s.chunks = int((h_stages + s.chunk - 1) / s.chunk);
-    s.bytes = s.parts + std::min<int64_t>((hidden + 31) / 32, kPlaces) * pairs * s.chunks * 32 * 4;
+    // (Never less than a set of the tokens' sums for every share, the size that small layers have.)
+    const int64_t sets = std::min<int64_t>((hidden + 31) / 32, kPlaces) * top_k * s.chunks;
+    s.bytes = s.parts + std::max<int64_t>(sets, kMaxParts4) * tokens * 32 * 4;
     return s;
 }
 
