@@ -101,15 +101,21 @@ __device__ __forceinline__ uint4 s4_operands(const uint4 &raw, float2 &factor_su
     return make_uint4(s4_pair(v[0], v[4]), s4_pair(v[2], v[6]), s4_pair(v[1], v[5]), s4_pair(v[3], v[7]));
 }
 
-// One FP32 activation of a block that a warp's 32 lanes hold, as two operands whose sum
-// has 22 bits (hi: rounded to binary16, lo: what that left), and the block's factor and sum.
+// One FP32 activation of a block that a warp's 32 lanes hold, as one operand of 11 bits (hi,
+// rounded to binary16) or, with PARTS 2, two whose sum has 22 (lo: what that left), and the
+// block's factor and sum: that of the numbers held, as n = c + 8 multiplies those and (8 + z)
+// takes their sum off again.  (A sum of the numbers before they are held would leave 8 + z times
+// what the rounding took, about four times the codes' own size.)
+template <int PARTS>
 __device__ __forceinline__ void s4_operand32(float v, int lane, __half &hi, __half &lo, float2 &factor_sum) {
     float down, factor;
     s4_powers(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu), down, factor);
-    const float x = __fmul_rn(v, down), part = __fmul_rn(x, (lane & 1) ? 0x1p-4f : 1.0f);
+    const float part = __fmul_rn(__fmul_rn(v, down), (lane & 1) ? 0x1p-4f : 1.0f);
     hi = __float2half_rn(part);
-    lo = __float2half_rn(__fsub_rn(part, __half2float(hi)));
-    float sum = x;
+    float held = __half2float(hi);
+    lo = __float2half_rn(__fsub_rn(part, held));
+    if constexpr (PARTS == 2) held = __fadd_rn(held, __half2float(lo));
+    float sum = __fmul_rn(held, (lane & 1) ? 0x1p4f : 1.0f);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     factor_sum = make_float2(factor, __fmul_rn(sum, 0x1p-24f));

@@ -344,8 +344,9 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     // Rows of y: with groups of 128 and more half a stage is one block, whose four blocks of
     // 32 of h are brought to one power of two as they are loaded.
     constexpr int UNIT_H = UNIT == 4 ? 4 : 1;
-    // h as one binary16 number where y is bfloat16 (2^-12 of an element, an eighth of y's own
-    // rounding: 1.01 times its error), two where it is binary16.
+    // h as one binary16 number where y is bfloat16, two where it is binary16.  One is off by
+    // 2^-11 of an element at most, an eighth of what y's own rounding is: as those errors are
+    // weighted as h itself is, sqrt(1 + 1 / 64) = 1.008 times y's error without them.
     constexpr int PARTS = std::is_same_v<X, __half> ? 2 : 1;
     extern __shared__ uint8_t moe_raw[];
     uint8_t *const smem = moe_raw + ((1024u - (smem_u32(moe_raw) & 1023u)) & 1023u);
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                 const float h = ib * 32 + lane < a.inner ? __fmul_rn(__fdiv_rn(gate, __fadd_rn(1.0f, expf(-gate))), up) : 0.0f;
                 __half hi, lo;
                 float2 ps;
-                s4_operand32(h, lane, hi, lo, ps);
+                s4_operand32<PARTS>(h, lane, hi, lo, ps);
                 const int64_t pair = pair0 + warp;
                 // [pair][stage][high parts of 256, low parts]
                 uint8_t *p = a.hs + (pair * a.h_stages + ib / 8) * (4 * kS4XBytes) + ((ib >> 2) & 1) * kS4XBytes +
@@ -689,11 +690,12 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                             most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
                             // (powers of two: the inverse and the quotient are exact)
                             const float rel = __fmul_rn(p[now].x, __uint_as_float((254u << 23) - __float_as_uint(most)));
-                            float sum = __fmul_rn(p[now].y, rel);
+                            // (binary16 as what it multiplies: 0 below 2^-24)
+                            const __half2 by = __float2half2_rn(rel);
+                            float sum = __fmul_rn(p[now].y, __low2float(by));
                             sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
                             sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
                             if (t == 0) mine[h * 32 + gr] = make_float2(most, sum);
-                            const __half2 by = __float2half2_rn(rel);
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
 #pragma unroll
