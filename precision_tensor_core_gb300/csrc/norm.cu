@@ -556,6 +556,10 @@ __global__ void __launch_bounds__(1024) grad_ring_kernel(const GradArgs a, int s
                                 continue;
                             }
                             const int have = c < a.cols ? int(max(int64_t(0), min(int64_t(PER), a.cols - c - w * PER))) : 0;
+                            if (HOW == kAlike && have == 0) {  // (the row's first element is no address for 16 bytes, even of none)
+                                to[((k * CH + i) * W + w) * threads] = make_uint4(0, 0, 0, 0);
+                                continue;
+                            }
                             copy16_or_zero(to + ((k * CH + i) * W + w) * threads, from[k] + (have > 0 ? c + w * PER : 0), have * int(sizeof(T)));
                         }
                     }
