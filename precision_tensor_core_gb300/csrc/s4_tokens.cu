@@ -172,7 +172,10 @@ __global__ void __launch_bounds__(kThreads4, 1) s4_kernel(const __grid_constant_
     // Activations of chunk c to the buffer of the place-th chunk: 4 UNIT lanes a block, a warp 32 / (4 UNIT),
     // four loads in flight per lane.
     int chunks_done = 0;
+    bool over = false;  // the CTA gave up: known to all of its threads
+    int brought = 0;    // chunks of operands asked for, alternately on the two barriers
     auto load_x = [&](int c, int place) {
+        ++brought;
         constexpr int LANES = 4 * UNIT, PER = 32 / LANES;
         const uint32_t buf = xs_base + (a.buffers == 2 && (place & 1) ? buf_bytes : 0u);
         const int first = c0 + c * a.chunk;
@@ -243,15 +246,18 @@ __global__ void __launch_bounds__(kThreads4, 1) s4_kernel(const __grid_constant_
 #pragma unroll
                 for (int i = 0; i < 4; ++i) tot[m][n][i] = 0.0f;
         for (int c = 0, st = c0 + share; c * a.chunk < c1 - c0; ++c) {
-            if (a.buffers == 2 || tile == tile0) __syncthreads();  // chunk c is there, and everyone is done with the other buffer
-            if (a.buffers == 2) {  // (the next tile begins with the first chunk again)
+            // Chunk c is there, and everyone is done with the other buffer.  After an abort nothing more is brought: a
+            // wait may have ended before its copies did, and their buffer and barrier are still theirs.
+            if (a.buffers == 2 || tile == tile0) over = __syncthreads_or(int(st4.abort.flag)) != 0;
+            ok = ok && !over;
+            if (a.buffers == 2 && !over) {  // (the next tile begins with the first chunk again)
                 const bool last = (c + 1) * a.chunk >= c1 - c0;
                 if (!last || tile + tile_step < tiles) load_x(last ? 0 : c + 1, chunks_done + 1);
             }
             const uint32_t buf = xs_base + (a.buffers == 2 && (chunks_done & 1) ? buf_bytes : 0u);
-            if (a.xs != nullptr && (a.buffers == 2 || tile == tile0))
+            if (a.xs != nullptr && ok && (a.buffers == 2 || tile == tile0))
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(&st4.operands[chunks_done & 1], uint32_t(chunks_done >> 1) & 1u, &st4.abort,
-                                                       &g_s4_error, a.wait_limit)) && ok;
+                                                       &g_s4_error, a.wait_limit));
             ++chunks_done;
             const int first = c0 + c * a.chunk, end = min(c1, first + a.chunk);
             for (; ok && st < end; st += S) {
@@ -332,8 +338,10 @@ __global__ void __launch_bounds__(kThreads4, 1) s4_kernel(const __grid_constant_
         }
     }
     // After an abort copies in flight land before the CTA exits.
-    if (st4.abort.flag && a.xs != nullptr && chunks_done > 0)
-        mbar_wait(&st4.operands[(chunks_done - 1) & 1], uint32_t((chunks_done - 1) >> 1) & 1u, nullptr, nullptr, a.wait_limit);
+    // (Operands: the last chunk on each barrier.)
+    if (st4.abort.flag && a.xs != nullptr)
+        for (int c = max(0, brought - 2); c < brought; ++c)
+            mbar_wait(&st4.operands[c & 1], uint32_t(c >> 1) & 1u, nullptr, nullptr, a.wait_limit);
     if (int(blockIdx.x) != a.stall)
         for (; taken < asked; ++taken)
             mbar_wait(&st4.full[warp][taken % D], uint32_t(taken / D) & 1u, nullptr, nullptr, a.wait_limit);
