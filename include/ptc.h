@@ -519,8 +519,8 @@ int ptc_rms_norm(int64_t rows, int64_t cols, const void *x, int64_t ldx, int typ
  * The same norm as 8-bit codes with a scale per row, the A and scale_a of
  * gemm_s8_scaled.  With t = s weight in FP32 and a the largest |t| of the row:
  * codes = 127 t / a rounded to nearest (ties to even; decided exactly), scale =
- * a r / 127.  A row of zeros has codes and scale 0; a row in which some t is not
- * finite has codes 0 and scale NaN.  codes: ldc >= cols bytes apart (gemm_s8_scaled takes
+ * a r / 127.  A row of zeros, or of no values, has codes and scale 0; a row in which some t is
+ * not finite has codes 0 and scale NaN.  codes: ldc >= cols bytes apart (gemm_s8_scaled takes
  * multiples of 16).
  */
 int ptc_rms_norm_s8(int64_t rows, int64_t cols, const void *x, int64_t ldx, int type, const void *residual, int64_t ldr,

@@ -915,6 +915,16 @@ cudaError_t run_grad(GradArgs a, int sms, float *dw, cudaStream_t s) {
     return e;
 }
 
+// `n` zeros: the sums of no rows.
+int start_zeros(float *p, int64_t n, cudaStream_t s, const char *what) {
+    int sms;
+    const int rc = usable_device(&sms);
+    if (rc) return rc;
+    const cudaError_t e = launch_norm(column_sums_kernel, dim3(unsigned((n + 31) / 32)), 256, s,
+                                      static_cast<const float *>(nullptr), 0, n, p);
+    return e == cudaSuccess ? PTC_OK : fail_launch(e, what);
+}
+
 }  // namespace
 }  // namespace ptc
 
@@ -941,11 +951,11 @@ int ptc_rms_norm_s8(int64_t rows, int64_t cols, const void *x, int64_t ldx, int 
                     float *scale, void *stream) {
     set_message("");
     int rc = check_sizes_n(rows, cols, type, weight_type, eps);
-    if (rc || rows == 0 || cols == 0) return rc;
-    rc = check_rows(codes, cols, ldc, 1);
-    if (rc) return rc;
+    if (rc || rows == 0) return rc;
+    if (cols > 0 && (rc = check_rows(codes, cols, ldc, 1))) return rc;
     if (!scale) return fail_status(PTC_ERR_INVALID, "scale is NULL");
     if (!aligned_to(scale, 4)) return fail_status(PTC_ERR_ALIGN, "scale must be 4-byte aligned");
+    if (cols == 0) return start_zeros(scale, rows, static_cast<cudaStream_t>(stream), "norm launch");
     const ByteRows c = elem_rows(codes, rows, cols, ldc, 1), sc = flat_bytes(scale, uint64_t(rows) * 4);
     const int es = bytes_of(type);
     rc = check_norm(rows, cols, x, ldx, type, residual, ldr, sum, lds, weight, weight_type, c, false);
@@ -973,12 +983,7 @@ int ptc_rms_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t ld
     if (!aligned_to(dweight, 4)) return fail_status(PTC_ERR_ALIGN, "dweight must be 4-byte aligned");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int sms;
-    if (rows == 0) {  // the empty sum
-        if ((rc = usable_device(&sms))) return rc;
-        const cudaError_t e = launch_norm(column_sums_kernel, dim3(unsigned((cols + 31) / 32)), 256, st,
-                                          static_cast<const float *>(nullptr), 0, cols, dweight);
-        return e == cudaSuccess ? PTC_OK : fail_launch(e, "norm gradient launch");
-    }
+    if (rows == 0) return start_zeros(dweight, cols, st, "norm gradient launch");
     const int es = bytes_of(type);
     rc = check_rows(dy, cols, lddy, es);
     if (!rc) rc = check_rows(s, cols, lds, es);
