@@ -34,3 +34,15 @@ def test_s8_rows_of_no_values_have_scale_zero(rows):
         assert got[0].shape == (rows, 0) and got[1].shape == (rows,) and not got[1].any()
     with pytest.raises(ptc.PtcError):
         ptc.ptc_rms_norm_s8(rows, 0, None, 0, ptc.PTC_OUT_BF16, None, 0, None, 0, None, ptc.PTC_OUT_BF16, 1e-6, None, 0, None, stream)
+
+
+def test_dweight_of_many_small_rows_beside_a_large_one():
+    """One row of 1 and 37 of 2^-24, among 300 that are all partial sums of their own: every sum of theirs passes
+    through at most 9 + 2 + 3 additions, each off by half an ulp.  (Added one after the other, all 37 are lost.)"""
+    rows, cols = 300, 64
+    dy = torch.zeros(rows, cols, device=DEV)
+    dy[::8] = 2.0 ** -24
+    dy[0] = 1.0
+    _, dw = ptc.rms_norm_backward(dy, torch.ones(rows, cols, device=DEV), eps=0.0)
+    want = dy.double().sum(0)
+    assert bool(((dw.double() - want).abs() <= 15 * 2.0 ** -24 * want).all()), ((dw.double() - want) * 2.0 ** 24)[0]
