@@ -576,7 +576,7 @@ PyObject *py_moe(PyObject *, PyObject *const *a, Py_ssize_t n) {
     at::Tensor y = result(a[6], rx.rows, rx.cols, x.scalar_type(), index, x.device());
     const Rows ry = rows_of(y, "out");
     at::Tensor ids, weights, ws = empty({bytes}, at::kByte, x.device());
-    if (routing && top_k >= 0) {
+    if (routing && top_k >= 0 && (bytes > 0 || rx.rows == 0)) {  // (of other sizes the call is refused)
         ids = empty({rx.rows, top_k}, at::kInt, x.device());
         weights = empty({rx.rows, top_k}, at::kFloat, x.device());
     }
