@@ -452,7 +452,8 @@ int gemm_a16_fp4(int64_t M, int64_t N, int64_t K, int type, const void *X, int64
  * matrix W of N rows of K (ldw bytes apart); C has X's type.  Products are exact and sums
  * FP32: a group's is taken of x (c + 8) less (8 + z) times that of x.  Activations are
  * taken as binary16 relative to a power of two per token and 32, 64 or 128 elements, which
- * is exact down to 2^-28 of the largest of them and off by at most 2^-35 of it below.
+ * is exact down to 2^-27 of the largest of them (binary16 X: 2^-24) and off by at most 2^-35
+ * of it below.
  * A token with an infinity or NaN gives NaN; other tokens do not see it.
  * Meant for M up to 16, where W is read once; more rows are taken 16 at a time.  X and C
  * are aligned to the element.  K == 0 writes zeros.  Results are the same from call to

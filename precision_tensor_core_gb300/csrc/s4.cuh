@@ -14,8 +14,10 @@
 // free as long as both operands agree.
 //
 // Activations.  Each block of 32, 64 or 128 (the smaller of that and the group) is held
-// as binary16 relative to a power of two that brings its largest into [2^14, 2^15): exact
-// for elements down to 2^-28 of the largest, off by at most 2^-35 of the largest
+// as binary16 relative to a power of two that brings its largest into [2^14, 2^15).  Those
+// divided by 16 lose what lies below 2^-20 before: bfloat16's eight bits are exact from 2^-13
+// on, 2^-27 of the largest, binary16's eleven from 2^-10 on, 2^-24 of it (the others four
+// binary digits further); off by at most half of 2^-20, 2^-35 of the largest,
 // below that, for either 16-bit type.  The block's power of two, times 2^12, and its sum
 // of x 2^-24 stand beside it; the other 2^12 is the output's factor, so that neither
 // bfloat16's largest nor its smallest numbers leave FP32.
