@@ -5,8 +5,8 @@
 // Every byte is read and written once: rows of up to 16384 elements stay in
 // registers between the sum of squares and the output.  The 16-bit norm is bound
 // by memory traffic (8192 x 8192 bfloat16 with a residual 85 us, 92% of the copy rate), the norm
-// to 8 bits by its instructions (the same without one 56 us), the gradient by both (100 us with
-// dsum, 79%); a row of one token by the start of a kernel and one reduction (2.2 us).
+// to 8 bits by its instructions (the same without one 56 us), the gradient by both (99 us with
+// dsum, 80% of the copy rate; 88 without, 67%); a row of one token by the start of a kernel and one reduction (2.2 us).
 //
 // In 8 bits the row's 1 / rms cancels out of the codes: with t = s w and a the
 // row's largest |t|, y / (max |y| / 127) = 127 t / a.  So the sum of squares and the
@@ -472,14 +472,14 @@ __global__ void __launch_bounds__(512) grad_kernel(const GradArgs a) {
         Pack8<T> s[CH], dy[CH];
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            s[i] = load_chunk<false>(static_cast<const T *>(a.s) + row * a.lds, i, tid, threads, a.cols);
-            dy[i] = load_chunk<false>(static_cast<const T *>(a.dy) + row * a.lddy, i, tid, threads, a.cols);
+            s[i] = load_chunk<kSpread>(static_cast<const T *>(a.s) + row * a.lds, i, tid, threads, a.cols);
+            dy[i] = load_chunk<kSpread>(static_cast<const T *>(a.dy) + row * a.lddy, i, tid, threads, a.cols);
         }
         float squares = 0.0f, gs = 0.0f;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             float w[8];
-            load_weight<false, T>(w, a.w, a.w_f32, i, tid, threads, a.cols);
+            load_weight<kSpread, T>(w, a.w, a.w_f32, i, tid, threads, a.cols);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float sv = to_float(s[i].get(e));
@@ -491,14 +491,14 @@ __global__ void __launch_bounds__(512) grad_kernel(const GradArgs a) {
         const float r = inverse_rms(squares, a.inv_cols, a.eps);
         const float m = __fmul_rn(r, __fmul_rn(gs, a.inv_cols));
 #pragma unroll
-        for (int i = 0; i < CH; ++i) grad_chunk<T, false>(a, row, s[i], dy[i], r, m, acc[i], i, tid, threads);
+        for (int i = 0; i < CH; ++i) grad_chunk<T, kSpread>(a, row, s[i], dy[i], r, m, acc[i], i, tid, threads);
     }
     float *part = a.part + int64_t(blockIdx.x) * a.cols;
 #pragma unroll
     for (int i = 0; i < CH; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int64_t c = column<false>(i, e, tid, threads);
+            const int64_t c = column<kSpread>(i, e, tid, threads);
             if (c < a.cols) part[c] = acc[i][e];
         }
 }
@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(512) grad_kernel(const GradArgs a) {
 // The same for aligned rows, which come through shared memory: every thread copies its own
 // elements of the next rows there, `slots` rows deep, and waits for nobody else's.  (Loads
 // at the row's beginning left the memory idle during the reduction and the stores: 8192 x
-// 8192 bfloat16 with ds 259 us instead of 101.)  With rows that lie alike (kAlike) the grid is a
+// 8192 bfloat16 with ds 259 us instead of 99.)  With rows that lie alike (kAlike) the grid is a
 // multiple of eight wherever a CTA has several, so that all of a CTA's begin at the same
 // element of a word and its columns stay where they are.
 template <typename T, int CH, int HOW>
@@ -766,7 +766,7 @@ int round32(int64_t n) { return int((n + 31) / 32 * 32); }
 template <typename T, bool S8, int HOW>
 cudaError_t run_norm(const NormArgs &a, int sms, cudaStream_t s) {
     const int64_t chunks = (a.cols + 7) / 8 + (HOW == kAlike ? 1 : 0);
-    if (chunks > 4 * 512 && !(chunks <= 1024 && a.rows <= sms))
+    if (chunks > 4 * 512)
         return launch_norm(norm_long_kernel<T, S8, HOW>, dim3(unsigned(a.rows)), 1024, s, a);
     if (a.rows > 2 * sms && chunks <= 128) {
         const dim3 grid(unsigned((a.rows + 7) / 8));
@@ -912,6 +912,7 @@ cudaError_t run_grad(GradArgs a, int sms, float *dw, cudaStream_t s) {
         if (HOW == kAlike && parts < a.rows) parts = std::max(8, parts / 8 * 8);
         e = launch_norm_smem(fn, dim3(unsigned(parts)), g.threads, smem, s, a, slots);
     } else {
+        // (also aligned FP32 rows of over 14336 elements with ds, of which the ring holds not one)
         const int ch = chunks <= 256 ? 1 : chunks <= 1024 ? 2 : 4;
         const int threads = round32((chunks + ch - 1) / ch);
         const int per_sm = std::max(1, (sizeof(T) == 2 && ch <= 2 ? 1024 : 512) / threads);
@@ -1044,8 +1045,8 @@ int ptc_rms_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t ld
     auto go = [&](auto t) {
         using T = decltype(t);
         if (vec) return run_grad<T, kWide>(a, sms, dweight, st);
-        // (2047 x 5003 f16 33 us instead of 50, 8192 x 8191 bf16 139 instead of 212; but with few rows
-        // per SM there is nothing to copy ahead: 333 x 777 f32 7.4 instead of 6.1)
+        // (Without ds 2047 x 5003 f16 31.5 us instead of 50, 8192 x 8191 bf16 125 instead of 212; but with
+        // few rows per SM there is nothing to copy ahead: 333 x 777 f32 7.4 instead of 6.1)
         if (rows > 4 * int64_t(sms) && alike(dy, a.lddy) && alike(dx, a.lddx) && (!ds || alike(ds, a.ldds))) return run_grad<T, kAlike>(a, sms, dweight, st);
         return run_grad<T, kSpread>(a, sms, dweight, st);
     };
