@@ -1,8 +1,8 @@
 // s4_tokens.cu -- product of a few rows of 16-bit activations with 4-bit integer
 // weights that have group scales (gemm_a16_s4 of include/ptc.h).
 //
-// The weights are read once and bound the call: 0.5 bytes each and their scales.  The
-// products run on mma.sync m16n8k16 with 16 rows of the weights as one operand and eight
+// The weights, 0.5 bytes each and their scales, are read once per 16 tokens and are all that a
+// call cannot do without.  The products run on mma.sync m16n8k16 with 16 rows of the weights as one operand and eight
 // tokens as the other (s4.cuh); sums stay in FP32.
 //
 // Layout.  The sixteen warps of a CTA are R row groups x S shares of K; a warp owns 16 MT
@@ -16,8 +16,9 @@
 // order through distributed shared memory.
 //
 // Rates (weights from HBM): one token 5.1 us with 4096 x 4096 weights in groups of 128 and 17.4
-// with 16384 x 8192 (3.9 TB/s); sixteen 8.3 and 29 (2.4 TB/s): those are bound by the issue
-// of instructions, 409 per 16 rows x 256 codes and sixteen tokens.
+// with 16384 x 8192 (3.9 TB/s); sixteen 8.3 and 29 (2.4 TB/s).  No one unit bounds those: 409
+// instructions per 16 rows x 256 codes and sixteen tokens take half of the issue slots, and 16 warps
+// per SM (registers, shared memory) do not fill the other half while they wait for each other's results.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -394,7 +395,7 @@ bool fit_s4(S4Shape &sh, const S4Args &a, int blocks, int toks, int tok) {
 // 2.0 for 16 rows and sixteen tokens, its sums over a cluster 1.6, clusters of four 0.8 to
 // start, of eight 2.0.  Operands that a CTA makes itself cost 0.03 us per stage and token, ones
 // that do not fit 1.1 per chunk and tile.  (Fitted to the times of every shape at 44 sizes
-// between 64 x 64 and 16384 x 8192 weights with 1 to 16 tokens; its choice takes 1.004
+// between 64 x 64 and 16384 x 8192 weights with 1 to 16 tokens; its choice takes 1.005
 // times the fastest shape's time there, 1.07 at most.)
 // The keys take a part of the shapes, all of them where that leaves none.
 S4Shape choose_s4(const S4Args &a, int unit, int sms) {
