@@ -21,10 +21,13 @@
 // next item's while it ends one.  The activations come from L2 into registers, half a stage
 // ahead: an expert has few of them.
 //
-// Times: 16 tokens through 4 each of 32 experts of 4096 x 2048 in bfloat16 138 us (367 MB, 2.7 TB/s),
-// bound by the issue of instructions (about 410 per 16 rows x 256 codes); one token through 8 of 64
-// experts of 2048 x 1024 22 us, a chain of waits: router 3.3, routing 2.6, rows of h 8, all of them
-// 3, rows of y 4, their shares 2.  With 16 rows of y per item instead of 32 the first took 155.
+// Times: 16 tokens through 4 each of 32 experts of 4096 x 2048 in bfloat16 142 us (367 MB, 2.6 TB/s),
+// in binary16 184; one token through 8 of 64 experts of 2048 x 1024 22 us, a chain of waits: router
+// 3.3, routing 2.6, rows of h 8, all of them 3, rows of y 4, their sums 2.  No one unit bounds the
+// first: about 410 instructions per 16 rows x 256 codes take 42% of the issue slots, and the 16 warps
+// that the registers leave an SM wait for each other's results and for the activations from L2.  With 16
+// rows of y per item instead of 32 it took a tenth more.  A fixed order of the sums, whichever warps
+// take the chunks, costs it 3%: a sum in shared memory by each warp for what it held took 138.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -761,12 +764,12 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                 for (int o = threadIdx.x; o < a.tokens * 32; o += kMoeThreads) {
                     const float *p = a.parts + (place + (o >> 5) * n) * 32 + (o & 31);
                     float v = 0.0f;
-                    for (int k = 0; k < n; k += 24) {  // (24 loads in flight)
-                        float c[24];
+                    for (int k = 0; k < n; k += 16) {  // (16 loads in flight)
+                        float c[16];
 #pragma unroll
-                        for (int i = 0; i < 24; ++i) c[i] = k + i < n ? __ldcg(p + (k + i) * 32) : 0.0f;
+                        for (int i = 0; i < 16; ++i) c[i] = k + i < n ? __ldcg(p + (k + i) * 32) : 0.0f;
 #pragma unroll
-                        for (int i = 0; i < 24; ++i) v = __fadd_rn(v, c[i]);
+                        for (int i = 0; i < 16; ++i) v = __fadd_rn(v, c[i]);
                     }
                     const int row = row0 + (o & 31);
                     if (row < a.hidden) static_cast<X *>(a.y)[int64_t(o >> 5) * a.ldy + row] = from_float<X>(__fmul_rn(v, kS4Out));
