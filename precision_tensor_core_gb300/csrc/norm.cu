@@ -869,7 +869,11 @@ NormArgs norm_args(int64_t rows, int64_t cols, const void *x, int64_t ldx, const
 // Partial sums of the weight's gradient: rows of them, and of the row pieces of long rows.
 constexpr int kMaxParts = 512;
 bool grad_long(int64_t cols) { return cols > 16384; }
-int64_t grad_parts(int64_t rows) { return std::min<int64_t>(rows, kMaxParts); }
+int64_t grad_pieces(int64_t cols) { return (cols + 2047) / 2048; }  // of 256 threads with eight columns each
+// (Long rows: their pieces' CTAs, eight per SM in all, of 152.)
+int64_t grad_parts(int64_t rows, int64_t cols) {
+    return std::min<int64_t>(rows, grad_long(cols) ? std::max<int64_t>(1, 8 * 152 / grad_pieces(cols)) : kMaxParts);
+}
 
 // Of grad_ring_kernel: threads and their chunks, bytes of a row in flight and of the weights.
 struct RingShape {
@@ -894,8 +898,8 @@ cudaError_t run_grad(GradArgs a, int sms, float *dw, cudaStream_t s) {
     cudaError_t e;
     constexpr int WIDE = HOW == kWide ? kWide : kSpread;
     if (grad_long(a.cols)) {
-        const int64_t pieces = (chunks + 255) / 256;
-        parts = int(std::min<int64_t>(grad_parts(a.rows), std::max<int64_t>(1, 8 * int64_t(sms) / pieces)));
+        const int64_t pieces = grad_pieces(a.cols);
+        parts = int(grad_parts(a.rows, a.cols));
         e = launch_norm(grad_stats_kernel<T, WIDE>, dim3(unsigned(a.rows)), 1024, s, a);
         if (e == cudaSuccess) e = launch_norm(grad_columns_kernel<T, WIDE>, dim3(unsigned(pieces), unsigned(parts)), 256, s, a);
     } else if (const RingShape g = ring_shape(chunks + (HOW == kAlike ? 1 : 0), a.ds ? 3 : 2, sizeof(T));
@@ -908,7 +912,7 @@ cudaError_t run_grad(GradArgs a, int sms, float *dw, cudaStream_t s) {
         auto *fn = g.ch == 1 ? grad_ring_kernel<T, 1, RING> : grad_ring_kernel<T, 2, RING>;
         e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kRingMost));
         if (e != cudaSuccess) return e;
-        parts = int(std::min<int64_t>(grad_parts(a.rows), int64_t(sms) * per_sm));
+        parts = int(std::min<int64_t>(grad_parts(a.rows, a.cols), int64_t(sms) * per_sm));
         if (HOW == kAlike && parts < a.rows) parts = std::max(8, parts / 8 * 8);
         e = launch_norm_smem(fn, dim3(unsigned(parts)), g.threads, smem, s, a, slots);
     } else {
@@ -916,7 +920,7 @@ cudaError_t run_grad(GradArgs a, int sms, float *dw, cudaStream_t s) {
         const int ch = chunks <= 256 ? 1 : chunks <= 1024 ? 2 : 4;
         const int threads = round32((chunks + ch - 1) / ch);
         const int per_sm = std::max(1, (sizeof(T) == 2 && ch <= 2 ? 1024 : 512) / threads);
-        parts = int(std::min<int64_t>(grad_parts(a.rows), int64_t(sms) * std::min(per_sm, 3)));
+        parts = int(std::min<int64_t>(grad_parts(a.rows, a.cols), int64_t(sms) * std::min(per_sm, 3)));
         const dim3 grid = dim3(unsigned(parts));
         e = ch == 1   ? launch_norm(grad_kernel<T, 1>, grid, threads, s, a)
             : ch == 2 ? launch_norm(grad_kernel<T, 2>, grid, threads, s, a)
@@ -983,7 +987,7 @@ int ptc_rms_norm_s8(int64_t rows, int64_t cols, const void *x, int64_t ldx, int 
 
 int64_t ptc_rms_norm_backward_workspace(int64_t rows, int64_t cols) {
     if (rows <= 0 || cols <= 0 || rows > kMaxDimN || cols > kMaxDimN) return 0;
-    return grad_parts(rows) * cols * 4 + (grad_long(cols) ? rows * 8 + 16 : 0);
+    return grad_parts(rows, cols) * cols * 4 + (grad_long(cols) ? rows * 8 + 16 : 0);
 }
 
 int ptc_rms_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t lddy, const void *s, int64_t lds, int type,
@@ -1030,7 +1034,7 @@ int ptc_rms_norm_backward(int64_t rows, int64_t cols, const void *dy, int64_t ld
     a.dx = dx;
     a.lddx = lddx;
     a.part = static_cast<float *>(workspace);
-    a.stat = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + (grad_parts(rows) * cols * 4 + 15) / 16 * 16);
+    a.stat = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + (grad_parts(rows, cols) * cols * 4 + 15) / 16 * 16);
     a.rows = rows;
     a.cols = cols;
     a.eps = eps;
